@@ -327,6 +327,75 @@ ROPE_API rope_status_t rope_partial_bwd_inplace_pos_multi(
     const double* inv_freq, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
     void* stream);
 
+/* ================= cos/sin from positions on several axes ================= */
+
+/* most axes of one call */
+#define ROPE_AXES_MAX 4
+
+/*
+ * rope_partial_{fwd,bwd}_inplace_axes, _out_axes, _inplace_axes_multi -- the
+ * position forms with positions on several axes (time, height and width of
+ * images and video): pair i of the slice belongs to the axis pair_axes[i]
+ * and turns by
+ *   θ = (double)positions[pair_axes[i], b, s] * inv_freq[i]
+ * cos and sin as for rope_partial_fwd_inplace_pos. Which pairs an axis takes
+ * (blocks, dealt in turn, any other order) and whether the frequencies run
+ * over all pairs or over each axis's own is the caller's choice of pair_axes
+ * and inv_freq.
+ *
+ *   positions          device int64 array; the position of (b,s) on axis k is
+ *                      positions[k*positions_strides[0] +
+ *                      b*positions_strides[1] + s*positions_strides[2]].
+ *   positions_shape    host {A, Bp, S}: A axes, 1 to ROPE_AXES_MAX; Bp is 1
+ *                      (every batch alike) or B, and S is x's S.
+ *   positions_strides  host, in elements, each >= 0; a size-1 dimension's
+ *                      stride is ignored.
+ *   pair_axes          host array of L/2 axes, each in [0, A), read during
+ *                      the call.
+ *   Other arguments, overlap rules, no-ops and memory are those of the _pos
+ *   entry point of the same form.
+ *
+ * Checks: those of the _pos entry points in their order; pair_axes NULL
+ * (ROPE_ERR_NULLPTR) after the other pointers; A outside [1, ROPE_AXES_MAX]
+ * before the other dimensions, and a pair's axis outside [0, A) last
+ * (ROPE_ERR_INVALID).
+ */
+ROPE_API rope_status_t rope_partial_fwd_inplace_axes(
+    void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream);
+
+ROPE_API rope_status_t rope_partial_bwd_inplace_axes(
+    void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream);
+
+ROPE_API rope_status_t rope_partial_fwd_out_axes(
+    void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream);
+
+ROPE_API rope_status_t rope_partial_bwd_out_axes(
+    void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream);
+
+ROPE_API rope_status_t rope_partial_fwd_inplace_axes_multi(
+    int32_t count, void* const xs[], const int64_t x_shapes[][4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream);
+
+ROPE_API rope_status_t rope_partial_bwd_inplace_axes_multi(
+    int32_t count, void* const xs[], const int64_t x_shapes[][4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream);
+
 /* ====================== checks and launch plans ====================== */
 
 /*
@@ -395,6 +464,16 @@ ROPE_API rope_status_t rope_partial_launch_info_pos(
     const void* x, const int64_t x_shape[4], rope_dtype_t dtype,
     const int64_t* positions, const int64_t positions_shape[2], const int64_t positions_strides[2],
     const double* inv_freq, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    int64_t info[ROPE_LAUNCH_INFO_LEN]);
+
+/*
+ * rope_partial_launch_info_axes -- the launch plan of an in-place call with
+ * positions on several axes; info as for rope_partial_launch_info_pos.
+ */
+ROPE_API rope_status_t rope_partial_launch_info_axes(
+    const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
     int64_t info[ROPE_LAUNCH_INFO_LEN]);
 
 /* ===================== projection with a rotary epilogue ===================== */

@@ -15,6 +15,7 @@ ANE实现" (section 先搞懂RoPE).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -24,6 +25,9 @@ __all__ = [
     "rope_partial_fwd_inplace_pos", "rope_partial_bwd_inplace_pos", "rope_inv_freq",
     "rope_partial_fwd_out_pos", "rope_partial_bwd_out_pos", "partial_rotary_mul_pos",
     "inplace_partial_rotary_mul_pos", "rope_partial_fwd_inplace_pos_multi", "rope_partial_bwd_inplace_pos_multi",
+    "rope_partial_fwd_inplace_axes", "rope_partial_bwd_inplace_axes", "rope_partial_fwd_out_axes",
+    "rope_partial_bwd_out_axes", "rope_partial_fwd_inplace_axes_multi", "rope_partial_bwd_inplace_axes_multi",
+    "inplace_partial_rotary_mul_axes", "partial_rotary_mul_axes", "rope_pair_axes", "rope_axes_inv_freq", "AXES_MAX",
     "rope_proj_fwd", "RopeError", "library", "LIB_PATH", "ROPE_OK", "ROPE_ERR_NULLPTR", "ROPE_ERR_INVALID",
     "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_RUNTIME", "MODES", "DTYPE_CODES",
 ]
@@ -35,8 +39,10 @@ ROPE_OK, ROPE_ERR_NULLPTR, ROPE_ERR_INVALID, ROPE_ERR_UNSUPPORTED, ROPE_ERR_RUNT
 MODES = {"rotate_half": 0, "interleave": 1}
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 MULTI_MAX = 4
+AXES_MAX = 4
 
 _I64x4 = ctypes.c_int64 * 4
+_I64x3 = ctypes.c_int64 * 3
 _I64x2 = ctypes.c_int64 * 2
 _ENTRY_ARGTYPES = [
     ctypes.c_void_p, ctypes.POINTER(ctypes.c_int64), ctypes.c_int,
@@ -90,6 +96,21 @@ def library() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = ctypes.c_int
             f.argtypes = [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p] + pos_args[2:] + [ctypes.c_void_p]
+        axes_args = pos_args[:7] + [ctypes.c_void_p] + pos_args[7:]   # the pairs' axes after the frequencies
+        for name in ("rope_partial_fwd_inplace_axes", "rope_partial_bwd_inplace_axes"):
+            f = getattr(L, name)
+            f.restype = ctypes.c_int
+            f.argtypes = axes_args + [ctypes.c_void_p]
+        for name in ("rope_partial_fwd_out_axes", "rope_partial_bwd_out_axes"):
+            f = getattr(L, name)
+            f.restype = ctypes.c_int
+            f.argtypes = [ctypes.c_void_p] + axes_args + [ctypes.c_void_p]
+        for name in ("rope_partial_fwd_inplace_axes_multi", "rope_partial_bwd_inplace_axes_multi"):
+            f = getattr(L, name)
+            f.restype = ctypes.c_int
+            f.argtypes = [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p] + axes_args[2:] + [ctypes.c_void_p]
+        L.rope_partial_launch_info_axes.restype = ctypes.c_int
+        L.rope_partial_launch_info_axes.argtypes = axes_args + [ctypes.POINTER(ctypes.c_int64)]
         L.rope_partial_launch_info_pos.restype = ctypes.c_int
         L.rope_partial_launch_info_pos.argtypes = pos_args + [ctypes.POINTER(ctypes.c_int64)]
         for name in ("rope_partial_fwd_inplace_multi", "rope_partial_bwd_inplace_multi"):
@@ -127,6 +148,13 @@ def _arr4(v):
         return _I64x4(*v)                       # tuples of ints (torch sizes and strides)
     except TypeError:
         return _I64x4(*[int(t) for t in v])     # other integer types
+
+
+@functools.lru_cache(maxsize=64)
+def _i32_array(values: tuple):
+    """A tuple of ints as a C int32 array (the same array for the same
+    values: a program's pairs keep their axes from call to call)."""
+    return (ctypes.c_int32 * max(1, len(values)))(*values)
 
 
 def raw_call(direction: str, x_ptr, x_shape, dtype: int, r1_ptr, r1_shape, r1_strides,
@@ -184,6 +212,47 @@ def raw_out_pos_call(direction: str, y_ptr, x_ptr, x_shape, dtype: int, pos_ptr,
               int(mode), sl, stream)
 
 
+def _axes_source(pos_shape, pos_strides, pair_axes):
+    """The C arrays of a positions shape and strides of three values and of
+    the pairs' axes (None = NULL)."""
+    ps = None if pos_shape is None else _I64x3(*pos_shape)
+    pt = None if pos_strides is None else _I64x3(*pos_strides)
+    return ps, pt, None if pair_axes is None else _i32_array(tuple(pair_axes))
+
+
+def raw_axes_call(direction: str, x_ptr, x_shape, dtype: int, pos_ptr, pos_shape, pos_strides, inv_freq_ptr,
+                  pair_axes, table_dtype: int, mode: int, partial_slice, stream=None, y_ptr=None,
+                  out: bool = False) -> int:
+    """rope_partial_{fwd,bwd}_inplace_axes, or with out=True the _out_axes
+    form into y_ptr, with plain integers and sequences (None = NULL); returns
+    the status code without raising."""
+    L = library()
+    ps, pt, pa = _axes_source(pos_shape, pos_strides, pair_axes)
+    sl = None if partial_slice is None else _I64x2(int(partial_slice[0]), int(partial_slice[1]))
+    rest = (x_ptr, _arr4(x_shape), int(dtype), pos_ptr, ps, pt, inv_freq_ptr, pa, int(table_dtype), int(mode), sl,
+            stream)
+    if out:
+        return (L.rope_partial_fwd_out_axes if direction == "fwd" else L.rope_partial_bwd_out_axes)(y_ptr, *rest)
+    return (L.rope_partial_fwd_inplace_axes if direction == "fwd" else L.rope_partial_bwd_inplace_axes)(*rest)
+
+
+def raw_axes_multi_call(direction: str, x_ptrs, x_shapes, dtype: int, pos_ptr, pos_shape, pos_strides, inv_freq_ptr,
+                        pair_axes, table_dtype: int, mode: int, partial_slice, stream=None, count=None) -> int:
+    """Call an _axes_multi entry point with plain integers and sequences
+    (None = NULL); returns the status code without raising."""
+    L = library()
+    fn = L.rope_partial_fwd_inplace_axes_multi if direction == "fwd" else L.rope_partial_bwd_inplace_axes_multi
+    n = len(x_ptrs) if x_ptrs is not None else 0
+    count = n if count is None else count
+    ptrs = None if x_ptrs is None else (ctypes.c_void_p * max(n, 1))(*x_ptrs)
+    flat = [] if x_shapes is None else [int(v) for sh in x_shapes for v in sh]
+    shapes = None if x_shapes is None else (ctypes.c_int64 * max(len(flat), 4))(*flat)
+    ps, pt, pa = _axes_source(pos_shape, pos_strides, pair_axes)
+    sl = None if partial_slice is None else _I64x2(int(partial_slice[0]), int(partial_slice[1]))
+    return fn(int(count), ptrs, shapes, int(dtype), pos_ptr, ps, pt, inv_freq_ptr, pa, int(table_dtype), int(mode),
+              sl, stream)
+
+
 def raw_check(x_ptr, x_shape, dtype: int, r1_ptr, r1_shape, r1_strides, r2_ptr, r2_shape, r2_strides,
               table_dtype: int, mode: int, partial_slice) -> int:
     """rope_partial_check with plain integers and sequences (None = NULL):
@@ -236,6 +305,18 @@ def raw_launch_info_pos(x_ptr, x_shape, dtype: int, pos_ptr, pos_shape, pos_stri
                     "threads_per_row": v[7]}
     return st, {"kernel": KERNELS.get(v[0], v[0]), "blocks": v[1], "threads": v[2], "heads_per_thread": v[3],
                 "head_lanes": v[4], "positions_per_block": v[5], "head_chunks": v[6], "row_vectors": v[7]}
+
+
+def raw_launch_info_axes(x_ptr, x_shape, dtype: int, pos_ptr, pos_shape, pos_strides, inv_freq_ptr, pair_axes,
+                         table_dtype: int, mode: int, partial_slice):
+    """rope_partial_launch_info_axes with plain integers and sequences (None =
+    NULL): (status, the kernel's name or None); nothing is launched."""
+    ps, pt, pa = _axes_source(pos_shape, pos_strides, pair_axes)
+    sl = None if partial_slice is None else _I64x2(int(partial_slice[0]), int(partial_slice[1]))
+    info = (ctypes.c_int64 * LAUNCH_INFO_LEN)()
+    st = library().rope_partial_launch_info_axes(x_ptr, _arr4(x_shape), int(dtype), pos_ptr, ps, pt, inv_freq_ptr, pa,
+                                                 int(table_dtype), int(mode), sl, info)
+    return st, KERNELS.get(info[0], info[0]) if st == ROPE_OK else None
 
 
 def raw_multi_call(direction: str, x_ptrs, x_shapes, dtype: int, r1_ptr, r1_shape, r1_strides,
@@ -518,9 +599,22 @@ def rope_inv_freq(L: int, base: float = 10000.0, device=None):
     return torch.pow(torch.tensor(float(base), dtype=torch.float64), -2.0 * i / L).to(device)
 
 
-def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtype, stream, y=None):
+def _check_pair_axes(positions, pair_axes, partial_slice):
+    """The pairs' axes as a tuple, one for each pair of the slice, and the
+    three-dimensional positions they count on."""
+    import torch
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 3 or positions.dtype != torch.int64:
+        raise ValueError("positions must be a 3-D int64 tensor (A, B or 1, S)")
+    pair_axes = pair_axes if type(pair_axes) is tuple else tuple(int(a) for a in pair_axes)
+    L = 0 if partial_slice is None else int(partial_slice[1]) - int(partial_slice[0])
+    if L > 0 and len(pair_axes) != L // 2:
+        raise ValueError(f"pair_axes must hold (end - start) / 2 = {L // 2} axes, got {len(pair_axes)}")
+    return pair_axes
+
+
+def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtype, stream, y=None, pair_axes=None):
     """The position entry points: in place on x, or (y given) out of place
-    from x into y."""
+    from x into y; with pair_axes, those with several axes."""
     import torch
     if isinstance(mode, str):
         if mode not in MODES:
@@ -532,7 +626,9 @@ def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtyp
             raise TypeError(f"{name} must be a torch.Tensor")
     if x.dim() != 4:
         raise ValueError(f"x must be 4-D (B,S,N,D layout), got {x.dim()}-D")
-    if positions.dim() != 2 or positions.dtype != torch.int64:
+    if pair_axes is not None:
+        pair_axes = _check_pair_axes(positions, pair_axes, partial_slice)
+    elif positions.dim() != 2 or positions.dtype != torch.int64:
         raise ValueError("positions must be a 2-D int64 tensor (B or 1, S)")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D float64 tensor")
@@ -568,7 +664,12 @@ def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtyp
         handle = getattr(stream, "cuda_stream", stream)
     switch = x.is_cuda and dev.index != torch.cuda.current_device()
     with torch.cuda.device(dev) if switch else _nullcontext():
-        if y is None:
+        if pair_axes is not None:
+            st = raw_axes_call(direction, x.data_ptr() or None, tuple(x.shape), _dtype_code(x),
+                               positions.data_ptr() or None, tuple(positions.shape), tuple(positions.stride()),
+                               inv_freq.data_ptr() or None, pair_axes, tdt, mode, partial_slice, handle,
+                               None if y is None else y.data_ptr() or None, y is not None)
+        elif y is None:
             st = raw_pos_call(direction, x.data_ptr() or None, tuple(x.shape), _dtype_code(x),
                               positions.data_ptr() or None, tuple(positions.shape), tuple(positions.stride()),
                               inv_freq.data_ptr() or None, tdt, mode, partial_slice, handle)
@@ -616,6 +717,81 @@ def rope_partial_bwd_out_pos(dx, dy, positions, inv_freq, rotary_mode="interleav
     gradient with respect to x for the incoming gradient ``dy``, which is
     left unchanged."""
     _call_pos("bwd", dy, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, y=dx)
+
+
+def rope_pair_axes(sections, dealt: bool = False) -> tuple:
+    """The axis of each pair for axes that take ``sections[k]`` pairs each:
+    in blocks, all of axis 0's pairs first (``sections=(16, 24, 24)`` gives
+    axis 0 to pairs 0 to 15), or ``dealt``: to the axes in turn, 0, 1, 2, 0,
+    1, 2, ..., an axis that has its pairs being passed over."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= AXES_MAX or min(left) < 0:
+        raise ValueError(f"sections must hold 1 to {AXES_MAX} counts of pairs")
+    if not dealt:
+        return tuple(a for a, n in enumerate(left) for _ in range(n))
+    got = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                got.append(a)
+    return tuple(got)
+
+
+def rope_axes_inv_freq(pair_axes, base: float = 10000.0, device=None):
+    """Frequencies for axes that count their own pairs: base^(-j/n) for the
+    j-th of the n pairs that an axis has in ``pair_axes``, as the float64
+    tensor the _axes entry points take (computed in double on the host).
+    Where the frequencies run over all pairs, use :func:`rope_inv_freq`."""
+    import torch
+    pair_axes = tuple(pair_axes)
+    seen, share = {}, []
+    for a in pair_axes:
+        share.append(seen.get(a, 0) / pair_axes.count(a))
+        seen[a] = seen.get(a, 0) + 1
+    return torch.pow(torch.tensor(float(base), dtype=torch.float64),
+                     -torch.tensor(share, dtype=torch.float64)).to(device)
+
+
+def rope_partial_fwd_inplace_axes(x, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
+                                  table_dtype=None, stream=None) -> None:
+    """:func:`rope_partial_fwd_inplace_pos` with positions on several axes
+    (time, height and width of images and video): pair i of the slice turns by
+    positions[pair_axes[i], b, s] * inv_freq[i].
+
+    positions: int64 GPU tensor (A, B or 1, S), 1 to AXES_MAX axes, any
+    strides.
+    pair_axes: the axis of each of the (end - start) / 2 pairs, in [0, A)
+    (``rope_pair_axes`` gives the usual orders). It stays on the host: a
+    captured graph keeps the axes it was captured with.
+    inv_freq: as there (``rope_axes_inv_freq`` where each axis counts its own
+    pairs).
+    """
+    _call_pos("fwd", x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, pair_axes=pair_axes)
+
+
+def rope_partial_bwd_inplace_axes(dx, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
+                                  table_dtype=None, stream=None) -> None:
+    """Backward of :func:`rope_partial_fwd_inplace_axes`, in place on the
+    incoming gradient."""
+    _call_pos("bwd", dx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, pair_axes=pair_axes)
+
+
+def rope_partial_fwd_out_axes(out, x, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
+                              table_dtype=None, stream=None) -> None:
+    """Out-of-place :func:`rope_partial_fwd_inplace_axes`: ``out`` receives x
+    with its slice rotated; x is left unchanged."""
+    _call_pos("fwd", x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, y=out,
+              pair_axes=pair_axes)
+
+
+def rope_partial_bwd_out_axes(dx, dy, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
+                              table_dtype=None, stream=None) -> None:
+    """Out-of-place backward with several axes: ``dx`` receives the gradient
+    with respect to x for the incoming gradient ``dy``, which is left
+    unchanged."""
+    _call_pos("bwd", dy, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, y=dx,
+              pair_axes=pair_axes)
 
 
 def rope_partial_fwd_inplace_multi(xs, r1, r2, rotary_mode="interleave", partial_slice=None, stream=None) -> None:
@@ -753,48 +929,52 @@ def partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None):
 
 # ---------------------------------------------------------------- autograd, cos/sin from positions
 
-def _grad_x_pos(grad, positions, inv_freq, rotary_mode, partial_slice, table_dtype):
+def _grad_x_pos(grad, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
     """The gradient with respect to x for ``grad`` in a new tensor, cos and
     sin computed from the positions (see _grad_x: grad is never modified)."""
     import torch
     if grad.is_contiguous():
         dx = torch.empty_like(grad, memory_format=torch.contiguous_format)
-        rope_partial_bwd_out_pos(dx, grad, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+        _call_pos("bwd", grad, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, y=dx,
+                  pair_axes=pair_axes)
         return dx
     dx = grad.contiguous()
-    rope_partial_bwd_inplace_pos(dx, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+    _call_pos("bwd", dx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, pair_axes=pair_axes)
     return dx
 
 
 def _pos_functions():
     import torch
 
-    def _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype):
+    def _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes):
         ctx.save_for_backward(positions, inv_freq)
         ctx.rotary_mode = rotary_mode
         ctx.partial_slice = None if partial_slice is None else tuple(int(v) for v in partial_slice)
         ctx.table_dtype = table_dtype
+        ctx.pair_axes = None if pair_axes is None else tuple(pair_axes)
 
     def _backward(ctx, grad):
         positions, inv_freq = ctx.saved_tensors
-        dx = _grad_x_pos(grad, positions, inv_freq, ctx.rotary_mode, ctx.partial_slice, ctx.table_dtype)
-        return dx, None, None, None, None, None
+        dx = _grad_x_pos(grad, positions, inv_freq, ctx.rotary_mode, ctx.partial_slice, ctx.table_dtype,
+                         ctx.pair_axes)
+        return dx, None, None, None, None, None, None
 
     class InplacePartialRotaryMulPosFn(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype):
-            rope_partial_fwd_inplace_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+        def forward(ctx, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes):
+            _call_pos("fwd", x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None,
+                      pair_axes=pair_axes)
             ctx.mark_dirty(x)
-            _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+            _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
             return x
 
         backward = staticmethod(_backward)
 
     class PartialRotaryMulPosFn(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype):
-            y = _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
-            _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+        def forward(ctx, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes):
+            y = _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
+            _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
             return y
 
         backward = staticmethod(_backward)
@@ -802,18 +982,42 @@ def _pos_functions():
     return InplacePartialRotaryMulPosFn, PartialRotaryMulPosFn
 
 
-def _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype):
+def _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
     import torch
     xc = x.contiguous()
     if xc.numel() and xc.data_ptr() != x.data_ptr():
-        rope_partial_fwd_inplace_pos(xc, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+        _call_pos("fwd", xc, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, pair_axes=pair_axes)
         return xc
     y = torch.empty_like(xc, memory_format=torch.contiguous_format)
-    rope_partial_fwd_out_pos(y, xc, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+    _call_pos("fwd", xc, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, y=y, pair_axes=pair_axes)
     return y
 
 
 _POS_FNS = None
+
+
+def _autograd_inplace_pos(name, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
+    import torch
+    global _POS_FNS
+    if torch.is_grad_enabled() and x.requires_grad:
+        if x.is_leaf:
+            raise RuntimeError(f"{name}: x is a leaf tensor that requires grad; "
+                               "rotate a non-leaf copy of it (e.g. y = x * 1.0)")
+        if _POS_FNS is None:
+            _POS_FNS = _pos_functions()
+        _POS_FNS[0].apply(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
+        return
+    _call_pos("fwd", x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, pair_axes=pair_axes)
+
+
+def _autograd_out_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
+    import torch
+    global _POS_FNS
+    if torch.is_grad_enabled() and x.requires_grad:
+        if _POS_FNS is None:
+            _POS_FNS = _pos_functions()
+        return _POS_FNS[1].apply(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
+    return _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
 
 
 def inplace_partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interleave", partial_slice=None,
@@ -822,18 +1026,8 @@ def inplace_partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interlea
     kernel from positions (see :func:`rope_partial_fwd_inplace_pos`).
     positions and inv_freq never get gradients; x must not be a leaf tensor
     that requires grad."""
-    import torch
-    global _POS_FNS
-    if torch.is_grad_enabled() and x.requires_grad:
-        if x.is_leaf:
-            raise RuntimeError("inplace_partial_rotary_mul_pos: x is a leaf tensor that requires grad; "
-                               "rotate a non-leaf copy of it (e.g. y = x * 1.0)")
-        if _POS_FNS is None:
-            _POS_FNS = _pos_functions()
-        _POS_FNS[0].apply(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
-        return None
-    rope_partial_fwd_inplace_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
-    return None
+    _autograd_inplace_pos("inplace_partial_rotary_mul_pos", x, positions, inv_freq, rotary_mode, partial_slice,
+                          table_dtype)
 
 
 def partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interleave", partial_slice=None,
@@ -842,16 +1036,25 @@ def partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interleave", par
     positions: returns a new tensor, x is not modified, and the backward is
     the out-of-place position backward. positions and inv_freq never get
     gradients."""
-    import torch
-    global _POS_FNS
-    if torch.is_grad_enabled() and x.requires_grad:
-        if _POS_FNS is None:
-            _POS_FNS = _pos_functions()
-        return _POS_FNS[1].apply(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
-    return _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+    return _autograd_out_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
 
 
-def _call_pos_multi(direction, xs, positions, inv_freq, mode, partial_slice, table_dtype, stream):
+def inplace_partial_rotary_mul_axes(x, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
+                                    table_dtype=None) -> None:
+    """:func:`inplace_partial_rotary_mul_pos` with positions on several axes
+    (see :func:`rope_partial_fwd_inplace_axes`)."""
+    _autograd_inplace_pos("inplace_partial_rotary_mul_axes", x, positions, inv_freq, rotary_mode, partial_slice,
+                          table_dtype, tuple(pair_axes))
+
+
+def partial_rotary_mul_axes(x, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
+                            table_dtype=None):
+    """:func:`partial_rotary_mul_pos` with positions on several axes (see
+    :func:`rope_partial_fwd_inplace_axes`)."""
+    return _autograd_out_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, tuple(pair_axes))
+
+
+def _call_pos_multi(direction, xs, positions, inv_freq, mode, partial_slice, table_dtype, stream, pair_axes=None):
     import torch
     xs = list(xs)
     if len(xs) > MULTI_MAX:
@@ -874,7 +1077,9 @@ def _call_pos_multi(direction, xs, positions, inv_freq, mode, partial_slice, tab
     devs = {x.device for x in xs if x.numel()}
     if len(devs) > 1:
         raise ValueError("all tensors of one call must be on one device")
-    if positions.dim() != 2 or positions.dtype != torch.int64:
+    if pair_axes is not None:
+        pair_axes = _check_pair_axes(positions, pair_axes, partial_slice)
+    elif positions.dim() != 2 or positions.dtype != torch.int64:
         raise ValueError("positions must be a 2-D int64 tensor (B or 1, S)")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D float64 tensor")
@@ -897,10 +1102,15 @@ def _call_pos_multi(direction, xs, positions, inv_freq, mode, partial_slice, tab
     else:
         handle = getattr(stream, "cuda_stream", stream)
     with torch.cuda.device(dev) if dev is not None else _nullcontext():
-        st = raw_pos_multi_call(direction, [x.data_ptr() or None for x in xs], [tuple(x.shape) for x in xs],
-                                _dtype_code(xs[0]), positions.data_ptr() or None, tuple(positions.shape),
-                                tuple(positions.stride()), inv_freq.data_ptr() or None, tdt, mode, partial_slice,
-                                handle)
+        ptrs, shapes = [x.data_ptr() or None for x in xs], [tuple(x.shape) for x in xs]
+        where = (positions.data_ptr() or None, tuple(positions.shape), tuple(positions.stride()),
+                 inv_freq.data_ptr() or None)
+        if pair_axes is not None:
+            st = raw_axes_multi_call(direction, ptrs, shapes, _dtype_code(xs[0]), *where, pair_axes, tdt, mode,
+                                     partial_slice, handle)
+        else:
+            st = raw_pos_multi_call(direction, ptrs, shapes, _dtype_code(xs[0]), *where, tdt, mode, partial_slice,
+                                    handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
 
@@ -917,6 +1127,20 @@ def rope_partial_bwd_inplace_pos_multi(xs, positions, inv_freq, rotary_mode="int
                                        table_dtype=None, stream=None) -> None:
     """Backward of :func:`rope_partial_fwd_inplace_pos_multi`."""
     _call_pos_multi("bwd", xs, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream)
+
+
+def rope_partial_fwd_inplace_axes_multi(xs, positions, inv_freq, pair_axes, rotary_mode="interleave",
+                                        partial_slice=None, table_dtype=None, stream=None) -> None:
+    """:func:`rope_partial_fwd_inplace_axes` on up to 4 tensors sharing the
+    positions (e.g. Q and K of one layer), in one launch when they share B,
+    S and D: each pair's cos and sin is then evaluated once per position."""
+    _call_pos_multi("fwd", xs, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, pair_axes)
+
+
+def rope_partial_bwd_inplace_axes_multi(xs, positions, inv_freq, pair_axes, rotary_mode="interleave",
+                                        partial_slice=None, table_dtype=None, stream=None) -> None:
+    """Backward of :func:`rope_partial_fwd_inplace_axes_multi`."""
+    _call_pos_multi("bwd", xs, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, pair_axes)
 
 
 def rope_proj_fwd(x, w, r1, r2, heads: int, rotary_mode="interleave", partial_slice=None, out=None,

@@ -16,12 +16,18 @@ namespace {
 // takes fewer). Any alignment, any start parity, any slice length; one
 // thread per rotation pair; 64-bit indexing throughout.
 // ---------------------------------------------------------------------------
+// Where the general kernels' cos and sin come from: tables, positions on one
+// axis, positions on several.
+constexpr int kSrcTables = 0;
+constexpr int kSrcPos = 1;
+constexpr int kSrcAxes = 2;
+
 struct ScalarArgs {
     void* x;
     const void* r1;
     const void* r2;
-    const int64_t* pos;     // POS: positions (position of (b,s) at pos[b*pos_sb + s*pos_ss])
-    const double* inv_freq; // POS: L/2 frequencies
+    const int64_t* pos;     // positions (position of (b,s) at pos[b*pos_sb + s*pos_ss])
+    const double* inv_freq; // their L/2 frequencies
     int64_t pos_sb, pos_ss;
     int64_t S, N, D, start, L;
     int64_t half;           // rotate_half: lanes between a pair's lanes (L/2, or L/c for a coefficient c)
@@ -29,9 +35,10 @@ struct ScalarArgs {
     int64_t items;          // rows * pairs
     int64_t t1b, t1s, t1n;  // cos strides in elements (0 = broadcast)
     int64_t t2b, t2s, t2n;
+    PosAxes ax;             // kSrcAxes
 };
 
-template <int DT, int TT, int DIR, int MODE, bool POS>
+template <int DT, int TT, int DIR, int MODE, int SRC>
 __global__ void __launch_bounds__(256) rope_scalar_kernel(ScalarArgs a)
 {
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
@@ -50,9 +57,11 @@ __global__ void __launch_bounds__(256) rope_scalar_kernel(ScalarArgs a)
         float xa = Store<DT>::load1(a.x, xo + j);
         float xb = Store<DT>::load1(a.x, xo + pj);
         float ca, cb, sa, sb;
-        if constexpr (POS) {
+        if constexpr (SRC != kSrcTables) {
             // both lanes of pair q share its angle
-            const float2 t = pos_cos_sin<TT>(a.pos[b * a.pos_sb + s * a.pos_ss], a.inv_freq[q]);
+            const int64_t* p = a.pos + b * a.pos_sb + s * a.pos_ss;
+            const float2 t = pos_cos_sin<TT>(SRC == kSrcAxes ? axis_position(a.ax, p, (uint32_t)q) : p[0],
+                                             a.inv_freq[q]);
             ca = cb = t.x;
             sa = sb = t.y;
         } else {
@@ -78,8 +87,8 @@ struct RowArgs {
     void* x;
     const void* r1;
     const void* r2;
-    const int64_t* pos;     // POS: positions (position of (b,s) at pos[b*pos_sb + s*pos_ss])
-    const double* inv_freq; // POS: L/2 frequencies
+    const int64_t* pos;     // positions (position of (b,s) at pos[b*pos_sb + s*pos_ss])
+    const double* inv_freq; // their L/2 frequencies
     int64_t pos_sb, pos_ss;
     int64_t D, start;       // row length and slice start, elements
     int64_t t1b, t1s, t1n;  // cos strides in elements (0 = broadcast)
@@ -91,9 +100,10 @@ struct RowArgs {
     uint32_t rpb, tpr;      // rows per block, threads per row
     uint32_t groups;        // ceil(rows / rpb)
     FastDiv tpr_div, n_div, s_div;
+    PosAxes ax;             // kSrcAxes
 };
 
-template <int DT, int TT, int DIR, int MODE, bool POS>
+template <int DT, int TT, int DIR, int MODE, int SRC>
 __global__ void __launch_bounds__(256) rope_rows_kernel(RowArgs a)
 {
     const uint32_t t = threadIdx.x;
@@ -110,7 +120,8 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RowArgs a)
         const int64_t xo = (int64_t)row * a.D + a.start;
         const int64_t co = b * a.t1b + s * a.t1s + n * a.t1n;
         const int64_t so = b * a.t2b + s * a.t2s + n * a.t2n;
-        const int64_t p = POS ? a.pos[b * a.pos_sb + s * a.pos_ss] : 0;
+        const int64_t* pp = a.pos + b * a.pos_sb + s * a.pos_ss;
+        const int64_t p = SRC == kSrcPos ? pp[0] : 0;
         for (uint32_t q = q0; q < a.pairs; q += a.tpr) {
             // negated-partner lane (see the scalar kernel)
             const uint32_t g = MODE == kModeIL ? 0 : fast_div(q, a.half_div);
@@ -119,9 +130,9 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RowArgs a)
             float xa = Store<DT>::load1(a.x, xo + j);
             float xb = Store<DT>::load1(a.x, xo + pj);
             float ca, cb, sa, sb;
-            if constexpr (POS) {
+            if constexpr (SRC != kSrcTables) {
                 // both lanes of pair q share its angle
-                const float2 t = pos_cos_sin<TT>(p, a.inv_freq[q]);
+                const float2 t = pos_cos_sin<TT>(SRC == kSrcAxes ? axis_position(a.ax, pp, q) : p, a.inv_freq[q]);
                 ca = cb = t.x;
                 sa = sb = t.y;
             } else {

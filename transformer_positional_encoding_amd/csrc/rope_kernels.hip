@@ -32,6 +32,7 @@
 
 #include "rope_device.hpp"
 #include "rope_general_kernels.hpp"
+#include "rope_host.hpp"
 #include "rope_partial.h"
 #include "rope_plan.hpp"
 #include "rope_pos_kernels.hpp"
@@ -45,12 +46,6 @@ namespace {
 // Host side
 // ---------------------------------------------------------------------------
 thread_local std::string g_last_error;
-
-rope_status_t set_error(rope_status_t st, const std::string& msg)
-{
-    g_last_error = msg;
-    return st;
-}
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cu_count[kMaxDevices];
@@ -338,29 +333,43 @@ hipError_t launch_vec(const Plan& p, const VecArgs& a, const VecConfig& cfg, hip
     return hipLaunchKernel(fn, dim3(vec_grid(a, cfg)), dim3(threads), args, 0, stream);
 }
 
-template <int DT, int TT, bool POS>
+// Where a plan's cos and sin come from.
+int source_of(const Plan& p) { return p.pos == nullptr ? kSrcTables : p.naxes == 0 ? kSrcPos : kSrcAxes; }
+
+void set_axes(const Plan& p, PosAxes* ax)
+{
+    ax->sa = p.pos_sa;
+    ax->last = p.naxes > 0 ? (uint32_t)(p.naxes - 1) : 0;
+    std::copy(std::begin(p.axis_words), std::end(p.axis_words), ax->words);
+}
+
+template <int DT, int TT, int SRC>
 const void* scalar_kernel_t(int dir, int mode)
 {
     if (dir == kFwd)
-        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kFwd, kModeIL, POS>)
-                               : reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kFwd, kModeRH, POS>);
-    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kBwd, kModeIL, POS>)
-                           : reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kBwd, kModeRH, POS>);
+        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kFwd, kModeIL, SRC>)
+                               : reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kFwd, kModeRH, SRC>);
+    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kBwd, kModeIL, SRC>)
+                           : reinterpret_cast<const void*>(&rope_scalar_kernel<DT, TT, kBwd, kModeRH, SRC>);
 }
 
 template <int DT, int TT>
-const void* scalar_kernel_p(bool pos, int dir, int mode)
+const void* scalar_kernel_p(int src, int dir, int mode)
 {
-    return pos ? scalar_kernel_t<DT, TT, true>(dir, mode) : scalar_kernel_t<DT, TT, false>(dir, mode);
+    switch (src) {
+    case kSrcTables: return scalar_kernel_t<DT, TT, kSrcTables>(dir, mode);
+    case kSrcPos: return scalar_kernel_t<DT, TT, kSrcPos>(dir, mode);
+    default: return scalar_kernel_t<DT, TT, kSrcAxes>(dir, mode);
+    }
 }
 
 template <int DT>
-const void* scalar_kernel_dt(int tt, bool pos, int dir, int mode)
+const void* scalar_kernel_dt(int tt, int src, int dir, int mode)
 {
     switch (tt) {
-    case ROPE_DTYPE_F32: return scalar_kernel_p<DT, ROPE_DTYPE_F32>(pos, dir, mode);
-    case ROPE_DTYPE_F16: return scalar_kernel_p<DT, ROPE_DTYPE_F16>(pos, dir, mode);
-    default: return scalar_kernel_p<DT, ROPE_DTYPE_BF16>(pos, dir, mode);
+    case ROPE_DTYPE_F32: return scalar_kernel_p<DT, ROPE_DTYPE_F32>(src, dir, mode);
+    case ROPE_DTYPE_F16: return scalar_kernel_p<DT, ROPE_DTYPE_F16>(src, dir, mode);
+    default: return scalar_kernel_p<DT, ROPE_DTYPE_BF16>(src, dir, mode);
     }
 }
 
@@ -369,6 +378,7 @@ hipError_t launch_scalar(const Plan& p, int cus, hipStream_t stream)
     ScalarArgs a;
     a.x = p.x; a.r1 = p.r1; a.r2 = p.r2;
     a.pos = p.pos; a.inv_freq = p.inv_freq; a.pos_sb = p.pos_sb; a.pos_ss = p.pos_ss;
+    set_axes(p, &a.ax);
     a.S = p.S; a.N = p.N; a.D = p.D; a.start = p.start; a.L = p.L;
     a.half = p.half;
     a.pairs = p.L / 2;
@@ -380,37 +390,41 @@ hipError_t launch_scalar(const Plan& p, int cus, hipStream_t stream)
     grid = std::max<uint64_t>(1, std::min<uint64_t>(grid, (a.items + threads - 1) / threads));
     const void* fn;
     switch (p.dtype) {
-    case ROPE_DTYPE_F32: fn = scalar_kernel_dt<ROPE_DTYPE_F32>(p.tdtype, p.pos != nullptr, p.dir, p.mode); break;
-    case ROPE_DTYPE_F16: fn = scalar_kernel_dt<ROPE_DTYPE_F16>(p.tdtype, p.pos != nullptr, p.dir, p.mode); break;
-    default: fn = scalar_kernel_dt<ROPE_DTYPE_BF16>(p.tdtype, p.pos != nullptr, p.dir, p.mode); break;
+    case ROPE_DTYPE_F32: fn = scalar_kernel_dt<ROPE_DTYPE_F32>(p.tdtype, source_of(p), p.dir, p.mode); break;
+    case ROPE_DTYPE_F16: fn = scalar_kernel_dt<ROPE_DTYPE_F16>(p.tdtype, source_of(p), p.dir, p.mode); break;
+    default: fn = scalar_kernel_dt<ROPE_DTYPE_BF16>(p.tdtype, source_of(p), p.dir, p.mode); break;
     }
     void* args[] = {&a};
     return hipLaunchKernel(fn, dim3((uint32_t)grid), dim3(threads), args, 0, stream);
 }
 
-template <int DT, int TT, bool POS>
+template <int DT, int TT, int SRC>
 const void* rows_kernel_t(int dir, int mode)
 {
     if (dir == kFwd)
-        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kFwd, kModeIL, POS>)
-                               : reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kFwd, kModeRH, POS>);
-    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kBwd, kModeIL, POS>)
-                           : reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kBwd, kModeRH, POS>);
+        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kFwd, kModeIL, SRC>)
+                               : reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kFwd, kModeRH, SRC>);
+    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kBwd, kModeIL, SRC>)
+                           : reinterpret_cast<const void*>(&rope_rows_kernel<DT, TT, kBwd, kModeRH, SRC>);
 }
 
 template <int DT, int TT>
-const void* rows_kernel_p(bool pos, int dir, int mode)
+const void* rows_kernel_p(int src, int dir, int mode)
 {
-    return pos ? rows_kernel_t<DT, TT, true>(dir, mode) : rows_kernel_t<DT, TT, false>(dir, mode);
+    switch (src) {
+    case kSrcTables: return rows_kernel_t<DT, TT, kSrcTables>(dir, mode);
+    case kSrcPos: return rows_kernel_t<DT, TT, kSrcPos>(dir, mode);
+    default: return rows_kernel_t<DT, TT, kSrcAxes>(dir, mode);
+    }
 }
 
 template <int DT>
-const void* rows_kernel_dt(int tt, bool pos, int dir, int mode)
+const void* rows_kernel_dt(int tt, int src, int dir, int mode)
 {
     switch (tt) {
-    case ROPE_DTYPE_F32: return rows_kernel_p<DT, ROPE_DTYPE_F32>(pos, dir, mode);
-    case ROPE_DTYPE_F16: return rows_kernel_p<DT, ROPE_DTYPE_F16>(pos, dir, mode);
-    default: return rows_kernel_p<DT, ROPE_DTYPE_BF16>(pos, dir, mode);
+    case ROPE_DTYPE_F32: return rows_kernel_p<DT, ROPE_DTYPE_F32>(src, dir, mode);
+    case ROPE_DTYPE_F16: return rows_kernel_p<DT, ROPE_DTYPE_F16>(src, dir, mode);
+    default: return rows_kernel_p<DT, ROPE_DTYPE_BF16>(src, dir, mode);
     }
 }
 
@@ -439,6 +453,7 @@ hipError_t launch_rows(const Plan& p, const RowShape& r, hipStream_t stream)
     RowArgs a;
     a.x = p.x; a.r1 = p.r1; a.r2 = p.r2;
     a.pos = p.pos; a.inv_freq = p.inv_freq; a.pos_sb = p.pos_sb; a.pos_ss = p.pos_ss;
+    set_axes(p, &a.ax);
     a.D = p.D; a.start = p.start;
     a.t1b = p.t1[0]; a.t1s = p.t1[1]; a.t1n = p.t1[2];
     a.t2b = p.t2[0]; a.t2s = p.t2[1]; a.t2n = p.t2[2];
@@ -456,9 +471,9 @@ hipError_t launch_rows(const Plan& p, const RowShape& r, hipStream_t stream)
     a.s_div = make_fastdiv((uint32_t)p.S);
     const void* fn;
     switch (p.dtype) {
-    case ROPE_DTYPE_F32: fn = rows_kernel_dt<ROPE_DTYPE_F32>(p.tdtype, p.pos != nullptr, p.dir, p.mode); break;
-    case ROPE_DTYPE_F16: fn = rows_kernel_dt<ROPE_DTYPE_F16>(p.tdtype, p.pos != nullptr, p.dir, p.mode); break;
-    default: fn = rows_kernel_dt<ROPE_DTYPE_BF16>(p.tdtype, p.pos != nullptr, p.dir, p.mode); break;
+    case ROPE_DTYPE_F32: fn = rows_kernel_dt<ROPE_DTYPE_F32>(p.tdtype, source_of(p), p.dir, p.mode); break;
+    case ROPE_DTYPE_F16: fn = rows_kernel_dt<ROPE_DTYPE_F16>(p.tdtype, source_of(p), p.dir, p.mode); break;
+    default: fn = rows_kernel_dt<ROPE_DTYPE_BF16>(p.tdtype, source_of(p), p.dir, p.mode); break;
     }
     void* args[] = {&a};
     return hipLaunchKernel(fn, dim3(r.grid), dim3(r.threads), args, 0, stream);
@@ -563,15 +578,6 @@ hipError_t launch_out(const Launch& L, int cus, hipStream_t s)
     hipError_t err = hipMemcpyAsync(L.p.x, L.p.src, (size_t)L.p.bytes, hipMemcpyDeviceToDevice, s);
     if (err != hipSuccess) return err;
     return L.rows ? launch_rows(L.p, L.rs, s) : launch_scalar(L.p, cus, s);
-}
-
-rope_status_t device_cus(int* cus)
-{
-    int dev = 0;
-    hipError_t err = hipGetDevice(&dev);
-    if (err != hipSuccess) return set_error(ROPE_ERR_RUNTIME, std::string("hipGetDevice: ") + hipGetErrorString(err));
-    *cus = cu_count(dev);
-    return ROPE_OK;
 }
 
 rope_status_t run(void* x, const int64_t x_shape[4], rope_dtype_t dtype,
@@ -710,81 +716,107 @@ bool pos_geometry_out(const Plan& p, PosArgs* a, uint32_t* threads, uint32_t* gr
                             pos_out_lanes(p.mode));
 }
 
-template <int DT, int TT, int DIR>
+template <class ARGS, int DT, int TT, int DIR>
 const void* pos_kernel_d(int mode, bool out, bool xchg, int u)
 {
     if (out)
-        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_out_kernel<DT, TT, DIR, kModeIL, false>)
-               : xchg          ? reinterpret_cast<const void*>(&rope_pos_out_kernel<DT, TT, DIR, kModeRH, true>)
-                               : reinterpret_cast<const void*>(&rope_pos_out_kernel<DT, TT, DIR, kModeRH, false>);
+        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_out_kernel<DT, TT, DIR, kModeIL, false, ARGS>)
+               : xchg          ? reinterpret_cast<const void*>(&rope_pos_out_kernel<DT, TT, DIR, kModeRH, true, ARGS>)
+                               : reinterpret_cast<const void*>(&rope_pos_out_kernel<DT, TT, DIR, kModeRH, false, ARGS>);
     if (u == 1)
-        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, false, 1>)
-                               : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, false, 1>);
-    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, false, kUPosLines>)
-                           : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, false, kUPosLines>);
+        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, false, 1, ARGS>)
+                               : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, false, 1, ARGS>);
+    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, false, kUPosLines, ARGS>)
+                           : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, false, kUPosLines, ARGS>);
 }
 
-template <int DT, int TT, int DIR>
+template <class ARGS, int DT, int TT, int DIR>
 const void* pos_multi_kernel_d(int mode, int u)
 {
     if (u == 1)
-        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, true, 1>)
-                               : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, true, 1>);
-    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, true, kUPosLines>)
-                           : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, true, kUPosLines>);
+        return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, true, 1, ARGS>)
+                               : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, true, 1, ARGS>);
+    return mode == kModeIL ? reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeIL, true, kUPosLines, ARGS>)
+                           : reinterpret_cast<const void*>(&rope_pos_kernel<DT, TT, DIR, kModeRH, true, kUPosLines, ARGS>);
 }
 
-template <int DT, int TT>
+template <class ARGS, int DT, int TT>
 const void* pos_multi_kernel_t(int dir, int mode, int u)
 {
-    return dir == kFwd ? pos_multi_kernel_d<DT, TT, kFwd>(mode, u) : pos_multi_kernel_d<DT, TT, kBwd>(mode, u);
+    return dir == kFwd ? pos_multi_kernel_d<ARGS, DT, TT, kFwd>(mode, u) : pos_multi_kernel_d<ARGS, DT, TT, kBwd>(mode, u);
 }
 
-template <int DT>
+template <class ARGS, int DT>
 const void* pos_multi_kernel_dt(int tt, int dir, int mode, int u)
 {
     switch (tt) {
-    case ROPE_DTYPE_F32: return pos_multi_kernel_t<DT, ROPE_DTYPE_F32>(dir, mode, u);
-    case ROPE_DTYPE_F16: return pos_multi_kernel_t<DT, ROPE_DTYPE_F16>(dir, mode, u);
-    default: return pos_multi_kernel_t<DT, ROPE_DTYPE_BF16>(dir, mode, u);
+    case ROPE_DTYPE_F32: return pos_multi_kernel_t<ARGS, DT, ROPE_DTYPE_F32>(dir, mode, u);
+    case ROPE_DTYPE_F16: return pos_multi_kernel_t<ARGS, DT, ROPE_DTYPE_F16>(dir, mode, u);
+    default: return pos_multi_kernel_t<ARGS, DT, ROPE_DTYPE_BF16>(dir, mode, u);
     }
 }
 
 // the position kernel over several tensors at once
-const void* pos_multi_kernel(const Plan& p, int u)
+template <class ARGS>
+const void* pos_multi_kernel_a(const Plan& p, int u)
 {
     switch (p.dtype) {
-    case ROPE_DTYPE_F32: return pos_multi_kernel_dt<ROPE_DTYPE_F32>(p.tdtype, p.dir, p.mode, u);
-    case ROPE_DTYPE_F16: return pos_multi_kernel_dt<ROPE_DTYPE_F16>(p.tdtype, p.dir, p.mode, u);
-    default: return pos_multi_kernel_dt<ROPE_DTYPE_BF16>(p.tdtype, p.dir, p.mode, u);
+    case ROPE_DTYPE_F32: return pos_multi_kernel_dt<ARGS, ROPE_DTYPE_F32>(p.tdtype, p.dir, p.mode, u);
+    case ROPE_DTYPE_F16: return pos_multi_kernel_dt<ARGS, ROPE_DTYPE_F16>(p.tdtype, p.dir, p.mode, u);
+    default: return pos_multi_kernel_dt<ARGS, ROPE_DTYPE_BF16>(p.tdtype, p.dir, p.mode, u);
     }
 }
 
-template <int DT, int TT>
+template <class ARGS, int DT, int TT>
 const void* pos_kernel_t(int dir, int mode, bool out, bool xchg, int u)
 {
-    return dir == kFwd ? pos_kernel_d<DT, TT, kFwd>(mode, out, xchg, u) : pos_kernel_d<DT, TT, kBwd>(mode, out, xchg, u);
+    return dir == kFwd ? pos_kernel_d<ARGS, DT, TT, kFwd>(mode, out, xchg, u) : pos_kernel_d<ARGS, DT, TT, kBwd>(mode, out, xchg, u);
 }
 
-template <int DT>
+template <class ARGS, int DT>
 const void* pos_kernel_dt(int tt, int dir, int mode, bool out, bool xchg, int u)
 {
     switch (tt) {
-    case ROPE_DTYPE_F32: return pos_kernel_t<DT, ROPE_DTYPE_F32>(dir, mode, out, xchg, u);
-    case ROPE_DTYPE_F16: return pos_kernel_t<DT, ROPE_DTYPE_F16>(dir, mode, out, xchg, u);
-    default: return pos_kernel_t<DT, ROPE_DTYPE_BF16>(dir, mode, out, xchg, u);
+    case ROPE_DTYPE_F32: return pos_kernel_t<ARGS, DT, ROPE_DTYPE_F32>(dir, mode, out, xchg, u);
+    case ROPE_DTYPE_F16: return pos_kernel_t<ARGS, DT, ROPE_DTYPE_F16>(dir, mode, out, xchg, u);
+    default: return pos_kernel_t<ARGS, DT, ROPE_DTYPE_BF16>(dir, mode, out, xchg, u);
     }
 }
 
 // out: the out-of-place kernel; xchg: its lane exchange (a row's threads
 // within one wave: rows of 64/k vectors)
-const void* pos_kernel(const Plan& p, bool out, bool xchg = false, int u = kUPosLines)
+template <class ARGS>
+const void* pos_kernel_a(const Plan& p, bool out, bool xchg, int u)
 {
     switch (p.dtype) {
-    case ROPE_DTYPE_F32: return pos_kernel_dt<ROPE_DTYPE_F32>(p.tdtype, p.dir, p.mode, out, xchg, u);
-    case ROPE_DTYPE_F16: return pos_kernel_dt<ROPE_DTYPE_F16>(p.tdtype, p.dir, p.mode, out, xchg, u);
-    default: return pos_kernel_dt<ROPE_DTYPE_BF16>(p.tdtype, p.dir, p.mode, out, xchg, u);
+    case ROPE_DTYPE_F32: return pos_kernel_dt<ARGS, ROPE_DTYPE_F32>(p.tdtype, p.dir, p.mode, out, xchg, u);
+    case ROPE_DTYPE_F16: return pos_kernel_dt<ARGS, ROPE_DTYPE_F16>(p.tdtype, p.dir, p.mode, out, xchg, u);
+    default: return pos_kernel_dt<ARGS, ROPE_DTYPE_BF16>(p.tdtype, p.dir, p.mode, out, xchg, u);
     }
+}
+
+// Launch the position kernel over one tensor (in place or out of place) or
+// several, with the arguments of its position source.
+enum PosKind { kPosOne = 0, kPosMulti = 1, kPosOut = 2 };
+
+template <class ARGS>
+hipError_t launch_pos_args(const Plan& p, ARGS& a, PosKind kind, bool xchg, uint32_t grid, uint32_t threads,
+                           hipStream_t s)
+{
+    const void* fn = kind == kPosMulti ? pos_multi_kernel_a<ARGS>(p, (int)a.U)
+                                       : pos_kernel_a<ARGS>(p, kind == kPosOut, xchg, (int)a.U);
+    void* args[] = {&a};
+    return hipLaunchKernel(fn, dim3(grid), dim3(threads), args, 0, s);
+}
+
+hipError_t launch_pos(const Plan& p, PosArgs& a, PosKind kind, bool xchg, uint32_t grid, uint32_t threads,
+                      hipStream_t s)
+{
+    if (p.naxes == 0) return launch_pos_args(p, a, kind, xchg, grid, threads, s);
+    PosAxesArgs b;
+    static_cast<PosArgs&>(b) = a;
+    set_axes(p, &b.ax);
+    return launch_pos_args(p, b, kind, xchg, grid, threads, s);
 }
 
 // Tables from positions, one planned tensor: the position vector kernel,
@@ -793,23 +825,18 @@ hipError_t launch_pos_plan(const Plan& p, int cus, hipStream_t s)
 {
     PosArgs a{};
     uint32_t threads = 0, grid = 0;
-    if (pos_geometry(p, &a, &threads, &grid)) {
-        void* args[] = {&a};
-        return hipLaunchKernel(pos_kernel(p, false, false, (int)a.U), dim3(grid), dim3(threads), args, 0, s);
-    }
+    if (pos_geometry(p, &a, &threads, &grid)) return launch_pos(p, a, kPosOne, false, grid, threads, s);
     RowShape rs;
     return rows_shape(p, &rs) ? launch_rows(p, rs, s) : launch_scalar(p, cus, s);
 }
 
-rope_status_t run_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
-                      const int64_t positions_shape[2], const int64_t positions_strides[2], const double* inv_freq,
+rope_status_t run_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, const Positions& in,
                       rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], void* stream,
                       Direction dir)
 {
     Plan p;
     std::string why;
-    rope_status_t st = make_plan_pos(x, x_shape, dtype, positions, positions_shape, positions_strides, inv_freq,
-                                     table_dtype, mode, partial_slice, dir, &p, &why);
+    rope_status_t st = make_plan_pos(x, x_shape, dtype, in, table_dtype, mode, partial_slice, dir, &p, &why);
     if (st != ROPE_OK) return set_error(st, why);
     if (p.noop) return ROPE_OK;
     int cus = 0;
@@ -825,9 +852,8 @@ rope_status_t run_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, con
 // pair's cos and sin evaluated once per position for every tensor;
 // otherwise one launch per tensor.
 rope_status_t run_pos_multi(int32_t count, void* const xs[], const int64_t (*x_shapes)[4], rope_dtype_t dtype,
-                            const int64_t* positions, const int64_t positions_shape[2],
-                            const int64_t positions_strides[2], const double* inv_freq, rope_dtype_t table_dtype,
-                            int64_t mode, const int64_t partial_slice[2], void* stream, Direction dir)
+                            const Positions& in, rope_dtype_t table_dtype, int64_t mode,
+                            const int64_t partial_slice[2], void* stream, Direction dir)
 {
     if (count < 0 || count > kMultiMax)
         return set_error(ROPE_ERR_INVALID, "count must be in [0, " + std::to_string(kMultiMax) + "]");
@@ -837,8 +863,8 @@ rope_status_t run_pos_multi(int32_t count, void* const xs[], const int64_t (*x_s
     int live = 0;
     for (int i = 0; i < count; ++i) {
         std::string why;
-        rope_status_t st = make_plan_pos(xs[i], x_shapes[i], dtype, positions, positions_shape, positions_strides,
-                                         inv_freq, table_dtype, mode, partial_slice, dir, &P[live], &why);
+        rope_status_t st = make_plan_pos(xs[i], x_shapes[i], dtype, in, table_dtype, mode, partial_slice, dir, &P[live],
+                                         &why);
         if (st != ROPE_OK) return set_error(st, "tensor " + std::to_string(i) + ": " + why);
         if (!P[live].noop) ++live;
     }
@@ -881,8 +907,7 @@ rope_status_t run_pos_multi(int32_t count, void* const xs[], const int64_t (*x_s
         together = false;
     }
     if (together) {
-        void* args[] = {&m};
-        err = hipLaunchKernel(pos_multi_kernel(P[0], (int)m.U), dim3(grid), dim3(threads), args, 0, s);
+        err = launch_pos(P[0], m, kPosMulti, false, grid, threads, s);
     } else {
         for (int i = 0; i < live && err == hipSuccess; ++i) err = launch_pos_plan(P[i], cus, s);
     }
@@ -892,15 +917,13 @@ rope_status_t run_pos_multi(int32_t count, void* const xs[], const int64_t (*x_s
 
 // Out of place from positions: the position out-of-place kernel, else a
 // device copy of x into y and the in-place position plan on y.
-rope_status_t run_out_pos(void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype,
-                          const int64_t* positions, const int64_t positions_shape[2],
-                          const int64_t positions_strides[2], const double* inv_freq, rope_dtype_t table_dtype,
-                          int64_t mode, const int64_t partial_slice[2], void* stream, Direction dir)
+rope_status_t run_out_pos(void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const Positions& in,
+                          rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], void* stream,
+                          Direction dir)
 {
     Plan p;
     std::string why;
-    rope_status_t st = make_plan_out_pos(y, x, x_shape, dtype, positions, positions_shape, positions_strides,
-                                         inv_freq, table_dtype, mode, partial_slice, dir, &p, &why);
+    rope_status_t st = make_plan_out_pos(y, x, x_shape, dtype, in, table_dtype, mode, partial_slice, dir, &p, &why);
     if (st != ROPE_OK) return set_error(st, why);
     if (p.noop) return ROPE_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -911,16 +934,14 @@ rope_status_t run_out_pos(void* y, const void* x, const int64_t x_shape[4], rope
         return ROPE_OK;
     }
     if (p.src == nullptr)   // y == x: the in-place call
-        return run_pos(p.x, x_shape, dtype, positions, positions_shape, positions_strides, inv_freq, table_dtype,
-                       mode, partial_slice, stream, dir);
+        return run_pos(p.x, x_shape, dtype, in, table_dtype, mode, partial_slice, stream, dir);
     int cus = 0;
     if ((st = device_cus(&cus)) != ROPE_OK) return st;
     PosArgs a{};
     uint32_t threads = 0, grid = 0;
     if (pos_geometry_out(p, &a, &threads, &grid)) {
-        void* args[] = {&a};
         const bool xchg = a.span <= 64 && 64 % a.span == 0;
-        err = hipLaunchKernel(pos_kernel(p, true, xchg), dim3(grid), dim3(threads), args, 0, s);
+        err = launch_pos(p, a, kPosOut, xchg, grid, threads, s);
     } else {
         err = hipMemcpyAsync(p.x, p.src, (size_t)p.bytes, hipMemcpyDeviceToDevice, s);
         if (err == hipSuccess) err = launch_pos_plan(p, cus, s);
@@ -1201,7 +1222,61 @@ rope_status_t run_multi(int32_t count, void* const xs[], const int64_t (*x_shape
     return ROPE_OK;
 }
 
+// The launch plan of an in-place position call.
+rope_status_t pos_launch_info(const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const Positions& in,
+                              rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+                              int64_t info[ROPE_LAUNCH_INFO_LEN])
+{
+    if (info == nullptr) return set_error(ROPE_ERR_NULLPTR, "info is NULL");
+    for (int i = 0; i < ROPE_LAUNCH_INFO_LEN; ++i) info[i] = 0;
+    Plan p;
+    std::string why;
+    rope_status_t st = make_plan_pos(const_cast<void*>(x), x_shape, dtype, in, table_dtype, mode, partial_slice, kFwd,
+                                     &p, &why);
+    if (st != ROPE_OK) return set_error(st, why);
+    if (p.noop) return ROPE_OK;
+    PosArgs a{};
+    uint32_t threads = 0, grid = 0;
+    RowShape rs;
+    if (pos_geometry(p, &a, &threads, &grid)) {
+        info[0] = ROPE_KERNEL_VECTOR;
+        info[1] = grid;
+        info[2] = threads;
+        info[3] = a.U;
+        info[4] = a.HL;
+        info[5] = a.P;
+        info[6] = a.chunks;
+        info[7] = a.span;
+    } else if (rows_shape(p, &rs)) {
+        info[0] = ROPE_KERNEL_ROWS;
+        info[1] = rs.grid;
+        info[2] = rs.threads;
+        info[4] = rs.rpb;
+        info[7] = rs.tpr;
+    } else {
+        info[0] = ROPE_KERNEL_SCALAR;
+        info[2] = 256;
+    }
+    return ROPE_OK;
+}
+
 }  // namespace
+
+rope_status_t set_error(rope_status_t st, const std::string& msg)
+{
+    g_last_error = msg;
+    return st;
+}
+
+rope_status_t device_cus(int* cus)
+{
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return set_error(ROPE_ERR_RUNTIME, std::string("hipGetDevice: ") + hipGetErrorString(err));
+    *cus = cu_count(dev);
+    return ROPE_OK;
+}
+
 }  // namespace rope
 
 extern "C" {
@@ -1252,8 +1327,8 @@ rope_status_t rope_partial_fwd_inplace_pos(void* x, const int64_t x_shape[4], ro
                                            rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                                            void* stream)
 {
-    return rope::run_pos(x, x_shape, dtype, positions, positions_shape, positions_strides, inv_freq, table_dtype,
-                         mode, partial_slice, stream, rope::kFwd);
+    return rope::run_pos(x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq},
+                         table_dtype, mode, partial_slice, stream, rope::kFwd);
 }
 
 rope_status_t rope_partial_bwd_inplace_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype,
@@ -1262,8 +1337,8 @@ rope_status_t rope_partial_bwd_inplace_pos(void* x, const int64_t x_shape[4], ro
                                            rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                                            void* stream)
 {
-    return rope::run_pos(x, x_shape, dtype, positions, positions_shape, positions_strides, inv_freq, table_dtype,
-                         mode, partial_slice, stream, rope::kBwd);
+    return rope::run_pos(x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq},
+                         table_dtype, mode, partial_slice, stream, rope::kBwd);
 }
 
 rope_status_t rope_partial_fwd_inplace_pos_multi(int32_t count, void* const xs[], const int64_t x_shapes[][4],
@@ -1272,7 +1347,7 @@ rope_status_t rope_partial_fwd_inplace_pos_multi(int32_t count, void* const xs[]
                                                  const double* inv_freq, rope_dtype_t table_dtype, int64_t mode,
                                                  const int64_t partial_slice[2], void* stream)
 {
-    return rope::run_pos_multi(count, xs, x_shapes, dtype, positions, positions_shape, positions_strides, inv_freq,
+    return rope::run_pos_multi(count, xs, x_shapes, dtype, {positions, positions_shape, positions_strides, inv_freq},
                                table_dtype, mode, partial_slice, stream, rope::kFwd);
 }
 
@@ -1282,7 +1357,7 @@ rope_status_t rope_partial_bwd_inplace_pos_multi(int32_t count, void* const xs[]
                                                  const double* inv_freq, rope_dtype_t table_dtype, int64_t mode,
                                                  const int64_t partial_slice[2], void* stream)
 {
-    return rope::run_pos_multi(count, xs, x_shapes, dtype, positions, positions_shape, positions_strides, inv_freq,
+    return rope::run_pos_multi(count, xs, x_shapes, dtype, {positions, positions_shape, positions_strides, inv_freq},
                                table_dtype, mode, partial_slice, stream, rope::kBwd);
 }
 
@@ -1292,7 +1367,7 @@ rope_status_t rope_partial_fwd_out_pos(void* y, const void* x, const int64_t x_s
                                        rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                                        void* stream)
 {
-    return rope::run_out_pos(y, x, x_shape, dtype, positions, positions_shape, positions_strides, inv_freq,
+    return rope::run_out_pos(y, x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq},
                              table_dtype, mode, partial_slice, stream, rope::kFwd);
 }
 
@@ -1302,8 +1377,70 @@ rope_status_t rope_partial_bwd_out_pos(void* y, const void* x, const int64_t x_s
                                        rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                                        void* stream)
 {
-    return rope::run_out_pos(y, x, x_shape, dtype, positions, positions_shape, positions_strides, inv_freq,
+    return rope::run_out_pos(y, x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq},
                              table_dtype, mode, partial_slice, stream, rope::kBwd);
+}
+
+rope_status_t rope_partial_fwd_inplace_axes(
+    void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream)
+{
+    return rope::run_pos(x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                         table_dtype, mode, partial_slice, stream, rope::kFwd);
+}
+
+rope_status_t rope_partial_bwd_inplace_axes(
+    void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream)
+{
+    return rope::run_pos(x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                         table_dtype, mode, partial_slice, stream, rope::kBwd);
+}
+
+rope_status_t rope_partial_fwd_out_axes(
+    void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream)
+{
+    return rope::run_out_pos(y, x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                             table_dtype, mode, partial_slice, stream, rope::kFwd);
+}
+
+rope_status_t rope_partial_bwd_out_axes(
+    void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream)
+{
+    return rope::run_out_pos(y, x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                             table_dtype, mode, partial_slice, stream, rope::kBwd);
+}
+
+rope_status_t rope_partial_fwd_inplace_axes_multi(
+    int32_t count, void* const xs[], const int64_t x_shapes[][4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream)
+{
+    return rope::run_pos_multi(count, xs, x_shapes, dtype,
+                               {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                               table_dtype, mode, partial_slice, stream, rope::kFwd);
+}
+
+rope_status_t rope_partial_bwd_inplace_axes_multi(
+    int32_t count, void* const xs[], const int64_t x_shapes[][4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* stream)
+{
+    return rope::run_pos_multi(count, xs, x_shapes, dtype,
+                               {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                               table_dtype, mode, partial_slice, stream, rope::kBwd);
 }
 
 rope_status_t rope_partial_fwd_inplace_multi(int32_t count, void* const xs[], const int64_t x_shapes[][4],
@@ -1382,38 +1519,18 @@ rope_status_t rope_partial_launch_info_pos(const void* x, const int64_t x_shape[
                                            rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                                            int64_t info[ROPE_LAUNCH_INFO_LEN])
 {
-    if (info == nullptr) return rope::set_error(ROPE_ERR_NULLPTR, "info is NULL");
-    for (int i = 0; i < ROPE_LAUNCH_INFO_LEN; ++i) info[i] = 0;
-    rope::Plan p;
-    std::string why;
-    rope_status_t st = rope::make_plan_pos(const_cast<void*>(x), x_shape, dtype, positions, positions_shape,
-                                           positions_strides, inv_freq, table_dtype, mode, partial_slice, rope::kFwd,
-                                           &p, &why);
-    if (st != ROPE_OK) return rope::set_error(st, why);
-    if (p.noop) return ROPE_OK;
-    rope::PosArgs a{};
-    uint32_t threads = 0, grid = 0;
-    rope::RowShape rs;
-    if (rope::pos_geometry(p, &a, &threads, &grid)) {
-        info[0] = ROPE_KERNEL_VECTOR;
-        info[1] = grid;
-        info[2] = threads;
-        info[3] = a.U;
-        info[4] = a.HL;
-        info[5] = a.P;
-        info[6] = a.chunks;
-        info[7] = a.span;
-    } else if (rope::rows_shape(p, &rs)) {
-        info[0] = ROPE_KERNEL_ROWS;
-        info[1] = rs.grid;
-        info[2] = rs.threads;
-        info[4] = rs.rpb;
-        info[7] = rs.tpr;
-    } else {
-        info[0] = ROPE_KERNEL_SCALAR;
-        info[2] = 256;
-    }
-    return ROPE_OK;
+    return rope::pos_launch_info(x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq},
+                                 table_dtype, mode, partial_slice, info);
+}
+
+rope_status_t rope_partial_launch_info_axes(
+    const void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    int64_t info[ROPE_LAUNCH_INFO_LEN])
+{
+    return rope::pos_launch_info(x, x_shape, dtype, {positions, positions_shape, positions_strides, inv_freq, true, pair_axes},
+                                 table_dtype, mode, partial_slice, info);
 }
 
 rope_status_t rope_proj_fwd(void* y, rope_dtype_t y_dtype, const void* x, const void* w, rope_dtype_t dtype,

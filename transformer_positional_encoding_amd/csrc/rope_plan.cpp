@@ -222,42 +222,56 @@ rope_status_t make_plan_out(void* y, const void* x, const int64_t x_shape[4], ro
     return ROPE_OK;
 }
 
-// The positions and frequencies of the _pos entry points (after the no-op
-// test): pointers, the {1 or B, S} shape, non-negative strides and 64-bit
-// offsets. Fills p's position fields.
-static rope_status_t check_positions(const int64_t x_shape[4], const int64_t* positions,
-                                     const int64_t positions_shape[2], const int64_t positions_strides[2],
-                                     const double* inv_freq, Plan* p, std::string* why)
+rope_status_t check_positions(int64_t B, int64_t S, int64_t L, const Positions& in, Plan* p, std::string* why)
 {
-    if (positions == nullptr) return fail(ROPE_ERR_NULLPTR, why, "positions is NULL");
-    if (inv_freq == nullptr) return fail(ROPE_ERR_NULLPTR, why, "inv_freq is NULL");
-    if (positions_shape == nullptr || positions_strides == nullptr)
+    if (in.data == nullptr) return fail(ROPE_ERR_NULLPTR, why, "positions is NULL");
+    if (in.inv_freq == nullptr) return fail(ROPE_ERR_NULLPTR, why, "inv_freq is NULL");
+    if (in.shape == nullptr || in.strides == nullptr)
         return fail(ROPE_ERR_NULLPTR, why, "positions shape or strides is NULL");
-    if (positions_shape[0] != 1 && positions_shape[0] != x_shape[0])
-        return fail(ROPE_ERR_INVALID, why, "positions: dimension B is " + std::to_string(positions_shape[0])
-                                               + ", must be 1 or " + std::to_string(x_shape[0]));
-    if (positions_shape[1] != x_shape[1])
-        return fail(ROPE_ERR_INVALID, why, "positions: dimension S is " + std::to_string(positions_shape[1])
-                                               + ", must be " + std::to_string(x_shape[1]));
-    if (positions_strides[0] < 0 || positions_strides[1] < 0)
+    if (in.axes && in.pair_axes == nullptr) return fail(ROPE_ERR_NULLPTR, why, "pair_axes is NULL");
+    const int64_t A = in.axes ? in.shape[0] : 1;
+    if (A < 1 || A > ROPE_AXES_MAX)
+        return fail(ROPE_ERR_INVALID, why, "positions: dimension A is " + std::to_string(A) + ", must be 1 to "
+                                               + std::to_string(ROPE_AXES_MAX));
+    const int64_t* shape = in.shape + (in.axes ? 1 : 0);
+    const int64_t* strides = in.strides + (in.axes ? 1 : 0);
+    if (shape[0] != 1 && shape[0] != B)
+        return fail(ROPE_ERR_INVALID, why, "positions: dimension B is " + std::to_string(shape[0])
+                                               + ", must be 1 or " + std::to_string(B));
+    if (shape[1] != S)
+        return fail(ROPE_ERR_INVALID, why, "positions: dimension S is " + std::to_string(shape[1])
+                                               + ", must be " + std::to_string(S));
+    if (strides[0] < 0 || strides[1] < 0 || in.strides[0] < 0)
         return fail(ROPE_ERR_INVALID, why, "positions: negative stride");
-    const int64_t sb = positions_shape[0] == 1 ? 0 : positions_strides[0];
-    const int64_t ss = positions_shape[1] == 1 ? 0 : positions_strides[1];
-    int64_t part_b, part_s;
-    if (!mul_ok(sb, positions_shape[0] - 1, &part_b) || !mul_ok(ss, positions_shape[1] - 1, &part_s) ||
-        part_b > std::numeric_limits<int64_t>::max() - part_s)
+    const int64_t sa = A == 1 ? 0 : in.strides[0];
+    const int64_t sb = shape[0] == 1 ? 0 : strides[0];
+    const int64_t ss = shape[1] == 1 ? 0 : strides[1];
+    int64_t part_a, part_b, part_s;
+    if (!mul_ok(sa, A - 1, &part_a) || !mul_ok(sb, shape[0] - 1, &part_b) || !mul_ok(ss, shape[1] - 1, &part_s) ||
+        part_b > std::numeric_limits<int64_t>::max() - part_s ||
+        part_a > std::numeric_limits<int64_t>::max() - part_s - part_b)
         return fail(ROPE_ERR_INVALID, why, "positions: strides overflow 64-bit offsets");
-    p->pos = positions;
-    p->inv_freq = inv_freq;
+    if (in.axes) {
+        for (int64_t i = 0; i < L / 2; ++i) {
+            if (in.pair_axes[i] < 0 || in.pair_axes[i] >= A)
+                return fail(ROPE_ERR_INVALID, why, "pair_axes: pair " + std::to_string(i) + " has axis "
+                                                       + std::to_string(in.pair_axes[i]) + ", must be 0 to "
+                                                       + std::to_string(A - 1));
+            p->axis_words[i / 16] |= (uint32_t)in.pair_axes[i] << (i % 16 * 2);
+        }
+        p->naxes = (int)A;
+        p->pos_sa = sa;
+    }
+    p->pos = in.data;
+    p->inv_freq = in.inv_freq;
     p->pos_sb = sb;
     p->pos_ss = ss;
     return ROPE_OK;
 }
 
-rope_status_t make_plan_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
-                            const int64_t positions_shape[2], const int64_t positions_strides[2],
-                            const double* inv_freq, rope_dtype_t table_dtype, int64_t mode,
-                            const int64_t partial_slice[2], Direction dir, Plan* plan, std::string* why)
+rope_status_t make_plan_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, const Positions& in,
+                            rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], Direction dir,
+                            Plan* plan, std::string* why)
 {
     Plan p;
     int64_t numel = 0;
@@ -269,7 +283,7 @@ rope_status_t make_plan_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtyp
         return ROPE_OK;
     }
     if (x == nullptr) return fail(ROPE_ERR_NULLPTR, why, "x is NULL");
-    st = check_positions(x_shape, positions, positions_shape, positions_strides, inv_freq, &p, why);
+    st = check_positions(p.B, p.S, p.L, in, &p, why);
     if (st != ROPE_OK) return st;
     p.x = x;
     *plan = p;
@@ -277,10 +291,8 @@ rope_status_t make_plan_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtyp
 }
 
 rope_status_t make_plan_out_pos(void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype,
-                                const int64_t* positions, const int64_t positions_shape[2],
-                                const int64_t positions_strides[2], const double* inv_freq,
-                                rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
-                                Direction dir, Plan* plan, std::string* why)
+                                const Positions& in, rope_dtype_t table_dtype, int64_t mode,
+                                const int64_t partial_slice[2], Direction dir, Plan* plan, std::string* why)
 {
     Plan p;
     int64_t numel = 0;
@@ -302,7 +314,7 @@ rope_status_t make_plan_out_pos(void* y, const void* x, const int64_t x_shape[4]
         p.noop = same;
         p.copy_only = !same;
     } else {
-        st = check_positions(x_shape, positions, positions_shape, positions_strides, inv_freq, &p, why);
+        st = check_positions(p.B, p.S, p.L, in, &p, why);
         if (st != ROPE_OK) return st;
     }
     p.x = y;

@@ -44,7 +44,32 @@ struct Plan {
     const int64_t* pos = nullptr;
     const double* inv_freq = nullptr;
     int64_t pos_sb = 0, pos_ss = 0;
+    // Several position axes (the _axes entry points): naxes > 0, the
+    // position of (b,s) on axis k lies k*pos_sa further, and pair i's axis is
+    // the two bits (i % 16)*2 of word i / 16.
+    int naxes = 0;
+    int64_t pos_sa = 0;
+    uint32_t axis_words[ROPE_D_LIMIT / 2 / 16] = {};
 };
+
+// The positions of a _pos or _axes call as the C ABI passes them. axes:
+// shape and strides hold {A, Bp, S} instead of {Bp, S}, and pair_axes the
+// axis of each of the L/2 pairs.
+struct Positions {
+    const int64_t* data = nullptr;
+    const int64_t* shape = nullptr;
+    const int64_t* strides = nullptr;
+    const double* inv_freq = nullptr;
+    bool axes = false;
+    const int32_t* pair_axes = nullptr;
+};
+
+// Check a call's positions, frequencies and axes against a tensor of B
+// batches of S rows whose slice has L > 0 lanes, and fill p's position
+// fields: NULL pointers, positions_shape {1 or B, S} (axes: 1 to
+// ROPE_AXES_MAX in front), strides >= 0 (a size-1 dimension's stride is
+// ignored) whose offsets fit in 64 bits, every pair's axis among them.
+rope_status_t check_positions(int64_t B, int64_t S, int64_t L, const Positions& in, Plan* p, std::string* why);
 
 // Validate the C-ABI arguments in the documented order and fill `plan`.
 // On failure returns the status and writes a one-line reason to `why`.
@@ -66,25 +91,19 @@ rope_status_t make_plan_out(void* y, const void* x, const int64_t x_shape[4], ro
                             rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                             Direction dir, Plan* plan, std::string* why);
 
-// The _pos form: cos and sin come from positions and per-pair frequencies
-// (checked in place of the tables). Checks, in order: the scalar arguments
-// of make_plan; an empty tensor or slice is a no-op; NULL x, positions,
-// inv_freq, positions_shape or positions_strides; positions_shape is
-// {1 or B, S} with strides >= 0 (a size-1 dimension's stride is ignored)
-// whose offsets fit in 64 bits.
-rope_status_t make_plan_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, const int64_t* positions,
-                            const int64_t positions_shape[2], const int64_t positions_strides[2],
-                            const double* inv_freq, rope_dtype_t table_dtype, int64_t mode,
-                            const int64_t partial_slice[2], Direction dir, Plan* plan, std::string* why);
+// The _pos and _axes forms: cos and sin come from positions and per-pair
+// frequencies (checked in place of the tables). Checks, in order: the scalar
+// arguments of make_plan; an empty tensor or slice is a no-op; NULL x; then
+// check_positions.
+rope_status_t make_plan_pos(void* x, const int64_t x_shape[4], rope_dtype_t dtype, const Positions& in,
+                            rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], Direction dir,
+                            Plan* plan, std::string* why);
 
-// Out of place from positions: the checks of make_plan_out with those of
-// make_plan_pos in place of the table checks (positions, frequencies,
-// shape and strides), in that order.
+// Out of place from positions: the checks of make_plan_out with
+// check_positions in place of the table checks, in that order.
 rope_status_t make_plan_out_pos(void* y, const void* x, const int64_t x_shape[4], rope_dtype_t dtype,
-                                const int64_t* positions, const int64_t positions_shape[2],
-                                const int64_t positions_strides[2], const double* inv_freq,
-                                rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
-                                Direction dir, Plan* plan, std::string* why);
+                                const Positions& in, rope_dtype_t table_dtype, int64_t mode,
+                                const int64_t partial_slice[2], Direction dir, Plan* plan, std::string* why);
 
 // The projection with a rotary epilogue (rope_proj_fwd): y (B,S,H,Dh) =
 // x (B*S, K) . w (H*Dh, K)^T, each head's slice rotated. `rope` holds y's

@@ -5,6 +5,8 @@
 // that selects and launches them.
 #pragma once
 
+#include <type_traits>
+
 #include "rope_vec_kernels.hpp"
 
 namespace rope {
@@ -247,6 +249,50 @@ struct PosArgs {
     FastDiv xcd_div;
 };
 
+// Positions on several axes (time, height, width): every pair has its axis,
+// and its angle is the position on that axis times the pair's frequency. The
+// axes of the pairs are kernel arguments, two bits each (at most 512 pairs,
+// 32 words). A thread that evaluates a pair loads the (b,s) position on every
+// axis and the pair's word at once and then selects: reading the word first
+// and then the one position would put a second memory latency in front of
+// the evaluation, which the block's other loads do not hide when it holds
+// few heads. On MI355X, bf16 rotate_half heads of 128 lanes, three axes,
+// against the same call with one axis: see the measurements at the kernels.
+struct PosAxes {
+    int64_t sa;              // axis k's positions lie k*sa further
+    uint32_t last;           // axes - 1
+    uint32_t words[ROPE_D_LIMIT / 2 / 16];
+};
+
+struct PosAxesArgs : PosArgs {
+    PosAxes ax;
+};
+
+// The axis of pair i.
+__device__ __forceinline__ uint32_t pair_axis(const PosAxes& ax, uint32_t i)
+{
+    return (ax.words[i >> 4] >> ((i & 15u) * 2)) & 3u;
+}
+
+// The position of pair i of the (b,s) whose first axis is at p.
+__device__ __forceinline__ int64_t axis_position(const PosAxes& ax, const int64_t* p, uint32_t i)
+{
+    const int64_t p0 = p[0];
+    const int64_t p1 = p[ax.last < 1 ? 0 : ax.sa];
+    const int64_t p2 = p[(ax.last < 2 ? ax.last : 2) * ax.sa];
+    const int64_t p3 = p[ax.last * ax.sa];
+    const uint32_t k = pair_axis(ax, i);
+    return k & 2u ? (k & 1u ? p3 : p2) : (k & 1u ? p1 : p0);
+}
+
+// The position of pair i at offset `off` of the positions.
+template <class ARGS>
+__device__ __forceinline__ int64_t pair_position(const ARGS& a, int64_t off, uint32_t i)
+{
+    if constexpr (std::is_same<ARGS, PosAxesArgs>::value) return axis_position(a.ax, a.pos + off, i);
+    else return a.pos[off];
+}
+
 // The block's first item under the XCD runs (a bijection of [0, gridDim.x)).
 __device__ __forceinline__ uint32_t pos_first_item(const PosArgs& a)
 {
@@ -274,14 +320,15 @@ __device__ __forceinline__ uint32_t pos_row(const PosArgs& a, uint32_t g, uint32
 
 // The (cos, sin) entries past the first blockDim of the block's table:
 // entry e is pair e % pairs of the block's position g0 + e / pairs.
-template <int TT>
-__device__ __forceinline__ void pos_fill_rest(const PosArgs& a, uint32_t g0, float2* cs)
+template <int TT, class ARGS>
+__device__ __forceinline__ void pos_fill_rest(const ARGS& a, uint32_t g0, float2* cs)
 {
     for (uint32_t e = threadIdx.x + blockDim.x; e < a.entries; e += blockDim.x) {
         const uint32_t q = fast_div(e, a.pairs_div);
         const uint32_t ge = g0 + q;
         if (ge >= a.bs) break;                    // later entries belong to later positions
-        cs[e] = pos_cos_sin<TT>(a.pos[pos_offset(a, ge)], a.inv_freq[e - q * a.pairs]);
+        const uint32_t i = e - q * a.pairs;
+        cs[e] = pos_cos_sin<TT>(pair_position(a, pos_offset(a, ge), i), a.inv_freq[i]);
     }
 }
 
@@ -314,8 +361,8 @@ __device__ __forceinline__ v4u* pos_row_vec(const PosArgs& a, uint32_t g, uint32
     }
 }
 
-template <int DT, int TT, int DIR, int MODE, bool MULTI, int U>
-__global__ void __launch_bounds__(256) rope_pos_kernel(PosArgs a)
+template <int DT, int TT, int DIR, int MODE, bool MULTI, int U, class ARGS = PosArgs>
+__global__ void __launch_bounds__(256) rope_pos_kernel(ARGS a)
 {
     __shared__ float2 cs[kPosLds];   // (cos, sin) of the block's positions, pair-major per position
     constexpr int K = Store<DT>::kLanes;
@@ -345,7 +392,7 @@ __global__ void __launch_bounds__(256) rope_pos_kernel(PosArgs a)
         const uint32_t g0 = grp * a.P;                        // the block's first position
         const uint32_t ge = g0 + eq;                          // the position of entry t
         const bool fill = t < a.entries && ge < a.bs;
-        const int64_t p0 = a.pos[pos_offset(a, min(ge, a.bs - 1))];
+        const int64_t p0 = pair_position(a, pos_offset(a, min(ge, a.bs - 1)), ei);
         const double f0 = a.inv_freq[ei];
         __builtin_amdgcn_sched_barrier(0);
         const uint32_t g = g0 + pp;
@@ -413,8 +460,8 @@ __global__ void __launch_bounds__(256) rope_pos_kernel(PosArgs a)
 // row's threads never straddle a wave); otherwise it is loaded from src as
 // well. Blocks, positions, loads and the LDS entries are those of the
 // in-place kernel above.
-template <int DT, int TT, int DIR, int MODE, bool XCHG>
-__global__ void __launch_bounds__(256) rope_pos_out_kernel(PosArgs a)
+template <int DT, int TT, int DIR, int MODE, bool XCHG, class ARGS = PosArgs>
+__global__ void __launch_bounds__(256) rope_pos_out_kernel(ARGS a)
 {
     __shared__ float2 cs[kPosLds];
     constexpr int K = Store<DT>::kLanes;
@@ -448,7 +495,7 @@ __global__ void __launch_bounds__(256) rope_pos_out_kernel(PosArgs a)
         const uint32_t g0 = grp * a.P;                        // the block's first position
         const uint32_t ge = g0 + eq;                          // the position of entry t
         const bool fill = t < a.entries && ge < a.bs;
-        const int64_t p0 = a.pos[pos_offset(a, min(ge, a.bs - 1))];
+        const int64_t p0 = pair_position(a, pos_offset(a, min(ge, a.bs - 1)), ei);
         const double f0 = a.inv_freq[ei];
         __builtin_amdgcn_sched_barrier(0);
         const uint32_t g = g0 + pp;
