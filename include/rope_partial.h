@@ -396,6 +396,119 @@ ROPE_API rope_status_t rope_partial_bwd_inplace_axes_multi(
     const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
     void* stream);
 
+/* ===================== paged key/value cache, quantised ===================== */
+
+/* how a cache holds its lanes */
+typedef enum rope_cache_format {
+    ROPE_CACHE_F32 = 0,   /* the storage types, as rope_dtype_t: no scales */
+    ROPE_CACHE_F16 = 1,
+    ROPE_CACHE_BF16 = 2,
+    ROPE_CACHE_E4M3 = 3,  /* 8-bit float, 4 exponent and 3 fraction bits, largest value 448 */
+    ROPE_CACHE_INT8 = 4,  /* -127 to 127 */
+    ROPE_CACHE_INT4 = 5   /* -7 to 7, two's complement; lane 2i in the low half of byte i, 2i+1 in the high half */
+} rope_cache_format_t;
+
+/*
+ * A paged cache of keys or values: `pages` pages of `page_size` slots, each
+ * slot holding `heads` rows of `dim` lanes. Slot number t is slot t %
+ * page_size of page t / page_size. A quantised format keeps one fp32 scale
+ * for every `group` lanes of a row: lane j stands for code[j] * scale[j / group].
+ */
+typedef struct rope_cache {
+    void* data;               /* device; the lanes of a row are consecutive */
+    float* scales;            /* device; the scales of a row are consecutive; NULL for the storage types */
+    int32_t format;           /* rope_cache_format_t */
+    int64_t pages, page_size, heads, dim;
+    int64_t group;            /* lanes per scale: even, divides dim (ignored for the storage types) */
+    int64_t strides[3];       /* BYTES from one page, slot and head to the next */
+    int64_t scale_strides[3]; /* floats from one page, slot and head to the next */
+} rope_cache_t;
+
+/* Rows of a (B, S, N, D) tensor whose last dimension is consecutive. */
+typedef struct rope_rows {
+    void* data;               /* device */
+    int64_t N, D;
+    int64_t strides[3];       /* elements from one b, s and n to the next, each >= 0 */
+} rope_rows_t;
+
+/*
+ * rope_cache_write -- rotate the keys of B x S tokens and write them, with
+ * the values, to their slots of a cache, quantised; and rotate the queries
+ * beside them. One launch. For each token (b,s) with slot t = slots[b,s] in
+ * [0, pages * page_size):
+ *   z = k[b,s,h,:] with its slice rotated from positions (forward, fp32, as
+ *       rope_partial_fwd_inplace_axes; never rounded to the storage type)
+ *       when rotate_k is not 0, else k itself;
+ *   quantised formats, for each group of lanes: m = the largest |z_j| of the
+ *       finite lanes, scale = m / Q rounded to fp32 and at least 2^-100 (1
+ *       when m = 0), code_j = z_j / scale (the exact quotient of the two
+ *       numbers) rounded once to the nearest code, ties to even. Q is 448
+ *       (e4m3), 127 or 7. An infinite lane takes the code of +-m, a NaN lane
+ *       NaN (e4m3) or 0: it does not touch the lanes beside it;
+ *   storage types: z rounded once.
+ * v is written the same way without rotation. Every other slot keeps its
+ * bytes: a token whose slot is negative or past the cache is not written
+ * (the padding of a batch). Slots of one call must differ; what a slot given
+ * twice holds afterwards is unspecified. q is rotated in place, for every
+ * token.
+ *
+ *   B, S        tokens; dtype: storage type of q, k and v.
+ *   q, v        NULL when there is none. q has k's D.
+ *   k, v        (B, S, heads, dim) of their cache; read only; any strides.
+ *   v_cache     NULL exactly when v is; pages and page_size of k_cache.
+ *               k and v caches: formats that are quantised, or `dtype`.
+ *   slots       device int64, at b*slots_strides[0] + s*slots_strides[1].
+ *   positions, positions_shape {A, Bp, S}, positions_strides, inv_freq,
+ *   pair_axes, table_dtype, mode, partial_slice
+ *               as for rope_partial_fwd_inplace_axes; pair_axes may be NULL
+ *               when A is 1. With an empty slice, or neither q nor rotate_k,
+ *               nothing is rotated and positions are not looked at.
+ *
+ * q must not share a byte with itself (rows that overlap are refused), nor
+ * with k, v or the caches (not checked: the rows of one fused projection lie
+ * between each other). Checks, in order: B, S, dtype, k, k_cache, v and
+ * v_cache present (ROPE_ERR_NULLPTR); mode, slice and types as
+ * rope_partial_fwd_inplace on k's shape; the caches' fields; q and v against
+ * them; strides; no token or no lanes: ROPE_OK; NULL data; then positions.
+ * ROPE_ERR_UNSUPPORTED: 2^31 rows of q, k and v or more. Asynchronous on
+ * `stream`; nothing is allocated; deterministic.
+ */
+ROPE_API rope_status_t rope_cache_write(
+    int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* q, const rope_rows_t* k, const rope_rows_t* v,
+    const rope_cache_t* k_cache, const rope_cache_t* v_cache, const int64_t* slots, const int64_t slots_strides[2],
+    const int64_t* positions, const int64_t positions_shape[3], const int64_t positions_strides[3],
+    const double* inv_freq, const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode,
+    const int64_t partial_slice[2], int32_t rotate_k, void* stream);
+
+/*
+ * rope_cache_read -- read cached tokens back: for every sequence b and s in
+ * [0, min(lengths[b], S)), token t = starts[b] + s of the sequence is slot
+ * t % page_size of page block_table[b, t / page_size], and
+ *   out[b,s,h,j] = code_j * scale (fp32), its slice rotated from positions
+ *                  when they are given, rounded once to `dtype`.
+ * Keys stored unrotated are rotated this way, and rotated ones moved to
+ * other positions. Every other row of out keeps its bytes: s >= lengths[b],
+ * tokens before 0 or past the block table, and pages outside [0, pages).
+ *
+ *   out           (B, S, heads, dim) rows of `dtype`; rows must not overlap.
+ *   cache         any quantised format, or the format of `dtype`.
+ *   block_table   device int32, B rows of table_pages pages, row b at
+ *                 b * table_stride.
+ *   lengths       device int32 (B); starts: device int32 (B) or NULL (0).
+ *   positions     NULL: nothing is rotated and the arguments up to
+ *                 partial_slice but table_dtype and mode are not looked at;
+ *                 else as for rope_cache_write, for out's (b,s).
+ *
+ * Checks, in order: as rope_cache_write's for its arguments; an empty out is
+ * ROPE_OK; NULL data, block_table or lengths; positions.
+ */
+ROPE_API rope_status_t rope_cache_read(
+    int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* out, const rope_cache_t* cache,
+    const int32_t* block_table, int64_t table_pages, int64_t table_stride, const int32_t* lengths,
+    const int32_t* starts, const int64_t* positions, const int64_t positions_shape[3],
+    const int64_t positions_strides[3], const double* inv_freq, const int32_t* pair_axes, rope_dtype_t table_dtype,
+    int64_t mode, const int64_t partial_slice[2], void* stream);
+
 /* ====================== checks and launch plans ====================== */
 
 /*

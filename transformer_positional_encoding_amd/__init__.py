@@ -28,7 +28,7 @@ __all__ = [
     "rope_partial_fwd_inplace_axes", "rope_partial_bwd_inplace_axes", "rope_partial_fwd_out_axes",
     "rope_partial_bwd_out_axes", "rope_partial_fwd_inplace_axes_multi", "rope_partial_bwd_inplace_axes_multi",
     "inplace_partial_rotary_mul_axes", "partial_rotary_mul_axes", "rope_pair_axes", "rope_axes_inv_freq", "AXES_MAX",
-    "rope_proj_fwd", "RopeError", "library", "LIB_PATH", "ROPE_OK", "ROPE_ERR_NULLPTR", "ROPE_ERR_INVALID",
+    "RopeCache", "rope_cache", "rope_cache_write", "rope_cache_read", "CACHE_FORMATS", "rope_proj_fwd", "RopeError", "library", "LIB_PATH", "ROPE_OK", "ROPE_ERR_NULLPTR", "ROPE_ERR_INVALID",
     "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_RUNTIME", "MODES", "DTYPE_CODES",
 ]
 
@@ -40,6 +40,7 @@ MODES = {"rotate_half": 0, "interleave": 1}
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 MULTI_MAX = 4
 AXES_MAX = 4
+CACHE_FORMATS = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3, "int8": 4, "int4": 5}
 
 _I64x4 = ctypes.c_int64 * 4
 _I64x3 = ctypes.c_int64 * 3
@@ -59,6 +60,20 @@ class RopeError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
         super().__init__(f"{rope_status_string(status)}: {detail}" if detail else rope_status_string(status))
+
+
+class RopeRows(ctypes.Structure):
+    """The C ABI's rope_rows_t."""
+    _fields_ = [("data", ctypes.c_void_p), ("N", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("strides", ctypes.c_int64 * 3)]
+
+
+class RopeCacheStruct(ctypes.Structure):
+    """The C ABI's rope_cache_t."""
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("group", ctypes.c_int64), ("strides", ctypes.c_int64 * 3),
+                ("scale_strides", ctypes.c_int64 * 3)]
 
 
 _lib = None
@@ -117,6 +132,15 @@ def library() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = ctypes.c_int
             f.argtypes = [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p] + _ENTRY_ARGTYPES[2:]
+        i64p, vp = ctypes.POINTER(ctypes.c_int64), ctypes.c_void_p
+        turn = [vp, i64p, i64p, vp, vp, ctypes.c_int, ctypes.c_int64, i64p]   # positions to partial_slice
+        rows, cache = ctypes.POINTER(RopeRows), ctypes.POINTER(RopeCacheStruct)
+        L.rope_cache_write.restype = ctypes.c_int
+        L.rope_cache_write.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, rows, rows, rows, cache, cache, vp,
+                                       i64p] + turn + [ctypes.c_int32, vp]
+        L.rope_cache_read.restype = ctypes.c_int
+        L.rope_cache_read.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, rows, cache, vp, ctypes.c_int64,
+                                      ctypes.c_int64, vp, vp] + turn + [vp]
         L.rope_partial_check.restype = ctypes.c_int
         L.rope_partial_check.argtypes = _ENTRY_ARGTYPES[:-1]
         L.rope_partial_launch_info.restype = ctypes.c_int
@@ -1141,6 +1165,264 @@ def rope_partial_bwd_inplace_axes_multi(xs, positions, inv_freq, pair_axes, rota
                                         partial_slice=None, table_dtype=None, stream=None) -> None:
     """Backward of :func:`rope_partial_fwd_inplace_axes_multi`."""
     _call_pos_multi("bwd", xs, positions, inv_freq, rotary_mode, partial_slice, table_dtype, stream, pair_axes)
+
+
+# ------------------------------------------------------------------- paged, quantised cache
+
+_CACHE_FORMAT_OF = {}
+
+
+def _cache_format(dtype):
+    if not _CACHE_FORMAT_OF:
+        import torch
+        _CACHE_FORMAT_OF.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3,
+                                 torch.int8: 4, torch.uint8: 5})
+    return _CACHE_FORMAT_OF.get(dtype)
+
+
+class RopeCache:
+    """A paged cache of keys or values, over tensors that the caller owns:
+    slot t is ``data[t // page_size, t % page_size]``.
+
+    data: (pages, page_size, heads, dim) of float32, float16 or bfloat16 (no
+    scales), float8_e4m3fn, or int8; or (pages, page_size, heads, dim // 2) of
+    uint8, two 4-bit codes a byte. Any strides (for example one half of a
+    (pages, 2, page_size, heads, dim) tensor), the lanes of a row consecutive.
+    scales: (pages, page_size, heads, dim // group) of float32 for the
+    quantised formats: lane j of a row stands for code[j] * scale[j // group].
+    """
+
+    __slots__ = ("data", "scales", "device", "struct")
+
+    def __init__(self, data, scales=None):
+        import torch
+        if not isinstance(data, torch.Tensor) or data.dim() != 4:
+            raise ValueError("data must be a 4-D torch.Tensor (pages, page_size, heads, dim)")
+        fmt = _cache_format(data.dtype)
+        if fmt is None:
+            raise TypeError(f"unsupported cache type {data.dtype}")
+        shape, st, es = data.shape, data.stride(), data.element_size()
+        if shape[3] > 1 and st[3] != 1:
+            raise ValueError("data: the lanes of a row must be consecutive")
+        dim = shape[3] * 2 if fmt == 5 else shape[3]
+        c = RopeCacheStruct(data.data_ptr() or None, None, fmt, shape[0], shape[1], shape[2], dim, dim,
+                            (st[0] * es, st[1] * es, st[2] * es))
+        if fmt >= 3:
+            if not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32:
+                raise TypeError("a quantised cache needs float32 scales")
+            if scales.dim() != 4 or scales.shape[:3] != shape[:3] or scales.device != data.device:
+                raise ValueError("scales must be (pages, page_size, heads, dim // group), on data's device")
+            groups, sc = scales.shape[3], scales.stride()
+            if dim and (groups < 1 or dim % groups):
+                raise ValueError(f"{groups} scales do not divide {dim} lanes")
+            if groups > 1 and sc[3] != 1:
+                raise ValueError("scales: the scales of a row must be consecutive")
+            c.scales = scales.data_ptr() or None
+            c.group = dim // groups if groups else 0
+            c.scale_strides[:] = sc[:3]
+        elif scales is not None:
+            raise ValueError(f"a {data.dtype} cache has no scales")
+        self.data, self.scales, self.device, self.struct = data, scales, data.device, c
+
+    @property
+    def group(self) -> int:
+        """Lanes per scale."""
+        return self.struct.group
+
+
+def rope_cache(pages: int, page_size: int, heads: int, dim: int, format: str = "e4m3", group: int | None = None,
+               device=None) -> RopeCache:
+    """A new zeroed cache of a CACHE_FORMATS format, ``group`` lanes per scale
+    (default: a row)."""
+    import torch
+    types = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn,
+             "int8": torch.int8, "int4": torch.uint8}
+    if format not in types:
+        raise ValueError(f"format must be one of {sorted(types)}")
+    device = "cuda" if device is None else device
+    data = torch.zeros(pages, page_size, heads, dim // 2 if format == "int4" else dim, dtype=types[format],
+                       device=device)
+    if CACHE_FORMATS[format] < 3:
+        return RopeCache(data)
+    group = dim if group is None else group
+    if group < 1 or dim % group:
+        raise ValueError(f"group {group} does not divide {dim} lanes")
+    return RopeCache(data, torch.zeros(pages, page_size, heads, dim // group, device=device))
+
+
+def _rows(name, t):
+    """A (B, S, N, D) tensor as the C ABI's rows."""
+    shape, st = t.shape, t.stride()
+    if shape[3] > 1 and st[3] != 1:
+        raise ValueError(f"{name}: the lanes of a row must be consecutive")
+    return RopeRows(t.data_ptr() or None, shape[2], shape[3], st[:3])
+
+
+def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, dtype_code, device):
+    """The C arguments from positions to partial_slice of a cache call, and
+    the tensors that have to be on `device`."""
+    import torch
+    mode = rotary_mode
+    if isinstance(mode, str):
+        if mode not in MODES:
+            raise ValueError(f"rotary_mode must be one of {sorted(MODES)}")
+        mode = MODES[mode]
+    if table_dtype is None:
+        tdt = dtype_code
+    else:
+        tdt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(table_dtype, DTYPE_CODES.get(table_dtype))
+        if tdt is None:
+            raise TypeError(f"unsupported table dtype {table_dtype}")
+    if positions is None or partial_slice is None:
+        return (None, None, None, None, None, tdt, mode, None)
+    start, end = int(partial_slice[0]), int(partial_slice[1])
+    for name, t in (("positions", positions), ("inv_freq", inv_freq)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+    if positions.dtype != torch.int64 or positions.dim() not in (2, 3):
+        raise ValueError("positions must be an int64 tensor (B or 1, S), or (A, B or 1, S) with pair_axes")
+    shape, st = tuple(positions.shape), tuple(positions.stride())
+    if positions.dim() == 2:
+        if pair_axes is not None:
+            raise ValueError("pair_axes goes with positions (A, B or 1, S)")
+        shape, st = (1,) + shape, (0,) + st
+    else:
+        if pair_axes is None:
+            raise ValueError("positions on several axes need pair_axes")
+        pair_axes = _check_pair_axes(positions, pair_axes, partial_slice)
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous 1-D float64 tensor")
+    if end > start and inv_freq.numel() != (end - start) // 2:
+        raise ValueError(f"inv_freq must hold (end - start) / 2 = {(end - start) // 2} frequencies")
+    return (positions.data_ptr() or None, _I64x3(*shape), _I64x3(*st), inv_freq.data_ptr() or None,
+            None if pair_axes is None else _i32_array(pair_axes), tdt, mode, _I64x2(start, end))
+
+
+def _stream_handle(stream, device):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return getattr(stream, "cuda_stream", stream)
+
+
+def rope_cache_write(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None, rotary_mode="interleave",
+                     partial_slice=None, q=None, pair_axes=None, table_dtype=None, rotate_k: bool = True,
+                     stream=None) -> None:
+    """Rotate ``k[..., start:end)`` from positions and write it, with ``v``, to
+    its slots of paged caches, quantised; rotate ``q`` in place beside it. One
+    launch (two when v's format is not k's).
+
+    k: (B, S, heads, dim) GPU tensor, float32/float16/bfloat16, any strides
+    with consecutive lanes (a slice of a fused projection's output); v: the
+    same of v_cache's heads and dim, or None with v_cache None; q: (B, S, any,
+    dim) or None.
+    k_cache, v_cache: :class:`RopeCache` of a quantised format or of k's type.
+    slots: int64 (B, S), the slot each token goes to (page * page_size +
+    offset); a negative one, or one past the cache, writes nothing. Slots of
+    one call must differ.
+    positions: int64 (B or 1, S), or (A, B or 1, S) with ``pair_axes`` (see
+    :func:`rope_partial_fwd_inplace_axes`), or None: nothing is rotated.
+    rotate_k=False stores k unrotated (q is still rotated), for a
+    :func:`rope_cache_read` that rotates.
+
+    The rotation is fp32 and k is not rounded before it is quantised: for
+    each group of lanes scale = largest finite magnitude / Q (448 for e4m3,
+    127, 7), code = k / scale rounded once to the nearest, ties to even."""
+    import torch
+    for name, t in (("k", k), ("v", v), ("q", q)):
+        if t is None and name != "k":
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a 4-D torch.Tensor (B, S, heads, dim)")
+        if t.dtype != k.dtype:
+            raise TypeError("q, k and v must share a dtype")
+        if t.shape[:2] != k.shape[:2]:
+            raise ValueError(f"{name} must have k's tokens")
+        if t.numel() and not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.device != k.device:
+            raise ValueError(f"{name} must be on {k.device}")
+    code, dev = _dtype_code(k), k.device
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c is None and name == "v_cache":
+            continue
+        if not isinstance(c, RopeCache):
+            raise TypeError(f"{name} must be a RopeCache")
+        if c.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or slots.shape != k.shape[:2]:
+        raise ValueError("slots must be an int64 tensor (B, S)")
+    if slots.device != dev:
+        raise ValueError(f"slots must be on {dev}")
+    turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
+    B, S = k.shape[:2]
+    switch = k.is_cuda and dev.index != torch.cuda.current_device()
+    handle = _stream_handle(stream, dev) if k.is_cuda else None
+    with torch.cuda.device(dev) if switch else _nullcontext():
+        st = library().rope_cache_write(
+            B, S, code, None if q is None else _rows("q", q), _rows("k", k), None if v is None else _rows("v", v),
+            k_cache.struct, None if v_cache is None else v_cache.struct, slots.data_ptr() or None,
+            _I64x2(*slots.stride()), *turn, 1 if rotate_k else 0, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
+
+
+def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=None, inv_freq=None,
+                    rotary_mode="interleave", partial_slice=None, pair_axes=None, table_dtype=None,
+                    stream=None) -> None:
+    """Read cached tokens back: ``out[b, s]`` becomes token ``starts[b] + s`` of
+    sequence b for s < lengths[b], its codes times their scales; with
+    positions its slice ``[start, end)`` is rotated on the way (keys stored
+    unrotated, or moved to other positions). Every other row of out keeps its
+    bytes: the padding behind a sequence, tokens past the block table, pages
+    outside the cache.
+
+    out: (B, S, heads, dim) GPU tensor, float32/float16/bfloat16, any strides
+    with consecutive lanes.
+    block_table: int32 (B, columns), token t of sequence b lies in page
+    block_table[b, t // page_size].
+    lengths: int32 (B); starts: int32 (B), 0 when None.
+    positions, inv_freq, pair_axes: as in :func:`rope_cache_write`, for out's
+    rows."""
+    import torch
+    if not isinstance(out, torch.Tensor) or out.dim() != 4:
+        raise ValueError("out must be a 4-D torch.Tensor (B, S, heads, dim)")
+    code, dev = _dtype_code(out), out.device
+    if out.numel() and not out.is_cuda:
+        raise ValueError("out must be a GPU tensor")
+    if not isinstance(cache, RopeCache):
+        raise TypeError("cache must be a RopeCache")
+    if cache.device != dev:
+        raise ValueError(f"cache must be on {dev}")
+    B, S = out.shape[:2]
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            block_table.shape[0] != B:
+        raise ValueError("block_table must be an int32 tensor (B, columns)")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: the pages of a sequence must be consecutive")
+    for name, t in (("lengths", lengths), ("starts", starts)):
+        if t is None and name == "starts":
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor (B)")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+    if block_table.device != dev:
+        raise ValueError(f"block_table must be on {dev}")
+    turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
+    switch = out.is_cuda and dev.index != torch.cuda.current_device()
+    handle = _stream_handle(stream, dev) if out.is_cuda else None
+    with torch.cuda.device(dev) if switch else _nullcontext():
+        st = library().rope_cache_read(
+            B, S, code, _rows("out", out), cache.struct, block_table.data_ptr() or None, block_table.shape[1],
+            block_table.stride(0), lengths.data_ptr() or None, None if starts is None else starts.data_ptr() or None,
+            *turn, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
 
 
 def rope_proj_fwd(x, w, r1, r2, heads: int, rotary_mode="interleave", partial_slice=None, out=None,

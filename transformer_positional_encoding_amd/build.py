@@ -8,6 +8,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "librope_partial.so")
-SOURCES = [os.path.join(CSRC, "rope_kernels.hip"), os.path.join(CSRC, "rope_plan.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("rope_kernels.hip", "rope_cache.hip", "rope_plan.cpp",
+                                           "rope_cache_plan.cpp")]
 # The bare access-pattern probe the benchmark times beside the kernels (its
 # own library; the rotation library does not use it).
 PROBE_LIB_PATH = os.path.join(LIB_DIR, "libhbm_probe.so")
@@ -32,7 +35,7 @@ def hipcc() -> str:
 
 def compile_flags() -> list[str]:
     return [
-        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
         # no packed fp32 instructions in device code
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wno-unused-command-line-argument",
@@ -40,17 +43,27 @@ def compile_flags() -> list[str]:
     ]
 
 
-def _compile(sources: list[str], out: str, verbose: bool) -> str:
-    os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = out + ".tmp"
-    cmd = [hipcc()] + compile_flags() + sources + ["-o", tmp]
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed to build {os.path.basename(out)}")
-    os.replace(tmp, out)
+        raise RuntimeError(f"hipcc failed to build {what}")
+
+
+def _compile(sources: list[str], out: str, verbose: bool) -> str:
+    """Each source to an object of its own, side by side, then one link."""
+    os.makedirs(LIB_DIR, exist_ok=True)
+    with tempfile.TemporaryDirectory(dir=LIB_DIR) as tmp:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in sources]
+        with ThreadPoolExecutor(len(sources)) as pool:
+            list(pool.map(lambda so: _run([hipcc()] + compile_flags() + ["-c", so[0], "-o", so[1]],
+                                          os.path.basename(so[0]), verbose), zip(sources, objects)))
+        lib = os.path.join(tmp, os.path.basename(out))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC"] + objects + ["-o", lib], os.path.basename(out),
+             verbose)
+        os.replace(lib, out)
     return out
 
 

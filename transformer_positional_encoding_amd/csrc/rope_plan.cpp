@@ -156,6 +156,15 @@ rope_status_t check_tables(const int64_t x_shape[4],
 
 }  // namespace
 
+rope_status_t make_plan_scalars(int64_t B, int64_t S, int64_t N, int64_t D, rope_dtype_t dtype,
+                                rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], Plan* plan,
+                                std::string* why)
+{
+    const int64_t shape[4] = {B, S, N, D};
+    int64_t numel = 0;
+    return check_scalars(shape, dtype, table_dtype, mode, partial_slice, kFwd, plan, &numel, why);
+}
+
 rope_status_t make_plan(void* x, const int64_t x_shape[4], rope_dtype_t dtype,
                         const void* r1, const int64_t r1_shape[4], const int64_t r1_strides[4],
                         const void* r2, const int64_t r2_shape[4], const int64_t r2_strides[4],
@@ -228,7 +237,8 @@ rope_status_t check_positions(int64_t B, int64_t S, int64_t L, const Positions& 
     if (in.inv_freq == nullptr) return fail(ROPE_ERR_NULLPTR, why, "inv_freq is NULL");
     if (in.shape == nullptr || in.strides == nullptr)
         return fail(ROPE_ERR_NULLPTR, why, "positions shape or strides is NULL");
-    if (in.axes && in.pair_axes == nullptr) return fail(ROPE_ERR_NULLPTR, why, "pair_axes is NULL");
+    if (in.axes && in.pair_axes == nullptr && !(in.pairs_optional && in.shape[0] == 1))
+        return fail(ROPE_ERR_NULLPTR, why, "pair_axes is NULL");
     const int64_t A = in.axes ? in.shape[0] : 1;
     if (A < 1 || A > ROPE_AXES_MAX)
         return fail(ROPE_ERR_INVALID, why, "positions: dimension A is " + std::to_string(A) + ", must be 1 to "
@@ -252,7 +262,7 @@ rope_status_t check_positions(int64_t B, int64_t S, int64_t L, const Positions& 
         part_a > std::numeric_limits<int64_t>::max() - part_s - part_b)
         return fail(ROPE_ERR_INVALID, why, "positions: strides overflow 64-bit offsets");
     if (in.axes) {
-        for (int64_t i = 0; i < L / 2; ++i) {
+        for (int64_t i = 0; in.pair_axes != nullptr && i < L / 2; ++i) {
             if (in.pair_axes[i] < 0 || in.pair_axes[i] >= A)
                 return fail(ROPE_ERR_INVALID, why, "pair_axes: pair " + std::to_string(i) + " has axis "
                                                        + std::to_string(in.pair_axes[i]) + ", must be 0 to "

@@ -62,6 +62,7 @@ struct Positions {
     const double* inv_freq = nullptr;
     bool axes = false;
     const int32_t* pair_axes = nullptr;
+    bool pairs_optional = false;   // pair_axes may be NULL with one axis
 };
 
 // Check a call's positions, frequencies and axes against a tensor of B
@@ -78,6 +79,12 @@ rope_status_t make_plan(void* x, const int64_t x_shape[4], rope_dtype_t dtype,
                         const void* r2, const int64_t r2_shape[4], const int64_t r2_strides[4],
                         rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
                         Direction dir, Plan* plan, std::string* why);
+
+// The scalar arguments alone (dimensions, types, mode, slice), for calls
+// whose tensors are described elsewhere.
+rope_status_t make_plan_scalars(int64_t B, int64_t S, int64_t N, int64_t D, rope_dtype_t dtype,
+                                rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], Plan* plan,
+                                std::string* why);
 
 // Out-of-place form: y receives x with its slice rotated and x is left
 // as it is. Checks, in order: the scalar arguments of make_plan; an empty
