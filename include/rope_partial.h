@@ -652,6 +652,60 @@ ROPE_API rope_status_t rope_proj_fwd(
     rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
     void* stream);
 
+/*
+ * Low-rank adapters of many requests beside one shared projection: `count`
+ * adapters of `rank`, and the adapter of each token.
+ */
+typedef struct rope_lora {
+    const void* a;            /* device (count, rank, K), of x's type: the products with x */
+    const void* b;            /* device (count, H*Dh, rank), of x's type: their products to output lanes */
+    const int32_t* adapters;  /* device (B*S): the adapter of each token; outside [0, count): none */
+    const float* scales;      /* device (count), or NULL: 1 */
+    int64_t count, rank;      /* rank: a multiple of 8, at most ROPE_LORA_RANK_MAX; count 0: no adapters */
+} rope_lora_t;
+
+#define ROPE_LORA_RANK_MAX 128
+
+/*
+ * rope_proj_lora_fwd -- rope_proj_fwd with the token's own low-rank adapter:
+ * for token m with adapter i = adapters[m],
+ *     h[m,r] = scales[i] * fl32( sum_k x[m,k] * a[i,r,k] )
+ *     p[m,n] = fl32( sum_k x[m,k] * w[n,k]  +  sum_r h[m,r] * b[i,n,r] )
+ *     y[b,s,h,j] = p rotated on the lanes [start,end) of each head, then
+ *                  rounded once to y's type.
+ * h is kept in fp32 (16-bit outputs may take it as the sum of two values of
+ * 8 bits each, fp32 outputs of three: the part left out is below 2^-16 and
+ * 2^-24 of it). A token without an adapter gives rope_proj_fwd's result up to
+ * the order of summation. Adapters of neighbouring tokens may differ in any
+ * pattern; runs of one adapter are fastest.
+ *
+ *   workspace        device buffer of workspace_bytes, 16-byte aligned, used
+ *                    during the call: at least
+ *                    rope_proj_lora_workspace(y_shape, K, rank). Two calls
+ *                    that may run at once need one each.
+ *   Other arguments are those of rope_proj_fwd, and so are the shapes it
+ *   takes, except that a slice's rotation groups may lie anywhere in a head.
+ *
+ * Checks: rope_proj_fwd's in their order, with these after the sizes of x
+ * and w: a NULL lora (ROPE_ERR_NULLPTR); count or rank negative, rank not a
+ * multiple of 8 (ROPE_ERR_INVALID) or above ROPE_LORA_RANK_MAX
+ * (ROPE_ERR_UNSUPPORTED), count or rank 0 is a projection without adapters;
+ * NULL a, b, adapters or workspace; a, b or workspace not 16-byte aligned,
+ * sizes beyond 64 bits, too small a workspace (ROPE_ERR_INVALID).
+ * Asynchronous on `stream`; nothing is allocated; deterministic.
+ */
+ROPE_API rope_status_t rope_proj_lora_fwd(
+    void* y, rope_dtype_t y_dtype, const void* x, const void* w, rope_dtype_t dtype,
+    const int64_t y_shape[4], int64_t K, const rope_lora_t* lora,
+    const void* r1, const int64_t r1_shape[4], const int64_t r1_strides[4],
+    const void* r2, const int64_t r2_shape[4], const int64_t r2_strides[4],
+    rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that a rope_proj_lora_fwd of this shape needs (0 when
+ * nothing is computed or the arguments are out of range). */
+ROPE_API int64_t rope_proj_lora_workspace(const int64_t y_shape[4], int64_t K, int64_t rank);
+
 /* Kernels of a projection's launch plan (rope_proj_launch_info). */
 #define ROPE_KERNEL_PROJ_HEADS 4  /* tiles of whole heads: 384 x 192 (12 waves) or 256 x 128 (8 waves) */
 #define ROPE_KERNEL_PROJ_SQUARE 5 /* 256 x 256 tiles, 4 waves of 128 x 128 */

@@ -1,0 +1,225 @@
+"""The projection with each token's own low-rank adapter, on the GPU, against
+its definition in 64 bits."""
+import pytest
+import torch
+
+import transformer_positional_encoding_amd as rp
+from axes_refs import BITS, TORCH, half_of
+
+pytestmark = pytest.mark.gpu
+
+
+def make(M, K, H, Dh, R, A, dtype, seed, ids="runs"):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = TORCH[dtype]
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    c = dict(x=rnd(1, M, K).to(t), w=(rnd(H * Dh, K) / K ** 0.5).to(t), a=(rnd(A, R, K) / K ** 0.5).to(t),
+             b=(rnd(A, H * Dh, R) / max(1, R) ** 0.5).to(t), scales=torch.rand(A, generator=g, device="cuda") + 0.5)
+    any_id = torch.randint(-1, A, (M,), generator=g, device="cuda")
+    if ids == "runs":      # runs of 1, 2, 3, ... tokens
+        run = torch.repeat_interleave(torch.arange(M, device="cuda"), torch.arange(1, M + 1, device="cuda"))[:M] if M < 3000 \
+            else torch.arange(M, device="cuda") // 700
+        any_id = any_id[run]
+    elif ids == "one":
+        any_id = torch.zeros_like(any_id)
+    elif ids == "none":
+        any_id = torch.where(any_id % 2 == 0, A, -5)   # past the end, and negative
+    c["ids"] = any_id.to(torch.int32)
+    return c
+
+
+def tables(M, L, mode, table, seed):
+    """Random cos and sin (no structure): every lane's own value is read."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [torch.randn(1, M, 1, L, generator=g, device="cuda").to(TORCH[table]) for _ in range(2)]
+
+
+def want64(c, cos, sin, H, mode, sl, out):
+    """(y, bound): the definition in 64 bits, and how far the kernels may lie
+    from it. Sums of n products in fp32 (in any order, a step rounding by at
+    most a unit in the last place, 2^-23) are within n 2^-23 of the sum of
+    magnitudes; h besides loses 2^-16 of itself where it is split into two
+    8-bit parts (16-bit outputs), 2^-23 in three; the rotation is three fp32
+    roundings; the result one to its type."""
+    x, w = c["x"][0].double(), c["w"].double()
+    M, K = x.shape
+    R, N = c["a"].shape[1], w.shape[0]
+    p, e = x @ w.T, (K + 8) * 2.0 ** -23 * (x.abs() @ w.abs().T)
+    for i in range(c["a"].shape[0]):
+        rows = torch.nonzero(c["ids"] == i)[:, 0]
+        if not len(rows):
+            continue
+        a, b, s = c["a"][i].double(), c["b"][i].double(), c["scales"][i].double()
+        h = s * (x[rows] @ a.T)
+        p[rows] += h @ b.T
+        part = 2.0 ** -16 if out != "f32" else 2.0 ** -23
+        dh = (K + 8) * 2.0 ** -23 * s * (x[rows].abs() @ a.abs().T) + part * h.abs()
+        e[rows] += (dh + (R + 8) * 2.0 ** -23 * h.abs()) @ b.abs().T
+    p, e = p.view(1, M, H, N // H), e.view(1, M, H, N // H)
+    lo, hi = sl
+    if hi > lo:
+        d = half_of(mode, hi - lo)
+        j = torch.arange(hi - lo, device="cuda")
+        first = (j // d) % 2 == 0
+        other = torch.where(first, j + d, j - d)
+        cs, sn = cos.double(), sin.double()
+        z, ez = p[..., lo:hi], e[..., lo:hi]
+        t1, t2 = z * cs, z[..., other] * sn
+        p, e = p.clone(), e.clone()
+        p[..., lo:hi] = t1 + torch.where(first, -1.0, 1.0) * t2
+        e[..., lo:hi] = ez * cs.abs() + ez[..., other] * sn.abs() + 3 * 2.0 ** -24 * (t1.abs() + t2.abs())
+    bits, emin = BITS[out]
+    return p, e + 2.0 ** -bits * (p.abs() + e) + 2.0 ** (emin - bits)
+
+
+def check(got, c, cos, sin, H, mode, sl, out, what):
+    want, lim = want64(c, cos, sin, H, mode, sl, out)
+    err = (got.double() - want).abs()
+    assert got.shape == want.shape and got.dtype == TORCH[out]
+    assert bool((err <= lim).all()), f"{what}: {int((err > lim).sum())} lanes off, worst {float((err / lim).max()):.3g}"
+    # roundings of a sum go both ways: in the 2-norm they grow as the root
+    # of their number
+    n = c["x"].shape[2] + c["a"].shape[1]
+    rel = float(err.norm() / want.norm()) if want.numel() else 0.0
+    assert rel <= 2.0 ** -BITS[out][0] + (0 if out == "f32" else 2.0 ** -16) + n ** 0.5 * 2.0 ** -23, f"{what}: 2-norm {rel:.3g}"
+
+
+def run(c, cos, sin, H, mode, sl, out_type, **kw):
+    return rp.rope_proj_lora_fwd(c["x"], c["w"], c["a"], c["b"], c["ids"], cos, sin, H, mode, sl, scales=c["scales"],
+                                 out_dtype=TORCH[out_type], **kw)
+
+
+# (M, K, H, Dh, R, A, slice, mode)
+CASES = [
+    (1, 64, 1, 32, 8, 1, (0, 32), "rotate_half"),
+    (1, 512, 8, 64, 8, 4, (0, 64), "rotate_half"),
+    (2, 1536, 4, 192, 16, 3, (0, 64), "interleave"),
+    (7, 192, 3, 128, 24, 5, (32, 96), "interleave"),
+    (16, 256, 2, 96, 32, 2, (0, 96), "rotate_half"),
+    (17, 320, 5, 128, 64, 40, (0, 128), "rotate_half"),
+    (33, 128, 1, 576, 16, 7, (512, 576), "interleave"),
+    (45, 384, 1, 576, 8, 3, (0, 576), "rotate_half"),
+    (64, 512, 3, 192, 16, 64, (0, 64), 4),
+    (65, 256, 2, 64, 128, 9, (5, 45), "rotate_half"),
+    (130, 128, 4, 128, 40, 11, (3, 61), "interleave"),
+    (300, 256, 4, 192, 16, 6, (0, 64), "interleave"),
+    (513, 128, 6, 128, 32, 3, (0, 128), "rotate_half"),
+    (700, 192, 3, 96, 8, 5, (0, 96), "rotate_half"),
+    (1025, 384, 2, 1024, 16, 4, (0, 1024), "rotate_half"),
+    (2500, 256, 4, 64, 72, 5, (0, 64), 8),
+]
+
+
+@pytest.mark.parametrize("M, K, H, Dh, R, A, sl, mode", CASES)
+@pytest.mark.parametrize("dtype, out, table", [("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("bf16", "f32", "f32"),
+                                               ("f16", "f32", "f16")])
+@pytest.mark.parametrize("ids", ["runs", "mixed"])
+def test_against_64_bits(M, K, H, Dh, R, A, sl, mode, dtype, out, table, ids):
+    c = make(M, K, H, Dh, R, A, dtype, seed=M + K, ids=ids)
+    cos, sin = tables(M, sl[1] - sl[0], mode, table, 5)
+    check(run(c, cos, sin, H, mode, sl, out), c, cos, sin, H, mode, sl, out, "projection")
+
+
+@pytest.mark.parametrize("M", [3, 40, 600])
+@pytest.mark.parametrize("ids", ["one", "none"])
+def test_one_adapter_and_none(M, ids):
+    c = make(M, 256, 2, 128, 16, 3, "bf16", seed=M, ids=ids)
+    cos, sin = tables(M, 64, "interleave", "bf16", 2)
+    check(run(c, cos, sin, 2, "interleave", (64, 128), "bf16"), c, cos, sin, 2, "interleave", (64, 128), "bf16", ids)
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_without_adapters_or_slice(M):
+    c = make(M, 256, 2, 128, 8, 2, "bf16", seed=1)
+    cos, sin = tables(M, 0, "interleave", "bf16", 2)
+    check(run(c, cos, sin, 2, "interleave", None, "bf16"), c, cos, sin, 2, "interleave", (0, 0), "bf16", "no slice")
+    cos, sin = tables(M, 128, "interleave", "bf16", 2)
+    for A, R in ((0, 8), (2, 0)):
+        d = make(M, 256, 2, 128, R, A, "bf16", seed=1, ids="none")
+        got = rp.rope_proj_lora_fwd(d["x"], d["w"], d["a"], d["b"], d["ids"], cos, sin, 2, "interleave", (0, 128))
+        check(got, d, cos, sin, 2, "interleave", (0, 128), "bf16", f"{A} adapters of rank {R}")
+
+
+@pytest.mark.parametrize("M", [4, 600])
+def test_tables_per_batch_and_per_head(M):
+    """Tables with strides in b, s and n, over a batch."""
+    B, S, H = 2, M // 2, 3
+    c = make(M, 128, H, 64, 16, 3, "bf16", seed=4)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    cos, sin = (torch.randn(B, S, H, 64, generator=g, device="cuda") for _ in range(2))
+    got = rp.rope_proj_lora_fwd(c["x"].view(B, S, 128), c["w"], c["a"], c["b"], c["ids"].view(B, S), cos, sin, H,
+                                "rotate_half", (0, 64), scales=c["scales"])
+    flat = lambda t: t.reshape(1, M, H, 64)  # noqa: E731
+    check(flat(got), c, flat(cos), flat(sin), H, "rotate_half", (0, 64), "bf16", "per head")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [6, 600])
+def test_large_products(dtype, M):
+    """h past the largest fp16 value, and rows of infinities in x."""
+    c = make(M, 256, 2, 64, 16, 3, dtype, seed=8)
+    c["x"] = (c["x"].float() * 200).to(TORCH[dtype])
+    c["a"] = (c["a"].float() * 300).to(TORCH[dtype])
+    c["b"] = (c["b"].float() * 2.0 ** -8).to(TORCH[dtype])
+    cos, sin = tables(M, 64, "interleave", "f32", 2)
+    assert float((c["x"][0].float() @ c["a"][0].float().T).abs().max()) > 65504
+    check(run(c, cos, sin, 2, "interleave", (0, 64), "f32"), c, cos, sin, 2, "interleave", (0, 64), "f32", "large h")
+    c["x"][0, 1] = float("inf")
+    got = run(c, cos, sin, 2, "interleave", (0, 64), "f32")
+    keep = torch.arange(M, device="cuda") != 1
+    assert bool(torch.isfinite(got[:, keep]).all()) and not bool(torch.isfinite(got[:, 1]).any())
+
+
+def test_not_finite_adapters_stay_with_their_tokens():
+    """An adapter of NaNs touches no token of another adapter."""
+    for M in (8, 300):
+        c = make(M, 256, 2, 128, 16, 4, "bf16", seed=3, ids="mixed")
+        cos, sin = tables(M, 128, "interleave", "bf16", 2)
+        clean = run(c, cos, sin, 2, "interleave", (0, 128), "bf16")
+        c["a"][2], c["b"][2] = float("nan"), float("inf")
+        got = run(c, cos, sin, 2, "interleave", (0, 128), "bf16")
+        others = c["ids"] != 2
+        assert torch.equal(got[:, others], clean[:, others])
+
+
+@pytest.mark.parametrize("M", [1, 3, 64, 513])
+def test_nothing_past_the_result_is_written(M):
+    c = make(M, 128, 3, 64, 8, 2, "bf16", seed=2)
+    cos, sin = tables(M, 64, "interleave", "bf16", 2)
+    n = M * 3 * 64
+    guarded = torch.full((n + 8192,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = guarded[4096:4096 + n].view(1, M, 3, 64)
+    ws = torch.full((M * 8 * 4 + 64,), 9, dtype=torch.uint8, device="cuda")
+    run(c, cos, sin, 3, "interleave", (0, 64), "bf16", out=out, workspace=ws[: M * 8 * 4])
+    assert bool((guarded[:4096] == 7).all()) and bool((guarded[4096 + n:] == 7).all()) and bool((ws[-64:] == 9).all())
+    assert torch.equal(out, run(c, cos, sin, 3, "interleave", (0, 64), "bf16")), "two runs differ"
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_graph_replays_follow_the_adapters(M):
+    c = make(M, 256, 2, 128, 16, 5, "bf16", seed=2)
+    cos, sin = tables(M, 128, "rotate_half", "bf16", 2)
+    run(c, cos, sin, 2, "rotate_half", (0, 128), "bf16")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run(c, cos, sin, 2, "rotate_half", (0, 128), "bf16")
+    for k in range(4):
+        c["ids"].copy_(torch.roll(c["ids"], 1 + k))
+        c["x"].mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, run(c, cos, sin, 2, "rotate_half", (0, 128), "bf16"))
+
+
+def test_two_streams_at_once():
+    cs = [make(200, 512, 8, 128, 16, 5, "bf16", seed=k) for k in range(2)]
+    cos, sin = tables(200, 128, "rotate_half", "bf16", 2)
+    want = [run(c, cos, sin, 8, "rotate_half", (0, 128), "bf16") for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(3):
+        got = [run(c, cos, sin, 8, "rotate_half", (0, 128), "bf16", stream=s) for c, s in zip(cs, streams)]
+        raw = run(cs[0], cos, sin, 8, "rotate_half", (0, 128), "bf16", stream=streams[0].cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(raw, want[0])

@@ -28,7 +28,8 @@ __all__ = [
     "rope_partial_fwd_inplace_axes", "rope_partial_bwd_inplace_axes", "rope_partial_fwd_out_axes",
     "rope_partial_bwd_out_axes", "rope_partial_fwd_inplace_axes_multi", "rope_partial_bwd_inplace_axes_multi",
     "inplace_partial_rotary_mul_axes", "partial_rotary_mul_axes", "rope_pair_axes", "rope_axes_inv_freq", "AXES_MAX",
-    "RopeCache", "rope_cache", "rope_cache_write", "rope_cache_read", "CACHE_FORMATS", "rope_proj_fwd", "RopeError", "library", "LIB_PATH", "ROPE_OK", "ROPE_ERR_NULLPTR", "ROPE_ERR_INVALID",
+    "RopeCache", "rope_cache", "rope_cache_write", "rope_cache_read", "CACHE_FORMATS", "rope_proj_fwd",
+    "rope_proj_lora_fwd", "rope_proj_lora_workspace", "LORA_RANK_MAX", "RopeError", "library", "LIB_PATH", "ROPE_OK", "ROPE_ERR_NULLPTR", "ROPE_ERR_INVALID",
     "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_RUNTIME", "MODES", "DTYPE_CODES",
 ]
 
@@ -40,6 +41,7 @@ MODES = {"rotate_half": 0, "interleave": 1}
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 MULTI_MAX = 4
 AXES_MAX = 4
+LORA_RANK_MAX = 128
 CACHE_FORMATS = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3, "int8": 4, "int4": 5}
 
 _I64x4 = ctypes.c_int64 * 4
@@ -74,6 +76,12 @@ class RopeCacheStruct(ctypes.Structure):
                 ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("group", ctypes.c_int64), ("strides", ctypes.c_int64 * 3),
                 ("scale_strides", ctypes.c_int64 * 3)]
+
+
+class RopeLora(ctypes.Structure):
+    """The C ABI's rope_lora_t."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("adapters", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("count", ctypes.c_int64), ("rank", ctypes.c_int64)]
 
 
 _lib = None
@@ -148,6 +156,11 @@ def library() -> ctypes.CDLL:
         L.rope_proj_fwd.restype = ctypes.c_int
         L.rope_proj_fwd.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                     ctypes.POINTER(ctypes.c_int64), ctypes.c_int64] + _ENTRY_ARGTYPES[3:]
+        L.rope_proj_lora_fwd.restype = ctypes.c_int
+        L.rope_proj_lora_fwd.argtypes = L.rope_proj_fwd.argtypes[:7] + [ctypes.POINTER(RopeLora)] + \
+            _ENTRY_ARGTYPES[3:-1] + [vp, ctypes.c_int64, vp]
+        L.rope_proj_lora_workspace.restype = ctypes.c_int64
+        L.rope_proj_lora_workspace.argtypes = [i64p, ctypes.c_int64, ctypes.c_int64]
         L.rope_proj_launch_info.restype = ctypes.c_int
         L.rope_proj_launch_info.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int64),
                                             ctypes.c_int64] + _ENTRY_ARGTYPES[3:-1] + [ctypes.POINTER(ctypes.c_int64)]
@@ -1474,6 +1487,104 @@ def rope_proj_fwd(x, w, r1, r2, heads: int, rotary_mode="interleave", partial_sl
                            _dtype_code(x), y_shape, K, r1.data_ptr() or None, tuple(r1.shape), tuple(r1.stride()),
                            r2.data_ptr() or None, tuple(r2.shape), tuple(r2.stride()),
                            _dtype_code(r1) if r1.dtype == r2.dtype else -1, rotary_mode, partial_slice, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
+    return out
+
+
+def rope_proj_lora_workspace(tokens: int, K: int, rank: int) -> int:
+    """Bytes of workspace that :func:`rope_proj_lora_fwd` needs for this many
+    tokens."""
+    return library().rope_proj_lora_workspace(_I64x4(1, tokens, 1, 1), K, rank)
+
+
+def _allocating_on(stream, dev):
+    """A context in which tensors are allocated for `stream` (a torch stream
+    or a raw hipStream_t)."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="interleave", partial_slice=None,
+                       scales=None, out=None, out_dtype=None, workspace=None, stream=None):
+    """:func:`rope_proj_fwd` for tokens of many requests, each with its own
+    low-rank adapter beside the shared weight: ``y[m] = rotate(x[m] @ w.T +
+    scales[i] * (x[m] @ a[i].T) @ b[i].T)`` for the token's adapter i.
+
+    x, w, r1, r2, heads, rotary_mode, partial_slice, out, out_dtype: as in
+    :func:`rope_proj_fwd`.
+    a: (count, rank, K) and b: (count, heads * Dh, rank) contiguous, of x's
+    dtype; rank a multiple of 8, at most LORA_RANK_MAX (pad with zeros).
+    adapters: int32, one per token (x's shape without K): an index into a and
+    b; one outside [0, count), such as -1, adds nothing. Any order; tokens of
+    one adapter beside each other are fastest.
+    scales: float32 (count) or None for ones.
+    workspace: a contiguous GPU tensor of at least
+    ``rope_proj_lora_workspace(tokens, K, rank)`` bytes, 16-byte aligned, that
+    no other call uses meanwhile; None allocates one.
+    Returns ``out`` (allocated when None)."""
+    import torch
+    if isinstance(rotary_mode, str):
+        if rotary_mode not in MODES:
+            raise ValueError(f"rotary_mode must be one of {sorted(MODES)}")
+        rotary_mode = MODES[rotary_mode]
+    for name, t in (("x", x), ("w", w), ("a", a), ("b", b), ("adapters", adapters), ("r1", r1), ("r2", r2)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dim() not in (2, 3) or w.dim() != 2:
+        raise ValueError("x must be (B, S, K) or (M, K) and w (H*Dh, K)")
+    B, S = (1, x.shape[0]) if x.dim() == 2 else (x.shape[0], x.shape[1])
+    K, N = x.shape[-1], w.shape[0]
+    if w.shape[1] != K or heads <= 0 or N % heads:
+        raise ValueError(f"w must be (heads*Dh, K={K}), got {tuple(w.shape)} for {heads} heads")
+    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != K or b.shape[1] != N or a.shape[0] != b.shape[0] or \
+            a.shape[1] != b.shape[2]:
+        raise ValueError(f"a must be (count, rank, {K}) and b (count, {N}, rank), got {tuple(a.shape)} and "
+                         f"{tuple(b.shape)}")
+    if w.dtype != x.dtype or a.dtype != x.dtype or b.dtype != x.dtype:
+        raise ValueError("x, w, a and b must share a dtype")
+    if adapters.dtype != torch.int32 or adapters.numel() != B * S:
+        raise ValueError("adapters must be an int32 tensor, one per token")
+    if scales is not None and (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or
+                               scales.shape != a.shape[:1]):
+        raise ValueError("scales must be a float32 tensor (count)")
+    y_shape = (B, S, heads, N // heads)
+    dev = x.device
+    count, rank = a.shape[0], a.shape[1]
+    if out is not None and tuple(out.shape) != y_shape:
+        raise ValueError(f"out must be a contiguous {y_shape} tensor")
+    # memory made here belongs to the call's stream: the allocator then hands
+    # it on only to work behind this call's
+    with _allocating_on(stream, dev) if stream is not None and x.is_cuda else _nullcontext():
+        if out is None:
+            out = torch.empty(y_shape, dtype=out_dtype or x.dtype, device=dev)
+        if workspace is None:
+            workspace = torch.empty(B * S * rank * 4 if count else 0, dtype=torch.uint8, device=dev)
+    for name, t in (("x", x), ("w", w), ("a", a), ("b", b), ("adapters", adapters), ("out", out),
+                    ("workspace", workspace)) + ((("scales", scales),) if scales is not None else ()):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() and not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+    for name, t in (("r1", r1), ("r2", r2)):
+        if t.numel() and out.numel() and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+    lora = RopeLora(a.data_ptr() or None, b.data_ptr() or None, adapters.data_ptr() or None,
+                    None if scales is None else scales.data_ptr() or None, count, rank)
+    handle = _stream_handle(stream, dev) if x.is_cuda else None
+    sl = None if partial_slice is None else _I64x2(*partial_slice)
+    switch = x.is_cuda and dev.index != torch.cuda.current_device()
+    with torch.cuda.device(dev) if switch else _nullcontext():
+        st = library().rope_proj_lora_fwd(
+            out.data_ptr() or None, _dtype_code(out), x.data_ptr() or None, w.data_ptr() or None, _dtype_code(x),
+            _I64x4(*y_shape), K, lora, r1.data_ptr() or None, _arr4(r1.shape), _arr4(r1.stride()),
+            r2.data_ptr() or None, _arr4(r2.shape), _arr4(r2.stride()),
+            _dtype_code(r1) if r1.dtype == r2.dtype else -1, rotary_mode, sl, workspace.data_ptr() or None,
+            workspace.numel() * workspace.element_size(), handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
     return out

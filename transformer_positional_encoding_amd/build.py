@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "librope_partial.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("rope_kernels.hip", "rope_cache.hip", "rope_plan.cpp",
+SOURCES = [os.path.join(CSRC, f) for f in ("rope_kernels.hip", "rope_cache.hip", "rope_lora.hip", "rope_plan.cpp",
                                            "rope_cache_plan.cpp")]
 # The bare access-pattern probe the benchmark times beside the kernels (its
 # own library; the rotation library does not use it).

@@ -385,12 +385,52 @@ bool proj_groups_in_column_tiles(int64_t Dh, int64_t N, int64_t start, int64_t L
     return true;
 }
 
+int64_t lora_workspace_bytes(int64_t M, int64_t rank)
+{
+    int64_t n;
+    return mul_ok(M, rank, &n) && mul_ok(n, 4, &n) ? n : -1;
+}
+
+namespace {
+
+// The adapters and workspace of an M x N projection over K.
+rope_status_t check_lora(const LoraCheck& c, int64_t M, int64_t N, int64_t K, std::string* why)
+{
+    if (c.lora == nullptr) return fail(ROPE_ERR_NULLPTR, why, "lora is NULL");
+    const rope_lora_t& l = *c.lora;
+    if (l.count < 0 || l.rank < 0) return fail(ROPE_ERR_INVALID, why, "lora: negative count or rank");
+    if (l.rank % 8 != 0) return fail(ROPE_ERR_INVALID, why, "lora: rank must be a multiple of 8");
+    if (l.rank > ROPE_LORA_RANK_MAX) return fail(ROPE_ERR_UNSUPPORTED, why, "lora: rank exceeds 128");
+    if (l.count == 0 || l.rank == 0) return ROPE_OK;
+    if (l.count > std::numeric_limits<int32_t>::max()) return fail(ROPE_ERR_INVALID, why, "lora: too many adapters");
+    if (l.a == nullptr) return fail(ROPE_ERR_NULLPTR, why, "lora: a is NULL");
+    if (l.b == nullptr) return fail(ROPE_ERR_NULLPTR, why, "lora: b is NULL");
+    if (l.adapters == nullptr) return fail(ROPE_ERR_NULLPTR, why, "lora: adapters is NULL");
+    if (c.workspace == nullptr) return fail(ROPE_ERR_NULLPTR, why, "workspace is NULL");
+    for (const void* ptr : {l.a, l.b, c.workspace})
+        if ((reinterpret_cast<uintptr_t>(ptr) & 15u) != 0)
+            return fail(ROPE_ERR_INVALID, why, "lora: a, b and workspace must be 16-byte aligned");
+    if (((reinterpret_cast<uintptr_t>(l.adapters) | reinterpret_cast<uintptr_t>(l.scales)) & 3u) != 0)
+        return fail(ROPE_ERR_INVALID, why, "lora: adapters or scales not aligned to their elements");
+    int64_t na, nb;
+    if (!mul_ok(l.count, l.rank, &na) || !mul_ok(na, N, &nb) || !mul_ok(na, K, &na) || !mul_ok(na, 2, &na) ||
+        !mul_ok(nb, 2, &nb))
+        return fail(ROPE_ERR_INVALID, why, "lora: a or b byte size overflows 64 bits");
+    const int64_t need = lora_workspace_bytes(M, l.rank);
+    if (need < 0 || c.workspace_bytes < need)
+        return fail(ROPE_ERR_INVALID, why, "workspace holds " + std::to_string(c.workspace_bytes) + " bytes, needs "
+                                               + std::to_string(need));
+    return ROPE_OK;
+}
+
+}  // namespace
+
 rope_status_t make_proj_plan(void* y, rope_dtype_t out_dtype, const void* x, const void* w, rope_dtype_t dtype,
                              const int64_t y_shape[4], int64_t K,
                              const void* r1, const int64_t r1_shape[4], const int64_t r1_strides[4],
                              const void* r2, const int64_t r2_shape[4], const int64_t r2_strides[4],
                              rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
-                             ProjPlan* plan, std::string* why)
+                             ProjPlan* plan, std::string* why, const LoraCheck* lora)
 {
     ProjPlan q;
     int64_t numel = 0;
@@ -418,7 +458,7 @@ rope_status_t make_proj_plan(void* y, rope_dtype_t out_dtype, const void* x, con
     // a rotation group must lie in one column tile of the kernel that takes
     // the call: a tile of whole heads (or of part of a wider head), or, with
     // K a multiple of 128, a 256-lane square tile
-    if (!proj_groups_in_tiles(Dh, q.rope.start, q.rope.L, q.rope.half) &&
+    if (lora == nullptr && !proj_groups_in_tiles(Dh, q.rope.start, q.rope.L, q.rope.half) &&
         !(K % 128 == 0 && proj_groups_in_column_tiles(Dh, y_shape[2] * Dh, q.rope.start, q.rope.L, q.rope.half, 256)))
         return fail(ROPE_ERR_UNSUPPORTED, why,
                     "a rotation group of the slice spans two column tiles of a head wider than the tile");
@@ -444,6 +484,7 @@ rope_status_t make_proj_plan(void* y, rope_dtype_t out_dtype, const void* x, con
     const uint64_t y_bytes = (uint64_t)q.rope.bytes;
     if (overlap(y, y_bytes, x, (uint64_t)x_bytes) || overlap(y, y_bytes, w, (uint64_t)w_bytes))
         return fail(ROPE_ERR_INVALID, why, "y overlaps x or w");
+    if (lora != nullptr && (st = check_lora(*lora, M, N, K, why)) != ROPE_OK) return st;
     if (q.rope.L > 0) {
         st = check_tables(y_shape, r1, r1_shape, r1_strides, r2, r2_shape, r2_strides, &q.rope, why);
         if (st != ROPE_OK) return st;

@@ -133,6 +133,17 @@ struct ProjPlan {
 // two calls). ROPE_ERR_INVALID names the first overlapping pair.
 rope_status_t check_disjoint(const Plan plans[], int n, std::string* why);
 
+// The adapters of a rope_proj_lora_fwd, checked within make_proj_plan: the
+// slice's rotation groups may then lie anywhere in a head.
+struct LoraCheck {
+    const rope_lora_t* lora = nullptr;
+    const void* workspace = nullptr;
+    int64_t workspace_bytes = 0;
+};
+
+// Bytes of workspace of an M-token call: h, M x rank floats. -1 past 64 bits.
+int64_t lora_workspace_bytes(int64_t M, int64_t rank);
+
 // Lanes per head the fused kernel takes: 32, 64, 96, 128 or 192 (block
 // tiles of whole heads), or a multiple of 192 or 128 up to 1024 (a head over
 // whole tiles).
@@ -167,7 +178,7 @@ rope_status_t make_proj_plan(void* y, rope_dtype_t out_dtype, const void* x, con
                              const void* r1, const int64_t r1_shape[4], const int64_t r1_strides[4],
                              const void* r2, const int64_t r2_shape[4], const int64_t r2_strides[4],
                              rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
-                             ProjPlan* plan, std::string* why);
+                             ProjPlan* plan, std::string* why, const LoraCheck* lora = nullptr);
 
 int element_size(int dtype);
 
