@@ -13,8 +13,6 @@
 namespace rope {
 namespace {
 
-constexpr uint64_t kMaxGridItems = 0xFFFFFFFFull;   // work-items of a launch
-
 Rows rows_of(const RowsPlan& p) { return Rows{p.data, p.sb, p.ss, p.sn}; }
 
 CacheRef cache_of(const CachePlan& p)

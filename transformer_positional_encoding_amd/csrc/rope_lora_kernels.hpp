@@ -26,8 +26,7 @@ struct LoraArgs {
     int32_t count, R;
 };
 
-struct LoraProjArgs {
-    ProjArgs p;
+struct LoraProjArgs : ProjArgs {
     LoraArgs l;
 };
 
@@ -93,6 +92,145 @@ __device__ __forceinline__ f32x4 mfma16(const v4u& a, const v4u& b, const f32x4&
                                                       0, 0);
 }
 
+// ---------------------------------------------------------------------------
+// The adapters' part of the tiled projections: after the K loop, R more k for
+// each adapter of the wave's tokens, on the same accumulators. A fragment of
+// 32 tokens that share an adapter (a prompt's) goes straight into them; one
+// of several adapters takes each in turn into cleared accumulators and adds
+// only its own tokens' values (not a product with h = 0, which an infinity
+// or NaN in one adapter would carry into every other's tokens).
+// h is fp32 and the MFMA takes 16 bits: h = p0 + p1 (+ p2) in bf16, each the
+// rest of the one before it rounded to 8 bits, two parts for 16-bit outputs
+// (what is left is below 2^-16 of h, the output rounds at 2^-9 or 2^-12) and
+// three for fp32 (2^-24). fp16 weights take the same route, b = q0 + q1
+// exactly (11 bits in two of 8): h may exceed fp16's range.
+// ---------------------------------------------------------------------------
+
+// v rounded to bf16, as 8 lanes; v becomes what is left.
+__device__ __forceinline__ v4u take_bf16(float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w[k] = Store<ROPE_DTYPE_BF16>::narrow(f32x2{v[2 * k], v[2 * k + 1]});
+        const f32x2 f = Store<ROPE_DTYPE_BF16>::widen(w[k]);
+        v[2 * k] -= f.x;
+        v[2 * k + 1] -= f.y;
+    }
+    return v4u{w[0], w[1], w[2], w[3]};
+}
+
+// One 32 x 32 tile: c += (8 k of b per lane, BQ parts) x (of h, `parts`).
+// COLS: tokens are the tile's columns (square tiles), else its rows.
+template <int BQ, bool COLS>
+__device__ __forceinline__ void lora_mfma(f32x16& c, const v4u (&b)[BQ], const v4u (&h)[3], int parts)
+{
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+        if (p < 2 || parts > 2)
+#pragma unroll
+            for (int q = 0; q < BQ; ++q)
+                c = COLS ? proj_mfma<ROPE_DTYPE_BF16>(b[q], h[p], c) : proj_mfma<ROPE_DTYPE_BF16>(h[p], b[q], c);
+}
+
+// The tiles of 32 tokens (this lane's id and row of h) and NT x 32 output
+// lanes from n0, at(nt) their accumulators.
+template <int DT, int NT, bool COLS, class AT>
+__device__ __forceinline__ void lora_add_tiles(const LoraProjArgs& a, int32_t m, int32_t n0, int lane, AT at)
+{
+    constexpr int BQ = DT == ROPE_DTYPE_F16 ? 2 : 1;
+    const LoraArgs& l = a.l;
+    const int parts = a.ydt == ROPE_DTYPE_F32 ? 3 : 2;
+    if (l.count == 0) return;                             // no adapters: nothing in l may be read
+    // tokens past the last repeat it (their results are never stored)
+    m = min(m, a.M - 1);
+    const int32_t id = lora_id(l, m);
+    const int rl = (lane >> 5) * 8;                       // the lane's 8 of each 16 ranks
+    uint64_t todo = __ballot(id >= 0);
+    while (todo != 0) {
+        const int32_t cur = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(todo));
+        const bool mine = id == cur;
+        const uint64_t same = __ballot(mine);
+        const bool all = same == ~0ull;
+        f32x16 d[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) d[nt] = all ? at(nt) : f32x16{};
+        for (int r = 0; r < l.R; r += 16) {
+            const bool live = r + rl < l.R;               // R may end halfway through a step
+            float hv[8] = {};
+            if (live && mine) {
+                const float4* hp = reinterpret_cast<const float4*>(l.h + (int64_t)m * l.R + r + rl);
+                const float4 h0 = hp[0], h1 = hp[1];
+                hv[0] = h0.x; hv[1] = h0.y; hv[2] = h0.z; hv[3] = h0.w;
+                hv[4] = h1.x; hv[5] = h1.y; hv[6] = h1.z; hv[7] = h1.w;
+            }
+            v4u hp[3];
+            hp[0] = take_bf16(hv);
+            hp[1] = take_bf16(hv);
+            hp[2] = take_bf16(hv);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int32_t n = min(n0 + nt * 32 + (lane & 31), a.N - 1);
+                v4u b[BQ] = {};
+                if (live) b[0] = *reinterpret_cast<const v4u*>(l.b + ((int64_t)cur * a.N + n) * l.R + r + rl);
+                if constexpr (DT == ROPE_DTYPE_F16) {
+                    float bv[8];
+                    widen8<DT>(b[0], bv);
+                    b[0] = take_bf16(bv);
+                    b[1] = take_bf16(bv);
+                }
+                lora_mfma<BQ, COLS>(d[nt], b, hp, parts);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (all) {
+                at(nt) = d[nt];
+            } else {
+                // accumulator register e of lane i: column i%32, row 8*(e/4) + 4*(i/32) + e%4
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const bool own = COLS ? mine
+                                          : ((same >> (8 * (e >> 2) + 4 * (lane >> 5) + (e & 3))) & 1u) != 0;
+                    at(nt)[e] = own ? at(nt)[e] + d[nt][e] : at(nt)[e];
+                }
+            }
+        }
+        todo &= ~same;
+    }
+}
+
+template <>
+struct ProjAdapters<LoraProjArgs> {
+    static constexpr bool kAny = true;
+
+    // square tiles: the wave's 4 x 4 tiles, [nt][mt], tokens in columns
+    template <int DT>
+    __device__ static __forceinline__ void add_square(const LoraProjArgs& a, f32x16 (&acc)[4][4], int32_t m0,
+                                                      int32_t n0, int lane)
+    {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+            lora_add_tiles<DT, 4, true>(a, m0 + mt * 32 + (lane & 31), n0, lane,
+                                        [&](int nt) -> f32x16& { return acc[nt][mt]; });
+    }
+
+    // tiles of whole heads: [mt][nt], tokens in rows
+    template <int DT, int MT, int NT>
+    __device__ static __forceinline__ void add_heads(const LoraProjArgs& a, f32x16 (&acc)[MT][NT], int32_t m0,
+                                                     int32_t n0, int lane)
+    {
+        // one tile at a time: cleared accumulators for all NT beside the
+        // wave's own would not fit its 168 registers
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                lora_add_tiles<DT, 1, false>(a, m0 + mt * 32 + (lane & 31), n0 + nt * 32, lane,
+                                             [&](int) -> f32x16& { return acc[mt][nt]; });
+    }
+};
+
 // One table value of runtime type.
 __device__ __forceinline__ float table_value(const void* t, int tdt, int64_t i)
 {
@@ -140,7 +278,7 @@ template <int DT>
 __global__ void __launch_bounds__(256) rope_lora_head_kernel(LoraProjArgs g, int tdt, int heads)
 {
     __shared__ __attribute__((aligned(16))) float P[kHeadTokens * kHeadPitch];
-    const ProjArgs& a = g.p;
+    const ProjArgs& a = g;
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     const int fr = lane & 15, fk = (lane >> 4) * 8;

@@ -210,9 +210,17 @@ struct ProjTab8 {
     }
 };
 
-template <int DT, int BN, int TT>
+// What the kernels' arguments say about low-rank adapters beside the shared
+// weight: none, unless a specialisation for other arguments adds their
+// products to the accumulators between the K loop and the epilogue.
+template <class ARGS>
+struct ProjAdapters {
+    static constexpr bool kAny = false;
+};
+
+template <int DT, int BN, int TT, class ARGS = ProjArgs>
 __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
-    __attribute__((amdgpu_waves_per_eu(ProjTile<BN>::NW / 4, ProjTile<BN>::NW / 4))) rope_proj_kernel(ProjArgs a)
+    __attribute__((amdgpu_waves_per_eu(ProjTile<BN>::NW / 4, ProjTile<BN>::NW / 4))) rope_proj_kernel(ARGS a)
 {
     using T_ = ProjTile<BN>;
     constexpr int BM = T_::BM, MT = T_::MT, NT = T_::NT, LW = T_::LW, LDC = T_::LDC;
@@ -305,6 +313,8 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
         mma_stage((int)(kt & 1));
     }
     __syncthreads();                                   // every wave is done with the ring
+    if constexpr (ProjAdapters<ARGS>::kAny)
+        ProjAdapters<ARGS>::template add_heads<DT, MT, NT>(a, acc, m0 + wm * 64, n0 + wn * (BN / 2), lane);
 
     // ---------------------------------------------------------------- epilogue
     // Half h holds accumulator row tile mt = h of every wave: tile rows
@@ -671,9 +681,9 @@ __device__ __forceinline__ void proj_sq_epilogue_vec(const ProjArgs& a, const f3
 // the vector epilogue with partners in the vector, 1 with partners whole
 // vectors away (a kernel of its own each: one kernel holding several
 // epilogues spills the accumulators)
-template <int DT, int TT, int EPI>
+template <int DT, int TT, int EPI, class ARGS = ProjArgs>
 __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
-    rope_proj_sq_kernel(ProjArgs a)
+    rope_proj_sq_kernel(ARGS a)
 {
     using T_ = ProjSq;
     constexpr int BM = T_::BM, BN = T_::BN, LW = T_::LW, LDC = T_::LDC;
@@ -854,6 +864,8 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     stage(S1{}, Last{}, Later{}, kt);
     proj_wait_vm<0>();                                 // this wave's table rows are in LDS
     __syncthreads();                                   // every wave is done with the ring
+    if constexpr (ProjAdapters<ARGS>::kAny)
+        ProjAdapters<ARGS>::template add_square<DT>(a, acc, m0 + wm * 128, n0 + wn * 128, lane);
 
     if constexpr (EPI >= 0) {
         proj_sq_epilogue_vec<DT, TT, EPI == 1>(a, acc, smem, m0, n0, wm, wn, wave, lane);
