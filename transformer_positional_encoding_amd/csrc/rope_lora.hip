@@ -14,12 +14,23 @@
 namespace rope {
 namespace {
 
+// Tokens up to which h is computed by dot products, a wave per token and
+// rank, and not by 32-token tiles: a tile's block walks a quarter of K per
+// wave, which few blocks cannot hide.
+constexpr int32_t kShrinkDotTokens = 64;
+
+// Tokens up to which the kernel for few tokens takes the call where the tiled
+// ones could: it reads w once per 64 tokens, they fill 256-token tiles.
+constexpr int32_t kFewTokens = 128;
+
 // A call's checked plan and what is launched for it.
 struct LoraLaunch {
     ProjLaunch P;
     LoraArgs l{};
     int heads = 0;
-    bool tiles = false;      // the tiled projection kernels (else the general one)
+    bool tiles = false;      // the tiled projection kernels
+    bool few = false;        // else the kernel for few tokens, else the general one
+    FewArgs units{};         // its fragments
 };
 
 rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const void* w, rope_dtype_t dtype,
@@ -49,7 +60,21 @@ rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const v
     }
     // the tiled kernels need each rotation group within one tile
     const bool fits = L->P.sq || proj_groups_in_tiles(p.D, p.start, p.L, L->P.a.half);
-    L->tiles = fits && L->P.a.M > kHeadTokens;
+    // the kernel for few tokens: adjacent pairs that start on an even lane,
+    // or partners whole fragments apart
+    const ProjArgs& a = L->P.a;
+    FewArgs& u = L->units;
+    u.head_units = a.Dh / 32;
+    u.apart = a.L > 0 && a.half > 1;
+    if (u.apart) {
+        u.first_frag = a.start / 16;
+        u.slice_frags = a.L / 16;
+        u.half_frags = a.half / 16;
+        u.slice_units = u.slice_frags / 2;
+    }
+    const bool units = u.apart ? a.start % 16 == 0 && a.half % 16 == 0 : a.start % 2 == 0;
+    L->tiles = fits && (a.M > kFewTokens || !units);
+    L->few = !L->tiles && units;
     return ROPE_OK;
 }
 
@@ -81,6 +106,17 @@ void launch_tiles_tt(const ProjLaunch& P, const LoraProjArgs& a, hipStream_t s)
     }
 }
 
+template <int DT, int MT>
+void launch_few(const FewArgs& a, int tdt, hipStream_t s)
+{
+    const dim3 grid((uint32_t)(a.N / 32), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)));
+    // 8 waves share a unit's K where 4 would leave the chip short of waves
+    if ((uint64_t)grid.x * grid.y < 512)
+        hipLaunchKernelGGL((rope_lora_few_kernel<DT, MT, 8>), grid, dim3(512), 0, s, a, tdt);
+    else
+        hipLaunchKernelGGL((rope_lora_few_kernel<DT, MT, 4>), grid, dim3(256), 0, s, a, tdt);
+}
+
 template <int DT>
 hipError_t launch_lora(const LoraLaunch& L, hipStream_t s)
 {
@@ -88,15 +124,24 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t s)
     static_cast<ProjArgs&>(a) = L.P.a;
     a.l = L.l;
     if (a.l.count > 0) {
-        const uint32_t gy = (uint32_t)(a.l.R + kShrinkWaves - 1) / kShrinkWaves;
-        const uint32_t gx = (uint32_t)std::min<uint64_t>((uint64_t)a.M, kMaxGridItems / (64 * kShrinkWaves) / gy);
-        hipLaunchKernelGGL((rope_lora_shrink_kernel<DT>), dim3(gx, gy), dim3(64 * kShrinkWaves), 0, s, a.l, a.x, a.M,
-                           a.K);
+        if (a.M > kShrinkDotTokens) {
+            hipLaunchKernelGGL((rope_lora_shrink_tile_kernel<DT>), dim3((uint32_t)((a.M + 31) / 32), (uint32_t)(a.l.R + 31) / 32),
+                               dim3(256), 0, s, a.l, a.x, a.M, a.K);
+        } else {
+            hipLaunchKernelGGL((rope_lora_shrink_kernel<DT>), dim3((uint32_t)a.M, (uint32_t)(a.l.R + kShrinkWaves - 1) / kShrinkWaves),
+                               dim3(64 * kShrinkWaves), 0, s, a.l, a.x, a.K);
+        }
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
     if (L.tiles) {
         launch_tiles_tt<DT>(L.P, a, s);
+    } else if (L.few) {
+        FewArgs f = L.units;
+        static_cast<LoraProjArgs&>(f) = a;
+        if (a.M <= 16) launch_few<DT, 1>(f, L.P.tdt, s);
+        else if (a.M <= 32) launch_few<DT, 2>(f, L.P.tdt, s);
+        else launch_few<DT, 4>(f, L.P.tdt, s);
     } else {
         const uint64_t tiles = (uint64_t)((a.M + kHeadTokens - 1) / kHeadTokens) * (uint64_t)L.heads;
         hipLaunchKernelGGL((rope_lora_head_kernel<DT>), dim3((uint32_t)std::min<uint64_t>(tiles, kMaxGridItems / 256)),

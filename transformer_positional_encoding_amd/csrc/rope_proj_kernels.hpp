@@ -216,6 +216,7 @@ struct ProjTab8 {
 template <class ARGS>
 struct ProjAdapters {
     static constexpr bool kAny = false;
+    struct Square {};        // what a square tile's wave holds through the K loop
 };
 
 template <int DT, int BN, int TT, class ARGS = ProjArgs>
@@ -838,6 +839,9 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     // K is a whole number of stage pairs (the host checks): the last pair
     // ends the loop without a branch on the stage count
     const int32_t KT = a.K / kProjBK;
+    typename ProjAdapters<ARGS>::Square adapters;
+    if constexpr (ProjAdapters<ARGS>::kAny)
+        ProjAdapters<ARGS>::template find_square<DT>(a, adapters, m0 + wm * 128, lane);
 #pragma unroll
     for (int i = 0; i < LW; ++i) load1(0, 0, i);
     if constexpr (EPI >= 0)
@@ -861,11 +865,13 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
         stage(S1{}, More{}, Later{}, kt);
         stage(S0{}, More{}, Later{}, kt + 1);
     }
+    if constexpr (ProjAdapters<ARGS>::kAny)
+        ProjAdapters<ARGS>::template fetch_square<DT>(a, adapters, m0 + wm * 128, n0 + wn * 128, lane);
     stage(S1{}, Last{}, Later{}, kt);
     proj_wait_vm<0>();                                 // this wave's table rows are in LDS
     __syncthreads();                                   // every wave is done with the ring
     if constexpr (ProjAdapters<ARGS>::kAny)
-        ProjAdapters<ARGS>::template add_square<DT>(a, acc, m0 + wm * 128, n0 + wn * 128, lane);
+        ProjAdapters<ARGS>::template add_square<DT>(a, adapters, acc, m0 + wm * 128, n0 + wn * 128, lane);
 
     if constexpr (EPI >= 0) {
         proj_sq_epilogue_vec<DT, TT, EPI == 1>(a, acc, smem, m0, n0, wm, wn, wave, lane);
