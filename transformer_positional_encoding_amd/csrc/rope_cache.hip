@@ -134,12 +134,167 @@ struct ReadGeneral {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_general_kernel<DT, FMT>); }
 };
 
+template <int C>
+struct WriteVec {
+    template <int DT, int FMT>
+    struct K {
+        static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_write_kernel<DT, FMT, C>); }
+    };
+};
+template <int DT, int FMT>
+struct ReadVec {
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_kernel<DT, FMT, false>); }
+};
+template <int DT, int FMT>
+struct ReadVecTurn {
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_kernel<DT, FMT, true>); }
+};
+template <int DT, int FMT>
+struct ReadWave {
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_wave_kernel<DT, FMT, false>); }
+};
+template <int DT, int FMT>
+struct ReadWaveTurn {
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_wave_kernel<DT, FMT, true>); }
+};
+
+// Whether 8-lane chunks of these rows are 16-byte aligned.
+bool rows_in_chunks(const RowsPlan& r, int esize)
+{
+    const int64_t per = 16 / esize;
+    return r.N == 0 || (r.D % 8 == 0 && aligned16(r.data) && r.sb % per == 0 && r.ss % per == 0 && r.sn % per == 0);
+}
+
+// Whether the codes of 8 lanes are aligned to their size.
+bool cache_in_chunks(const CachePlan& c)
+{
+    const uintptr_t bytes = !c.quantised ? 16 : c.format == ROPE_CACHE_INT4 ? 4 : 8;
+    if (reinterpret_cast<uintptr_t>(c.data) % bytes != 0) return false;
+    for (int k = 0; k < 3; ++k)
+        if (c.st[k] % (int64_t)bytes != 0) return false;
+    return true;
+}
+
+// Whether the slice is whole chunks whose partners are in the chunk or whole
+// chunks away.
+bool turn_in_chunks(const Plan& p)
+{
+    return p.start % 8 == 0 && p.L % 8 == 0 && (p.half == 1 || p.half % 8 == 0);
+}
+
+bool power_of_two(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
+
+uint32_t log2_of(uint32_t v)
+{
+    uint32_t s = 0;
+    while ((1u << s) < v) ++s;
+    return s;
+}
+
+// Chunks per scale for the write kernel: 0 for one scale a row; -1 if the
+// kernel does not take the group.
+int group_chunks(const CachePlan& c, int64_t D)
+{
+    if (!c.quantised || c.group == D) return 0;
+    return c.group % 8 == 0 && power_of_two(c.group / 8) && c.group / 8 <= 64 ? (int)(c.group / 8) : -1;
+}
+
+// The vector write kernel's arguments and shape; false if a row or a group
+// is not in whole chunks.
+bool write_vec_args(const CacheWritePlan& p, CacheWriteVecArgs* a, int* C, uint32_t* grid, size_t* lds)
+{
+    const int es = p.rope.esize;
+    if (!rows_in_chunks(p.q, es) || !rows_in_chunks(p.k, es) || !rows_in_chunks(p.v, es)) return false;
+    if ((p.k.N > 0 && !cache_in_chunks(p.kc)) || (p.v.N > 0 && !cache_in_chunks(p.vc))) return false;
+    const bool turning = p.rotate_q || p.rotate_k;
+    if (turning && !turn_in_chunks(p.rope)) return false;
+    const int gk = p.k.N > 0 ? group_chunks(p.kc, p.k.D) : 0, gv = p.v.N > 0 ? group_chunks(p.vc, p.v.D) : 0;
+    if (gk < 0 || gv < 0) return false;
+    // the threads and chunks per thread that leave the fewest lanes idle
+    const uint32_t chunks = (uint32_t)std::max(p.q.N + p.k.N > 0 ? p.rope.D : 0, p.v.N > 0 ? p.v.D : 0) / 8;
+    uint32_t best = ~0u;
+    for (uint32_t c = 1; c <= 3; ++c) {
+        const uint32_t T = 1u << log2_of(std::max<uint32_t>((chunks + c - 1) / c, (uint32_t)std::max(std::max(gk, gv), 1)));
+        if (T <= 64 && T * c < best) {
+            best = T * c;
+            a->T = T;
+            *C = (int)c;
+        }
+    }
+    if (best == ~0u) return false;
+    a->rows_per_block = kVecThreads / a->T;
+    const uint64_t blocks = (a->rows + a->rows_per_block - 1) / a->rows_per_block;
+    if (blocks > kMaxGridItems / kVecThreads) return false;
+    *grid = (uint32_t)blocks;
+    a->turned = (uint32_t)(p.q.N + (p.rotate_k ? p.k.N : 0));
+    if (!turning) {
+        a->turned = 0;
+        a->turn.L = a->turn.pairs = 0;
+    }
+    a->gvk = (uint32_t)gk;
+    a->gvv = (uint32_t)gv;
+    a->small_slots = a->nslots < (1ll << 31);
+    a->page_div = make_fastdiv(a->small_slots ? (uint32_t)std::max<int64_t>(1, std::min<int64_t>(a->page_size, INT32_MAX)) : 1);
+    a->pairs_div = make_fastdiv(std::max<uint32_t>(1, a->turn.pairs));
+    const uint32_t token_rows = a->Nq + a->Nk + a->Nv;
+    const uint32_t tokens = (a->rows_per_block + token_rows - 2) / token_rows + 1;
+    *lds = (size_t)tokens * a->turn.pairs * 2 * sizeof(float);
+    return *lds <= 64 * 1024;
+}
+
 hipError_t launch_write(const CacheWritePlan& p, hipStream_t s)
 {
+    const int fmt = kernel_format(p.k.N > 0 ? p.kc : p.v.N > 0 ? p.vc : p.kc);
+    CacheWriteVecArgs v{};
+    static_cast<CacheWriteArgs&>(v) = write_args(p);
+    int C = 1;
+    uint32_t grid = 0;
+    size_t lds = 0;
+    if (write_vec_args(p, &v, &C, &grid, &lds)) {
+        void* args[] = {&v};
+        const void* fn = C == 1   ? by_types<WriteVec<1>::K>(p.rope.dtype, fmt)
+                         : C == 2 ? by_types<WriteVec<2>::K>(p.rope.dtype, fmt)
+                                  : by_types<WriteVec<3>::K>(p.rope.dtype, fmt);
+        return hipLaunchKernel(fn, dim3(grid), dim3(kVecThreads), args, lds, s);
+    }
     CacheWriteArgs a = write_args(p);
     void* args[] = {&a};
-    return hipLaunchKernel(by_types<WriteGeneral>(p.rope.dtype, kernel_format(p.kc)), dim3(general_grid(a.rows)),
-                           dim3(kGenThreads), args, 0, s);
+    return hipLaunchKernel(by_types<WriteGeneral>(p.rope.dtype, fmt), dim3(general_grid(a.rows)), dim3(kGenThreads),
+                           args, 0, s);
+}
+
+hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
+{
+    CacheReadVecArgs a{};
+    static_cast<CacheReadArgs&>(a) = read_args(p);
+    const int fmt = kernel_format(p.c);
+    const int64_t groups = p.rope.D / p.c.group;
+    a.chunks = (uint32_t)(p.rope.D / 8);
+    const uint64_t items = a.rows * a.chunks;
+    const bool vec = p.rope.D % 8 == 0 && rows_in_chunks(p.out, p.rope.esize) && cache_in_chunks(p.c) &&
+                     (!p.rotate || turn_in_chunks(p.rope)) && (groups == 1 || (p.c.group % 8 == 0 && power_of_two(p.c.group / 8))) &&
+                     items < (1ull << 31);
+    if (vec) {
+        a.token_chunks = a.N * a.chunks;
+        a.tokens = (uint32_t)(p.B * p.S);
+        a.group_shift = groups == 1 ? 31 : log2_of((uint32_t)(p.c.group / 8));
+        a.small_tokens = p.table_pages <= (int64_t)INT32_MAX / p.page_size;
+        a.chunk_div = make_fastdiv(a.chunks);
+        a.token_div = make_fastdiv(a.token_chunks);
+        a.page_div = make_fastdiv(a.small_tokens ? (uint32_t)p.page_size : 1);
+        a.pairs_div = make_fastdiv(std::max<uint32_t>(1, a.turn.pairs));
+        void* args[] = {&a};
+        const int dt = p.rope.dtype;
+        const bool wave = a.token_chunks >= kWaveTokenChunks;
+        const void* fn = wave ? (p.rotate ? by_types<ReadWaveTurn>(dt, fmt) : by_types<ReadWave>(dt, fmt))
+                              : (p.rotate ? by_types<ReadVecTurn>(dt, fmt) : by_types<ReadVec>(dt, fmt));
+        const uint32_t grid = wave ? (a.tokens + 3) / 4 : (uint32_t)((items + kVecThreads - 1) / kVecThreads);
+        return hipLaunchKernel(fn, dim3(grid), dim3(kVecThreads), args, 0, s);
+    }
+    CacheReadArgs g = a;
+    void* args[] = {&g};
+    return hipLaunchKernel(by_types<ReadGeneral>(p.rope.dtype, fmt), dim3(general_grid(a.rows)), dim3(kGenThreads), args,
+                           0, s);
 }
 
 rope_status_t launched(hipError_t err)
@@ -195,11 +350,7 @@ rope_status_t rope_cache_read(
                                                   lengths, starts, in, table_dtype, mode, partial_slice, &p, &why);
     if (st != ROPE_OK) return rope::set_error(st, why);
     if (p.noop) return ROPE_OK;
-    rope::CacheReadArgs a = rope::read_args(p);
-    void* args[] = {&a};
-    return rope::launched(hipLaunchKernel(rope::by_types<rope::ReadGeneral>(p.rope.dtype, rope::kernel_format(p.c)),
-                                          dim3(rope::general_grid(a.rows)), dim3(rope::kGenThreads), args, 0,
-                                          static_cast<hipStream_t>(stream)));
+    return rope::launched(rope::launch_read(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

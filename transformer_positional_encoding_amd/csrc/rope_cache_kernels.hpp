@@ -103,9 +103,9 @@ template <int FMT>
 __device__ __forceinline__ float code_of(float x, float m, float s, float inv)
 {
     const float c = fminf(fmaxf(x, -m), m);        // an infinity takes the code of +-m
+    // at most a unit or two in the last place over the largest code: rounds to it
     float q = quotient(c, s, inv);
     if constexpr (FMT != kFmtE4M3) q = rintf(q);
-    q = fminf(fmaxf(q, -fmt_max<FMT>()), fmt_max<FMT>());
     if (x != x) q = FMT == kFmtE4M3 ? x : 0.0f;
     return q;
 }
@@ -310,6 +310,452 @@ __global__ void __launch_bounds__(kGenThreads) rope_cache_read_general_kernel(Ca
             }
             Store<DT>::store1(a.out.data, off + j, x);
         }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Vector kernels: rows of whole 8-lane chunks. T threads of one wave share a
+// row, a thread holding C chunks (number c*T + t for c < C, so that the
+// threads of a row read consecutive 16 bytes of 16-bit lanes).
+//
+// Write: a block takes 256/T consecutive rows (q, k and v rows of a token
+// follow each other). The rows' chunks, and the chunk that holds a chunk's
+// partners where those lie whole chunks away, are loaded first; then the
+// block's tokens' cos and sin, each pair of each token once, go to LDS while
+// those loads are in flight; then a thread rotates, its group's largest
+// magnitude is found by shuffles among the threads that share the group, and
+// codes and scales are stored. q is rotated in place: a row lies in one wave,
+// whose loads have all returned before its first store is issued.
+// ---------------------------------------------------------------------------
+constexpr int kVecThreads = 256;
+
+// 8 lanes of storage type DT at p (16-byte aligned), as loaded.
+template <int DT>
+struct Chunk {
+    static constexpr int kVecs = DT == ROPE_DTYPE_F32 ? 2 : 1;
+    v4u q[kVecs];
+    __device__ __forceinline__ void load(const char* p)
+    {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) q[i] = reinterpret_cast<const v4u*>(p)[i];
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            Lanes<DT> t;
+            t.unpack(q[i]);
+#pragma unroll
+            for (int e = 0; e < 8 / kVecs; ++e) f[i * (8 / kVecs) + e] = t.v[e];
+        }
+    }
+};
+
+// 8 floats rounded to DT at p (16-byte aligned).
+template <int DT>
+__device__ __forceinline__ void store_chunk(char* p, const float (&f)[8])
+{
+    constexpr int V = Chunk<DT>::kVecs;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        Lanes<DT> t;
+#pragma unroll
+        for (int e = 0; e < 8 / V; ++e) t.v[e] = f[i * (8 / V) + e];
+        reinterpret_cast<v4u*>(p)[i] = t.pack();
+    }
+}
+
+// The codes of 8 lanes at p.
+template <int FMT>
+__device__ __forceinline__ void store_codes(char* p, const float (&c)[8])
+{
+    if constexpr (FMT == kFmtE4M3) {
+        int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+        w0 = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w0, true);
+        int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+        w1 = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], w1, true);
+        *reinterpret_cast<v2u*>(p) = v2u{(uint32_t)w0, (uint32_t)w1};
+    } else if constexpr (FMT == kFmtInt8) {
+        *reinterpret_cast<v2u*>(p) = v2u{pack2<FMT>(c[0], c[1]) | (pack2<FMT>(c[2], c[3]) << 16),
+                                         pack2<FMT>(c[4], c[5]) | (pack2<FMT>(c[6], c[7]) << 16)};
+    } else {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w |= ((uint32_t)(int)c[e] & 15u) << (4 * e);
+        *reinterpret_cast<uint32_t*>(p) = w;
+    }
+}
+
+// Where a chunk stands in the slice: its place among the block's cos and sin
+// (first pair), whether it holds first lanes, its partners' chunk as a
+// distance in lanes (0: within the chunk).
+struct ChunkTurn {
+    bool in;
+    bool first;
+    int32_t to_partner;
+    uint32_t pair;
+};
+
+__device__ __forceinline__ ChunkTurn chunk_turn(const Turn& t, uint32_t lane0)
+{
+    ChunkTurn k;
+    const uint32_t rel = lane0 - t.start;                // wraps below the slice
+    k.in = lane0 >= t.start && rel < t.L;
+    if (t.half == 1) {
+        k.first = true;
+        k.to_partner = 0;
+        k.pair = rel / 2;
+    } else {
+        const uint32_t h = fast_div(k.in ? rel : 0, t.half_div);
+        k.first = (h & 1u) == 0;
+        k.to_partner = k.first ? (int32_t)t.half : -(int32_t)t.half;
+        k.pair = (h >> 1) * t.half + rel - h * t.half;
+    }
+    return k;
+}
+
+// The 8 lanes of a chunk in the slice, rotated: x and its partners p (the
+// chunk itself where pairs are adjacent), cos and sin of its pairs.
+__device__ __forceinline__ void turn_chunk(float (&x)[8], const float (&p)[8], const ChunkTurn& k, bool adjacent,
+                                           const float* cosv, const float* sinv)
+{
+    const float4* c4 = reinterpret_cast<const float4*>(cosv + k.pair);
+    const float4* s4 = reinterpret_cast<const float4*>(sinv + k.pair);
+    if (adjacent) {
+        const float4 c = c4[0], s = s4[0];
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = rotate_own_unfused(a, b, cc[i], ss[i], true);
+            x[2 * i + 1] = rotate_own_unfused(b, a, cc[i], ss[i], false);
+        }
+    } else {
+        const float4 c0 = c4[0], c1 = c4[1], s0 = s4[0], s1 = s4[1];
+        const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = rotate_own_unfused(x[e], p[e], cc[e], ss[e], k.first);
+    }
+}
+
+struct CacheWriteVecArgs : CacheWriteArgs {
+    uint32_t T;               // threads per row (a power of two up to 64)
+    uint32_t rows_per_block;  // 256 / T
+    uint32_t turned;          // rows of a token that are rotated: its first ones
+    uint32_t gvk, gvv;        // chunks per scale of k and v: a power of two up to T, or 0: the whole row
+    int32_t small_slots;      // slots fit 32 bits
+    FastDiv page_div, pairs_div;
+};
+
+template <int DT, int FMT, int C>
+__global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWriteVecArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) float turn_lds[];   // cos of the block's tokens' pairs, then sin
+    constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
+    const uint32_t t = threadIdx.x;
+    const uint32_t T = a.T;
+    const uint32_t tt = t & (T - 1);
+    const uint32_t row0 = blockIdx.x * a.rows_per_block;
+    const uint32_t rows = (uint32_t)a.rows;
+    const uint32_t last = min(row0 + a.rows_per_block, rows) - 1;
+    const uint32_t tok0 = fast_div(row0, a.row_div), tok1 = fast_div(last, a.row_div);
+    // whether the block holds a rotated row
+    const bool turning = a.turned > 0 && (tok1 > tok0 || row0 - tok0 * a.row_div.d < a.turned);
+    const uint32_t entries = turning ? (tok1 - tok0 + 1) * a.turn.pairs : 0;
+    float* cosv = turn_lds;
+    float* sinv = turn_lds + (tok1 - tok0 + 1) * a.turn.pairs;
+    // the thread's first (cos, sin) entry: its position and frequency
+    const uint32_t row = min(row0 + t / T, last);
+    const bool live = row0 + t / T <= last;
+    const RowAt r = row_at(a, row);
+    const Rows& src = r.kind == 0 ? a.q : r.kind == 1 ? a.k : a.v;
+    const uint32_t D = r.kind == 2 ? a.Dv : a.Dk;
+    char* base = src.data + (r.b * src.sb + r.s * src.ss + r.n * src.sn) * ES;
+    const bool turned = r.kind == 0 || (r.kind == 1 && a.rotate_k);
+    const bool adjacent = a.turn.half == 1;
+    int64_t slot = 0;
+    if (r.kind != 0) slot = a.slots[r.b * a.slot_sb + r.s * a.slot_ss];
+    Chunk<DT> own[C], par[C];
+    ChunkTurn kt[C];
+    bool in[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const uint32_t lane0 = (c * T + tt) * 8;
+        in[c] = lane0 < D;
+        kt[c] = chunk_turn(a.turn, lane0);
+        kt[c].in = kt[c].in && turned && in[c];
+        const uint32_t at = in[c] ? lane0 : 0;
+        own[c].load(base + at * ES);
+        if (!adjacent && kt[c].in) par[c].load(base + (int64_t)((int32_t)at + kt[c].to_partner) * ES);
+    }
+    for (uint32_t e = t; e < entries; e += kVecThreads) {
+        const uint32_t k = fast_div(e, a.pairs_div);
+        const uint32_t tok = tok0 + k;
+        const uint32_t b = fast_div(tok, a.s_div);
+        const float2 cs = turn_cos_sin(a.turn, b, tok - b * a.s_div.d, e - k * a.turn.pairs);
+        cosv[e] = cs.x;
+        sinv[e] = cs.y;
+    }
+    if (turning) __syncthreads();
+    const uint32_t tok_off = (r.b * a.s_div.d + r.s - tok0) * a.turn.pairs;
+    float x[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        own[c].widen(x[c]);
+        if (kt[c].in) {
+            float p[8];
+            if (adjacent) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = 0.0f;
+            } else {
+                par[c].widen(p);
+            }
+            turn_chunk(x[c], p, kt[c], adjacent, cosv + tok_off, sinv + tok_off);
+        }
+    }
+    if (r.kind == 0) {
+        // (a wave may hold q and k rows: the shuffles below take every lane)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (live && kt[c].in) store_chunk<DT>(base + (c * T + tt) * 8 * ES, x[c]);
+    }
+    const CacheRef& ch = r.kind == 2 ? a.vc : a.kc;
+    const bool store = live && r.kind != 0 && slot >= 0 && slot < a.nslots;
+    int64_t page, in_page;
+    if (a.small_slots) {
+        const uint32_t s32 = store ? (uint32_t)slot : 0;
+        const uint32_t pg = fast_div(s32, a.page_div);
+        page = pg;
+        in_page = s32 - pg * a.page_div.d;
+    } else {
+        page = slot / a.page_size;
+        in_page = slot - page * a.page_size;
+    }
+    char* dst = ch.data + page * ch.st[0] + in_page * ch.st[1] + r.n * ch.st[2];
+    if constexpr (FMT == kFmtSame) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (store && in[c]) store_chunk<DT>(dst + (c * T + tt) * 8 * ES, x[c]);
+    } else {
+        float mag[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            mag[c] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mag[c] = fmaxf(mag[c], in[c] ? finite_mag(x[c][e]) : 0.0f);
+        }
+        const uint32_t gv = r.kind == 2 ? a.gvv : a.gvk;
+        if (C > 1 && gv == 0) {
+            float m = mag[0];
+#pragma unroll
+            for (int c = 1; c < C; ++c) m = fmaxf(m, mag[c]);
+#pragma unroll
+            for (int c = 0; c < C; ++c) mag[c] = m;
+        }
+        const uint32_t width = gv == 0 ? T : gv;
+        for (uint32_t d = 1; d < T; d <<= 1) {             // the same steps for every lane
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float o = __shfl_xor(mag[c], (int)d);
+                if (d < width) mag[c] = fmaxf(mag[c], o);
+            }
+        }
+        float* sc = ch.scales + page * ch.sc[0] + in_page * ch.sc[1] + r.n * ch.sc[2];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float s = group_scale<FMT>(mag[c]), inv = 1.0f / s;
+            float code[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) code[e] = code_of<FMT>(x[c][e], mag[c], s, inv);
+            if (store && in[c]) {
+                const uint32_t chunk = c * T + tt;
+                store_codes<FMT>(dst + (FMT == kFmtInt4 ? chunk * 4 : chunk * 8), code);
+                if (gv == 0) {
+                    if (chunk == 0) sc[0] = s;
+                } else if ((chunk & (gv - 1)) == 0) {
+                    sc[chunk / gv] = s;
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Read, vector form: bound by the bytes it moves. A token's N rows are N * D/8
+// chunks; a wave takes a whole token (WAVE, tokens of 48 chunks or more), so
+// that its sequence, page and addresses are scalar work, or 256 consecutive
+// chunks of the output go to a block, each thread finding its token.
+// ---------------------------------------------------------------------------
+struct CacheReadVecArgs : CacheReadArgs {
+    uint32_t chunks;          // of a row
+    uint32_t token_chunks;    // of a token: N * chunks
+    uint32_t tokens;
+    uint32_t group_shift;     // log2 of the lanes per scale / 8, or 31: one scale a row
+    int32_t small_tokens;     // a block table's token numbers fit 31 bits
+    FastDiv chunk_div, token_div, page_div, pairs_div;
+};
+
+// 8 codes as numbers (not yet scaled).
+template <int DT, int FMT>
+struct CodeChunk {
+    using Raw = typename std::conditional<FMT == kFmtSame, Chunk<DT>,
+                                          typename std::conditional<FMT == kFmtInt4, uint32_t, v2u>::type>::type;
+    Raw q;
+    float s;
+    __device__ __forceinline__ void load(const CacheReadVecArgs& a, const char* src, const float* sc, uint32_t chunk)
+    {
+        if constexpr (FMT == kFmtSame) {
+            q.load(src + chunk * (DT == ROPE_DTYPE_F32 ? 32 : 16));
+        } else {
+            q = *reinterpret_cast<const Raw*>(src + chunk * (FMT == kFmtInt4 ? 4 : 8));
+            s = sc[a.group_shift == 31 ? 0 : chunk >> a.group_shift];
+        }
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const
+    {
+        if constexpr (FMT == kFmtSame) {
+            q.widen(f);
+        } else if constexpr (FMT == kFmtE4M3) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
+                const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
+                f[4 * i] = lo.x * s;
+                f[4 * i + 1] = lo.y * s;
+                f[4 * i + 2] = hi.x * s;
+                f[4 * i + 3] = hi.y * s;
+            }
+        } else if constexpr (FMT == kFmtInt8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = (float)((int)(q[e / 4] << (24 - 8 * (e % 4))) >> 24) * s;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = (float)((int)(q << (28 - 4 * e)) >> 28) * s;
+        }
+    }
+};
+
+// As read_place, with the token's number in 32 bits where it fits.
+__device__ __forceinline__ bool read_place32(const CacheReadVecArgs& a, uint32_t b, uint32_t s, int64_t* page,
+                                             int64_t* in_page)
+{
+    if (!a.small_tokens) return read_place(a, b, s, page, in_page);
+    const int32_t len = a.lengths[b], start = a.starts != nullptr ? a.starts[b] : 0;
+    const int64_t tok64 = (int64_t)start + s;
+    const bool ok = (int64_t)s < (int64_t)len && tok64 >= 0 && tok64 < (int64_t)0x7FFFFFFF;
+    const uint32_t tok = ok ? (uint32_t)tok64 : 0;
+    const uint32_t col = fast_div(tok, a.page_div);
+    if (!ok || (int64_t)col >= a.table_pages) return false;
+    *page = a.table[b * a.table_stride + col];
+    *in_page = tok - col * a.page_div.d;
+    return *page >= 0 && *page < a.pages;
+}
+
+template <int DT, int FMT, bool ROT>
+__device__ __forceinline__ void read_chunk(const CacheReadVecArgs& a, const char* src, const float* sc, char* dst,
+                                           uint32_t chunk, const float* cosv, const float* sinv)
+{
+    constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
+    CodeChunk<DT, FMT> own, par;
+    own.load(a, src, sc, chunk);
+    float x[8];
+    if constexpr (ROT) {
+        const ChunkTurn k = chunk_turn(a.turn, chunk * 8);
+        const bool adjacent = a.turn.half == 1;
+        if (k.in && !adjacent) par.load(a, src, sc, (uint32_t)((int32_t)(chunk * 8) + k.to_partner) / 8);
+        own.widen(x);
+        if (k.in) {
+            float p[8];
+            if (adjacent) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = 0.0f;
+            } else {
+                par.widen(p);
+            }
+            turn_chunk(x, p, k, adjacent, cosv, sinv);
+        }
+    } else {
+        own.widen(x);
+    }
+    store_chunk<DT>(dst + chunk * 8 * ES, x);
+}
+
+template <int DT, int FMT, bool ROT>
+__global__ void __launch_bounds__(kVecThreads) rope_cache_read_kernel(CacheReadVecArgs a)
+{
+    constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
+    __shared__ __attribute__((aligned(16))) float turn_lds[ROT ? 4096 : 4];
+    const uint32_t i0 = blockIdx.x * kVecThreads;
+    const uint32_t total = a.tokens * a.token_chunks;
+    const uint32_t i = min(i0 + threadIdx.x, total - 1);
+    const uint32_t tok = fast_div(i, a.token_div);
+    const uint32_t c = i - tok * a.token_chunks;
+    const uint32_t n = fast_div(c, a.chunk_div), chunk = c - n * a.chunks;
+    const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.s_div.d;
+    const uint32_t tok0 = fast_div(i0, a.token_div);
+    float* cosv = turn_lds;
+    float* sinv = turn_lds;
+    if constexpr (ROT) {
+        const uint32_t tok1 = fast_div(min(i0 + kVecThreads, total) - 1, a.token_div);
+        const uint32_t entries = (tok1 - tok0 + 1) * a.turn.pairs;
+        sinv = turn_lds + entries;
+        for (uint32_t e = threadIdx.x; e < entries; e += kVecThreads) {
+            const uint32_t k = fast_div(e, a.pairs_div);
+            const uint32_t be = fast_div(tok0 + k, a.s_div);
+            const float2 cs = turn_cos_sin(a.turn, be, tok0 + k - be * a.s_div.d, e - k * a.turn.pairs);
+            cosv[e] = cs.x;
+            sinv[e] = cs.y;
+        }
+        __syncthreads();
+        cosv += (tok - tok0) * a.turn.pairs;
+        sinv += (tok - tok0) * a.turn.pairs;
+    }
+    int64_t page, in_page;
+    if (i0 + threadIdx.x >= total || !read_place32(a, b, s, &page, &in_page)) return;
+    const char* src = a.c.data + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
+    const float* sc = a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2];
+    char* dst = a.out.data + (b * a.out.sb + s * a.out.ss + n * a.out.sn) * ES;
+    read_chunk<DT, FMT, ROT>(a, src, sc, dst, chunk, cosv, sinv);
+}
+
+constexpr uint32_t kWaveTokenChunks = 48;
+
+template <int DT, int FMT, bool ROT>
+__global__ void __launch_bounds__(kVecThreads) rope_cache_read_wave_kernel(CacheReadVecArgs a)
+{
+    constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
+    __shared__ __attribute__((aligned(16))) float turn_lds[ROT ? 4 * ROPE_D_LIMIT : 4];
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t tok = blockIdx.x * 4 + wave;
+    if (tok >= a.tokens) return;
+    const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.s_div.d;
+    int64_t page, in_page;
+    if (!read_place32(a, b, s, &page, &in_page)) return;
+    const float* cosv = nullptr;
+    const float* sinv = nullptr;
+    if constexpr (ROT) {
+        // the token's cos and sin, by the wave for itself
+        float* mine = turn_lds + wave * ROPE_D_LIMIT;
+        for (uint32_t e = lane; e < a.turn.pairs; e += 64) {
+            const float2 cs = turn_cos_sin(a.turn, b, s, e);
+            mine[e] = cs.x;
+            mine[a.turn.pairs + e] = cs.y;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        cosv = mine;
+        sinv = mine + a.turn.pairs;
+    }
+    const char* src = a.c.data + page * a.c.st[0] + in_page * a.c.st[1];
+    const float* sc = a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1];
+    char* dst = a.out.data + (b * a.out.sb + s * a.out.ss) * ES;
+#pragma unroll 2
+    for (uint32_t c = lane; c < a.token_chunks; c += 64) {
+        const uint32_t n = fast_div(c, a.chunk_div), chunk = c - n * a.chunks;
+        read_chunk<DT, FMT, ROT>(a, src + n * a.c.st[2], sc + n * a.c.sc[2], dst + n * a.out.sn * ES, chunk, cosv, sinv);
     }
 }
 
