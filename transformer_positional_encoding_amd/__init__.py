@@ -78,6 +78,20 @@ class RopeCacheStruct(ctypes.Structure):
                 ("scale_strides", ctypes.c_int64 * 3)]
 
 
+class _StructPointer:
+    """Argument type of a pointer to one of the structures above: the structure
+    itself, an array of 64-bit numbers of the same layout (which is quicker to
+    make), or None."""
+
+    @classmethod
+    def from_param(cls, v):
+        return ctypes.byref(v) if isinstance(v, ctypes.Structure) else v
+
+
+_RowsWords = ctypes.c_int64 * 6
+_CacheWords = ctypes.c_int64 * 14      # the 32-bit format with its padding as one number
+
+
 class RopeLora(ctypes.Structure):
     """The C ABI's rope_lora_t."""
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("adapters", ctypes.c_void_p),
@@ -142,7 +156,7 @@ def library() -> ctypes.CDLL:
             f.argtypes = [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p] + _ENTRY_ARGTYPES[2:]
         i64p, vp = ctypes.POINTER(ctypes.c_int64), ctypes.c_void_p
         turn = [vp, i64p, i64p, vp, vp, ctypes.c_int, ctypes.c_int64, i64p]   # positions to partial_slice
-        rows, cache = ctypes.POINTER(RopeRows), ctypes.POINTER(RopeCacheStruct)
+        rows = cache = _StructPointer
         L.rope_cache_write.restype = ctypes.c_int
         L.rope_cache_write.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, rows, rows, rows, cache, cache, vp,
                                        i64p] + turn + [ctypes.c_int32, vp]
@@ -559,6 +573,24 @@ class _nullcontext:
         return False
 
 
+_NOTHING = _nullcontext()
+
+
+def _on_device(t, stream):
+    """(stream handle, context) of a launch on t's device: torch's current
+    stream there unless one is given, and that device made current when it is
+    not. A CPU tensor (an empty call) has neither."""
+    import torch
+    if not t.is_cuda:
+        return None, _NOTHING
+    index = t.device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = getattr(stream, "cuda_stream", stream)
+    return handle, _NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+
+
 def rope_partial_check(x, r1, r2, rotary_mode="interleave", partial_slice=None) -> None:
     """Run the entry points' argument checks on tensors (on any device:
     nothing is launched or read); raises RopeError on the first failure."""
@@ -694,13 +726,8 @@ def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtyp
         tdt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(table_dtype, DTYPE_CODES.get(table_dtype))
         if tdt is None:
             raise TypeError(f"unsupported table dtype {table_dtype}")
-    dev = x.device
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream if x.is_cuda else None
-    else:
-        handle = getattr(stream, "cuda_stream", stream)
-    switch = x.is_cuda and dev.index != torch.cuda.current_device()
-    with torch.cuda.device(dev) if switch else _nullcontext():
+    handle, current = _on_device(x, stream)
+    with current:
         if pair_axes is not None:
             st = raw_axes_call(direction, x.data_ptr() or None, tuple(x.shape), _dtype_code(x),
                                positions.data_ptr() or None, tuple(positions.shape), tuple(positions.stride()),
@@ -1134,11 +1161,11 @@ def _call_pos_multi(direction, xs, positions, inv_freq, mode, partial_slice, tab
         tdt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(table_dtype, DTYPE_CODES.get(table_dtype))
         if tdt is None:
             raise TypeError(f"unsupported table dtype {table_dtype}")
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream if dev is not None else None
+    if dev is not None:
+        handle, current = _on_device(next(x for x in xs if x.numel()), stream)
     else:
-        handle = getattr(stream, "cuda_stream", stream)
-    with torch.cuda.device(dev) if dev is not None else _nullcontext():
+        handle, current = getattr(stream, "cuda_stream", stream), _NOTHING
+    with current:
         ptrs, shapes = [x.data_ptr() or None for x in xs], [tuple(x.shape) for x in xs]
         where = (positions.data_ptr() or None, tuple(positions.shape), tuple(positions.stride()),
                  inv_freq.data_ptr() or None)
@@ -1205,7 +1232,7 @@ class RopeCache:
     quantised formats: lane j of a row stands for code[j] * scale[j // group].
     """
 
-    __slots__ = ("data", "scales", "device", "struct")
+    __slots__ = ("data", "scales", "device", "words")
 
     def __init__(self, data, scales=None):
         import torch
@@ -1214,33 +1241,43 @@ class RopeCache:
         fmt = _cache_format(data.dtype)
         if fmt is None:
             raise TypeError(f"unsupported cache type {data.dtype}")
-        shape, st, es = data.shape, data.stride(), data.element_size()
-        if shape[3] > 1 and st[3] != 1:
+        pages, size, heads, dim = data.shape
+        s0, s1, s2, s3 = data.stride()
+        if s3 != 1 and dim > 1:
             raise ValueError("data: the lanes of a row must be consecutive")
-        dim = shape[3] * 2 if fmt == 5 else shape[3]
-        c = RopeCacheStruct(data.data_ptr() or None, None, fmt, shape[0], shape[1], shape[2], dim, dim,
-                            (st[0] * es, st[1] * es, st[2] * es))
-        if fmt >= 3:
-            if not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32:
-                raise TypeError("a quantised cache needs float32 scales")
-            if scales.dim() != 4 or scales.shape[:3] != shape[:3] or scales.device != data.device:
-                raise ValueError("scales must be (pages, page_size, heads, dim // group), on data's device")
-            groups, sc = scales.shape[3], scales.stride()
-            if dim and (groups < 1 or dim % groups):
-                raise ValueError(f"{groups} scales do not divide {dim} lanes")
-            if groups > 1 and sc[3] != 1:
-                raise ValueError("scales: the scales of a row must be consecutive")
-            c.scales = scales.data_ptr() or None
-            c.group = dim // groups if groups else 0
-            c.scale_strides[:] = sc[:3]
-        elif scales is not None:
-            raise ValueError(f"a {data.dtype} cache has no scales")
-        self.data, self.scales, self.device, self.struct = data, scales, data.device, c
+        self.data, self.scales, self.device = data, scales, data.device
+        if fmt < 3:
+            if scales is not None:
+                raise ValueError(f"a {data.dtype} cache has no scales")
+            es = data.element_size()
+            self.words = _CacheWords(data.data_ptr(), 0, fmt, pages, size, heads, dim, dim, s0 * es, s1 * es, s2 * es)
+            return
+        if fmt == 5:
+            dim *= 2
+        if not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32:
+            raise TypeError("a quantised cache needs float32 scales")
+        if scales.dim() != 4 or scales.device != self.device:
+            raise ValueError("scales must be (pages, page_size, heads, dim // group), on data's device")
+        p, z, h, groups = scales.shape
+        if p != pages or z != size or h != heads:
+            raise ValueError("scales must be (pages, page_size, heads, dim // group), on data's device")
+        c0, c1, c2, c3 = scales.stride()
+        if dim and (groups < 1 or dim % groups):
+            raise ValueError(f"{groups} scales do not divide {dim} lanes")
+        if groups > 1 and c3 != 1:
+            raise ValueError("scales: the scales of a row must be consecutive")
+        self.words = _CacheWords(data.data_ptr(), scales.data_ptr(), fmt, pages, size, heads, dim,
+                                 dim // groups if groups else 0, s0, s1, s2, c0, c1, c2)
 
     @property
     def group(self) -> int:
         """Lanes per scale."""
-        return self.struct.group
+        return self.words[7]
+
+    @property
+    def struct(self) -> RopeCacheStruct:
+        """The C ABI's description of the cache."""
+        return RopeCacheStruct.from_buffer(self.words)
 
 
 def rope_cache(pages: int, page_size: int, heads: int, dim: int, format: str = "e4m3", group: int | None = None,
@@ -1265,10 +1302,11 @@ def rope_cache(pages: int, page_size: int, heads: int, dim: int, format: str = "
 
 def _rows(name, t):
     """A (B, S, N, D) tensor as the C ABI's rows."""
-    shape, st = t.shape, t.stride()
-    if shape[3] > 1 and st[3] != 1:
+    _, _, n, d = t.shape
+    sb, ss, sn, sd = t.stride()
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: the lanes of a row must be consecutive")
-    return RopeRows(t.data_ptr() or None, shape[2], shape[3], st[:3])
+    return _RowsWords(t.data_ptr(), n, d, sb, ss, sn)
 
 
 def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, dtype_code, device):
@@ -1277,13 +1315,13 @@ def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table
     import torch
     mode = rotary_mode
     if isinstance(mode, str):
-        if mode not in MODES:
+        mode = MODES.get(mode)
+        if mode is None:
             raise ValueError(f"rotary_mode must be one of {sorted(MODES)}")
-        mode = MODES[mode]
     if table_dtype is None:
         tdt = dtype_code
     else:
-        tdt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(table_dtype, DTYPE_CODES.get(table_dtype))
+        tdt = _DTYPE_OF_TORCH.get(table_dtype, DTYPE_CODES.get(table_dtype))
         if tdt is None:
             raise TypeError(f"unsupported table dtype {table_dtype}")
     if positions is None or partial_slice is None:
@@ -1296,11 +1334,11 @@ def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table
             raise ValueError(f"{name} must be on {device}")
     if positions.dtype != torch.int64 or positions.dim() not in (2, 3):
         raise ValueError("positions must be an int64 tensor (B or 1, S), or (A, B or 1, S) with pair_axes")
-    shape, st = tuple(positions.shape), tuple(positions.stride())
-    if positions.dim() == 2:
+    shape, st = positions.shape, positions.stride()
+    if len(st) == 2:
         if pair_axes is not None:
             raise ValueError("pair_axes goes with positions (A, B or 1, S)")
-        shape, st = (1,) + shape, (0,) + st
+        shape, st = (1, *shape), (0, *st)
     else:
         if pair_axes is None:
             raise ValueError("positions on several axes need pair_axes")
@@ -1311,13 +1349,6 @@ def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table
         raise ValueError(f"inv_freq must hold (end - start) / 2 = {(end - start) // 2} frequencies")
     return (positions.data_ptr() or None, _I64x3(*shape), _I64x3(*st), inv_freq.data_ptr() or None,
             None if pair_axes is None else _i32_array(pair_axes), tdt, mode, _I64x2(start, end))
-
-
-def _stream_handle(stream, device):
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return getattr(stream, "cuda_stream", stream)
 
 
 def rope_cache_write(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None, rotary_mode="interleave",
@@ -1344,41 +1375,41 @@ def rope_cache_write(k, v, k_cache, v_cache, slots, positions=None, inv_freq=Non
     each group of lanes scale = largest finite magnitude / Q (448 for e4m3,
     127, 7), code = k / scale rounded once to the nearest, ties to even."""
     import torch
-    for name, t in (("k", k), ("v", v), ("q", q)):
-        if t is None and name != "k":
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a 4-D torch.Tensor (B, S, heads, dim)")
+    if k.numel() and not k.is_cuda:
+        raise ValueError("k must be a GPU tensor")
+    code, dev, dtype = _dtype_code(k), k.device, k.dtype
+    B, S, _, _ = k.shape
+    for name, t in (("v", v), ("q", q)):
+        if t is None:
             continue
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a 4-D torch.Tensor (B, S, heads, dim)")
-        if t.dtype != k.dtype:
+        if t.dtype != dtype:
             raise TypeError("q, k and v must share a dtype")
-        if t.shape[:2] != k.shape[:2]:
+        b, s, _, _ = t.shape
+        if b != B or s != S:
             raise ValueError(f"{name} must have k's tokens")
-        if t.numel() and not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor")
-        if t.device != k.device:
-            raise ValueError(f"{name} must be on {k.device}")
-    code, dev = _dtype_code(k), k.device
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c is None and name == "v_cache":
-            continue
-        if not isinstance(c, RopeCache):
-            raise TypeError(f"{name} must be a RopeCache")
-        if c.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
-    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or slots.shape != k.shape[:2]:
+    if not isinstance(k_cache, RopeCache) or not (v_cache is None or isinstance(v_cache, RopeCache)):
+        raise TypeError("k_cache and v_cache must be RopeCache objects")
+    if k_cache.device != dev or (v_cache is not None and v_cache.device != dev):
+        raise ValueError(f"k_cache and v_cache must be on {dev}")
+    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or slots.dim() != 2 or \
+            slots.size(0) != B or slots.size(1) != S:
         raise ValueError("slots must be an int64 tensor (B, S)")
     if slots.device != dev:
         raise ValueError(f"slots must be on {dev}")
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
-    B, S = k.shape[:2]
-    switch = k.is_cuda and dev.index != torch.cuda.current_device()
-    handle = _stream_handle(stream, dev) if k.is_cuda else None
-    with torch.cuda.device(dev) if switch else _nullcontext():
+    handle, current = _on_device(k, stream)
+    with current:
         st = library().rope_cache_write(
             B, S, code, None if q is None else _rows("q", q), _rows("k", k), None if v is None else _rows("v", v),
-            k_cache.struct, None if v_cache is None else v_cache.struct, slots.data_ptr() or None,
+            k_cache.words, None if v_cache is None else v_cache.words, slots.data_ptr() or None,
             _I64x2(*slots.stride()), *turn, 1 if rotate_k else 0, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
@@ -1427,11 +1458,10 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
     if block_table.device != dev:
         raise ValueError(f"block_table must be on {dev}")
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
-    switch = out.is_cuda and dev.index != torch.cuda.current_device()
-    handle = _stream_handle(stream, dev) if out.is_cuda else None
-    with torch.cuda.device(dev) if switch else _nullcontext():
+    handle, current = _on_device(out, stream)
+    with current:
         st = library().rope_cache_read(
-            B, S, code, _rows("out", out), cache.struct, block_table.data_ptr() or None, block_table.shape[1],
+            B, S, code, _rows("out", out), cache.words, block_table.data_ptr() or None, block_table.shape[1],
             block_table.stride(0), lengths.data_ptr() or None, None if starts is None else starts.data_ptr() or None,
             *turn, handle)
     if st != ROPE_OK:
@@ -1563,10 +1593,12 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
         if workspace is None:
             workspace = torch.empty(B * S * rank * 4 if count else 0, dtype=torch.uint8, device=dev)
     for name, t in (("x", x), ("w", w), ("a", a), ("b", b), ("adapters", adapters), ("out", out),
-                    ("workspace", workspace)) + ((("scales", scales),) if scales is not None else ()):
+                    ("workspace", workspace), ("scales", scales)):
+        if t is None:
+            continue
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.numel() and not t.is_cuda:
+        if not t.is_cuda and t.numel():
             raise ValueError(f"{name} must be a GPU tensor")
         if t.device != dev:
             raise ValueError(f"{name} must be on {dev}")
@@ -1575,10 +1607,9 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
             raise ValueError(f"{name} must be on {dev}")
     lora = RopeLora(a.data_ptr() or None, b.data_ptr() or None, adapters.data_ptr() or None,
                     None if scales is None else scales.data_ptr() or None, count, rank)
-    handle = _stream_handle(stream, dev) if x.is_cuda else None
+    handle, current = _on_device(x, stream)
     sl = None if partial_slice is None else _I64x2(*partial_slice)
-    switch = x.is_cuda and dev.index != torch.cuda.current_device()
-    with torch.cuda.device(dev) if switch else _nullcontext():
+    with current:
         st = library().rope_proj_lora_fwd(
             out.data_ptr() or None, _dtype_code(out), x.data_ptr() or None, w.data_ptr() or None, _dtype_code(x),
             _I64x4(*y_shape), K, lora, r1.data_ptr() or None, _arr4(r1.shape), _arr4(r1.stride()),

@@ -134,13 +134,25 @@ struct ReadGeneral {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_general_kernel<DT, FMT>); }
 };
 
-template <int C>
+template <int C, bool PAR>
 struct WriteVec {
     template <int DT, int FMT>
     struct K {
-        static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_write_kernel<DT, FMT, C>); }
+        static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_write_kernel<DT, FMT, C, PAR>); }
     };
 };
+
+template <bool PAR>
+const void* write_kernel(int C, int dtype, int fmt)
+{
+    switch (C) {
+    case 1: return by_types<WriteVec<1, PAR>::template K>(dtype, fmt);
+    case 2: return by_types<WriteVec<2, PAR>::template K>(dtype, fmt);
+    case 3: return by_types<WriteVec<3, PAR>::template K>(dtype, fmt);
+    default: return by_types<WriteVec<9, PAR>::template K>(dtype, fmt);
+    }
+}
+
 template <int DT, int FMT>
 struct ReadVec {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_kernel<DT, FMT, false>); }
@@ -210,35 +222,44 @@ bool write_vec_args(const CacheWritePlan& p, CacheWriteVecArgs* a, int* C, uint3
     if (turning && !turn_in_chunks(p.rope)) return false;
     const int gk = p.k.N > 0 ? group_chunks(p.kc, p.k.D) : 0, gv = p.v.N > 0 ? group_chunks(p.vc, p.v.D) : 0;
     if (gk < 0 || gv < 0) return false;
-    // the threads and chunks per thread that leave the fewest lanes idle
+    // Threads per row and chunks per thread: the fewest idle lanes; among
+    // those the most chunks per thread that leave a row 8 threads (128 bytes
+    // of 16-bit lanes a load).
     const uint32_t chunks = (uint32_t)std::max(p.q.N + p.k.N > 0 ? p.rope.D : 0, p.v.N > 0 ? p.v.D : 0) / 8;
     uint32_t best = ~0u;
-    for (uint32_t c = 1; c <= 3; ++c) {
+    for (const uint32_t c : {1u, 2u, 3u, 9u}) {
         const uint32_t T = 1u << log2_of(std::max<uint32_t>((chunks + c - 1) / c, (uint32_t)std::max(std::max(gk, gv), 1)));
-        if (T <= 64 && T * c < best) {
-            best = T * c;
+        if (T > 64) continue;
+        const uint32_t cost = 2 * T * c + (T < 8 ? 1 : 0);
+        if (cost < best || (cost == best && T >= 8)) {
+            best = cost;
             a->T = T;
             *C = (int)c;
         }
     }
     if (best == ~0u) return false;
     a->rows_per_block = kVecThreads / a->T;
-    const uint64_t blocks = (a->rows + a->rows_per_block - 1) / a->rows_per_block;
-    if (blocks > kMaxGridItems / kVecThreads) return false;
-    *grid = (uint32_t)blocks;
-    a->turned = (uint32_t)(p.q.N + (p.rotate_k ? p.k.N : 0));
-    if (!turning) {
-        a->turned = 0;
-        a->turn.L = a->turn.pairs = 0;
-    }
+    a->t_div = make_fastdiv(a->T);
+    if (!turning) a->turn.L = a->turn.pairs = 0;
+    a->own_partner = *C == 2 && p.rope.start == 0 && p.rope.half == 8 * (int64_t)a->T && p.rope.L == 2 * p.rope.half;
     a->gvk = (uint32_t)gk;
     a->gvv = (uint32_t)gv;
     a->small_slots = a->nslots < (1ll << 31);
     a->page_div = make_fastdiv(a->small_slots ? (uint32_t)std::max<int64_t>(1, std::min<int64_t>(a->page_size, INT32_MAX)) : 1);
     a->pairs_div = make_fastdiv(std::max<uint32_t>(1, a->turn.pairs));
-    const uint32_t token_rows = a->Nq + a->Nk + a->Nv;
-    const uint32_t tokens = (a->rows_per_block + token_rows - 2) / token_rows + 1;
-    *lds = (size_t)tokens * a->turn.pairs * 2 * sizeof(float);
+    a->nq_div = make_fastdiv(std::max<uint32_t>(1, a->Nq));
+    a->nk_div = make_fastdiv(std::max<uint32_t>(1, a->Nk));
+    a->nv_div = make_fastdiv(std::max<uint32_t>(1, a->Nv));
+    const auto blocks = [&](uint32_t N) { return ((uint64_t)a->tokens * N + a->rows_per_block - 1) / a->rows_per_block; };
+    // tokens that a block's rows of a kind can span
+    const auto spans = [&](uint32_t N) { return N == 0 ? 0 : (a->rows_per_block + N - 2) / N + 1; };
+    const uint64_t all = blocks(a->Nq) + blocks(a->Nk) + blocks(a->Nv);
+    if (all > kMaxGridItems / kVecThreads) return false;
+    a->blocks_q = (uint32_t)blocks(a->Nq);
+    a->blocks_k = (uint32_t)blocks(a->Nk);
+    *grid = (uint32_t)all;
+    a->lds_floats = std::max(spans(a->Nq), a->rotate_k ? spans(a->Nk) : 0) * a->turn.pairs;
+    *lds = 2 * (size_t)a->lds_floats * sizeof(float);
     return *lds <= 64 * 1024;
 }
 
@@ -252,9 +273,8 @@ hipError_t launch_write(const CacheWritePlan& p, hipStream_t s)
     size_t lds = 0;
     if (write_vec_args(p, &v, &C, &grid, &lds)) {
         void* args[] = {&v};
-        const void* fn = C == 1   ? by_types<WriteVec<1>::K>(p.rope.dtype, fmt)
-                         : C == 2 ? by_types<WriteVec<2>::K>(p.rope.dtype, fmt)
-                                  : by_types<WriteVec<3>::K>(p.rope.dtype, fmt);
+        const bool par = v.turn.L > 0 && v.turn.half != 1;
+        const void* fn = par ? write_kernel<true>(C, p.rope.dtype, fmt) : write_kernel<false>(C, p.rope.dtype, fmt);
         return hipLaunchKernel(fn, dim3(grid), dim3(kVecThreads), args, lds, s);
     }
     CacheWriteArgs a = write_args(p);

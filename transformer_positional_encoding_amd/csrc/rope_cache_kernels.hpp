@@ -69,41 +69,48 @@ __device__ __forceinline__ uint32_t turn_pair(const Turn& t, uint32_t j, bool* f
     return (h >> 1) * t.half + (j - h * t.half);
 }
 
-// The scale of a group whose largest finite magnitude is m.
+// The scale of a group whose largest finite magnitude is m: m / Q rounded to
+// fp32, by the residual of its approximation (exact, and 1/Q is a correctly
+// rounded constant, so the second product's sum rounds as the quotient does).
+// Below 2^-100 the floor takes over.
 template <int FMT>
 __device__ __forceinline__ float group_scale(float m)
 {
-    return m > 0.0f ? fmaxf(m / fmt_max<FMT>(), 0x1p-100f) : 1.0f;
+    constexpr float Q = fmt_max<FMT>(), inv = 1.0f / Q;
+    const float s = m * inv;
+    return m > 0.0f ? fmaxf(__builtin_fmaf(__builtin_fmaf(-s, Q, m), inv, s), 0x1p-100f) : 1.0f;
 }
+
+// 1 / s to a unit in the last place, which is all that quotient() needs.
+__device__ __forceinline__ float scale_inverse(float s) { return __builtin_amdgcn_rcpf(s); }
 
 // A float on the same side of every code and of every midpoint between two
 // codes as the exact x / s, and equal to one only where x / s is. Codes and
 // midpoints (t below) have at most 8 significant bits, so among fp32 numbers
 // their significands are even. q is x / s within one unit in the last place
-// (one Newton step on x * (1/s)) and e its residual, exact by the fused
-// multiply-add. q odd: q is not a t and the nearest t are more than a unit
-// away. q even and e not 0: one unit towards x / s makes it odd, and leaves
-// it on the side where x / s lies. Quotients below 2^-12 round to zero in
-// every format and are left alone, so the scale's floor of 2^-100 keeps
-// every residual that decides out of the subnormals.
+// (one Newton step on x * (1/s)) and e its residual, whose sign the fused
+// multiply-add gives exactly; where e is not 0, q becomes the odd number on
+// the side of q where x / s lies (q - 1 unit if it lies nearer to zero, with
+// the last bit set): past no t, as a t next to it is q itself or further than
+// a unit. A q that underflows has x's sign, as e does. Scales are 2^-100 or
+// more, which keeps every residual that decides out of the subnormals.
 __device__ __forceinline__ float quotient(float x, float s, float inv)
 {
     const float q0 = x * inv;
     const float q = __builtin_fmaf(__builtin_fmaf(-q0, s, x), inv, q0);
     const float e = __builtin_fmaf(-q, s, x);
-    const uint32_t u = __float_as_uint(q);
-    const uint32_t away = (__float_as_uint(e) ^ u) >> 31;          // 1: x / s lies nearer to zero
-    const bool move = e != 0.0f && (u & 1u) == 0 && fabsf(q) >= 0x1p-12f;
-    return __uint_as_float(move ? u + 1u - 2u * away : u);
+    const int32_t u = (int32_t)__float_as_uint(q);
+    const int32_t nearer = ((int32_t)__float_as_uint(e) ^ u) >> 31;       // -1 or 0
+    return __uint_as_float((uint32_t)(e != 0.0f ? (u + nearer) | 1 : u));
 }
 
 // The code of lane value x (as a float that the format holds) in a group of
-// largest finite magnitude m and scale s.
+// largest finite magnitude m and scale s. A quotient lies at most a unit or
+// two in the last place over the largest code, and rounds to it.
 template <int FMT>
 __device__ __forceinline__ float code_of(float x, float m, float s, float inv)
 {
     const float c = fminf(fmaxf(x, -m), m);        // an infinity takes the code of +-m
-    // at most a unit or two in the last place over the largest code: rounds to it
     float q = quotient(c, s, inv);
     if constexpr (FMT != kFmtE4M3) q = rintf(q);
     if (x != x) q = FMT == kFmtE4M3 ? x : 0.0f;
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(kGenThreads) rope_cache_write_general_kernel(C
             // lanes 2i and 2i+1 share a group (groups are even)
             for (uint32_t i = t; i < D / 2; i += kGenThreads) {
                 const float m = __uint_as_float(mag[2 * i / c.group]);
-                const float s = group_scale<FMT>(m), inv = 1.0f / s;
+                const float s = group_scale<FMT>(m), inv = scale_inverse(s);
                 const float c0 = code_of<FMT>(z[2 * i], m, s, inv), c1 = code_of<FMT>(z[2 * i + 1], m, s, inv);
                 if constexpr (FMT == kFmtInt4) {
                     dst[i] = (char)(((uint32_t)(int)c0 & 15u) | (((uint32_t)(int)c1 & 15u) << 4));
@@ -314,30 +321,56 @@ __global__ void __launch_bounds__(kGenThreads) rope_cache_read_general_kernel(Ca
 }
 
 // ---------------------------------------------------------------------------
-// Vector kernels: rows of whole 8-lane chunks. T threads of one wave share a
-// row, a thread holding C chunks (number c*T + t for c < C, so that the
-// threads of a row read consecutive 16 bytes of 16-bit lanes).
+// Vector kernels: rows of whole 8-lane chunks.
 //
-// Write: a block takes 256/T consecutive rows (q, k and v rows of a token
-// follow each other). The rows' chunks, and the chunk that holds a chunk's
-// partners where those lie whole chunks away, are loaded first; then the
-// block's tokens' cos and sin, each pair of each token once, go to LDS while
-// those loads are in flight; then a thread rotates, its group's largest
-// magnitude is found by shuffles among the threads that share the group, and
-// codes and scales are stored. q is rotated in place: a row lies in one wave,
-// whose loads have all returned before its first store is issued.
+// Write. T threads of one wave share a row, a thread holding C chunks (number
+// c*T + t for c < C, so that the threads of a row read consecutive 16 bytes of
+// 16-bit lanes). A block takes 256/T consecutive rows of one kind (q, k or v):
+// what belongs to the kind is then scalar work. It is bound by instructions as
+// much as by bytes: finding a row's place costs a thread some 80 of them, a
+// chunk's rotation 24 and its codes 100, so a thread takes as many chunks of a
+// row as leave no lane idle (D = 128: 8 threads of 2 chunks; 576: 8 of 9).
+// Measured on MI355X (K and V of 3 x 2039 tokens, 8 heads of 128 lanes, bf16
+// to int8, and the (4,4096,1,576) latent to e4m3, us): one chunk a thread and
+// waves of mixed kinds 23.7 and 20.2; several items a block with the next
+// item's loads ahead 34.9 and 25.3 (its registers halve the waves).
+// All loads of a row, and those of the chunks that hold its partners where
+// these lie whole chunks away, go out first; the block's tokens' cos and sin,
+// each pair of each token once, go to LDS while they are in flight; then a
+// thread rotates, its group's largest magnitude is found by shuffles among the
+// threads that share the group, and codes and scales are stored. q is rotated
+// in place: a row lies in one wave, whose loads have all returned before its
+// first store is issued.
 // ---------------------------------------------------------------------------
 constexpr int kVecThreads = 256;
+
+// Global memory. Pointers that pass through an asm statement or a choice lose
+// what the compiler knew of theirs, and would be accessed with the slower
+// instructions for any memory.
+#define ROPE_GLOBAL __attribute__((address_space(1)))
+typedef ROPE_GLOBAL char gchar;
+
+__device__ __forceinline__ gchar* as_global(const void* p) { return (gchar*)(uintptr_t)p; }
+template <class V>
+__device__ __forceinline__ V gload(const gchar* p)
+{
+    return *(const ROPE_GLOBAL V*)p;
+}
+template <class V>
+__device__ __forceinline__ void gstore(gchar* p, V v)
+{
+    *(ROPE_GLOBAL V*)p = v;
+}
 
 // 8 lanes of storage type DT at p (16-byte aligned), as loaded.
 template <int DT>
 struct Chunk {
     static constexpr int kVecs = DT == ROPE_DTYPE_F32 ? 2 : 1;
     v4u q[kVecs];
-    __device__ __forceinline__ void load(const char* p)
+    __device__ __forceinline__ void load(const gchar* p)
     {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) q[i] = reinterpret_cast<const v4u*>(p)[i];
+        for (int i = 0; i < kVecs; ++i) q[i] = gload<v4u>(p + 16 * i);
     }
     __device__ __forceinline__ void widen(float (&f)[8]) const
     {
@@ -353,7 +386,7 @@ struct Chunk {
 
 // 8 floats rounded to DT at p (16-byte aligned).
 template <int DT>
-__device__ __forceinline__ void store_chunk(char* p, const float (&f)[8])
+__device__ __forceinline__ void store_chunk(gchar* p, const float (&f)[8])
 {
     constexpr int V = Chunk<DT>::kVecs;
 #pragma unroll
@@ -361,28 +394,65 @@ __device__ __forceinline__ void store_chunk(char* p, const float (&f)[8])
         Lanes<DT> t;
 #pragma unroll
         for (int e = 0; e < 8 / V; ++e) t.v[e] = f[i * (8 / V) + e];
-        reinterpret_cast<v4u*>(p)[i] = t.pack();
+        gstore<v4u>(p + 16 * i, t.pack());
     }
 }
 
-// The codes of 8 lanes at p.
-template <int FMT>
-__device__ __forceinline__ void store_codes(char* p, const float (&c)[8])
+// The largest finite magnitude of 8 lanes; *all: every lane is finite.
+__device__ __forceinline__ float chunk_mag(const float (&x)[8], bool* all)
 {
+    float m = 0.0f, zero = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        m = fmaxf(m, fabsf(x[e]));
+        zero = __builtin_fmaf(x[e], 0.0f, zero);        // NaN once a lane is not finite
+    }
+    *all = zero == 0.0f;
+    if (!*all) {
+        m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(x[e]));
+    }
+    return m;
+}
+
+// The codes of 8 lanes at p; finite: no lane of the wave is NaN or infinite,
+// so that none has to be looked at.
+template <int FMT>
+__device__ __forceinline__ void store_codes(gchar* p, const float (&x)[8], float m, float s, float inv, bool finite)
+{
+    float c[8];
+    if (finite) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = quotient(x[e], s, inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = code_of<FMT>(x[e], m, s, inv);
+    }
     if constexpr (FMT == kFmtE4M3) {
         int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
         w0 = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w0, true);
         int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
         w1 = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], w1, true);
-        *reinterpret_cast<v2u*>(p) = v2u{(uint32_t)w0, (uint32_t)w1};
-    } else if constexpr (FMT == kFmtInt8) {
-        *reinterpret_cast<v2u*>(p) = v2u{pack2<FMT>(c[0], c[1]) | (pack2<FMT>(c[2], c[3]) << 16),
-                                         pack2<FMT>(c[4], c[5]) | (pack2<FMT>(c[6], c[7]) << 16)};
+        gstore<v2u>(p, v2u{(uint32_t)w0, (uint32_t)w1});
     } else {
-        uint32_t w = 0;
+        // adding 1.5 * 2^23 rounds to the nearest whole number, ties to even,
+        // and leaves it in the low bits
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w |= ((uint32_t)(int)c[e] & 15u) << (4 * e);
-        *reinterpret_cast<uint32_t*>(p) = w;
+        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(c[e] + 12582912.0f);
+        if constexpr (FMT == kFmtInt8) {
+            const auto four = [](uint32_t a, uint32_t b, uint32_t d, uint32_t f) {
+                return __builtin_amdgcn_perm(__builtin_amdgcn_perm(f, d, 0x0c0c0400), __builtin_amdgcn_perm(b, a, 0x0c0c0400),
+                                             0x05040100);
+            };
+            gstore<v2u>(p, v2u{four(w[0], w[1], w[2], w[3]), four(w[4], w[5], w[6], w[7])});
+        } else {
+            uint32_t v = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v |= (w[e] & 15u) << (4 * e);
+            gstore<uint32_t>(p, v);
+        }
     }
 }
 
@@ -442,86 +512,117 @@ __device__ __forceinline__ void turn_chunk(float (&x)[8], const float (&p)[8], c
 struct CacheWriteVecArgs : CacheWriteArgs {
     uint32_t T;               // threads per row (a power of two up to 64)
     uint32_t rows_per_block;  // 256 / T
-    uint32_t turned;          // rows of a token that are rotated: its first ones
+    uint32_t blocks_q, blocks_k;   // blocks of q rows, then of k rows; the rest of v rows
     uint32_t gvk, gvv;        // chunks per scale of k and v: a power of two up to T, or 0: the whole row
+    uint32_t lds_floats;      // of cos (sin follows)
+    int32_t own_partner;      // C 2: a thread's two chunks hold each other's partners
     int32_t small_slots;      // slots fit 32 bits
-    FastDiv page_div, pairs_div;
+    FastDiv t_div, nq_div, nk_div, nv_div, page_div, pairs_div;
 };
 
-template <int DT, int FMT, int C>
+// One kind of rows (scalar).
+struct KindRef {
+    gchar* data;
+    int64_t sb, ss, sn;       // elements
+    uint32_t N, D;
+    FastDiv n_div;
+    bool turned;
+};
+
+// An argument's value, in a scalar register. A choice between two arguments
+// would otherwise become a choice between their addresses, for which the
+// compiler copies all of the arguments to scratch memory.
+template <class V>
+__device__ __forceinline__ V held(V v)
+{
+    asm("" : "+s"(v));
+    return v;
+}
+
+template <int DT, int FMT, int C, bool PAR>
 __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWriteVecArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) float turn_lds[];   // cos of the block's tokens' pairs, then sin
     constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
-    const uint32_t t = threadIdx.x;
-    const uint32_t T = a.T;
-    const uint32_t tt = t & (T - 1);
-    const uint32_t row0 = blockIdx.x * a.rows_per_block;
-    const uint32_t rows = (uint32_t)a.rows;
+    const uint32_t t = threadIdx.x, tt = t & (a.T - 1);
+    const int kind = blockIdx.x < a.blocks_q ? 0 : blockIdx.x < a.blocks_q + a.blocks_k ? 1 : 2;
+    const uint32_t block = blockIdx.x - (kind == 0 ? 0 : kind == 1 ? a.blocks_q : a.blocks_q + a.blocks_k);
+    KindRef kr;
+    if (kind == 0) kr = {as_global(held(a.q.data)), held(a.q.sb), held(a.q.ss), held(a.q.sn), held(a.Nq), held(a.Dk),
+                         {held(a.nq_div.d), held(a.nq_div.mul), held(a.nq_div.shift)}, true};
+    else if (kind == 1) kr = {as_global(held(a.k.data)), held(a.k.sb), held(a.k.ss), held(a.k.sn), held(a.Nk), held(a.Dk),
+                              {held(a.nk_div.d), held(a.nk_div.mul), held(a.nk_div.shift)}, held(a.rotate_k) != 0};
+    else kr = {as_global(held(a.v.data)), held(a.v.sb), held(a.v.ss), held(a.v.sn), held(a.Nv), held(a.Dv),
+               {held(a.nv_div.d), held(a.nv_div.mul), held(a.nv_div.shift)}, false};
+    const uint32_t rows = a.tokens * kr.N;
+    const uint32_t row0 = block * a.rows_per_block;
     const uint32_t last = min(row0 + a.rows_per_block, rows) - 1;
-    const uint32_t tok0 = fast_div(row0, a.row_div), tok1 = fast_div(last, a.row_div);
-    // whether the block holds a rotated row
-    const bool turning = a.turned > 0 && (tok1 > tok0 || row0 - tok0 * a.row_div.d < a.turned);
-    const uint32_t entries = turning ? (tok1 - tok0 + 1) * a.turn.pairs : 0;
-    float* cosv = turn_lds;
-    float* sinv = turn_lds + (tok1 - tok0 + 1) * a.turn.pairs;
-    // the thread's first (cos, sin) entry: its position and frequency
-    const uint32_t row = min(row0 + t / T, last);
-    const bool live = row0 + t / T <= last;
-    const RowAt r = row_at(a, row);
-    const Rows& src = r.kind == 0 ? a.q : r.kind == 1 ? a.k : a.v;
-    const uint32_t D = r.kind == 2 ? a.Dv : a.Dk;
-    char* base = src.data + (r.b * src.sb + r.s * src.ss + r.n * src.sn) * ES;
-    const bool turned = r.kind == 0 || (r.kind == 1 && a.rotate_k);
-    const bool adjacent = a.turn.half == 1;
-    int64_t slot = 0;
-    if (r.kind != 0) slot = a.slots[r.b * a.slot_sb + r.s * a.slot_ss];
-    Chunk<DT> own[C], par[C];
+    const uint32_t tok0 = fast_div(row0, kr.n_div), tok1 = fast_div(last, kr.n_div);
+
+    // the thread's row (past the last: that one again, nothing stored)
+    const uint32_t want = row0 + fast_div(t, a.t_div);
+    const bool live = want <= last;
+    const uint32_t row = live ? want : last;
+    const uint32_t tok = fast_div(row, kr.n_div), n = row - tok * kr.N;
+    const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.s_div.d;
+    const int64_t slot = kind != 0 ? a.slots[b * a.slot_sb + s * a.slot_ss] : 0;
+    gchar* base = kr.data + (b * kr.sb + s * kr.ss + n * kr.sn) * ES;
+    Chunk<DT> own[C], par[PAR ? C : 1];
     ChunkTurn kt[C];
-    bool in[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const uint32_t lane0 = (c * T + tt) * 8;
-        in[c] = lane0 < D;
-        kt[c] = chunk_turn(a.turn, lane0);
-        kt[c].in = kt[c].in && turned && in[c];
-        const uint32_t at = in[c] ? lane0 : 0;
+        const uint32_t lane0 = (c * a.T + tt) * 8;
+        const uint32_t at = lane0 < kr.D ? lane0 : 0;
         own[c].load(base + at * ES);
-        if (!adjacent && kt[c].in) par[c].load(base + (int64_t)((int32_t)at + kt[c].to_partner) * ES);
+        kt[c] = chunk_turn(a.turn, lane0);
+        kt[c].in = kt[c].in && kr.turned;
+        if constexpr (PAR)
+            if (kt[c].in && !(C == 2 && a.own_partner)) par[c].load(base + (int32_t)(at + kt[c].to_partner) * ES);
     }
-    for (uint32_t e = t; e < entries; e += kVecThreads) {
-        const uint32_t k = fast_div(e, a.pairs_div);
-        const uint32_t tok = tok0 + k;
-        const uint32_t b = fast_div(tok, a.s_div);
-        const float2 cs = turn_cos_sin(a.turn, b, tok - b * a.s_div.d, e - k * a.turn.pairs);
-        cosv[e] = cs.x;
-        sinv[e] = cs.y;
+    if (kr.turned) {
+        const uint32_t entries = (tok1 - tok0 + 1) * a.turn.pairs;
+        for (uint32_t e = t; e < entries; e += kVecThreads) {
+            const uint32_t k = fast_div(e, a.pairs_div);
+            const uint32_t be = fast_div(tok0 + k, a.s_div);
+            const float2 cs = turn_cos_sin(a.turn, be, tok0 + k - be * a.s_div.d, e - k * a.turn.pairs);
+            turn_lds[e] = cs.x;
+            turn_lds[a.lds_floats + e] = cs.y;
+        }
+        __syncthreads();
     }
-    if (turning) __syncthreads();
-    const uint32_t tok_off = (r.b * a.s_div.d + r.s - tok0) * a.turn.pairs;
+    const float* cosv = turn_lds + (tok - tok0) * a.turn.pairs;
+    const float* sinv = cosv + a.lds_floats;
     float x[C][8];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        own[c].widen(x[c]);
-        if (kt[c].in) {
-            float p[8];
-            if (adjacent) {
+    for (int c = 0; c < C; ++c) own[c].widen(x[c]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = 0.0f;
-            } else {
-                par[c].widen(p);
-            }
-            turn_chunk(x[c], p, kt[c], adjacent, cosv + tok_off, sinv + tok_off);
+    for (int c = 0; c < C; ++c) {
+        if (!kt[c].in) continue;
+        if constexpr (PAR) {
+            float p[8];
+            if (C == 2 && a.own_partner) own[C - 1 - c].widen(p);
+            else par[c].widen(p);
+            turn_chunk(x[c], p, kt[c], false, cosv, sinv);
+        } else {
+            turn_chunk(x[c], x[c], kt[c], true, cosv, sinv);
         }
     }
-    if (r.kind == 0) {
-        // (a wave may hold q and k rows: the shuffles below take every lane)
+    if (kind == 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (live && kt[c].in) store_chunk<DT>(base + (c * T + tt) * 8 * ES, x[c]);
+            if (live && kt[c].in) store_chunk<DT>(base + (c * a.T + tt) * 8 * ES, x[c]);
+        return;
     }
-    const CacheRef& ch = r.kind == 2 ? a.vc : a.kc;
-    const bool store = live && r.kind != 0 && slot >= 0 && slot < a.nslots;
+    CacheRef cr;
+    const bool is_v = kind == 2;
+    cr.data = is_v ? held(a.vc.data) : held(a.kc.data);
+    cr.scales = is_v ? held(a.vc.scales) : held(a.kc.scales);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        cr.st[i] = is_v ? held(a.vc.st[i]) : held(a.kc.st[i]);
+        cr.sc[i] = is_v ? held(a.vc.sc[i]) : held(a.kc.sc[i]);
+    }
+    const bool store = live && slot >= 0 && slot < a.nslots;
     int64_t page, in_page;
     if (a.small_slots) {
         const uint32_t s32 = store ? (uint32_t)slot : 0;
@@ -532,20 +633,26 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWrit
         page = slot / a.page_size;
         in_page = slot - page * a.page_size;
     }
-    char* dst = ch.data + page * ch.st[0] + in_page * ch.st[1] + r.n * ch.st[2];
+    gchar* dst = as_global(cr.data) + (page * cr.st[0] + in_page * cr.st[1] + n * cr.st[2]);
     if constexpr (FMT == kFmtSame) {
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (store && in[c]) store_chunk<DT>(dst + (c * T + tt) * 8 * ES, x[c]);
+        for (int c = 0; c < C; ++c) {
+            const uint32_t lane0 = (c * a.T + tt) * 8;
+            if (store && lane0 < kr.D) store_chunk<DT>(dst + lane0 * ES, x[c]);
+        }
     } else {
         float mag[C];
+        bool fine = true;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            mag[c] = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mag[c] = fmaxf(mag[c], in[c] ? finite_mag(x[c][e]) : 0.0f);
+            bool all;
+            mag[c] = chunk_mag(x[c], &all);
+            const bool in = (c * a.T + tt) * 8 < kr.D;
+            mag[c] = in ? mag[c] : 0.0f;
+            fine = fine && (all || !in);
         }
-        const uint32_t gv = r.kind == 2 ? a.gvv : a.gvk;
+        const bool finite = __ballot(!fine) == 0;
+        const uint32_t gv = is_v ? held(a.gvv) : held(a.gvk);
         if (C > 1 && gv == 0) {
             float m = mag[0];
 #pragma unroll
@@ -553,29 +660,23 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWrit
 #pragma unroll
             for (int c = 0; c < C; ++c) mag[c] = m;
         }
-        const uint32_t width = gv == 0 ? T : gv;
-        for (uint32_t d = 1; d < T; d <<= 1) {             // the same steps for every lane
+        const uint32_t width = gv == 0 ? a.T : gv;
+        for (uint32_t d = 1; d < width; d <<= 1)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const float o = __shfl_xor(mag[c], (int)d);
-                if (d < width) mag[c] = fmaxf(mag[c], o);
-            }
-        }
-        float* sc = ch.scales + page * ch.sc[0] + in_page * ch.sc[1] + r.n * ch.sc[2];
+            for (int c = 0; c < C; ++c)
+                if (c == 0 || gv != 0) mag[c] = fmaxf(mag[c], __shfl_xor(mag[c], (int)d));
+        gchar* sc = as_global(cr.scales) + (page * cr.sc[0] + in_page * cr.sc[1] + n * cr.sc[2]) * 4;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const float s = group_scale<FMT>(mag[c]), inv = 1.0f / s;
-            float code[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) code[e] = code_of<FMT>(x[c][e], mag[c], s, inv);
-            if (store && in[c]) {
-                const uint32_t chunk = c * T + tt;
-                store_codes<FMT>(dst + (FMT == kFmtInt4 ? chunk * 4 : chunk * 8), code);
-                if (gv == 0) {
-                    if (chunk == 0) sc[0] = s;
-                } else if ((chunk & (gv - 1)) == 0) {
-                    sc[chunk / gv] = s;
-                }
+            const uint32_t chunk = c * a.T + tt;
+            if (!store || chunk * 8 >= kr.D) continue;
+            const float m = gv != 0 ? mag[c] : mag[0];
+            const float sv = group_scale<FMT>(m), inv = scale_inverse(sv);
+            store_codes<FMT>(dst + (FMT == kFmtInt4 ? chunk * 4 : chunk * 8), x[c], m, sv, inv, finite);
+            if (gv == 0) {
+                if (chunk == 0) gstore<float>(sc, sv);
+            } else if ((chunk & (gv - 1)) == 0) {
+                gstore<float>(sc + chunk / gv * 4, sv);
             }
         }
     }
@@ -603,13 +704,13 @@ struct CodeChunk {
                                           typename std::conditional<FMT == kFmtInt4, uint32_t, v2u>::type>::type;
     Raw q;
     float s;
-    __device__ __forceinline__ void load(const CacheReadVecArgs& a, const char* src, const float* sc, uint32_t chunk)
+    __device__ __forceinline__ void load(const CacheReadVecArgs& a, const gchar* src, const gchar* sc, uint32_t chunk)
     {
         if constexpr (FMT == kFmtSame) {
             q.load(src + chunk * (DT == ROPE_DTYPE_F32 ? 32 : 16));
         } else {
-            q = *reinterpret_cast<const Raw*>(src + chunk * (FMT == kFmtInt4 ? 4 : 8));
-            s = sc[a.group_shift == 31 ? 0 : chunk >> a.group_shift];
+            q = gload<Raw>(src + chunk * (FMT == kFmtInt4 ? 4 : 8));
+            s = gload<float>(sc + (a.group_shift == 31 ? 0 : chunk >> a.group_shift) * 4);
         }
     }
     __device__ __forceinline__ void widen(float (&f)[8]) const
@@ -653,7 +754,7 @@ __device__ __forceinline__ bool read_place32(const CacheReadVecArgs& a, uint32_t
 }
 
 template <int DT, int FMT, bool ROT>
-__device__ __forceinline__ void read_chunk(const CacheReadVecArgs& a, const char* src, const float* sc, char* dst,
+__device__ __forceinline__ void read_chunk(const CacheReadVecArgs& a, const gchar* src, const gchar* sc, gchar* dst,
                                            uint32_t chunk, const float* cosv, const float* sinv)
 {
     constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
@@ -713,9 +814,9 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_read_kernel(CacheReadV
     }
     int64_t page, in_page;
     if (i0 + threadIdx.x >= total || !read_place32(a, b, s, &page, &in_page)) return;
-    const char* src = a.c.data + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
-    const float* sc = a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2];
-    char* dst = a.out.data + (b * a.out.sb + s * a.out.ss + n * a.out.sn) * ES;
+    const gchar* src = as_global(a.c.data) + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
+    const gchar* sc = as_global(a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2]);
+    gchar* dst = as_global(a.out.data) + (b * a.out.sb + s * a.out.ss + n * a.out.sn) * ES;
     read_chunk<DT, FMT, ROT>(a, src, sc, dst, chunk, cosv, sinv);
 }
 
@@ -749,13 +850,13 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_read_wave_kernel(Cache
         cosv = mine;
         sinv = mine + a.turn.pairs;
     }
-    const char* src = a.c.data + page * a.c.st[0] + in_page * a.c.st[1];
-    const float* sc = a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1];
-    char* dst = a.out.data + (b * a.out.sb + s * a.out.ss) * ES;
+    const gchar* src = as_global(a.c.data) + page * a.c.st[0] + in_page * a.c.st[1];
+    const gchar* sc = as_global(a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1]);
+    gchar* dst = as_global(a.out.data) + (b * a.out.sb + s * a.out.ss) * ES;
 #pragma unroll 2
     for (uint32_t c = lane; c < a.token_chunks; c += 64) {
         const uint32_t n = fast_div(c, a.chunk_div), chunk = c - n * a.chunks;
-        read_chunk<DT, FMT, ROT>(a, src + n * a.c.st[2], sc + n * a.c.sc[2], dst + n * a.out.sn * ES, chunk, cosv, sinv);
+        read_chunk<DT, FMT, ROT>(a, src + n * a.c.st[2], sc + n * a.c.sc[2] * 4, dst + n * a.out.sn * ES, chunk, cosv, sinv);
     }
 }
 
