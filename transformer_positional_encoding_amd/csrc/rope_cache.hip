@@ -148,8 +148,7 @@ const void* write_kernel(int C, int dtype, int fmt)
     switch (C) {
     case 1: return by_types<WriteVec<1, PAR>::template K>(dtype, fmt);
     case 2: return by_types<WriteVec<2, PAR>::template K>(dtype, fmt);
-    case 3: return by_types<WriteVec<3, PAR>::template K>(dtype, fmt);
-    default: return by_types<WriteVec<9, PAR>::template K>(dtype, fmt);
+    default: return by_types<WriteVec<3, PAR>::template K>(dtype, fmt);
     }
 }
 
@@ -227,7 +226,7 @@ bool write_vec_args(const CacheWritePlan& p, CacheWriteVecArgs* a, int* C, uint3
     // of 16-bit lanes a load).
     const uint32_t chunks = (uint32_t)std::max(p.q.N + p.k.N > 0 ? p.rope.D : 0, p.v.N > 0 ? p.v.D : 0) / 8;
     uint32_t best = ~0u;
-    for (const uint32_t c : {1u, 2u, 3u, 9u}) {
+    for (uint32_t c = 1; c <= 3; ++c) {
         const uint32_t T = 1u << log2_of(std::max<uint32_t>((chunks + c - 1) / c, (uint32_t)std::max(std::max(gk, gv), 1)));
         if (T > 64) continue;
         const uint32_t cost = 2 * T * c + (T < 8 ? 1 : 0);

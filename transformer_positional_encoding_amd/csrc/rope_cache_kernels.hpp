@@ -328,12 +328,15 @@ __global__ void __launch_bounds__(kGenThreads) rope_cache_read_general_kernel(Ca
 // 16-bit lanes). A block takes 256/T consecutive rows of one kind (q, k or v):
 // what belongs to the kind is then scalar work. It is bound by instructions as
 // much as by bytes: finding a row's place costs a thread some 80 of them, a
-// chunk's rotation 24 and its codes 100, so a thread takes as many chunks of a
-// row as leave no lane idle (D = 128: 8 threads of 2 chunks; 576: 8 of 9).
-// Measured on MI355X (K and V of 3 x 2039 tokens, 8 heads of 128 lanes, bf16
-// to int8, and the (4,4096,1,576) latent to e4m3, us): one chunk a thread and
-// waves of mixed kinds 23.7 and 20.2; several items a block with the next
-// item's loads ahead 34.9 and 25.3 (its registers halve the waves).
+// chunk's rotation 24 and its codes 100, so a thread takes up to three chunks
+// of a row where that leaves no more lanes idle (D = 128: 8 threads of 2
+// chunks; 576: 32 of 3).
+// Measured on MI355X (GPU time in a graph; K and V of 3 x 2039 tokens, 8 heads
+// of 128 lanes, bf16 to int8, and the (4,4096,1,576) latent to e4m3, us): 14.6
+// and 16.3; one chunk a thread 21.1 and 46; nine (the latent) 16.8; blocks of 64
+// or 128 threads the same within 0.3; one chunk a thread and waves of mixed
+// kinds 23.7 and 20.2; several items a block with the next item's loads ahead
+// 34.9 and 25.3 (its registers halve the waves).
 // All loads of a row, and those of the chunks that hold its partners where
 // these lie whole chunks away, go out first; the block's tokens' cos and sin,
 // each pair of each token once, go to LDS while they are in flight; then a
