@@ -50,6 +50,8 @@ def test_an_empty_call_reads_no_pointer():
 
 def test_workspace_sizes():
     assert rp.rope_proj_lora_workspace(10, 64, 8) == 320
+    # past 64 tokens also their order, each adapter's filled up to 32 rows
+    assert 100 * 8 * 4 + 32 * 100 * 4 < rp.rope_proj_lora_workspace(100, 64, 8) < 100 * 8 * 4 + 33 * 100 * 4 + 4096
     for M, K, R in ((0, 64, 8), (10, 0, 8), (10, 64, 0), (10, 64, 129), (-1, 64, 8)):
         assert rp.rope_proj_lora_workspace(M, K, R) == 0
 

@@ -189,8 +189,9 @@ def test_nothing_past_the_result_is_written(M):
     n = M * 3 * 64
     guarded = torch.full((n + 8192,), 7.0, dtype=torch.bfloat16, device="cuda")
     out = guarded[4096:4096 + n].view(1, M, 3, 64)
-    ws = torch.full((M * 8 * 4 + 64,), 9, dtype=torch.uint8, device="cuda")
-    run(c, cos, sin, 3, "interleave", (0, 64), "bf16", out=out, workspace=ws[: M * 8 * 4])
+    size = rp.rope_proj_lora_workspace(M, 128, 8)
+    ws = torch.full((size + 64,), 9, dtype=torch.uint8, device="cuda")
+    run(c, cos, sin, 3, "interleave", (0, 64), "bf16", out=out, workspace=ws[:size])
     assert bool((guarded[:4096] == 7).all()) and bool((guarded[4096 + n:] == 7).all()) and bool((ws[-64:] == 9).all())
     assert torch.equal(out, run(c, cos, sin, 3, "interleave", (0, 64), "bf16")), "two runs differ"
 

@@ -1591,7 +1591,7 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
         if out is None:
             out = torch.empty(y_shape, dtype=out_dtype or x.dtype, device=dev)
         if workspace is None:
-            workspace = torch.empty(B * S * rank * 4 if count else 0, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(rope_proj_lora_workspace(B * S, K, rank) if count else 0, dtype=torch.uint8, device=dev)
     for name, t in (("x", x), ("w", w), ("a", a), ("b", b), ("adapters", adapters), ("out", out),
                     ("workspace", workspace), ("scales", scales)):
         if t is None:

@@ -14,15 +14,6 @@
 namespace rope {
 namespace {
 
-// Tokens up to which h is computed by dot products, a wave per token and
-// rank, and not by 32-token tiles: a tile's block walks a quarter of K per
-// wave, which few blocks cannot hide.
-constexpr int32_t kShrinkDotTokens = 64;
-
-// Tokens up to which the kernel for few tokens takes the call where the tiled
-// ones could: it reads w once per 64 tokens, they fill 256-token tiles.
-constexpr int32_t kFewTokens = 128;
-
 // A call's checked plan and what is launched for it.
 struct LoraLaunch {
     ProjLaunch P;
@@ -58,8 +49,6 @@ rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const v
         l.count = (int32_t)lora->count;
         l.R = (int32_t)lora->rank;
     }
-    // the tiled kernels need each rotation group within one tile
-    const bool fits = L->P.sq || proj_groups_in_tiles(p.D, p.start, p.L, L->P.a.half);
     // the kernel for few tokens: adjacent pairs that start on an even lane,
     // or partners whole fragments apart
     const ProjArgs& a = L->P.a;
@@ -73,7 +62,15 @@ rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const v
         u.slice_units = u.slice_frags / 2;
     }
     const bool units = u.apart ? a.start % 16 == 0 && a.half % 16 == 0 : a.start % 2 == 0;
-    L->tiles = fits && (a.M > kFewTokens || !units);
+    // the tiled kernels need each rotation group within one tile, and, with
+    // adapters, sorted rows: their tiles for a bound on these
+    const bool fits = L->P.sq || proj_groups_in_tiles(p.D, p.start, p.L, a.half);
+    L->tiles = fits && a.M > kLoraFewTokens && l.count <= kLoraSortAdapters;
+    if (L->tiles && l.count > 0) {
+        const int64_t MB = (lora_row_bound(a.M, l.count) + L->P.BM - 1) / L->P.BM;
+        if (MB * a.NB > (int64_t)(kMaxGridItems / (uint64_t)L->P.threads)) L->tiles = false;
+        else L->P.grid = (uint32_t)(MB * a.NB);
+    }
     L->few = !L->tiles && units;
     return ROPE_OK;
 }
@@ -96,8 +93,8 @@ void launch_tiles(const ProjLaunch& P, const ARGS& a, hipStream_t s)
     }
 }
 
-template <int DT>
-void launch_tiles_tt(const ProjLaunch& P, const LoraProjArgs& a, hipStream_t s)
+template <int DT, class ARGS>
+void launch_tiles_tt(const ProjLaunch& P, const ARGS& a, hipStream_t s)
 {
     switch (P.tdt) {
     case ROPE_DTYPE_F32: return launch_tiles<DT, ROPE_DTYPE_F32>(P, a, s);
@@ -124,18 +121,36 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t s)
     static_cast<ProjArgs&>(a) = L.P.a;
     a.l = L.l;
     if (a.l.count > 0) {
-        if (a.M > kShrinkDotTokens) {
-            hipLaunchKernelGGL((rope_lora_shrink_tile_kernel<DT>), dim3((uint32_t)((a.M + 31) / 32), (uint32_t)(a.l.R + 31) / 32),
-                               dim3(256), 0, s, a.l, a.x, a.M, a.K);
+        if (L.tiles) {
+            // rows in the order of their adapters, in the workspace behind h
+            const int64_t bound = lora_row_bound(a.M, a.l.count), places = bound + kLoraTileRows;
+            int32_t* order = reinterpret_cast<int32_t*>(a.l.h + (int64_t)a.M * a.l.R);
+            int32_t* group_ids = order + places;
+            int32_t* rows = group_ids + places / 32 + 1;
+            hipLaunchKernelGGL(rope_lora_sort_kernel, dim3(1), dim3(kSortThreads), 0, s, a.l.ids, a.l.count, a.M, order,
+                               group_ids, rows);
+            hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+            a.l.order = order;
+            a.l.group_ids = group_ids;
+            a.l.rows = rows;
+            hipLaunchKernelGGL((rope_lora_shrink_tile_kernel<DT>),
+                               dim3((uint32_t)((bound + 31) / 32), (uint32_t)(a.l.R + 31) / 32), dim3(256), 0, s, a.l, a.x,
+                               a.K);
+            err = hipGetLastError();
+            if (err != hipSuccess) return err;
         } else {
-            hipLaunchKernelGGL((rope_lora_shrink_kernel<DT>), dim3((uint32_t)a.M, (uint32_t)(a.l.R + kShrinkWaves - 1) / kShrinkWaves),
+            hipLaunchKernelGGL((rope_lora_shrink_kernel<DT>),
+                               dim3((uint32_t)a.M, (uint32_t)(a.l.R + kShrinkWaves - 1) / kShrinkWaves),
                                dim3(64 * kShrinkWaves), 0, s, a.l, a.x, a.K);
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
         }
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
     }
-    if (L.tiles) {
+    if (L.tiles && a.l.count > 0) {
         launch_tiles_tt<DT>(L.P, a, s);
+    } else if (L.tiles) {
+        launch_tiles_tt<DT>(L.P, static_cast<const ProjArgs&>(a), s);
     } else if (L.few) {
         FewArgs f = L.units;
         static_cast<LoraProjArgs&>(f) = a;

@@ -20,10 +20,15 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 struct LoraArgs {
     const uint16_t* a;     // (count, R, K)
     const uint16_t* b;     // (count, N, R)
-    const int32_t* ids;    // (M); outside [0, count): none
+    const int32_t* ids;    // (M) adapter of each token; outside [0, count): none
     const float* scales;   // (count) or NULL
     float* h;              // (M, R) workspace
     int32_t count, R;
+    // the tiled kernels' rows (see the sort): the token of each, the adapter
+    // of every 32, and how many there are
+    const int32_t* order;
+    const int32_t* group_ids;
+    const int32_t* rows;
 };
 
 struct LoraProjArgs : ProjArgs {
@@ -45,6 +50,96 @@ __device__ __forceinline__ void widen8(const v4u& q, float (&f)[8])
     t.unpack(q);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = t.v[k];
+}
+
+// ---------------------------------------------------------------------------
+// Rows for the tiled kernels: the tokens in the order of their adapters (those
+// without one last), tokens of one adapter in their own order, each adapter's
+// rows filled up to whole groups of 32 with gaps (-1). A 32-token column of a
+// tile then has one adapter whatever the batch looks like: its products go
+// straight into the accumulators, from operands fetched ahead. (With rows
+// packed, a column of several took a pass for each into cleared accumulators,
+// whose operands came 1.9 us apart under load: 100 us more than this on 8190
+// tokens of 8 adapters.) The gaps cost up to 31 rows an adapter.
+// A counting sort by one block: its 16 waves count a sixteenth of the tokens
+// each, the counts are summed over adapters and waves, and the waves place
+// their tokens, a token's rank among its 64 from the ballots of its adapter's
+// bits. No order of execution enters the result.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortBins = kLoraSortAdapters + 1;   // and one for none
+
+__global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int32_t* ids, int32_t count, int32_t M,
+                                                                     int32_t* order, int32_t* group_ids, int32_t* rows)
+{
+    static_assert(kSortBins <= kSortThreads, "a thread for each bin");
+    __shared__ int32_t at[kSortWaves][kSortBins];
+    __shared__ int32_t sums[kSortWaves];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int bins = count + 1;
+    int bits = 1;
+    while ((1 << bits) < bins) ++bits;
+    for (int w = 0; w < kSortWaves; ++w)
+        if (t < bins) at[w][t] = 0;
+    __syncthreads();
+    const int64_t seg = (((int64_t)M + kSortThreads - 1) / kSortThreads) * 64;    // tokens of a wave, whole 64s
+    const int64_t begin = wave * seg, end = min((int64_t)M, begin + seg);
+    const auto key = [&](int64_t m) {
+        const int32_t i = ids[m];
+        return i >= 0 && i < count ? i : count;
+    };
+    for (int64_t m = begin + lane; m < end; m += 64) atomicAdd(&at[wave][key(m)], 1);
+    __syncthreads();
+    // exclusive sums: over the waves for each bin, then of the bins' padded
+    // sizes over the bins
+    int32_t total = 0;
+    if (t < bins)
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int32_t n = at[w][t];
+            at[w][t] = total;
+            total += n;
+        }
+    const int32_t padded = (total + 31) & ~31;
+    int32_t sum = padded;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t o = __shfl_up(sum, d);
+        if (lane >= d) sum += o;
+    }
+    if (lane == 63) sums[wave] = sum;
+    __syncthreads();
+    int32_t before = sum - padded, all = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) before += sums[w];
+        all += sums[w];
+    }
+    if (t < bins) {
+        for (int w = 0; w < kSortWaves; ++w) at[w][t] += before;
+        for (int32_t i = total; i < padded; ++i) order[before + i] = -1;
+    }
+    // gaps to the end of the last tile of either kind
+    for (int32_t i = t; i < kLoraTileRows; i += kSortThreads) order[all + i] = -1;
+    if (t < kLoraTileRows / 32) group_ids[all / 32 + t] = -1;
+    if (t == 0) *rows = all;
+    __syncthreads();
+    for (int64_t m64 = begin; m64 < end; m64 += 64) {                    // the same turns for the whole wave
+        const int64_t m = m64 + lane;
+        const bool live = m < end;
+        const int32_t k = live ? key(m) : count;
+        uint64_t same = __ballot(live);
+        for (int i = 0; i < bits; ++i) {
+            const uint64_t set = __ballot((k >> i) & 1);
+            same &= ((k >> i) & 1) ? set : ~set;
+        }
+        if (live) {
+            const int32_t to = at[wave][k] + __popcll(same & ((1ull << lane) - 1));
+            order[to] = (int32_t)m;
+            if ((to & 31) == 0) group_ids[to / 32] = k == count ? -1 : k;
+            // the adapter's last token of the 64 moves its place on: after
+            // every read of it, a wave's LDS accesses being in order
+            if ((same >> lane) == 1) at[wave][k] = to + 1;
+        }
+    }
 }
 
 // h[m,r] of the token's adapter by the whole wave: 16 bytes of x and of a per
@@ -87,76 +182,50 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) rope_lora_shrink_kernel(Lor
 }
 
 // ---------------------------------------------------------------------------
-// h by MFMA, for prompts: a block takes 32 tokens and 32 ranks, its waves a
-// quarter of K each (whole 64-k blocks, one 128-byte line of each row), with
-// 32x32x16 MFMAs whose operands come straight from memory; the four partial
-// tiles meet in LDS in a fixed order. The k of a 64-k block may go to any MFMA
-// slot as long as a and x agree: lane l takes 16 bytes (8 k) at (2j + l/32) *
-// 16 of its row's line in step j, so a step's 64 loads fill half lines that
-// the next steps complete. Tokens of several adapters take one pass over K
-// for each; a block with more than kShrinkPasses of them takes its tokens
-// one by one with dot products, as the kernel above does: a pass costs the
-// block about what 8 tokens' dot products do.
+// h by MFMA, for prompts: a block takes 32 sorted rows, whose tokens have one
+// adapter, and 32 ranks, its waves a quarter of K each (whole 64-k blocks, one
+// 128-byte line of each row), with 32x32x16 MFMAs whose operands come straight
+// from memory; the four partial tiles meet in LDS in a fixed order. The k of a
+// 64-k block may go to any MFMA slot as long as a and x agree: lane l takes 16
+// bytes (8 k) at (2j + l/32) * 16 of its row's line in step j, so a step's 64
+// loads fill half lines that the next steps complete.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkPasses = 4;
-
 template <int DT>
-__global__ void __launch_bounds__(256) rope_lora_shrink_tile_kernel(LoraArgs l, const uint16_t* x, int32_t M, int32_t K)
+__global__ void __launch_bounds__(256) rope_lora_shrink_tile_kernel(LoraArgs l, const uint16_t* x, int32_t K)
 {
     __shared__ float part[4][32][33];
+    const int32_t row0 = (int32_t)blockIdx.x * 32;
+    if (row0 >= *l.rows) return;
+    const int32_t id = l.group_ids[blockIdx.x];
+    if (id < 0) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int fr = lane & 31, hw = lane >> 5;
-    const int32_t m0 = (int32_t)blockIdx.x * 32;
     const int r0 = (int)blockIdx.y * 32;
-    const int32_t m = min(m0 + fr, M - 1);
-    const int32_t id = lora_id(l, m);
-    uint64_t todo = __ballot(id >= 0);
-    int passes = 0;
-    for (uint64_t t = todo; t != 0; ++passes)
-        t &= ~__ballot(id == __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(t)));
-    if (passes > kShrinkPasses) {
-        // the same for every wave: all read the same ids
-        for (int i = wave; i < 32 * 32; i += 4) {
-            const int t = i >> 5, r = r0 + (i & 31);
-            if (m0 + t >= M || r >= l.R) continue;
-            const int32_t own = __builtin_amdgcn_readlane(id, t);
-            if (own < 0) continue;
-            lora_dot_k<DT>(l, x, m0 + t, own, r, K, lane);
-        }
-        return;
-    }
+    const int32_t tok = l.order[row0 + fr];
     const int32_t blocks = K / 64;
-    const uint16_t* xr = x + (int64_t)m * K + hw * 8;
-    while (todo != 0) {
-        const int32_t cur = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(todo));
-        const uint16_t* ar = l.a + ((int64_t)cur * l.R + min(r0 + fr, l.R - 1)) * K + hw * 8;
-        f32x16 acc = {};
-#pragma unroll 2
-        for (int32_t kb = wave; kb < blocks; kb += 4) {
-            v4u fx[4], fa[4];
+    const uint16_t* xr = x + (int64_t)max(tok, 0) * K + hw * 8;
+    const uint16_t* ar = l.a + ((int64_t)id * l.R + min(r0 + fr, l.R - 1)) * K + hw * 8;
+    f32x16 acc = {};
+    for (int32_t kb = wave; kb < blocks; kb += 4) {
+        v4u fx[4], fa[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                fx[j] = *reinterpret_cast<const v4u*>(xr + (int64_t)kb * 64 + j * 16);
-                fa[j] = *reinterpret_cast<const v4u*>(ar + (int64_t)kb * 64 + j * 16);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc = proj_mfma<DT>(fa[j], fx[j], acc);
+        for (int j = 0; j < 4; ++j) {
+            fx[j] = *reinterpret_cast<const v4u*>(xr + (int64_t)kb * 64 + j * 16);
+            fa[j] = *reinterpret_cast<const v4u*>(ar + (int64_t)kb * 64 + j * 16);
         }
-        // register e of lane i: rank 8*(e/4) + 4*(i/32) + e%4, token i%32
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[wave][fr][8 * (e >> 2) + 4 * hw + (e & 3)] = acc[e];
-        __syncthreads();
-        const float s = l.scales != nullptr ? l.scales[cur] : 1.0f;
-        for (int i = threadIdx.x; i < 32 * 32; i += 256) {
-            const int t = i >> 5, r = i & 31;
-            // the token's adapter from the lane that holds it: every lane of
-            // a wave reads it, so before any branch
-            const int32_t own = __shfl(id, t);
-            const float sum = (part[0][t][r] + part[1][t][r]) + (part[2][t][r] + part[3][t][r]);
-            if (own == cur && m0 + t < M && r0 + r < l.R) l.h[(int64_t)(m0 + t) * l.R + r0 + r] = sum * s;
-        }
-        todo &= ~__ballot(id == cur);
-        if (todo != 0) __syncthreads();      // the next pass rewrites part
+        for (int j = 0; j < 4; ++j) acc = proj_mfma<DT>(fa[j], fx[j], acc);
+    }
+    // register e of lane i: rank 8*(e/4) + 4*(i/32) + e%4, row i%32
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[wave][fr][8 * (e >> 2) + 4 * hw + (e & 3)] = acc[e];
+    __syncthreads();
+    const float s = l.scales != nullptr ? l.scales[id] : 1.0f;
+    for (int i = threadIdx.x; i < 32 * 32; i += 256) {
+        const int t = i >> 5, r = i & 31;
+        const int32_t to = __shfl(tok, t);
+        const float sum = (part[0][t][r] + part[1][t][r]) + (part[2][t][r] + part[3][t][r]);
+        if (to >= 0 && r0 + r < l.R) l.h[(int64_t)to * l.R + r0 + r] = sum * s;
     }
 }
 
@@ -172,17 +241,15 @@ __device__ __forceinline__ f32x4 mfma16(const v4u& a, const v4u& b, const f32x4&
 }
 
 // ---------------------------------------------------------------------------
-// The adapters' part of the tiled projections: after the K loop, R more k for
-// each adapter of the wave's tokens, on the same accumulators. A fragment of
-// 32 tokens that share an adapter (a prompt's) goes straight into them; one
-// of several adapters takes each in turn into cleared accumulators and adds
-// only its own tokens' values (not a product with h = 0, which an infinity
-// or NaN in one adapter would carry into every other's tokens).
+// The adapters' part of the tiled projections: after the K loop, R more k on
+// the same accumulators, a 32-row column at a time with its own adapter.
 // h is fp32 and the MFMA takes 16 bits: h = p0 + p1 (+ p2) in bf16, each the
 // rest of the one before it rounded to 8 bits, two parts for 16-bit outputs
 // (what is left is below 2^-16 of h, the output rounds at 2^-9 or 2^-12) and
 // three for fp32 (2^-24). fp16 weights take the same route, b = q0 + q1
 // exactly (11 bits in two of 8): h may exceed fp16's range.
+// Columns without an adapter multiply zeros by zeros. A gap's row takes the h
+// of token 0; its values are never stored.
 // ---------------------------------------------------------------------------
 
 // v rounded to bf16, as 8 lanes; v becomes what is left.
@@ -199,208 +266,124 @@ __device__ __forceinline__ v4u take_bf16(float (&v)[8])
     return v4u{w[0], w[1], w[2], w[3]};
 }
 
-// One 32 x 32 tile: c += (8 k of b per lane, BQ parts) x (of h, `parts`).
-// COLS: tokens are the tile's columns (square tiles), else its rows.
-template <int BQ, bool COLS>
-__device__ __forceinline__ void lora_mfma(f32x16& c, const v4u (&b)[BQ], const v4u (&h)[3], int parts)
+// 16 bytes of b and 8 of h (fp32) per lane: one step of 16 ranks of 32 rows and
+// 32 output lanes.
+__device__ __forceinline__ v4u lora_load_b(const LoraProjArgs& a, int32_t id, int32_t n, int r, int lane)
 {
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-        if (p < 2 || parts > 2)
-#pragma unroll
-            for (int q = 0; q < BQ; ++q)
-                c = COLS ? proj_mfma<ROPE_DTYPE_BF16>(b[q], h[p], c) : proj_mfma<ROPE_DTYPE_BF16>(h[p], b[q], c);
+    // ranks past R (the upper half of a last half step) re-read the lower half
+    const int rk = r + (lane >> 5) * 8 < a.l.R ? r + (lane >> 5) * 8 : r;
+    return *reinterpret_cast<const v4u*>(a.l.b + ((int64_t)max(id, 0) * a.N + min(n, a.N - 1)) * a.l.R + rk);
 }
 
-// The tiles of 32 tokens (this lane's id and row of h) and NT x 32 output
-// lanes from n0, at(nt) their accumulators; nothing unless `any`.
-template <int DT, int NT, bool COLS, class AT>
-__device__ __forceinline__ void lora_add_tiles(const LoraProjArgs& a, int32_t m, int32_t n0, int lane, bool any,
-                                               AT at)
-{
-    constexpr int BQ = DT == ROPE_DTYPE_F16 ? 2 : 1;
-    const LoraArgs& l = a.l;
-    const int parts = a.ydt == ROPE_DTYPE_F32 ? 3 : 2;
-    // tokens past the last repeat it (their results are never stored)
-    m = min(m, a.M - 1);
-    const int32_t id = any ? lora_id(l, m) : -1;
-    const int rl = (lane >> 5) * 8;                       // the lane's 8 of each 16 ranks
-    uint64_t todo = __ballot(id >= 0);
-    while (todo != 0) {
-        const int32_t cur = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(todo));
-        const bool mine = id == cur;
-        const uint64_t same = __ballot(mine);
-        const bool all = same == ~0ull;
-        f32x16 d[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) d[nt] = all ? at(nt) : f32x16{};
-        for (int r = 0; r < l.R; r += 16) {
-            const bool live = r + rl < l.R;               // R may end halfway through a step
-            float hv[8] = {};
-            if (live && mine) {
-                const float4* hp = reinterpret_cast<const float4*>(l.h + (int64_t)m * l.R + r + rl);
-                const float4 h0 = hp[0], h1 = hp[1];
-                hv[0] = h0.x; hv[1] = h0.y; hv[2] = h0.z; hv[3] = h0.w;
-                hv[4] = h1.x; hv[5] = h1.y; hv[6] = h1.z; hv[7] = h1.w;
-            }
-            v4u hp[3];
-            hp[0] = take_bf16(hv);
-            hp[1] = take_bf16(hv);
-            hp[2] = take_bf16(hv);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int32_t n = min(n0 + nt * 32 + (lane & 31), a.N - 1);
-                v4u b[BQ] = {};
-                if (live) b[0] = *reinterpret_cast<const v4u*>(l.b + ((int64_t)cur * a.N + n) * l.R + r + rl);
-                if constexpr (DT == ROPE_DTYPE_F16) {
-                    float bv[8];
-                    widen8<DT>(b[0], bv);
-                    b[0] = take_bf16(bv);
-                    b[1] = take_bf16(bv);
-                }
-                lora_mfma<BQ, COLS>(d[nt], b, hp, parts);
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (all) {
-                at(nt) = d[nt];
-            } else {
-                // accumulator register e of lane i: column i%32, row 8*(e/4) + 4*(i/32) + e%4
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const bool own = COLS ? mine
-                                          : ((same >> (8 * (e >> 2) + 4 * (lane >> 5) + (e & 3))) & 1u) != 0;
-                    at(nt)[e] = own ? at(nt)[e] + d[nt][e] : at(nt)[e];
-                }
-            }
-        }
-        todo &= ~same;
+struct LoraH {
+    float4 q[2];
+    __device__ __forceinline__ void load(const LoraProjArgs& a, int32_t tok, int r, int lane)
+    {
+        const int rk = r + (lane >> 5) * 8 < a.l.R ? r + (lane >> 5) * 8 : r;
+        const float4* p = reinterpret_cast<const float4*>(a.l.h + (int64_t)max(tok, 0) * a.l.R + rk);
+        q[0] = p[0];
+        q[1] = p[1];
     }
+};
+
+// The operands of a step, for the MFMAs: zeros unless the lane's ranks exist
+// and the column has an adapter.
+template <int DT>
+__device__ __forceinline__ void lora_parts(const v4u& bl, bool live, v4u (&b)[DT == ROPE_DTYPE_F16 ? 2 : 1])
+{
+    b[0] = live ? bl : v4u{};
+    if constexpr (DT == ROPE_DTYPE_F16) {
+        float v[8];
+        widen8<DT>(b[0], v);
+        b[0] = take_bf16(v);
+        b[1] = take_bf16(v);
+    }
+}
+
+__device__ __forceinline__ void lora_parts(const LoraH& hl, bool live, v4u (&h)[3])
+{
+    float v[8] = {hl.q[0].x, hl.q[0].y, hl.q[0].z, hl.q[0].w, hl.q[1].x, hl.q[1].y, hl.q[1].z, hl.q[1].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = live ? v[e] : 0.0f;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) h[p] = take_bf16(v);
 }
 
 template <>
 struct ProjAdapters<LoraProjArgs> {
     static constexpr bool kAny = true;
 
-    // One step of 16 ranks of a square tile's wave whose 128 tokens share an
-    // adapter: b of its 4 x 32 output lanes and h of its 4 x 32 tokens.
-    struct Step {
-        v4u b[4];
-        float4 h[4][2];
-    };
-    // A square tile's wave: the adapter that all its tokens have (-1: none
-    // has one; kMixed: several) and the first step, fetched while the last K
-    // stage's MFMAs run, which hide its latency.
-    static constexpr int32_t kMixed = -2;
+    __device__ static __forceinline__ int32_t rows(const LoraProjArgs& a) { return *a.l.rows; }
+    __device__ static __forceinline__ int32_t row_token(const LoraProjArgs& a, int32_t row) { return a.l.order[row]; }
+
+    // A square tile's wave: its four columns' adapters and tokens, and the
+    // operands of their first step, fetched while the last K stage's MFMAs
+    // run, which hide their latency.
     struct Square {
-        int32_t id;
-        Step step;
+        int32_t id[4];
+        int32_t tok[4];
+        v4u b[4][4];         // [column][32 output lanes]
+        LoraH h[4];
     };
 
     template <int DT>
     __device__ static __forceinline__ void find_square(const LoraProjArgs& a, Square& q, int32_t m0, int lane)
     {
-        q.id = -1;
-        if (a.l.count == 0) return;
-        int32_t id[4];
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) id[mt] = lora_id(a.l, min(m0 + mt * 32 + (lane & 31), a.M - 1));
-        const int32_t first = __builtin_amdgcn_readfirstlane(id[0]);
-        const bool same = id[0] == first && id[1] == first && id[2] == first && id[3] == first;
-        q.id = __ballot(same) == ~0ull ? first : kMixed;
-    }
-
-    __device__ static __forceinline__ void load_step(const LoraProjArgs& a, Step& t, int32_t id, int32_t m0, int32_t n0,
-                                                     int r, int lane)
-    {
-        const LoraArgs& l = a.l;
-        // ranks past R (the upper half of a last half step) re-read the lower
-        // half; add_step clears h there, and b is finite or its own tokens'
-        const int rk = r + (lane >> 5) * 8 < l.R ? r + (lane >> 5) * 8 : r;
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            const int32_t n = min(n0 + nt * 32 + (lane & 31), a.N - 1);
-            t.b[nt] = *reinterpret_cast<const v4u*>(l.b + ((int64_t)id * a.N + n) * l.R + rk);
-        }
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const int32_t m = min(m0 + mt * 32 + (lane & 31), a.M - 1);
-            const float4* hp = reinterpret_cast<const float4*>(l.h + (int64_t)m * l.R + rk);
-            t.h[mt][0] = hp[0];
-            t.h[mt][1] = hp[1];
+            q.id[mt] = a.l.group_ids[(m0 >> 5) + mt];
+            q.tok[mt] = a.l.order[m0 + mt * 32 + (lane & 31)];
         }
+    }
+
+    __device__ static __forceinline__ void load_column(const LoraProjArgs& a, Square& q, int mt, int32_t n0, int r, int lane)
+    {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) q.b[mt][nt] = lora_load_b(a, q.id[mt], n0 + nt * 32 + (lane & 31), r, lane);
+        q.h[mt].load(a, q.tok[mt], r, lane);
     }
 
     template <int DT>
-    __device__ static __forceinline__ void fetch_square(const LoraProjArgs& a, Square& q, int32_t m0, int32_t n0,
-                                                        int lane)
+    __device__ static __forceinline__ void fetch_square(const LoraProjArgs& a, Square& q, int32_t n0, int lane)
     {
-        if (q.id >= 0) load_step(a, q.step, q.id, m0, n0, 0, lane);
-    }
-
-    // The products of one step. Its operands are rounded to bf16 parts first;
-    // their registers then take the step at `next` (if next < R), whose
-    // latency the MFMAs hide.
-    template <int DT>
-    __device__ static __forceinline__ void add_step(const LoraProjArgs& a, Square& s, f32x16 (&acc)[4][4], int32_t m0,
-                                                    int32_t n0, int r, int lane)
-    {
-        constexpr int BQ = DT == ROPE_DTYPE_F16 ? 2 : 1;
-        const bool live = r + (lane >> 5) * 8 < a.l.R;
-        v4u b[4][BQ], h[3][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            b[nt][0] = live ? s.step.b[nt] : v4u{};
-            if constexpr (DT == ROPE_DTYPE_F16) {
-                float bv[8];
-                widen8<DT>(b[nt][0], bv);
-                b[nt][0] = take_bf16(bv);
-                b[nt][1] = take_bf16(bv);
-            }
-        }
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            const float4 h0 = s.step.h[mt][0], h1 = s.step.h[mt][1];
-            float v[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = live ? v[e] : 0.0f;
-#pragma unroll
-            for (int p = 0; p < 3; ++p) h[p][mt] = take_bf16(v);
-        }
-        if (r + 16 < a.l.R) load_step(a, s.step, s.id, m0, n0, r + 16, lane);
-        // one part of h at a time over all 16 tiles: MFMAs on one
-        // accumulator are 16 apart
-        auto part = [&](const v4u (&hp)[4]) {
-#pragma unroll
-            for (int q = 0; q < BQ; ++q)
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int mt = 0; mt < 4; ++mt)
-                        acc[nt][mt] = proj_mfma<ROPE_DTYPE_BF16>(b[nt][q], hp[mt], acc[nt][mt]);
-        };
-        part(h[0]);
-        part(h[1]);
-        if (a.ydt == ROPE_DTYPE_F32) part(h[2]);
+        for (int mt = 0; mt < 4; ++mt) load_column(a, q, mt, n0, 0, lane);
     }
 
     // square tiles: the wave's 4 x 4 tiles, [nt][mt], tokens in columns
     template <int DT>
-    __device__ static __forceinline__ void add_square(const LoraProjArgs& a, Square& q, f32x16 (&acc)[4][4],
-                                                      int32_t m0, int32_t n0, int lane)
+    __device__ static __forceinline__ void add_square(const LoraProjArgs& a, Square& q, f32x16 (&acc)[4][4], int32_t n0,
+                                                      int lane)
     {
-        // one loop behind the other, each with no turns where it does not
-        // apply: branches that the 256 accumulators meet behind make the
-        // compiler spill them
-        const int fast = q.id >= 0 ? a.l.R : 0;
+        constexpr int BQ = DT == ROPE_DTYPE_F16 ? 2 : 1;
+        const bool three = a.ydt == ROPE_DTYPE_F32;
+        const bool any = q.id[0] >= 0 || q.id[1] >= 0 || q.id[2] >= 0 || q.id[3] >= 0;
+        const int R = any ? a.l.R : 0;
 #pragma unroll 1
-        for (int r = 0; r < fast; r += 16) add_step<DT>(a, q, acc, m0, n0, r, lane);
-        const bool mixed = q.id == kMixed;
+        for (int r = 0; r < R; r += 16) {
+            const bool in = r + (lane >> 5) * 8 < a.l.R;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-            lora_add_tiles<DT, 4, true>(a, m0 + mt * 32 + (lane & 31), n0, lane, mixed,
-                                        [&](int nt) -> f32x16& { return acc[nt][mt]; });
+            for (int mt = 0; mt < 4; ++mt) {
+                const bool live = in && q.id[mt] >= 0;
+                v4u h[3], b[4][BQ];
+                lora_parts(q.h[mt], live, h);
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) lora_parts<DT>(q.b[mt][nt], live, b[nt]);
+                // the column's next step (past the last: the first again,
+                // unused), while the MFMAs of this one and of the other
+                // columns run
+                load_column(a, q, mt, n0, r + 16 < a.l.R ? r + 16 : 0, lane);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    if (p == 2 && !three) break;
+#pragma unroll
+                    for (int k = 0; k < BQ; ++k)
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt)
+                            acc[nt][mt] = proj_mfma<ROPE_DTYPE_BF16>(b[nt][k], h[p], acc[nt][mt]);
+                }
+            }
+        }
     }
 
     // tiles of whole heads: [mt][nt], tokens in rows
@@ -408,14 +391,36 @@ struct ProjAdapters<LoraProjArgs> {
     __device__ static __forceinline__ void add_heads(const LoraProjArgs& a, f32x16 (&acc)[MT][NT], int32_t m0,
                                                      int32_t n0, int lane)
     {
-        // one tile at a time: cleared accumulators for all NT beside the
-        // wave's own would not fit its 168 registers
+        constexpr int BQ = DT == ROPE_DTYPE_F16 ? 2 : 1;
+        const bool three = a.ydt == ROPE_DTYPE_F32;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+            const int32_t id = a.l.group_ids[(m0 >> 5) + mt];
+            const int32_t tok = a.l.order[m0 + mt * 32 + (lane & 31)];
+            const int R = id >= 0 ? a.l.R : 0;
+#pragma unroll 1
+            for (int r = 0; r < R; r += 16) {
+                const bool live = r + (lane >> 5) * 8 < a.l.R;
+                LoraH hl;
+                hl.load(a, tok, r, lane);
+                v4u bl[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                lora_add_tiles<DT, 1, false>(a, m0 + mt * 32 + (lane & 31), n0 + nt * 32, lane, a.l.count > 0,
-                                             [&](int) -> f32x16& { return acc[mt][nt]; });
+                for (int nt = 0; nt < NT; ++nt) bl[nt] = lora_load_b(a, id, n0 + nt * 32 + (lane & 31), r, lane);
+                v4u h[3];
+                lora_parts(hl, live, h);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    v4u b[BQ];
+                    lora_parts<DT>(bl[nt], live, b);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        if (p == 2 && !three) break;
+#pragma unroll
+                        for (int k = 0; k < BQ; ++k) acc[mt][nt] = proj_mfma<ROPE_DTYPE_BF16>(h[p], b[k], acc[mt][nt]);
+                    }
+                }
+            }
+        }
     }
 };
 
@@ -512,7 +517,6 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
     for (int t = 0; t < MT; ++t) xr[t] = a.x + (int64_t)min(m0 + t * 16 + fr, a.M - 1) * a.K + quad * 8;
     f32x4 acc[2][MT] = {};
     const int32_t blocks = a.K / 64;
-#pragma unroll 2
     for (int32_t kb = wave; kb < blocks; kb += W) {
         v4u fw[2][2], fx[MT][2];
 #pragma unroll

@@ -388,7 +388,11 @@ bool proj_groups_in_column_tiles(int64_t Dh, int64_t N, int64_t start, int64_t L
 int64_t lora_workspace_bytes(int64_t M, int64_t rank)
 {
     int64_t n;
-    return mul_ok(M, rank, &n) && mul_ok(n, 4, &n) ? n : -1;
+    if (!mul_ok(M, rank, &n) || !mul_ok(n, 4, &n)) return -1;
+    if (M <= kLoraFewTokens) return n;
+    if (M > std::numeric_limits<int64_t>::max() / 256) return -1;
+    const int64_t rows = lora_row_bound(M, kLoraSortAdapters) + kLoraTileRows;
+    return n > std::numeric_limits<int64_t>::max() - 8 * rows ? -1 : n + 4 * (rows + rows / 32 + 2);
 }
 
 namespace {

@@ -141,7 +141,21 @@ struct LoraCheck {
     int64_t workspace_bytes = 0;
 };
 
-// Bytes of workspace of an M-token call: h, M x rank floats. -1 past 64 bits.
+// Tokens up to which the kernels for few tokens take a projection with
+// adapters.
+constexpr int64_t kLoraFewTokens = 64;
+// Adapters that the tiled kernels' sort takes.
+constexpr int64_t kLoraSortAdapters = 1023;
+// Rows of the largest tile.
+constexpr int64_t kLoraTileRows = 384;
+
+// Most rows of the sorted order: every adapter that has a token may leave 31
+// rows open.
+inline int64_t lora_row_bound(int64_t M, int64_t count) { return M + 31 * (count + 1 < M ? count + 1 : M); }
+
+// Bytes of workspace of an M-token call: h, M x rank floats, and for more than
+// kLoraFewTokens the rows' tokens, the adapter of every 32 rows and the number
+// of rows. -1 past 64 bits.
 int64_t lora_workspace_bytes(int64_t M, int64_t rank);
 
 // Lanes per head the fused kernel takes: 32, 64, 96, 128 or 192 (block

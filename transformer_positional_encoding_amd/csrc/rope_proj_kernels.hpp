@@ -168,14 +168,14 @@ __device__ __forceinline__ f32x16 proj_mfma(const v4u& a, const v4u& b, const f3
 // share operands then share one L2), and tile numbers walk groups of
 // group_m M-tiles across all N-tiles, M fastest, so that the blocks in
 // flight on an XCD share a few x tiles and a few w tiles.
-__device__ __forceinline__ void proj_tile(const ProjArgs& a, int32_t& mb, int32_t& nb)
+__device__ __forceinline__ void proj_tile(const ProjArgs& a, int32_t MB, int32_t xcd_chunk, int32_t& mb, int32_t& nb)
 {
     int32_t bid = (int32_t)blockIdx.x;
-    if (bid < 8 * a.xcd_chunk) bid = (bid & 7) * a.xcd_chunk + (bid >> 3);
+    if (bid < 8 * xcd_chunk) bid = (bid & 7) * xcd_chunk + (bid >> 3);
     const int32_t in_group = a.group_m * a.NB;
     const int32_t g = bid / in_group;
     const int32_t first = g * a.group_m;
-    const int32_t gsize = min(a.MB - first, a.group_m);
+    const int32_t gsize = min(MB - first, a.group_m);
     const int32_t r = bid - g * in_group;
     mb = first + r % gsize;
     nb = r / gsize;
@@ -213,6 +213,8 @@ struct ProjTab8 {
 // What the kernels' arguments say about low-rank adapters beside the shared
 // weight: none, unless a specialisation for other arguments adds their
 // products to the accumulators between the K loop and the epilogue.
+// With adapters the rows of the tiles are the tokens in another order, with
+// gaps: row_token is the token at a row, negative in a gap.
 template <class ARGS>
 struct ProjAdapters {
     static constexpr bool kAny = false;
@@ -228,7 +230,14 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
     __shared__ __attribute__((aligned(16))) uint16_t smem[T_::LDS / 2];
 
     int32_t mb, nb;
-    proj_tile(a, mb, nb);
+    if constexpr (ProjAdapters<ARGS>::kAny) {
+        // the tiles in use, which the device counted; the grid is their bound
+        const int32_t MB = (ProjAdapters<ARGS>::rows(a) + BM - 1) / BM;
+        if ((int32_t)blockIdx.x >= MB * a.NB) return;
+        proj_tile(a, MB, MB * a.NB / 8, mb, nb);
+    } else {
+        proj_tile(a, a.MB, a.xcd_chunk, mb, nb);
+    }
     const int32_t m0 = mb * BM;
     const int32_t n0 = nb * BN;
     const int t = threadIdx.x;
@@ -254,7 +263,14 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
         from_x[i] = li * 8 < BM;
         const int row = from_x[i] ? srow : srow - BM;
         const int kv = (lane & 7) ^ proj_swz(row & 31);
-        const int32_t g = from_x[i] ? min(m0 + row, a.M - 1) : min(n0 + row, a.N - 1);
+        int32_t g;
+        if constexpr (ProjAdapters<ARGS>::kAny) {
+            const int32_t tok = max(ProjAdapters<ARGS>::row_token(a, m0 + (from_x[i] ? row : 0)), 0);
+            const int32_t gw = min(n0 + row, a.N - 1);
+            g = from_x[i] ? tok : gw;
+        } else {
+            g = from_x[i] ? min(m0 + row, a.M - 1) : min(n0 + row, a.N - 1);
+        }
         goff[i] = ((uint32_t)g * (uint32_t)a.K + (uint32_t)(kv * 8)) * 2u;
     }
     const uint32_t smem_lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint16_t*)smem);
@@ -361,12 +377,20 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         int64_t m[T_::PR], o1[T_::PR], o2[T_::PR];
+        int32_t tok[T_::PR];
         ProjTab8<TT> pc[T_::PR][VP], ps[T_::PR][VP];
 #pragma unroll
         for (int p = 0; p < T_::PR; ++p) {
             const int lr = tr + p * T_::RPP;
             m[p] = m0 + (lr >> 5) * 64 + h * 32 + (lr & 31);
-            const int32_t mc = (int32_t)min<int64_t>(m[p], a.M - 1);
+            int32_t mc;
+            if constexpr (ProjAdapters<ARGS>::kAny) {
+                tok[p] = ProjAdapters<ARGS>::row_token(a, (int32_t)m[p]);
+                mc = max(tok[p], 0);
+            } else {
+                tok[p] = m[p] < a.M ? (int32_t)m[p] : -1;
+                mc = (int32_t)min<int64_t>(m[p], a.M - 1);
+            }
             const int32_t b = (int32_t)fast_div((uint32_t)mc, a.s_div), sp = mc - b * a.S;
             o1[p] = b * a.t1b + sp * a.t1s;
             o2[p] = b * a.t2b + sp * a.t2s;
@@ -384,12 +408,12 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
         __syncthreads();
 #pragma unroll
         for (int p = 0; p < T_::PR; ++p) {
-            if (m[p] >= a.M) continue;
+            if (tok[p] < 0) continue;
             const float* crow = Cs + (tr + p * T_::RPP) * LDC;
 #pragma unroll
             for (int i = 0; i < T_::VI; ++i) {
                 if (!live_v[i]) continue;
-                const int64_t yo = m[p] * a.N + n0 + c0[i];
+                const int64_t yo = (int64_t)tok[p] * a.N + n0 + c0[i];
                 if (rot[i] && !a.fast) {
                     // any other geometry: lane by lane from the row in LDS
                     // (partners there too), cos and sin read one by one, one
@@ -542,7 +566,8 @@ struct ProjSq {
 // XOR-swizzled by the token's low bits), else from global memory.
 template <int DT, int TT, bool PV>
 __device__ __forceinline__ void proj_sq_epilogue_vec(const ProjArgs& a, const f32x16 (&acc)[4][4], uint16_t* smem,
-                                                     int32_t m0, int32_t n0, int wm, int wn, int wave, int lane)
+                                                     const int32_t* toks, int32_t m0, int32_t n0, int wm, int wn,
+                                                     int wave, int lane)
 {
     constexpr int LDW = ProjSq::LDW;                    // staging row pitch in floats
     constexpr int TS = TT == ROPE_DTYPE_F32 ? 4 : 2;   // table element bytes
@@ -590,7 +615,7 @@ __device__ __forceinline__ void proj_sq_epilogue_vec(const ProjArgs& a, const f3
                 for (int k = 0; k < 8; ++k) f[k] = T.v[k];
             }
         } else {
-            const int32_t mc = min(m, a.M - 1);
+            const int32_t mc = toks != nullptr ? max(toks[tr], 0) : min(m, a.M - 1);
             const int32_t b = (int32_t)fast_div((uint32_t)mc, a.s_div), sp = mc - b * a.S;
             ProjTab8<TT> q;
             q.load(table ? a.r2 : a.r1,
@@ -656,8 +681,9 @@ __device__ __forceinline__ void proj_sq_epilogue_vec(const ProjArgs& a, const f3
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int32_t m = m0 + wm * 128 + q * 32 + lr0 + 8 * k;
-                if (m < a.M && liveg[G]) {
-                    const int64_t yo = (int64_t)m * a.N + colg[G];
+                const int32_t tok = toks != nullptr ? toks[m - m0] : m;
+                if ((toks != nullptr ? tok >= 0 : m < a.M) && liveg[G]) {
+                    const int64_t yo = (int64_t)tok * a.N + colg[G];
                     if (a.ydt == ROPE_DTYPE_F32) {
                         v4u* yp = reinterpret_cast<v4u*>(static_cast<float*>(a.y) + yo);
                         __builtin_nontemporal_store(v4u{__float_as_uint(val[k][0]), __float_as_uint(val[k][1]),
@@ -689,15 +715,28 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     using T_ = ProjSq;
     constexpr int BM = T_::BM, BN = T_::BN, LW = T_::LW, LDC = T_::LDC;
     __shared__ __attribute__((aligned(16))) uint16_t smem[T_::LDS / 2];
+    // with adapters: the tile's tokens, for the epilogue
+    __shared__ int32_t toks[ProjAdapters<ARGS>::kAny ? BM : 1];
 
     int32_t mb, nb;
-    proj_tile(a, mb, nb);
+    if constexpr (ProjAdapters<ARGS>::kAny) {
+        // the tiles in use, which the device counted; the grid is their bound
+        const int32_t MB = (ProjAdapters<ARGS>::rows(a) + BM - 1) / BM;
+        if ((int32_t)blockIdx.x >= MB * a.NB) return;
+        proj_tile(a, MB, MB * a.NB / 8, mb, nb);
+    } else {
+        proj_tile(a, a.MB, a.xcd_chunk, mb, nb);
+    }
     const int32_t m0 = mb * BM;
     const int32_t n0 = nb * BN;
     const int t = threadIdx.x;
     const int lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave & 1, wn = wave >> 1;
+    if constexpr (ProjAdapters<ARGS>::kAny) {
+        toks[t] = ProjAdapters<ARGS>::row_token(a, m0 + t);
+        __syncthreads();
+    }
 
     // ---------------------------------------------------------------- loads
     // A stage: rows 0..255 of x then rows 0..255 of w, 128 bytes each; waves
@@ -714,7 +753,16 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     for (int i = 0; i < LW; ++i) {
         const int row = (wave & 1) * 128 + 8 * i + (lane >> 3);
         const int kv = (lane & 7) ^ proj_swz(row & 31);
-        const int32_t g = wx ? min(m0 + row, a.M - 1) : min(n0 + row, a.N - 1);
+        int32_t g;
+        if constexpr (ProjAdapters<ARGS>::kAny) {
+            // looked up by every wave: a branch around each load would wait
+            // for them one by one
+            const int32_t tok = max(toks[row], 0);
+            const int32_t gw = min(n0 + row, a.N - 1);
+            g = wx ? tok : gw;
+        } else {
+            g = wx ? min(m0 + row, a.M - 1) : min(n0 + row, a.N - 1);
+        }
         goff[i] = ((uint32_t)g * (uint32_t)a.K + (uint32_t)(kv * 8)) * 2u;
     }
     const uint32_t smem_lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint16_t*)smem);
@@ -784,7 +832,11 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
         };
         const uint32_t last = row(a.M - 1);            // rows past M re-read the last token's row
         int32_t m = m0 + tr0;
-        if (a.S >= tstep) {
+        if constexpr (ProjAdapters<ARGS>::kAny) {
+            // tokens in any order: no stepping
+#pragma unroll
+            for (int i = 0; i < LW; ++i) toff[i] = row(max(toks[min(m - m0 + i * tstep, BM - 1)], 0)) * TS + cb;
+        } else if (a.S >= tstep) {
             const int32_t mc = min(m, a.M - 1);
             const uint32_t b = fast_div((uint32_t)mc, a.s_div);
             uint32_t sp = (uint32_t)mc - b * (uint32_t)a.S;
@@ -866,15 +918,16 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
         stage(S0{}, More{}, Later{}, kt + 1);
     }
     if constexpr (ProjAdapters<ARGS>::kAny)
-        ProjAdapters<ARGS>::template fetch_square<DT>(a, adapters, m0 + wm * 128, n0 + wn * 128, lane);
+        ProjAdapters<ARGS>::template fetch_square<DT>(a, adapters, n0 + wn * 128, lane);
     stage(S1{}, Last{}, Later{}, kt);
     proj_wait_vm<0>();                                 // this wave's table rows are in LDS
     __syncthreads();                                   // every wave is done with the ring
     if constexpr (ProjAdapters<ARGS>::kAny)
-        ProjAdapters<ARGS>::template add_square<DT>(a, adapters, acc, m0 + wm * 128, n0 + wn * 128, lane);
+        ProjAdapters<ARGS>::template add_square<DT>(a, adapters, acc, n0 + wn * 128, lane);
 
     if constexpr (EPI >= 0) {
-        proj_sq_epilogue_vec<DT, TT, EPI == 1>(a, acc, smem, m0, n0, wm, wn, wave, lane);
+        proj_sq_epilogue_vec<DT, TT, EPI == 1>(a, acc, smem, ProjAdapters<ARGS>::kAny ? toks : nullptr, m0, n0, wm, wn,
+                                               wave, lane);
         return;
     }
 
@@ -901,12 +954,20 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         int64_t m[T_::PR], o1[T_::PR], o2[T_::PR];
+        int32_t tok[T_::PR];
         ProjTab8<TT> pc[T_::PR][VP], ps[T_::PR][VP];
 #pragma unroll
         for (int p = 0; p < T_::PR; ++p) {
             const int lr = tr + p * T_::RPP;
             m[p] = m0 + (lr >> 6) * 128 + h * 64 + (lr & 63);
-            const int32_t mc = (int32_t)min<int64_t>(m[p], a.M - 1);
+            int32_t mc;
+            if constexpr (ProjAdapters<ARGS>::kAny) {
+                tok[p] = ProjAdapters<ARGS>::row_token(a, (int32_t)m[p]);
+                mc = max(tok[p], 0);
+            } else {
+                tok[p] = m[p] < a.M ? (int32_t)m[p] : -1;
+                mc = (int32_t)min<int64_t>(m[p], a.M - 1);
+            }
             const int32_t b = (int32_t)fast_div((uint32_t)mc, a.s_div), sp = mc - b * a.S;
             o1[p] = b * a.t1b + sp * a.t1s;
             o2[p] = b * a.t2b + sp * a.t2s;
@@ -936,12 +997,12 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
         __syncthreads();
 #pragma unroll
         for (int p = 0; p < T_::PR; ++p) {
-            if (m[p] >= a.M) continue;
+            if (tok[p] < 0) continue;
             const float* crow = Cs + (tr + p * T_::RPP) * LDC;
 #pragma unroll
             for (int i = 0; i < T_::VI; ++i) {
                 if (!live_v[i]) continue;
-                const int64_t yo = m[p] * a.N + n0 + c0[i];
+                const int64_t yo = (int64_t)tok[p] * a.N + n0 + c0[i];
                 if (rot[i] && !a.fast) {
 #pragma unroll 1
                     for (int e = 0; e < 8; ++e) {
