@@ -135,7 +135,7 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t s)
             a.l.group_ids = group_ids;
             a.l.rows = rows;
             hipLaunchKernelGGL((rope_lora_shrink_tile_kernel<DT>),
-                               dim3((uint32_t)((bound + 31) / 32), (uint32_t)(a.l.R + 31) / 32), dim3(256), 0, s, a.l, a.x,
+                               dim3((uint32_t)((bound + 31) / 32), (uint32_t)(a.l.R + 31) / 32), dim3(64 * kShrinkTileWaves), 0, s, a.l, a.x,
                                a.K);
             err = hipGetLastError();
             if (err != hipSuccess) return err;

@@ -69,6 +69,7 @@ __device__ __forceinline__ void widen8(const v4u& q, float (&f)[8])
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortBins = kLoraSortAdapters + 1;   // and one for none
+constexpr int kSortKept = 16;                      // tokens a lane keeps in registers: 16384 tokens in all
 
 __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int32_t* ids, int32_t count, int32_t M,
                                                                      int32_t* order, int32_t* group_ids, int32_t* rows)
@@ -85,21 +86,50 @@ __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int3
     __syncthreads();
     const int64_t seg = (((int64_t)M + kSortThreads - 1) / kSortThreads) * 64;    // tokens of a wave, whole 64s
     const int64_t begin = wave * seg, end = min((int64_t)M, begin + seg);
+    // (a token past the last repeats it: a branch around each load would wait
+    // for them one by one)
     const auto key = [&](int64_t m) {
-        const int32_t i = ids[m];
+        const int32_t i = ids[min(m, (int64_t)M - 1)];
         return i >= 0 && i < count ? i : count;
     };
-    for (int64_t m = begin + lane; m < end; m += 64) atomicAdd(&at[wave][key(m)], 1);
+    // the wave's first tokens stay in registers: their loads go out together
+    // and serve both walks
+    int32_t kept[kSortKept];
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i) kept[i] = key(begin + i * 64 + lane);
+    // the lanes of 64 tokens that hold this lane's adapter (the whole wave
+    // calls it); adding a group's size once spares the LDS 64 additions to one
+    // place
+    const auto alike = [&](bool live, int32_t k) {
+        uint64_t same = __ballot(live);
+        for (int i = 0; i < bits; ++i) {
+            const uint64_t set = __ballot((k >> i) & 1);
+            same &= ((k >> i) & 1) ? set : ~set;
+        }
+        return same;
+    };
+    const auto add = [&](int64_t m, int32_t k) {
+        const uint64_t same = alike(m < end, k);
+        if (m < end && (same & ((1ull << lane) - 1)) == 0) at[wave][k] += __popcll(same);
+    };
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i)
+        if (begin + i * 64 < end) add(begin + i * 64 + lane, kept[i]);
+    for (int64_t m64 = begin + kSortKept * 64; m64 < end; m64 += 64)
+        add(m64 + lane, key(m64 + lane));
     __syncthreads();
     // exclusive sums: over the waves for each bin, then of the bins' padded
     // sizes over the bins
     int32_t total = 0;
-    if (t < bins)
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int32_t n = at[w][t];
-            at[w][t] = total;
-            total += n;
-        }
+    int32_t mine[kSortWaves];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) mine[w] = t < bins ? at[w][t] : 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+        const int32_t n = mine[w];
+        mine[w] = total;
+        total += n;
+    }
     const int32_t padded = (total + 31) & ~31;
     int32_t sum = padded;
     for (int d = 1; d < 64; d <<= 1) {
@@ -114,7 +144,8 @@ __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int3
         all += sums[w];
     }
     if (t < bins) {
-        for (int w = 0; w < kSortWaves; ++w) at[w][t] += before;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) at[w][t] = before + mine[w];
         for (int32_t i = total; i < padded; ++i) order[before + i] = -1;
     }
     // gaps to the end of the last tile of either kind
@@ -122,16 +153,9 @@ __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int3
     if (t < kLoraTileRows / 32) group_ids[all / 32 + t] = -1;
     if (t == 0) *rows = all;
     __syncthreads();
-    for (int64_t m64 = begin; m64 < end; m64 += 64) {                    // the same turns for the whole wave
-        const int64_t m = m64 + lane;
-        const bool live = m < end;
-        const int32_t k = live ? key(m) : count;
-        uint64_t same = __ballot(live);
-        for (int i = 0; i < bits; ++i) {
-            const uint64_t set = __ballot((k >> i) & 1);
-            same &= ((k >> i) & 1) ? set : ~set;
-        }
-        if (live) {
+    const auto place = [&](int64_t m, int32_t k) {                       // by the whole wave
+        const uint64_t same = alike(m < end, k);
+        if (m < end) {
             const int32_t to = at[wave][k] + __popcll(same & ((1ull << lane) - 1));
             order[to] = (int32_t)m;
             if ((to & 31) == 0) group_ids[to / 32] = k == count ? -1 : k;
@@ -139,7 +163,12 @@ __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int3
             // every read of it, a wave's LDS accesses being in order
             if ((same >> lane) == 1) at[wave][k] = to + 1;
         }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i)
+        if (begin + i * 64 < end) place(begin + i * 64 + lane, kept[i]);
+    for (int64_t m64 = begin + kSortKept * 64; m64 < end; m64 += 64)
+        place(m64 + lane, key(m64 + lane));
 }
 
 // h[m,r] of the token's adapter by the whole wave: 16 bytes of x and of a per
@@ -183,17 +212,22 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) rope_lora_shrink_kernel(Lor
 
 // ---------------------------------------------------------------------------
 // h by MFMA, for prompts: a block takes 32 sorted rows, whose tokens have one
-// adapter, and 32 ranks, its waves a quarter of K each (whole 64-k blocks, one
-// 128-byte line of each row), with 32x32x16 MFMAs whose operands come straight
-// from memory; the four partial tiles meet in LDS in a fixed order. The k of a
+// adapter, and 32 ranks, its 8 waves an eighth of K each (whole 64-k blocks,
+// one 128-byte line of each row), with 32x32x16 MFMAs whose operands come
+// straight from memory; the partial tiles meet in LDS in a fixed order. Bound
+// by the latency of a wave's few rounds of loads: a prompt of 8190 tokens is
+// one block for each compute unit. The k of a
 // 64-k block may go to any MFMA slot as long as a and x agree: lane l takes 16
 // bytes (8 k) at (2j + l/32) * 16 of its row's line in step j, so a step's 64
 // loads fill half lines that the next steps complete.
 // ---------------------------------------------------------------------------
+constexpr int kShrinkTileWaves = 8;
+
 template <int DT>
-__global__ void __launch_bounds__(256) rope_lora_shrink_tile_kernel(LoraArgs l, const uint16_t* x, int32_t K)
+__global__ void __launch_bounds__(64 * kShrinkTileWaves)
+    rope_lora_shrink_tile_kernel(LoraArgs l, const uint16_t* x, int32_t K)
 {
-    __shared__ float part[4][32][33];
+    __shared__ float part[kShrinkTileWaves][32][33];
     const int32_t row0 = (int32_t)blockIdx.x * 32;
     if (row0 >= *l.rows) return;
     const int32_t id = l.group_ids[blockIdx.x];
@@ -206,7 +240,7 @@ __global__ void __launch_bounds__(256) rope_lora_shrink_tile_kernel(LoraArgs l, 
     const uint16_t* xr = x + (int64_t)max(tok, 0) * K + hw * 8;
     const uint16_t* ar = l.a + ((int64_t)id * l.R + min(r0 + fr, l.R - 1)) * K + hw * 8;
     f32x16 acc = {};
-    for (int32_t kb = wave; kb < blocks; kb += 4) {
+    for (int32_t kb = wave; kb < blocks; kb += kShrinkTileWaves) {
         v4u fx[4], fa[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -221,10 +255,12 @@ __global__ void __launch_bounds__(256) rope_lora_shrink_tile_kernel(LoraArgs l, 
     for (int e = 0; e < 16; ++e) part[wave][fr][8 * (e >> 2) + 4 * hw + (e & 3)] = acc[e];
     __syncthreads();
     const float s = l.scales != nullptr ? l.scales[id] : 1.0f;
-    for (int i = threadIdx.x; i < 32 * 32; i += 256) {
+    for (int i = threadIdx.x; i < 32 * 32; i += 64 * kShrinkTileWaves) {
         const int t = i >> 5, r = i & 31;
         const int32_t to = __shfl(tok, t);
-        const float sum = (part[0][t][r] + part[1][t][r]) + (part[2][t][r] + part[3][t][r]);
+        float sum = part[0][t][r];
+#pragma unroll
+        for (int w = 1; w < kShrinkTileWaves; ++w) sum += part[w][t][r];
         if (to >= 0 && r0 + r < l.R) l.h[(int64_t)to * l.R + r0 + r] = sum * s;
     }
 }
@@ -515,6 +551,20 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
     for (int f = 0; f < 2; ++f) wr[f] = a.w + (n0 + lane0[f] + fr) * a.K + quad * 8;
 #pragma unroll
     for (int t = 0; t < MT; ++t) xr[t] = a.x + (int64_t)min(m0 + t * 16 + fr, a.M - 1) * a.K + quad * 8;
+    // The token and output lanes that this thread finishes. Its adapter's b is
+    // touched now, a word of each 128-byte line, so that the adapter's part
+    // finds it in L2 instead of waiting for HBM.
+    int32_t fin_id = -1;
+    uint32_t touched = 0;
+    if (a.l.count > 0 && threadIdx.x < 64 * MT) {
+        const int32_t m = m0 + (int)(threadIdx.x >> 6) * 16 + (lane & 15);
+        if (m < a.M) fin_id = lora_id(a.l, m);
+        if (fin_id >= 0)
+            for (int o = 0; o < 4 * a.l.R; o += 64)          // 16-bit elements of 4 lanes' rows
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    touched |= a.l.b[((int64_t)fin_id * a.N + n0 + lane0[f] + quad * 4) * a.l.R + o];
+    }
     f32x4 acc[2][MT] = {};
     const int32_t blocks = a.K / 64;
     for (int32_t kb = wave; kb < blocks; kb += W) {
@@ -534,16 +584,18 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
 #pragma unroll
                 for (int t = 0; t < MT; ++t) acc[f][t] = mfma16<DT>(fw[f][s], fx[t][s], acc[f][t]);
     }
+    asm volatile("" ::"v"(touched));
     // register e of lane i: output lane 4*(i/16) + e of the fragment, token i%16
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int t = 0; t < MT; ++t) part[wave][f][t][lane] = acc[f][t];
     __syncthreads();
-    for (int i = threadIdx.x; i < 64 * MT; i += 64 * W) {
-        const int t = i >> 6;
+    static_assert(W >= MT, "a thread for each token and four lanes");
+    if (threadIdx.x < 64 * MT) {
+        const int i = (int)threadIdx.x, t = i >> 6;
         const int32_t m = m0 + t * 16 + (i & 15);
-        if (m >= a.M) continue;
+        if (m >= a.M) return;
         float v[2][4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -554,13 +606,34 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
             for (int e = 0; e < 4; ++e) v[f][e] = sum[e];
         }
         const int q4 = ((i & 63) >> 4) * 4;        // first of the thread's 4 lanes in each fragment
-        const int32_t id = a.l.count > 0 ? lora_id(a.l, m) : -1;
-        if (id >= 0) {
+        if (fin_id >= 0) {
             const float* h = a.l.h + (int64_t)m * a.l.R;
+            const uint16_t* br[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) br[f] = a.l.b + ((int64_t)fin_id * a.N + n0 + lane0[f] + q4) * a.l.R;
+            float sum[2][4] = {};
+            for (int r = 0; r < a.l.R; r += 8) {
+                v4u bq[2][4];
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bq[f][e] = *reinterpret_cast<const v4u*>(br[f] + e * a.l.R + r);
+                const float4 h0 = *reinterpret_cast<const float4*>(h + r), h1 = *reinterpret_cast<const float4*>(h + r + 4);
+                const float hv[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float fb[8];
+                        widen8<DT>(bq[f][e], fb);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) sum[f][e] = __builtin_fmaf(hv[k], fb[k], sum[f][e]);
+                    }
+            }
 #pragma unroll
             for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[f][e] += lora_dot<DT>(a.l, h, id, n0 + lane0[f] + q4 + e, a.N);
+                for (int e = 0; e < 4; ++e) v[f][e] += sum[f][e];
         }
         if (a.L > 0) {
             const int32_t b = (int32_t)fast_div((uint32_t)m, a.s_div), s = m - b * a.S;

@@ -913,12 +913,25 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     // then pairs, then the last stage (KT even)
     stage(S0{}, More{}, First{}, 0);
     int32_t kt = 1;
-    for (; kt + 2 < KT; kt += 2) {
-        stage(S1{}, More{}, Later{}, kt);
-        stage(S0{}, More{}, Later{}, kt + 1);
-    }
-    if constexpr (ProjAdapters<ARGS>::kAny)
+    if constexpr (ProjAdapters<ARGS>::kAny) {
+        // the adapters' operands are fetched three stages before the end:
+        // under load they take longer than one
+        for (; kt + 4 < KT; kt += 2) {
+            stage(S1{}, More{}, Later{}, kt);
+            stage(S0{}, More{}, Later{}, kt + 1);
+        }
         ProjAdapters<ARGS>::template fetch_square<DT>(a, adapters, n0 + wn * 128, lane);
+        if (kt + 2 < KT) {
+            stage(S1{}, More{}, Later{}, kt);
+            stage(S0{}, More{}, Later{}, kt + 1);
+            kt += 2;
+        }
+    } else {
+        for (; kt + 2 < KT; kt += 2) {
+            stage(S1{}, More{}, Later{}, kt);
+            stage(S0{}, More{}, Later{}, kt + 1);
+        }
+    }
     stage(S1{}, Last{}, Later{}, kt);
     proj_wait_vm<0>();                                 // this wave's table rows are in LDS
     __syncthreads();                                   // every wave is done with the ring
