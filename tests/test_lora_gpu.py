@@ -224,3 +224,32 @@ def test_two_streams_at_once():
         raw = run(cs[0], cos, sin, 8, "rotate_half", (0, 128), "bf16", stream=streams[0].cuda_stream)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(raw, want[0])
+
+
+def rows_of(c, cos, sin, at):
+    """The call's tokens `at` as a call of their own."""
+    return dict(c, x=c["x"][:, at], ids=c["ids"][at]), cos[:, at], sin[:, at]
+
+
+@pytest.mark.parametrize("M, sl", [(65, (0, 64)), (700, (0, 64)), (700, (5, 45))])
+def test_more_adapters_than_a_sort_takes(M, sl):
+    """1500 adapters: tokens stay in their order, on the kernels for few
+    tokens and for any slice."""
+    c = make(M, 128, 3, 64, 8, 1500, "bf16", seed=M, ids="mixed")
+    cos, sin = tables(M, sl[1] - sl[0], "rotate_half", "f32", 3)
+    check(run(c, cos, sin, 3, "rotate_half", sl, "bf16"), c, cos, sin, 3, "rotate_half", sl, "bf16", "1500 adapters")
+
+
+@pytest.mark.parametrize("A", [3, 1500])
+def test_more_tokens_than_blocks_of_a_grid(A):
+    """2^24 + 77 tokens: past 2^32 threads of a block of 256 each, and past
+    65535 blocks of 64 tokens."""
+    M = 2 ** 24 + 77
+    c = make(M, 64, 1, 32, 8, A, "bf16", seed=1, ids="mixed")
+    cos, sin = tables(M, 4, "interleave", "bf16", 3)
+    got = run(c, cos, sin, 1, "interleave", (28, 32), "bf16")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    at = torch.cat([torch.arange(40, device="cuda"), torch.randint(0, M, (3000,), generator=g, device="cuda"),
+                    torch.arange(M - 120, M, device="cuda")])
+    c, cos, sin = rows_of(c, cos, sin, at)
+    check(got[:, at], c, cos, sin, 1, "interleave", (28, 32), "bf16", "rows of a long call")

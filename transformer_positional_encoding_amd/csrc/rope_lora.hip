@@ -14,6 +14,10 @@
 namespace rope {
 namespace {
 
+// A grid's second dimension counts the few-token kernel's 64-token blocks;
+// calls of more tokens that no tiled kernel takes go to the general one.
+constexpr int64_t kFewTokensMax = 64 * 65535ll;
+
 // A call's checked plan and what is launched for it.
 struct LoraLaunch {
     ProjLaunch P;
@@ -71,7 +75,7 @@ rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const v
         if (MB * a.NB > (int64_t)(kMaxGridItems / (uint64_t)L->P.threads)) L->tiles = false;
         else L->P.grid = (uint32_t)(MB * a.NB);
     }
-    L->few = !L->tiles && units;
+    L->few = !L->tiles && units && a.M <= kFewTokensMax;
     return ROPE_OK;
 }
 
@@ -134,15 +138,17 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t s)
             a.l.order = order;
             a.l.group_ids = group_ids;
             a.l.rows = rows;
+            // (x has fewer than 2^31 elements: 2^25 tokens at most, 2^20 groups)
             hipLaunchKernelGGL((rope_lora_shrink_tile_kernel<DT>),
-                               dim3((uint32_t)((bound + 31) / 32), (uint32_t)(a.l.R + 31) / 32), dim3(64 * kShrinkTileWaves), 0, s, a.l, a.x,
-                               a.K);
+                               dim3((uint32_t)((bound + 31) / 32), (uint32_t)(a.l.R + 31) / 32),
+                               dim3(64 * kShrinkTileWaves), 0, s, a.l, a.x, a.K);
             err = hipGetLastError();
             if (err != hipSuccess) return err;
         } else {
             hipLaunchKernelGGL((rope_lora_shrink_kernel<DT>),
-                               dim3((uint32_t)a.M, (uint32_t)(a.l.R + kShrinkWaves - 1) / kShrinkWaves),
-                               dim3(64 * kShrinkWaves), 0, s, a.l, a.x, a.K);
+                               dim3((uint32_t)std::min<uint64_t>((uint64_t)a.M, kMaxGridItems / (64 * kShrinkWaves)),
+                                    (uint32_t)(a.l.R + kShrinkWaves - 1) / kShrinkWaves),
+                               dim3(64 * kShrinkWaves), 0, s, a.l, a.x, a.M, a.K);
             const hipError_t err = hipGetLastError();
             if (err != hipSuccess) return err;
         }

@@ -200,14 +200,16 @@ __device__ __forceinline__ void lora_dot_k(const LoraArgs& l, const uint16_t* x,
 constexpr int kShrinkWaves = 4;
 
 template <int DT>
-__global__ void __launch_bounds__(64 * kShrinkWaves) rope_lora_shrink_kernel(LoraArgs l, const uint16_t* x, int32_t K)
+__global__ void __launch_bounds__(64 * kShrinkWaves) rope_lora_shrink_kernel(LoraArgs l, const uint16_t* x, int32_t M,
+                                                                            int32_t K)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = blockIdx.y * kShrinkWaves + wave;
     if (r >= l.R) return;
-    const int32_t m = (int32_t)blockIdx.x;
-    const int32_t id = lora_id(l, m);
-    if (id >= 0) lora_dot_k<DT>(l, x, m, id, r, K, lane);
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        const int32_t id = lora_id(l, (int32_t)m);
+        if (id >= 0) lora_dot_k<DT>(l, x, (int32_t)m, id, r, K, lane);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -216,10 +218,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) rope_lora_shrink_kernel(Lor
 // one 128-byte line of each row), with 32x32x16 MFMAs whose operands come
 // straight from memory; the partial tiles meet in LDS in a fixed order. Bound
 // by the latency of a wave's few rounds of loads: a prompt of 8190 tokens is
-// one block for each compute unit. The k of a
-// 64-k block may go to any MFMA slot as long as a and x agree: lane l takes 16
-// bytes (8 k) at (2j + l/32) * 16 of its row's line in step j, so a step's 64
-// loads fill half lines that the next steps complete.
+// one block for each compute unit. The k of a 64-k block may go to any MFMA
+// slot as long as a and x agree: lane l takes 16 bytes (8 k) at
+// (2j + l/32) * 16 of its row's line in step j, so a step's 64 loads fill half
+// lines that the next steps complete.
 // ---------------------------------------------------------------------------
 constexpr int kShrinkTileWaves = 8;
 
