@@ -495,14 +495,22 @@ __device__ __forceinline__ float lora_dot(const LoraArgs& l, const float* h, int
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: bound by reading w once. A block takes a unit of 32 output lanes
-// (two 16-lane fragments) and up to 64 tokens; its W waves take 64-k blocks of
-// K in turn (one 128-byte line of each row of w), with 16x16x32 MFMAs whose
-// operands come straight from memory: w is read by one wave only, and x, which
-// every block reads, comes from L2. The waves' partial tiles meet in LDS in a
-// fixed order; then a thread holds one token and 4 lanes of both fragments,
-// adds the adapter's part by dot products (each token has its own b: MFMA
-// tiles would be one token wide) and rotates.
+// Few tokens: bound by reading w once and, from 32 tokens on, by x, which every
+// block reads from L2. A block takes a unit of 32 output lanes (two 16-lane
+// fragments) and up to 64 tokens; its W waves take 64-k blocks of K in turn
+// (one 128-byte line of each row of w), with 16x16x32 MFMAs whose operands
+// come straight from memory: w is read by one wave only. The adapters' part
+// are dot products (each token has its own b: MFMA tiles would be one token
+// wide), dealt to all waves. The waves' tiles and the adapters' part meet in
+// LDS in a fixed order; then a thread holds one token and 4 lanes of both
+// fragments, and rotates.
+// Measured on MI355X (K 1536, 24576 output lanes, rank 16, 64 adapters; with
+// the launch of h; us): 1, 16, 32, 64 tokens of an adapter each 24, 31, 38, 54,
+// without adapters 20, 23, 28, 38 (w alone: 75 MB, 15 us). The adapters' part
+// behind the products, its lines touched before: 25, 31, 41, 60; by the threads
+// that store: 26, 33, 37, 53, but in twice the registers. Two units a block
+// halve x and read 36 where one reads 40 (64 tokens, no adapters), but 26 for 20
+// (1 token) and 65 for 53 (64 adapters: registers).
 // Where partners lie whole fragments apart, a unit is a fragment of a group's
 // first half and the matching one of its second, so that partners meet in one
 // thread; otherwise fragments go in order.
@@ -536,7 +544,7 @@ __device__ __forceinline__ void few_unit(const FewArgs& a, int32_t u, int32_t (&
 template <int DT, int MT, int W>
 __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int tdt)
 {
-    __shared__ f32x4 part[W][2][MT][64];
+    __shared__ f32x4 part[W + 1][2][MT][64];     // the waves' tiles, and the adapters' part
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, quad = lane >> 4;
@@ -553,19 +561,60 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
     for (int f = 0; f < 2; ++f) wr[f] = a.w + (n0 + lane0[f] + fr) * a.K + quad * 8;
 #pragma unroll
     for (int t = 0; t < MT; ++t) xr[t] = a.x + (int64_t)min(m0 + t * 16 + fr, a.M - 1) * a.K + quad * 8;
-    // The token and output lanes that this thread finishes. Its adapter's b is
-    // touched now, a word of each 128-byte line, so that the adapter's part
-    // finds it in L2 instead of waiting for HBM.
-    int32_t fin_id = -1;
-    uint32_t touched = 0;
-    if (a.l.count > 0 && threadIdx.x < 64 * MT) {
-        const int32_t m = m0 + (int)(threadIdx.x >> 6) * 16 + (lane & 15);
-        if (m < a.M) fin_id = lora_id(a.l, m);
-        if (fin_id >= 0)
-            for (int o = 0; o < 4 * a.l.R; o += 64)          // 16-bit elements of 4 lanes' rows
+    // The adapters' part first, so that its loads from all over memory go out
+    // at once in all blocks, and the products follow without a wait for them:
+    // output lane 4*(i/16) + e of a fragment and token i%16 to lane i, the
+    // fragments, e and 16-token tiles dealt to the waves.
+    if (a.l.count > 0) {
+        constexpr int P = 8 * MT / W;            // of these to a wave
+        static_assert(W % MT == 0 && 8 * MT % W == 0, "a wave has one tile of tokens");
+        const int t = wave % MT;
+        const int32_t m = m0 + t * 16 + fr;
+        const int32_t id = m < a.M ? lora_id(a.l, m) : -1;
+        float sum[P] = {};
+        if (id >= 0) {
+            const float* h = a.l.h + (int64_t)m * a.l.R;
+            const uint16_t* br[P];
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    touched |= a.l.b[((int64_t)fin_id * a.N + n0 + lane0[f] + quad * 4) * a.l.R + o];
+            for (int i = 0; i < P; ++i) {
+                const int fe = wave / MT + W / MT * i;
+                br[i] = a.l.b + ((int64_t)id * a.N + n0 + lane0[fe / 4] + quad * 4 + fe % 4) * a.l.R;
+            }
+            for (int r = 0; r < a.l.R; r += 16) {
+                const int r8 = r + 8 < a.l.R ? r + 8 : r;      // (of 24 ranks, the last 8 alone)
+                v4u bq[P][2];
+                float hv[16];
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    bq[i][0] = *reinterpret_cast<const v4u*>(br[i] + r);
+                    bq[i][1] = *reinterpret_cast<const v4u*>(br[i] + r8);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 q = *reinterpret_cast<const float4*>(h + (k < 2 ? r : r8) + 4 * (k & 1));
+                    hv[4 * k] = q.x;
+                    hv[4 * k + 1] = q.y;
+                    hv[4 * k + 2] = q.z;
+                    hv[4 * k + 3] = q.w;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c == 1 && r8 == r) break;
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        float fb[8];
+                        widen8<DT>(bq[i][c], fb);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) sum[i] = __builtin_fmaf(hv[8 * c + k], fb[k], sum[i]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int fe = wave / MT + W / MT * i;
+            reinterpret_cast<float*>(&part[W][fe / 4][t][lane])[fe % 4] = sum[i];
+        }
     }
     f32x4 acc[2][MT] = {};
     const int32_t blocks = a.K / 64;
@@ -586,7 +635,6 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
 #pragma unroll
                 for (int t = 0; t < MT; ++t) acc[f][t] = mfma16<DT>(fw[f][s], fx[t][s], acc[f][t]);
     }
-    asm volatile("" ::"v"(touched));
     // register e of lane i: output lane 4*(i/16) + e of the fragment, token i%16
 #pragma unroll
     for (int f = 0; f < 2; ++f)
@@ -604,39 +652,11 @@ __global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int td
             f32x4 sum = part[0][f][t][i & 63];
 #pragma unroll
             for (int w = 1; w < W; ++w) sum += part[w][f][t][i & 63];
+            if (a.l.count > 0) sum += part[W][f][t][i & 63];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[f][e] = sum[e];
         }
         const int q4 = ((i & 63) >> 4) * 4;        // first of the thread's 4 lanes in each fragment
-        if (fin_id >= 0) {
-            const float* h = a.l.h + (int64_t)m * a.l.R;
-            const uint16_t* br[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) br[f] = a.l.b + ((int64_t)fin_id * a.N + n0 + lane0[f] + q4) * a.l.R;
-            float sum[2][4] = {};
-            for (int r = 0; r < a.l.R; r += 8) {
-                v4u bq[2][4];
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) bq[f][e] = *reinterpret_cast<const v4u*>(br[f] + e * a.l.R + r);
-                const float4 h0 = *reinterpret_cast<const float4*>(h + r), h1 = *reinterpret_cast<const float4*>(h + r + 4);
-                const float hv[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float fb[8];
-                        widen8<DT>(bq[f][e], fb);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) sum[f][e] = __builtin_fmaf(hv[k], fb[k], sum[f][e]);
-                    }
-            }
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[f][e] += sum[f][e];
-        }
         if (a.L > 0) {
             const int32_t b = (int32_t)fast_div((uint32_t)m, a.s_div), s = m - b * a.S;
             const int64_t o1 = b * a.t1b + s * a.t1s + hd * a.t1n, o2 = b * a.t2b + s * a.t2s + hd * a.t2n;
