@@ -36,7 +36,7 @@ Turn turn_of(const Plan& p)
     t.sb = p.pos_sb;
     t.ss = p.pos_ss;
     t.ax.sa = p.pos_sa;
-    t.ax.last = p.naxes > 0 ? (uint32_t)(p.naxes - 1) : 0;
+    t.ax.nwords = p.naxes > 1 ? (uint32_t)((p.L / 2 + 15) / 16) : 0;
     std::copy(std::begin(p.axis_words), std::end(p.axis_words), t.ax.words);
     t.tdt = p.tdtype;
     t.start = (uint32_t)p.start;

@@ -52,7 +52,7 @@ struct Turn {
 // cos and sin of pair i of token (b, s), rounded to the table type.
 __device__ __forceinline__ float2 turn_cos_sin(const Turn& t, uint32_t b, uint32_t s, uint32_t i)
 {
-    const int64_t p = axis_position(t.ax, t.pos + b * t.sb + s * t.ss, i);
+    const int64_t p = t.pos[b * t.sb + s * t.ss + axis_offset(t.ax, i)];
     const double f = t.inv_freq[i];
     switch (t.tdt) {
     case ROPE_DTYPE_F32: return pos_cos_sin<ROPE_DTYPE_F32>(p, f);

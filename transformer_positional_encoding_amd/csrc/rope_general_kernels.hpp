@@ -60,8 +60,7 @@ __global__ void __launch_bounds__(256) rope_scalar_kernel(ScalarArgs a)
         if constexpr (SRC != kSrcTables) {
             // both lanes of pair q share its angle
             const int64_t* p = a.pos + b * a.pos_sb + s * a.pos_ss;
-            const float2 t = pos_cos_sin<TT>(SRC == kSrcAxes ? axis_position(a.ax, p, (uint32_t)q) : p[0],
-                                             a.inv_freq[q]);
+            const float2 t = pos_cos_sin<TT>(p[SRC == kSrcAxes ? axis_offset(a.ax, (uint32_t)q) : 0], a.inv_freq[q]);
             ca = cb = t.x;
             sa = sb = t.y;
         } else {
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RowArgs a)
             float ca, cb, sa, sb;
             if constexpr (SRC != kSrcTables) {
                 // both lanes of pair q share its angle
-                const float2 t = pos_cos_sin<TT>(SRC == kSrcAxes ? axis_position(a.ax, pp, q) : p, a.inv_freq[q]);
+                const float2 t = pos_cos_sin<TT>(SRC == kSrcAxes ? pp[axis_offset(a.ax, q)] : p, a.inv_freq[q]);
                 ca = cb = t.x;
                 sa = sb = t.y;
             } else {

@@ -335,7 +335,7 @@ int source_of(const Plan& p) { return p.pos == nullptr ? kSrcTables : p.naxes ==
 void set_axes(const Plan& p, PosAxes* ax)
 {
     ax->sa = p.pos_sa;
-    ax->last = p.naxes > 0 ? (uint32_t)(p.naxes - 1) : 0;
+    ax->nwords = p.naxes > 1 ? (uint32_t)((p.L / 2 + 15) / 16) : 0;
     std::copy(std::begin(p.axis_words), std::end(p.axis_words), ax->words);
 }
 

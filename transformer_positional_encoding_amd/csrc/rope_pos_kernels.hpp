@@ -252,15 +252,10 @@ struct PosArgs {
 // Positions on several axes (time, height, width): every pair has its axis,
 // and its angle is the position on that axis times the pair's frequency. The
 // axes of the pairs are kernel arguments, two bits each (at most 512 pairs,
-// 32 words). A thread that evaluates a pair loads the (b,s) position on every
-// axis and the pair's word at once and then selects: reading the word first
-// and then the one position would put a second memory latency in front of
-// the evaluation, which the block's other loads do not hide when it holds
-// few heads. On MI355X, bf16 rotate_half heads of 128 lanes, three axes,
-// against the same call with one axis: see the measurements at the kernels.
+// 32 words).
 struct PosAxes {
     int64_t sa;              // axis k's positions lie k*sa further
-    uint32_t last;           // axes - 1
+    uint32_t nwords;         // words in use: 0 with one axis
     uint32_t words[ROPE_D_LIMIT / 2 / 16];
 };
 
@@ -268,29 +263,32 @@ struct PosAxesArgs : PosArgs {
     PosAxes ax;
 };
 
-// The axis of pair i.
-__device__ __forceinline__ uint32_t pair_axis(const PosAxes& ax, uint32_t i)
+// How far the positions on pair i's axis lie behind those on the first. The
+// words come by scalar loads and each lane picks its own, which costs no
+// memory latency beyond that of the arguments themselves. (Indexed by lane
+// they would be vector loads of the arguments, which may lie in host memory:
+// (2,8191) positions on three axes, 36 bf16 heads of 128 lanes, 73 us; one
+// axis 47.)
+__device__ __forceinline__ int64_t axis_offset(const PosAxes& ax, uint32_t i)
 {
-    return (ax.words[i >> 4] >> ((i & 15u) * 2)) & 3u;
+    uint32_t word = 0;
+    for (uint32_t w = 0; w < ax.nwords; w += 4) {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            uint32_t v = ax.words[w + k];
+            asm("" : "+s"(v));           // a value: a choice of addresses would load by lane again
+            word = (i >> 4) == w + k ? v : word;
+        }
+    }
+    return ((word >> ((i & 15u) * 2)) & 3u) * ax.sa;
 }
 
-// The position of pair i of the (b,s) whose first axis is at p.
-__device__ __forceinline__ int64_t axis_position(const PosAxes& ax, const int64_t* p, uint32_t i)
-{
-    const int64_t p0 = p[0];
-    const int64_t p1 = p[ax.last < 1 ? 0 : ax.sa];
-    const int64_t p2 = p[(ax.last < 2 ? ax.last : 2) * ax.sa];
-    const int64_t p3 = p[ax.last * ax.sa];
-    const uint32_t k = pair_axis(ax, i);
-    return k & 2u ? (k & 1u ? p3 : p2) : (k & 1u ? p1 : p0);
-}
-
-// The position of pair i at offset `off` of the positions.
+// The same for the position source of ARGS.
 template <class ARGS>
-__device__ __forceinline__ int64_t pair_position(const ARGS& a, int64_t off, uint32_t i)
+__device__ __forceinline__ int64_t pair_offset(const ARGS& a, uint32_t i)
 {
-    if constexpr (std::is_same<ARGS, PosAxesArgs>::value) return axis_position(a.ax, a.pos + off, i);
-    else return a.pos[off];
+    if constexpr (std::is_same<ARGS, PosAxesArgs>::value) return axis_offset(a.ax, i);
+    else return 0;
 }
 
 // The block's first item under the XCD runs (a bijection of [0, gridDim.x)).
@@ -328,7 +326,7 @@ __device__ __forceinline__ void pos_fill_rest(const ARGS& a, uint32_t g0, float2
         const uint32_t ge = g0 + q;
         if (ge >= a.bs) break;                    // later entries belong to later positions
         const uint32_t i = e - q * a.pairs;
-        cs[e] = pos_cos_sin<TT>(pair_position(a, pos_offset(a, ge), i), a.inv_freq[i]);
+        cs[e] = pos_cos_sin<TT>(a.pos[pos_offset(a, ge) + pair_offset(a, i)], a.inv_freq[i]);
     }
 }
 
@@ -385,6 +383,7 @@ __global__ void __launch_bounds__(256) rope_pos_kernel(ARGS a)
     // the table entry this thread evaluates first: position eq, pair ei
     const uint32_t eq = fast_div(t, a.pairs_div);
     const uint32_t ei = t - eq * a.pairs;
+    const int64_t eo = pair_offset(a, ei);
     // every thread runs the same iterations, so the barriers below are uniform
     for (uint32_t w = pos_first_item(a); w < a.items; w += gridDim.x) {
         const uint32_t grp = fast_div(w, a.chunk_div);
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(256) rope_pos_kernel(ARGS a)
         const uint32_t g0 = grp * a.P;                        // the block's first position
         const uint32_t ge = g0 + eq;                          // the position of entry t
         const bool fill = t < a.entries && ge < a.bs;
-        const int64_t p0 = pair_position(a, pos_offset(a, min(ge, a.bs - 1)), ei);
+        const int64_t p0 = a.pos[pos_offset(a, min(ge, a.bs - 1)) + eo];
         const double f0 = a.inv_freq[ei];
         __builtin_amdgcn_sched_barrier(0);
         const uint32_t g = g0 + pp;
@@ -489,13 +488,14 @@ __global__ void __launch_bounds__(256) rope_pos_out_kernel(ARGS a)
     const int xlane = XCHG ? (int)((t & 63u) + (partner - c)) * 4 : 0;
     const uint32_t eq = fast_div(t, a.pairs_div);
     const uint32_t ei = t - eq * a.pairs;
+    const int64_t eo = pair_offset(a, ei);
     for (uint32_t w = pos_first_item(a); w < a.items; w += gridDim.x) {
         const uint32_t grp = fast_div(w, a.chunk_div);
         const uint32_t chunk = w - grp * a.chunks;
         const uint32_t g0 = grp * a.P;                        // the block's first position
         const uint32_t ge = g0 + eq;                          // the position of entry t
         const bool fill = t < a.entries && ge < a.bs;
-        const int64_t p0 = pair_position(a, pos_offset(a, min(ge, a.bs - 1)), ei);
+        const int64_t p0 = a.pos[pos_offset(a, min(ge, a.bs - 1)) + eo];
         const double f0 = a.inv_freq[ei];
         __builtin_amdgcn_sched_barrier(0);
         const uint32_t g = g0 + pp;
