@@ -676,8 +676,10 @@ typedef struct rope_lora {
  * h is kept in fp32 (16-bit outputs may take it as the sum of two values of
  * 8 bits each, fp32 outputs of three: the part left out is below 2^-16 and
  * 2^-24 of it). A token without an adapter gives rope_proj_fwd's result up to
- * the order of summation. Adapters of neighbouring tokens may differ in any
- * pattern; runs of one adapter are fastest.
+ * the order of summation. Tokens may have their adapters in any order (calls
+ * of many tokens sort them); up to 1023 adapters are fastest. A token whose h
+ * or whose adapter is not finite may get NaN where an infinity would be exact;
+ * no other token's result changes.
  *
  *   workspace        device buffer of workspace_bytes, 16-byte aligned, used
  *                    during the call: at least

@@ -1548,8 +1548,7 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
     a: (count, rank, K) and b: (count, heads * Dh, rank) contiguous, of x's
     dtype; rank a multiple of 8, at most LORA_RANK_MAX (pad with zeros).
     adapters: int32, one per token (x's shape without K): an index into a and
-    b; one outside [0, count), such as -1, adds nothing. Any order; tokens of
-    one adapter beside each other are fastest.
+    b; one outside [0, count), such as -1, adds nothing. Any order.
     scales: float32 (count) or None for ones.
     workspace: a contiguous GPU tensor of at least
     ``rope_proj_lora_workspace(tokens, K, rank)`` bytes, 16-byte aligned, that

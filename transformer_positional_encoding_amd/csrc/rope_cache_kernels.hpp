@@ -332,11 +332,14 @@ __global__ void __launch_bounds__(kGenThreads) rope_cache_read_general_kernel(Ca
 // of a row where that leaves no more lanes idle (D = 128: 8 threads of 2
 // chunks; 576: 32 of 3).
 // Measured on MI355X (GPU time in a graph; K and V of 3 x 2039 tokens, 8 heads
-// of 128 lanes, bf16 to int8, and the (4,4096,1,576) latent to e4m3, us): 14.6
-// and 16.3; one chunk a thread 21.1 and 46; nine (the latent) 16.8; blocks of 64
-// or 128 threads the same within 0.3; one chunk a thread and waves of mixed
-// kinds 23.7 and 20.2; several items a block with the next item's loads ahead
-// 34.9 and 25.3 (its registers halve the waves).
+// of 128 lanes, bf16 to int8, and the (4,4096,1,576) latent to e4m3, us): 14.0
+// and 15.6 (without the rotation 11.9 and 13); with 32 heads of Q beside the
+// first 32.5. While the axes of the pairs were
+// loaded by lane 14.6, 16.3 and 37.4; against those: one chunk a thread 21.1
+// and 46; nine (the latent) 16.8; blocks of 64 or 128 threads the same within
+// 0.3; one chunk a thread and waves of mixed kinds 23.7 and 20.2; several items
+// a block with the next item's loads ahead 34.9 and 25.3 (its registers halve
+// the waves).
 // All loads of a row, and those of the chunks that hold its partners where
 // these lie whole chunks away, go out first; the block's tokens' cos and sin,
 // each pair of each token once, go to LDS while they are in flight; then a
@@ -687,9 +690,13 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWrit
 
 // ---------------------------------------------------------------------------
 // Read, vector form: bound by the bytes it moves. A token's N rows are N * D/8
-// chunks; a wave takes a whole token (WAVE, tokens of 48 chunks or more), so
-// that its sequence, page and addresses are scalar work, or 256 consecutive
-// chunks of the output go to a block, each thread finding its token.
+// chunks; a wave takes a whole token (tokens of 48 chunks or more), so that its
+// sequence, page and addresses are scalar work, or 256 consecutive chunks of
+// the output go to a block, each thread finding its token.
+// Measured on MI355X: 12 sequences of up to 16384 tokens, 8 heads of 128 lanes,
+// e4m3 to bf16, 88 us (5.2 TB/s); 3 x 6135 tokens of int8, 14.5; 5 x 3257 tokens
+// of 4 heads, int4 to fp16, 8.4, and with 32 pairs turned by fp32 cos and sin,
+// whose double evaluation a token's wave waits for, 13.4.
 // ---------------------------------------------------------------------------
 struct CacheReadVecArgs : CacheReadArgs {
     uint32_t chunks;          // of a row

@@ -1,8 +1,8 @@
 // rope_device.hpp -- device-side building blocks of the kernels: vector types, fp32 <->
 // storage conversions, the rotation of a pair, table lanes.
-// Included once, by rope_kernels.hip (the one translation unit of the
-// library): its kernels are instantiated there, next to the host code
-// that selects and launches them.
+// Included by rope_kernels.hip, rope_cache.hip and rope_lora.hip:
+// kernels are instantiated next to the host code that selects and launches
+// them.
 #pragma once
 
 #include <hip/hip_runtime.h>

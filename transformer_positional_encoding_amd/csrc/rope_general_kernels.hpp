@@ -1,9 +1,9 @@
 // rope_general_kernels.hpp -- the general kernels (any alignment, start parity and
 // slice length): the row kernel and the 64-bit scalar kernel, with tables
 // or positions.
-// Included once, by rope_kernels.hip (the one translation unit of the
-// library): its kernels are instantiated there, next to the host code
-// that selects and launches them.
+// Included by rope_kernels.hip:
+// kernels are instantiated next to the host code that selects and launches
+// them.
 #pragma once
 
 #include "rope_pos_kernels.hpp"

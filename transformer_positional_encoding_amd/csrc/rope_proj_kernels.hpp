@@ -1,8 +1,8 @@
 // rope_proj_kernels.hpp -- a head projection whose epilogue rotates each
 // head's slice before the single store: y = rotate(x . w^T).
-// Included once, by rope_kernels.hip (the one translation unit of the
-// library): its kernels are instantiated there, next to the host code
-// that selects and launches them.
+// Included by rope_kernels.hip and rope_lora.hip:
+// kernels are instantiated next to the host code that selects and launches
+// them.
 //
 // Operation: "ascend-transformer-boost 的 MlaPreprocessOperation：MLA 预处理
 // 四阶段融合算子深度解析", section 3 (the WUQ matmul gives Q with headNum x 192

@@ -1,8 +1,8 @@
 // rope_vec_kernels.hpp -- the 16-byte vector kernels (in place, out of place,
 // several tensors) that read cos/sin tables.
-// Included once, by rope_kernels.hip (the one translation unit of the
-// library): its kernels are instantiated there, next to the host code
-// that selects and launches them.
+// Included by rope_kernels.hip, and by rope_cache.hip for its building blocks:
+// kernels are instantiated next to the host code that selects and launches
+// them.
 #pragma once
 
 #include "rope_device.hpp"
