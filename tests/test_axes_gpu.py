@@ -208,3 +208,34 @@ def test_on_another_stream():
     rp.rope_partial_fwd_out_axes(got, x, *how, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_a_captured_training_step():
+    """Forward and backward in a graph, replayed with other positions and
+    gradients."""
+    x = inputs((2, 40, 4, 128), "bf16", 1).cuda().requires_grad_()
+    up = inputs((2, 40, 4, 128), "bf16", 2).cuda()
+    f, ax = freqs(128).cuda(), axes_of(128, 3, 2)
+    pos = grid(3, 2, 40, 3).cuda()
+
+    def step():
+        y = rp.partial_rotary_mul_axes(x, pos, f, ax, "interleave", (0, 128))
+        return y.detach(), torch.autograd.grad(y, x, up)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dx = step()
+    for k in range(4):
+        pos.add_(17 * k + 1)
+        up.neg_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want_y, want_dx = step()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and torch.equal(dx, want_dx)

@@ -401,3 +401,39 @@ def test_on_another_stream():
     s.synchronize()
     rp.rope_cache_write(k, None, b, None, slots)
     assert torch.equal(a.data.view(torch.uint8), b.data.view(torch.uint8)) and torch.equal(a.scales, b.scales)
+
+
+@pytest.mark.parametrize("N, D", [(8, 128), (1, 64), (1, 50)])
+def test_lengths_and_starts_at_the_ends_of_their_type(N, D):
+    """Rows without a cached token keep their bytes whatever lengths and
+    starts hold."""
+    c = filled(4, 3, N, D, "int8", D, "bf16", 1)
+    table = torch.tensor([[0, 1], [2, 3], [1, 2], [3, 0]], dtype=torch.int32)
+    top, low = 2 ** 31 - 1, -2 ** 31
+    for lengths, starts in (([top, low, 5, top], [top, 0, low, 0]), ([5, 5, 5, 5], [5, -4, top - 2, low])):
+        out = torch.full((4, 7, N, D), 3.0, dtype=torch.bfloat16, device="cuda")
+        lengths, starts = (torch.tensor(v, dtype=torch.int32) for v in (lengths, starts))
+        want = read_want(c, out, table, lengths, starts, None, None, None, "bf16")
+        rp.rope_cache_read(out, c, table.cuda(), lengths.cuda(), starts.cuda())
+        assert torch.equal(out.cpu(), want)
+
+
+def test_two_streams_at_once():
+    """Writes and reads of two caches at a time, against one after the other."""
+    g = torch.Generator().manual_seed(3)
+    ks = [torch.randn(3, 200, 4, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    slots, f = slots_for(3, 200, 160, 4, 1).cuda(), rp.rope_inv_freq(128).cuda()
+    pos = torch.arange(200).expand(3, 200).contiguous().cuda()
+    table, lengths = torch.arange(160, dtype=torch.int32).view(1, 160).cuda(), torch.tensor([640], dtype=torch.int32).cuda()
+    state = lambda: (rp.rope_cache(160, 4, 4, 128), torch.zeros(1, 640, 4, 128, dtype=torch.bfloat16, device="cuda"))  # noqa: E731
+    got, want = [state() for _ in ks], [state() for _ in ks]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ks]
+    for k, (c, out), s in zip(ks, got, streams):
+        rp.rope_cache_write(k, None, c, None, slots, pos, f, "rotate_half", (0, 128), stream=s)
+        rp.rope_cache_read(out, c, table, lengths, stream=s)
+    torch.cuda.synchronize()
+    for k, (c, out), (c2, out2) in zip(ks, want, got):
+        rp.rope_cache_write(k, None, c, None, slots, pos, f, "rotate_half", (0, 128))
+        rp.rope_cache_read(out, c, table, lengths)
+        assert torch.equal(out, out2) and torch.equal(c.scales, c2.scales) and bool(out.any())

@@ -253,3 +253,27 @@ def test_more_tokens_than_blocks_of_a_grid(A):
                     torch.arange(M - 120, M, device="cuda")])
     c, cos, sin = rows_of(c, cos, sin, at)
     check(got[:, at], c, cos, sin, 1, "interleave", (28, 32), "bf16", "rows of a long call")
+
+
+@pytest.mark.parametrize("M, K, H, Dh, sl", [(520, 192, 3, 64, (0, 64)), (260, 192, 1, 576, (512, 576)),
+                                             (300, 128, 1, 576, (512, 576)), (17000, 64, 2, 32, (0, 32))])
+@pytest.mark.parametrize("dtype, out", [("bf16", "bf16"), ("f16", "f32")])
+def test_tiles_of_whole_heads_and_of_parts(M, K, H, Dh, sl, dtype, out):
+    """Tiles of 128 and of 192 lanes, heads over several tiles, and more
+    tokens than the sort holds in registers."""
+    c = make(M, K, H, Dh, 24, 5, dtype, seed=M, ids="mixed")
+    cos, sin = tables(M, sl[1] - sl[0], "interleave", "f32", 6)
+    check(run(c, cos, sin, H, "interleave", sl, out), c, cos, sin, H, "interleave", sl, out, "tiles")
+
+
+def test_two_dimensional_tokens_and_one_workspace_in_turn():
+    """(M, K) tokens, and one workspace for calls behind each other on a
+    stream."""
+    ws = torch.empty(rp.rope_proj_lora_workspace(300, 256, 16), dtype=torch.uint8, device="cuda")
+    for seed, M in ((1, 300), (2, 5), (3, 90)):
+        c = make(M, 256, 2, 128, 16, 3, "bf16", seed=seed)
+        cos, sin = tables(M, 128, "rotate_half", "bf16", 2)
+        want = run(c, cos, sin, 2, "rotate_half", (0, 128), "bf16")
+        got = rp.rope_proj_lora_fwd(c["x"][0], c["w"], c["a"], c["b"], c["ids"], cos, sin, 2, "rotate_half", (0, 128),
+                                    scales=c["scales"], workspace=ws)
+        assert torch.equal(got, want)
