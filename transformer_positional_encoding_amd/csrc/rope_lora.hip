@@ -14,6 +14,16 @@
 namespace rope {
 namespace {
 
+// Blocks of the few-token kernel (64 tokens by 32 output lanes) up to which it
+// is taken for more tokens than kLoraFewTokens too: it has no sort, and fills
+// the chip sooner. Measured on MI355X, rank 16, each token its own of 8
+// adapters, us here and on tiles: K 512, 512 lanes: 128 blocks 14 and 33, 512
+// blocks 24 and 35, 1024 blocks 48 and 37; K 1536, 2048 lanes: 256 blocks 21 and
+// 52, 512 blocks 33 and 52, 1024 blocks 61 and 52; K 2048, 5120 lanes: 640
+// blocks 56 and 58, 1280 blocks 89 and 58. (Up to 64 tokens the tiles are mostly
+// empty: K 1536, 24576 lanes, 64 tokens 47 and 60, 80 tokens 76 and 61.)
+constexpr int64_t kFewBlocks = 640;
+
 // A grid's second dimension counts the few-token kernel's 64-token blocks;
 // calls of more tokens that no tiled kernel takes go to the general one.
 constexpr int64_t kFewTokensMax = 64 * 65535ll;
@@ -69,7 +79,8 @@ rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const v
     // the tiled kernels need each rotation group within one tile, and, with
     // adapters, sorted rows: their tiles for a bound on these
     const bool fits = L->P.sq || proj_groups_in_tiles(p.D, p.start, p.L, a.half);
-    L->tiles = fits && a.M > kLoraFewTokens && l.count <= kLoraSortAdapters;
+    const int64_t few_blocks = (a.M + 63) / 64 * (a.N / 32);
+    L->tiles = fits && a.M > kLoraFewTokens && l.count <= kLoraSortAdapters && !(units && few_blocks <= kFewBlocks);
     if (L->tiles && l.count > 0) {
         const int64_t MB = (lora_row_bound(a.M, l.count) + L->P.BM - 1) / L->P.BM;
         if (MB * a.NB > (int64_t)(kMaxGridItems / (uint64_t)L->P.threads)) L->tiles = false;
@@ -111,11 +122,7 @@ template <int DT, int MT>
 void launch_few(const FewArgs& a, int tdt, hipStream_t s)
 {
     const dim3 grid((uint32_t)(a.N / 32), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)));
-    // 8 waves share a unit's K where 4 would leave the chip short of waves
-    if ((uint64_t)grid.x * grid.y < 512)
-        hipLaunchKernelGGL((rope_lora_few_kernel<DT, MT, 8>), grid, dim3(512), 0, s, a, tdt);
-    else
-        hipLaunchKernelGGL((rope_lora_few_kernel<DT, MT, 4>), grid, dim3(256), 0, s, a, tdt);
+    hipLaunchKernelGGL((rope_lora_few_kernel<DT, MT>), grid, dim3(64 * kFewWaves), 0, s, a, tdt);
 }
 
 template <int DT>

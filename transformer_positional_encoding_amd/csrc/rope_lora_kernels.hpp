@@ -542,9 +542,12 @@ __device__ __forceinline__ void few_unit(const FewArgs& a, int32_t u, int32_t (&
     }
 }
 
-template <int DT, int MT, int W>
-__global__ void __launch_bounds__(64 * W) rope_lora_few_kernel(FewArgs a, int tdt)
+constexpr int kFewWaves = 4;      // 8 are the same within 4% up to 32 tokens, and 50 us for 40 with 64
+
+template <int DT, int MT>
+__global__ void __launch_bounds__(64 * kFewWaves) rope_lora_few_kernel(FewArgs a, int tdt)
 {
+    constexpr int W = kFewWaves;
     __shared__ f32x4 part[W + 1][2][MT][64];     // the waves' tiles, and the adapters' part
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

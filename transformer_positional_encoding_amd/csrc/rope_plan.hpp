@@ -141,8 +141,8 @@ struct LoraCheck {
     int64_t workspace_bytes = 0;
 };
 
-// Tokens up to which the kernels for few tokens take a projection with
-// adapters.
+// Tokens up to which no projection with adapters is sorted for the tiled
+// kernels.
 constexpr int64_t kLoraFewTokens = 64;
 // Adapters that the tiled kernels' sort takes.
 constexpr int64_t kLoraSortAdapters = 1023;
