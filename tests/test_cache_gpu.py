@@ -437,3 +437,26 @@ def test_two_streams_at_once():
         rp.rope_cache_write(k, None, c, None, slots, pos, f, "rotate_half", (0, 128))
         rp.rope_cache_read(out, c, table, lengths)
         assert torch.equal(out, out2) and torch.equal(c.scales, c2.scales) and bool(out.any())
+
+
+@pytest.mark.parametrize("N, D, sl, mode", [(1, 64, (0, 64), "interleave"), (5, 64, (0, 64), "rotate_half"),
+                                            (9, 128, (0, 128), "rotate_half"), (1, 1024, (0, 1024), "interleave"),
+                                            (17, 64, (32, 64), "interleave"), (1, 8, (0, 8), "interleave"),
+                                            (18, 64, (0, 64), "rotate_half")])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_read_of_tokens_of_every_width(N, D, sl, mode, fmt):
+    """Tokens of 1 to 144 chunks, many blocks of them, padded rows between."""
+    B, S, page, pages = 3, 150, 16, 40
+    c = filled(pages, page, N, D, fmt, D, "bf16", N)
+    g = torch.Generator().manual_seed(3)
+    table = torch.randperm(pages, generator=g)[:30].view(3, 10).to(torch.int32)
+    lengths = torch.tensor([150, 1, 97], dtype=torch.int32)
+    L = sl[1] - sl[0]
+    pos, f = torch.randint(0, 50000, (1, B, S), generator=g), rp.rope_inv_freq(L)
+    for turned in (False, True):
+        out = torch.full((B, S, N, D), 3.0, dtype=torch.bfloat16, device="cuda")
+        kw = dict(positions=pos[0].cuda(), inv_freq=f.cuda(), rotary_mode=mode, partial_slice=sl) if turned else {}
+        turn = pair_tables(pos, f, (0,) * (L // 2), "bf16") if turned else None
+        want = read_want(c, out, table, lengths, [0] * B, turn, mode, sl, "bf16")
+        rp.rope_cache_read(out, c, table.cuda(), lengths.cuda(), **kw)
+        assert torch.equal(out.cpu().view(torch.uint8), want.view(torch.uint8)), f"turned={turned}"

@@ -282,6 +282,10 @@ hipError_t launch_write(const CacheWritePlan& p, hipStream_t s)
                            args, 0, s);
 }
 
+// Whether a token of so many chunks fills a wave's passes more than three
+// quarters (as every token of more than 144 chunks does).
+bool read_by_wave(uint32_t chunks) { return 4 * chunks > 3 * 64 * ((chunks + 63) / 64); }
+
 hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
 {
     CacheReadVecArgs a{};
@@ -304,11 +308,17 @@ hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
         a.pairs_div = make_fastdiv(std::max<uint32_t>(1, a.turn.pairs));
         void* args[] = {&a};
         const int dt = p.rope.dtype;
-        const bool wave = a.token_chunks >= kWaveTokenChunks;
+        const bool wave = read_by_wave(a.token_chunks);
         const void* fn = wave ? (p.rotate ? by_types<ReadWaveTurn>(dt, fmt) : by_types<ReadWave>(dt, fmt))
                               : (p.rotate ? by_types<ReadVecTurn>(dt, fmt) : by_types<ReadVec>(dt, fmt));
-        const uint32_t grid = wave ? (a.tokens + 3) / 4 : (uint32_t)((items + kVecThreads - 1) / kVecThreads);
-        return hipLaunchKernel(fn, dim3(grid), dim3(kVecThreads), args, 0, s);
+        // (a wave's token has 49 chunks or more, so its grid fits as the block's)
+        const uint32_t block = kReadChunks * kVecThreads;
+        const uint32_t grid = wave ? (a.tokens + 3) / 4 : (uint32_t)((items + block - 1) / block);
+        // tokens that a block's chunks can span: at most 4 pairs for each of its
+        // chunks and of two tokens of 144, 25 KB of cos and sin
+        const size_t spans = (block + a.token_chunks - 2) / a.token_chunks + 1;
+        const size_t lds = !wave && p.rotate ? 2 * spans * a.turn.pairs * sizeof(float) : 0;
+        return hipLaunchKernel(fn, dim3(grid), dim3(kVecThreads), args, lds, s);
     }
     CacheReadArgs g = a;
     void* args[] = {&g};

@@ -690,14 +690,22 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWrit
 
 // ---------------------------------------------------------------------------
 // Read, vector form: bound by the bytes it moves. A token's N rows are N * D/8
-// chunks; a wave takes a whole token (tokens of 48 chunks or more), so that its
-// sequence, page and addresses are scalar work, or 256 consecutive chunks of
-// the output go to a block, each thread finding its token.
-// Measured on MI355X: 12 sequences of up to 16384 tokens, 8 heads of 128 lanes,
-// e4m3 to bf16, 88 us (5.2 TB/s); 3 x 6135 tokens of int8, 14.5; 5 x 3257 tokens
-// of 4 heads, int4 to fp16, 8.4, and with 32 pairs turned by fp32 cos and sin,
-// whose double evaluation a token's wave waits for, 13.4.
+// chunks. A wave takes a whole token, so that its sequence, page and addresses
+// are scalar work, where the token fills the wave's passes of 64 chunks more
+// than three quarters; otherwise 512 consecutive chunks of the output go to a
+// block, two a thread whose loads go out together, each finding its token.
+// Measured on MI355X (134 million lanes of e4m3 to bf16, us; by waves and by
+// blocks): tokens of 16 chunks 256 and 99, 32: 156 and 98, 48: 117 and 98, 64: 92
+// and 98, 72 (a 576-lane latent): 123 and 98, 128: 77 and 101; with 32 pairs
+// turned, 48: 181 and 156, 64: 146 and 142, 72: 174 and 142, 128: 105 and 168 (one
+// chunk a thread). Blocks of one chunk a thread 121, of four 100.
+// 12 sequences of up to 16384 tokens, 8 heads of 128 lanes, e4m3 to bf16, take
+// 88 us (5.2 TB/s); 3 x 6135 tokens of int8, 14.5; 5 x 3257 tokens of 4 heads,
+// int4 to fp16, 8.4, and with 32 pairs turned by fp32 cos and sin, whose double
+// evaluation a token's wave waits for, 13.4.
 // ---------------------------------------------------------------------------
+constexpr int kReadChunks = 2;
+
 struct CacheReadVecArgs : CacheReadArgs {
     uint32_t chunks;          // of a row
     uint32_t token_chunks;    // of a token: N * chunks
@@ -792,45 +800,98 @@ __device__ __forceinline__ void read_chunk(const CacheReadVecArgs& a, const gcha
     store_chunk<DT>(dst + chunk * 8 * ES, x);
 }
 
+// As read_place32 without a branch: where there is no cached token, page and
+// slot 0, which may be read.
+__device__ __forceinline__ bool read_place_always(const CacheReadVecArgs& a, uint32_t b, uint32_t s, int64_t* page,
+                                                  int64_t* in_page)
+{
+    const int32_t len = a.lengths[b], start = a.starts != nullptr ? a.starts[b] : 0;
+    const int64_t tok64 = (int64_t)start + s;
+    bool ok = (int64_t)s < (int64_t)len && tok64 >= 0;
+    int64_t col, in;
+    if (a.small_tokens) {
+        ok = ok && tok64 < (int64_t)0x7FFFFFFF;
+        const uint32_t tok = ok ? (uint32_t)tok64 : 0;
+        const uint32_t c32 = fast_div(tok, a.page_div);
+        col = c32;
+        in = tok - c32 * a.page_div.d;
+    } else {
+        const int64_t tok = ok ? tok64 : 0;
+        col = tok / a.page_size;
+        in = tok - col * a.page_size;
+    }
+    ok = ok && col < a.table_pages;
+    const int64_t pg = a.table[b * a.table_stride + min(col, a.table_pages - 1)];
+    ok = ok && pg >= 0 && pg < a.pages;
+    *page = ok ? pg : 0;
+    *in_page = ok ? in : 0;
+    return ok;
+}
+
 template <int DT, int FMT, bool ROT>
 __global__ void __launch_bounds__(kVecThreads) rope_cache_read_kernel(CacheReadVecArgs a)
 {
     constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
-    __shared__ __attribute__((aligned(16))) float turn_lds[ROT ? 4096 : 4];
-    const uint32_t i0 = blockIdx.x * kVecThreads;
+    constexpr int U = kReadChunks;
+    extern __shared__ __attribute__((aligned(16))) float turn_lds[];   // ROT: cos of the block's tokens' pairs, then sin
+    const uint32_t i0 = blockIdx.x * (U * kVecThreads);
     const uint32_t total = a.tokens * a.token_chunks;
-    const uint32_t i = min(i0 + threadIdx.x, total - 1);
-    const uint32_t tok = fast_div(i, a.token_div);
-    const uint32_t c = i - tok * a.token_chunks;
-    const uint32_t n = fast_div(c, a.chunk_div), chunk = c - n * a.chunks;
-    const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.s_div.d;
     const uint32_t tok0 = fast_div(i0, a.token_div);
-    float* cosv = turn_lds;
+    CodeChunk<DT, FMT> own[U], par[ROT ? U : 1];
+    ChunkTurn kt[ROT ? U : 1];
+    gchar* dst[U];
+    uint32_t at[U];
+    bool ok[U];
+    const bool adjacent = a.turn.half == 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t want = i0 + u * kVecThreads + threadIdx.x;
+        const uint32_t i = min(want, total - 1);
+        const uint32_t tok = fast_div(i, a.token_div);
+        const uint32_t c = i - tok * a.token_chunks;
+        const uint32_t n = fast_div(c, a.chunk_div), chunk = c - n * a.chunks;
+        const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.s_div.d;
+        int64_t page, in_page;
+        ok[u] = read_place_always(a, b, s, &page, &in_page) && want < total;
+        const gchar* src = as_global(a.c.data) + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
+        const gchar* sc = as_global(a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2]);
+        own[u].load(a, src, sc, chunk);
+        if constexpr (ROT) {
+            kt[u] = chunk_turn(a.turn, chunk * 8);
+            const int32_t away = kt[u].in && !adjacent ? kt[u].to_partner : 0;
+            par[u].load(a, src, sc, (uint32_t)((int32_t)(chunk * 8) + away) / 8);
+        }
+        dst[u] = as_global(a.out.data) + (b * a.out.sb + s * a.out.ss + n * a.out.sn) * ES + chunk * 8 * ES;
+        at[u] = (tok - tok0) * a.turn.pairs;
+    }
     float* sinv = turn_lds;
     if constexpr (ROT) {
-        const uint32_t tok1 = fast_div(min(i0 + kVecThreads, total) - 1, a.token_div);
+        const uint32_t tok1 = fast_div(min(i0 + U * kVecThreads, total) - 1, a.token_div);
         const uint32_t entries = (tok1 - tok0 + 1) * a.turn.pairs;
-        sinv = turn_lds + entries;
+        sinv += entries;
         for (uint32_t e = threadIdx.x; e < entries; e += kVecThreads) {
             const uint32_t k = fast_div(e, a.pairs_div);
             const uint32_t be = fast_div(tok0 + k, a.s_div);
             const float2 cs = turn_cos_sin(a.turn, be, tok0 + k - be * a.s_div.d, e - k * a.turn.pairs);
-            cosv[e] = cs.x;
+            turn_lds[e] = cs.x;
             sinv[e] = cs.y;
         }
         __syncthreads();
-        cosv += (tok - tok0) * a.turn.pairs;
-        sinv += (tok - tok0) * a.turn.pairs;
     }
-    int64_t page, in_page;
-    if (i0 + threadIdx.x >= total || !read_place32(a, b, s, &page, &in_page)) return;
-    const gchar* src = as_global(a.c.data) + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
-    const gchar* sc = as_global(a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2]);
-    gchar* dst = as_global(a.out.data) + (b * a.out.sb + s * a.out.ss + n * a.out.sn) * ES;
-    read_chunk<DT, FMT, ROT>(a, src, sc, dst, chunk, cosv, sinv);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float x[8];
+        own[u].widen(x);
+        if constexpr (ROT) {
+            if (kt[u].in) {
+                float p[8];
+                par[u].widen(p);
+                turn_chunk(x, p, kt[u], adjacent, turn_lds + at[u], sinv + at[u]);
+            }
+        }
+        if (ok[u]) store_chunk<DT>(dst[u], x);
+    }
 }
-
-constexpr uint32_t kWaveTokenChunks = 48;
 
 template <int DT, int FMT, bool ROT>
 __global__ void __launch_bounds__(kVecThreads) rope_cache_read_wave_kernel(CacheReadVecArgs a)
