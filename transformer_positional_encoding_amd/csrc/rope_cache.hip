@@ -101,7 +101,6 @@ CacheReadArgs read_args(const CacheReadPlan& p)
     a.rotate = p.rotate ? 1 : 0;
     a.turn = turn_of(p.rope);
     a.s_div = make_fastdiv(a.S);
-    a.n_div = make_fastdiv(a.N);
     return a;
 }
 
@@ -322,7 +321,8 @@ hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
     }
     CacheReadArgs g = a;
     void* args[] = {&g};
-    return hipLaunchKernel(by_types<ReadGeneral>(p.rope.dtype, fmt), dim3(general_grid(a.rows)), dim3(kGenThreads), args,
+    const uint64_t blocks = std::min<uint64_t>((uint64_t)p.B * (uint64_t)p.S, kMaxGridItems / kGenReadThreads);
+    return hipLaunchKernel(by_types<ReadGeneral>(p.rope.dtype, fmt), dim3((uint32_t)blocks), dim3(kGenReadThreads), args,
                            0, s);
 }
 

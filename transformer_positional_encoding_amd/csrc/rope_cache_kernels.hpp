@@ -136,7 +136,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
 }
 
 // ---------------------------------------------------------------------------
-// General kernels: any dimensions, alignment, slice and group. One wave per
+// General kernels: any dimensions, alignment, slice and group. Writing, one wave per
 // row; the row's rotated values in LDS, its groups' largest magnitudes by LDS
 // maxima (of the bits of non-negative floats: the order does not matter).
 // ---------------------------------------------------------------------------
@@ -255,7 +255,7 @@ struct CacheReadArgs {
     int64_t pages, page_size;
     int32_t rotate;
     Turn turn;
-    FastDiv s_div, n_div;
+    FastDiv s_div;
 };
 
 // The page and the slot within it of row s of sequence b; false when the row
@@ -293,29 +293,42 @@ __device__ __forceinline__ float cached_lane(const CacheRef& c, const char* src,
     }
 }
 
+// A block takes a token, its waves the token's rows in turn: cos and sin are
+// evaluated once a token. (A wave a row, each evaluating its own twice a pair:
+// 17 x 2947 tokens of 8 heads of 80 lanes, int4 to fp32, lanes [3,75) turned,
+// 208 us; this 144.)
+constexpr int kGenReadThreads = 256;
+
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kGenThreads) rope_cache_read_general_kernel(CacheReadArgs a)
+__global__ void __launch_bounds__(kGenReadThreads) rope_cache_read_general_kernel(CacheReadArgs a)
 {
-    for (uint64_t row64 = blockIdx.x; row64 < a.rows; row64 += gridDim.x) {
-        const uint32_t row = (uint32_t)row64;
-        const uint32_t bs = fast_div(row, a.n_div);
-        const uint32_t n = row - bs * a.N;
-        const uint32_t b = fast_div(bs, a.s_div), s = bs - b * a.s_div.d;
+    __shared__ float2 cs[ROPE_D_LIMIT / 2];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t tokens = a.rows / a.N;
+    for (uint64_t tok64 = blockIdx.x; tok64 < tokens; tok64 += gridDim.x) {
+        const uint32_t tok = (uint32_t)tok64;
+        const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.s_div.d;
         int64_t page, in_page;
-        if (!read_place(a, b, s, &page, &in_page)) continue;
-        const char* src = a.c.data + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
-        const float* sc = a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2];
-        const int64_t off = b * a.out.sb + s * a.out.ss + n * a.out.sn;
-        for (uint32_t j = threadIdx.x; j < a.D; j += kGenThreads) {
-            float x = cached_lane<DT, FMT>(a.c, src, sc, j);
-            if (a.rotate && j >= a.turn.start && j < a.turn.start + a.turn.L) {
-                bool first;
-                const uint32_t i = turn_pair(a.turn, j - a.turn.start, &first);
-                const float p = cached_lane<DT, FMT>(a.c, src, sc, first ? j + a.turn.half : j - a.turn.half);
-                const float2 cs = turn_cos_sin(a.turn, b, s, i);
-                x = rotate_own_unfused(x, p, cs.x, cs.y, first);
+        if (!read_place(a, b, s, &page, &in_page)) continue;      // the same for the whole block
+        if (a.rotate) {
+            __syncthreads();                                      // the rows of the token before are done
+            for (uint32_t i = threadIdx.x; i < a.turn.pairs; i += kGenReadThreads) cs[i] = turn_cos_sin(a.turn, b, s, i);
+            __syncthreads();
+        }
+        for (uint32_t n = wave; n < a.N; n += kGenReadThreads / 64) {
+            const char* src = a.c.data + page * a.c.st[0] + in_page * a.c.st[1] + n * a.c.st[2];
+            const float* sc = a.c.scales + page * a.c.sc[0] + in_page * a.c.sc[1] + n * a.c.sc[2];
+            const int64_t off = b * a.out.sb + s * a.out.ss + n * a.out.sn;
+            for (uint32_t j = lane; j < a.D; j += 64) {
+                float x = cached_lane<DT, FMT>(a.c, src, sc, j);
+                if (a.rotate && j >= a.turn.start && j < a.turn.start + a.turn.L) {
+                    bool first;
+                    const uint32_t i = turn_pair(a.turn, j - a.turn.start, &first);
+                    const float p = cached_lane<DT, FMT>(a.c, src, sc, first ? j + a.turn.half : j - a.turn.half);
+                    x = rotate_own_unfused(x, p, cs[i].x, cs[i].y, first);
+                }
+                Store<DT>::store1(a.out.data, off + j, x);
             }
-            Store<DT>::store1(a.out.data, off + j, x);
         }
     }
 }
