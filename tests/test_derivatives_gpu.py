@@ -1,0 +1,97 @@
+"""Derivatives of the autograd operators beyond the first, and in forward mode,
+on the GPU's kernels, against the same rotation in recorded fp64 operations."""
+import pytest
+import torch
+import torch.autograd.forward_ad as fw
+
+import transformer_positional_encoding_amd as rp
+from axes_refs import pair_tables
+from test_derivatives_cpu import plain_rotation
+
+pytestmark = pytest.mark.gpu
+
+SHAPE, SL = (2, 37, 3, 64), (16, 48)
+AXES = rp.rope_pair_axes((6, 5, 5), dealt=True)
+FORMS = ["axes", "axes in place", "pos", "pos in place"]
+
+
+def rand(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+def operators(form, mode):
+    """(the operator on GPU tensors, its plain form on CPU tensors, and that
+    with every term's magnitude: of magnitudes, the size of all its terms)."""
+    positions = torch.randint(0, 900, (3, 2, 37), generator=torch.Generator().manual_seed(1))
+    freq = rp.rope_inv_freq(SL[1] - SL[0])
+    if form.startswith("axes"):
+        how, (cos, sin) = (positions.cuda(), freq.cuda(), AXES, mode, SL), pair_tables(positions, freq, AXES, "f32")
+        out, inplace = rp.partial_rotary_mul_axes, rp.inplace_partial_rotary_mul_axes
+    else:
+        how = (positions[0].cuda(), freq.cuda(), mode, SL)
+        cos, sin = pair_tables(positions[:1], freq, (0,) * 16, "f32")
+        out, inplace = rp.partial_rotary_mul_pos, rp.inplace_partial_rotary_mul_pos
+
+    def changed(x):
+        y = x * 1.0
+        inplace(y, *how)
+        return y
+    return (changed if form.endswith("in place") else lambda x: out(x, *how),
+            lambda x: plain_rotation(x, cos, sin, mode, SL),
+            lambda x: plain_rotation(x, cos.abs(), sin.abs(), mode, SL, 1.0))
+
+
+def close(got, want, size, depth):
+    """The results here are polynomials of their inputs: with `depth` fp32
+    roundings between an input and a lane, of 2^-24 each, a lane is off by at
+    most (1 + 2^-24)^depth - 1 of the size of its terms, the polynomial of the
+    magnitudes."""
+    assert bool(((got.double().cpu() - want).abs() <= 1.01 * depth * 2.0 ** -24 * size).all())
+    assert float(want.abs().max()) > 0
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("mode", ["interleave", "rotate_half"])
+def test_gradient_penalty(form, mode):
+    op, ref, sizes = operators(form, mode)
+    x, w = rand((2, 37, 7), 2), rand((7, 192), 3)
+
+    def penalty(f, xx, ww):
+        xx, ww = xx.clone().requires_grad_(), ww.clone().requires_grad_()
+        y = f((xx.reshape(-1, 7) @ ww).view(SHAPE))
+        (g,) = torch.autograd.grad((y ** 3).sum(), xx, create_graph=True)
+        return torch.autograd.grad((g ** 2).sum(), ww)[0]
+
+    # y sums 7 products, g 192, the second backward 7, 192 and 74 tokens, with
+    # four rotations of 3 roundings (and cos and sin's own) and the powers
+    # between them
+    x, w = x.double(), w.double()
+    close(penalty(op, x.float().cuda(), w.float().cuda()), penalty(ref, x, w), penalty(sizes, x.abs(), w.abs()),
+          2 * (7 + 192) + 74 + 4 * 4 + 12)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("mode", ["interleave", "rotate_half"])
+@pytest.mark.parametrize("needs", [False, True])
+def test_forward_mode(form, mode, needs):
+    op, ref, sizes = operators(form, mode)
+    x, t = rand(SHAPE, 6).double(), rand(SHAPE, 7).double()
+    with fw.dual_level():
+        y = fw.unpack_dual(op(fw.make_dual(x.float().cuda().requires_grad_(needs), t.float().cuda())))
+        close(y.tangent.detach(), ref(t), sizes(t.abs()), 4)
+        close(y.primal.detach(), ref(x), sizes(x.abs()), 4)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_forward_over_reverse(form):
+    op, ref, sizes = operators(form, "rotate_half")
+    x, t = rand(SHAPE, 8).double(), rand(SHAPE, 9).double()
+
+    def hvp(f, x, t):
+        with fw.dual_level():
+            d = fw.make_dual(x.clone().requires_grad_(), t)
+            (g,) = torch.autograd.grad((f(d) ** 3).sum(), d, create_graph=True)
+            return fw.unpack_dual(g).tangent.detach()
+
+    # three rotations, the powers and the product with the tangent
+    close(hvp(op, x.float().cuda(), t.float().cuda()), hvp(ref, x, t), hvp(sizes, x.abs(), t.abs()), 3 * 4 + 8)

@@ -681,7 +681,7 @@ def _check_pair_axes(positions, pair_axes, partial_slice):
     return pair_axes
 
 
-def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtype, stream, y=None, pair_axes=None):
+def _call_pos(direction, x, positions, inv_freq, mode, partial_slice, table_dtype, stream, pair_axes=None, y=None):
     """The position entry points: in place on x, or (y given) out of place
     from x into y; with pair_axes, those with several axes."""
     import torch
@@ -993,95 +993,119 @@ def partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None):
 
 # ---------------------------------------------------------------- autograd, cos/sin from positions
 
-def _grad_x_pos(grad, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
-    """The gradient with respect to x for ``grad`` in a new tensor, cos and
-    sin computed from the positions (see _grad_x: grad is never modified)."""
+_OTHER = {"fwd": "bwd", "bwd": "fwd"}
+_TORCH = None
+
+
+def _differentiated(x):
+    """Whether autograd follows x: it needs a gradient, or has a tangent."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = (torch.is_grad_enabled, torch.autograd.forward_ad)
+    enabled, fw = _TORCH
+    return x.requires_grad and enabled() or fw._current_level >= 0 and fw.unpack_dual(x).tangent is not None
+
+
+def _rotated_new(rotate, direction, x, a, b, how):
+    """A new contiguous tensor holding x with its slice rotated. x is never
+    modified (as an incoming gradient, autograd may hand it to other
+    consumers): a contiguous one is read by the out-of-place kernel (one pass),
+    any other layout (e.g. the stride-0 gradient of an expand) is first made
+    into a private contiguous copy, which is then rotated in place."""
     import torch
-    if grad.is_contiguous():
-        dx = torch.empty_like(grad, memory_format=torch.contiguous_format)
-        _call_pos("bwd", grad, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, y=dx,
-                  pair_axes=pair_axes)
-        return dx
-    dx = grad.contiguous()
-    _call_pos("bwd", dx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, pair_axes=pair_axes)
-    return dx
-
-
-def _pos_functions():
-    import torch
-
-    def _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes):
-        ctx.save_for_backward(positions, inv_freq)
-        ctx.rotary_mode = rotary_mode
-        ctx.partial_slice = None if partial_slice is None else tuple(int(v) for v in partial_slice)
-        ctx.table_dtype = table_dtype
-        ctx.pair_axes = None if pair_axes is None else tuple(pair_axes)
-
-    def _backward(ctx, grad):
-        positions, inv_freq = ctx.saved_tensors
-        dx = _grad_x_pos(grad, positions, inv_freq, ctx.rotary_mode, ctx.partial_slice, ctx.table_dtype,
-                         ctx.pair_axes)
-        return dx, None, None, None, None, None, None
-
-    class InplacePartialRotaryMulPosFn(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes):
-            _call_pos("fwd", x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None,
-                      pair_axes=pair_axes)
-            ctx.mark_dirty(x)
-            _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
-            return x
-
-        backward = staticmethod(_backward)
-
-    class PartialRotaryMulPosFn(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes):
-            y = _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
-            _save(ctx, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
-            return y
-
-        backward = staticmethod(_backward)
-
-    return InplacePartialRotaryMulPosFn, PartialRotaryMulPosFn
-
-
-def _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
-    import torch
-    xc = x.contiguous()
-    if xc.numel() and xc.data_ptr() != x.data_ptr():
-        _call_pos("fwd", xc, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, pair_axes=pair_axes)
-        return xc
-    y = torch.empty_like(xc, memory_format=torch.contiguous_format)
-    _call_pos("fwd", xc, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, y=y, pair_axes=pair_axes)
+    if x.is_contiguous():
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        rotate(direction, x, a, b, *how, y)
+        return y
+    y = x.contiguous()
+    rotate(direction, y, a, b, *how)
     return y
 
 
-_POS_FNS = None
-
-
-def _autograd_inplace_pos(name, x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
+def _rotation_functions():
+    """The autograd functions of a rotation, in place and out of place. Their
+    arguments: rotate(direction, x, a, b, *how[, y]), the direction, x, the two
+    tensors that cos and sin come from, and what else rotate takes. The
+    rotation is linear in x, so its backward is the rotation in the other
+    direction and its tangent the tangent's rotation, both recorded in their
+    turn where something follows them."""
     import torch
-    global _POS_FNS
-    if torch.is_grad_enabled() and x.requires_grad:
-        if x.is_leaf:
-            raise RuntimeError(f"{name}: x is a leaf tensor that requires grad; "
-                               "rotate a non-leaf copy of it (e.g. y = x * 1.0)")
-        if _POS_FNS is None:
-            _POS_FNS = _pos_functions()
-        _POS_FNS[0].apply(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
+
+    def save(ctx, rotate, direction, a, b, how):
+        ctx.save_for_backward(a, b)
+        if torch.autograd.forward_ad._current_level >= 0:
+            ctx.save_for_forward(a, b)
+        ctx.call = rotate, direction, how
+
+    def backward(ctx, grad):
+        rotate, direction, how = ctx.call
+        a, b = ctx.saved_tensors
+        turn = _autograd_out if _differentiated(grad) else _rotated_new
+        return None, None, turn(rotate, _OTHER[direction], grad, a, b, how), None, None, None
+
+    def tangent(ctx, t):
+        rotate, direction, how = ctx.call
+        a, b = ctx.saved_tensors
+        return _autograd_out(rotate, direction, t, a, b, how)
+
+    class InplaceRotationFn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rotate, direction, x, a, b, how):
+            rotate(direction, x, a, b, *how)
+            ctx.mark_dirty(x)
+            save(ctx, rotate, direction, a, b, how)
+            return x
+
+        @staticmethod
+        def jvp(ctx, _rotate, _direction, t, *_):
+            # the tangent of a value changed in place has to change in place
+            return t.copy_(tangent(ctx, t))
+
+    class RotationFn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rotate, direction, x, a, b, how):
+            y = _rotated_new(rotate, direction, x, a, b, how)
+            save(ctx, rotate, direction, a, b, how)
+            return y
+
+        @staticmethod
+        def jvp(ctx, _rotate, _direction, t, *_):
+            return tangent(ctx, t)
+
+    InplaceRotationFn.backward = RotationFn.backward = staticmethod(backward)
+    return InplaceRotationFn, RotationFn
+
+
+_ROTATION_FNS = None
+
+
+def _rotation_fn(inplace):
+    global _ROTATION_FNS
+    if _ROTATION_FNS is None:
+        _ROTATION_FNS = _rotation_functions()
+    return _ROTATION_FNS[0 if inplace else 1]
+
+
+def _autograd_inplace(name, rotate, x, a, b, how):
+    if not _differentiated(x):
+        rotate("fwd", x, a, b, *how)
         return
-    _call_pos("fwd", x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, None, pair_axes=pair_axes)
+    if x.is_leaf and x.requires_grad and _TORCH[0]():
+        raise RuntimeError(f"{name}: x is a leaf tensor that requires grad; "
+                           "rotate a non-leaf copy of it (e.g. y = x * 1.0)")
+    _rotation_fn(True).apply(rotate, "fwd", x, a, b, how)
 
 
-def _autograd_out_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes=None):
-    import torch
-    global _POS_FNS
-    if torch.is_grad_enabled() and x.requires_grad:
-        if _POS_FNS is None:
-            _POS_FNS = _pos_functions()
-        return _POS_FNS[1].apply(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
-    return _rotated_copy_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, pair_axes)
+def _autograd_out(rotate, direction, x, a, b, how):
+    if _differentiated(x):
+        return _rotation_fn(False).apply(rotate, direction, x, a, b, how)
+    return _rotated_new(rotate, direction, x, a, b, how)
+
+
+def _pos_how(rotary_mode, partial_slice, table_dtype, pair_axes=None):
+    sl = None if partial_slice is None else (int(partial_slice[0]), int(partial_slice[1]))
+    return rotary_mode, sl, table_dtype, None, pair_axes
 
 
 def inplace_partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interleave", partial_slice=None,
@@ -1089,33 +1113,35 @@ def inplace_partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interlea
     """:func:`inplace_partial_rotary_mul` with cos and sin computed in the
     kernel from positions (see :func:`rope_partial_fwd_inplace_pos`).
     positions and inv_freq never get gradients; x must not be a leaf tensor
-    that requires grad."""
-    _autograd_inplace_pos("inplace_partial_rotary_mul_pos", x, positions, inv_freq, rotary_mode, partial_slice,
-                          table_dtype)
+    that requires grad. Differentiable any number of times and in forward
+    mode."""
+    _autograd_inplace("inplace_partial_rotary_mul_pos", _call_pos, x, positions, inv_freq,
+                      _pos_how(rotary_mode, partial_slice, table_dtype))
 
 
 def partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interleave", partial_slice=None,
                            table_dtype=None):
     """:func:`partial_rotary_mul` with cos and sin computed in the kernel from
     positions: returns a new tensor, x is not modified, and the backward is
-    the out-of-place position backward. positions and inv_freq never get
-    gradients."""
-    return _autograd_out_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype)
+    the out-of-place position backward, differentiable in its turn, as is the
+    tangent in forward mode. positions and inv_freq never get gradients."""
+    return _autograd_out(_call_pos, "fwd", x, positions, inv_freq, _pos_how(rotary_mode, partial_slice, table_dtype))
 
 
 def inplace_partial_rotary_mul_axes(x, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
                                     table_dtype=None) -> None:
     """:func:`inplace_partial_rotary_mul_pos` with positions on several axes
     (see :func:`rope_partial_fwd_inplace_axes`)."""
-    _autograd_inplace_pos("inplace_partial_rotary_mul_axes", x, positions, inv_freq, rotary_mode, partial_slice,
-                          table_dtype, tuple(pair_axes))
+    _autograd_inplace("inplace_partial_rotary_mul_axes", _call_pos, x, positions, inv_freq,
+                      _pos_how(rotary_mode, partial_slice, table_dtype, tuple(pair_axes)))
 
 
 def partial_rotary_mul_axes(x, positions, inv_freq, pair_axes, rotary_mode="interleave", partial_slice=None,
                             table_dtype=None):
     """:func:`partial_rotary_mul_pos` with positions on several axes (see
     :func:`rope_partial_fwd_inplace_axes`)."""
-    return _autograd_out_pos(x, positions, inv_freq, rotary_mode, partial_slice, table_dtype, tuple(pair_axes))
+    return _autograd_out(_call_pos, "fwd", x, positions, inv_freq,
+                         _pos_how(rotary_mode, partial_slice, table_dtype, tuple(pair_axes)))
 
 
 def _call_pos_multi(direction, xs, positions, inv_freq, mode, partial_slice, table_dtype, stream, pair_axes=None):
