@@ -15,7 +15,7 @@ PAIR_AXES = (0, 1, 2, 0)
 
 
 def unseen(y, x, cos, sin, mode, sl, direction):
-    """y's bytes become x's rotated ones."""
+    """y's bytes become x's rotated ones; cos and sin a pair's."""
     out = rotate64(x.detach().clone().double(), cos, sin, mode, sl, back=direction == "bwd")[0]
     np.copyto(y.detach().numpy(), out.numpy())
 
@@ -29,7 +29,13 @@ def kernels(monkeypatch):
         cos, sin = pair_tables(positions, inv_freq, pair_axes, "f32")
         unseen(x if y is None else y, x, cos, sin, mode, partial_slice, direction)
 
+    def call_out(direction, y, x, r1, r2, mode, partial_slice, stream):
+        assert x.is_contiguous()
+        unseen(y, x, r1, r2, mode, partial_slice, direction)
+
     monkeypatch.setattr(rp, "_call_pos", call_pos)
+    monkeypatch.setattr(rp, "_call_out", call_out)
+    monkeypatch.setattr(rp, "_call", lambda direction, x, *how: call_out(direction, x, x, *how))
 
 
 def rand(shape, seed):
@@ -71,11 +77,15 @@ def operators(form, mode):
         how = (POSITIONS[0], FREQ, mode, SL)
         cos, sin = pair_tables(POSITIONS[:1], FREQ, (0,) * 4, "f32")
         out, inplace = rp.partial_rotary_mul_pos, rp.inplace_partial_rotary_mul_pos
+    else:
+        cos, sin = rand((2, 5, 1, 4), 40), rand((2, 5, 1, 4), 41)
+        how = (cos, sin, mode, SL)
+        out, inplace = rp.partial_rotary_mul, rp.inplace_partial_rotary_mul
     op = in_place(lambda y: inplace(y, *how)) if form.endswith("in place") else lambda x: out(x, *how)
     return op, lambda x: plain_rotation(x, cos, sin, mode)
 
 
-FORMS = ["axes", "axes in place", "pos", "pos in place"]
+FORMS = ["axes", "axes in place", "pos", "pos in place", "tables", "tables in place"]
 both = [pytest.mark.parametrize("form", FORMS), pytest.mark.parametrize("mode", ["interleave", "rotate_half"])]
 
 
@@ -133,17 +143,18 @@ def test_forward_mode(form, mode):
             close(y.primal.detach(), ref(x))
 
 
-@pytest.mark.parametrize("form", ["axes", "pos"])
+@pytest.mark.parametrize("form", ["axes", "pos", "tables"])
 @pytest.mark.parametrize("mode", ["interleave", "rotate_half"])
 def test_forward_mode_in_place_of_a_value_without_gradient(form, mode):
     """In place on the dual tensor itself, its tangent not contiguous."""
     x, t = rand(SHAPE, 6), rand((16, 3, 5, 2), 7).permute(3, 2, 1, 0)
-    how = (POSITIONS, FREQ, PAIR_AXES, mode, SL) if form == "axes" else (POSITIONS[0], FREQ, mode, SL)
-    rotate = rp.inplace_partial_rotary_mul_axes if form == "axes" else rp.inplace_partial_rotary_mul_pos
+    rotate, how = {"axes": (rp.inplace_partial_rotary_mul_axes, (POSITIONS, FREQ, PAIR_AXES)),
+                   "pos": (rp.inplace_partial_rotary_mul_pos, (POSITIONS[0], FREQ)),
+                   "tables": (rp.inplace_partial_rotary_mul, (rand((2, 5, 1, 4), 40), rand((2, 5, 1, 4), 41)))}[form]
     _, ref = operators(form, mode)
     with fw.dual_level():
         d = fw.make_dual(x.clone(), t.clone())
-        rotate(d, *how)
+        rotate(d, *how, mode, SL)
         y = fw.unpack_dual(d)
         close(y.tangent, ref(t))
         close(y.primal, ref(x))

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 SHAPE, SL = (2, 37, 3, 64), (16, 48)
 AXES = rp.rope_pair_axes((6, 5, 5), dealt=True)
-FORMS = ["axes", "axes in place", "pos", "pos in place"]
+FORMS = ["axes", "axes in place", "pos", "pos in place", "tables", "tables in place"]
 
 
 def rand(shape, seed):
@@ -27,6 +27,13 @@ def operators(form, mode):
     if form.startswith("axes"):
         how, (cos, sin) = (positions.cuda(), freq.cuda(), AXES, mode, SL), pair_tables(positions, freq, AXES, "f32")
         out, inplace = rp.partial_rotary_mul_axes, rp.inplace_partial_rotary_mul_axes
+    elif form.startswith("tables"):
+        cos, sin = rand((2, 37, 1, 16), 40).double(), rand((2, 37, 1, 16), 41).double()
+        # a lane's table value is its pair's
+        lanes = torch.arange(32)
+        pair = lanes // 2 if mode == "interleave" else lanes % 16
+        how = (cos[..., pair].float().cuda(), sin[..., pair].float().cuda(), mode, SL)
+        out, inplace = rp.partial_rotary_mul, rp.inplace_partial_rotary_mul
     else:
         how = (positions[0].cuda(), freq.cuda(), mode, SL)
         cos, sin = pair_tables(positions[:1], freq, (0,) * 16, "f32")

@@ -874,124 +874,9 @@ def rope_partial_bwd_inplace_multi(dxs, r1, r2, rotary_mode="interleave", partia
 # Autograd op over the C ABI ("CANN ops-transformer 算子详解：
 # inplace_partial_rotary_mul 原地部分旋转位置编码", section 自动微分说明 and the
 # training-mode example of section 调用说明): the forward rotates x in place
-# and marks it dirty; the backward runs the in-place backward entry point on
-# the incoming gradient; r1 and r2 receive no gradient.
+# and marks it dirty; the backward is the rotation in the other direction of
+# the incoming gradient; what cos and sin come from receives no gradient.
 # ---------------------------------------------------------------------------
-
-def _autograd_function():
-    import torch
-
-    class InplacePartialRotaryMulFn(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, r1, r2, rotary_mode, partial_slice):
-            rope_partial_fwd_inplace(x, r1, r2, rotary_mode, partial_slice)
-            ctx.mark_dirty(x)
-            ctx.save_for_backward(r1, r2)
-            ctx.rotary_mode = rotary_mode
-            ctx.partial_slice = None if partial_slice is None else tuple(int(v) for v in partial_slice)
-            return x
-
-        @staticmethod
-        def backward(ctx, grad):
-            r1, r2 = ctx.saved_tensors
-            return _grad_x(grad, r1, r2, ctx.rotary_mode, ctx.partial_slice), None, None, None, None
-
-    return InplacePartialRotaryMulFn
-
-
-def _grad_x(grad, r1, r2, rotary_mode, partial_slice):
-    """The gradient with respect to x for the incoming gradient ``grad``,
-    in a new tensor. Autograd may hand the same gradient buffer to other
-    consumers, so it is never modified: a contiguous gradient is read by
-    the out-of-place backward (one pass), any other layout (e.g. the stride-0
-    gradient of an expand) is first made into a private contiguous copy,
-    which is then rotated in place."""
-    import torch
-    if grad.is_contiguous():
-        dx = torch.empty_like(grad, memory_format=torch.contiguous_format)
-        rope_partial_bwd_out(dx, grad, r1, r2, rotary_mode, partial_slice)
-        return dx
-    dx = grad.contiguous()
-    rope_partial_bwd_inplace(dx, r1, r2, rotary_mode, partial_slice)
-    return dx
-
-
-def _rotated_copy(x, r1, r2, rotary_mode, partial_slice):
-    """A new contiguous tensor holding x with its slice rotated. A
-    non-contiguous x is first made into a private contiguous copy, which is
-    then rotated in place (one pass less than copying it again)."""
-    import torch
-    xc = x.contiguous()
-    if xc.numel() and xc.data_ptr() != x.data_ptr():
-        rope_partial_fwd_inplace(xc, r1, r2, rotary_mode, partial_slice)
-        return xc
-    y = torch.empty_like(xc, memory_format=torch.contiguous_format)
-    rope_partial_fwd_out(y, xc, r1, r2, rotary_mode, partial_slice)
-    return y
-
-
-def _out_of_place_function():
-    import torch
-
-    class PartialRotaryMulFn(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, r1, r2, rotary_mode, partial_slice):
-            y = _rotated_copy(x, r1, r2, rotary_mode, partial_slice)
-            ctx.save_for_backward(r1, r2)
-            ctx.rotary_mode = rotary_mode
-            ctx.partial_slice = None if partial_slice is None else tuple(int(v) for v in partial_slice)
-            return y
-
-        @staticmethod
-        def backward(ctx, grad):
-            r1, r2 = ctx.saved_tensors
-            return _grad_x(grad, r1, r2, ctx.rotary_mode, ctx.partial_slice), None, None, None, None
-
-    return PartialRotaryMulFn
-
-
-_FN = None
-_FN_OUT = None
-
-
-def inplace_partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None) -> None:
-    """In-place partial RoPE that records itself for autograd when x needs a
-    gradient, and calls the forward entry point directly otherwise.
-
-    x must not be a leaf tensor that requires grad: in-place changes to such
-    a tensor are illegal in autograd, so rotate a non-leaf copy (y = x * 1.0),
-    as the training example on the page does. r1 and r2 never get gradients.
-    """
-    import torch
-    global _FN
-    if torch.is_grad_enabled() and x.requires_grad:
-        if x.is_leaf:
-            raise RuntimeError("inplace_partial_rotary_mul: x is a leaf tensor that requires grad; "
-                               "rotate a non-leaf copy of it (e.g. y = x * 1.0)")
-        if _FN is None:
-            _FN = _autograd_function()
-        _FN.apply(x, r1, r2, rotary_mode, partial_slice)
-        return None
-    rope_partial_fwd_inplace(x, r1, r2, rotary_mode, partial_slice)
-    return None
-
-
-def partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None):
-    """Out-of-place partial RoPE: returns a new contiguous tensor holding x
-    with ``x[..., start:end)`` rotated; x is not modified. Records itself for
-    autograd (the backward is the out-of-place backward entry point) and
-    works on leaf tensors too, so a training step needs no ``x * 1.0`` copy
-    before the in-place op. r1 and r2 never get gradients."""
-    import torch
-    global _FN_OUT
-    if torch.is_grad_enabled() and x.requires_grad:
-        if _FN_OUT is None:
-            _FN_OUT = _out_of_place_function()
-        return _FN_OUT.apply(x, r1, r2, rotary_mode, partial_slice)
-    return _rotated_copy(x, r1, r2, rotary_mode, partial_slice)
-
-
-# ---------------------------------------------------------------- autograd, cos/sin from positions
 
 _OTHER = {"fwd": "bwd", "bwd": "fwd"}
 _TORCH = None
@@ -1102,6 +987,42 @@ def _autograd_out(rotate, direction, x, a, b, how):
         return _rotation_fn(False).apply(rotate, direction, x, a, b, how)
     return _rotated_new(rotate, direction, x, a, b, how)
 
+
+def _rotate_tables(direction, x, r1, r2, mode, partial_slice, y=None):
+    """x rotated by tables in place, or into y."""
+    if y is None:
+        _call(direction, x, r1, r2, mode, partial_slice, None)
+    else:
+        _call_out(direction, y, x, r1, r2, mode, partial_slice, None)
+
+
+def _tables_how(rotary_mode, partial_slice):
+    return rotary_mode, None if partial_slice is None else (int(partial_slice[0]), int(partial_slice[1]))
+
+
+def inplace_partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None) -> None:
+    """In-place partial RoPE that records itself for autograd when x needs a
+    gradient, and calls the forward entry point directly otherwise.
+
+    x must not be a leaf tensor that requires grad: in-place changes to such
+    a tensor are illegal in autograd, so rotate a non-leaf copy (y = x * 1.0),
+    as the training example on the page does. r1 and r2 never get gradients.
+    Differentiable any number of times and in forward mode.
+    """
+    _autograd_inplace("inplace_partial_rotary_mul", _rotate_tables, x, r1, r2, _tables_how(rotary_mode, partial_slice))
+
+
+def partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None):
+    """Out-of-place partial RoPE: returns a new contiguous tensor holding x
+    with ``x[..., start:end)`` rotated; x is not modified. Records itself for
+    autograd (the backward is the out-of-place backward entry point) and
+    works on leaf tensors too, so a training step needs no ``x * 1.0`` copy
+    before the in-place op. Differentiable any number of times and in forward
+    mode. r1 and r2 never get gradients."""
+    return _autograd_out(_rotate_tables, "fwd", x, r1, r2, _tables_how(rotary_mode, partial_slice))
+
+
+# ---------------------------------------------------------------- autograd, cos/sin from positions
 
 def _pos_how(rotary_mode, partial_slice, table_dtype, pair_axes=None):
     sl = None if partial_slice is None else (int(partial_slice[0]), int(partial_slice[1]))
