@@ -892,6 +892,13 @@ def _differentiated(x):
     return x.requires_grad and enabled() or fw._current_level >= 0 and fw.unpack_dual(x).tangent is not None
 
 
+def _changed(*tensors):
+    """Move the version counters of tensors that a call wrote in place unseen
+    by autograd, so that a backward which needs an old value raises."""
+    import torch
+    torch.autograd.graph.increment_version(tensors)
+
+
 def _rotated_new(rotate, direction, x, a, b, how):
     """A new contiguous tensor holding x with its slice rotated. x is never
     modified (as an incoming gradient, autograd may hand it to other
@@ -975,6 +982,7 @@ def _rotation_fn(inplace):
 def _autograd_inplace(name, rotate, x, a, b, how):
     if not _differentiated(x):
         rotate("fwd", x, a, b, *how)
+        _changed(x)
         return
     if x.is_leaf and x.requires_grad and _TORCH[0]():
         raise RuntimeError(f"{name}: x is a leaf tensor that requires grad; "
