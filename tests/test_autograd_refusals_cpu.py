@@ -17,6 +17,7 @@ def no_library(monkeypatch):
             return lambda *a: rp.ROPE_OK
 
     monkeypatch.setattr(rp, "library", Library)
+    monkeypatch.setattr(rp, "_words_entry", lambda name: getattr(Library(), name))
     for name in ("_call", "_call_pos"):
         monkeypatch.setattr(rp, name, lambda *a, **k: None)
 
@@ -39,3 +40,59 @@ def test_unrecorded_rotations_in_place_are_seen(no_library):
                 y.sum().backward()
         with torch.inference_mode():
             rotate(torch.zeros(B, S, N, D))
+
+
+def cache_operands(**kw):
+    bf = torch.bfloat16
+    a = dict(q=torch.zeros(B, S, 3, D, dtype=bf), k=torch.zeros(B, S, N, D, dtype=bf), v=torch.zeros(B, S, N, D, dtype=bf),
+             data=torch.zeros(2, 4, N, D, dtype=bf), out=torch.zeros(B, S, N, D, dtype=bf))
+    a.update(kw)
+    return a
+
+
+def as_on_a_gpu(monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(rp, "_on_device", lambda t, stream: (None, rp._NOTHING))
+
+
+def write(a):
+    c = rp.RopeCache(a["data"])
+    v_cache = rp.RopeCache(torch.zeros(2, 4, N, D, dtype=torch.int8), torch.zeros(2, 4, N, 1))
+    rp.rope_cache_write(a["k"], a["v"], c, v_cache, torch.zeros(B, S, dtype=torch.int64), q=a["q"])
+
+
+def read(a):
+    rp.rope_cache_read(a["out"], rp.RopeCache(a["data"]), torch.zeros(B, 1, dtype=torch.int32),
+                       torch.zeros(B, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("call, names", [(write, ("q", "k", "v", "data")), (read, ("out", "data"))])
+def test_cache_calls_refuse_what_needs_a_gradient(call, names, no_library, monkeypatch):
+    as_on_a_gpu(monkeypatch)
+    call(cache_operands())
+    for name in names:
+        a = cache_operands()
+        a[name].requires_grad_()
+        with pytest.raises(RuntimeError, match="needs a gradient"):
+            call(a)
+        with torch.no_grad():
+            call(a)
+        with torch.inference_mode():
+            call(cache_operands())
+        a[name] = a[name].detach()
+        call(a)
+        with torch.autograd.forward_ad.dual_level(), torch.no_grad():
+            a[name] = torch.autograd.forward_ad.make_dual(a[name], torch.ones_like(a[name]))
+            with pytest.raises(RuntimeError, match="needs a gradient"):
+                call(a)
+
+
+@pytest.mark.parametrize("call, name", [(write, "q"), (write, "data"), (read, "out")])
+def test_cache_calls_in_place_are_seen(call, name, no_library, monkeypatch):
+    as_on_a_gpu(monkeypatch)
+    a = cache_operands()
+    w = torch.ones_like(a[name], requires_grad=True)
+    y = w * a[name]
+    call(a)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()

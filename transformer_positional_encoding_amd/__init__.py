@@ -201,6 +201,16 @@ def _arr4(v):
         return _I64x4(*[int(t) for t in v])     # other integer types
 
 
+@functools.lru_cache(maxsize=None)
+def _words_entry(name):
+    """A cache entry point whose structures are given as arrays of words, which
+    ctypes passes on without a conversion in Python."""
+    L = library()
+    f = getattr(L, name)
+    types = [ctypes.c_void_p if t is _StructPointer else t for t in f.argtypes]
+    return ctypes.CFUNCTYPE(f.restype, *types)((name, L))
+
+
 @functools.lru_cache(maxsize=64)
 def _i32_array(values: tuple):
     """A tuple of ints as a C int32 array (the same array for the same
@@ -882,21 +892,35 @@ _OTHER = {"fwd": "bwd", "bwd": "fwd"}
 _TORCH = None
 
 
-def _differentiated(x):
-    """Whether autograd follows x: it needs a gradient, or has a tangent."""
+def _autograd():
+    """torch's test of enabled gradients, its forward mode, and what moves the
+    version counters of tensors written in place unseen by autograd (so that a
+    backward which needs an old value raises)."""
     global _TORCH
     if _TORCH is None:
         import torch
-        _TORCH = (torch.is_grad_enabled, torch.autograd.forward_ad)
-    enabled, fw = _TORCH
+        _TORCH = torch.is_grad_enabled, torch.autograd.forward_ad, torch._C._increment_version
+    return _TORCH
+
+
+def _differentiated(x):
+    """Whether autograd follows x: it needs a gradient, or has a tangent."""
+    enabled, fw, _ = _TORCH or _autograd()
     return x.requires_grad and enabled() or fw._current_level >= 0 and fw.unpack_dual(x).tangent is not None
 
 
-def _changed(*tensors):
-    """Move the version counters of tensors that a call wrote in place unseen
-    by autograd, so that a backward which needs an old value raises."""
-    import torch
-    torch.autograd.graph.increment_version(tensors)
+def _refuse_differentiated(call, names, tensors):
+    """A call that gives no gradient takes no tensor that needs one. names: of
+    the first tensors; the rest belong to caches."""
+    enabled, fw, _ = _TORCH or _autograd()
+    dual = fw._current_level >= 0
+    if not dual and not enabled():
+        return
+    for i, t in enumerate(tensors):
+        if t is not None and (t.requires_grad or dual) and _differentiated(t):
+            name = names[i] if i < len(names) else "the cache"
+            raise RuntimeError(f"{call}: {name} needs a gradient, which this call does not give; call it under "
+                               "torch.no_grad() or with a detached tensor")
 
 
 def _rotated_new(rotate, direction, x, a, b, how):
@@ -982,7 +1006,7 @@ def _rotation_fn(inplace):
 def _autograd_inplace(name, rotate, x, a, b, how):
     if not _differentiated(x):
         rotate("fwd", x, a, b, *how)
-        _changed(x)
+        _TORCH[2]((x,))
         return
     if x.is_leaf and x.requires_grad and _TORCH[0]():
         raise RuntimeError(f"{name}: x is a leaf tensor that requires grad; "
@@ -1187,7 +1211,7 @@ class RopeCache:
     quantised formats: lane j of a row stands for code[j] * scale[j // group].
     """
 
-    __slots__ = ("data", "scales", "device", "words")
+    __slots__ = ("data", "scales", "device", "words", "tensors")
 
     def __init__(self, data, scales=None):
         import torch
@@ -1201,6 +1225,7 @@ class RopeCache:
         if s3 != 1 and dim > 1:
             raise ValueError("data: the lanes of a row must be consecutive")
         self.data, self.scales, self.device = data, scales, data.device
+        self.tensors = (data,) if scales is None else (data, scales)
         if fmt < 3:
             if scales is not None:
                 raise ValueError(f"a {data.dtype} cache has no scales")
@@ -1264,6 +1289,24 @@ def _rows(name, t):
     return _RowsWords(t.data_ptr(), n, d, sb, ss, sn)
 
 
+def _rows_beside(name, t, B, S, dtype, dev):
+    """The rows of q or v beside those of k."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D torch.Tensor (B, S, heads, dim)")
+    if t.dtype != dtype:
+        raise TypeError("q, k and v must share a dtype")
+    b, s, n, d = t.shape
+    if b != B or s != S:
+        raise ValueError(f"{name} must have k's tokens")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    sb, ss, sn, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the lanes of a row must be consecutive")
+    return _RowsWords(t.data_ptr(), n, d, sb, ss, sn)
+
+
 def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, dtype_code, device):
     """The C arguments from positions to partial_slice of a cache call, and
     the tensors that have to be on `device`."""
@@ -1282,14 +1325,13 @@ def _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table
     if positions is None or partial_slice is None:
         return (None, None, None, None, None, tdt, mode, None)
     start, end = int(partial_slice[0]), int(partial_slice[1])
-    for name, t in (("positions", positions), ("inv_freq", inv_freq)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}")
-    if positions.dtype != torch.int64 or positions.dim() not in (2, 3):
-        raise ValueError("positions must be an int64 tensor (B or 1, S), or (A, B or 1, S) with pair_axes")
+    if not (isinstance(positions, torch.Tensor) and isinstance(inv_freq, torch.Tensor)):
+        raise TypeError("positions and inv_freq must be torch.Tensors")
+    if positions.device != device or inv_freq.device != device:
+        raise ValueError(f"positions and inv_freq must be on {device}")
     shape, st = positions.shape, positions.stride()
+    if positions.dtype != torch.int64 or len(st) not in (2, 3):
+        raise ValueError("positions must be an int64 tensor (B or 1, S), or (A, B or 1, S) with pair_axes")
     if len(st) == 2:
         if pair_axes is not None:
             raise ValueError("pair_axes goes with positions (A, B or 1, S)")
@@ -1328,26 +1370,23 @@ def rope_cache_write(k, v, k_cache, v_cache, slots, positions=None, inv_freq=Non
 
     The rotation is fp32 and k is not rounded before it is quantised: for
     each group of lanes scale = largest finite magnitude / Q (448 for e4m3,
-    127, 7), code = k / scale rounded once to the nearest, ties to even."""
+    127, 7), code = k / scale rounded once to the nearest, ties to even.
+
+    No gradient passes through the call: it refuses q, k, v and caches that
+    need one (while gradients are enabled). Their changes in place are seen by
+    a backward that needs the old values."""
     import torch
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a 4-D torch.Tensor (B, S, heads, dim)")
     if k.numel() and not k.is_cuda:
         raise ValueError("k must be a GPU tensor")
-    code, dev, dtype = _dtype_code(k), k.device, k.dtype
-    B, S, _, _ = k.shape
-    for name, t in (("v", v), ("q", q)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{name} must be a 4-D torch.Tensor (B, S, heads, dim)")
-        if t.dtype != dtype:
-            raise TypeError("q, k and v must share a dtype")
-        b, s, _, _ = t.shape
-        if b != B or s != S:
-            raise ValueError(f"{name} must have k's tokens")
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
+    code, dev = _dtype_code(k), k.device
+    B, S, n, d = k.shape
+    sb, ss, sn, sd = k.stride()
+    if sd != 1 and d > 1:
+        raise ValueError("k: the lanes of a row must be consecutive")
+    rows_v = None if v is None else _rows_beside("v", v, B, S, k.dtype, dev)
+    rows_q = None if q is None else _rows_beside("q", q, B, S, k.dtype, dev)
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
     if not isinstance(k_cache, RopeCache) or not (v_cache is None or isinstance(v_cache, RopeCache)):
@@ -1359,15 +1398,18 @@ def rope_cache_write(k, v, k_cache, v_cache, slots, positions=None, inv_freq=Non
         raise ValueError("slots must be an int64 tensor (B, S)")
     if slots.device != dev:
         raise ValueError(f"slots must be on {dev}")
+    written = k_cache.tensors if v_cache is None else k_cache.tensors + v_cache.tensors
+    _refuse_differentiated("rope_cache_write", "kvq", (k, v, q) + written)
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
     handle, current = _on_device(k, stream)
     with current:
-        st = library().rope_cache_write(
-            B, S, code, None if q is None else _rows("q", q), _rows("k", k), None if v is None else _rows("v", v),
-            k_cache.words, None if v_cache is None else v_cache.words, slots.data_ptr() or None,
+        st = _words_entry("rope_cache_write")(
+            B, S, code, rows_q, _RowsWords(k.data_ptr(), n, d, sb, ss, sn), rows_v, k_cache.words,
+            None if v_cache is None else v_cache.words, slots.data_ptr() or None,
             _I64x2(*slots.stride()), *turn, 1 if rotate_k else 0, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
+    _TORCH[2](written if q is None else written + (q,))
 
 
 def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=None, inv_freq=None,
@@ -1386,7 +1428,10 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
     block_table[b, t // page_size].
     lengths: int32 (B); starts: int32 (B), 0 when None.
     positions, inv_freq, pair_axes: as in :func:`rope_cache_write`, for out's
-    rows."""
+    rows.
+
+    No gradient passes through the call: out and a cache that need one are
+    refused (while gradients are enabled)."""
     import torch
     if not isinstance(out, torch.Tensor) or out.dim() != 4:
         raise ValueError("out must be a 4-D torch.Tensor (B, S, heads, dim)")
@@ -1412,15 +1457,17 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
             raise ValueError(f"{name} must be on {dev}")
     if block_table.device != dev:
         raise ValueError(f"block_table must be on {dev}")
+    _refuse_differentiated("rope_cache_read", ("out",), (out,) + cache.tensors)
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
     handle, current = _on_device(out, stream)
     with current:
-        st = library().rope_cache_read(
+        st = _words_entry("rope_cache_read")(
             B, S, code, _rows("out", out), cache.words, block_table.data_ptr() or None, block_table.shape[1],
             block_table.stride(0), lengths.data_ptr() or None, None if starts is None else starts.data_ptr() or None,
             *turn, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
+    _TORCH[2]((out,))
 
 
 def rope_proj_fwd(x, w, r1, r2, heads: int, rotary_mode="interleave", partial_slice=None, out=None,
