@@ -96,3 +96,33 @@ def test_cache_calls_in_place_are_seen(call, name, no_library, monkeypatch):
     call(a)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def project(a):
+    return rp.rope_proj_lora_fwd(heads=2, partial_slice=(0, 32), **a)
+
+
+def lora_operands():
+    bf = torch.bfloat16
+    return dict(x=torch.zeros(6, 64, dtype=bf), w=torch.zeros(64, 64, dtype=bf), a=torch.zeros(3, 8, 64, dtype=bf),
+                b=torch.zeros(3, 64, 8, dtype=bf), adapters=torch.zeros(6, dtype=torch.int32),
+                r1=torch.zeros(1, 6, 1, 32, dtype=bf), r2=torch.zeros(1, 6, 1, 32, dtype=bf), scales=torch.ones(3),
+                out=torch.zeros(1, 6, 2, 32, dtype=bf), workspace=torch.zeros(1024, dtype=torch.uint8))
+
+
+def test_the_projection_with_adapters_refuses_what_needs_a_gradient(no_library, monkeypatch):
+    as_on_a_gpu(monkeypatch)
+    project(lora_operands())
+    for name in ("x", "w", "a", "b", "r1", "r2", "scales", "out"):
+        a = lora_operands()
+        a[name].requires_grad_()
+        with pytest.raises(RuntimeError, match=f"{name} needs a gradient"):
+            project(a)
+        with torch.no_grad():
+            project(a)
+    w = torch.ones(1, 6, 2, 32, requires_grad=True)
+    a = lora_operands()
+    y = w.bfloat16() * a["out"]
+    project(a)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()

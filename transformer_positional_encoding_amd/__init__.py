@@ -1555,7 +1555,8 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
     workspace: a contiguous GPU tensor of at least
     ``rope_proj_lora_workspace(tokens, K, rank)`` bytes, 16-byte aligned, that
     no other call uses meanwhile; None allocates one.
-    Returns ``out`` (allocated when None)."""
+    Returns ``out`` (allocated when None). No gradient passes through the call:
+    tensors that need one are refused (while gradients are enabled)."""
     import torch
     if isinstance(rotary_mode, str):
         if rotary_mode not in MODES:
@@ -1581,6 +1582,8 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
     if scales is not None and (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or
                                scales.shape != a.shape[:1]):
         raise ValueError("scales must be a float32 tensor (count)")
+    _refuse_differentiated("rope_proj_lora_fwd", ("x", "w", "a", "b", "r1", "r2", "scales", "out"),
+                           (x, w, a, b, r1, r2, scales, out))
     y_shape = (B, S, heads, N // heads)
     dev = x.device
     count, rank = a.shape[0], a.shape[1]
@@ -1619,4 +1622,5 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
             workspace.numel() * workspace.element_size(), handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
+    _TORCH[2]((out,))
     return out
