@@ -1301,6 +1301,8 @@ def _rows_beside(name, t, B, S, dtype, dev):
         raise ValueError(f"{name} must have k's tokens")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
+    if not t.is_cuda and t.numel():
+        raise ValueError(f"{name} must be a GPU tensor")
     sb, ss, sn, sd = t.stride()
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the lanes of a row must be consecutive")
