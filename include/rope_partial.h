@@ -693,7 +693,10 @@ typedef struct rope_lora {
  * multiple of 8 (ROPE_ERR_INVALID) or above ROPE_LORA_RANK_MAX
  * (ROPE_ERR_UNSUPPORTED), count or rank 0 is a projection without adapters;
  * NULL a, b, adapters or workspace; a, b or workspace not 16-byte aligned,
- * sizes beyond 64 bits, too small a workspace (ROPE_ERR_INVALID).
+ * sizes beyond 64 bits, too small a workspace, y overlapping a, b, adapters,
+ * scales or the workspace, the workspace overlapping any input (ROPE_ERR_INVALID;
+ * of a larger workspace only the bytes it has to hold count); and, after the
+ * tables' own checks, y or the workspace overlapping a table.
  * Asynchronous on `stream`; nothing is allocated; deterministic.
  */
 ROPE_API rope_status_t rope_proj_lora_fwd(

@@ -4,6 +4,7 @@
 #include "rope_plan.hpp"
 
 #include <algorithm>
+#include <initializer_list>
 #include <limits>
 
 namespace rope {
@@ -397,8 +398,32 @@ int64_t lora_workspace_bytes(int64_t M, int64_t rank)
 
 namespace {
 
-// The adapters and workspace of an M x N projection over K.
-rope_status_t check_lora(const LoraCheck& c, int64_t M, int64_t N, int64_t K, std::string* why)
+// `bytes` of memory from p on, by name.
+struct Span {
+    const char* name;
+    const void* p;
+    uint64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b)
+{
+    const uintptr_t au = reinterpret_cast<uintptr_t>(a.p), bu = reinterpret_cast<uintptr_t>(b.p);
+    return (au >= bu && (uint64_t)(au - bu) < b.bytes) || (bu >= au && (uint64_t)(bu - au) < a.bytes);
+}
+
+// `written` shares no byte with any of `others`.
+rope_status_t check_apart(const Span& written, std::initializer_list<Span> others, std::string* why)
+{
+    for (const Span& o : others)
+        if (o.p != nullptr && overlap(written, o))
+            return fail(ROPE_ERR_INVALID, why, std::string(written.name) + " overlaps " + o.name);
+    return ROPE_OK;
+}
+
+// The adapters and workspace of an M x N projection over K; *space: the bytes
+// of the workspace in use.
+rope_status_t check_lora(const LoraCheck& c, int64_t M, int64_t N, int64_t K, const Span& y, const Span& x,
+                         const Span& w, Span* space, std::string* why)
 {
     if (c.lora == nullptr) return fail(ROPE_ERR_NULLPTR, why, "lora is NULL");
     const rope_lora_t& l = *c.lora;
@@ -424,7 +449,21 @@ rope_status_t check_lora(const LoraCheck& c, int64_t M, int64_t N, int64_t K, st
     if (need < 0 || c.workspace_bytes < need)
         return fail(ROPE_ERR_INVALID, why, "workspace holds " + std::to_string(c.workspace_bytes) + " bytes, needs "
                                                + std::to_string(need));
-    return ROPE_OK;
+    // y is written while other blocks still read the adapters, and the
+    // workspace before the inputs are read
+    const Span a{"lora a", l.a, (uint64_t)na}, b{"lora b", l.b, (uint64_t)nb};
+    const Span ids{"lora adapters", l.adapters, 4 * (uint64_t)M}, scales{"lora scales", l.scales, 4 * (uint64_t)l.count};
+    *space = Span{"workspace", c.workspace, (uint64_t)need};
+    rope_status_t st = check_apart(y, {a, b, ids, scales, *space}, why);
+    return st != ROPE_OK ? st : check_apart(*space, {x, w, a, b, ids, scales}, why);
+}
+
+// The bytes that a checked table's strides reach (its last lane's offset fits 64 bits).
+Span table_span(const void* r, const int64_t t[3], const Plan& p)
+{
+    const uint64_t last = (uint64_t)((p.B - 1) * t[0] + (p.S - 1) * t[1] + (p.N - 1) * t[2] + p.L - 1);
+    const uint64_t most = std::numeric_limits<uint64_t>::max() / (uint64_t)p.tesize;
+    return Span{"a table", r, std::min(last + 1, most) * (uint64_t)p.tesize};
 }
 
 }  // namespace
@@ -481,17 +520,18 @@ rope_status_t make_proj_plan(void* y, rope_dtype_t out_dtype, const void* x, con
     // the kernel addresses x and w with 32-bit element offsets
     if (M * K >= (int64_t(1) << 31) || N * K >= (int64_t(1) << 31))
         return fail(ROPE_ERR_UNSUPPORTED, why, "x and w must each hold fewer than 2^31 elements");
-    const auto overlap = [](const void* a, uint64_t na, const void* b, uint64_t nb) {
-        const uintptr_t au = reinterpret_cast<uintptr_t>(a), bu = reinterpret_cast<uintptr_t>(b);
-        return (au >= bu && (uint64_t)(au - bu) < nb) || (bu >= au && (uint64_t)(bu - au) < na);
-    };
-    const uint64_t y_bytes = (uint64_t)q.rope.bytes;
-    if (overlap(y, y_bytes, x, (uint64_t)x_bytes) || overlap(y, y_bytes, w, (uint64_t)w_bytes))
-        return fail(ROPE_ERR_INVALID, why, "y overlaps x or w");
-    if (lora != nullptr && (st = check_lora(*lora, M, N, K, why)) != ROPE_OK) return st;
+    const Span ys{"y", y, (uint64_t)q.rope.bytes}, xs{"x", x, (uint64_t)x_bytes}, ws{"w", w, (uint64_t)w_bytes};
+    if (overlap(ys, xs) || overlap(ys, ws)) return fail(ROPE_ERR_INVALID, why, "y overlaps x or w");
+    Span space{"workspace", nullptr, 0};
+    if (lora != nullptr && (st = check_lora(*lora, M, N, K, ys, xs, ws, &space, why)) != ROPE_OK) return st;
     if (q.rope.L > 0) {
         st = check_tables(y_shape, r1, r1_shape, r1_strides, r2, r2_shape, r2_strides, &q.rope, why);
         if (st != ROPE_OK) return st;
+    }
+    if (lora != nullptr && q.rope.L > 0) {
+        const Span t1 = table_span(r1, q.rope.t1, q.rope), t2 = table_span(r2, q.rope.t2, q.rope);
+        if ((st = check_apart(ys, {t1, t2}, why)) != ROPE_OK) return st;
+        if (space.p != nullptr && (st = check_apart(space, {t1, t2}, why)) != ROPE_OK) return st;
     }
     q.x = x;
     q.w = w;
