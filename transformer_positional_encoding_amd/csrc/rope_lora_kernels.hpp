@@ -65,11 +65,21 @@ __device__ __forceinline__ void widen8(const v4u& q, float (&f)[8])
 // each, the counts are summed over adapters and waves, and the waves place
 // their tokens, a token's rank among its 64 from the ballots of its adapter's
 // bits. No order of execution enters the result.
+// Lanes of a wave hand counts and places to one another through LDS; the
+// hardware keeps a wave's LDS accesses in order, and wave_lds() tells the
+// compiler that other lanes' reads and writes lie on either side.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortBins = kLoraSortAdapters + 1;   // and one for none
 constexpr int kSortKept = 16;                      // tokens a lane keeps in registers: 16384 tokens in all
+
+__device__ __forceinline__ void wave_lds()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int32_t* ids, int32_t count, int32_t M,
                                                                      int32_t* order, int32_t* group_ids, int32_t* rows)
@@ -111,6 +121,7 @@ __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int3
     const auto add = [&](int64_t m, int32_t k) {
         const uint64_t same = alike(m < end, k);
         if (m < end && (same & ((1ull << lane) - 1)) == 0) at[wave][k] += __popcll(same);
+        wave_lds();
     };
 #pragma unroll
     for (int i = 0; i < kSortKept; ++i)
@@ -155,14 +166,15 @@ __global__ void __launch_bounds__(kSortThreads) rope_lora_sort_kernel(const int3
     __syncthreads();
     const auto place = [&](int64_t m, int32_t k) {                       // by the whole wave
         const uint64_t same = alike(m < end, k);
+        const int32_t to = m < end ? at[wave][k] + __popcll(same & ((1ull << lane) - 1)) : 0;
+        wave_lds();
         if (m < end) {
-            const int32_t to = at[wave][k] + __popcll(same & ((1ull << lane) - 1));
             order[to] = (int32_t)m;
             if ((to & 31) == 0) group_ids[to / 32] = k == count ? -1 : k;
-            // the adapter's last token of the 64 moves its place on: after
-            // every read of it, a wave's LDS accesses being in order
+            // the adapter's last token of the 64 moves its place on
             if ((same >> lane) == 1) at[wave][k] = to + 1;
         }
+        wave_lds();
     };
 #pragma unroll
     for (int i = 0; i < kSortKept; ++i)
