@@ -744,6 +744,25 @@ ROPE_API rope_status_t rope_proj_launch_info(
     rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
     int64_t info[ROPE_LAUNCH_INFO_LEN]);
 
+/* Kernels of a projection with adapters beside its tiles (rope_proj_lora_launch_info). */
+#define ROPE_KERNEL_PROJ_FEW 6     /* units of 32 output lanes by up to 64 tokens, unsorted */
+#define ROPE_KERNEL_PROJ_GENERAL 7 /* 16 tokens of one head, any slice, unsorted */
+
+/*
+ * rope_proj_lora_launch_info -- the launch plan rope_proj_lora_fwd would use
+ * for these arguments and `count` adapters of `rank`, for tests and profiling:
+ * as rope_proj_launch_info, with stand-ins for the adapters' pointers and the
+ * workspace too. info[0] ROPE_KERNEL_NONE, ROPE_KERNEL_PROJ_HEADS, _SQUARE,
+ * _FEW or _GENERAL; [1] to [6] as there ([1] a bound on the blocks with work
+ * where tokens are sorted); [7] 1 when the tokens are sorted by adapter first.
+ */
+ROPE_API rope_status_t rope_proj_lora_launch_info(
+    rope_dtype_t y_dtype, rope_dtype_t dtype, const int64_t y_shape[4], int64_t K, int64_t count, int64_t rank,
+    const void* r1, const int64_t r1_shape[4], const int64_t r1_strides[4],
+    const void* r2, const int64_t r2_shape[4], const int64_t r2_strides[4],
+    rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2],
+    int64_t info[ROPE_LAUNCH_INFO_LEN]);
+
 /* ============================== status ============================== */
 
 /* Static text for a status code; never NULL. */

@@ -173,6 +173,9 @@ def library() -> ctypes.CDLL:
         L.rope_proj_lora_fwd.restype = ctypes.c_int
         L.rope_proj_lora_fwd.argtypes = L.rope_proj_fwd.argtypes[:7] + [ctypes.POINTER(RopeLora)] + \
             _ENTRY_ARGTYPES[3:-1] + [vp, ctypes.c_int64, vp]
+        L.rope_proj_lora_launch_info.restype = ctypes.c_int
+        L.rope_proj_lora_launch_info.argtypes = [ctypes.c_int, ctypes.c_int, i64p, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.c_int64] + _ENTRY_ARGTYPES[3:-1] + [i64p]
         L.rope_proj_lora_workspace.restype = ctypes.c_int64
         L.rope_proj_lora_workspace.argtypes = [i64p, ctypes.c_int64, ctypes.c_int64]
         L.rope_proj_launch_info.restype = ctypes.c_int
@@ -425,7 +428,7 @@ def raw_proj_call(y_ptr, y_dtype: int, x_ptr, w_ptr, dtype: int, y_shape, K: int
                                    _arr4(r2_strides), table_dtype, mode, sl, stream)
 
 
-PROJ_KERNELS = {0: "none", 4: "heads", 5: "square"}
+PROJ_KERNELS = {0: "none", 4: "heads", 5: "square", 6: "few", 7: "general"}
 PROJ_EPILOGUES = {0: "general", 1: "vector", 2: "vector_partner"}
 
 
@@ -445,6 +448,23 @@ def raw_proj_launch_info(y_dtype: int, dtype: int, y_shape, K: int, r1_ptr, r1_s
     return st, {"kernel": PROJ_KERNELS.get(v[0], v[0]), "blocks": v[1], "threads": v[2], "tile_tokens": v[3],
                 "tile_lanes": v[4], "epilogue": PROJ_EPILOGUES.get(v[5], v[5]) if v[0] == 5 else None,
                 "tables_in_lds": bool(v[6])}
+
+
+def raw_proj_lora_launch_info(y_dtype: int, dtype: int, y_shape, K: int, count: int, rank: int, r1_ptr, r1_shape,
+                              r1_strides, r2_ptr, r2_shape, r2_strides, table_dtype: int, mode: int, partial_slice):
+    """rope_proj_lora_launch_info with plain integers and sequences (None =
+    NULL): (status, plan dict or None), as raw_proj_launch_info; "sorted": the
+    tokens are sorted by adapter first."""
+    sl = None if partial_slice is None else _I64x2(*partial_slice)
+    v = (ctypes.c_int64 * LAUNCH_INFO_LEN)()
+    st = library().rope_proj_lora_launch_info(int(y_dtype), int(dtype), _arr4(y_shape), int(K), int(count), int(rank),
+                                              r1_ptr, _arr4(r1_shape), _arr4(r1_strides), r2_ptr, _arr4(r2_shape),
+                                              _arr4(r2_strides), int(table_dtype), int(mode), sl, v)
+    if st != ROPE_OK:
+        return st, None
+    return st, {"kernel": PROJ_KERNELS.get(v[0], v[0]), "blocks": v[1], "threads": v[2], "tile_tokens": v[3],
+                "tile_lanes": v[4], "epilogue": PROJ_EPILOGUES.get(v[5], v[5]) if v[0] == 5 else None,
+                "tables_in_lds": bool(v[6]), "sorted": bool(v[7])}
 
 
 def last_error() -> str:

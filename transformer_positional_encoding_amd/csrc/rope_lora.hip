@@ -118,6 +118,16 @@ void launch_tiles_tt(const ProjLaunch& P, const ARGS& a, hipStream_t s)
     }
 }
 
+// Tokens of a block of the few-token kernel, in 16s.
+int few_tiles(int32_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+
+// Blocks of the general kernel.
+uint32_t head_blocks(const LoraLaunch& L)
+{
+    const uint64_t tiles = (uint64_t)((L.P.a.M + kHeadTokens - 1) / kHeadTokens) * (uint64_t)L.heads;
+    return (uint32_t)std::min<uint64_t>(tiles, kMaxGridItems / 256);
+}
+
 template <int DT, int MT>
 void launch_few(const FewArgs& a, int tdt, hipStream_t s)
 {
@@ -167,13 +177,13 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t s)
     } else if (L.few) {
         FewArgs f = L.units;
         static_cast<LoraProjArgs&>(f) = a;
-        if (a.M <= 16) launch_few<DT, 1>(f, L.P.tdt, s);
-        else if (a.M <= 32) launch_few<DT, 2>(f, L.P.tdt, s);
-        else launch_few<DT, 4>(f, L.P.tdt, s);
+        switch (few_tiles(a.M)) {
+        case 1: launch_few<DT, 1>(f, L.P.tdt, s); break;
+        case 2: launch_few<DT, 2>(f, L.P.tdt, s); break;
+        default: launch_few<DT, 4>(f, L.P.tdt, s); break;
+        }
     } else {
-        const uint64_t tiles = (uint64_t)((a.M + kHeadTokens - 1) / kHeadTokens) * (uint64_t)L.heads;
-        hipLaunchKernelGGL((rope_lora_head_kernel<DT>), dim3((uint32_t)std::min<uint64_t>(tiles, kMaxGridItems / 256)),
-                           dim3(256), 0, s, a, L.P.tdt, L.heads);
+        hipLaunchKernelGGL((rope_lora_head_kernel<DT>), dim3(head_blocks(L)), dim3(256), 0, s, a, L.P.tdt, L.heads);
     }
     return hipGetLastError();
 }
@@ -203,6 +213,51 @@ rope_status_t rope_proj_lora_fwd(
                                                            : rope::launch_lora<ROPE_DTYPE_F16>(L, s);
     if (err != hipSuccess)
         return rope::set_error(ROPE_ERR_RUNTIME, std::string("kernel launch: ") + hipGetErrorString(err));
+    return ROPE_OK;
+}
+
+rope_status_t rope_proj_lora_launch_info(rope_dtype_t y_dtype, rope_dtype_t dtype, const int64_t y_shape[4], int64_t K,
+                                         int64_t count, int64_t rank, const void* r1, const int64_t r1_shape[4],
+                                         const int64_t r1_strides[4], const void* r2, const int64_t r2_shape[4],
+                                         const int64_t r2_strides[4], rope_dtype_t table_dtype, int64_t mode,
+                                         const int64_t partial_slice[2], int64_t info[ROPE_LAUNCH_INFO_LEN])
+{
+    if (info == nullptr) return rope::set_error(ROPE_ERR_NULLPTR, "info is NULL");
+    for (int i = 0; i < ROPE_LAUNCH_INFO_LEN; ++i) info[i] = 0;
+    // distinct, 16-byte aligned stand-ins, never dereferenced
+    const auto nowhere = [](int i) { return reinterpret_cast<void*>(uint64_t(i) << 60); };
+    const rope_lora_t lora{nowhere(5), nowhere(8), static_cast<const int32_t*>(nowhere(11)), nullptr, count, rank};
+    rope::LoraLaunch L;
+    std::string why;
+    rope_status_t st = rope::prepare_lora(nowhere(2), y_dtype, nowhere(3), nowhere(4), dtype, y_shape, K, &lora, r1,
+                                          r1_shape, r1_strides, r2, r2_shape, r2_strides, table_dtype, mode,
+                                          partial_slice, nowhere(12), int64_t(1) << 60, &L, &why);
+    if (st != ROPE_OK) return rope::set_error(st, why);
+    const rope::ProjLaunch& P = L.P;
+    if (P.q.noop) return ROPE_OK;
+    if (L.tiles) {
+        info[0] = P.sq ? ROPE_KERNEL_PROJ_SQUARE : ROPE_KERNEL_PROJ_HEADS;
+        info[1] = P.grid;
+        info[2] = P.threads;
+        info[3] = P.BM;
+        info[4] = P.BN;
+        info[5] = P.sq && P.a.epi >= 0 ? 1 + P.a.epi : 0;
+        info[6] = P.sq && P.a.epi >= 0 && P.q.rope.L > 0 && P.a.tab_crl >= 0 ? 1 : 0;
+        info[7] = L.l.count > 0 ? 1 : 0;
+    } else if (L.few) {
+        const int64_t tokens = 16 * rope::few_tiles(P.a.M);
+        info[0] = ROPE_KERNEL_PROJ_FEW;
+        info[1] = P.a.N / 32 * ((P.a.M + tokens - 1) / tokens);
+        info[2] = 64 * rope::kFewWaves;
+        info[3] = tokens;
+        info[4] = 32;
+    } else {
+        info[0] = ROPE_KERNEL_PROJ_GENERAL;
+        info[1] = rope::head_blocks(L);
+        info[2] = 256;
+        info[3] = rope::kHeadTokens;
+        info[4] = P.a.Dh;
+    }
     return ROPE_OK;
 }
 
