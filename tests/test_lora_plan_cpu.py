@@ -41,3 +41,14 @@ def test_null_info():
     L = rp.library()
     assert L.rope_proj_lora_launch_info(2, 2, None, 0, 0, 0, None, None, None, None, None, None, 2, 1, None,
                                         None) == rp.ROPE_ERR_NULLPTR
+
+
+@pytest.mark.parametrize("M, K, N, R, few", [
+    (6000, 2048, 192, 8, True), (6000, 2048, 192, 16, False), (6000, 2048, 192, 128, False), (1280, 1536, 192, 128, True),
+    (2560, 1536, 192, 128, False), (640, 1536, 576, 128, True), (1280, 1536, 576, 128, False), (2560, 512, 576, 8, True),
+    (640, 1536, 2048, 8, True), (640, 1536, 2048, 32, True), (640, 1536, 2048, 128, False), (1280, 1536, 2048, 8, False),
+    (160, 4096, 5120, 128, True), (320, 4096, 5120, 128, False), (64, 1536, 24576, 128, True), (65, 1536, 24576, 8, False),
+])
+def test_rank_and_tokens_decide_for_tiles(M, K, N, R, few):
+    """The kernel that was measured to be the faster one at these sizes."""
+    assert plan(M, K, N // 64, 64, R=R, sl=(0, 64))[1]["kernel"] == ("few" if few else "square")

@@ -72,3 +72,59 @@ def test_tiles_of_whole_heads_and_of_parts(M, K, H, Dh, sl, dtype, out):
     assert plan(c, H, sl, "interleave", torch.float32, rp.DTYPE_CODES[out]) == ("heads", True)
     cos, sin = tables(M, sl[1] - sl[0], "interleave", "f32", 6)
     check(run(c, cos, sin, H, "interleave", sl, out), c, cos, sin, H, "interleave", sl, out, "tiles")
+
+
+@pytest.mark.parametrize("K, kernel", [(128, "square"), (192, "heads")])
+def test_tiles_with_tables_per_batch_and_per_head(K, kernel):
+    B, S, H = 2, 700, 40
+    M = B * S
+    c = make(M, K, H, 64, 16, 3, "bf16", seed=4, ids="mixed")
+    assert plan(c, H, (0, 64), "rotate_half") == (kernel, True)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for heads in (H, 1):
+        cos, sin = (torch.randn(B, S, heads, 64, generator=g, device="cuda") for _ in range(2))
+        got = rp.rope_proj_lora_fwd(c["x"].view(B, S, K), c["w"], c["a"], c["b"], c["ids"].view(B, S), cos, sin, H,
+                                    "rotate_half", (0, 64), scales=c["scales"])
+        flat = lambda t: t.reshape(1, M, -1, 64)  # noqa: E731
+        check(flat(got), c, flat(cos), flat(sin), H, "rotate_half", (0, 64), "bf16", f"tables of {heads} heads")
+
+
+@pytest.mark.parametrize("K, kernel", [(128, "square"), (192, "heads")])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tiles_keep_what_is_not_finite_with_its_tokens(K, kernel, dtype):
+    M, H = 1400, 40
+    c = make(M, K, H, 64, 16, 3, dtype, seed=8, ids="mixed")
+    assert plan(c, H, (0, 64), "interleave", torch.float32, 0) == (kernel, True)
+    cos, sin = tables(M, 64, "interleave", "f32", 2)
+    clean = run(c, cos, sin, H, "interleave", (0, 64), "f32")
+    check(clean, c, cos, sin, H, "interleave", (0, 64), "f32", "before")
+    c["x"][0, 1] = float("inf")
+    c["a"][2], c["b"][2] = float("nan"), float("inf")
+    got = run(c, cos, sin, H, "interleave", (0, 64), "f32")
+    keep = (torch.arange(M, device="cuda") != 1) & (c["ids"] != 2)
+    assert torch.equal(got[:, keep], clean[:, keep]) and not bool(torch.isfinite(got[:, ~keep]).any())
+
+
+@pytest.mark.parametrize("M, K, kernel", [(1313, 128, "square"), (1400, 192, "heads")])
+def test_tiles_write_nothing_past_the_result(M, K, kernel):
+    H = 40
+    c = make(M, K, H, 64, 8, 2, "bf16", seed=2, ids="mixed")
+    assert plan(c, H, (0, 64), "interleave") == (kernel, True)
+    cos, sin = tables(M, 64, "interleave", "bf16", 2)
+    n = M * H * 64
+    guarded = torch.full((n + 8192,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = guarded[4096:4096 + n].view(1, M, H, 64)
+    size = rp.rope_proj_lora_workspace(M, K, 8)
+    ws = torch.full((size + 64,), 9, dtype=torch.uint8, device="cuda")
+    run(c, cos, sin, H, "interleave", (0, 64), "bf16", out=out, workspace=ws[:size])
+    assert bool((guarded[:4096] == 7).all()) and bool((guarded[4096 + n:] == 7).all()) and bool((ws[-64:] == 9).all())
+
+
+@pytest.mark.parametrize("dtype, out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("A, ids", [(70, "runs"), (70, "mixed"), (1023, "mixed"), (1, "none")])
+def test_tiles_of_many_adapters(A, ids, dtype, out):
+    M, H, K = 1300, 24, 192
+    c = make(M, K, H, 96, 24, A, dtype, seed=A, ids=ids)
+    assert plan(c, H, (0, 96), "rotate_half", torch.float32, rp.DTYPE_CODES[out]) == ("heads", True)
+    cos, sin = tables(M, 96, "rotate_half", "f32", 6)
+    check(run(c, cos, sin, H, "rotate_half", (0, 96), out), c, cos, sin, H, "rotate_half", (0, 96), out, f"{A} adapters")

@@ -7,7 +7,7 @@ import torch
 import transformer_positional_encoding_amd as rp
 
 pytestmark = pytest.mark.gpu
-RANK, K, H, DH = 8, 64, 4, 64
+RANK, K, H, DH = 8, 64, 8, 64
 
 
 def want(ids, count):
@@ -37,6 +37,9 @@ def test_order(M, count, ids):
     none = torch.zeros(1, 1, 1, 0, device="cuda")
     ws = torch.full((rp.rope_proj_lora_workspace(M, K, RANK),), 0x55, dtype=torch.uint8, device="cuda")
     rows, groups = want(a, count)
+    st, plan = rp.raw_proj_lora_launch_info(2, 2, (1, M, H, DH), K, count, RANK, None, (1, 1, 1, 0), (0, 0, 0, 1), None,
+                                            (1, 1, 1, 0), (0, 0, 0, 1), 2, 1, None)
+    assert st == rp.ROPE_OK and plan["sorted"]
     places = M + 31 * min(count + 1, M) + 384
     for _ in range(3):
         rp.rope_proj_lora_fwd(x, w, la, lb, a.cuda(), none, none, H, workspace=ws)

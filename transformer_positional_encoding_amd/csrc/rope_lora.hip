@@ -14,15 +14,38 @@
 namespace rope {
 namespace {
 
-// Blocks of the few-token kernel (64 tokens by 32 output lanes) up to which it
-// is taken for more tokens than kLoraFewTokens too: it has no sort, and fills
-// the chip sooner. Measured on MI355X, rank 16, each token its own of 8
-// adapters, us here and on tiles: K 512, 512 lanes: 128 blocks 14 and 33, 512
-// blocks 24 and 35, 1024 blocks 48 and 37; K 1536, 2048 lanes: 256 blocks 21 and
-// 52, 512 blocks 33 and 52, 1024 blocks 61 and 52; K 2048, 5120 lanes: 640
-// blocks 56 and 58, 1280 blocks 89 and 58. (Up to 64 tokens the tiles are mostly
-// empty: K 1536, 24576 lanes, 64 tokens 47 and 60, 80 tokens 76 and 61.)
-constexpr int64_t kFewBlocks = 640;
+// Whether the few-token kernel (blocks of 64 tokens by 32 output lanes) is
+// taken for more tokens than kLoraFewTokens too: it has no sort and fills the
+// chip sooner, but its adapters' part, and h before it, are dot products that
+// grow with the rank R: it takes as long as blocks * (1 + R/192) + M * R/256
+// blocks without adapters would, and tiles as long as 960 of them. Measured on
+// MI355X (8 adapters, each token its own, weights from memory; us here and on
+// tiles, both with the launches before them):
+//   blocks:     R 8                     R 32                    R 128
+//   K 1536, 192 lanes:
+//     120       22, 61                  33, 64                  77, 81
+//     240       26, 61                  44, 65                  118, 90
+//     564       57, 66                  101, 70                 264, 105
+//   K 1536, 2048 lanes:
+//     320       31, 63                  40, 68                  75, 87
+//     640       42, 65                  57, 69                  113, 89
+//     1280      68, 64                  92, 67                  182, 88
+//   K 1536, 5120 lanes:
+//     480       31, 63                  39, 68                  71, 91
+//     800       55, 64                  71, 69                  128, 88
+// Without adapters 640 blocks of these take 34 and 45, 800 47 and 44, 1280 57
+// and 47. K of 512 and 4096 meet within a fifth of the same sums (2048 lanes, R
+// 128: 320 blocks 55 and 58, 121 and 155; 640 blocks 80 and 60, 186 and 158).
+// One adapter for all tokens is up to a quarter quicker here, 100 adapters up
+// to a third slower. Of 266 calls measured the rule picks the slower kernel for
+// 10, at worst 1.24 times the other's time. (Up to 64 tokens the tiles are
+// mostly empty: K 1536, 24576 lanes, 64 tokens, R 8 of 64 adapters 47 and 138,
+// one adapter of R 128 65 and 62, 64 of these 275 and 245; every narrower call
+// is quicker here.)
+bool few_for_more(int64_t blocks, int64_t M, int64_t R)
+{
+    return blocks * (768 + 4 * R) + 3 * M * R <= 960 * 768;
+}
 
 // A grid's second dimension counts the few-token kernel's 64-token blocks;
 // calls of more tokens that no tiled kernel takes go to the general one.
@@ -80,7 +103,8 @@ rope_status_t prepare_lora(void* y, rope_dtype_t y_dtype, const void* x, const v
     // adapters, sorted rows: their tiles for a bound on these
     const bool fits = L->P.sq || proj_groups_in_tiles(p.D, p.start, p.L, a.half);
     const int64_t few_blocks = (a.M + 63) / 64 * (a.N / 32);
-    L->tiles = fits && a.M > kLoraFewTokens && l.count <= kLoraSortAdapters && !(units && few_blocks <= kFewBlocks);
+    L->tiles = fits && a.M > kLoraFewTokens && l.count <= kLoraSortAdapters &&
+               !(units && few_for_more(few_blocks, a.M, l.R));
     if (L->tiles && l.count > 0) {
         const int64_t MB = (lora_row_bound(a.M, l.count) + L->P.BM - 1) / L->P.BM;
         if (MB * a.NB > (int64_t)(kMaxGridItems / (uint64_t)L->P.threads)) L->tiles = false;
