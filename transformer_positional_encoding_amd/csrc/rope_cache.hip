@@ -281,9 +281,15 @@ hipError_t launch_write(const CacheWritePlan& p, hipStream_t s)
                            args, 0, s);
 }
 
-// Whether a token of so many chunks fills a wave's passes more than three
-// quarters (as every token of more than 144 chunks does).
-bool read_by_wave(uint32_t chunks) { return 4 * chunks > 3 * 64 * ((chunks + 63) / 64); }
+// Whether a wave takes a token of so many chunks, with so many pairs to turn
+// (measured figures at the kernels): where the token is one full pass of the
+// wave, unless its lanes idle over the cos and sin of 32 pairs or fewer, or
+// enough passes that the last one's open lanes weigh little.
+bool read_by_wave(uint32_t chunks, uint32_t pairs)
+{
+    if (chunks == 64) return pairs == 0 || pairs > 32;
+    return chunks > (pairs == 0 ? 96u : 127u);
+}
 
 hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
 {
@@ -307,14 +313,14 @@ hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
         a.pairs_div = make_fastdiv(std::max<uint32_t>(1, a.turn.pairs));
         void* args[] = {&a};
         const int dt = p.rope.dtype;
-        const bool wave = read_by_wave(a.token_chunks);
+        const bool wave = read_by_wave(a.token_chunks, p.rotate ? a.turn.pairs : 0);
         const void* fn = wave ? (p.rotate ? by_types<ReadWaveTurn>(dt, fmt) : by_types<ReadWave>(dt, fmt))
                               : (p.rotate ? by_types<ReadVecTurn>(dt, fmt) : by_types<ReadVec>(dt, fmt));
-        // (a wave's token has 49 chunks or more, so its grid fits as the block's)
+        // (a wave's token has 64 chunks or more, so its grid fits as the block's)
         const uint32_t block = kReadChunks * kVecThreads;
         const uint32_t grid = wave ? (a.tokens + 3) / 4 : (uint32_t)((items + block - 1) / block);
         // tokens that a block's chunks can span: at most 4 pairs for each of its
-        // chunks and of two tokens of 144, 25 KB of cos and sin
+        // chunks and of two tokens of 127, 25 KB of cos and sin
         const size_t spans = (block + a.token_chunks - 2) / a.token_chunks + 1;
         const size_t lds = !wave && p.rotate ? 2 * spans * a.turn.pairs * sizeof(float) : 0;
         return hipLaunchKernel(fn, dim3(grid), dim3(kVecThreads), args, lds, s);

@@ -704,14 +704,23 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWrit
 // ---------------------------------------------------------------------------
 // Read, vector form: bound by the bytes it moves. A token's N rows are N * D/8
 // chunks. A wave takes a whole token, so that its sequence, page and addresses
-// are scalar work, where the token fills the wave's passes of 64 chunks more
-// than three quarters; otherwise 512 consecutive chunks of the output go to a
-// block, two a thread whose loads go out together, each finding its token.
-// Measured on MI355X (134 million lanes of e4m3 to bf16, us; by waves and by
-// blocks): tokens of 16 chunks 256 and 99, 32: 156 and 98, 48: 117 and 98, 64: 92
-// and 98, 72 (a 576-lane latent): 123 and 98, 128: 77 and 101; with 32 pairs
-// turned, 48: 181 and 156, 64: 146 and 142, 72: 174 and 142, 128: 105 and 168 (one
-// chunk a thread). Blocks of one chunk a thread 121, of four 100.
+// are scalar work, where the token fills its passes of 64 chunks (below);
+// otherwise 512 consecutive chunks of the output go to a block, two a thread
+// whose loads go out together, each finding its token.
+// Measured on MI355X (e4m3 to bf16, 134 million lanes and, in brackets, 8
+// million; us by waves and by blocks, tokens of
+//   chunks    not turned               32 pairs turned          64 pairs turned
+//   16        258, 99 (18, 8.1)        468, 203 (34, 17)        470, 284 (33, 24)
+//   48        119, 101 (9.8, 8.2)      184, 159 (15, 13)        184, 180 (15, 15)
+//   56        105, 102 (9.2, 8.2)      165, 156 (14, 13)
+//   64        93, 99 (8.8, 8.2)        148, 145 (13, 12)        148, 163 (13, 14)
+//   72        124, 100 (10, 8.2)       176, 145 (16, 12)        184, 163 (16, 13)
+//   96        106, 101 (9.4, 8.2)      159, 143 (15, 12)        160, 158 (15, 13)
+//   112       95, 100 (9.0, 8.1)       142, 143 (14, 12)        142, 157 (14, 13)
+//   128       78, 99 (7.8, 8.2)        106, 140 (12, 12)        107, 144 (12, 12)
+//   144       84, 101 (8.0, 8.2)       117, 142 (12, 12)        117, 151 (12, 13)
+// and no further apart with the other formats.) Blocks of one chunk a thread 121
+// where two take 99, of four 100.
 // 12 sequences of up to 16384 tokens, 8 heads of 128 lanes, e4m3 to bf16, take
 // 88 us (5.2 TB/s); 3 x 6135 tokens of int8, 14.5; 5 x 3257 tokens of 4 heads,
 // int4 to fp16, 8.4, and with 32 pairs turned by fp32 cos and sin, whose double
