@@ -92,8 +92,12 @@ __device__ __forceinline__ float scale_inverse(float s) { return __builtin_amdgc
 // multiply-add gives exactly; where e is not 0, q becomes the odd number on
 // the side of q where x / s lies (q - 1 unit if it lies nearer to zero, with
 // the last bit set): past no t, as a t next to it is q itself or further than
-// a unit. A q that underflows has x's sign, as e does. Scales are 2^-100 or
-// more, which keeps every residual that decides out of the subnormals.
+// a unit. A q that underflows has x's sign, as e does. A residual decides only
+// where q is a t; x and t s are then multiples of s's last place (2^-123 or
+// more, scales being 2^-100 or more) times t's (2^-10 in e4m3, 2^-1 else), so
+// it is 2^-133 or more: for e4m3 and scales below 2^-93 a subnormal, which the
+// code relies on being kept (as fp32 subnormals are here unless a compiler
+// option asks otherwise).
 __device__ __forceinline__ float quotient(float x, float s, float inv)
 {
     const float q0 = x * inv;
