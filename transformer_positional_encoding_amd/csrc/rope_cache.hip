@@ -363,6 +363,7 @@ rope_status_t rope_cache_write(
         rope::CacheWritePlan kp = p, vp = p;
         kp.v.N = 0;
         vp.q.N = vp.k.N = 0;
+        vp.rotate_q = vp.rotate_k = false;
         vp.kc = p.vc;
         hipError_t err = kp.q.N + kp.k.N > 0 ? rope::launch_write(kp, s) : hipSuccess;
         if (err == hipSuccess) err = rope::launch_write(vp, s);
