@@ -1229,12 +1229,19 @@ class RopeCache:
     (pages, 2, page_size, heads, dim) tensor), the lanes of a row consecutive.
     scales: (pages, page_size, heads, dim // group) of float32 for the
     quantised formats: lane j of a row stands for code[j] * scale[j // group].
+    The object stays with these tensors: for others, make another.
     """
 
     __slots__ = ("data", "scales", "device", "words", "tensors")
 
+    def __setattr__(self, name, value):
+        raise AttributeError("a RopeCache stays with the tensors it was made of: make another")
+
+    __delattr__ = functools.partialmethod(__setattr__, value=None)
+
     def __init__(self, data, scales=None):
         import torch
+        put = functools.partial(object.__setattr__, self)
         if not isinstance(data, torch.Tensor) or data.dim() != 4:
             raise ValueError("data must be a 4-D torch.Tensor (pages, page_size, heads, dim)")
         fmt = _cache_format(data.dtype)
@@ -1244,19 +1251,21 @@ class RopeCache:
         s0, s1, s2, s3 = data.stride()
         if s3 != 1 and dim > 1:
             raise ValueError("data: the lanes of a row must be consecutive")
-        self.data, self.scales, self.device = data, scales, data.device
-        self.tensors = (data,) if scales is None else (data, scales)
+        put("data", data)
+        put("scales", scales)
+        put("device", data.device)
+        put("tensors", (data,) if scales is None else (data, scales))
         if fmt < 3:
             if scales is not None:
                 raise ValueError(f"a {data.dtype} cache has no scales")
             es = data.element_size()
-            self.words = _CacheWords(data.data_ptr(), 0, fmt, pages, size, heads, dim, dim, s0 * es, s1 * es, s2 * es)
+            put("words", _CacheWords(data.data_ptr(), 0, fmt, pages, size, heads, dim, dim, s0 * es, s1 * es, s2 * es))
             return
         if fmt == 5:
             dim *= 2
         if not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32:
             raise TypeError("a quantised cache needs float32 scales")
-        if scales.dim() != 4 or scales.device != self.device:
+        if scales.dim() != 4 or scales.device != data.device:
             raise ValueError("scales must be (pages, page_size, heads, dim // group), on data's device")
         p, z, h, groups = scales.shape
         if p != pages or z != size or h != heads:
@@ -1266,8 +1275,8 @@ class RopeCache:
             raise ValueError(f"{groups} scales do not divide {dim} lanes")
         if groups > 1 and c3 != 1:
             raise ValueError("scales: the scales of a row must be consecutive")
-        self.words = _CacheWords(data.data_ptr(), scales.data_ptr(), fmt, pages, size, heads, dim,
-                                 dim // groups if groups else 0, s0, s1, s2, c0, c1, c2)
+        put("words", _CacheWords(data.data_ptr(), scales.data_ptr(), fmt, pages, size, heads, dim,
+                                 dim // groups if groups else 0, s0, s1, s2, c0, c1, c2))
 
     @property
     def group(self) -> int:
