@@ -913,31 +913,32 @@ _TORCH = None
 
 
 def _autograd():
-    """torch's test of enabled gradients, its forward mode, and what moves the
+    """torch's test of enabled gradients, its forward mode, what moves the
     version counters of tensors written in place unseen by autograd (so that a
-    backward which needs an old value raises)."""
+    backward which needs an old value raises), and whether any of some tensors
+    (or None) requires a gradient."""
     global _TORCH
     if _TORCH is None:
         import torch
-        _TORCH = torch.is_grad_enabled, torch.autograd.forward_ad, torch._C._increment_version
+        _TORCH = (torch.is_grad_enabled, torch.autograd.forward_ad, torch._C._increment_version,
+                  torch._C._any_requires_grad)
     return _TORCH
 
 
 def _differentiated(x):
     """Whether autograd follows x: it needs a gradient, or has a tangent."""
-    enabled, fw, _ = _TORCH or _autograd()
+    enabled, fw, _, _ = _TORCH or _autograd()
     return x.requires_grad and enabled() or fw._current_level >= 0 and fw.unpack_dual(x).tangent is not None
 
 
 def _refuse_differentiated(call, names, tensors):
     """A call that gives no gradient takes no tensor that needs one. names: of
     the first tensors; the rest belong to caches."""
-    enabled, fw, _ = _TORCH or _autograd()
-    dual = fw._current_level >= 0
-    if not dual and not enabled():
+    enabled, fw, _, any_requires_grad = _TORCH or _autograd()
+    if fw._current_level < 0 and not (enabled() and any_requires_grad(*tensors)):
         return
     for i, t in enumerate(tensors):
-        if t is not None and (t.requires_grad or dual) and _differentiated(t):
+        if t is not None and _differentiated(t):
             name = names[i] if i < len(names) else "the cache"
             raise RuntimeError(f"{call}: {name} needs a gradient, which this call does not give; call it under "
                                "torch.no_grad() or with a detached tensor")
