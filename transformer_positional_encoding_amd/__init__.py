@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 __all__ = [
@@ -1233,16 +1234,17 @@ class RopeCache:
     The object stays with these tensors: for others, make another.
     """
 
-    __slots__ = ("data", "scales", "device", "words", "tensors")
+    __slots__ = ("_data", "_scales", "_device", "_words", "_tensors")
 
-    def __setattr__(self, name, value):
+    def _stays(self, value=None):
         raise AttributeError("a RopeCache stays with the tensors it was made of: make another")
 
-    __delattr__ = functools.partialmethod(__setattr__, value=None)
+    data = property(operator.attrgetter("_data"), _stays, _stays)
+    scales = property(operator.attrgetter("_scales"), _stays, _stays)
+    device = property(operator.attrgetter("_device"), _stays, _stays)
 
     def __init__(self, data, scales=None):
         import torch
-        put = functools.partial(object.__setattr__, self)
         if not isinstance(data, torch.Tensor) or data.dim() != 4:
             raise ValueError("data must be a 4-D torch.Tensor (pages, page_size, heads, dim)")
         fmt = _cache_format(data.dtype)
@@ -1252,15 +1254,13 @@ class RopeCache:
         s0, s1, s2, s3 = data.stride()
         if s3 != 1 and dim > 1:
             raise ValueError("data: the lanes of a row must be consecutive")
-        put("data", data)
-        put("scales", scales)
-        put("device", data.device)
-        put("tensors", (data,) if scales is None else (data, scales))
+        self._data, self._scales, self._device = data, scales, data.device
+        self._tensors = (data,) if scales is None else (data, scales)
         if fmt < 3:
             if scales is not None:
                 raise ValueError(f"a {data.dtype} cache has no scales")
             es = data.element_size()
-            put("words", _CacheWords(data.data_ptr(), 0, fmt, pages, size, heads, dim, dim, s0 * es, s1 * es, s2 * es))
+            self._words = _CacheWords(data.data_ptr(), 0, fmt, pages, size, heads, dim, dim, s0 * es, s1 * es, s2 * es)
             return
         if fmt == 5:
             dim *= 2
@@ -1276,18 +1276,18 @@ class RopeCache:
             raise ValueError(f"{groups} scales do not divide {dim} lanes")
         if groups > 1 and c3 != 1:
             raise ValueError("scales: the scales of a row must be consecutive")
-        put("words", _CacheWords(data.data_ptr(), scales.data_ptr(), fmt, pages, size, heads, dim,
-                                 dim // groups if groups else 0, s0, s1, s2, c0, c1, c2))
+        self._words = _CacheWords(data.data_ptr(), scales.data_ptr(), fmt, pages, size, heads, dim,
+                                  dim // groups if groups else 0, s0, s1, s2, c0, c1, c2)
 
     @property
     def group(self) -> int:
         """Lanes per scale."""
-        return self.words[7]
+        return self._words[7]
 
     @property
     def struct(self) -> RopeCacheStruct:
         """The C ABI's description of the cache."""
-        return RopeCacheStruct.from_buffer(self.words)
+        return RopeCacheStruct.from_buffer(self._words)
 
 
 def rope_cache(pages: int, page_size: int, heads: int, dim: int, format: str = "e4m3", group: int | None = None,
@@ -1423,21 +1423,21 @@ def rope_cache_write(k, v, k_cache, v_cache, slots, positions=None, inv_freq=Non
         raise ValueError("v and v_cache go together")
     if not isinstance(k_cache, RopeCache) or not (v_cache is None or isinstance(v_cache, RopeCache)):
         raise TypeError("k_cache and v_cache must be RopeCache objects")
-    if k_cache.device != dev or (v_cache is not None and v_cache.device != dev):
+    if k_cache._device != dev or (v_cache is not None and v_cache._device != dev):
         raise ValueError(f"k_cache and v_cache must be on {dev}")
     if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or slots.dim() != 2 or \
             slots.size(0) != B or slots.size(1) != S:
         raise ValueError("slots must be an int64 tensor (B, S)")
     if slots.device != dev:
         raise ValueError(f"slots must be on {dev}")
-    written = k_cache.tensors if v_cache is None else k_cache.tensors + v_cache.tensors
+    written = k_cache._tensors if v_cache is None else k_cache._tensors + v_cache._tensors
     _refuse_differentiated("rope_cache_write", "kvq", (k, v, q) + written)
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
     handle, current = _on_device(k, stream)
     with current:
         st = _words_entry("rope_cache_write")(
-            B, S, code, rows_q, _RowsWords(k.data_ptr(), n, d, sb, ss, sn), rows_v, k_cache.words,
-            None if v_cache is None else v_cache.words, slots.data_ptr() or None,
+            B, S, code, rows_q, _RowsWords(k.data_ptr(), n, d, sb, ss, sn), rows_v, k_cache._words,
+            None if v_cache is None else v_cache._words, slots.data_ptr() or None,
             _I64x2(*slots.stride()), *turn, 1 if rotate_k else 0, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
@@ -1472,7 +1472,7 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
         raise ValueError("out must be a GPU tensor")
     if not isinstance(cache, RopeCache):
         raise TypeError("cache must be a RopeCache")
-    if cache.device != dev:
+    if cache._device != dev:
         raise ValueError(f"cache must be on {dev}")
     B, S = out.shape[:2]
     if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
@@ -1489,12 +1489,12 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
             raise ValueError(f"{name} must be on {dev}")
     if block_table.device != dev:
         raise ValueError(f"block_table must be on {dev}")
-    _refuse_differentiated("rope_cache_read", ("out",), (out,) + cache.tensors)
+    _refuse_differentiated("rope_cache_read", ("out",), (out,) + cache._tensors)
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
     handle, current = _on_device(out, stream)
     with current:
         st = _words_entry("rope_cache_read")(
-            B, S, code, _rows("out", out), cache.words, block_table.data_ptr() or None, block_table.shape[1],
+            B, S, code, _rows("out", out), cache._words, block_table.data_ptr() or None, block_table.shape[1],
             block_table.stride(0), lengths.data_ptr() or None, None if starts is None else starts.data_ptr() or None,
             *turn, handle)
     if st != ROPE_OK:
