@@ -1621,6 +1621,7 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
     count, rank = a.shape[0], a.shape[1]
     if out is not None and tuple(out.shape) != y_shape:
         raise ValueError(f"out must be a contiguous {y_shape} tensor")
+    given = out is not None
     # memory made here belongs to the call's stream: the allocator then hands
     # it on only to work behind this call's
     with _allocating_on(stream, dev) if stream is not None and x.is_cuda else _nullcontext():
@@ -1628,10 +1629,10 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
             out = torch.empty(y_shape, dtype=out_dtype or x.dtype, device=dev)
         if workspace is None:
             workspace = torch.empty(rope_proj_lora_workspace(B * S, K, rank) if count else 0, dtype=torch.uint8, device=dev)
-    for name, t in (("x", x), ("w", w), ("a", a), ("b", b), ("adapters", adapters), ("out", out),
-                    ("workspace", workspace), ("scales", scales)):
-        if t is None:
+    for i, t in enumerate((x, w, a, b, adapters, out, workspace, scales)):
+        if t is None or (t.is_contiguous() and t.is_cuda and t.device == dev):
             continue
+        name = ("x", "w", "a", "b", "adapters", "out", "workspace", "scales")[i]
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if not t.is_cuda and t.numel():
@@ -1651,8 +1652,9 @@ def rope_proj_lora_fwd(x, w, a, b, adapters, r1, r2, heads: int, rotary_mode="in
             _I64x4(*y_shape), K, lora, r1.data_ptr() or None, _arr4(r1.shape), _arr4(r1.stride()),
             r2.data_ptr() or None, _arr4(r2.shape), _arr4(r2.stride()),
             _dtype_code(r1) if r1.dtype == r2.dtype else -1, rotary_mode, sl, workspace.data_ptr() or None,
-            workspace.numel() * workspace.element_size(), handle)
+            workspace.nbytes, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
-    _TORCH[2]((out,))
+    if given:
+        _TORCH[2]((out,))
     return out
