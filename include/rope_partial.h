@@ -465,8 +465,8 @@ typedef struct rope_rows {
  *               nothing is rotated and positions are not looked at.
  *
  * q must not share a byte with itself (rows that overlap are refused), nor
- * with k, v or the caches (not checked: the rows of one fused projection lie
- * between each other). Checks, in order: B, S, dtype, k, k_cache, v and
+ * with k, v or the caches, nor k and v with the caches (not checked: the rows
+ * of one fused projection lie between each other). Checks, in order: B, S, dtype, k, k_cache, v and
  * v_cache present (ROPE_ERR_NULLPTR); mode, slice and types as
  * rope_partial_fwd_inplace on k's shape; the caches' fields; q and v against
  * them; strides; no token or no lanes: ROPE_OK; NULL data; then positions.
@@ -490,7 +490,8 @@ ROPE_API rope_status_t rope_cache_write(
  * other positions. Every other row of out keeps its bytes: s >= lengths[b],
  * tokens before 0 or past the block table, and pages outside [0, pages).
  *
- *   out           (B, S, heads, dim) rows of `dtype`; rows must not overlap.
+ *   out           (B, S, heads, dim) rows of `dtype`; rows must not overlap
+ *                 each other, nor any input (the latter is not checked).
  *   cache         any quantised format, or the format of `dtype`.
  *   block_table   device int32, B rows of table_pages pages, row b at
  *                 b * table_stride.

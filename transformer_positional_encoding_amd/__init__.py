@@ -665,6 +665,9 @@ def rope_partial_fwd_inplace(x, r1, r2, rotary_mode="interleave", partial_slice=
     interleave).
     partial_slice: (start, end) or None for the empty slice [0, 0).
     stream: a torch stream or raw hipStream_t; default torch's current stream.
+
+    The rope_partial_* calls are not recorded by autograd
+    (:func:`inplace_partial_rotary_mul` is).
     """
     _call("fwd", x, r1, r2, rotary_mode, partial_slice, stream)
 
@@ -1514,7 +1517,8 @@ def rope_proj_fwd(x, w, r1, r2, heads: int, rotary_mode="interleave", partial_sl
     x: (B, S, K) or (M, K) bf16/fp16; w: (H*Dh, K) of x's dtype (a linear
     layer's weight); r1/r2: 4-D tables broadcasting against (B, S, H, L).
     Returns ``out`` (allocated when None): (B, S, H, Dh) of ``out_dtype``
-    (x's dtype by default, or torch.float32)."""
+    (x's dtype by default, or torch.float32). The call is not recorded by
+    autograd: the result gives x and w no gradient."""
     import torch
     if isinstance(rotary_mode, str):
         if rotary_mode not in MODES:

@@ -299,8 +299,8 @@ __device__ __forceinline__ float cached_lane(const CacheRef& c, const char* src,
 
 // A block takes a token, its waves the token's rows in turn: cos and sin are
 // evaluated once a token. (A wave a row, each evaluating its own twice a pair:
-// 17 x 2947 tokens of 8 heads of 80 lanes, int4 to fp32, lanes [3,75) turned,
-// 208 us; this 144.)
+// 17 sequences of up to 2947 tokens of 8 heads of 80 lanes, int4 to fp32, lanes
+// [3,75) turned, 208 us; this 144, and 194 where all have 2947.)
 constexpr int kGenReadThreads = 256;
 
 template <int DT, int FMT>
@@ -727,8 +727,8 @@ __global__ void __launch_bounds__(kVecThreads) rope_cache_write_kernel(CacheWrit
 // where two take 99, of four 100.
 // 12 sequences of up to 16384 tokens, 8 heads of 128 lanes, e4m3 to bf16, take
 // 88 us (5.2 TB/s); 3 x 6135 tokens of int8, 14.5; 5 x 3257 tokens of 4 heads,
-// int4 to fp16, 8.4, and with 32 pairs turned by fp32 cos and sin, whose double
-// evaluation a token's wave waits for, 13.4.
+// int4 to fp16, 8.3, and with 32 pairs turned by fp32 cos and sin, evaluated in
+// double by their blocks, 11.8.
 // ---------------------------------------------------------------------------
 constexpr int kReadChunks = 2;
 
