@@ -1063,8 +1063,9 @@ def inplace_partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slic
 
     x must not be a leaf tensor that requires grad: in-place changes to such
     a tensor are illegal in autograd, so rotate a non-leaf copy (y = x * 1.0),
-    as the training example on the page does. r1 and r2 never get gradients.
-    Differentiable any number of times and in forward mode.
+    as the training example on the page does. r1 and r2 never get gradients,
+    nor are tangents of theirs followed. Differentiable any number of times
+    and in forward mode.
     """
     _autograd_inplace("inplace_partial_rotary_mul", _rotate_tables, x, r1, r2, _tables_how(rotary_mode, partial_slice))
 
@@ -1075,7 +1076,7 @@ def partial_rotary_mul(x, r1, r2, rotary_mode="interleave", partial_slice=None):
     autograd (the backward is the out-of-place backward entry point) and
     works on leaf tensors too, so a training step needs no ``x * 1.0`` copy
     before the in-place op. Differentiable any number of times and in forward
-    mode. r1 and r2 never get gradients."""
+    mode. r1 and r2 never get gradients, nor are tangents of theirs followed."""
     return _autograd_out(_rotate_tables, "fwd", x, r1, r2, _tables_how(rotary_mode, partial_slice))
 
 
@@ -1102,7 +1103,8 @@ def partial_rotary_mul_pos(x, positions, inv_freq, rotary_mode="interleave", par
     """:func:`partial_rotary_mul` with cos and sin computed in the kernel from
     positions: returns a new tensor, x is not modified, and the backward is
     the out-of-place position backward, differentiable in its turn, as is the
-    tangent in forward mode. positions and inv_freq never get gradients."""
+    tangent in forward mode. positions and inv_freq never get gradients, nor
+    are tangents of theirs followed."""
     return _autograd_out(_call_pos, "fwd", x, positions, inv_freq, _pos_how(rotary_mode, partial_slice, table_dtype))
 
 
