@@ -510,6 +510,160 @@ ROPE_API rope_status_t rope_cache_read(
     const int64_t positions_strides[3], const double* inv_freq, const int32_t* pair_axes, rope_dtype_t table_dtype,
     int64_t mode, const int64_t partial_slice[2], void* stream);
 
+/* most sequences of one rope_cache_reserve */
+#define ROPE_RESERVE_MAX 16384
+
+/*
+ * rope_cache_reserve -- a step's bookkeeping of a paged cache, on the device:
+ * pages are given to sequences that grow and taken back from those that
+ * shrink or end, and the new tokens get their slots and positions (what
+ * rope_cache_write and the position calls take). With pages(n) = ceil(n /
+ * page_size):
+ *   1. For every b with counts[b] < 0, in order: the sequence keeps k =
+ *      max(0, lengths[b] + counts[b]) tokens. The pages of columns [pages(k),
+ *      pages(lengths[b])) of its row go to the end of the free list, in order
+ *      (what would pass its capacity is dropped), and -1 takes their place.
+ *   2. For every b with 0 < counts[b] <= S whose lengths[b] + counts[b] tokens
+ *      fit in its row of the table: it needs the columns [pages(lengths[b]),
+ *      pages(lengths[b] + counts[b])). It gets them from the end of the free
+ *      list, the first column the last page, if it needs none, or the pages
+ *      needed by it and every sequence before it (served or not) are no more
+ *      than the list holds. Otherwise, or where the row is too short, nothing
+ *      of it changes.
+ *   granted[b]     what is added to lengths[b]: counts[b] where it was served,
+ *                  minus the tokens dropped in 1, else 0.
+ *   positions[b,s] k + s in 1, else lengths[b] (before) + s; for every s < S.
+ *   slots[b,s]     for s < granted[b] the slot of token positions[b,s]: its
+ *                  page * page_size + its place in it; else, or where the page
+ *                  is negative, -1.
+ * A row whose length is negative or past its columns is left alone (granted
+ * 0). Every other entry of the table, and the free list's places behind its
+ * count, keep their values.
+ *
+ *   block_table   device int32, B rows of table_pages pages, row b at
+ *                 b * table_stride >= table_pages; changed in place, as are
+ *   lengths       device int32 (B),
+ *   free_pages    device int32 (free_capacity): a list of free pages of
+ *   free_count    device int32 (1) entries.
+ *   counts        device int32 (B).
+ *   slots, positions  device int64 (B, S), contiguous; granted: int32 (B).
+ *
+ * The arrays must not overlap. Checks: sizes (ROPE_ERR_INVALID; S at least 1;
+ * B of 0 is ROPE_OK; more than ROPE_RESERVE_MAX sequences, or B * S, page_size,
+ * free_capacity or table_pages of 2^31 or more: ROPE_ERR_UNSUPPORTED), NULL
+ * pointers, alignment. Asynchronous on `stream`; nothing is allocated;
+ * deterministic. Calls on the same table must follow each other.
+ */
+ROPE_API rope_status_t rope_cache_reserve(
+    int64_t B, int64_t S, int32_t* block_table, int64_t table_pages, int64_t table_stride, int32_t* lengths,
+    const int32_t* counts, int32_t* free_pages, int64_t free_capacity, int32_t* free_count, int64_t page_size,
+    int64_t* slots, int64_t* positions, int32_t* granted, void* stream);
+
+/*
+ * rope_cache_attention -- attention of a step's new tokens over a paged cache
+ * held in 4 bits. Sequence b has lengths[b] cached tokens, the last counts[b]
+ * of which are the new ones whose queries are given: query s < counts[b]
+ * stands at token lengths[b] - counts[b] + s. With k_t and v_t the cached rows
+ * (code * scale) of the cached head that query head h belongs to (h / (q heads
+ * / heads)):
+ *   x_t = scale * q[b,s,h,:] . k_t
+ *   out[b,s,h,:] = sum_t exp(x_t) v_t / sum_t exp(x_t)
+ * over the tokens t in [0, lengths[b]) that the block table holds (row b's
+ * page t / page_size, in [0, pages)) and, when causal is not 0, t no later than
+ * the query's own. A row that sees no token is 0. Rows s >= counts[b] of out
+ * keep their bytes.
+ * Products with q are exact and summed in fp32, as are the softmax's sums
+ * and its products with v; 16-bit outputs may round exp(x_t) times v's scale
+ * to 11 bits before the product. out is rounded once.
+ *
+ *   B, S          tokens of q and out; dtype: their storage type.
+ *   out, q        (B, S, heads of q, lanes of v or k) rows; out's must not
+ *                 overlap each other or an input (the latter is not checked).
+ *   k_cache, v_cache  ROPE_CACHE_INT4, the same pages, page_size and heads
+ *                 (which divide q's); dim and group may differ.
+ *   block_table, table_pages, table_stride   as for rope_cache_read.
+ *   lengths       device int32 (B); counts: device int32 (B) or NULL (S).
+ *                 Counts outside [0, S] are taken as the nearest of the two.
+ *   scale         positive.
+ *   workspace     device buffer of workspace_bytes, 16-byte aligned, used
+ *                 during the call: at least rope_cache_attention_workspace(B,
+ *                 S, heads of q, heads, lanes of v). Two calls that may run at
+ *                 once need one each. Not looked at where that is 0.
+ *
+ * Checks, in order: q's dimensions and type; the caches' fields, formats
+ * (ROPE_ERR_UNSUPPORTED unless ROPE_CACHE_INT4) and shapes; strides; scale; an
+ * empty q is ROPE_OK; NULL or misaligned pointers; the workspace.
+ * ROPE_ERR_UNSUPPORTED: 2^31 rows or more. Asynchronous on `stream`; nothing
+ * is allocated; deterministic.
+ */
+ROPE_API rope_status_t rope_cache_attention(
+    int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* out, const rope_rows_t* q, const rope_cache_t* k_cache,
+    const rope_cache_t* v_cache, const int32_t* block_table, int64_t table_pages, int64_t table_stride,
+    const int32_t* lengths, const int32_t* counts, double scale, int32_t causal, void* workspace,
+    int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that a rope_cache_attention of this shape needs, however
+ * many tokens are cached (0 when the arguments are out of range). */
+ROPE_API int64_t rope_cache_attention_workspace(int64_t B, int64_t S, int64_t q_heads, int64_t heads, int64_t v_dim);
+
+/* ============== norms of query and key heads with their rotation ============== */
+
+/*
+ * rope_qk_norm_fwd -- RMS norms of the heads of Q and K and their rotation in
+ * one pass: for every row x of D lanes
+ *     n_j = x_j / sqrt(mean(x^2) + eps) * weight_j
+ *     out = n with its slice rotated from positions, forward, as
+ *           rope_partial_fwd_inplace_axes rotates fp32 data
+ * in fp32, rounded once to `dtype`. The mean is over all D lanes.
+ *
+ *   B, S, dtype   tokens; storage type of q, k and their results.
+ *   q, k          (B, S, heads, D) rows, read; any strides (slices of a fused
+ *                 projection's output). k and k_out are NULL when there is no
+ *                 k. Heads may differ, D may not.
+ *   q_out, k_out  rows of the same shapes; theirs must not overlap each other.
+ *                 q_out may be q, with its strides, and k_out k (in place).
+ *   q_weight, k_weight  device arrays of D weight_dtype numbers, or NULL: ones.
+ *   eps           finite, not negative.
+ *   positions, ... partial_slice  as for rope_cache_write; positions NULL, or
+ *                 an empty slice: nothing is rotated.
+ *
+ * Checks, in order: NULL rows; q's dimensions, types, mode and slice; eps; the
+ * other rows' shapes and strides; 2^31 rows or more (ROPE_ERR_UNSUPPORTED); no
+ * row: ROPE_OK; NULL or misaligned data; positions. Asynchronous on `stream`;
+ * nothing is allocated; deterministic.
+ */
+ROPE_API rope_status_t rope_qk_norm_fwd(
+    int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* q_out, const rope_rows_t* k_out, const rope_rows_t* q,
+    const rope_rows_t* k, const void* q_weight, const void* k_weight, rope_dtype_t weight_dtype, double eps,
+    const int64_t* positions, const int64_t positions_shape[3], const int64_t positions_strides[3],
+    const double* inv_freq, const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode,
+    const int64_t partial_slice[2], void* stream);
+
+/*
+ * rope_qk_norm_bwd -- its backward pass: dq and dk receive the gradients for q
+ * and k, dq_weight and dk_weight (D weight_dtype numbers) those for the
+ * weights, summed over every row in fp32 and rounded once; either may be NULL
+ * (not computed), and must be where the weight is. q_grad and k_grad are the
+ * gradients for q_out and k_out; dq may be q_grad, with its strides, and dk
+ * k_grad. Without rows the weights' gradients are 0.
+ *
+ *   workspace     device buffer of workspace_bytes, 16-byte aligned, at least
+ *                 rope_qk_norm_workspace(D); not looked at when neither
+ *                 weight's gradient is asked for. Two calls that may run at
+ *                 once need one each.
+ *   Other arguments and checks as above; the workspace before positions.
+ */
+ROPE_API rope_status_t rope_qk_norm_bwd(
+    int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* dq, const rope_rows_t* dk, void* dq_weight,
+    void* dk_weight, const rope_rows_t* q_grad, const rope_rows_t* k_grad, const rope_rows_t* q, const rope_rows_t* k,
+    const void* q_weight, const void* k_weight, rope_dtype_t weight_dtype, double eps, const int64_t* positions,
+    const int64_t positions_shape[3], const int64_t positions_strides[3], const double* inv_freq,
+    const int32_t* pair_axes, rope_dtype_t table_dtype, int64_t mode, const int64_t partial_slice[2], void* workspace,
+    int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that a rope_qk_norm_bwd with heads of D lanes needs. */
+ROPE_API int64_t rope_qk_norm_workspace(int64_t D);
+
 /* ====================== checks and launch plans ====================== */
 
 /*

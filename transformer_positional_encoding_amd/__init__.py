@@ -29,7 +29,9 @@ __all__ = [
     "rope_partial_fwd_inplace_axes", "rope_partial_bwd_inplace_axes", "rope_partial_fwd_out_axes",
     "rope_partial_bwd_out_axes", "rope_partial_fwd_inplace_axes_multi", "rope_partial_bwd_inplace_axes_multi",
     "inplace_partial_rotary_mul_axes", "partial_rotary_mul_axes", "rope_pair_axes", "rope_axes_inv_freq", "AXES_MAX",
-    "RopeCache", "rope_cache", "rope_cache_write", "rope_cache_read", "CACHE_FORMATS", "rope_proj_fwd",
+    "RopeCache", "rope_cache", "rope_cache_write", "rope_cache_read", "rope_cache_reserve", "RESERVE_MAX",
+    "rope_cache_attention", "rope_cache_attention_workspace", "rope_qk_norm_fwd", "rope_qk_norm_bwd",
+    "rope_qk_norm_workspace", "qk_norm_rotary", "CACHE_FORMATS", "rope_proj_fwd",
     "rope_proj_lora_fwd", "rope_proj_lora_workspace", "LORA_RANK_MAX", "RopeError", "library", "LIB_PATH", "ROPE_OK", "ROPE_ERR_NULLPTR", "ROPE_ERR_INVALID",
     "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_RUNTIME", "MODES", "DTYPE_CODES",
 ]
@@ -43,6 +45,7 @@ DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 MULTI_MAX = 4
 AXES_MAX = 4
 LORA_RANK_MAX = 128
+RESERVE_MAX = 16384
 CACHE_FORMATS = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3, "int8": 4, "int4": 5}
 
 _I64x4 = ctypes.c_int64 * 4
@@ -164,6 +167,23 @@ def library() -> ctypes.CDLL:
         L.rope_cache_read.restype = ctypes.c_int
         L.rope_cache_read.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, rows, cache, vp, ctypes.c_int64,
                                       ctypes.c_int64, vp, vp] + turn + [vp]
+        L.rope_cache_reserve.restype = ctypes.c_int
+        L.rope_cache_reserve.argtypes = [ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, ctypes.c_int64, vp, vp, vp,
+                                         ctypes.c_int64, vp, ctypes.c_int64, vp, vp, vp, vp]
+        L.rope_cache_attention.restype = ctypes.c_int
+        L.rope_cache_attention.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, rows, rows, cache, cache, vp,
+                                           ctypes.c_int64, ctypes.c_int64, vp, vp, ctypes.c_double, ctypes.c_int32, vp,
+                                           ctypes.c_int64, vp]
+        L.rope_cache_attention_workspace.restype = ctypes.c_int64
+        L.rope_cache_attention_workspace.argtypes = [ctypes.c_int64] * 5
+        weights = [vp, vp, ctypes.c_int, ctypes.c_double]
+        L.rope_qk_norm_fwd.restype = ctypes.c_int
+        L.rope_qk_norm_fwd.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int] + [rows] * 4 + weights + turn + [vp]
+        L.rope_qk_norm_bwd.restype = ctypes.c_int
+        L.rope_qk_norm_bwd.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, rows, rows, vp, vp] + [rows] * 4 + \
+            weights + turn + [vp, ctypes.c_int64, vp]
+        L.rope_qk_norm_workspace.restype = ctypes.c_int64
+        L.rope_qk_norm_workspace.argtypes = [ctypes.c_int64]
         L.rope_partial_check.restype = ctypes.c_int
         L.rope_partial_check.argtypes = _ENTRY_ARGTYPES[:-1]
         L.rope_partial_launch_info.restype = ctypes.c_int
@@ -1505,6 +1525,345 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
     if st != ROPE_OK:
         raise RopeError(st, last_error())
     _TORCH[2]((out,))
+
+
+def _arrays(name, t, dtype, shape, dev):
+    """A contiguous tensor of a call's bookkeeping."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype).split('.')[-1]} tensor {shape}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return t.data_ptr() or None
+
+
+def rope_cache_reserve(block_table, lengths, counts, free_pages, free_count, page_size: int, tokens: int | None = None,
+                       slots=None, positions=None, granted=None, stream=None):
+    """A step's bookkeeping of a paged cache, on the GPU: sequence b grows by
+    ``counts[b]`` tokens, taking pages from the end of the list of free ones as
+    it needs them, or where that is negative drops as many, its pages going
+    back to the list (-lengths[b] or less ends it). Pages are given back before
+    any are taken, both in the order of the sequences; a sequence is refused,
+    and nothing of it changes, when the list is too short for the pages that it
+    and those before it need, or its row of the table is.
+
+    block_table: int32 (B, columns), lengths: int32 (B), free_pages: int32
+    (capacity), free_count: int32 (1); all changed in place. counts: int32 (B).
+    tokens: columns of slots and positions, the most that a sequence may grow
+    (default: those of slots or positions, or 1).
+
+    Returns (slots, positions, granted), allocated when None: the int64 (B,
+    tokens) slots (-1 past a sequence's new tokens) and positions that
+    :func:`rope_cache_write` takes, and int32 (B) what was added to each
+    length: 0 for a refused sequence, the count for
+    :func:`rope_cache_attention`. At most RESERVE_MAX sequences."""
+    import torch
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor (B, columns)")
+    B, cols = block_table.shape
+    dev = block_table.device
+    if cols > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: the pages of a sequence must be consecutive")
+    if B and not block_table.is_cuda:
+        raise ValueError("block_table must be a GPU tensor")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a contiguous int32 tensor (capacity)")
+    if tokens is None:
+        given = slots if slots is not None else positions
+        tokens = given.shape[1] if given is not None and given.dim() == 2 else 1
+    ins = [_arrays(n, t, torch.int32, sh, dev) for n, t, sh in (
+        ("lengths", lengths, (B,)), ("counts", counts, (B,)), ("free_pages", free_pages, (free_pages.shape[0],)),
+        ("free_count", free_count, (1,)))]
+    with _allocating_on(stream, dev) if stream is not None and block_table.is_cuda else _nullcontext():
+        if slots is None:
+            slots = torch.empty(B, tokens, dtype=torch.int64, device=dev)
+        if positions is None:
+            positions = torch.empty(B, tokens, dtype=torch.int64, device=dev)
+        if granted is None:
+            granted = torch.empty(B, dtype=torch.int32, device=dev)
+    outs = [_arrays("slots", slots, torch.int64, (B, tokens), dev),
+            _arrays("positions", positions, torch.int64, (B, tokens), dev),
+            _arrays("granted", granted, torch.int32, (B,), dev)]
+    handle, current = _on_device(block_table, stream)
+    with current:
+        st = library().rope_cache_reserve(B, tokens, block_table.data_ptr() or None, cols, block_table.stride(0), ins[0],
+                                          ins[1], ins[2], free_pages.shape[0], ins[3], page_size, *outs, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
+    (_TORCH or _autograd())[2]((block_table, lengths, free_pages, free_count, slots, positions, granted))
+    return slots, positions, granted
+
+
+def rope_cache_attention_workspace(B: int, S: int, q_heads: int, heads: int, v_dim: int) -> int:
+    """Bytes of workspace that :func:`rope_cache_attention` needs for queries
+    (B, S, q_heads, any) over caches of ``heads`` heads, however many tokens
+    are cached."""
+    return library().rope_cache_attention_workspace(B, S, q_heads, heads, v_dim)
+
+
+def rope_cache_attention(q, k_cache, v_cache, block_table, lengths, counts=None, causal: bool = True,
+                         scale: float | None = None, out=None, workspace=None, stream=None):
+    """Attention of a step's new tokens over a paged cache held in 4 bits:
+    sequence b has ``lengths[b]`` cached tokens, of which the last
+    ``counts[b]`` are new, and ``q[b, s]`` for s < counts[b] are their queries
+    (each sees the tokens up to its own; without ``causal``, all). The heads of
+    q share the caches' heads in groups.
+
+    q: (B, S, heads, dim) GPU tensor, float32/float16/bfloat16, any strides
+    with consecutive lanes, heads a multiple of the caches'.
+    k_cache, v_cache: :class:`RopeCache` of 4 bits, filled by
+    :func:`rope_cache_write`.
+    block_table: int32 (B, columns); lengths: int32 (B); counts: int32 (B) or
+    None: S.
+    scale: of the products with k, positive; dim ** -0.5 when None.
+    workspace: a contiguous GPU tensor of at least
+    ``rope_cache_attention_workspace(B, S, heads, cache heads, v's dim)``
+    bytes, 16-byte aligned, that no other call uses meanwhile; None allocates
+    one.
+
+    Returns ``out``, (B, S, heads, v's dim) of q's type (allocated when None,
+    then zero past each sequence's count; a given one keeps its bytes there). A
+    query that sees no token gives zeros. No gradient passes through the call:
+    tensors that need one are refused (while gradients are enabled)."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a 4-D torch.Tensor (B, S, heads, dim)")
+    code, dev = _dtype_code(q), q.device
+    if q.numel() and not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    if not isinstance(k_cache, RopeCache) or not isinstance(v_cache, RopeCache):
+        raise TypeError("k_cache and v_cache must be RopeCache objects")
+    if k_cache._device != dev or v_cache._device != dev:
+        raise ValueError(f"k_cache and v_cache must be on {dev}")
+    B, S, heads, dim = q.shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            block_table.shape[0] != B:
+        raise ValueError("block_table must be an int32 tensor (B, columns)")
+    cols = block_table.shape[1]
+    if cols > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: the pages of a sequence must be consecutive")
+    if block_table.device != dev:
+        raise ValueError(f"block_table must be on {dev}")
+    at_lengths = _arrays("lengths", lengths, torch.int32, (B,), dev)
+    at_counts = None if counts is None else _arrays("counts", counts, torch.int32, (B,), dev)
+    _refuse_differentiated("rope_cache_attention", ("q", "out"), (q, out) + k_cache._tensors + v_cache._tensors)
+    kv_heads, v_dim = k_cache._words[5], v_cache._words[6]
+    given = out is not None
+    if given:
+        if not isinstance(out, torch.Tensor) or tuple(out.shape) != (B, S, heads, v_dim):
+            raise ValueError(f"out must be a {(B, S, heads, v_dim)} tensor")
+        if out.dtype != q.dtype or out.device != dev:
+            raise ValueError(f"out must be {q.dtype} on {dev}")
+    with _allocating_on(stream, dev) if stream is not None and q.is_cuda else _nullcontext():
+        if out is None:
+            make = torch.empty if counts is None else torch.zeros
+            out = make(B, S, heads, v_dim, dtype=q.dtype, device=dev)
+        if workspace is None:
+            need = library().rope_cache_attention_workspace(B, S, heads, kv_heads, v_dim)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    handle, current = _on_device(q, stream)
+    with current:
+        st = _words_entry("rope_cache_attention")(
+            B, S, code, _rows("out", out), _rows("q", q), k_cache._words, v_cache._words, block_table.data_ptr() or None,
+            cols, block_table.stride(0), at_lengths, at_counts, dim ** -0.5 if scale is None and dim else scale or 0.0,
+            1 if causal else 0, workspace.data_ptr() or None, workspace.nbytes, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
+    if given:
+        _TORCH[2]((out,))
+    return out
+
+
+# ------------------------------------------------- norms of query and key heads with their rotation
+
+def _norm_weights(q, k, q_weight, k_weight):
+    """(pointer, pointer, type) of the weights of a norm's heads."""
+    import torch
+    types = set()
+    ptrs = []
+    for name, w, x in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
+        if w is None:
+            ptrs.append(None)
+            continue
+        if x is None:
+            raise ValueError("k_weight goes with k")
+        if not isinstance(w, torch.Tensor) or w.dim() != 1 or w.shape[0] != x.shape[3] or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor ({x.shape[3]})")
+        if w.device != x.device:
+            raise ValueError(f"{name} must be on {x.device}")
+        types.add(_dtype_code(w))
+        ptrs.append(w.data_ptr() or None)
+    if len(types) > 1:
+        raise TypeError("q_weight and k_weight must share a dtype")
+    return (*ptrs, types.pop() if types else 0)
+
+
+def _norm_rows(name, t, like):
+    """Rows beside those of q or k: the same shape, type and device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be a {tuple(like.shape)} {like.dtype} tensor on {like.device}")
+    return _rows(name, t)
+
+
+def _norm_args(q, k, names=("q", "k")):
+    import torch
+    for name, t in zip(names, (q, k)):
+        if t is None and name != names[0]:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a 4-D torch.Tensor (B, S, heads, dim)")
+        if t.numel() and not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+    if k is not None and (k.dtype != q.dtype or k.device != q.device or k.shape[:2] != q.shape[:2]):
+        raise ValueError("k must have q's tokens, type and device")
+
+
+def rope_qk_norm_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, rotary_mode="interleave",
+                     partial_slice=None, eps: float = 1e-6, q_out=None, k_out=None, pair_axes=None, table_dtype=None,
+                     stream=None):
+    """RMS norms of the heads of q and k, and their rotation, in one pass: each
+    row x of the last dimension becomes ``x / sqrt(mean(x^2) + eps) * weight``
+    with its slice ``[start, end)`` rotated from positions, in fp32, rounded
+    once.
+
+    q, k: (B, S, heads, dim) GPU tensors of one type, any strides with
+    consecutive lanes (slices of a fused projection's output); k may be None.
+    q_weight, k_weight: (dim) tensors of one of the three types, or None: ones.
+    positions, inv_freq, rotary_mode, partial_slice, pair_axes, table_dtype: as
+    in :func:`rope_cache_write`; positions None: nothing is rotated.
+    q_out, k_out: where the results go: tensors of q's and k's shapes, which
+    may be q and k themselves (in place); new contiguous ones when None.
+
+    Returns (q_out, k_out). No gradient passes through the call: tensors that
+    need one are refused (while gradients are enabled; :func:`qk_norm_rotary`
+    gives them)."""
+    import torch
+    _norm_args(q, k)
+    ptrs = _norm_weights(q, k, q_weight, k_weight)
+    _refuse_differentiated("rope_qk_norm_fwd", ("q", "k", "q_weight", "k_weight", "q_out", "k_out"),
+                           (q, k, q_weight, k_weight, q_out, k_out))
+    given = tuple(t for t in (q_out, k_out) if t is not None)
+    if k is None and k_out is not None:
+        raise ValueError("k_out goes with k")
+    with _allocating_on(stream, q.device) if stream is not None and q.is_cuda else _nullcontext():
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    code = _dtype_code(q)
+    turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, q.device)
+    handle, current = _on_device(q, stream)
+    with current:
+        st = _words_entry("rope_qk_norm_fwd")(
+            q.shape[0], q.shape[1], code, _norm_rows("q_out", q_out, q), None if k is None else _norm_rows("k_out", k_out, k),
+            _rows("q", q), None if k is None else _rows("k", k), *ptrs, eps, *turn, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
+    if given:
+        (_TORCH or _autograd())[2](given)
+    return q_out, k_out
+
+
+def rope_qk_norm_workspace(dim: int) -> int:
+    """Bytes of workspace that :func:`rope_qk_norm_bwd` needs for heads of
+    ``dim`` lanes."""
+    return library().rope_qk_norm_workspace(dim)
+
+
+def rope_qk_norm_bwd(q_grad, k_grad, q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                     rotary_mode="interleave", partial_slice=None, eps: float = 1e-6, dq=None, dk=None,
+                     weight_grads: bool = True, pair_axes=None, table_dtype=None, workspace=None, stream=None):
+    """Backward of :func:`rope_qk_norm_fwd`: for the gradients q_grad and k_grad
+    of its results, (dq, dk, dq_weight, dk_weight). q and k are the forward's
+    inputs. dq and dk may be given, q_grad and k_grad themselves among them; a
+    weight's gradient is None where the weight is, or without ``weight_grads``.
+    workspace: a contiguous GPU tensor of ``rope_qk_norm_workspace(dim)`` bytes,
+    16-byte aligned, that no other call uses meanwhile; None allocates one. Not
+    recorded by autograd."""
+    import torch
+    _norm_args(q, k)
+    ptrs = _norm_weights(q, k, q_weight, k_weight)
+    if k is None and not (k_grad is None and dk is None):
+        raise ValueError("k_grad and dk go with k")
+    given = tuple(t for t in (dq, dk) if t is not None)
+    want = weight_grads and not (q_weight is None and k_weight is None)
+    dev = q.device
+    with _allocating_on(stream, dev) if stream is not None and q.is_cuda else _nullcontext():
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if k is not None and dk is None:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        dw = [None if w is None or not weight_grads else torch.empty_like(w) for w in (q_weight, k_weight)]
+        if want and workspace is None:
+            workspace = torch.empty(library().rope_qk_norm_workspace(q.shape[3]), dtype=torch.uint8, device=dev)
+    if want and (not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    code = _dtype_code(q)
+    turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
+    handle, current = _on_device(q, stream)
+    none = k is None
+    with current:
+        st = _words_entry("rope_qk_norm_bwd")(
+            q.shape[0], q.shape[1], code, _norm_rows("dq", dq, q), None if none else _norm_rows("dk", dk, k),
+            *(None if w is None else w.data_ptr() or None for w in dw), _norm_rows("q_grad", q_grad, q),
+            None if none else _norm_rows("k_grad", k_grad, k), _rows("q", q), None if none else _rows("k", k), *ptrs, eps,
+            *turn, workspace.data_ptr() or None if want else None, workspace.nbytes if want else 0, handle)
+    if st != ROPE_OK:
+        raise RopeError(st, last_error())
+    if given:
+        (_TORCH or _autograd())[2](given)
+    return dq, dk, dw[0], dw[1]
+
+
+_QK_NORM_FN = None
+
+
+def _qk_norm_fn():
+    """The autograd function of the norms. Its arguments: q, k, their weights,
+    positions, inv_freq, and what else the calls take."""
+    global _QK_NORM_FN
+    if _QK_NORM_FN is not None:
+        return _QK_NORM_FN
+    import torch
+
+    def lanes(t):
+        return t if t is None or t.shape[3] < 2 or t.stride(3) == 1 else t.contiguous()
+
+    class QkNormFn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, how):
+            ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+            ctx.how = how
+            mode, sl, eps, pair_axes, table_dtype = how
+            return rope_qk_norm_fwd(q, k, q_weight, k_weight, positions, inv_freq, mode, sl, eps, pair_axes=pair_axes,
+                                    table_dtype=table_dtype)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, q_grad, k_grad):
+            q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+            mode, sl, eps, pair_axes, table_dtype = ctx.how
+            need = ctx.needs_input_grad
+            got = rope_qk_norm_bwd(lanes(q_grad), None if k is None else lanes(k_grad), q, k, q_weight, k_weight,
+                                   positions, inv_freq, mode, sl, eps, weight_grads=need[2] or need[3],
+                                   pair_axes=pair_axes, table_dtype=table_dtype)
+            return *(g if n else None for g, n in zip(got, need)), None, None, None
+
+    _QK_NORM_FN = QkNormFn
+    return QkNormFn
+
+
+def qk_norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, rotary_mode="interleave",
+                   partial_slice=None, eps: float = 1e-6, pair_axes=None, table_dtype=None):
+    """:func:`rope_qk_norm_fwd` recorded for autograd: returns new tensors
+    (q, k); gradients go to q, k and both weights, and not to positions and
+    inv_freq. Differentiable once, not in forward mode."""
+    how = (rotary_mode, None if partial_slice is None else (int(partial_slice[0]), int(partial_slice[1])), eps,
+           None if pair_axes is None else tuple(pair_axes), table_dtype)
+    return _qk_norm_fn().apply(q, k, q_weight, k_weight, positions, inv_freq, how)
 
 
 def rope_proj_fwd(x, w, r1, r2, heads: int, rotary_mode="interleave", partial_slice=None, out=None,

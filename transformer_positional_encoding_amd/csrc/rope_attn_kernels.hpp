@@ -1,0 +1,244 @@
+// rope_attn_kernels.hpp -- attention of new tokens over a paged cache held in 4
+// bits. Included by rope_attn.hip, next to the host code that launches them.
+//
+// Mathematics. A sequence's query rows q (the new tokens by the heads that share
+// a cached head) and cached tokens t, with k_t and v_t codes times the scales of
+// their groups of lanes:
+//   x_t = scale q.k_t,  m = max x_t,  l = sum exp(x_t - m),  o = sum exp(x_t - m) v_t / l
+// over the tokens that a row sees, in one pass with the running m, l and o. A
+// part of a sequence's tokens leaves m, l and sum exp(x_t - m) v_t; parts are
+// joined in order by a second kernel.
+#pragma once
+
+#include "rope_cache_kernels.hpp"
+
+namespace rope {
+namespace {
+
+struct AttnArgs {
+    Rows q, out;
+    CacheRef kc, vc;
+    uint32_t D, Dv, S, Hq, heads, rep;
+    uint32_t rows;             // of a cached head: S * rep; row r is token r / rep, head r % rep of the group
+    uint32_t tiles;            // of rows
+    uint32_t splits;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lengths;
+    const int32_t* counts;
+    int64_t pages;
+    int32_t most;              // tokens that a block table holds
+    float scale2;              // scale * log2(e)
+    int32_t causal;
+    float* part;               // per part, sequence, token and head: Dv sums; then m and l of all
+    uint64_t part_rows;        // B * S * Hq
+    FastDiv rep_div, heads_div, tiles_div, splits_div, page_div;
+};
+
+// A block's place: part, tile of rows, cached head, sequence.
+struct AttnAt {
+    uint32_t split, tile, head, b;
+};
+
+__device__ __forceinline__ AttnAt attn_at(const AttnArgs& a, uint32_t block)
+{
+    AttnAt p;
+    uint32_t i = fast_div(block, a.splits_div);
+    p.split = block - i * a.splits;
+    uint32_t j = fast_div(i, a.tiles_div);
+    p.tile = i - j * a.tiles;
+    p.b = fast_div(j, a.heads_div);
+    p.head = j - p.b * a.heads;
+    return p;
+}
+
+// A sequence: its cached tokens, its new ones, and the place of the first.
+struct AttnSeq {
+    int32_t tokens;            // that the block table holds
+    int32_t count;             // rows that are computed
+    int64_t first;             // query s stands at token first + s
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, uint32_t b)
+{
+    AttnSeq s;
+    const int32_t length = a.lengths[b];
+    const int32_t count = a.counts != nullptr ? a.counts[b] : (int32_t)a.S;
+    s.count = min(max(count, 0), (int32_t)a.S);
+    s.first = (int64_t)length - s.count;
+    s.tokens = min(max(length, 0), a.most);
+    return s;
+}
+
+// The tokens [*t0, *t1) of part `split` of `splits` of n tokens, in whole units.
+__device__ __forceinline__ void attn_part(uint32_t n, uint32_t split, uint32_t splits, uint32_t unit, uint32_t* t0, uint32_t* t1)
+{
+    const uint32_t units = (n + unit - 1) / unit, per = (units + splits - 1) / splits;
+    *t0 = (uint32_t)min((uint64_t)n, (uint64_t)split * per * unit);
+    *t1 = (uint32_t)min((uint64_t)n, ((uint64_t)split + 1) * per * unit);
+}
+
+// The partial result of (part, sequence, token, head).
+__device__ __forceinline__ uint64_t part_row(const AttnArgs& a, uint32_t split, uint32_t b, uint32_t s, uint32_t h)
+{
+    return (uint64_t)split * a.part_rows + ((uint64_t)b * a.S + s) * a.Hq + h;
+}
+
+__device__ __forceinline__ float2* part_stats(const AttnArgs& a)
+{
+    return reinterpret_cast<float2*>(a.part + (uint64_t)a.splits * a.part_rows * a.Dv);
+}
+
+// ---------------------------------------------------------------------------
+// General kernel: any dimensions, groups, alignment and types. A block takes up
+// to 4 rows that share a cached head, 256 tokens at a time: a thread a token's
+// products with q, then a thread one to four lanes of v.
+// ---------------------------------------------------------------------------
+constexpr int kAttnGenThreads = 256;
+constexpr int kAttnGenRows = 4;
+constexpr float kAttnNone = -__builtin_inff();
+
+template <int DT>
+__global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(AttnArgs a)
+{
+    __shared__ float q[kAttnGenRows][ROPE_D_LIMIT];
+    __shared__ float p[kAttnGenRows][kAttnGenThreads];
+    __shared__ int64_t v_at[kAttnGenThreads], vs_at[kAttnGenThreads];
+    __shared__ float red[kAttnGenRows][kAttnGenThreads / 64];
+    const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const AttnAt at = attn_at(a, blockIdx.x);
+    const AttnSeq seq = attn_seq(a, at.b);
+    const uint32_t r0 = at.tile * kAttnGenRows;
+    const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
+    if (r0 >= live) return;                      // the same for the whole block
+    const uint32_t nr = min((uint32_t)kAttnGenRows, live - r0);
+    for (uint32_t r = 0; r < nr; ++r) {
+        const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
+        for (uint32_t j = t; j < a.D; j += kAttnGenThreads)
+            q[r][j] = Store<DT>::load1(a.q.data, at.b * a.q.sb + s * a.q.ss + h * a.q.sn + j);
+    }
+    float m[kAttnGenRows], l[kAttnGenRows], o[kAttnGenRows][ROPE_D_LIMIT / kAttnGenThreads];
+    int64_t last[kAttnGenRows];                  // the last token that the row sees
+    for (int r = 0; r < kAttnGenRows; ++r) {
+        m[r] = kAttnNone;
+        l[r] = 0.0f;
+        for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) o[r][k] = 0.0f;
+        last[r] = a.causal ? seq.first + fast_div(min(r0 + r, a.rows - 1), a.rep_div) : INT64_MAX;
+    }
+    uint32_t from, to;
+    attn_part((uint32_t)seq.tokens, at.split, a.splits, kAttnGenThreads, &from, &to);
+    __syncthreads();
+    for (uint32_t base = from; base < to; base += kAttnGenThreads) {
+        const uint32_t tok = base + t;
+        int64_t page = -1, in_page = 0;
+        if (tok < to) {
+            const uint32_t col = fast_div(tok, a.page_div);
+            page = a.table[at.b * a.table_stride + col];
+            in_page = tok - col * a.page_div.d;
+        }
+        const bool there = page >= 0 && page < a.pages;
+        float x[kAttnGenRows];
+        for (int r = 0; r < kAttnGenRows; ++r) x[r] = 0.0f;
+        if (there) {
+            const char* k = a.kc.data + page * a.kc.st[0] + in_page * a.kc.st[1] + at.head * a.kc.st[2];
+            const float* ks = a.kc.scales + page * a.kc.sc[0] + in_page * a.kc.sc[1] + at.head * a.kc.sc[2];
+            for (uint32_t g = 0; g * a.kc.group < a.D; ++g) {
+                float dot[kAttnGenRows] = {};
+                for (uint32_t j = g * a.kc.group; j < (g + 1) * a.kc.group; j += 2) {
+                    const uint32_t w = (uint8_t)k[j / 2];
+                    const float c0 = (float)((int32_t)(w << 28) >> 28), c1 = (float)((int32_t)(w << 24) >> 28);
+                    for (int r = 0; r < kAttnGenRows; ++r)
+                        dot[r] = __builtin_fmaf(q[r][j + 1], c1, __builtin_fmaf(q[r][j], c0, dot[r]));
+                }
+                for (int r = 0; r < kAttnGenRows; ++r) x[r] = __builtin_fmaf(dot[r], ks[g], x[r]);
+            }
+        }
+        v_at[t] = there ? page * a.vc.st[0] + in_page * a.vc.st[1] + at.head * a.vc.st[2] : -1;
+        vs_at[t] = page * a.vc.sc[0] + in_page * a.vc.sc[1] + at.head * a.vc.sc[2];
+        // the tile's maxima
+        for (int r = 0; r < kAttnGenRows; ++r) {
+            x[r] = there && (int64_t)tok <= last[r] ? x[r] * a.scale2 : kAttnNone;
+            float most = x[r];
+            for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+            if (lane == 0) red[r][wave] = most;
+        }
+        __syncthreads();
+        for (int r = 0; r < kAttnGenRows; ++r) {
+            float most = m[r];
+            for (int w = 0; w < kAttnGenThreads / 64; ++w) most = fmaxf(most, red[r][w]);
+            const float keep = m[r] == most ? 1.0f : exp2f(m[r] - most);
+            m[r] = most;
+            const bool seen = there && (int64_t)tok <= last[r];
+            const float e = !seen ? 0.0f : exp2f(x[r] - most);
+            p[r][t] = e;
+            l[r] = l[r] * keep + e;              // this thread's share
+            for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) o[r][k] *= keep;
+        }
+        __syncthreads();
+        const uint32_t n = min((uint32_t)kAttnGenThreads, to - base);
+        for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
+            const uint32_t j = k * kAttnGenThreads + t;
+            if (j >= a.Dv) continue;
+            const uint32_t g = j / a.vc.group;
+            for (uint32_t i = 0; i < n; ++i) {
+                if (v_at[i] < 0) continue;
+                const uint32_t w = (uint8_t)a.vc.data[v_at[i] + j / 2];
+                const float v = (float)((int32_t)(w << ((j & 1u) ? 24 : 28)) >> 28) * a.vc.scales[vs_at[i] + g];
+                for (int r = 0; r < kAttnGenRows; ++r)
+                    if (p[r][i] != 0.0f) o[r][k] = __builtin_fmaf(p[r][i], v, o[r][k]);
+            }
+        }
+        __syncthreads();                         // the next tile overwrites p, v_at and red
+    }
+    for (int r = 0; r < kAttnGenRows; ++r) {
+        float sum = l[r];
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        if (lane == 0) red[r][wave] = sum;
+    }
+    __syncthreads();
+    for (uint32_t r = 0; r < nr; ++r) {
+        float sum = 0.0f;
+        for (int w = 0; w < kAttnGenThreads / 64; ++w) sum += red[r][w];
+        const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
+        const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;      // NaN stays
+        const uint64_t row = part_row(a, at.split, at.b, s, h);
+        for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
+            const uint32_t j = k * kAttnGenThreads + t;
+            if (j >= a.Dv) continue;
+            if (a.splits == 1) Store<DT>::store1(a.out.data, at.b * a.out.sb + s * a.out.ss + h * a.out.sn + j, o[r][k] * inv);
+            else a.part[row * a.Dv + j] = o[r][k];
+        }
+        if (a.splits > 1 && t == 0) part_stats(a)[row] = make_float2(m[r], sum);
+    }
+}
+
+// Joins the parts of a row: a wave a row, the parts in order.
+template <int DT>
+__global__ void __launch_bounds__(256) rope_attn_join_kernel(AttnArgs a)
+{
+    const uint64_t row64 = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row64 >= a.part_rows) return;
+    const uint32_t row = (uint32_t)row64, lane = threadIdx.x & 63;
+    const uint32_t tok = row / a.Hq, h = row - tok * a.Hq, b = tok / a.S, s = tok - b * a.S;
+    if ((int32_t)s >= attn_seq(a, b).count) return;
+    const float2* stats = part_stats(a);
+    float m = kAttnNone;
+    for (uint32_t i = 0; i < a.splits; ++i) m = fmaxf(m, stats[(uint64_t)i * a.part_rows + row].x);
+    float l = 0.0f, o[ROPE_D_LIMIT / 64] = {};
+    for (uint32_t i = 0; i < a.splits; ++i) {
+        const float2 st = stats[(uint64_t)i * a.part_rows + row];
+        if (st.x == kAttnNone && st.y == 0.0f) continue;         // the part saw nothing
+        const float w = st.x == m ? 1.0f : exp2f(st.x - m);
+        l = __builtin_fmaf(st.y, w, l);
+#pragma unroll
+        for (int k = 0; k < ROPE_D_LIMIT / 64; ++k)
+            if (k * 64 + lane < a.Dv) o[k] = __builtin_fmaf(a.part[((uint64_t)i * a.part_rows + row) * a.Dv + k * 64 + lane], w, o[k]);
+    }
+    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+#pragma unroll
+    for (int k = 0; k < ROPE_D_LIMIT / 64; ++k)
+        if (k * 64 + lane < a.Dv) Store<DT>::store1(a.out.data, b * a.out.sb + s * a.out.ss + h * a.out.sn + k * 64 + lane, o[k] * inv);
+}
+
+}  // namespace
+}  // namespace rope

@@ -6,46 +6,10 @@
 #include <algorithm>
 #include <string>
 
-#include "rope_cache_kernels.hpp"
-#include "rope_cache_plan.hpp"
-#include "rope_host.hpp"
+#include "rope_rows_host.hpp"
 
 namespace rope {
 namespace {
-
-Rows rows_of(const RowsPlan& p) { return Rows{p.data, p.sb, p.ss, p.sn}; }
-
-CacheRef cache_of(const CachePlan& p)
-{
-    CacheRef c{};
-    c.data = p.data;
-    c.scales = p.scales;
-    for (int k = 0; k < 3; ++k) {
-        c.st[k] = p.st[k];
-        c.sc[k] = p.sc[k];
-    }
-    c.group = (uint32_t)std::max<int64_t>(1, p.group);
-    return c;
-}
-
-Turn turn_of(const Plan& p)
-{
-    Turn t{};
-    t.pos = p.pos;
-    t.inv_freq = p.inv_freq;
-    t.sb = p.pos_sb;
-    t.ss = p.pos_ss;
-    t.ax.sa = p.pos_sa;
-    t.ax.nwords = p.naxes > 1 ? (uint32_t)((p.L / 2 + 15) / 16) : 0;
-    std::copy(std::begin(p.axis_words), std::end(p.axis_words), t.ax.words);
-    t.tdt = p.tdtype;
-    t.start = (uint32_t)p.start;
-    t.L = (uint32_t)p.L;
-    t.half = (uint32_t)std::max<int64_t>(1, p.half);
-    t.pairs = (uint32_t)(p.L / 2);
-    t.half_div = make_fastdiv(t.half);
-    return t;
-}
 
 int kernel_format(const CachePlan& c) { return c.quantised ? c.format : kFmtSame; }
 
@@ -168,13 +132,6 @@ struct ReadWaveTurn {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_cache_read_wave_kernel<DT, FMT, true>); }
 };
 
-// Whether 8-lane chunks of these rows are 16-byte aligned.
-bool rows_in_chunks(const RowsPlan& r, int esize)
-{
-    const int64_t per = 16 / esize;
-    return r.N == 0 || (r.D % 8 == 0 && aligned16(r.data) && r.sb % per == 0 && r.ss % per == 0 && r.sn % per == 0);
-}
-
 // Whether the codes of 8 lanes are aligned to their size.
 bool cache_in_chunks(const CachePlan& c)
 {
@@ -183,22 +140,6 @@ bool cache_in_chunks(const CachePlan& c)
     for (int k = 0; k < 3; ++k)
         if (c.st[k] % (int64_t)bytes != 0) return false;
     return true;
-}
-
-// Whether the slice is whole chunks whose partners are in the chunk or whole
-// chunks away.
-bool turn_in_chunks(const Plan& p)
-{
-    return p.start % 8 == 0 && p.L % 8 == 0 && (p.half == 1 || p.half % 8 == 0);
-}
-
-bool power_of_two(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
-
-uint32_t log2_of(uint32_t v)
-{
-    uint32_t s = 0;
-    while ((1u << s) < v) ++s;
-    return s;
 }
 
 // Chunks per scale for the write kernel: 0 for one scale a row; -1 if the
@@ -330,12 +271,6 @@ hipError_t launch_read(const CacheReadPlan& p, hipStream_t s)
     const uint64_t blocks = std::min<uint64_t>((uint64_t)p.B * (uint64_t)p.S, kMaxGridItems / kGenReadThreads);
     return hipLaunchKernel(by_types<ReadGeneral>(p.rope.dtype, fmt), dim3((uint32_t)blocks), dim3(kGenReadThreads), args,
                            0, s);
-}
-
-rope_status_t launched(hipError_t err)
-{
-    if (err != hipSuccess) return set_error(ROPE_ERR_RUNTIME, std::string("kernel launch: ") + hipGetErrorString(err));
-    return ROPE_OK;
 }
 
 }  // namespace

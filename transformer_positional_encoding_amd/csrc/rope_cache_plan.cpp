@@ -10,13 +10,14 @@ namespace {
 
 constexpr int64_t kI64Max = std::numeric_limits<int64_t>::max();
 
+}  // namespace
+
 rope_status_t fail(rope_status_t st, std::string* why, const std::string& msg)
 {
     if (why) *why = msg;
     return st;
 }
 
-// Sum of (count - 1) * stride over dimensions plus `last`, or -1 past 64 bits.
 int64_t extent(const int64_t counts[], const int64_t strides[], int n, int64_t last)
 {
     int64_t sum = last;
@@ -29,9 +30,8 @@ int64_t extent(const int64_t counts[], const int64_t strides[], int n, int64_t l
     return sum;
 }
 
-// Whether no two index triples reach a common element of rows of `width`:
-// by rising stride, each dimension steps past everything the smaller ones
-// cover. (Sufficient, and met by every slice or permutation of a tensor.)
+// By rising stride, each dimension steps past everything the smaller ones
+// cover.
 bool disjoint_rows(const int64_t counts[3], const int64_t strides[3], int64_t width)
 {
     int64_t c[3], s[3];
@@ -75,7 +75,6 @@ rope_status_t check_rows(const char* name, const rope_rows_t& r, int64_t B, int6
     return ROPE_OK;
 }
 
-// A cache's own fields; `written`: its rows must not overlap.
 rope_status_t check_cache(const char* name, const rope_cache_t& c, rope_dtype_t dtype, bool written, CachePlan* p,
                           std::string* why)
 {
@@ -131,8 +130,6 @@ rope_status_t check_data(const char* name, const RowsPlan& r, int esize, std::st
         return fail(ROPE_ERR_INVALID, why, std::string(name) + ": data not aligned to its elements");
     return ROPE_OK;
 }
-
-}  // namespace
 
 rope_status_t make_cache_write_plan(int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* q,
                                     const rope_rows_t* k, const rope_rows_t* v, const rope_cache_t* k_cache,

@@ -61,6 +61,29 @@ inline int64_t cache_row_bytes(int format, int64_t dim)
     }
 }
 
+// ---- checks shared by the calls on rows and caches; each writes a one-line
+// reason to `why` on failure.
+rope_status_t fail(rope_status_t st, std::string* why, const std::string& msg);
+
+// Sum of (count - 1) * stride over dimensions plus `last`, or -1 past 64 bits.
+int64_t extent(const int64_t counts[], const int64_t strides[], int n, int64_t last);
+
+// Whether no two index triples reach a common element of rows of `width`.
+// (Sufficient, and met by every slice or permutation of a tensor.)
+bool disjoint_rows(const int64_t counts[3], const int64_t strides[3], int64_t width);
+
+// The strides of (B, S, r.N, r.D) rows; `written`: they must not overlap.
+rope_status_t check_rows(const char* name, const rope_rows_t& r, int64_t B, int64_t S, int esize, bool written,
+                         RowsPlan* p, std::string* why);
+
+// A cache's own fields; `written`: its rows must not overlap.
+rope_status_t check_cache(const char* name, const rope_cache_t& c, rope_dtype_t dtype, bool written, CachePlan* p,
+                          std::string* why);
+
+// Pointers that are looked at: not NULL, aligned to their elements.
+rope_status_t check_pointers(const char* name, const CachePlan& c, std::string* why);
+rope_status_t check_data(const char* name, const RowsPlan& r, int esize, std::string* why);
+
 rope_status_t make_cache_write_plan(int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* q,
                                     const rope_rows_t* k, const rope_rows_t* v, const rope_cache_t* k_cache,
                                     const rope_cache_t* v_cache, const int64_t* slots,
