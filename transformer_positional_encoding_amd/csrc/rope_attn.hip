@@ -5,7 +5,8 @@
 #include <algorithm>
 #include <string>
 
-#include "rope_attn_kernels.hpp"
+#include "rope_attn_host.hpp"
+#include "rope_attn_mfma_kernels.hpp"
 #include "rope_attn_plan.hpp"
 #include "rope_rows_host.hpp"
 
@@ -64,17 +65,53 @@ AttnArgs attn_args(const AttnPlan& p)
     return a;
 }
 
+// Whether rows of codes start and step at multiples of `bytes`.
+bool codes_aligned(const CachePlan& c, uintptr_t bytes)
+{
+    return reinterpret_cast<uintptr_t>(c.data) % bytes == 0 && c.st[0] % (int64_t)bytes == 0 &&
+           c.st[1] % (int64_t)bytes == 0 && c.st[2] % (int64_t)bytes == 0;
+}
+
+// The matrix-core kernel of a call, and its lanes; NULL if it does not take the
+// shapes.
+const void* mfma_kernel(const AttnPlan& p, int tiles, int lanes)
+{
+    const int64_t D = p.q.D, Dv = p.out.D;
+    if (p.rope.dtype == ROPE_DTYPE_F32 || D > 256 || Dv > 256 || !rows_in_chunks(p.q, 2) || !rows_in_chunks(p.out, 2))
+        return nullptr;
+    const bool k_row = p.kc.group == D, v_row = p.vc.group == Dv;
+    if ((!k_row && p.kc.group % 32 != 0) || (!v_row && p.vc.group % 32 != 0)) return nullptr;
+    const bool k_whole = k_row && D == lanes && codes_aligned(p.kc, lanes == 64 ? 8 : 16);
+    const int scales = !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
+    if (!codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4)) return nullptr;
+    return p.rope.dtype == ROPE_DTYPE_BF16 ? attn_kernel_bf16(lanes, scales, tiles) : attn_kernel_f16(lanes, scales, tiles);
+}
+
 rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
 {
-    AttnArgs a = attn_args(p);
-    void* args[] = {&a};
-    a.tiles = (a.rows + kAttnGenRows - 1) / kAttnGenRows;
+    AttnVecArgs a{};
+    static_cast<AttnArgs&>(a) = attn_args(p);
+    const int lanes = std::max(p.q.D, p.out.D) <= 64 ? 64 : std::max(p.q.D, p.out.D) <= 128 ? 128 : 256;
+    const int tiles = lanes == 256 || a.rows <= 16 ? 1 : 2;
+    const void* fn = mfma_kernel(p, tiles, lanes);
+    const bool mfma = fn != nullptr;
+    a.join = a.rows <= 64;
+    a.k_group = a.kc.group;
+    a.v_group = a.vc.group;
+    a.k_groups = a.D / a.k_group;
+    a.v_groups = a.Dv / a.v_group;
+    const uint32_t block_rows = !mfma ? kAttnGenRows : (a.join ? 16 : 64) * tiles;
+    a.tiles = (a.rows + block_rows - 1) / block_rows;
     a.tiles_div = make_fastdiv(a.tiles);
     const uint64_t blocks = (uint64_t)p.B * a.heads * a.tiles * a.splits;
     if (blocks >= (1ull << 31) || blocks > kMaxGridItems / kAttnGenThreads)
         return set_error(ROPE_ERR_UNSUPPORTED, "a grid too large for one launch");
-    hipError_t err = hipLaunchKernel(by_type<General>(p.rope.dtype), dim3((uint32_t)blocks), dim3(kAttnGenThreads), args, 0, s);
+    AttnArgs g = a;
+    void* args[] = {mfma ? (void*)&a : (void*)&g};
+    hipError_t err = hipLaunchKernel(mfma ? fn : by_type<General>(p.rope.dtype), dim3((uint32_t)blocks), dim3(kAttnGenThreads),
+                                     args, 0, s);
     if (err != hipSuccess || a.splits == 1) return launched(err);
+    args[0] = &g;
     return launched(hipLaunchKernel(by_type<Join>(p.rope.dtype), dim3((uint32_t)((a.part_rows + 3) / 4)), dim3(256), args, 0, s));
 }
 

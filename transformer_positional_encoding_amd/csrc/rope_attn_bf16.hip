@@ -1,0 +1,8 @@
+// The matrix-core attention kernels for bf16 queries.
+#include "rope_attn_select.hpp"
+
+namespace rope {
+
+const void* attn_kernel_bf16(int lanes, int scales, int tiles) { return attn_kernel<ROPE_DTYPE_BF16>(lanes, scales, tiles); }
+
+}  // namespace rope

@@ -1,0 +1,18 @@
+// What the attention's launch and its kernels' translation units share.
+#pragma once
+
+namespace rope {
+
+// Scales of a cached row: one of K and one of V; K's by 32-lane steps (also
+// where rows are short of the kernel's lanes, or not aligned for one load), V's
+// one; both by 32-lane segments.
+constexpr int kAttnRowScales = 0;
+constexpr int kAttnKSegments = 1;
+constexpr int kAttnSegments = 2;
+
+// The kernel for rows of up to `lanes` lanes (64, 128, 256) and `tiles` tiles of
+// 16 rows a wave (1; 2 up to 128 lanes).
+const void* attn_kernel_bf16(int lanes, int scales, int tiles);
+const void* attn_kernel_f16(int lanes, int scales, int tiles);
+
+}  // namespace rope

@@ -1,0 +1,578 @@
+// rope_attn_mfma_kernels.hpp -- attention over a cache held in 4 bits on the
+// matrix cores: 16-bit queries, rows of whole 8-lane chunks up to 256 lanes,
+// one scale a row or groups of whole 32-lane segments.
+// Included by rope_attn.hip.
+//
+// A wave takes 16 query rows (NT such tiles) and 64 cached tokens at a time.
+// Both products have the cached rows as their first operand, so that a query
+// row is a column of every accumulator, one lane's: x^T = K Q^T, o^T = V^T P^T.
+// The weights then leave the first product in the very lanes and order in which
+// the second takes them (a product's sum may take its tokens in any order), and
+// a row's running maximum and sum are a lane's own but for two exchanges.
+//
+// Codes to numbers. A nibble n = code + 8 put into the fraction of 16 makes 16 +
+// n, an exact bf16 and fp16 number, for a shift and one more operation per two
+// codes; K stays like that and the accumulator starts from -24 sum(q). V's
+// sums run over many tokens, where such a part would cost digits: its nibbles
+// become 1024 + n in fp16 and lose the 1032 by a packed subtraction. The order
+// of lanes within a product is free too: a lane takes a 32-bit word of 8 codes
+// of a K row as it comes (pairs of nibbles 16 bits apart, q's fragment in the
+// same order), and of V the words of 8 tokens at the same place of their rows,
+// whose 16-bit halves, put side by side, hold the codes of two tokens at equal
+// nibbles. With a scale for each segment of 32 lanes (VF) a segment has to be
+// whole products, a byte a lane: lanes in fours exchange the bytes of words of
+// four segments.
+//
+// Scales stay outside of the products: K's multiply the finished sums of their
+// lanes (one a row, or one for each 32-lane step, KF), V's the weights. exp(x -
+// m) times V's scale is rounded to fp16, times a power of two that keeps the
+// row's largest such weight of a segment within 2^-1 and 2^8 (2^-e below), so
+// that only weights below 2^-13 of the largest lose digits, and at most 2^-24
+// of it. m follows the maximum when it is passed by 2^6; a tile that moves
+// neither m nor e leaves the accumulators as they are.
+//
+// The bytes are 4 bits a code; at the rate of a large copy that is 10^13 codes a
+// second, against 4 * 10^13 operations of the vector units, so operations per
+// code decide: 1.1 for K, 1.6 for V (2.1 with VF), the softmax 0.4 for 4 rows
+// a head (its 16 columns) and 128 lanes.
+//
+// Loads go straight to registers, a tile ahead; addresses by a lane a token,
+// through the wave's part of LDS. Four waves of a block share the rows and take
+// tiles in turn (join), or have rows of their own.
+#pragma once
+
+#include "rope_attn_kernels.hpp"
+
+namespace rope {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t v3u __attribute__((ext_vector_type(3)));
+
+struct AttnVecArgs : AttnArgs {
+    int32_t join;              // the block's waves share their rows
+    uint32_t k_groups, v_groups;   // scales of a row
+    uint32_t k_group, v_group;     // lanes of each
+};
+
+template <int DT>
+__device__ __forceinline__ f32x4 attn_mfma(const v4u& a, const v4u& b, const f32x4& c)
+{
+    if constexpr (DT == ROPE_DTYPE_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// 8 codes as 16 + (code + 8), nibbles i and i + 4 in the halves of word i.
+template <int DT>
+__device__ __forceinline__ v4u k_numbers(uint32_t w)
+{
+    w ^= 0x88888888u;
+    if constexpr (DT == ROPE_DTYPE_BF16) {
+        constexpr uint32_t mask = 0x00780078u, one = 0x41804180u;
+        return v4u{((w << 3) & mask) | one, ((w >> 1) & mask) | one, ((w >> 5) & mask) | one, ((w >> 9) & mask) | one};
+    } else {
+        constexpr uint32_t mask = 0x03C003C0u, one = 0x4C004C00u;
+        return v4u{((w << 6) & mask) | one, ((w << 2) & mask) | one, ((w >> 2) & mask) | one, ((w >> 6) & mask) | one};
+    }
+}
+
+// 8 elements of a query row in the order of k_numbers.
+__device__ __forceinline__ v4u q_order(const v4u& v)
+{
+    return v4u{__builtin_amdgcn_perm(v[2], v[0], 0x05040100), __builtin_amdgcn_perm(v[2], v[0], 0x07060302),
+               __builtin_amdgcn_perm(v[3], v[1], 0x05040100), __builtin_amdgcn_perm(v[3], v[1], 0x07060302)};
+}
+
+// The codes that stand at nibbles `sh` / 4 of both halves of w (code + 8 each).
+__device__ __forceinline__ uint32_t v_numbers(uint32_t w, int sh)
+{
+    const f16x2 n = __builtin_bit_cast(f16x2, ((w >> sh) & 0x000F000Fu) | 0x64006400u);
+    return __builtin_bit_cast(uint32_t, n - f16x2{(_Float16)1032.0f, (_Float16)1032.0f});
+}
+
+// Word i of lane i of four (by lane number) receives byte a of lane a's word in
+// its byte a.
+__device__ __forceinline__ uint32_t quad_bytes(uint32_t w, uint32_t sel1, uint32_t sel2)
+{
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);     // lane ^ 1
+    w = __builtin_amdgcn_perm(o, w, sel1);
+    const uint32_t p = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0x4E, 0xF, 0xF, true);     // lane ^ 2
+    return __builtin_amdgcn_perm(p, w, sel2);
+}
+
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Over the four lanes that hold a column.
+__device__ __forceinline__ float column_max(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float column_sum(float v)
+{
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+template <int DP, int DVP, bool KF, bool VF, int NT>
+struct alignas(16) AttnLds {
+    static constexpr int NGK = KF ? DP / 32 : 1, NGV = VF ? DVP / 32 : 1;
+    struct Wave {
+        int64_t k_at[64], v_at[64];
+        float ks[NGK][64], vs[NGV][64];
+    };
+    struct Join {
+        float o[4][16][DVP + 4];
+        float m[4][16], l[4][16];
+    };
+    union {
+        Wave wave[4];
+        Join join;
+    };
+};
+
+template <int DT, int DP, int DVP, bool KF, bool VF, int NT>
+__global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
+{
+    using Lds = AttnLds<DP, DVP, KF, VF, NT>;
+    constexpr int KW = DP / 32;                    // words of a K row that a lane takes
+    constexpr int VT = DVP / 16;                   // products of 16 lanes of V
+    constexpr int VR = DVP >= 128 ? DVP / 128 : 1; // registers of a token's V
+    constexpr int VH = DVP / 64;                   // 16-bit halves of them
+    constexpr int NGK = Lds::NGK, NGV = Lds::NGV;
+    __shared__ Lds lds;
+    const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typename Lds::Wave& my = lds.wave[wave];
+
+    const AttnAt at = attn_at(a, blockIdx.x);
+    const AttnSeq seq = attn_seq(a, at.b);
+    const uint32_t waves = a.join ? 4 : 1;         // that share a tile of rows
+    const uint32_t block_row = at.tile * (a.join ? 16 * NT : 64 * NT);
+    const uint32_t r0 = a.join ? block_row : block_row + wave * 16 * NT;
+    const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
+    if (r0 >= live) return;                        // with join the same for the whole block
+    // the tokens that some row sees, this part of them, and those that all see
+    uint32_t n = (uint32_t)seq.tokens, all = n;
+    if (a.causal) {
+        const int64_t most = seq.first + fast_div(min(r0 + 16 * NT, live) - 1, a.rep_div) + 1;
+        const int64_t least = seq.first + fast_div(r0, a.rep_div) + 1;
+        n = (uint32_t)max((int64_t)0, min((int64_t)n, most));
+        all = (uint32_t)max((int64_t)0, min((int64_t)n, least));
+    }
+    uint32_t from, to;
+    attn_part(n, at.split, a.splits, 64 * waves, &from, &to);
+    all = min(all, to);
+
+    // queries: a column a row, 8 elements a step in k_numbers' order
+    v4u q[NT][KW];
+    f32x4 start[NT][KF ? KW : 1];
+    int32_t last[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const uint32_t r = min(r0 + t * 16 + n16, live - 1);
+        const uint32_t s = fast_div(r, a.rep_div), h = at.head * a.rep + (r - s * a.rep);
+        last[t] = a.causal ? (int32_t)(seq.first + s) : INT32_MAX;
+        const gchar* row = as_global(a.q.data) + (at.b * a.q.sb + s * a.q.ss + h * a.q.sn) * 2;
+        float sum = 0.0f;
+#pragma unroll
+        for (int st = 0; st < KW; ++st) {
+            const uint32_t d = KF ? 32 * st + 8 * kq : kq * (DP / 4) + 8 * st;
+            v4u v{0, 0, 0, 0};
+            if (d < a.D) v = gload<v4u>(row + d * 2);
+            Lanes<DT> f;
+            f.unpack(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += f.v[e];
+            q[t][st] = q_order(v);
+            if (KF || st == KW - 1) {
+                const float c = -24.0f * column_sum(sum);
+                start[t][KF ? st : 0] = f32x4{c, c, c, c};
+                sum = 0.0f;
+            }
+        }
+    }
+
+    // where this lane's words of a row start
+    const gchar* const k_base = as_global(a.kc.data) + at.head * a.kc.st[2];
+    const gchar* const v_base = as_global(a.vc.data) + at.head * a.vc.st[2];
+    const gchar* const ks_base = as_global(a.kc.scales) + at.head * a.kc.sc[2] * 4;
+    const gchar* const vs_base = as_global(a.vc.scales) + at.head * a.vc.sc[2] * 4;
+    const int32_t* const table = a.table + at.b * a.table_stride;
+    const uint32_t k_bytes = a.D / 2, v_bytes = a.Dv / 2;
+    const uint32_t q4 = n16 >> 2, a4 = n16 & 3, q2 = n16 >> 1, a2 = n16 & 1;
+    const uint32_t sel1 = (lane & 1) ? 0x03070105u : 0x06020400u;
+    const uint32_t sel2 = (lane & 2) ? 0x03020706u : 0x05040100u;
+
+    struct Place {
+        int32_t page;
+        uint32_t in_page;
+    };
+    const auto look_up = [&](uint32_t base) -> Place {
+        const uint32_t tok = base + lane;
+        Place p{-1, 0};
+        if (tok < to) {
+            const uint32_t col = fast_div(tok, a.page_div);
+            p.page = table[col];
+            p.in_page = tok - col * a.page_div.d;
+        }
+        return p;
+    };
+
+    f32x4 acc[NT][VT];
+    float m[NT], l[NT], top[NT][NGV];
+    int32_t e[NT][NGV];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t] = kAttnNone;
+        l[t] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) {
+            top[t][g] = 0.0f;
+            e[t][g] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < VT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
+    }
+
+    uint32_t kw[4][KW], vw[16][VR];
+    float ks[NGK], vs[NGV];
+    bool there = false;
+    // addresses, scales and codes of a tile whose pages are known
+    const auto fetch = [&](const Place& p) {
+        there = p.page >= 0 && p.page < a.pages;
+        const int64_t page = there ? p.page : 0, in_page = there ? p.in_page : 0;
+        my.k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
+        my.v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
+        const gchar* sk = ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1]) * 4;
+        const gchar* sv = vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1]) * 4;
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) {
+            const uint32_t at_g = KF ? min((uint32_t)g * 32 / a.k_group, a.k_groups - 1) : 0;
+            ks[g] = there ? gload<float>(sk + at_g * 4) : 0.0f;
+        }
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) {
+            const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
+            vs[g] = there ? gload<float>(sv + at_g * 4) : 0.0f;
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const gchar* row = k_base + my.k_at[16 * i + n16];
+            if constexpr (KF) {
+#pragma unroll
+                for (int st = 0; st < KW; ++st) {
+                    const uint32_t off = 16 * st + 4 * kq;
+                    kw[i][st] = gload<uint32_t>(row + (off < k_bytes ? off : 0));
+                }
+            } else if constexpr (KW == 2) {
+                const v2u w = gload<v2u>(row + 8 * kq);
+                kw[i][0] = w[0];
+                kw[i][1] = w[1];
+            } else {
+#pragma unroll
+                for (int c = 0; c < KW / 4; ++c) {
+                    const v4u w = gload<v4u>(row + 4 * KW * kq + 16 * c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) kw[i][4 * c + j] = w[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const gchar* row = v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
+            if constexpr (VF && DVP == 64) {
+                const uint32_t off = 16 * a2 + 2 * q2;
+                vw[i][0] = gload<uint16_t>(row + (off < v_bytes ? off : 0));
+            } else if constexpr (VF) {
+#pragma unroll
+                for (int c = 0; c < VR; ++c) {
+                    const uint32_t off = 64 * c + 16 * a4 + 4 * q4;
+                    vw[i][c] = gload<uint32_t>(row + (off < v_bytes ? off : 0));
+                }
+            } else if constexpr (DVP == 64) {
+                const uint32_t off = 2 * n16;
+                vw[i][0] = gload<uint16_t>(row + (off < v_bytes ? off : 0));
+            } else if constexpr (DVP == 128) {
+                const uint32_t off = 4 * n16;
+                vw[i][0] = gload<uint32_t>(row + (off < v_bytes ? off : 0));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t off = 8 * n16 + 4 * c;
+                    vw[i][c] = gload<uint32_t>(row + (off < v_bytes ? off : 0));
+                }
+            }
+        }
+    };
+
+    const uint32_t step = 64 * waves;
+    uint32_t base = from + (a.join ? 64 * wave : 0);
+    Place next = look_up(base);
+    if (base < to) fetch(next);
+    next = look_up(base + step < base ? to : base + step);
+    for (; base < to; base += step) {
+        // the tile's scales, by token, and its codes
+        const uint64_t valid = __ballot(there);
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) my.ks[g][lane] = ks[g] * a.scale2;
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) my.vs[g][lane] = vs[g];
+        uint32_t kc[4][KW], vc[16][VR];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int st = 0; st < KW; ++st) kc[i][st] = kw[i][st];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int c = 0; c < VR; ++c) vc[i][c] = vw[i][c];
+        wave_sync();
+        if (to - base > step) {
+            fetch(next);
+            next = look_up(to - base > 2 * step ? base + 2 * step : to);
+        }
+
+        // x^T = K Q^T, a token a row of the product
+        f32x4 x[NT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int st = 0; st < KW; ++st) {
+                const v4u k = k_numbers<DT>(kc[i][st]);
+                if constexpr (KF) {
+                    const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[st][16 * i + 4 * kq]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const f32x4 d = attn_mfma<DT>(k, q[t][st], start[t][st]);
+                        if (st == 0) x[t][i] = d * s;
+                        else
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(d[r], s[r], x[t][i][r]);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) x[t][i] = attn_mfma<DT>(k, q[t][st], st == 0 ? start[t][0] : x[t][i]);
+                }
+            }
+            if constexpr (!KF) {
+                const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[0][16 * i + 4 * kq]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) x[t][i] *= s;
+            }
+        }
+        if (base + 64 > all || valid != ~0ull) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = (uint32_t)(valid >> (16 * i + 4 * kq));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int32_t tok = (int32_t)(base + 16 * i + 4 * kq + r);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) x[t][i][r] = ((bits >> r) & 1u) && tok <= last[t] ? x[t][i][r] : kAttnNone;
+                }
+            }
+        }
+
+        // the weights exp(x - m) and, by segments, what the second product takes
+        v4u p[NT][NGV][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float most = x[t][0][0];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) most = fmaxf(most, x[t][i][r]);
+            most = column_max(most);
+            float keep = 1.0f;
+            const bool moved = __any(most > m[t] + 6.0f);
+            if (moved) {
+                const float now = fmaxf(m[t], most);
+                keep = now == m[t] ? 1.0f : exp2f(m[t] - now);
+                m[t] = now;
+                l[t] *= keep;
+#pragma unroll
+                for (int g = 0; g < NGV; ++g) top[t][g] *= keep;
+            }
+            const float less = m[t] == kAttnNone ? 0.0f : m[t];
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    x[t][i][r] = __builtin_amdgcn_exp2f(x[t][i][r] - less);
+                    sum += x[t][i][r];
+                }
+            l[t] += sum;
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) {
+                f32x4 w[4];
+                float high = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = x[t][i] * *reinterpret_cast<const f32x4*>(&my.vs[g][16 * i + 4 * kq]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) high = fmaxf(high, fabsf(w[i][r]));
+                }
+                top[t][g] = fmaxf(top[t][g], column_max(high));
+                if (moved || __any(__builtin_ldexpf(top[t][g], -e[t][g]) > 256.0f)) {
+                    int32_t now = __builtin_amdgcn_frexp_expf(top[t][g]);
+                    now = top[t][g] > 0.0f ? min(max(now, -120), 120) : e[t][g];
+                    const float f = __builtin_ldexpf(keep, e[t][g] - now);
+                    e[t][g] = now;
+#pragma unroll
+                    for (int i = 0; i < VT / NGV; ++i) acc[t][g * (VT / NGV) + i] *= f;
+                }
+                const float c = __builtin_ldexpf(1.0f, -e[t][g]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4& v = w[2 * h + (j >> 1)];
+                        const f32x2 pair{v[2 * (j & 1)] * c, v[2 * (j & 1) + 1] * c};
+                        p[t][g][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
+                    }
+            }
+        }
+
+        // o^T += V^T P^T, 32 tokens a product
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t two[VH][4];                   // codes of two tokens at equal nibbles
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = 8 * h + 4 * (j >> 1) + 2 * (j & 1);
+                if constexpr (DVP == 64) {
+                    uint32_t w = vc[i][0] | (vc[i + 1][0] << 16);
+                    if constexpr (VF) {            // halves of two lanes: bytes 0, 2 and 1, 3 change places
+                        const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
+                        w = __builtin_amdgcn_perm(o, w, sel1);
+                    }
+                    two[0][j] = w ^ 0x88888888u;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < VR; ++c) {
+                        uint32_t w0 = vc[i][c], w1 = vc[i + 1][c];
+                        if constexpr (VF) {
+                            w0 = quad_bytes(w0, sel1, sel2);
+                            w1 = quad_bytes(w1, sel1, sel2);
+                        }
+                        two[2 * c][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100) ^ 0x88888888u;
+                        two[2 * c + 1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302) ^ 0x88888888u;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VT; ++i) {
+                v4u v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = v_numbers(two[i >> 2][j], 4 * (i & 3));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][VF ? i / 2 : 0][h], acc[t][i]);
+            }
+        }
+    }
+
+    // lane j of v that product i's row 4 kq + r holds
+    const auto lane_of = [&](int i, int r) -> uint32_t {
+        return VF ? 32 * (i >> 1) + 8 * kq + 2 * r + (i & 1) : VT * (4 * kq + r) + i;
+    };
+    // ... and 8 consecutive ones: number c of a lane's VT / 2
+    const auto eight_at = [&](int c) -> uint32_t { return VF ? 32 * c + 8 * kq : 4 * VT * kq + 8 * c; };
+    const auto eight = [&](const f32x4 (&o)[VT], int c, float (&v)[8], const float (&f)[NGV]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (VF) v[k] = o[2 * c + (k & 1)][k >> 1] * f[c];
+            else v[k] = o[(8 * c + k) % VT][(8 * c + k) / VT] * f[0];
+        }
+    };
+
+    if (!a.join) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t r = r0 + t * 16 + n16;
+            const float sum = column_sum(l[t]);
+            if (r >= live) continue;
+            const uint32_t s = fast_div(r, a.rep_div), h = at.head * a.rep + (r - s * a.rep);
+            const float inv = a.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+            float f[NGV];
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) f[g] = __builtin_ldexpf(inv, e[t][g]);
+            const uint64_t row = part_row(a, at.split, at.b, s, h);
+            gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
+#pragma unroll
+            for (int c = 0; c < VT / 2; ++c) {
+                float v[8];
+                eight(acc[t], c, v, f);
+                const uint32_t j = eight_at(c);
+                if (j >= a.Dv) continue;
+                if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
+                else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
+            }
+            if (a.splits > 1 && kq == 0) part_stats(a)[row] = make_float2(m[t], sum);
+        }
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const float sum = column_sum(l[t]);
+        __syncthreads();                           // the tiles (or the rows before) are done with this memory
+        if (kq == 0) {
+            lds.join.m[wave][n16] = m[t];
+            lds.join.l[wave][n16] = sum;
+        }
+        __syncthreads();
+        float most = lds.join.m[0][n16];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) most = fmaxf(most, lds.join.m[w][n16]);
+        const float keep = m[t] == kAttnNone ? 0.0f : m[t] == most ? 1.0f : exp2f(m[t] - most);
+#pragma unroll
+        for (int i = 0; i < VT; ++i) {
+            const float f = __builtin_ldexpf(keep, e[t][VF ? i / 2 : 0]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) lds.join.o[wave][n16][lane_of(i, r)] = acc[t][i][r] * f;
+        }
+        __syncthreads();
+        // 16 threads a row, 8 lanes at a time
+        const uint32_t row16 = threadIdx.x >> 4, r = r0 + t * 16 + row16;
+        if (r >= live) continue;                   // (the barriers above are passed by every thread again)
+        float high = lds.join.m[0][row16], whole = 0.0f;
+#pragma unroll
+        for (int w = 1; w < 4; ++w) high = fmaxf(high, lds.join.m[w][row16]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float mw = lds.join.m[w][row16];
+            whole += lds.join.l[w][row16] * (mw == kAttnNone ? 0.0f : mw == high ? 1.0f : exp2f(mw - high));
+        }
+        const uint32_t s = fast_div(r, a.rep_div), h = at.head * a.rep + (r - s * a.rep);
+        const float inv = a.splits > 1 ? 1.0f : whole > 0.0f ? 1.0f / whole : whole == 0.0f ? 0.0f : whole;
+        const uint64_t row = part_row(a, at.split, at.b, s, h);
+        gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
+        for (uint32_t j = 8 * (threadIdx.x & 15); j < a.Dv; j += 128) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = lds.join.o[0][row16][j + k];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) v[k] += lds.join.o[w][row16][j + k];
+                v[k] *= inv;
+            }
+            if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
+            else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
+        }
+        if (a.splits > 1 && (threadIdx.x & 15) == 0) part_stats(a)[row] = make_float2(high, whole);
+    }
+}
+
+}  // namespace
+}  // namespace rope
