@@ -28,8 +28,12 @@ struct General {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_general_kernel<DT>); }
 };
 template <int DT>
-struct Join {
-    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_kernel<DT>); }
+struct JoinFew {
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_kernel<DT, 1>); }
+};
+template <int DT>
+struct JoinMany {
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_kernel<DT, kJoinWaves>); }
 };
 
 AttnArgs attn_args(const AttnPlan& p)
@@ -112,7 +116,10 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
                                      args, 0, s);
     if (err != hipSuccess || a.splits == 1) return launched(err);
     args[0] = &g;
-    return launched(hipLaunchKernel(by_type<Join>(p.rope.dtype), dim3((uint32_t)((a.part_rows + 3) / 4)), dim3(256), args, 0, s));
+    const bool many = a.splits > 8;
+    const uint64_t rows = many ? 1 : kJoinWaves;
+    return launched(hipLaunchKernel(many ? by_type<JoinMany>(p.rope.dtype) : by_type<JoinFew>(p.rope.dtype),
+                                    dim3((uint32_t)((a.part_rows + rows - 1) / rows)), dim3(kJoinThreads), args, 0, s));
 }
 
 }  // namespace

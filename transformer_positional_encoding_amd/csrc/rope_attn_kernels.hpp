@@ -10,10 +10,13 @@
 // joined in order by a second kernel.
 #pragma once
 
+#include "rope_attn_plan.hpp"
 #include "rope_cache_kernels.hpp"
 
 namespace rope {
 namespace {
+
+constexpr float kAttnNone = -__builtin_inff();   // the maximum of nothing
 
 struct AttnArgs {
     Rows q, out;
@@ -96,7 +99,7 @@ __device__ __forceinline__ float2* part_stats(const AttnArgs& a)
 // ---------------------------------------------------------------------------
 constexpr int kAttnGenThreads = 256;
 constexpr int kAttnGenRows = 4;
-constexpr float kAttnNone = -__builtin_inff();
+
 
 template <int DT>
 __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(AttnArgs a)
@@ -212,32 +215,67 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
     }
 }
 
-// Joins the parts of a row: a wave a row, the parts in order.
-template <int DT>
-__global__ void __launch_bounds__(256) rope_attn_join_kernel(AttnArgs a)
+// Joins the parts of a row. W waves take a row's parts in turn, a strand of
+// lanes each, and are added in order: latency is all there is to it. (One wave
+// a row of 256 parts: 250 us.)
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWaves = kJoinThreads / 64;
+
+template <int DT, int W>
+__global__ void __launch_bounds__(kJoinThreads) rope_attn_join_kernel(AttnArgs a)
 {
-    const uint64_t row64 = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row64 >= a.part_rows) return;
-    const uint32_t row = (uint32_t)row64, lane = threadIdx.x & 63;
+    constexpr int R = kJoinWaves / W;              // rows of a block
+    constexpr int K = 4;                           // parts whose loads go out together
+    __shared__ float weight[R][W == 1 ? 1 : kAttnMaxParts];
+    __shared__ float sums[W == 1 ? 1 : W][W == 1 ? 1 : ROPE_D_LIMIT];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mine = wave % W;
+    const uint64_t row64 = (uint64_t)blockIdx.x * R + wave / W;
+    if (row64 >= a.part_rows) return;              // (W > 1: a row a block)
+    const uint32_t row = (uint32_t)row64;
     const uint32_t tok = row / a.Hq, h = row - tok * a.Hq, b = tok / a.S, s = tok - b * a.S;
     if ((int32_t)s >= attn_seq(a, b).count) return;
-    const float2* stats = part_stats(a);
-    float m = kAttnNone;
-    for (uint32_t i = 0; i < a.splits; ++i) m = fmaxf(m, stats[(uint64_t)i * a.part_rows + row].x);
-    float l = 0.0f, o[ROPE_D_LIMIT / 64] = {};
-    for (uint32_t i = 0; i < a.splits; ++i) {
-        const float2 st = stats[(uint64_t)i * a.part_rows + row];
-        if (st.x == kAttnNone && st.y == 0.0f) continue;         // the part saw nothing
-        const float w = st.x == m ? 1.0f : exp2f(st.x - m);
+    const float2* stats = part_stats(a) + row;
+    float m = kAttnNone, l = 0.0f;
+    for (uint32_t i = lane; i < a.splits; i += 64) m = fmaxf(m, stats[i * a.part_rows].x);
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const auto weigh = [&](const float2& st) { return st.x == kAttnNone ? 0.0f : st.x == m ? 1.0f : exp2f(st.x - m); };
+    for (uint32_t i = lane; i < a.splits; i += 64) {
+        const float2 st = stats[i * a.part_rows];
+        const float w = weigh(st);
         l = __builtin_fmaf(st.y, w, l);
-#pragma unroll
-        for (int k = 0; k < ROPE_D_LIMIT / 64; ++k)
-            if (k * 64 + lane < a.Dv) o[k] = __builtin_fmaf(a.part[((uint64_t)i * a.part_rows + row) * a.Dv + k * 64 + lane], w, o[k]);
+        if (W > 1 && mine == 0) weight[0][i] = w;
     }
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
     const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    if (W > 1) __syncthreads();
+    const int64_t out = b * a.out.sb + s * a.out.ss + h * a.out.sn;
+    for (uint32_t j = lane; j < a.Dv; j += 64) {
+        const float* part = a.part + (uint64_t)row * a.Dv + j;
+        const uint64_t step = a.part_rows * a.Dv;
+        float o = 0.0f;
+        for (uint32_t i = mine; i < a.splits; i += W * K) {
+            float v[K], w[K];
 #pragma unroll
-    for (int k = 0; k < ROPE_D_LIMIT / 64; ++k)
-        if (k * 64 + lane < a.Dv) Store<DT>::store1(a.out.data, b * a.out.sb + s * a.out.ss + h * a.out.sn + k * 64 + lane, o[k] * inv);
+            for (int k = 0; k < K; ++k) {
+                const uint32_t at = min(i + k * W, a.splits - 1);
+                v[k] = part[at * step];
+                w[k] = W > 1 ? weight[0][at] : weigh(stats[at * a.part_rows]);
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (i + k * W < a.splits && w[k] != 0.0f) o = __builtin_fmaf(v[k], w[k], o);
+        }
+        if (W == 1) Store<DT>::store1(a.out.data, out + j, o * inv);
+        else sums[mine][j] = o;
+    }
+    if (W == 1) return;
+    __syncthreads();
+    for (uint32_t j = threadIdx.x; j < a.Dv; j += kJoinThreads) {
+        float o = sums[0][j];
+#pragma unroll
+        for (int w = 1; w < W; ++w) o += sums[w][j];
+        Store<DT>::store1(a.out.data, out + j, o * inv);
+    }
 }
 
 }  // namespace

@@ -66,18 +66,38 @@ __device__ __forceinline__ f32x4 attn_mfma(const v4u& a, const v4u& b, const f32
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// 8 codes as 16 + (code + 8), nibbles i and i + 4 in the halves of word i.
-template <int DT>
-__device__ __forceinline__ v4u k_numbers(uint32_t w)
+// A constant in a vector register: "and" and "or" are one operation on
+// registers, but not on two literals.
+__device__ __forceinline__ uint32_t vector_constant(uint32_t v)
 {
-    w ^= 0x88888888u;
-    if constexpr (DT == ROPE_DTYPE_BF16) {
-        constexpr uint32_t mask = 0x00780078u, one = 0x41804180u;
-        return v4u{((w << 3) & mask) | one, ((w >> 1) & mask) | one, ((w >> 5) & mask) | one, ((w >> 9) & mask) | one};
-    } else {
-        constexpr uint32_t mask = 0x03C003C0u, one = 0x4C004C00u;
-        return v4u{((w << 6) & mask) | one, ((w << 2) & mask) | one, ((w >> 2) & mask) | one, ((w >> 6) & mask) | one};
-    }
+    uint32_t r;
+    asm("v_mov_b32 %0, %1" : "=v"(r) : "i"(v));
+    return r;
+}
+
+// What makes numbers of nibbles: the nibble's bits, and the number that has them
+// in its fraction.
+struct Numbers {
+    uint32_t mask, one;
+};
+
+// 8 codes + 8 as 16 + (code + 8), nibbles i and i + 4 in the halves of word i.
+template <int DT>
+__device__ __forceinline__ Numbers k_constants()
+{
+    if constexpr (DT == ROPE_DTYPE_BF16) return Numbers{vector_constant(0x00780078u), vector_constant(0x41804180u)};
+    else return Numbers{vector_constant(0x03C003C0u), vector_constant(0x4C004C00u)};
+}
+
+template <int DT>
+__device__ __forceinline__ v4u k_numbers(uint32_t w, const Numbers& c)
+{
+    if constexpr (DT == ROPE_DTYPE_BF16)
+        return v4u{((w << 3) & c.mask) | c.one, ((w >> 1) & c.mask) | c.one, ((w >> 5) & c.mask) | c.one,
+                   ((w >> 9) & c.mask) | c.one};
+    else
+        return v4u{((w << 6) & c.mask) | c.one, ((w << 2) & c.mask) | c.one, ((w >> 2) & c.mask) | c.one,
+                   ((w >> 6) & c.mask) | c.one};
 }
 
 // 8 elements of a query row in the order of k_numbers.
@@ -88,9 +108,9 @@ __device__ __forceinline__ v4u q_order(const v4u& v)
 }
 
 // The codes that stand at nibbles `sh` / 4 of both halves of w (code + 8 each).
-__device__ __forceinline__ uint32_t v_numbers(uint32_t w, int sh)
+__device__ __forceinline__ uint32_t v_numbers(uint32_t w, int sh, const Numbers& c)
 {
-    const f16x2 n = __builtin_bit_cast(f16x2, ((w >> sh) & 0x000F000Fu) | 0x64006400u);
+    const f16x2 n = __builtin_bit_cast(f16x2, ((w >> sh) & c.mask) | c.one);
     return __builtin_bit_cast(uint32_t, n - f16x2{(_Float16)1032.0f, (_Float16)1032.0f});
 }
 
@@ -140,8 +160,14 @@ struct alignas(16) AttnLds {
     };
 };
 
+// Waves that a SIMD is to hold: what their registers allow.
+constexpr int attn_waves(int lanes, bool kf, int tiles)
+{
+    return lanes == 256 ? 1 : (lanes == 64 || !kf ? 4 : 3) - tiles;
+}
+
 template <int DT, int DP, int DVP, bool KF, bool VF, int NT>
-__global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
+__global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_kernel(AttnVecArgs a)
 {
     using Lds = AttnLds<DP, DVP, KF, VF, NT>;
     constexpr int KW = DP / 32;                    // words of a K row that a lane takes
@@ -229,12 +255,12 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
     };
 
     f32x4 acc[NT][VT];
-    float m[NT], l[NT], top[NT][NGV];
+    float m[NT], less[NT], l[NT], top[NT][NGV];  // less: m, or 0 where there is none yet
     int32_t e[NT][NGV];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         m[t] = kAttnNone;
-        l[t] = 0.0f;
+        less[t] = l[t] = 0.0f;
 #pragma unroll
         for (int g = 0; g < NGV; ++g) {
             top[t][g] = 0.0f;
@@ -288,8 +314,10 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
+            if (i == 8) __builtin_amdgcn_sched_barrier(0);
             const gchar* row = v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
             if constexpr (VF && DVP == 64) {
                 const uint32_t off = 16 * a2 + 2 * q2;
@@ -316,6 +344,7 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
         }
     };
 
+    const Numbers k_const = k_constants<DT>(), v_const{vector_constant(0x000F000Fu), vector_constant(0x64006400u)};
     const uint32_t step = 64 * waves;
     uint32_t base = from + (a.join ? 64 * wave : 0);
     Place next = look_up(base);
@@ -328,37 +357,22 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
         for (int g = 0; g < NGK; ++g) my.ks[g][lane] = ks[g] * a.scale2;
 #pragma unroll
         for (int g = 0; g < NGV; ++g) my.vs[g][lane] = vs[g];
-        uint32_t kc[4][KW], vc[16][VR];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int st = 0; st < KW; ++st) kc[i][st] = kw[i][st];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int c = 0; c < VR; ++c) vc[i][c] = vw[i][c];
         wave_sync();
-        if (to - base > step) {
-            fetch(next);
-            next = look_up(to - base > 2 * step ? base + 2 * step : to);
-        }
 
-        // x^T = K Q^T, a token a row of the product
+        // x^T = K Q^T, a token a row of the product, less the row's m
         f32x4 x[NT][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int st = 0; st < KW; ++st) {
-                const v4u k = k_numbers<DT>(kc[i][st]);
+                const v4u k = k_numbers<DT>(kw[i][st] ^ 0x88888888u, k_const);
                 if constexpr (KF) {
                     const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[st][16 * i + 4 * kq]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const f32x4 d = attn_mfma<DT>(k, q[t][st], start[t][st]);
-                        if (st == 0) x[t][i] = d * s;
-                        else
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(d[r], s[r], x[t][i][r]);
+                        for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(d[r], s[r], st == 0 ? -less[t] : x[t][i][r]);
                     }
                 } else {
 #pragma unroll
@@ -368,24 +382,65 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
             if constexpr (!KF) {
                 const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[0][16 * i + 4 * kq]);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) x[t][i] *= s;
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(x[t][i][r], s[r], -less[t]);
             }
+            __builtin_amdgcn_sched_barrier(0);     // (else conversions of all tiles pile up in registers)
         }
         if (base + 64 > all || valid != ~0ull) {
+            // most tiles have nothing to hide: this keeps the comparisons in the
+            // branch
+            int32_t tile = (int32_t)base;
+            asm volatile("" : "+s"(tile));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t bits = (uint32_t)(valid >> (16 * i + 4 * kq));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int32_t tok = (int32_t)(base + 16 * i + 4 * kq + r);
+                    const int32_t tok = tile + (int32_t)(16 * i + 4 * kq + r);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) x[t][i][r] = ((bits >> r) & 1u) && tok <= last[t] ? x[t][i][r] : kAttnNone;
                 }
             }
         }
 
-        // the weights exp(x - m) and, by segments, what the second product takes
-        v4u p[NT][NGV][2];
+        // V's codes + 8, of two tokens at equal nibbles; then the next tile's loads
+        uint32_t two[2][VH][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = 8 * h + 4 * (j >> 1) + 2 * (j & 1);
+                if constexpr (DVP == 64) {
+                    uint32_t w = vw[i][0] | (vw[i + 1][0] << 16);
+                    if constexpr (VF) {            // two lanes exchange bytes of both halves
+                        const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
+                        w = __builtin_amdgcn_perm(o, w, sel1);
+                    }
+                    two[h][0][j] = w ^ 0x88888888u;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < VR; ++c) {
+                        uint32_t w0 = vw[i][c], w1 = vw[i + 1][c];
+                        if constexpr (VF) {
+                            w0 = quad_bytes(w0, sel1, sel2);
+                            w1 = quad_bytes(w1, sel1, sel2);
+                        }
+                        two[h][2 * c][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100) ^ 0x88888888u;
+                        two[h][2 * c + 1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302) ^ 0x88888888u;
+                    }
+                }
+            }
+        // (behind the last tile nothing new: a branch around the loads would cost
+        // a copy of their registers in every tile)
+        fetch(next);
+        next = look_up(to - base > 2 * step ? base + 2 * step : to);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // the weights exp(x - m)
+        float keep[NT];
+        bool moved[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float most = x[t][0][0];
@@ -394,28 +449,41 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) most = fmaxf(most, x[t][i][r]);
             most = column_max(most);
-            float keep = 1.0f;
-            const bool moved = __any(most > m[t] + 6.0f);
-            if (moved) {
-                const float now = fmaxf(m[t], most);
-                keep = now == m[t] ? 1.0f : exp2f(m[t] - now);
+            keep[t] = 1.0f;
+            moved[t] = __any(most > (m[t] == kAttnNone ? kAttnNone : 6.0f));
+            if (moved[t]) {
+                const float now = fmaxf(m[t], most + less[t]);
+                keep[t] = now == m[t] ? 1.0f : exp2f(m[t] - now);
                 m[t] = now;
-                l[t] *= keep;
+                const float was = less[t];
+                less[t] = now == kAttnNone ? 0.0f : now;
+                const float more = less[t] - was;
+                l[t] *= keep[t];
 #pragma unroll
-                for (int g = 0; g < NGV; ++g) top[t][g] *= keep;
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[t][i][r] -= more;
             }
-            const float less = m[t] == kAttnNone ? 0.0f : m[t];
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    x[t][i][r] = __builtin_amdgcn_exp2f(x[t][i][r] - less);
+                    x[t][i][r] = __builtin_amdgcn_exp2f(x[t][i][r]);
                     sum += x[t][i][r];
                 }
             l[t] += sum;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // by segments: the weights times V's scales, in fp16, and o^T += V^T P^T,
+        // 32 tokens a product
 #pragma unroll
-            for (int g = 0; g < NGV; ++g) {
+        for (int g = 0; g < NGV; ++g) {
+            constexpr int T = VT / NGV;            // products of a segment
+            v4u p[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
                 f32x4 w[4];
                 float high = 0.0f;
 #pragma unroll
@@ -424,14 +492,15 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) high = fmaxf(high, fabsf(w[i][r]));
                 }
+                if (moved[t]) top[t][g] *= keep[t];
                 top[t][g] = fmaxf(top[t][g], column_max(high));
-                if (moved || __any(__builtin_ldexpf(top[t][g], -e[t][g]) > 256.0f)) {
+                if (moved[t] || __any(__builtin_ldexpf(top[t][g], -e[t][g]) > 256.0f)) {
                     int32_t now = __builtin_amdgcn_frexp_expf(top[t][g]);
                     now = top[t][g] > 0.0f ? min(max(now, -120), 120) : e[t][g];
-                    const float f = __builtin_ldexpf(keep, e[t][g] - now);
+                    const float f = __builtin_ldexpf(keep[t], e[t][g] - now);
                     e[t][g] = now;
 #pragma unroll
-                    for (int i = 0; i < VT / NGV; ++i) acc[t][g * (VT / NGV) + i] *= f;
+                    for (int i = 0; i < T; ++i) acc[t][g * T + i] *= f;
                 }
                 const float c = __builtin_ldexpf(1.0f, -e[t][g]);
 #pragma unroll
@@ -440,46 +509,20 @@ __global__ void __launch_bounds__(256) rope_attn_mfma_kernel(AttnVecArgs a)
                     for (int j = 0; j < 4; ++j) {
                         const f32x4& v = w[2 * h + (j >> 1)];
                         const f32x2 pair{v[2 * (j & 1)] * c, v[2 * (j & 1) + 1] * c};
-                        p[t][g][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
+                        p[t][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
                     }
             }
-        }
-
-        // o^T += V^T P^T, 32 tokens a product
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t two[VH][4];                   // codes of two tokens at equal nibbles
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 8 * h + 4 * (j >> 1) + 2 * (j & 1);
-                if constexpr (DVP == 64) {
-                    uint32_t w = vc[i][0] | (vc[i + 1][0] << 16);
-                    if constexpr (VF) {            // halves of two lanes: bytes 0, 2 and 1, 3 change places
-                        const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
-                        w = __builtin_amdgcn_perm(o, w, sel1);
-                    }
-                    two[0][j] = w ^ 0x88888888u;
-                } else {
+                for (int i = g * T; i < (g + 1) * T; ++i) {
+                    v4u v;
 #pragma unroll
-                    for (int c = 0; c < VR; ++c) {
-                        uint32_t w0 = vc[i][c], w1 = vc[i + 1][c];
-                        if constexpr (VF) {
-                            w0 = quad_bytes(w0, sel1, sel2);
-                            w1 = quad_bytes(w1, sel1, sel2);
-                        }
-                        two[2 * c][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100) ^ 0x88888888u;
-                        two[2 * c + 1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302) ^ 0x88888888u;
-                    }
+                    for (int j = 0; j < 4; ++j) v[j] = v_numbers(two[h][i >> 2][j], 4 * (i & 3), v_const);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][h], acc[t][i]);
+                    if (i & 1) __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < VT; ++i) {
-                v4u v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = v_numbers(two[i >> 2][j], 4 * (i & 3));
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][VF ? i / 2 : 0][h], acc[t][i]);
-            }
         }
     }
 

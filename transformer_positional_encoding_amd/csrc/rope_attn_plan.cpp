@@ -14,7 +14,6 @@ constexpr int64_t kI64Max = std::numeric_limits<int64_t>::max();
 // are worth a block of their own.
 constexpr int64_t kAttnBlocks = 2048;
 constexpr int64_t kAttnSplitTokens = 256;
-constexpr int64_t kAttnMaxSplits = 512;
 // Rows of a tile: the partial results of a call are B * heads * tiles * 16 at
 // most for each part.
 constexpr int64_t kAttnTileRows = 16;
@@ -25,7 +24,7 @@ int64_t attn_splits(int64_t B, int64_t heads, int64_t rows, int64_t tokens)
 {
     const int64_t tiles = (rows + kAttnTileRows - 1) / kAttnTileRows;
     const int64_t base = std::max<int64_t>(1, B * heads * tiles);
-    const int64_t want = std::min(kAttnMaxSplits, kAttnBlocks / base);
+    const int64_t want = std::min(kAttnMaxParts, kAttnBlocks / base);
     return std::max<int64_t>(1, std::min(want, tokens / kAttnSplitTokens));
 }
 

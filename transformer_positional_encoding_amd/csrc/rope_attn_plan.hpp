@@ -6,6 +6,9 @@
 
 namespace rope {
 
+// Most parts that a sequence's tokens are divided into.
+constexpr int64_t kAttnMaxParts = 512;
+
 struct AttnPlan {
     Plan rope;                     // dimensions and storage type
     int64_t B = 0, S = 0;
