@@ -99,15 +99,23 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     const int tiles = lanes == 256 || a.rows <= 16 ? 1 : 2;
     const void* fn = mfma_kernel(p, tiles, lanes);
     const bool mfma = fn != nullptr;
-    a.join = a.rows <= 64;
+    // Few rows: a wave a head, as far as heads go by fours, which then read
+    // neighbouring bytes; else waves take turns at the tokens. Many: a wave a
+    // tile of rows.
+    a.head_waves = a.token_waves = a.row_waves = 1;
+    if (a.rows > 64) a.row_waves = 4;
+    else if (a.heads % 4 == 0) a.head_waves = 4;
+    else a.token_waves = a.heads % 2 == 0 ? 2 : 4;
+    if (a.token_waves == 2) a.head_waves = 2;
+    if (mfma) a.heads_div = make_fastdiv(a.heads / a.head_waves);
     a.k_group = a.kc.group;
     a.v_group = a.vc.group;
     a.k_groups = a.D / a.k_group;
     a.v_groups = a.Dv / a.v_group;
-    const uint32_t block_rows = !mfma ? kAttnGenRows : (a.join ? 16 : 64) * tiles;
+    const uint32_t block_rows = !mfma ? kAttnGenRows : 16 * tiles * (int)a.row_waves;
     a.tiles = (a.rows + block_rows - 1) / block_rows;
     a.tiles_div = make_fastdiv(a.tiles);
-    const uint64_t blocks = (uint64_t)p.B * a.heads * a.tiles * a.splits;
+    const uint64_t blocks = (uint64_t)p.B * a.heads_div.d * a.tiles * a.splits;
     if (blocks >= (1ull << 31) || blocks > kMaxGridItems / kAttnGenThreads)
         return set_error(ROPE_ERR_UNSUPPORTED, "a grid too large for one launch");
     AttnArgs g = a;

@@ -38,7 +38,9 @@ struct AttnArgs {
     FastDiv rep_div, heads_div, tiles_div, splits_div, page_div;
 };
 
-// A block's place: part, tile of rows, cached head, sequence.
+// A block's place: cached head (or group of heads), tile of rows, part, sequence,
+// the first changing fastest: heads lie beside each other in memory, and what
+// blocks read at the same time should too.
 struct AttnAt {
     uint32_t split, tile, head, b;
 };
@@ -46,12 +48,12 @@ struct AttnAt {
 __device__ __forceinline__ AttnAt attn_at(const AttnArgs& a, uint32_t block)
 {
     AttnAt p;
-    uint32_t i = fast_div(block, a.splits_div);
-    p.split = block - i * a.splits;
-    uint32_t j = fast_div(i, a.tiles_div);
+    const uint32_t i = fast_div(block, a.heads_div);
+    p.head = block - i * a.heads_div.d;
+    const uint32_t j = fast_div(i, a.tiles_div);
     p.tile = i - j * a.tiles;
-    p.b = fast_div(j, a.heads_div);
-    p.head = j - p.b * a.heads;
+    p.b = fast_div(j, a.splits_div);
+    p.split = j - p.b * a.splits;
     return p;
 }
 

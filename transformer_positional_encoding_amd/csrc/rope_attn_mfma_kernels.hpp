@@ -52,7 +52,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t v3u __attribute__((ext_vector_type(3)));
 
 struct AttnVecArgs : AttnArgs {
-    int32_t join;              // the block's waves share their rows
+    // what a block's four waves have of their own: cached heads, turns at the
+    // tokens (whose results are joined), tiles of rows; one times another is 4
+    uint32_t head_waves, token_waves, row_waves;
     uint32_t k_groups, v_groups;   // scales of a row
     uint32_t k_group, v_group;     // lanes of each
 };
@@ -182,11 +184,11 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 
     const AttnAt at = attn_at(a, blockIdx.x);
     const AttnSeq seq = attn_seq(a, at.b);
-    const uint32_t waves = a.join ? 4 : 1;         // that share a tile of rows
-    const uint32_t block_row = at.tile * (a.join ? 16 * NT : 64 * NT);
-    const uint32_t r0 = a.join ? block_row : block_row + wave * 16 * NT;
+    const uint32_t head_wave = wave & (a.head_waves - 1), token_wave = a.row_waves > 1 ? 0 : wave / a.head_waves;
+    const uint32_t head = at.head * a.head_waves + head_wave, waves = a.token_waves;
+    const uint32_t r0 = (at.tile * a.row_waves + (a.row_waves > 1 ? wave : 0)) * 16 * NT;
     const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
-    if (r0 >= live) return;                        // with join the same for the whole block
+    if (r0 >= live) return;                        // where waves are joined the same for the whole block
     // the tokens that some row sees, this part of them, and those that all see
     uint32_t n = (uint32_t)seq.tokens, all = n;
     if (a.causal) {
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const uint32_t r = min(r0 + t * 16 + n16, live - 1);
-        const uint32_t s = fast_div(r, a.rep_div), h = at.head * a.rep + (r - s * a.rep);
+        const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
         last[t] = a.causal ? (int32_t)(seq.first + s) : INT32_MAX;
         const gchar* row = as_global(a.q.data) + (at.b * a.q.sb + s * a.q.ss + h * a.q.sn) * 2;
         float sum = 0.0f;
@@ -229,10 +231,10 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
     }
 
     // where this lane's words of a row start
-    const gchar* const k_base = as_global(a.kc.data) + at.head * a.kc.st[2];
-    const gchar* const v_base = as_global(a.vc.data) + at.head * a.vc.st[2];
-    const gchar* const ks_base = as_global(a.kc.scales) + at.head * a.kc.sc[2] * 4;
-    const gchar* const vs_base = as_global(a.vc.scales) + at.head * a.vc.sc[2] * 4;
+    const gchar* const k_base = as_global(a.kc.data) + head * a.kc.st[2];
+    const gchar* const v_base = as_global(a.vc.data) + head * a.vc.st[2];
+    const gchar* const ks_base = as_global(a.kc.scales) + head * a.kc.sc[2] * 4;
+    const gchar* const vs_base = as_global(a.vc.scales) + head * a.vc.sc[2] * 4;
     const int32_t* const table = a.table + at.b * a.table_stride;
     const uint32_t k_bytes = a.D / 2, v_bytes = a.Dv / 2;
     const uint32_t q4 = n16 >> 2, a4 = n16 & 3, q2 = n16 >> 1, a2 = n16 & 1;
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 
     const Numbers k_const = k_constants<DT>(), v_const{vector_constant(0x000F000Fu), vector_constant(0x64006400u)};
     const uint32_t step = 64 * waves;
-    uint32_t base = from + (a.join ? 64 * wave : 0);
+    uint32_t base = from + 64 * token_wave;
     Place next = look_up(base);
     if (base < to) fetch(next);
     next = look_up(base + step < base ? to : base + step);
@@ -540,13 +542,13 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         }
     };
 
-    if (!a.join) {
+    if (waves == 1) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const uint32_t r = r0 + t * 16 + n16;
             const float sum = column_sum(l[t]);
             if (r >= live) continue;
-            const uint32_t s = fast_div(r, a.rep_div), h = at.head * a.rep + (r - s * a.rep);
+            const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
             const float inv = a.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
             float f[NGV];
 #pragma unroll
@@ -575,9 +577,8 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             lds.join.l[wave][n16] = sum;
         }
         __syncthreads();
-        float most = lds.join.m[0][n16];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) most = fmaxf(most, lds.join.m[w][n16]);
+        float most = kAttnNone;
+        for (uint32_t w = head_wave; w < 4; w += a.head_waves) most = fmaxf(most, lds.join.m[w][n16]);
         const float keep = m[t] == kAttnNone ? 0.0f : m[t] == most ? 1.0f : exp2f(m[t] - most);
 #pragma unroll
         for (int i = 0; i < VT; ++i) {
@@ -588,32 +589,30 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         __syncthreads();
         // 16 threads a row, 8 lanes at a time
         const uint32_t row16 = threadIdx.x >> 4, r = r0 + t * 16 + row16;
-        if (r >= live) continue;                   // (the barriers above are passed by every thread again)
-        float high = lds.join.m[0][row16], whole = 0.0f;
-#pragma unroll
-        for (int w = 1; w < 4; ++w) high = fmaxf(high, lds.join.m[w][row16]);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float mw = lds.join.m[w][row16];
-            whole += lds.join.l[w][row16] * (mw == kAttnNone ? 0.0f : mw == high ? 1.0f : exp2f(mw - high));
-        }
-        const uint32_t s = fast_div(r, a.rep_div), h = at.head * a.rep + (r - s * a.rep);
-        const float inv = a.splits > 1 ? 1.0f : whole > 0.0f ? 1.0f / whole : whole == 0.0f ? 0.0f : whole;
-        const uint64_t row = part_row(a, at.split, at.b, s, h);
-        gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
-        for (uint32_t j = 8 * (threadIdx.x & 15); j < a.Dv; j += 128) {
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[k] = lds.join.o[0][row16][j + k];
-#pragma unroll
-                for (int w = 1; w < 4; ++w) v[k] += lds.join.o[w][row16][j + k];
-                v[k] *= inv;
+        const uint32_t s = fast_div(min(r, live - 1), a.rep_div);
+        for (uint32_t hw = 0; hw < a.head_waves; ++hw) {
+            float high = kAttnNone, whole = 0.0f;
+            for (uint32_t w = hw; w < 4; w += a.head_waves) high = fmaxf(high, lds.join.m[w][row16]);
+            for (uint32_t w = hw; w < 4; w += a.head_waves) {
+                const float mw = lds.join.m[w][row16];
+                whole += lds.join.l[w][row16] * (mw == kAttnNone ? 0.0f : mw == high ? 1.0f : exp2f(mw - high));
             }
-            if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
-            else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
+            const uint32_t h = (at.head * a.head_waves + hw) * a.rep + (r - s * a.rep);
+            const float inv = a.splits > 1 ? 1.0f : whole > 0.0f ? 1.0f / whole : whole == 0.0f ? 0.0f : whole;
+            const uint64_t row = part_row(a, at.split, at.b, s, h);
+            gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
+            for (uint32_t j = 8 * (threadIdx.x & 15); j < a.Dv && r < live; j += 128) {
+                float v[8] = {};
+                for (uint32_t w = hw; w < 4; w += a.head_waves)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += lds.join.o[w][row16][j + k];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= inv;
+                if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
+                else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
+            }
+            if (a.splits > 1 && r < live && (threadIdx.x & 15) == 0) part_stats(a)[row] = make_float2(high, whole);
         }
-        if (a.splits > 1 && (threadIdx.x & 15) == 0) part_stats(a)[row] = make_float2(high, whole);
     }
 }
 
