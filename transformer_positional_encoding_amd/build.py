@@ -19,7 +19,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "librope_partial.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("rope_kernels.hip", "rope_cache.hip", "rope_lora.hip", "rope_norm.hip",
                                            "rope_reserve.hip", "rope_attn.hip", "rope_attn_bf16.hip",
-                                           "rope_attn_f16.hip", "rope_plan.cpp",
+                                           "rope_attn_f16.hip", "rope_attn_bf16_any.hip", "rope_attn_f16_any.hip",
+                                           "rope_plan.cpp",
                                            "rope_cache_plan.cpp", "rope_norm_plan.cpp", "rope_attn_plan.cpp")]
 # The bare access-pattern probe the benchmark times beside the kernels (its
 # own library; the rotation library does not use it).

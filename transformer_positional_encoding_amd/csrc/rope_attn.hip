@@ -56,6 +56,7 @@ AttnArgs attn_args(const AttnPlan& p)
     a.lengths = p.lengths;
     a.counts = p.counts;
     a.pages = p.pages;
+    a.page_limit = (uint32_t)std::min<int64_t>(p.pages, INT32_MAX);
     a.most = (int32_t)p.most;
     // (no token number reaches 2^31 - 1, so a page of as many or more holds all)
     a.page_div = make_fastdiv((uint32_t)std::min<int64_t>(p.page_size, INT32_MAX));
@@ -88,7 +89,10 @@ const void* mfma_kernel(const AttnPlan& p, int tiles, int lanes)
     const bool k_whole = k_row && D == lanes && codes_aligned(p.kc, lanes == 64 ? 8 : 16);
     const int scales = !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
     if (!codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4)) return nullptr;
-    return p.rope.dtype == ROPE_DTYPE_BF16 ? attn_kernel_bf16(lanes, scales, tiles) : attn_kernel_f16(lanes, scales, tiles);
+    const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
+    if (p.rope.dtype == ROPE_DTYPE_BF16)
+        return whole16 ? attn_kernel_bf16(lanes, scales, tiles) : attn_kernel_bf16_any(lanes, scales, tiles);
+    return whole16 ? attn_kernel_f16(lanes, scales, tiles) : attn_kernel_f16_any(lanes, scales, tiles);
 }
 
 rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)

@@ -1,8 +1,11 @@
-// The matrix-core attention kernels for bf16 queries.
+// The matrix-core attention kernels for bf16 queries, pages of whole 16 tokens.
 #include "rope_attn_select.hpp"
 
 namespace rope {
 
-const void* attn_kernel_bf16(int lanes, int scales, int tiles) { return attn_kernel<ROPE_DTYPE_BF16>(lanes, scales, tiles); }
+const void* attn_kernel_bf16(int lanes, int scales, int tiles)
+{
+    return attn_kernel<ROPE_DTYPE_BF16, true>(lanes, scales, tiles);
+}
 
 }  // namespace rope

@@ -1,8 +1,11 @@
-// The matrix-core attention kernels for f16 queries.
+// The matrix-core attention kernels for f16 queries, pages of whole 16 tokens.
 #include "rope_attn_select.hpp"
 
 namespace rope {
 
-const void* attn_kernel_f16(int lanes, int scales, int tiles) { return attn_kernel<ROPE_DTYPE_F16>(lanes, scales, tiles); }
+const void* attn_kernel_f16(int lanes, int scales, int tiles)
+{
+    return attn_kernel<ROPE_DTYPE_F16, true>(lanes, scales, tiles);
+}
 
 }  // namespace rope

@@ -30,6 +30,7 @@ struct AttnArgs {
     const int32_t* lengths;
     const int32_t* counts;
     int64_t pages;
+    uint32_t page_limit;       // pages, as far as 32-bit numbers name them
     int32_t most;              // tokens that a block table holds
     float scale2;              // scale * log2(e)
     int32_t causal;

@@ -68,8 +68,8 @@ __device__ __forceinline__ f32x4 attn_mfma(const v4u& a, const v4u& b, const f32
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// A constant in a vector register: "and" and "or" are one operation on
-// registers, but not on two literals.
+// A constant in a register, which takes part in three-operand logic as two
+// literals could not.
 __device__ __forceinline__ uint32_t vector_constant(uint32_t v)
 {
     uint32_t r;
@@ -77,29 +77,52 @@ __device__ __forceinline__ uint32_t vector_constant(uint32_t v)
     return r;
 }
 
-// What makes numbers of nibbles: the nibble's bits, and the number that has them
-// in its fraction.
+// What makes numbers of nibbles: their bits, and what they are added to, with
+// the nibbles' upper bit (which turns -8..7 in two's complement into 0..15).
 struct Numbers {
     uint32_t mask, one;
 };
+__device__ __forceinline__ uint32_t number(uint32_t w, const Numbers& c) { return (w & c.mask) ^ c.one; }
 
-// 8 codes + 8 as 16 + (code + 8), nibbles i and i + 4 in the halves of word i.
+// 8 codes as 16 + (code + 8), nibbles i and i + 4 in the halves of word i.
 template <int DT>
 __device__ __forceinline__ Numbers k_constants()
 {
-    if constexpr (DT == ROPE_DTYPE_BF16) return Numbers{vector_constant(0x00780078u), vector_constant(0x41804180u)};
-    else return Numbers{vector_constant(0x03C003C0u), vector_constant(0x4C004C00u)};
+    if constexpr (DT == ROPE_DTYPE_BF16) return Numbers{vector_constant(0x00780078u), vector_constant(0x41C041C0u)};
+    else return Numbers{vector_constant(0x03C003C0u), vector_constant(0x4E004E00u)};
 }
 
 template <int DT>
 __device__ __forceinline__ v4u k_numbers(uint32_t w, const Numbers& c)
 {
-    if constexpr (DT == ROPE_DTYPE_BF16)
-        return v4u{((w << 3) & c.mask) | c.one, ((w >> 1) & c.mask) | c.one, ((w >> 5) & c.mask) | c.one,
-                   ((w >> 9) & c.mask) | c.one};
-    else
-        return v4u{((w << 6) & c.mask) | c.one, ((w << 2) & c.mask) | c.one, ((w >> 2) & c.mask) | c.one,
-                   ((w >> 6) & c.mask) | c.one};
+    if constexpr (DT == ROPE_DTYPE_BF16) return v4u{number(w << 3, c), number(w >> 1, c), number(w >> 5, c), number(w >> 9, c)};
+    else return v4u{number(w << 6, c), number(w << 2, c), number(w >> 2, c), number(w >> 6, c)};
+}
+
+// What makes codes in fp16 of nibbles 0 (1024 + n, less 1032) and 1 (1024 + 16
+// n, times 1/16, less 72) of both halves of a word.
+struct VConstants {
+    Numbers low, high;
+};
+__device__ __forceinline__ VConstants v_constants()
+{
+    return VConstants{{vector_constant(0x000F000Fu), vector_constant(0x64086408u)},
+                      {vector_constant(0x00F000F0u), vector_constant(0x64806480u)}};
+}
+
+// The codes at nibble i of both halves of w.
+template <int I>
+__device__ __forceinline__ uint32_t v_numbers(uint32_t w, const VConstants& c)
+{
+    w >>= 8 * (I / 2);
+    if constexpr (I % 2 == 0) {
+        const f16x2 n = __builtin_bit_cast(f16x2, number(w, c.low));
+        return __builtin_bit_cast(uint32_t, n - (_Float16)1032.0f);
+    } else {
+        const f16x2 n = __builtin_bit_cast(f16x2, number(w, c.high)), k{(_Float16)0.0625f, (_Float16)0.0625f},
+                    o{(_Float16)-72.0f, (_Float16)-72.0f};
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(n, k, o));
+    }
 }
 
 // 8 elements of a query row in the order of k_numbers.
@@ -107,13 +130,6 @@ __device__ __forceinline__ v4u q_order(const v4u& v)
 {
     return v4u{__builtin_amdgcn_perm(v[2], v[0], 0x05040100), __builtin_amdgcn_perm(v[2], v[0], 0x07060302),
                __builtin_amdgcn_perm(v[3], v[1], 0x05040100), __builtin_amdgcn_perm(v[3], v[1], 0x07060302)};
-}
-
-// The codes that stand at nibbles `sh` / 4 of both halves of w (code + 8 each).
-__device__ __forceinline__ uint32_t v_numbers(uint32_t w, int sh, const Numbers& c)
-{
-    const f16x2 n = __builtin_bit_cast(f16x2, ((w >> sh) & c.mask) | c.one);
-    return __builtin_bit_cast(uint32_t, n - f16x2{(_Float16)1032.0f, (_Float16)1032.0f});
 }
 
 // Word i of lane i of four (by lane number) receives byte a of lane a's word in
@@ -133,16 +149,21 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Over the four lanes that hold a column.
+// Over the four lanes that hold a column: rows of 16 lanes, then halves of the
+// wave, change places between two copies.
 __device__ __forceinline__ float column_max(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float column_sum(float v)
 {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 template <int DP, int DVP, bool KF, bool VF, int NT>
@@ -168,7 +189,7 @@ constexpr int attn_waves(int lanes, bool kf, int tiles)
     return lanes == 256 ? 1 : (lanes == 64 || !kf ? 4 : 3) - tiles;
 }
 
-template <int DT, int DP, int DVP, bool KF, bool VF, int NT>
+template <int DT, int DP, int DVP, bool KF, bool VF, bool P16, int NT>
 __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_kernel(AttnVecArgs a)
 {
     using Lds = AttnLds<DP, DVP, KF, VF, NT>;
@@ -241,19 +262,26 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
     const uint32_t sel1 = (lane & 1) ? 0x03070105u : 0x06020400u;
     const uint32_t sel2 = (lane & 2) ? 0x03020706u : 0x05040100u;
 
+    // a token's page, and its place there; page 0 where it has none
     struct Place {
-        int32_t page;
-        uint32_t in_page;
+        uint32_t page, in_page;
+        bool there;
     };
     const auto look_up = [&](uint32_t base) -> Place {
         const uint32_t tok = base + lane;
-        Place p{-1, 0};
+        Place p{0, 0, false};
         if (tok < to) {
             const uint32_t col = fast_div(tok, a.page_div);
-            p.page = table[col];
+            p.page = (uint32_t)table[col];
             p.in_page = tok - col * a.page_div.d;
+            p.there = true;
         }
         return p;
+    };
+    const auto settle = [&](Place& p) {            // (apart from the look-up, so as not to wait for it there)
+        p.there = p.there && p.page < a.page_limit;
+        p.page = p.there ? p.page : 0;
+        p.in_page = p.there ? p.in_page : 0;
     };
 
     f32x4 acc[NT][VT];
@@ -275,12 +303,20 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
     uint32_t kw[4][KW], vw[16][VR];
     float ks[NGK], vs[NGV];
     bool there = false;
-    // addresses, scales and codes of a tile whose pages are known
-    const auto fetch = [&](const Place& p) {
-        there = p.page >= 0 && p.page < a.pages;
-        const int64_t page = there ? p.page : 0, in_page = there ? p.in_page : 0;
-        my.k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
-        my.v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
+    // Where 16 consecutive tokens stand in one page (P16) their rows start at one
+    // scalar address, and a lane's words at offsets from it that do not change;
+    // else each row's address comes from the lane that has its token.
+    const uint32_t k_step = n16 * (uint32_t)a.kc.st[1], v_step = 4 * kq * (uint32_t)a.vc.st[1];
+    const auto group_at = [&](const Place& p, int i, const gchar* base, const CacheRef& c) -> const gchar* {
+        const uint32_t page = __builtin_amdgcn_readlane((int)p.page, 16 * i);
+        const uint32_t in_page = __builtin_amdgcn_readlane((int)p.in_page, 16 * i);
+        return base + (int64_t)page * c.st[0] + (int64_t)in_page * c.st[1];
+    };
+    // the scales and K's codes of a tile whose pages are known
+    const auto fetch_k = [&](Place& p) {
+        settle(p);
+        there = p.there;
+        const int64_t page = p.page, in_page = p.in_page;
         const gchar* sk = ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1]) * 4;
         const gchar* sv = vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1]) * 4;
 #pragma unroll
@@ -293,64 +329,79 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
             vs[g] = there ? gload<float>(sv + at_g * 4) : 0.0f;
         }
-        wave_sync();
+        if constexpr (!P16) {
+            my.k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
+            my.v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
+            wave_sync();
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const gchar* row = k_base + my.k_at[16 * i + n16];
+            const gchar* row = P16 ? group_at(p, i, k_base, a.kc) : k_base + my.k_at[16 * i + n16];
+            const uint32_t step = P16 ? k_step : 0;
             if constexpr (KF) {
 #pragma unroll
                 for (int st = 0; st < KW; ++st) {
                     const uint32_t off = 16 * st + 4 * kq;
-                    kw[i][st] = gload<uint32_t>(row + (off < k_bytes ? off : 0));
+                    kw[i][st] = gload<uint32_t>(row + (step + (off < k_bytes ? off : 0)));
                 }
             } else if constexpr (KW == 2) {
-                const v2u w = gload<v2u>(row + 8 * kq);
+                const v2u w = gload<v2u>(row + (step + 8 * kq));
                 kw[i][0] = w[0];
                 kw[i][1] = w[1];
             } else {
 #pragma unroll
                 for (int c = 0; c < KW / 4; ++c) {
-                    const v4u w = gload<v4u>(row + 4 * KW * kq + 16 * c);
+                    const v4u w = gload<v4u>(row + (step + 4 * KW * kq + 16 * c));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) kw[i][4 * c + j] = w[j];
                 }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto fetch_v = [&](const Place& p) {
+        const gchar* group[4];
+        if constexpr (P16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) group[i] = group_at(p, i, v_base, a.vc);
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            if (i == 8) __builtin_amdgcn_sched_barrier(0);
-            const gchar* row = v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
+            const gchar* row = P16 ? group[i >> 2] : v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
+            const uint32_t step = P16 ? v_step + (i & 3) * (uint32_t)a.vc.st[1] : 0;
             if constexpr (VF && DVP == 64) {
                 const uint32_t off = 16 * a2 + 2 * q2;
-                vw[i][0] = gload<uint16_t>(row + (off < v_bytes ? off : 0));
+                vw[i][0] = gload<uint16_t>(row + (step + (off < v_bytes ? off : 0)));
             } else if constexpr (VF) {
 #pragma unroll
                 for (int c = 0; c < VR; ++c) {
                     const uint32_t off = 64 * c + 16 * a4 + 4 * q4;
-                    vw[i][c] = gload<uint32_t>(row + (off < v_bytes ? off : 0));
+                    vw[i][c] = gload<uint32_t>(row + (step + (off < v_bytes ? off : 0)));
                 }
             } else if constexpr (DVP == 64) {
                 const uint32_t off = 2 * n16;
-                vw[i][0] = gload<uint16_t>(row + (off < v_bytes ? off : 0));
+                vw[i][0] = gload<uint16_t>(row + (step + (off < v_bytes ? off : 0)));
             } else if constexpr (DVP == 128) {
                 const uint32_t off = 4 * n16;
-                vw[i][0] = gload<uint32_t>(row + (off < v_bytes ? off : 0));
+                vw[i][0] = gload<uint32_t>(row + (step + (off < v_bytes ? off : 0)));
             } else {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const uint32_t off = 8 * n16 + 4 * c;
-                    vw[i][c] = gload<uint32_t>(row + (off < v_bytes ? off : 0));
+                    vw[i][c] = gload<uint32_t>(row + (step + (off < v_bytes ? off : 0)));
                 }
             }
         }
     };
 
-    const Numbers k_const = k_constants<DT>(), v_const{vector_constant(0x000F000Fu), vector_constant(0x64006400u)};
+    const Numbers k_const = k_constants<DT>();
+    const VConstants v_const = v_constants();
     const uint32_t step = 64 * waves;
     uint32_t base = from + 64 * token_wave;
     Place next = look_up(base);
-    if (base < to) fetch(next);
+    if (base < to) {
+        fetch_k(next);
+        fetch_v(next);
+    }
     next = look_up(base + step < base ? to : base + step);
     for (; base < to; base += step) {
         // the tile's scales, by token, and its codes
@@ -367,7 +418,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int st = 0; st < KW; ++st) {
-                const v4u k = k_numbers<DT>(kw[i][st] ^ 0x88888888u, k_const);
+                const v4u k = k_numbers<DT>(kw[i][st], k_const);
                 if constexpr (KF) {
                     const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[st][16 * i + 4 * kq]);
 #pragma unroll
@@ -407,37 +458,11 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             }
         }
 
-        // V's codes + 8, of two tokens at equal nibbles; then the next tile's loads
-        uint32_t two[2][VH][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 8 * h + 4 * (j >> 1) + 2 * (j & 1);
-                if constexpr (DVP == 64) {
-                    uint32_t w = vw[i][0] | (vw[i + 1][0] << 16);
-                    if constexpr (VF) {            // two lanes exchange bytes of both halves
-                        const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
-                        w = __builtin_amdgcn_perm(o, w, sel1);
-                    }
-                    two[h][0][j] = w ^ 0x88888888u;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < VR; ++c) {
-                        uint32_t w0 = vw[i][c], w1 = vw[i + 1][c];
-                        if constexpr (VF) {
-                            w0 = quad_bytes(w0, sel1, sel2);
-                            w1 = quad_bytes(w1, sel1, sel2);
-                        }
-                        two[h][2 * c][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100) ^ 0x88888888u;
-                        two[h][2 * c + 1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302) ^ 0x88888888u;
-                    }
-                }
-            }
-        // (behind the last tile nothing new: a branch around the loads would cost
-        // a copy of their registers in every tile)
-        fetch(next);
-        next = look_up(to - base > 2 * step ? base + 2 * step : to);
+        // The next tile's scales and K; its V when this one's is used up. (Behind
+        // the last tile nothing new: a branch around the loads would cost a copy
+        // of their registers in every tile.)
+        fetch_k(next);
+        Place after = look_up(to - base > 2 * step ? base + 2 * step : to);
         __builtin_amdgcn_sched_barrier(0);
 
         // the weights exp(x - m)
@@ -477,6 +502,34 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             l[t] += sum;
         }
         __builtin_amdgcn_sched_barrier(0);
+
+        // V's words, the codes of two tokens at equal nibbles of their halves
+        uint32_t two[2][VH][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = 8 * h + 4 * (j >> 1) + 2 * (j & 1);
+                if constexpr (DVP == 64) {
+                    uint32_t w = vw[i][0] | (vw[i + 1][0] << 16);
+                    if constexpr (VF) {            // two lanes exchange bytes of both halves
+                        const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
+                        w = __builtin_amdgcn_perm(o, w, sel1);
+                    }
+                    two[h][0][j] = w;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < VR; ++c) {
+                        uint32_t w0 = vw[i][c], w1 = vw[i + 1][c];
+                        if constexpr (VF) {
+                            w0 = quad_bytes(w0, sel1, sel2);
+                            w1 = quad_bytes(w1, sel1, sel2);
+                        }
+                        two[h][2 * c][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100);
+                        two[h][2 * c + 1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302);
+                    }
+                }
+            }
 
         // by segments: the weights times V's scales, in fp16, and o^T += V^T P^T,
         // 32 tokens a product
@@ -520,12 +573,18 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                 for (int i = g * T; i < (g + 1) * T; ++i) {
                     v4u v;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = v_numbers(two[h][i >> 2][j], 4 * (i & 3), v_const);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w = two[h][i >> 2][j];
+                        v[j] = (i & 3) == 0 ? v_numbers<0>(w, v_const) : (i & 3) == 1 ? v_numbers<1>(w, v_const) :
+                               (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
+                    }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][h], acc[t][i]);
                     if (i & 1) __builtin_amdgcn_sched_barrier(0);
                 }
         }
+        fetch_v(next);
+        next = after;
     }
 
     // lane j of v that product i's row 4 kq + r holds
