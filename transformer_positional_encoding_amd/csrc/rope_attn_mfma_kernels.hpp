@@ -312,6 +312,12 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         const uint32_t in_page = __builtin_amdgcn_readlane((int)p.in_page, 16 * i);
         return base + (int64_t)page * c.st[0] + (int64_t)in_page * c.st[1];
     };
+    // (an offset that the compiler cannot widen outside of the loop: a load then
+    // takes it as it is, beside the scalar address)
+    const auto offset = [](uint32_t v) {
+        asm volatile("" : "+v"(v));
+        return v;
+    };
     // the scales and K's codes of a tile whose pages are known
     const auto fetch_k = [&](Place& p) {
         settle(p);
@@ -334,24 +340,26 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             my.v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
             wave_sync();
         }
+        uint32_t k_off[KF ? KW : 1];
+#pragma unroll
+        for (int st = 0; st < (KF ? KW : 1); ++st) {
+            const uint32_t off = KF ? 16 * st + 4 * kq : 4 * KW * kq;
+            k_off[st] = offset((P16 ? k_step : 0) + (off < k_bytes ? off : 0));
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const gchar* row = P16 ? group_at(p, i, k_base, a.kc) : k_base + my.k_at[16 * i + n16];
-            const uint32_t step = P16 ? k_step : 0;
             if constexpr (KF) {
 #pragma unroll
-                for (int st = 0; st < KW; ++st) {
-                    const uint32_t off = 16 * st + 4 * kq;
-                    kw[i][st] = gload<uint32_t>(row + (step + (off < k_bytes ? off : 0)));
-                }
+                for (int st = 0; st < KW; ++st) kw[i][st] = gload<uint32_t>(row + k_off[st]);
             } else if constexpr (KW == 2) {
-                const v2u w = gload<v2u>(row + (step + 8 * kq));
+                const v2u w = gload<v2u>(row + k_off[0]);
                 kw[i][0] = w[0];
                 kw[i][1] = w[1];
             } else {
 #pragma unroll
                 for (int c = 0; c < KW / 4; ++c) {
-                    const v4u w = gload<v4u>(row + (step + 4 * KW * kq + 16 * c));
+                    const v4u w = gload<v4u>(row + k_off[0] + 16 * c);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) kw[i][4 * c + j] = w[j];
                 }
@@ -364,31 +372,25 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 #pragma unroll
             for (int i = 0; i < 4; ++i) group[i] = group_at(p, i, v_base, a.vc);
         }
+        // a register of a lane's V: 4 bytes (2 of 64 lanes) in a place that ends
+        // with the row, or lane 0's
+        constexpr int W = DVP == 64 ? 2 : 4;
+        uint32_t v_off[P16 ? 4 : 1][VR];
+#pragma unroll
+        for (int c = 0; c < VR; ++c) {
+            const uint32_t off = VF ? (DVP == 64 ? 16 * a2 + 2 * q2 : 64 * c + 16 * a4 + 4 * q4) : W * VR * n16 + 4 * c;
+#pragma unroll
+            for (int r = 0; r < (P16 ? 4 : 1); ++r)
+                v_off[r][c] = offset((P16 ? v_step + r * (uint32_t)a.vc.st[1] : 0) + (off < v_bytes ? off : 0));
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const gchar* row = P16 ? group[i >> 2] : v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
-            const uint32_t step = P16 ? v_step + (i & 3) * (uint32_t)a.vc.st[1] : 0;
-            if constexpr (VF && DVP == 64) {
-                const uint32_t off = 16 * a2 + 2 * q2;
-                vw[i][0] = gload<uint16_t>(row + (step + (off < v_bytes ? off : 0)));
-            } else if constexpr (VF) {
 #pragma unroll
-                for (int c = 0; c < VR; ++c) {
-                    const uint32_t off = 64 * c + 16 * a4 + 4 * q4;
-                    vw[i][c] = gload<uint32_t>(row + (step + (off < v_bytes ? off : 0)));
-                }
-            } else if constexpr (DVP == 64) {
-                const uint32_t off = 2 * n16;
-                vw[i][0] = gload<uint16_t>(row + (step + (off < v_bytes ? off : 0)));
-            } else if constexpr (DVP == 128) {
-                const uint32_t off = 4 * n16;
-                vw[i][0] = gload<uint32_t>(row + (step + (off < v_bytes ? off : 0)));
-            } else {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t off = 8 * n16 + 4 * c;
-                    vw[i][c] = gload<uint32_t>(row + (step + (off < v_bytes ? off : 0)));
-                }
+            for (int c = 0; c < VR; ++c) {
+                const gchar* at = row + v_off[P16 ? i & 3 : 0][c];
+                if constexpr (W == 2) vw[i][c] = gload<uint16_t>(at);
+                else vw[i][c] = gload<uint32_t>(at);
             }
         }
     };
@@ -413,7 +415,11 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         wave_sync();
 
         // x^T = K Q^T, a token a row of the product, less the row's m
-        f32x4 x[NT][4];
+        f32x4 x[NT][4], k_scale[4];
+        if constexpr (!KF) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k_scale[i] = *reinterpret_cast<const f32x4*>(&my.ks[0][16 * i + 4 * kq]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -432,14 +438,16 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                     for (int t = 0; t < NT; ++t) x[t][i] = attn_mfma<DT>(k, q[t][st], st == 0 ? start[t][0] : x[t][i]);
                 }
             }
-            if constexpr (!KF) {
-                const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[0][16 * i + 4 * kq]);
+            __builtin_amdgcn_sched_barrier(0);     // (else conversions of all tiles pile up in registers)
+        }
+        if constexpr (!KF) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(x[t][i][r], s[r], -less[t]);
+                    for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(x[t][i][r], k_scale[i][r], -less[t]);
             }
-            __builtin_amdgcn_sched_barrier(0);     // (else conversions of all tiles pile up in registers)
         }
         if (base + 64 > all || valid != ~0ull) {
             // most tiles have nothing to hide: this keeps the comparisons in the
