@@ -54,12 +54,86 @@ template <int DT>
 struct BwdGeneral {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_bwd_general_kernel<DT>); }
 };
+template <int C, int PAR>
+struct Vec {
+    template <int DT>
+    struct Fwd {
+        static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_fwd_kernel<DT, C, PAR>); }
+    };
+    template <int DT>
+    struct Bwd {
+        static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_bwd_kernel<DT, C, PAR>); }
+    };
+};
+
+template <int C, int PAR>
+const void* vec_kernel(int dtype, bool backward)
+{
+    return backward ? by_type<Vec<C, PAR>::template Bwd>(dtype) : by_type<Vec<C, PAR>::template Fwd>(dtype);
+}
+
+// The vector kernel of a call, its arguments and LDS; NULL if rows or the slice
+// are not in whole chunks.
+const void* norm_vec(const NormPlan& p, bool backward, NormVecArgs* a, size_t* lds)
+{
+    const int es = p.rope.esize;
+    for (int i = 0; i < 2; ++i)
+        if (!rows_in_chunks(p.x[i], es) || !rows_in_chunks(p.y[i], es) || (backward && !rows_in_chunks(p.dy[i], es))) return nullptr;
+    if (p.rotate && !turn_in_chunks(p.rope)) return nullptr;
+    // Threads per row and chunks per thread: the fewest idle lanes; among those
+    // two chunks where that leaves a row 8 threads (128 bytes of 16-bit lanes a
+    // load).
+    const uint32_t chunks = a->D / 8;
+    uint32_t best = ~0u;
+    int C = 1;
+    for (uint32_t c = 1; c <= 2; ++c) {
+        const uint32_t T = 1u << log2_of((chunks + c - 1) / c);
+        if (T > 64) continue;
+        const uint32_t cost = 2 * T * c + (T < 8 ? 1 : 0);
+        if (cost < best || (cost == best && T >= 8)) {
+            best = cost;
+            a->T = T;
+            C = (int)c;
+        }
+    }
+    a->rows_per_block = kNormThreads / a->T;
+    const bool own = C == 2 && p.rope.start == 0 && p.rope.half == 8 * (int64_t)a->T && p.rope.L == 2 * p.rope.half;
+    // Tokens of a block: as many as leave 1024 blocks (cos and sin then keep
+    // more of its threads busy, and K's rows fill it), up to 8. Fewer tokens
+    // than that: a token's heads to as many blocks as its rows fill.
+    uint32_t per = 1;
+    while (per < 8 && a->tokens / (2 * per) >= 1024) per *= 2;
+    a->tokens_per_block = per;
+    a->groups = (a->tokens + per - 1) / per;
+    const uint32_t most = std::max(a->N[0], a->N[1]);
+    a->splits = backward || per > 1 || a->tokens >= 1024 ? 1 : std::max<uint32_t>(1, (most + a->rows_per_block - 1) / a->rows_per_block);
+    a->lds_floats = per * a->turn.pairs;
+    *lds = std::max<size_t>(2 * (size_t)a->lds_floats, backward ? (size_t)kNormWaves * a->T * 8 : 0) * sizeof(float);
+    a->t_div = make_fastdiv(a->T);
+    for (int i = 0; i < 2; ++i) a->n_div[i] = make_fastdiv(std::max<uint32_t>(1, a->N[i]));
+    a->pairs_div = make_fastdiv(std::max<uint32_t>(1, a->turn.pairs));
+    a->splits_div = make_fastdiv(a->splits);
+    // (rows of a block's tokens fit 31 bits, as all rows do)
+    if ((uint64_t)a->groups * a->splits > kMaxGridItems / kNormThreads) return nullptr;
+    const int par = a->turn.L == 0 || a->turn.half == 1 ? kParNear : own ? kParOwn : kParLoad;
+    if (C == 1) return par == kParNear ? vec_kernel<1, kParNear>(p.rope.dtype, backward) : vec_kernel<1, kParLoad>(p.rope.dtype, backward);
+    return par == kParNear  ? vec_kernel<2, kParNear>(p.rope.dtype, backward)
+           : par == kParOwn ? vec_kernel<2, kParOwn>(p.rope.dtype, backward)
+                            : vec_kernel<2, kParLoad>(p.rope.dtype, backward);
+}
 
 hipError_t launch_fwd(const NormPlan& p, hipStream_t s)
 {
-    NormArgs a = norm_args(p);
-    void* args[] = {&a};
-    const uint32_t blocks = (uint32_t)std::min<uint64_t>(a.tokens, kMaxGridItems / kNormThreads);
+    NormVecArgs a{};
+    static_cast<NormArgs&>(a) = norm_args(p);
+    size_t lds = 0;
+    if (const void* fn = norm_vec(p, false, &a, &lds)) {
+        void* args[] = {&a};
+        return hipLaunchKernel(fn, dim3(a.groups * a.splits), dim3(kNormThreads), args, lds, s);
+    }
+    NormArgs g = a;
+    void* args[] = {&g};
+    const uint32_t blocks = (uint32_t)std::min<uint64_t>(g.tokens, kMaxGridItems / kNormThreads);
     return hipLaunchKernel(by_type<FwdGeneral>(p.rope.dtype), dim3(blocks), dim3(kNormThreads), args, 0, s);
 }
 
@@ -67,10 +141,15 @@ hipError_t launch_bwd(const NormPlan& p, hipStream_t s)
 {
     uint32_t blocks = 0;
     if (!p.noop) {
-        NormArgs a = norm_args(p);
-        void* args[] = {&a};
-        blocks = (uint32_t)std::min<uint64_t>(a.tokens, kNormBwdBlocks);
-        hipError_t err = hipLaunchKernel(by_type<BwdGeneral>(p.rope.dtype), dim3(blocks), dim3(kNormThreads), args, 0, s);
+        NormVecArgs a{};
+        static_cast<NormArgs&>(a) = norm_args(p);
+        size_t lds = 0;
+        const void* fn = norm_vec(p, true, &a, &lds);
+        NormArgs g = a;
+        void* args[] = {fn != nullptr ? (void*)&a : (void*)&g};
+        blocks = (uint32_t)std::min<uint64_t>(fn != nullptr ? a.groups : a.tokens, kNormBwdBlocks);
+        hipError_t err = hipLaunchKernel(fn != nullptr ? fn : by_type<BwdGeneral>(p.rope.dtype), dim3(blocks), dim3(kNormThreads),
+                                         args, fn != nullptr ? lds : 0, s);
         if (err != hipSuccess) return err;
     }
     if (p.dw[0] == nullptr && p.dw[1] == nullptr) return hipSuccess;

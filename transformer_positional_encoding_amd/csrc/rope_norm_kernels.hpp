@@ -39,6 +39,19 @@ __device__ __forceinline__ float norm_weight(const NormArgs& a, int kind, uint32
     }
 }
 
+// Pairs that lie beside each other, turned back.
+__device__ __forceinline__ void turn_back_adjacent(float (&g)[8], const ChunkTurn& k, const float* cosv, const float* sinv)
+{
+    const float4 c = *reinterpret_cast<const float4*>(cosv + k.pair), s = *reinterpret_cast<const float4*>(sinv + k.pair);
+    const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float p = g[2 * i], q = g[2 * i + 1];
+        g[2 * i] = rotate_own_unfused(p, q, cc[i], sn[i], false);
+        g[2 * i + 1] = rotate_own_unfused(q, p, cc[i], sn[i], true);
+    }
+}
+
 // The sum over the lanes of a wave that differ in the bits below `width`.
 __device__ __forceinline__ float lanes_sum(float v, uint32_t width)
 {
@@ -168,6 +181,281 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_general_kernel(Nor
         }
         __syncthreads();
     }
+}
+
+// ---------------------------------------------------------------------------
+// Vector kernels: rows of whole 8-lane chunks. T threads of one wave share a
+// row, a thread holding C chunks (number c * T + t), as in the cache's write.
+// A block takes a few tokens: their cos and sin go to LDS, each pair of a token
+// evaluated once for all of its heads while the first rows are loaded; then the
+// rows of Q, then those of K, so that a thread's weights stay in registers for
+// all rows of a kind. Partners that lie whole chunks away are loaded with the
+// row (from the cache's line that the row's own thread loads) and normalised
+// again, unless the thread has them.
+// ---------------------------------------------------------------------------
+// Where a chunk's partners are: in the chunk (or it is not turned), in a chunk
+// that is loaded, in the thread's other chunk (C 2).
+constexpr int kParNear = 0, kParLoad = 1, kParOwn = 2;
+
+struct NormVecArgs : NormArgs {
+    uint32_t T;                // threads per row
+    uint32_t rows_per_block;   // 256 / T
+    uint32_t tokens_per_block;
+    uint32_t groups;           // of tokens_per_block tokens
+    uint32_t splits;           // blocks that share a token's heads (tokens_per_block is 1 then)
+    uint32_t lds_floats;       // of cos (sin follows)
+    FastDiv t_div, n_div[2], pairs_div, splits_div;
+};
+
+// The weights of a thread's chunks, and of their partners' where these are
+// loaded.
+template <int C, int PAR>
+struct NormWeights {
+    float own[C][8], par[PAR == kParLoad ? C : 1][8];
+    __device__ __forceinline__ void load(const NormVecArgs& a, int kind, const ChunkTurn (&k)[C], uint32_t tt)
+    {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint32_t lane0 = (c * a.T + tt) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                own[c][e] = lane0 < a.D ? norm_weight(a, kind, lane0 + e) : 0.0f;
+                if constexpr (PAR == kParLoad) par[c][e] = k[c].in ? norm_weight(a, kind, lane0 + k[c].to_partner + e) : 0.0f;
+            }
+        }
+    }
+};
+
+// cos and sin of n tokens' pairs from token tok0 on, to LDS.
+__device__ __forceinline__ void norm_turn_table(const NormVecArgs& a, uint32_t tok0, uint32_t n, float* lds)
+{
+    const uint32_t entries = n * a.turn.pairs;
+    for (uint32_t i = threadIdx.x; i < entries; i += kNormThreads) {
+        const uint32_t k = fast_div(i, a.pairs_div);
+        const uint32_t b = fast_div(tok0 + k, a.s_div);
+        const float2 cs = turn_cos_sin(a.turn, b, tok0 + k - b * a.S, i - k * a.turn.pairs);
+        lds[i] = cs.x;
+        lds[a.lds_floats + i] = cs.y;
+    }
+}
+
+// The row of a thread among those of a kind: token tok0 + k, head n.
+struct NormRow {
+    uint32_t k, b, s, n;
+};
+__device__ __forceinline__ NormRow norm_row(const NormVecArgs& a, int kind, uint32_t tok0, uint32_t n0, uint32_t it)
+{
+    NormRow r;
+    r.k = a.splits > 1 ? 0 : fast_div(it, a.n_div[kind]);
+    r.n = n0 + it - r.k * a.N[kind];
+    const uint32_t tok = tok0 + r.k;
+    r.b = fast_div(tok, a.s_div);
+    r.s = tok - r.b * a.S;
+    return r;
+}
+
+template <int DT, int C, int PAR>
+__global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_kernel(NormVecArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) float norm_lds[];
+    constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
+    const uint32_t t = threadIdx.x, tt = t & (a.T - 1), r0 = fast_div(t, a.t_div);
+    const uint32_t group = fast_div(blockIdx.x, a.splits_div), split = blockIdx.x - group * a.splits;
+    const uint32_t tok0 = group * a.tokens_per_block, ntok = min(a.tokens_per_block, a.tokens - tok0);
+    ChunkTurn kt[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) kt[c] = chunk_turn(a.turn, (c * a.T + tt) * 8);
+    if (a.turn.L > 0) {
+        norm_turn_table(a, tok0, ntok, norm_lds);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+        const uint32_t per = (a.N[kind] + a.splits - 1) / a.splits;
+        const uint32_t n0 = min(a.N[kind], split * per), n1 = min(a.N[kind], n0 + per);
+        const uint32_t rows = ntok * (n1 - n0);
+        if (rows == 0) continue;
+        NormWeights<C, PAR> w;
+        w.load(a, kind, kt, tt);
+        const gchar* const xd = as_global(a.x[kind].data);
+        gchar* const yd = as_global(a.y[kind].data);
+        for (uint32_t it = r0; it < rows; it += a.rows_per_block) {
+            const NormRow r = norm_row(a, kind, tok0, n0, it);
+            const gchar* src = xd + (r.b * a.x[kind].sb + r.s * a.x[kind].ss + r.n * a.x[kind].sn) * ES;
+            gchar* dst = yd + (r.b * a.y[kind].sb + r.s * a.y[kind].ss + r.n * a.y[kind].sn) * ES;
+            Chunk<DT> own[C], par[PAR == kParLoad ? C : 1];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t lane0 = (c * a.T + tt) * 8, at = lane0 < a.D ? lane0 : 0;
+                own[c].load(src + at * ES);
+                if constexpr (PAR == kParLoad)
+                    if (kt[c].in) par[c].load(src + (int32_t)(at + kt[c].to_partner) * ES);
+            }
+            float x[C][8], ss = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                own[c].widen(x[c]);
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(x[c][e], x[c][e], sum);
+                ss += (c * a.T + tt) * 8 < a.D ? sum : 0.0f;
+            }
+            const float inv = rsqrtf(__builtin_fmaf(lanes_sum(ss, a.T), a.inv_d, a.eps));
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[c][e] = x[c][e] * inv * w.own[c][e];
+            const float* cosv = norm_lds + r.k * a.turn.pairs;
+            const float* sinv = cosv + a.lds_floats;
+            if constexpr (PAR == kParOwn) {
+                float first[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) first[e] = x[0][e];
+                turn_chunk(x[0], x[C - 1], kt[0], false, cosv, sinv);
+                turn_chunk(x[C - 1], first, kt[C - 1], false, cosv, sinv);
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if (!kt[c].in) continue;
+                    if constexpr (PAR == kParLoad) {
+                        float p[8];
+                        par[c].widen(p);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) p[e] = p[e] * inv * w.par[c][e];
+                        turn_chunk(x[c], p, kt[c], false, cosv, sinv);
+                    } else {
+                        turn_chunk(x[c], x[c], kt[c], true, cosv, sinv);
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t lane0 = (c * a.T + tt) * 8;
+                if (lane0 < a.D) store_chunk<DT>(dst + lane0 * ES, x[c]);
+            }
+        }
+    }
+}
+
+// Backward: blocks take groups of tokens in turn; a thread sums its lanes' part
+// of the weight's gradient over all of its rows, and the block leaves one sum
+// per lane (lanes of one chunk lie in threads T apart).
+template <int DT, int C, int PAR>
+__global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(NormVecArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) float norm_lds[];
+    constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
+    const uint32_t t = threadIdx.x, tt = t & (a.T - 1), r0 = fast_div(t, a.t_div);
+    ChunkTurn kt[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) kt[c] = chunk_turn(a.turn, (c * a.T + tt) * 8);
+    float dw[2][C][8] = {};
+    for (uint32_t group = blockIdx.x; group < a.groups; group += gridDim.x) {
+        const uint32_t tok0 = group * a.tokens_per_block, ntok = min(a.tokens_per_block, a.tokens - tok0);
+        if (a.turn.L > 0) {
+            __syncthreads();                       // the rows of the group before are done
+            norm_turn_table(a, tok0, ntok, norm_lds);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const uint32_t rows = ntok * a.N[kind];
+            if (rows == 0) continue;
+            float w[C][8];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t j = (c * a.T + tt) * 8 + e;
+                    w[c][e] = j < a.D ? norm_weight(a, kind, j) : 0.0f;
+                }
+            const gchar* const xd = as_global(a.x[kind].data);
+            const gchar* const gd = as_global(a.dy[kind].data);
+            gchar* const yd = as_global(a.y[kind].data);
+            for (uint32_t it = r0; it < rows; it += a.rows_per_block) {
+                const NormRow r = norm_row(a, kind, tok0, 0, it);
+                const gchar* src = xd + (r.b * a.x[kind].sb + r.s * a.x[kind].ss + r.n * a.x[kind].sn) * ES;
+                const gchar* grad = gd + (r.b * a.dy[kind].sb + r.s * a.dy[kind].ss + r.n * a.dy[kind].sn) * ES;
+                gchar* dst = yd + (r.b * a.y[kind].sb + r.s * a.y[kind].ss + r.n * a.y[kind].sn) * ES;
+                Chunk<DT> own[C], up[C], par[PAR == kParLoad ? C : 1];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t lane0 = (c * a.T + tt) * 8, at = lane0 < a.D ? lane0 : 0;
+                    own[c].load(src + at * ES);
+                    up[c].load(grad + at * ES);
+                    if constexpr (PAR == kParLoad)
+                        if (kt[c].in) par[c].load(grad + (int32_t)(at + kt[c].to_partner) * ES);
+                }
+                const float* cosv = norm_lds + r.k * a.turn.pairs;
+                const float* sinv = cosv + a.lds_floats;
+                float x[C][8], g[C][8], ss = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) up[c].widen(g[c]);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    own[c].widen(x[c]);
+                    if (!kt[c].in) continue;
+                    ChunkTurn back = kt[c];        // turned back: the other sign
+                    back.first = !back.first;
+                    if constexpr (PAR != kParNear) {
+                        float p[8];
+                        if constexpr (PAR == kParOwn) up[C - 1 - c].widen(p);
+                        else par[c].widen(p);
+                        turn_chunk(g[c], p, back, false, cosv, sinv);
+                    } else {
+                        turn_back_adjacent(g[c], kt[c], cosv, sinv);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const bool in = (c * a.T + tt) * 8 < a.D;
+                    float s = 0.0f, d = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        s = __builtin_fmaf(x[c][e], x[c][e], s);
+                        d = __builtin_fmaf(g[c][e] * w[c][e], x[c][e], d);
+                    }
+                    ss += in ? s : 0.0f;
+                    dot += in ? d : 0.0f;
+                }
+                const float inv = rsqrtf(__builtin_fmaf(lanes_sum(ss, a.T), a.inv_d, a.eps));
+                const float m = lanes_sum(dot, a.T) * inv * a.inv_d;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t lane0 = (c * a.T + tt) * 8;
+                    float d[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float n = x[c][e] * inv;
+                        dw[kind][c][e] = __builtin_fmaf(g[c][e], n, dw[kind][c][e]);
+                        d[e] = inv * (g[c][e] * w[c][e] - n * m);
+                    }
+                    if (lane0 < a.D) store_chunk<DT>(dst + lane0 * ES, d);
+                }
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+    // lanes of a wave that hold the same chunk, then the waves
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v = dw[kind][c][e];
+                for (uint32_t d = a.T; d < 64; d <<= 1) v += __shfl_xor(v, (int)d);
+                if ((t & 63) < a.T) norm_lds[((t >> 6) * a.T + tt) * 8 + e] = v;
+            }
+            __syncthreads();
+            for (uint32_t j = t; j < a.T * 8; j += kNormThreads) {
+                float sum = 0.0f;
+                for (int w = 0; w < kNormWaves; ++w) sum += norm_lds[w * a.T * 8 + j];
+                const uint32_t lane = c * a.T * 8 + j;
+                if (lane < a.D) a.part[((uint64_t)blockIdx.x * 2 + kind) * a.D + lane] = sum;
+            }
+        }
 }
 
 // The weights' gradients: the blocks' sums added in a fixed order, rounded
