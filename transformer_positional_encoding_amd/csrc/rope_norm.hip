@@ -78,7 +78,9 @@ const void* norm_vec(const NormPlan& p, bool backward, NormVecArgs* a, size_t* l
 {
     const int es = p.rope.esize;
     for (int i = 0; i < 2; ++i)
-        if (!rows_in_chunks(p.x[i], es) || !rows_in_chunks(p.y[i], es) || (backward && !rows_in_chunks(p.dy[i], es))) return nullptr;
+        if ((p.w[i] != nullptr && !aligned16(p.w[i])) || !rows_in_chunks(p.x[i], es) || !rows_in_chunks(p.y[i], es) ||
+            (backward && !rows_in_chunks(p.dy[i], es)))
+            return nullptr;
     if (p.rotate && !turn_in_chunks(p.rope)) return nullptr;
     // Threads per row and chunks per thread: the fewest idle lanes; among those
     // two chunks where that leaves a row 8 threads (128 bytes of 16-bit lanes a
@@ -90,7 +92,7 @@ const void* norm_vec(const NormPlan& p, bool backward, NormVecArgs* a, size_t* l
         const uint32_t T = 1u << log2_of((chunks + c - 1) / c);
         if (T > 64) continue;
         const uint32_t cost = 2 * T * c + (T < 8 ? 1 : 0);
-        if (cost < best || (cost == best && T >= 8)) {
+        if (cost < best || (cost == best && T >= 8 && !backward)) {
             best = cost;
             a->T = T;
             C = (int)c;
@@ -155,7 +157,7 @@ hipError_t launch_bwd(const NormPlan& p, hipStream_t s)
     if (p.dw[0] == nullptr && p.dw[1] == nullptr) return hipSuccess;
     NormWeightArgs w{p.part, {p.dw[0], p.dw[1]}, blocks, (uint32_t)p.rope.D, p.wdtype};
     void* args[] = {&w};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&rope_norm_weight_grad_kernel), dim3((w.D + 15) / 16, 2), dim3(1024),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&rope_norm_weight_grad_kernel), dim3((w.D + 3) / 4, 2), dim3(kStrands),
                            args, 0, s);
 }
 

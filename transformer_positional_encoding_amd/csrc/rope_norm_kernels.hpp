@@ -52,10 +52,27 @@ __device__ __forceinline__ void turn_back_adjacent(float (&g)[8], const ChunkTur
     }
 }
 
-// The sum over the lanes of a wave that differ in the bits below `width`.
+// The sum over the lanes of a wave that differ in the bits below `width` (a
+// power of two), the same in all of them: by exchanges on the vector unit. (A
+// lane of the mirrored half row holds what the lane 4 or 8 away does, once
+// quads or eights are summed.)
 __device__ __forceinline__ float lanes_sum(float v, uint32_t width)
 {
-    for (uint32_t d = 1; d < width; d <<= 1) v += __shfl_xor(v, (int)d);
+    const auto dpp = [](float x, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    if (width > 1) v += dpp(v, std::integral_constant<int, 0xB1>{});       // lane ^ 1
+    if (width > 2) v += dpp(v, std::integral_constant<int, 0x4E>{});       // lane ^ 2
+    if (width > 4) v += dpp(v, std::integral_constant<int, 0x141>{});      // mirrored eights
+    if (width > 8) v += dpp(v, std::integral_constant<int, 0x140>{});      // mirrored sixteens
+    if (width > 16) {
+        const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+    if (width > 32) {
+        const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
     return v;
 }
 
@@ -207,6 +224,30 @@ struct NormVecArgs : NormArgs {
     FastDiv t_div, n_div[2], pairs_div, splits_div;
 };
 
+// 8 lanes of a weight.
+__device__ __forceinline__ void norm_weight8(const NormVecArgs& a, int kind, uint32_t j, float (&w)[8])
+{
+    const gchar* p = as_global(a.w[kind]);
+    if (a.w[kind] == nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+    } else if (a.wdt == ROPE_DTYPE_F32) {
+        Chunk<ROPE_DTYPE_F32> c;
+        c.load(p + j * 4);
+        c.widen(w);
+    } else {
+        Chunk<ROPE_DTYPE_F16> c;
+        c.load(p + j * 2);
+        if (a.wdt == ROPE_DTYPE_F16) {
+            c.widen(w);
+        } else {
+            Chunk<ROPE_DTYPE_BF16> b;
+            b.q[0] = c.q[0];
+            b.widen(w);
+        }
+    }
+}
+
 // The weights of a thread's chunks, and of their partners' where these are
 // loaded.
 template <int C, int PAR>
@@ -216,12 +257,9 @@ struct NormWeights {
     {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const uint32_t lane0 = (c * a.T + tt) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                own[c][e] = lane0 < a.D ? norm_weight(a, kind, lane0 + e) : 0.0f;
-                if constexpr (PAR == kParLoad) par[c][e] = k[c].in ? norm_weight(a, kind, lane0 + k[c].to_partner + e) : 0.0f;
-            }
+            const uint32_t lane0 = (c * a.T + tt) * 8, at = lane0 < a.D ? lane0 : 0;      // (past the row: not stored)
+            norm_weight8(a, kind, at, own[c]);
+            if constexpr (PAR == kParLoad) norm_weight8(a, kind, k[c].in ? at + k[c].to_partner : at, par[c]);
         }
     }
 };
@@ -265,25 +303,21 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_kernel(NormVecArgs
     ChunkTurn kt[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) kt[c] = chunk_turn(a.turn, (c * a.T + tt) * 8);
-    if (a.turn.L > 0) {
-        norm_turn_table(a, tok0, ntok, norm_lds);
-        __syncthreads();
-    }
+    bool table = a.turn.L == 0;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
         const uint32_t per = (a.N[kind] + a.splits - 1) / a.splits;
         const uint32_t n0 = min(a.N[kind], split * per), n1 = min(a.N[kind], n0 + per);
         const uint32_t rows = ntok * (n1 - n0);
         if (rows == 0) continue;
-        NormWeights<C, PAR> w;
-        w.load(a, kind, kt, tt);
         const gchar* const xd = as_global(a.x[kind].data);
         gchar* const yd = as_global(a.y[kind].data);
-        for (uint32_t it = r0; it < rows; it += a.rows_per_block) {
-            const NormRow r = norm_row(a, kind, tok0, n0, it);
+        Chunk<DT> own[C], par[PAR == kParLoad ? C : 1];
+        // a row's loads go out ahead of the row before it, the first ones' ahead
+        // of the table (threads without a row: the last one's)
+        const auto load = [&](uint32_t it) {
+            const NormRow r = norm_row(a, kind, tok0, n0, min(it, rows - 1));
             const gchar* src = xd + (r.b * a.x[kind].sb + r.s * a.x[kind].ss + r.n * a.x[kind].sn) * ES;
-            gchar* dst = yd + (r.b * a.y[kind].sb + r.s * a.y[kind].ss + r.n * a.y[kind].sn) * ES;
-            Chunk<DT> own[C], par[PAR == kParLoad ? C : 1];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const uint32_t lane0 = (c * a.T + tt) * 8, at = lane0 < a.D ? lane0 : 0;
@@ -291,15 +325,30 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_kernel(NormVecArgs
                 if constexpr (PAR == kParLoad)
                     if (kt[c].in) par[c].load(src + (int32_t)(at + kt[c].to_partner) * ES);
             }
-            float x[C][8], ss = 0.0f;
+            return r;
+        };
+        NormRow next = load(r0);
+        NormWeights<C, PAR> w;
+        w.load(a, kind, kt, tt);
+        if (!table) {
+            norm_turn_table(a, tok0, ntok, norm_lds);
+            __syncthreads();
+            table = true;
+        }
+        for (uint32_t it = r0; it < rows; it += a.rows_per_block) {
+            const NormRow r = next;
+            gchar* dst = yd + (r.b * a.y[kind].sb + r.s * a.y[kind].ss + r.n * a.y[kind].sn) * ES;
+            float x[C][8], p[PAR == kParLoad ? C : 1][8], ss = 0.0f;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 own[c].widen(x[c]);
+                if constexpr (PAR == kParLoad) par[c].widen(p[c]);
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(x[c][e], x[c][e], sum);
                 ss += (c * a.T + tt) * 8 < a.D ? sum : 0.0f;
             }
+            next = load(it + a.rows_per_block);
             const float inv = rsqrtf(__builtin_fmaf(lanes_sum(ss, a.T), a.inv_d, a.eps));
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -318,11 +367,9 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_kernel(NormVecArgs
                 for (int c = 0; c < C; ++c) {
                     if (!kt[c].in) continue;
                     if constexpr (PAR == kParLoad) {
-                        float p[8];
-                        par[c].widen(p);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) p[e] = p[e] * inv * w.par[c][e];
-                        turn_chunk(x[c], p, kt[c], false, cosv, sinv);
+                        for (int e = 0; e < 8; ++e) p[c][e] = p[c][e] * inv * w.par[c][e];
+                        turn_chunk(x[c], p[c], kt[c], false, cosv, sinv);
                     } else {
                         turn_chunk(x[c], x[c], kt[c], true, cosv, sinv);
                     }
@@ -341,7 +388,7 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_kernel(NormVecArgs
 // of the weight's gradient over all of its rows, and the block leaves one sum
 // per lane (lanes of one chunk lie in threads T apart).
 template <int DT, int C, int PAR>
-__global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(NormVecArgs a)
+__global__ void __launch_bounds__(kNormThreads, C == 1 ? 4 : 2) rope_norm_bwd_kernel(NormVecArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) float norm_lds[];
     constexpr int ES = DT == ROPE_DTYPE_F32 ? 4 : 2;
@@ -363,21 +410,15 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(NormVecArgs
             if (rows == 0) continue;
             float w[C][8];
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t j = (c * a.T + tt) * 8 + e;
-                    w[c][e] = j < a.D ? norm_weight(a, kind, j) : 0.0f;
-                }
+            for (int c = 0; c < C; ++c) norm_weight8(a, kind, (c * a.T + tt) * 8 < a.D ? (c * a.T + tt) * 8 : 0, w[c]);
             const gchar* const xd = as_global(a.x[kind].data);
             const gchar* const gd = as_global(a.dy[kind].data);
             gchar* const yd = as_global(a.y[kind].data);
-            for (uint32_t it = r0; it < rows; it += a.rows_per_block) {
-                const NormRow r = norm_row(a, kind, tok0, 0, it);
+            Chunk<DT> own[C], up[C], par[PAR == kParLoad ? C : 1];
+            const auto load = [&](uint32_t it) {   // as in the forward
+                const NormRow r = norm_row(a, kind, tok0, 0, min(it, rows - 1));
                 const gchar* src = xd + (r.b * a.x[kind].sb + r.s * a.x[kind].ss + r.n * a.x[kind].sn) * ES;
                 const gchar* grad = gd + (r.b * a.dy[kind].sb + r.s * a.dy[kind].ss + r.n * a.dy[kind].sn) * ES;
-                gchar* dst = yd + (r.b * a.y[kind].sb + r.s * a.y[kind].ss + r.n * a.y[kind].sn) * ES;
-                Chunk<DT> own[C], up[C], par[PAR == kParLoad ? C : 1];
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const uint32_t lane0 = (c * a.T + tt) * 8, at = lane0 < a.D ? lane0 : 0;
@@ -386,6 +427,12 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(NormVecArgs
                     if constexpr (PAR == kParLoad)
                         if (kt[c].in) par[c].load(grad + (int32_t)(at + kt[c].to_partner) * ES);
                 }
+                return r;
+            };
+            NormRow next = load(r0);
+            for (uint32_t it = r0; it < rows; it += a.rows_per_block) {
+                const NormRow r = next;
+                gchar* dst = yd + (r.b * a.y[kind].sb + r.s * a.y[kind].ss + r.n * a.y[kind].sn) * ES;
                 const float* cosv = norm_lds + r.k * a.turn.pairs;
                 const float* sinv = cosv + a.lds_floats;
                 float x[C][8], g[C][8], ss = 0.0f, dot = 0.0f;
@@ -406,6 +453,7 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(NormVecArgs
                         turn_back_adjacent(g[c], kt[c], cosv, sinv);
                     }
                 }
+                next = load(it + a.rows_per_block);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const bool in = (c * a.T + tt) * 8 < a.D;
@@ -459,7 +507,10 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(NormVecArgs
 }
 
 // The weights' gradients: the blocks' sums added in a fixed order, rounded
-// once. A block takes 16 lanes of one weight, 64 strands of partial sums.
+// once. A block takes 4 lanes of one weight, a thread a strand of partial sums:
+// many small blocks, since each sum has to come from another chiplet's cache.
+// (16 lanes a block, 64 strands: 7.6 us for 1024 sums of 128 lanes; 256 strands
+// of 16 lanes 9.2.)
 struct NormWeightArgs {
     const float* part;
     void* dw[2];
@@ -467,25 +518,34 @@ struct NormWeightArgs {
     int32_t wdt;
 };
 
-constexpr int kStrands = 64;
+constexpr int kStrands = 256;
 
-__global__ void __launch_bounds__(1024) rope_norm_weight_grad_kernel(NormWeightArgs a)
+__global__ void __launch_bounds__(kStrands) rope_norm_weight_grad_kernel(NormWeightArgs a)
 {
-    __shared__ float sums[kStrands][16];
-    const uint32_t strand = threadIdx.x >> 4, l = threadIdx.x & 15, j = blockIdx.x * 16 + l;
+    __shared__ float sums[kStrands / 64][4];
+    const uint32_t strand = threadIdx.x, j = blockIdx.x * 4;
     const int kind = blockIdx.y;
     if (a.dw[kind] == nullptr) return;
-    float sum = 0.0f;
-    if (j < a.D)
-        for (uint32_t b = strand; b < a.blocks; b += kStrands) sum += a.part[((uint64_t)b * 2 + kind) * a.D + j];
-    sums[strand][l] = sum;
+    float sum[4] = {};
+#pragma unroll 4
+    for (uint32_t b = strand; b < a.blocks; b += kStrands) {
+        const float* p = a.part + ((uint64_t)b * 2 + kind) * a.D + j;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += j + e < a.D ? p[e] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sum[e] = lanes_sum(sum[e], 64);
+        if ((strand & 63) == 0) sums[strand >> 6][e] = sum[e];
+    }
     __syncthreads();
-    if (strand != 0 || j >= a.D) return;
-    for (int k = 1; k < kStrands; ++k) sum += sums[k][l];
+    const uint32_t at = j + strand;
+    if (strand >= 4 || at >= a.D) return;
+    const float v = (sums[0][strand] + sums[1][strand]) + (sums[2][strand] + sums[3][strand]);
     switch (a.wdt) {
-    case ROPE_DTYPE_F32: Store<ROPE_DTYPE_F32>::store1(a.dw[kind], j, sum); break;
-    case ROPE_DTYPE_F16: Store<ROPE_DTYPE_F16>::store1(a.dw[kind], j, sum); break;
-    default: Store<ROPE_DTYPE_BF16>::store1(a.dw[kind], j, sum); break;
+    case ROPE_DTYPE_F32: Store<ROPE_DTYPE_F32>::store1(a.dw[kind], at, v); break;
+    case ROPE_DTYPE_F16: Store<ROPE_DTYPE_F16>::store1(a.dw[kind], at, v); break;
+    default: Store<ROPE_DTYPE_BF16>::store1(a.dw[kind], at, v); break;
     }
 }
 
