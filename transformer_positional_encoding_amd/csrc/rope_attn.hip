@@ -29,12 +29,15 @@ struct General {
 };
 template <int DT>
 struct JoinFew {
-    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_kernel<DT, 1>); }
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_few_kernel<DT>); }
 };
 template <int DT>
 struct JoinMany {
-    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_kernel<DT, kJoinWaves>); }
+    static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_many_kernel<DT>); }
 };
+
+// Parts up to which a wave joins a row.
+constexpr uint32_t kJoinFew = 8;
 
 AttnArgs attn_args(const AttnPlan& p)
 {
@@ -128,10 +131,11 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
                                      args, 0, s);
     if (err != hipSuccess || a.splits == 1) return launched(err);
     args[0] = &g;
-    const bool many = a.splits > 8;
-    const uint64_t rows = many ? 1 : kJoinWaves;
-    return launched(hipLaunchKernel(many ? by_type<JoinMany>(p.rope.dtype) : by_type<JoinFew>(p.rope.dtype),
-                                    dim3((uint32_t)((a.part_rows + rows - 1) / rows)), dim3(kJoinThreads), args, 0, s));
+    if (a.splits > kJoinFew)       // (few rows, then)
+        return launched(hipLaunchKernel(by_type<JoinMany>(p.rope.dtype), dim3((uint32_t)a.part_rows, (a.Dv + kJoinLanes - 1) / kJoinLanes),
+                                        dim3(kJoinThreads), args, 0, s));
+    return launched(hipLaunchKernel(by_type<JoinFew>(p.rope.dtype), dim3((uint32_t)((a.part_rows + kJoinRows - 1) / kJoinRows)),
+                                    dim3(kJoinThreads), args, 0, s));
 }
 
 }  // namespace

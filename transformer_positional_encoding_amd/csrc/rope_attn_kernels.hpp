@@ -95,6 +95,13 @@ __device__ __forceinline__ float2* part_stats(const AttnArgs& a)
     return reinterpret_cast<float2*>(a.part + (uint64_t)a.splits * a.part_rows * a.Dv);
 }
 
+// How much a part counts whose maximum is m.
+__device__ __forceinline__ float part_weight(float m, float most)
+{
+    return m == kAttnNone ? 0.0f : m == most ? 1.0f : exp2f(m - most);
+}
+__device__ __forceinline__ float one_over(float sum) { return sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum; }   // NaN stays
+
 // ---------------------------------------------------------------------------
 // General kernel: any dimensions, groups, alignment and types. A block takes up
 // to 4 rows that share a cached head, 256 tokens at a time: a thread a token's
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
         float sum = 0.0f;
         for (int w = 0; w < kAttnGenThreads / 64; ++w) sum += red[r][w];
         const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
-        const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;      // NaN stays
+        const float inv = one_over(sum);
         const uint64_t row = part_row(a, at.split, at.b, s, h);
         for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
             const uint32_t j = k * kAttnGenThreads + t;
@@ -218,67 +225,109 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
     }
 }
 
-// Joins the parts of a row. W waves take a row's parts in turn, a strand of
-// lanes each, and are added in order: latency is all there is to it. (One wave
-// a row of 256 parts: 250 us.)
+// Joins the parts of a row, which are added in a fixed order. Latency is all
+// there is to it. Few parts: a wave a row. Many: a block takes 32 lanes of a
+// row, half a wave a part, 16 parts at a time in as many strands. (One wave a
+// row of 256 parts: 250 us; a block a row 10.)
 constexpr int kJoinThreads = 512;
-constexpr int kJoinWaves = kJoinThreads / 64;
+constexpr int kJoinRows = kJoinThreads / 64;       // of a block, with few parts
+constexpr int kJoinLanes = 32;                     // of a block, with many
+constexpr int kJoinAhead = 4;                      // parts whose loads go out together
 
-template <int DT, int W>
-__global__ void __launch_bounds__(kJoinThreads) rope_attn_join_kernel(AttnArgs a)
+template <int DT>
+__global__ void __launch_bounds__(kJoinThreads) rope_attn_join_few_kernel(AttnArgs a)
 {
-    constexpr int R = kJoinWaves / W;              // rows of a block
-    constexpr int K = 4;                           // parts whose loads go out together
-    __shared__ float weight[R][W == 1 ? 1 : kAttnMaxParts];
-    __shared__ float sums[W == 1 ? 1 : W][W == 1 ? 1 : ROPE_D_LIMIT];
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mine = wave % W;
-    const uint64_t row64 = (uint64_t)blockIdx.x * R + wave / W;
-    if (row64 >= a.part_rows) return;              // (W > 1: a row a block)
+    const uint32_t lane = threadIdx.x & 63;
+    const uint64_t row64 = (uint64_t)blockIdx.x * kJoinRows + (threadIdx.x >> 6);
+    if (row64 >= a.part_rows) return;
     const uint32_t row = (uint32_t)row64;
     const uint32_t tok = row / a.Hq, h = row - tok * a.Hq, b = tok / a.S, s = tok - b * a.S;
     if ((int32_t)s >= attn_seq(a, b).count) return;
     const float2* stats = part_stats(a) + row;
-    float m = kAttnNone, l = 0.0f;
-    for (uint32_t i = lane; i < a.splits; i += 64) m = fmaxf(m, stats[i * a.part_rows].x);
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const auto weigh = [&](const float2& st) { return st.x == kAttnNone ? 0.0f : st.x == m ? 1.0f : exp2f(st.x - m); };
-    for (uint32_t i = lane; i < a.splits; i += 64) {
-        const float2 st = stats[i * a.part_rows];
-        const float w = weigh(st);
-        l = __builtin_fmaf(st.y, w, l);
-        if (W > 1 && mine == 0) weight[0][i] = w;
-    }
-    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-    if (W > 1) __syncthreads();
     const int64_t out = b * a.out.sb + s * a.out.ss + h * a.out.sn;
-    for (uint32_t j = lane; j < a.Dv; j += 64) {
+    const uint64_t step = a.part_rows * a.Dv;
+    float m = kAttnNone, l = 0.0f;
+    for (uint32_t i = 0; i < a.splits; ++i) m = fmaxf(m, stats[i * a.part_rows].x);
+    for (uint32_t i = 0; i < a.splits; ++i) {
+        const float2 st = stats[i * a.part_rows];
+        l = __builtin_fmaf(st.y, part_weight(st.x, m), l);
+    }
+    const float inv = one_over(l);
+    for (uint32_t j = 2 * lane; j < a.Dv; j += 128) {          // (Dv is even)
         const float* part = a.part + (uint64_t)row * a.Dv + j;
-        const uint64_t step = a.part_rows * a.Dv;
-        float o = 0.0f;
-        for (uint32_t i = mine; i < a.splits; i += W * K) {
-            float v[K], w[K];
+        float o[2] = {};
+        for (uint32_t i = 0; i < a.splits; i += kJoinAhead) {
+            float2 v[kJoinAhead];
+            float w[kJoinAhead];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const uint32_t at = min(i + k * W, a.splits - 1);
-                v[k] = part[at * step];
-                w[k] = W > 1 ? weight[0][at] : weigh(stats[at * a.part_rows]);
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const uint32_t at = min(i + k, a.splits - 1);
+                v[k] = *reinterpret_cast<const float2*>(part + at * step);
+                w[k] = part_weight(stats[at * a.part_rows].x, m);
             }
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (i + k * W < a.splits && w[k] != 0.0f) o = __builtin_fmaf(v[k], w[k], o);
+            for (int k = 0; k < kJoinAhead; ++k)
+                if (i + k < a.splits && w[k] != 0.0f) {
+                    o[0] = __builtin_fmaf(v[k].x, w[k], o[0]);
+                    o[1] = __builtin_fmaf(v[k].y, w[k], o[1]);
+                }
         }
-        if (W == 1) Store<DT>::store1(a.out.data, out + j, o * inv);
-        else sums[mine][j] = o;
+        Store<DT>::store1(a.out.data, out + j, o[0] * inv);
+        Store<DT>::store1(a.out.data, out + j + 1, o[1] * inv);
     }
-    if (W == 1) return;
-    __syncthreads();
-    for (uint32_t j = threadIdx.x; j < a.Dv; j += kJoinThreads) {
-        float o = sums[0][j];
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kJoinThreads) rope_attn_join_many_kernel(AttnArgs a)
+{
+    constexpr int kStrandsOf = kJoinThreads / kJoinLanes;
+    __shared__ float weight[kAttnMaxParts];
+    __shared__ float sums[kStrandsOf][kJoinLanes];
+    const uint32_t t = threadIdx.x, lane = t & 63;
+    const uint32_t row = blockIdx.x, j = blockIdx.y * kJoinLanes + (t & (kJoinLanes - 1)), strand = t / kJoinLanes;
+    const uint32_t tok = row / a.Hq, h = row - tok * a.Hq, b = tok / a.S, s = tok - b * a.S;
+    if ((int32_t)s >= attn_seq(a, b).count) return;
+    const float2* stats = part_stats(a) + row;
+    // every wave for itself: the parts' maximum and sum
+    float m = kAttnNone, l = 0.0f;
+    float2 st[kAttnMaxParts / 64];
 #pragma unroll
-        for (int w = 1; w < W; ++w) o += sums[w][j];
-        Store<DT>::store1(a.out.data, out + j, o * inv);
+    for (int k = 0; k < kAttnMaxParts / 64; ++k) {
+        const uint32_t i = k * 64 + lane;
+        st[k] = i < a.splits ? stats[i * a.part_rows] : make_float2(kAttnNone, 0.0f);
+        m = fmaxf(m, st[k].x);
     }
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+#pragma unroll
+    for (int k = 0; k < kAttnMaxParts / 64; ++k) {
+        const float w = part_weight(st[k].x, m);
+        if (k * 64 + lane < a.splits) {
+            l = __builtin_fmaf(st[k].y, w, l);
+            if (t < 64) weight[k * 64 + lane] = w;
+        }
+    }
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+    __syncthreads();
+    float o = 0.0f;
+    const uint64_t step = a.part_rows * a.Dv;
+    const float* part = a.part + (uint64_t)row * a.Dv + min(j, a.Dv - 1);
+    for (uint32_t i = strand; i < a.splits; i += kStrandsOf * kJoinAhead) {
+        float v[kJoinAhead];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) v[k] = part[min(i + k * kStrandsOf, a.splits - 1) * step];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const uint32_t at = i + k * kStrandsOf;
+            if (at < a.splits && weight[at] != 0.0f) o = __builtin_fmaf(v[k], weight[at], o);
+        }
+    }
+    sums[strand][t & (kJoinLanes - 1)] = o;
+    __syncthreads();
+    if (t >= kJoinLanes || j >= a.Dv) return;
+    o = sums[0][t];
+#pragma unroll
+    for (int k = 1; k < kStrandsOf; ++k) o += sums[k][t];
+    Store<DT>::store1(a.out.data, b * a.out.sb + s * a.out.ss + h * a.out.sn + j, o * one_over(l));
 }
 
 }  // namespace

@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             const float sum = column_sum(l[t]);
             if (r >= live) continue;
             const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
-            const float inv = a.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+            const float inv = a.splits > 1 ? 1.0f : one_over(sum);
             float f[NGV];
 #pragma unroll
             for (int g = 0; g < NGV; ++g) f[g] = __builtin_ldexpf(inv, e[t][g]);
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         __syncthreads();
         float most = kAttnNone;
         for (uint32_t w = head_wave; w < 4; w += a.head_waves) most = fmaxf(most, lds.join.m[w][n16]);
-        const float keep = m[t] == kAttnNone ? 0.0f : m[t] == most ? 1.0f : exp2f(m[t] - most);
+        const float keep = part_weight(m[t], most);
 #pragma unroll
         for (int i = 0; i < VT; ++i) {
             const float f = __builtin_ldexpf(keep, e[t][VF ? i / 2 : 0]);
@@ -662,10 +662,10 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             for (uint32_t w = hw; w < 4; w += a.head_waves) high = fmaxf(high, lds.join.m[w][row16]);
             for (uint32_t w = hw; w < 4; w += a.head_waves) {
                 const float mw = lds.join.m[w][row16];
-                whole += lds.join.l[w][row16] * (mw == kAttnNone ? 0.0f : mw == high ? 1.0f : exp2f(mw - high));
+                whole += lds.join.l[w][row16] * (part_weight(mw, high));
             }
             const uint32_t h = (at.head * a.head_waves + hw) * a.rep + (r - s * a.rep);
-            const float inv = a.splits > 1 ? 1.0f : whole > 0.0f ? 1.0f / whole : whole == 0.0f ? 0.0f : whole;
+            const float inv = a.splits > 1 ? 1.0f : one_over(whole);
             const uint64_t row = part_row(a, at.split, at.b, s, h);
             gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
             for (uint32_t j = 8 * (threadIdx.x & 15); j < a.Dv && r < live; j += 128) {

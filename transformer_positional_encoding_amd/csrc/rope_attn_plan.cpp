@@ -13,7 +13,7 @@ constexpr int64_t kI64Max = std::numeric_limits<int64_t>::max();
 // Blocks that fill the card several times over, and the fewest tokens that
 // are worth a block of their own.
 constexpr int64_t kAttnBlocks = 2048;
-constexpr int64_t kAttnSplitTokens = 256;
+constexpr int64_t kAttnSplitTokens = 64;
 // Rows of a tile: the partial results of a call are B * heads * tiles * 16 at
 // most for each part.
 constexpr int64_t kAttnTileRows = 16;
