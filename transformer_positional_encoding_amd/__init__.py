@@ -1527,10 +1527,9 @@ def rope_cache_read(out, cache, block_table, lengths, starts=None, positions=Non
     _TORCH[2]((out,))
 
 
-def _arrays(name, t, dtype, shape, dev):
-    """A contiguous tensor of a call's bookkeeping."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+def _array(name, t, tensor, dtype, shape, dev):
+    """The address of a contiguous tensor of a call's bookkeeping."""
+    if not isinstance(t, tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {str(dtype).split('.')[-1]} tensor {shape}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
@@ -1571,23 +1570,22 @@ def rope_cache_reserve(block_table, lengths, counts, free_pages, free_count, pag
     if tokens is None:
         given = slots if slots is not None else positions
         tokens = given.shape[1] if given is not None and given.dim() == 2 else 1
-    ins = [_arrays(n, t, torch.int32, sh, dev) for n, t, sh in (
-        ("lengths", lengths, (B,)), ("counts", counts, (B,)), ("free_pages", free_pages, (free_pages.shape[0],)),
-        ("free_count", free_count, (1,)))]
-    with _allocating_on(stream, dev) if stream is not None and block_table.is_cuda else _nullcontext():
-        if slots is None:
-            slots = torch.empty(B, tokens, dtype=torch.int64, device=dev)
-        if positions is None:
-            positions = torch.empty(B, tokens, dtype=torch.int64, device=dev)
-        if granted is None:
-            granted = torch.empty(B, dtype=torch.int32, device=dev)
-    outs = [_arrays("slots", slots, torch.int64, (B, tokens), dev),
-            _arrays("positions", positions, torch.int64, (B, tokens), dev),
-            _arrays("granted", granted, torch.int32, (B,), dev)]
+    T, i32, i64 = torch.Tensor, torch.int32, torch.int64
+    capacity = free_pages.shape[0]
+    at = (_array("lengths", lengths, T, i32, (B,), dev), _array("counts", counts, T, i32, (B,), dev),
+          _array("free_pages", free_pages, T, i32, (capacity,), dev), capacity,
+          _array("free_count", free_count, T, i32, (1,), dev))
+    if slots is None or positions is None or granted is None:
+        with _allocating_on(stream, dev) if stream is not None and block_table.is_cuda else _NOTHING:
+            slots = torch.empty(B, tokens, dtype=i64, device=dev) if slots is None else slots
+            positions = torch.empty(B, tokens, dtype=i64, device=dev) if positions is None else positions
+            granted = torch.empty(B, dtype=i32, device=dev) if granted is None else granted
+    outs = (_array("slots", slots, T, i64, (B, tokens), dev), _array("positions", positions, T, i64, (B, tokens), dev),
+            _array("granted", granted, T, i32, (B,), dev))
     handle, current = _on_device(block_table, stream)
     with current:
-        st = library().rope_cache_reserve(B, tokens, block_table.data_ptr() or None, cols, block_table.stride(0), ins[0],
-                                          ins[1], ins[2], free_pages.shape[0], ins[3], page_size, *outs, handle)
+        st = _words_entry("rope_cache_reserve")(B, tokens, block_table.data_ptr() or None, cols, block_table.stride(0), *at,
+                                                page_size, *outs, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
     (_TORCH or _autograd())[2]((block_table, lengths, free_pages, free_count, slots, positions, granted))
@@ -1644,23 +1642,24 @@ def rope_cache_attention(q, k_cache, v_cache, block_table, lengths, counts=None,
         raise ValueError("block_table: the pages of a sequence must be consecutive")
     if block_table.device != dev:
         raise ValueError(f"block_table must be on {dev}")
-    at_lengths = _arrays("lengths", lengths, torch.int32, (B,), dev)
-    at_counts = None if counts is None else _arrays("counts", counts, torch.int32, (B,), dev)
+    at_lengths = _array("lengths", lengths, torch.Tensor, torch.int32, (B,), dev)
+    at_counts = None if counts is None else _array("counts", counts, torch.Tensor, torch.int32, (B,), dev)
     _refuse_differentiated("rope_cache_attention", ("q", "out"), (q, out) + k_cache._tensors + v_cache._tensors)
     kv_heads, v_dim = k_cache._words[5], v_cache._words[6]
     given = out is not None
     if given:
-        if not isinstance(out, torch.Tensor) or tuple(out.shape) != (B, S, heads, v_dim):
+        if not isinstance(out, torch.Tensor) or out.shape != (B, S, heads, v_dim):
             raise ValueError(f"out must be a {(B, S, heads, v_dim)} tensor")
         if out.dtype != q.dtype or out.device != dev:
             raise ValueError(f"out must be {q.dtype} on {dev}")
-    with _allocating_on(stream, dev) if stream is not None and q.is_cuda else _nullcontext():
-        if out is None:
-            make = torch.empty if counts is None else torch.zeros
-            out = make(B, S, heads, v_dim, dtype=q.dtype, device=dev)
-        if workspace is None:
-            need = library().rope_cache_attention_workspace(B, S, heads, kv_heads, v_dim)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if out is None or workspace is None:
+        with _allocating_on(stream, dev) if stream is not None and q.is_cuda else _NOTHING:
+            if out is None:
+                make = torch.empty if counts is None else torch.zeros
+                out = make(B, S, heads, v_dim, dtype=q.dtype, device=dev)
+            if workspace is None:
+                need = rope_cache_attention_workspace(B, S, heads, kv_heads, v_dim)
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     handle, current = _on_device(q, stream)
@@ -1708,6 +1707,13 @@ def _norm_rows(name, t, like):
     return _rows(name, t)
 
 
+def _new_rows(like):
+    """A new contiguous tensor of the same shape, and its rows."""
+    b, s, n, d = like.shape
+    t = like.new_empty(like.shape)
+    return t, _RowsWords(t.data_ptr(), n, d, s * n * d, n * d, d)
+
+
 def _norm_args(q, k, names=("q", "k")):
     import torch
     for name, t in zip(names, (q, k)):
@@ -1745,25 +1751,30 @@ def rope_qk_norm_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     ptrs = _norm_weights(q, k, q_weight, k_weight)
     _refuse_differentiated("rope_qk_norm_fwd", ("q", "k", "q_weight", "k_weight", "q_out", "k_out"),
                            (q, k, q_weight, k_weight, q_out, k_out))
-    given = tuple(t for t in (q_out, k_out) if t is not None)
+    given = q_out is not None or k_out is not None
     if k is None and k_out is not None:
         raise ValueError("k_out goes with k")
-    with _allocating_on(stream, q.device) if stream is not None and q.is_cuda else _nullcontext():
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     code = _dtype_code(q)
+    rows_q = _rows("q", q)
+    rows_k = None if k is None else _rows("k", k)
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, q.device)
+    written = () if not given else tuple(t for t in (q_out, k_out) if t is not None)
+    rows_qo = None if q_out is None else _norm_rows("q_out", q_out, q)
+    rows_ko = None if k_out is None else _norm_rows("k_out", k_out, k)
+    if q_out is None or (k_out is None and k is not None):
+        with _allocating_on(stream, q.device) if stream is not None and q.is_cuda else _NOTHING:
+            if q_out is None:
+                q_out, rows_qo = _new_rows(q)
+            if k is not None and k_out is None:
+                k_out, rows_ko = _new_rows(k)
     handle, current = _on_device(q, stream)
     with current:
-        st = _words_entry("rope_qk_norm_fwd")(
-            q.shape[0], q.shape[1], code, _norm_rows("q_out", q_out, q), None if k is None else _norm_rows("k_out", k_out, k),
-            _rows("q", q), None if k is None else _rows("k", k), *ptrs, eps, *turn, handle)
+        st = _words_entry("rope_qk_norm_fwd")(q.shape[0], q.shape[1], code, rows_qo, rows_ko, rows_q, rows_k, *ptrs, eps,
+                                              *turn, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
     if given:
-        (_TORCH or _autograd())[2](given)
+        _TORCH[2](written)
     return q_out, k_out
 
 
