@@ -82,7 +82,7 @@ bool codes_aligned(const CachePlan& c, uintptr_t bytes)
 
 // The matrix-core kernel of a call, and its lanes; NULL if it does not take the
 // shapes.
-const void* mfma_kernel(const AttnPlan& p, int tiles, int lanes)
+const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes)
 {
     const int64_t D = p.q.D, Dv = p.out.D;
     if (p.rope.dtype == ROPE_DTYPE_F32 || D > 256 || Dv > 256 || !rows_in_chunks(p.q, 2) || !rows_in_chunks(p.out, 2))
@@ -94,8 +94,8 @@ const void* mfma_kernel(const AttnPlan& p, int tiles, int lanes)
     if (!codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4)) return nullptr;
     const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
     if (p.rope.dtype == ROPE_DTYPE_BF16)
-        return whole16 ? attn_kernel_bf16(lanes, scales, tiles) : attn_kernel_bf16_any(lanes, scales, tiles);
-    return whole16 ? attn_kernel_f16(lanes, scales, tiles) : attn_kernel_f16_any(lanes, scales, tiles);
+        return whole16 ? attn_kernel_bf16(lanes, scales, rows) : attn_kernel_bf16_any(lanes, scales, rows);
+    return whole16 ? attn_kernel_f16(lanes, scales, rows) : attn_kernel_f16_any(lanes, scales, rows);
 }
 
 rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
@@ -103,12 +103,12 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     AttnVecArgs a{};
     static_cast<AttnArgs&>(a) = attn_args(p);
     const int lanes = std::max(p.q.D, p.out.D) <= 64 ? 64 : std::max(p.q.D, p.out.D) <= 128 ? 128 : 256;
-    const int tiles = lanes == 256 || a.rows <= 16 ? 1 : 2;
-    const void* fn = mfma_kernel(p, tiles, lanes);
+    const AttnRowsOf rows = lanes == 256 || a.rows <= 16 ? AttnRowsOf::kOneTile : a.rows <= 64 ? AttnRowsOf::kTwoTiles : AttnRowsOf::kShared;
+    const void* fn = mfma_kernel(p, rows, lanes);
     const bool mfma = fn != nullptr;
     // Few rows: a wave a head, as far as heads go by fours, which then read
-    // neighbouring bytes; else waves take turns at the tokens. Many: a wave a
-    // tile of rows.
+    // neighbouring bytes; else waves take turns at the tokens. Many: a wave its
+    // own rows.
     a.head_waves = a.token_waves = a.row_waves = 1;
     if (a.rows > 64) a.row_waves = 4;
     else if (a.heads % 4 == 0) a.head_waves = 4;
@@ -119,7 +119,7 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     a.v_group = a.vc.group;
     a.k_groups = a.D / a.k_group;
     a.v_groups = a.Dv / a.v_group;
-    const uint32_t block_rows = !mfma ? kAttnGenRows : 16 * tiles * (int)a.row_waves;
+    const uint32_t block_rows = !mfma ? kAttnGenRows : (rows == AttnRowsOf::kOneTile ? 16 : 32) * a.row_waves;
     a.tiles = (a.rows + block_rows - 1) / block_rows;
     a.tiles_div = make_fastdiv(a.tiles);
     const uint64_t blocks = (uint64_t)p.B * a.heads_div.d * a.tiles * a.splits;

@@ -3,9 +3,9 @@
 
 namespace rope {
 
-const void* attn_kernel_bf16(int lanes, int scales, int tiles)
+const void* attn_kernel_bf16(int lanes, int scales, AttnRowsOf rows)
 {
-    return attn_kernel<ROPE_DTYPE_BF16, true>(lanes, scales, tiles);
+    return attn_kernel<ROPE_DTYPE_BF16, true>(lanes, scales, rows);
 }
 
 }  // namespace rope

@@ -3,9 +3,9 @@
 
 namespace rope {
 
-const void* attn_kernel_f16(int lanes, int scales, int tiles)
+const void* attn_kernel_f16(int lanes, int scales, AttnRowsOf rows)
 {
-    return attn_kernel<ROPE_DTYPE_F16, true>(lanes, scales, tiles);
+    return attn_kernel<ROPE_DTYPE_F16, true>(lanes, scales, rows);
 }
 
 }  // namespace rope

@@ -3,9 +3,9 @@
 
 namespace rope {
 
-const void* attn_kernel_f16_any(int lanes, int scales, int tiles)
+const void* attn_kernel_f16_any(int lanes, int scales, AttnRowsOf rows)
 {
-    return attn_kernel<ROPE_DTYPE_F16, false>(lanes, scales, tiles);
+    return attn_kernel<ROPE_DTYPE_F16, false>(lanes, scales, rows);
 }
 
 }  // namespace rope

@@ -10,12 +10,16 @@ constexpr int kAttnRowScales = 0;
 constexpr int kAttnKSegments = 1;
 constexpr int kAttnSegments = 2;
 
-// The kernel for rows of up to `lanes` lanes (64, 128, 256) and `tiles` tiles of
-// 16 rows a wave (1; 2 up to 128 lanes). _any: for pages of any size, the others
-// for pages of whole 16 tokens less than 2^26 bytes apart.
-const void* attn_kernel_bf16(int lanes, int scales, int tiles);
-const void* attn_kernel_f16(int lanes, int scales, int tiles);
-const void* attn_kernel_bf16_any(int lanes, int scales, int tiles);
-const void* attn_kernel_f16_any(int lanes, int scales, int tiles);
+// Query rows of a cached head that a kernel takes: 16 or 32 a wave, by waves on
+// their own, or 32 a wave, 128 a block, whose waves share their tiles' numbers.
+enum class AttnRowsOf { kOneTile, kTwoTiles, kShared };
+
+// The kernel for rows of up to `lanes` lanes (64, 128; 256: kOneTile only).
+// _any: for pages of any size, the others for pages of whole 16 tokens less
+// than 2^26 bytes apart.
+const void* attn_kernel_bf16(int lanes, int scales, AttnRowsOf rows);
+const void* attn_kernel_f16(int lanes, int scales, AttnRowsOf rows);
+const void* attn_kernel_bf16_any(int lanes, int scales, AttnRowsOf rows);
+const void* attn_kernel_f16_any(int lanes, int scales, AttnRowsOf rows);
 
 }  // namespace rope

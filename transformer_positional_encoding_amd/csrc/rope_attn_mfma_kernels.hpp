@@ -183,250 +183,79 @@ struct alignas(16) AttnLds {
     };
 };
 
-// Waves that a SIMD is to hold: what their registers allow.
-constexpr int attn_waves(int lanes, bool kf, int tiles)
-{
-    return lanes == 256 ? 1 : (lanes == 64 || !kf ? 4 : 3) - tiles;
-}
+// A wave's query rows, 16 to a tile, and what it holds of their attention: all
+// that does not depend on where a tile's numbers come from.
+template <int DT, int DP, int DVP, bool KF, bool VF, int NT>
+struct AttnRows {
+    static constexpr int KW = DP / 32;             // steps of a product with K
+    static constexpr int VT = DVP / 16;            // products of 16 lanes of V
+    static constexpr int NGV = VF ? DVP / 32 : 1;
 
-template <int DT, int DP, int DVP, bool KF, bool VF, bool P16, int NT>
-__global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_kernel(AttnVecArgs a)
-{
-    using Lds = AttnLds<DP, DVP, KF, VF, NT>;
-    constexpr int KW = DP / 32;                    // words of a K row that a lane takes
-    constexpr int VT = DVP / 16;                   // products of 16 lanes of V
-    constexpr int VR = DVP >= 128 ? DVP / 128 : 1; // registers of a token's V
-    constexpr int VH = DVP / 64;                   // 16-bit halves of them
-    constexpr int NGK = Lds::NGK, NGV = Lds::NGV;
-    __shared__ Lds lds;
-    const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    typename Lds::Wave& my = lds.wave[wave];
-
-    const AttnAt at = attn_at(a, blockIdx.x);
-    const AttnSeq seq = attn_seq(a, at.b);
-    const uint32_t head_wave = wave & (a.head_waves - 1), token_wave = a.row_waves > 1 ? 0 : wave / a.head_waves;
-    const uint32_t head = at.head * a.head_waves + head_wave, waves = a.token_waves;
-    const uint32_t r0 = (at.tile * a.row_waves + (a.row_waves > 1 ? wave : 0)) * 16 * NT;
-    const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
-    if (r0 >= live) return;                        // where waves are joined the same for the whole block
-    // the tokens that some row sees, this part of them, and those that all see
-    uint32_t n = (uint32_t)seq.tokens, all = n;
-    if (a.causal) {
-        const int64_t most = seq.first + fast_div(min(r0 + 16 * NT, live) - 1, a.rep_div) + 1;
-        const int64_t least = seq.first + fast_div(r0, a.rep_div) + 1;
-        n = (uint32_t)max((int64_t)0, min((int64_t)n, most));
-        all = (uint32_t)max((int64_t)0, min((int64_t)n, least));
-    }
-    uint32_t from, to;
-    attn_part(n, at.split, a.splits, 64 * waves, &from, &to);
-    all = min(all, to);
-
-    // queries: a column a row, 8 elements a step in k_numbers' order
     v4u q[NT][KW];
     f32x4 start[NT][KF ? KW : 1];
-    int32_t last[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const uint32_t r = min(r0 + t * 16 + n16, live - 1);
-        const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
-        last[t] = a.causal ? (int32_t)(seq.first + s) : INT32_MAX;
-        const gchar* row = as_global(a.q.data) + (at.b * a.q.sb + s * a.q.ss + h * a.q.sn) * 2;
-        float sum = 0.0f;
-#pragma unroll
-        for (int st = 0; st < KW; ++st) {
-            const uint32_t d = KF ? 32 * st + 8 * kq : kq * (DP / 4) + 8 * st;
-            v4u v{0, 0, 0, 0};
-            if (d < a.D) v = gload<v4u>(row + d * 2);
-            Lanes<DT> f;
-            f.unpack(v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum += f.v[e];
-            q[t][st] = q_order(v);
-            if (KF || st == KW - 1) {
-                const float c = -24.0f * column_sum(sum);
-                start[t][KF ? st : 0] = f32x4{c, c, c, c};
-                sum = 0.0f;
-            }
-        }
-    }
-
-    // where this lane's words of a row start
-    const gchar* const k_base = as_global(a.kc.data) + head * a.kc.st[2];
-    const gchar* const v_base = as_global(a.vc.data) + head * a.vc.st[2];
-    const gchar* const ks_base = as_global(a.kc.scales) + head * a.kc.sc[2] * 4;
-    const gchar* const vs_base = as_global(a.vc.scales) + head * a.vc.sc[2] * 4;
-    const int32_t* const table = a.table + at.b * a.table_stride;
-    const uint32_t k_bytes = a.D / 2, v_bytes = a.Dv / 2;
-    const uint32_t q4 = n16 >> 2, a4 = n16 & 3, q2 = n16 >> 1, a2 = n16 & 1;
-    const uint32_t sel1 = (lane & 1) ? 0x03070105u : 0x06020400u;
-    const uint32_t sel2 = (lane & 2) ? 0x03020706u : 0x05040100u;
-
-    // a token's page, and its place there; page 0 where it has none
-    struct Place {
-        uint32_t page, in_page;
-        bool there;
-    };
-    const auto look_up = [&](uint32_t base) -> Place {
-        const uint32_t tok = base + lane;
-        Place p{0, 0, false};
-        if (tok < to) {
-            const uint32_t col = fast_div(tok, a.page_div);
-            p.page = (uint32_t)table[col];
-            p.in_page = tok - col * a.page_div.d;
-            p.there = true;
-        }
-        return p;
-    };
-    const auto settle = [&](Place& p) {            // (apart from the look-up, so as not to wait for it there)
-        p.there = p.there && p.page < a.page_limit;
-        p.page = p.there ? p.page : 0;
-        p.in_page = p.there ? p.in_page : 0;
-    };
-
+    int32_t last[NT];                              // the last token that a row sees
     f32x4 acc[NT][VT];
-    float m[NT], less[NT], l[NT], top[NT][NGV];  // less: m, or 0 where there is none yet
+    float m[NT], less[NT], l[NT], top[NT][NGV];    // less: m, or 0 where there is none yet
     int32_t e[NT][NGV];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        m[t] = kAttnNone;
-        less[t] = l[t] = 0.0f;
-#pragma unroll
-        for (int g = 0; g < NGV; ++g) {
-            top[t][g] = 0.0f;
-            e[t][g] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < VT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
-    }
 
-    uint32_t kw[4][KW], vw[16][VR];
-    float ks[NGK], vs[NGV];
-    bool there = false;
-    // Where 16 consecutive tokens stand in one page (P16) their rows start at one
-    // scalar address, and a lane's words at offsets from it that do not change;
-    // else each row's address comes from the lane that has its token.
-    const uint32_t k_step = n16 * (uint32_t)a.kc.st[1], v_step = 4 * kq * (uint32_t)a.vc.st[1];
-    const auto group_at = [&](const Place& p, int i, const gchar* base, const CacheRef& c) -> const gchar* {
-        const uint32_t page = __builtin_amdgcn_readlane((int)p.page, 16 * i);
-        const uint32_t in_page = __builtin_amdgcn_readlane((int)p.in_page, 16 * i);
-        return base + (int64_t)page * c.st[0] + (int64_t)in_page * c.st[1];
-    };
-    // (an offset that the compiler cannot widen outside of the loop: a load then
-    // takes it as it is, beside the scalar address)
-    const auto offset = [](uint32_t v) {
-        asm volatile("" : "+v"(v));
-        return v;
-    };
-    // the scales and K's codes of a tile whose pages are known
-    const auto fetch_k = [&](Place& p) {
-        settle(p);
-        there = p.there;
-        const int64_t page = p.page, in_page = p.in_page;
-        const gchar* sk = ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1]) * 4;
-        const gchar* sv = vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1]) * 4;
+    // Rows r0 to live - 1 (or fewer) of a cached head: a column a row, 8 elements
+    // a step in k_numbers' order.
+    __device__ __forceinline__ void load(const AttnArgs& a, const AttnSeq& seq, uint32_t b, uint32_t head, uint32_t r0, uint32_t live,
+                                         uint32_t n16, uint32_t kq)
+    {
 #pragma unroll
-        for (int g = 0; g < NGK; ++g) {
-            const uint32_t at_g = KF ? min((uint32_t)g * 32 / a.k_group, a.k_groups - 1) : 0;
-            ks[g] = there ? gload<float>(sk + at_g * 4) : 0.0f;
-        }
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t r = min(r0 + t * 16 + n16, live - 1);
+            const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
+            last[t] = a.causal ? (int32_t)(seq.first + s) : INT32_MAX;
+            const gchar* row = as_global(a.q.data) + (b * a.q.sb + s * a.q.ss + h * a.q.sn) * 2;
+            float sum = 0.0f;
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) {
-            const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
-            vs[g] = there ? gload<float>(sv + at_g * 4) : 0.0f;
-        }
-        if constexpr (!P16) {
-            my.k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
-            my.v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
-            wave_sync();
-        }
-        uint32_t k_off[KF ? KW : 1];
+            for (int st = 0; st < KW; ++st) {
+                const uint32_t d = KF ? 32 * st + 8 * kq : kq * (DP / 4) + 8 * st;
+                v4u v{0, 0, 0, 0};
+                if (d < a.D) v = gload<v4u>(row + d * 2);
+                Lanes<DT> f;
+                f.unpack(v);
 #pragma unroll
-        for (int st = 0; st < (KF ? KW : 1); ++st) {
-            const uint32_t off = KF ? 16 * st + 4 * kq : 4 * KW * kq;
-            k_off[st] = offset((P16 ? k_step : 0) + (off < k_bytes ? off : 0));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const gchar* row = P16 ? group_at(p, i, k_base, a.kc) : k_base + my.k_at[16 * i + n16];
-            if constexpr (KF) {
-#pragma unroll
-                for (int st = 0; st < KW; ++st) kw[i][st] = gload<uint32_t>(row + k_off[st]);
-            } else if constexpr (KW == 2) {
-                const v2u w = gload<v2u>(row + k_off[0]);
-                kw[i][0] = w[0];
-                kw[i][1] = w[1];
-            } else {
-#pragma unroll
-                for (int c = 0; c < KW / 4; ++c) {
-                    const v4u w = gload<v4u>(row + k_off[0] + 16 * c);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) kw[i][4 * c + j] = w[j];
+                for (int k = 0; k < 8; ++k) sum += f.v[k];
+                q[t][st] = q_order(v);
+                if (KF || st == KW - 1) {
+                    const float c = -24.0f * column_sum(sum);
+                    start[t][KF ? st : 0] = f32x4{c, c, c, c};
+                    sum = 0.0f;
                 }
             }
-        }
-    };
-    const auto fetch_v = [&](const Place& p) {
-        const gchar* group[4];
-        if constexpr (P16) {
+            m[t] = kAttnNone;
+            less[t] = l[t] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) group[i] = group_at(p, i, v_base, a.vc);
-        }
-        // a register of a lane's V: 4 bytes (2 of 64 lanes) in a place that ends
-        // with the row, or lane 0's
-        constexpr int W = DVP == 64 ? 2 : 4;
-        uint32_t v_off[P16 ? 4 : 1][VR];
-#pragma unroll
-        for (int c = 0; c < VR; ++c) {
-            const uint32_t off = VF ? (DVP == 64 ? 16 * a2 + 2 * q2 : 64 * c + 16 * a4 + 4 * q4) : W * VR * n16 + 4 * c;
-#pragma unroll
-            for (int r = 0; r < (P16 ? 4 : 1); ++r)
-                v_off[r][c] = offset((P16 ? v_step + r * (uint32_t)a.vc.st[1] : 0) + (off < v_bytes ? off : 0));
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const gchar* row = P16 ? group[i >> 2] : v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
-#pragma unroll
-            for (int c = 0; c < VR; ++c) {
-                const gchar* at = row + v_off[P16 ? i & 3 : 0][c];
-                if constexpr (W == 2) vw[i][c] = gload<uint16_t>(at);
-                else vw[i][c] = gload<uint32_t>(at);
+            for (int g = 0; g < NGV; ++g) {
+                top[t][g] = 0.0f;
+                e[t][g] = 0;
             }
+#pragma unroll
+            for (int i = 0; i < VT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
         }
-    };
-
-    const Numbers k_const = k_constants<DT>();
-    const VConstants v_const = v_constants();
-    const uint32_t step = 64 * waves;
-    uint32_t base = from + 64 * token_wave;
-    Place next = look_up(base);
-    if (base < to) {
-        fetch_k(next);
-        fetch_v(next);
     }
-    next = look_up(base + step < base ? to : base + step);
-    for (; base < to; base += step) {
-        // the tile's scales, by token, and its codes
-        const uint64_t valid = __ballot(there);
-#pragma unroll
-        for (int g = 0; g < NGK; ++g) my.ks[g][lane] = ks[g] * a.scale2;
-#pragma unroll
-        for (int g = 0; g < NGV; ++g) my.vs[g][lane] = vs[g];
-        wave_sync();
 
-        // x^T = K Q^T, a token a row of the product, less the row's m
-        f32x4 x[NT][4], k_scale[4];
+    // x^T = K Q^T, a token a row of the product, less the row's m. k_numbers_of(i,
+    // st): step st of the tile's tokens 16 i to 16 i + 15; ks: K's scales by
+    // token, of each step or one.
+    template <class F>
+    __device__ __forceinline__ void scores(f32x4 (&x)[NT][4], const F& k_numbers_of, const float (*ks)[64], uint32_t kq)
+    {
+        f32x4 scale[4];
         if constexpr (!KF) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) k_scale[i] = *reinterpret_cast<const f32x4*>(&my.ks[0][16 * i + 4 * kq]);
+            for (int i = 0; i < 4; ++i) scale[i] = *reinterpret_cast<const f32x4*>(&ks[0][16 * i + 4 * kq]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int st = 0; st < KW; ++st) {
-                const v4u k = k_numbers<DT>(kw[i][st], k_const);
+                const v4u k = k_numbers_of(i, st);
                 if constexpr (KF) {
-                    const f32x4 s = *reinterpret_cast<const f32x4*>(&my.ks[st][16 * i + 4 * kq]);
+                    const f32x4 s = *reinterpret_cast<const f32x4*>(&ks[st][16 * i + 4 * kq]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const f32x4 d = attn_mfma<DT>(k, q[t][st], start[t][st]);
@@ -438,44 +267,42 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                     for (int t = 0; t < NT; ++t) x[t][i] = attn_mfma<DT>(k, q[t][st], st == 0 ? start[t][0] : x[t][i]);
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);     // (else conversions of all tiles pile up in registers)
+            __builtin_amdgcn_sched_barrier(0);     // (else the numbers of all tokens pile up in registers)
         }
         if constexpr (!KF) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(x[t][i][r], k_scale[i][r], -less[t]);
+                    for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(x[t][i][r], scale[i][r], -less[t]);
+        }
+    }
+
+    // Tokens of the tile at `base` that are not there (valid: a bit each) or come
+    // after a row's own.
+    __device__ __forceinline__ void hide(f32x4 (&x)[NT][4], uint32_t base, uint64_t valid, uint32_t kq)
+    {
+        // most tiles have nothing to hide: this keeps the comparisons in the
+        // caller's branch
+        int32_t tile = __builtin_amdgcn_readfirstlane((int)base);
+        asm volatile("" : "+s"(tile));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t bits = (uint32_t)(valid >> (16 * i + 4 * kq));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int32_t tok = tile + (int32_t)(16 * i + 4 * kq + r);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) x[t][i][r] = ((bits >> r) & 1u) && tok <= last[t] ? x[t][i][r] : kAttnNone;
             }
         }
-        if (base + 64 > all || valid != ~0ull) {
-            // most tiles have nothing to hide: this keeps the comparisons in the
-            // branch
-            int32_t tile = (int32_t)base;
-            asm volatile("" : "+s"(tile));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t bits = (uint32_t)(valid >> (16 * i + 4 * kq));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int32_t tok = tile + (int32_t)(16 * i + 4 * kq + r);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) x[t][i][r] = ((bits >> r) & 1u) && tok <= last[t] ? x[t][i][r] : kAttnNone;
-                }
-            }
-        }
+    }
 
-        // The next tile's scales and K; its V when this one's is used up. (Behind
-        // the last tile nothing new: a branch around the loads would cost a copy
-        // of their registers in every tile.)
-        fetch_k(next);
-        Place after = look_up(to - base > 2 * step ? base + 2 * step : to);
-        __builtin_amdgcn_sched_barrier(0);
-
-        // the weights exp(x - m)
-        float keep[NT];
-        bool moved[NT];
+    // The weights exp(x - m), in x's place; keep: what the sums before are worth
+    // now, where moved.
+    __device__ __forceinline__ void weigh(f32x4 (&x)[NT][4], float (&keep)[NT], bool (&moved)[NT])
+    {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float most = x[t][0][0];
@@ -510,6 +337,320 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             l[t] += sum;
         }
         __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // By segments: the weights times V's scales, in fp16, and o^T += V^T P^T, 32
+    // tokens a product. v_numbers_of(h, i): product i's V of half h of the tokens;
+    // vs: V's scales by token, of each segment or one.
+    template <class F>
+    __device__ __forceinline__ void add(const f32x4 (&x)[NT][4], const float (&keep)[NT], const bool (&moved)[NT], const F& v_numbers_of,
+                                        const float (*vs)[64], uint32_t kq)
+    {
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) {
+            constexpr int T = VT / NGV;            // products of a segment
+            v4u p[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f32x4 w[4];
+                float high = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) high = fmaxf(high, fabsf(w[i][r]));
+                }
+                if (moved[t]) top[t][g] *= keep[t];
+                top[t][g] = fmaxf(top[t][g], column_max(high));
+                if (moved[t] || __any(__builtin_ldexpf(top[t][g], -e[t][g]) > 256.0f)) {
+                    int32_t now = __builtin_amdgcn_frexp_expf(top[t][g]);
+                    now = top[t][g] > 0.0f ? min(max(now, -120), 120) : e[t][g];
+                    const float f = __builtin_ldexpf(keep[t], e[t][g] - now);
+                    e[t][g] = now;
+#pragma unroll
+                    for (int i = 0; i < T; ++i) acc[t][g * T + i] *= f;
+                }
+                const float c = __builtin_ldexpf(1.0f, -e[t][g]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4& v = w[2 * h + (j >> 1)];
+                        const f32x2 pair{v[2 * (j & 1)] * c, v[2 * (j & 1) + 1] * c};
+                        p[t][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = g * T; i < (g + 1) * T; ++i) {
+                    const v4u v = v_numbers_of(h, i);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][h], acc[t][i]);
+                    if (i & 1) __builtin_amdgcn_sched_barrier(0);
+                }
+        }
+    }
+
+    // Lane j of v that product i's row 4 kq + r holds.
+    __device__ __forceinline__ static uint32_t lane_of(int i, int r, uint32_t kq)
+    {
+        return VF ? 32 * (i >> 1) + 8 * kq + 2 * r + (i & 1) : VT * (4 * kq + r) + i;
+    }
+
+    // The rows' results, or (splits) their part of them.
+    __device__ __forceinline__ void store(const AttnArgs& a, const AttnAt& at, uint32_t head, uint32_t r0, uint32_t live, uint32_t n16,
+                                          uint32_t kq)
+    {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t r = r0 + t * 16 + n16;
+            const float sum = column_sum(l[t]);
+            if (r >= live) continue;
+            const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
+            const float inv = a.splits > 1 ? 1.0f : one_over(sum);
+            const uint64_t row = part_row(a, at.split, at.b, s, h);
+            gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
+#pragma unroll
+            for (int c = 0; c < VT / 2; ++c) {     // 8 consecutive lanes
+                const float f = __builtin_ldexpf(inv, e[t][VF ? c : 0]);
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = f * (VF ? acc[t][2 * c + (k & 1)][k >> 1] : acc[t][(8 * c + k) % VT][(8 * c + k) / VT]);
+                const uint32_t j = VF ? 32 * c + 8 * kq : 4 * VT * kq + 8 * c;
+                if (j >= a.Dv) continue;
+                if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
+                else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
+            }
+            if (a.splits > 1 && kq == 0) part_stats(a)[row] = make_float2(m[t], sum);
+        }
+    }
+};
+
+// Where a tile's tokens are: a lane a token.
+struct AttnPlace {
+    uint32_t page, in_page;                        // page 0 where there is none
+    bool there;
+};
+
+__device__ __forceinline__ AttnPlace attn_look_up(const AttnArgs& a, const int32_t* table, uint32_t tok, uint32_t to)
+{
+    AttnPlace p{0, 0, false};
+    if (tok < to) {
+        const uint32_t col = fast_div(tok, a.page_div);
+        p.page = (uint32_t)table[col];
+        p.in_page = tok - col * a.page_div.d;
+        p.there = true;
+    }
+    return p;
+}
+
+// (apart from the look-up, so as not to wait for it there)
+__device__ __forceinline__ void attn_settle(const AttnArgs& a, AttnPlace& p)
+{
+    p.there = p.there && p.page < a.page_limit;
+    p.page = p.there ? p.page : 0;
+    p.in_page = p.there ? p.in_page : 0;
+}
+
+// The first row of 16 tokens that stand in one page, as a scalar address.
+__device__ __forceinline__ const gchar* attn_group_at(const AttnPlace& p, int i, const gchar* base, const CacheRef& c)
+{
+    const uint32_t page = __builtin_amdgcn_readlane((int)p.page, 16 * i);
+    const uint32_t in_page = __builtin_amdgcn_readlane((int)p.in_page, 16 * i);
+    return base + (int64_t)page * c.st[0] + (int64_t)in_page * c.st[1];
+}
+
+// An offset that the compiler cannot widen outside of a loop: a load then takes
+// it as it is, beside its scalar address.
+__device__ __forceinline__ uint32_t attn_offset(uint32_t v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Where a register of a lane's V starts in its row: 4 bytes (2 of rows of up to
+// 64 lanes) that end with the row, or the first ones.
+template <int DVP, bool VF>
+__device__ __forceinline__ uint32_t attn_v_byte(uint32_t n16, int c, uint32_t v_bytes)
+{
+    const uint32_t off = VF ? (DVP == 64 ? 16 * (n16 & 1) + 2 * (n16 >> 1) : 64 * c + 16 * (n16 & 3) + 4 * (n16 >> 2))
+                            : DVP == 64 ? 2 * n16 : DVP / 32 * n16 + 4 * c;
+    return off < v_bytes ? off : 0;
+}
+
+// The tokens that the rows r0 to r1 - 1 see, and those that all of them see.
+struct AttnSpan {
+    uint32_t some, all;
+};
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnSeq& seq, uint32_t r0, uint32_t r1)
+{
+    AttnSpan s{(uint32_t)seq.tokens, (uint32_t)seq.tokens};
+    if (a.causal) {
+        s.some = (uint32_t)max((int64_t)0, min((int64_t)s.some, seq.first + fast_div(r1 - 1, a.rep_div) + 1));
+        s.all = (uint32_t)max((int64_t)0, min((int64_t)s.all, seq.first + fast_div(r0, a.rep_div) + 1));
+    }
+    return s;
+}
+
+// Waves that a SIMD is to hold: what their registers allow.
+constexpr int attn_waves(int lanes, bool kf, int tiles)
+{
+    return lanes == 256 ? 1 : (lanes == 64 || !kf ? 4 : 3) - tiles;
+}
+
+template <int DT, int DP, int DVP, bool KF, bool VF, bool P16, int NT>
+__global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_kernel(AttnVecArgs a)
+{
+    using Lds = AttnLds<DP, DVP, KF, VF, NT>;
+    using R = AttnRows<DT, DP, DVP, KF, VF, NT>;
+    constexpr int KW = R::KW;                      // words of a K row that a lane takes
+    constexpr int VT = R::VT;
+    constexpr int VR = DVP >= 128 ? DVP / 128 : 1; // registers of a token's V
+    constexpr int VH = DVP / 64;                   // 16-bit halves of them
+    constexpr int NGK = Lds::NGK, NGV = Lds::NGV;
+    __shared__ Lds lds;
+    const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typename Lds::Wave& my = lds.wave[wave];
+
+    const AttnAt at = attn_at(a, blockIdx.x);
+    const AttnSeq seq = attn_seq(a, at.b);
+    const uint32_t head_wave = wave & (a.head_waves - 1), token_wave = a.row_waves > 1 ? 0 : wave / a.head_waves;
+    const uint32_t head = at.head * a.head_waves + head_wave, waves = a.token_waves;
+    const uint32_t r0 = (at.tile * a.row_waves + (a.row_waves > 1 ? wave : 0)) * 16 * NT;
+    const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
+    if (r0 >= live) return;                        // where waves are joined the same for the whole block
+    const AttnSpan span = attn_span(a, seq, r0, min(r0 + 16 * NT, live));
+    uint32_t from, to;
+    attn_part(span.some, at.split, a.splits, 64 * waves, &from, &to);
+    const uint32_t all = min(span.all, to);
+    R rows;
+    rows.load(a, seq, at.b, head, r0, live, n16, kq);
+
+    // where this lane's words of a row start
+    const gchar* const k_base = as_global(a.kc.data) + head * a.kc.st[2];
+    const gchar* const v_base = as_global(a.vc.data) + head * a.vc.st[2];
+    const gchar* const ks_base = as_global(a.kc.scales) + head * a.kc.sc[2] * 4;
+    const gchar* const vs_base = as_global(a.vc.scales) + head * a.vc.sc[2] * 4;
+    const int32_t* const table = a.table + at.b * a.table_stride;
+    const uint32_t k_bytes = a.D / 2, v_bytes = a.Dv / 2;
+    const uint32_t sel1 = (lane & 1) ? 0x03070105u : 0x06020400u;
+    const uint32_t sel2 = (lane & 2) ? 0x03020706u : 0x05040100u;
+
+    uint32_t kw[4][KW], vw[16][VR];
+    float ks[NGK], vs[NGV];
+    bool there = false;
+    // Where 16 consecutive tokens stand in one page (P16) their rows start at one
+    // scalar address, and a lane's words at offsets from it that do not change;
+    // else each row's address comes from the lane that has its token.
+    const uint32_t k_step = n16 * (uint32_t)a.kc.st[1], v_step = 4 * kq * (uint32_t)a.vc.st[1];
+    // the scales and K's codes of a tile whose pages are known
+    const auto fetch_k = [&](AttnPlace& p) {
+        attn_settle(a, p);
+        there = p.there;
+        const int64_t page = p.page, in_page = p.in_page;
+        const gchar* sk = ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1]) * 4;
+        const gchar* sv = vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1]) * 4;
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) {
+            const uint32_t at_g = KF ? min((uint32_t)g * 32 / a.k_group, a.k_groups - 1) : 0;
+            ks[g] = there ? gload<float>(sk + at_g * 4) : 0.0f;
+        }
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) {
+            const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
+            vs[g] = there ? gload<float>(sv + at_g * 4) : 0.0f;
+        }
+        if constexpr (!P16) {
+            my.k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
+            my.v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
+            wave_sync();
+        }
+        uint32_t k_off[KF ? KW : 1];
+#pragma unroll
+        for (int st = 0; st < (KF ? KW : 1); ++st) {
+            const uint32_t off = KF ? 16 * st + 4 * kq : 4 * KW * kq;
+            k_off[st] = attn_offset((P16 ? k_step : 0) + (off < k_bytes ? off : 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const gchar* row = P16 ? attn_group_at(p, i, k_base, a.kc) : k_base + my.k_at[16 * i + n16];
+            if constexpr (KF) {
+#pragma unroll
+                for (int st = 0; st < KW; ++st) kw[i][st] = gload<uint32_t>(row + k_off[st]);
+            } else if constexpr (KW == 2) {
+                const v2u w = gload<v2u>(row + k_off[0]);
+                kw[i][0] = w[0];
+                kw[i][1] = w[1];
+            } else {
+#pragma unroll
+                for (int c = 0; c < KW / 4; ++c) {
+                    const v4u w = gload<v4u>(row + k_off[0] + 16 * c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) kw[i][4 * c + j] = w[j];
+                }
+            }
+        }
+    };
+    const auto fetch_v = [&](const AttnPlace& p) {
+        const gchar* group[4];
+        if constexpr (P16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) group[i] = attn_group_at(p, i, v_base, a.vc);
+        }
+        uint32_t v_off[P16 ? 4 : 1][VR];
+#pragma unroll
+        for (int c = 0; c < VR; ++c)
+#pragma unroll
+            for (int r = 0; r < (P16 ? 4 : 1); ++r)
+                v_off[r][c] = attn_offset((P16 ? v_step + r * (uint32_t)a.vc.st[1] : 0) + attn_v_byte<DVP, VF>(n16, c, v_bytes));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const gchar* row = P16 ? group[i >> 2] : v_base + my.v_at[16 * (i >> 2) + 4 * kq + (i & 3)];
+#pragma unroll
+            for (int c = 0; c < VR; ++c) {
+                const gchar* at = row + v_off[P16 ? i & 3 : 0][c];
+                if constexpr (DVP == 64) vw[i][c] = gload<uint16_t>(at);
+                else vw[i][c] = gload<uint32_t>(at);
+            }
+        }
+    };
+
+    const Numbers k_const = k_constants<DT>();
+    const VConstants v_const = v_constants();
+    const uint32_t step = 64 * waves;
+    uint32_t base = from + 64 * token_wave;
+    AttnPlace next = attn_look_up(a, table, base + lane, to);
+    if (base < to) {
+        fetch_k(next);
+        fetch_v(next);
+    }
+    next = attn_look_up(a, table, (base + step < base ? to : base + step) + lane, to);
+    for (; base < to; base += step) {
+        // the tile's scales, by token, and its codes
+        const uint64_t valid = __ballot(there);
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) my.ks[g][lane] = ks[g] * a.scale2;
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) my.vs[g][lane] = vs[g];
+        wave_sync();
+
+        f32x4 x[NT][4];
+        rows.scores(x, [&](int i, int st) { return k_numbers<DT>(kw[i][st], k_const); }, my.ks, kq);
+        if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
+
+        // The next tile's scales and K; its V when this one's is used up. (Behind
+        // the last tile nothing new: a branch around the loads would cost a copy
+        // of their registers in every tile.)
+        fetch_k(next);
+        const AttnPlace after = attn_look_up(a, table, (to - base > 2 * step ? base + 2 * step : to) + lane, to);
+        __builtin_amdgcn_sched_barrier(0);
+
+        float keep[NT];
+        bool moved[NT];
+        rows.weigh(x, keep, moved);
 
         // V's words, the codes of two tokens at equal nibbles of their halves
         uint32_t two[2][VH][4];
@@ -539,119 +680,41 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                 }
             }
 
-        // by segments: the weights times V's scales, in fp16, and o^T += V^T P^T,
-        // 32 tokens a product
+        rows.add(x, keep, moved, [&](int h, int i) {
+            v4u v;
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) {
-            constexpr int T = VT / NGV;            // products of a segment
-            v4u p[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4 w[4];
-                float high = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[i] = x[t][i] * *reinterpret_cast<const f32x4*>(&my.vs[g][16 * i + 4 * kq]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) high = fmaxf(high, fabsf(w[i][r]));
-                }
-                if (moved[t]) top[t][g] *= keep[t];
-                top[t][g] = fmaxf(top[t][g], column_max(high));
-                if (moved[t] || __any(__builtin_ldexpf(top[t][g], -e[t][g]) > 256.0f)) {
-                    int32_t now = __builtin_amdgcn_frexp_expf(top[t][g]);
-                    now = top[t][g] > 0.0f ? min(max(now, -120), 120) : e[t][g];
-                    const float f = __builtin_ldexpf(keep[t], e[t][g] - now);
-                    e[t][g] = now;
-#pragma unroll
-                    for (int i = 0; i < T; ++i) acc[t][g * T + i] *= f;
-                }
-                const float c = __builtin_ldexpf(1.0f, -e[t][g]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f32x4& v = w[2 * h + (j >> 1)];
-                        const f32x2 pair{v[2 * (j & 1)] * c, v[2 * (j & 1) + 1] * c};
-                        p[t][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
-                    }
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = two[h][i >> 2][j];
+                v[j] = (i & 3) == 0 ? v_numbers<0>(w, v_const) : (i & 3) == 1 ? v_numbers<1>(w, v_const) :
+                       (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = g * T; i < (g + 1) * T; ++i) {
-                    v4u v;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w = two[h][i >> 2][j];
-                        v[j] = (i & 3) == 0 ? v_numbers<0>(w, v_const) : (i & 3) == 1 ? v_numbers<1>(w, v_const) :
-                               (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][h], acc[t][i]);
-                    if (i & 1) __builtin_amdgcn_sched_barrier(0);
-                }
-        }
+            return v;
+        }, my.vs, kq);
         fetch_v(next);
         next = after;
     }
 
-    // lane j of v that product i's row 4 kq + r holds
-    const auto lane_of = [&](int i, int r) -> uint32_t {
-        return VF ? 32 * (i >> 1) + 8 * kq + 2 * r + (i & 1) : VT * (4 * kq + r) + i;
-    };
-    // ... and 8 consecutive ones: number c of a lane's VT / 2
-    const auto eight_at = [&](int c) -> uint32_t { return VF ? 32 * c + 8 * kq : 4 * VT * kq + 8 * c; };
-    const auto eight = [&](const f32x4 (&o)[VT], int c, float (&v)[8], const float (&f)[NGV]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if constexpr (VF) v[k] = o[2 * c + (k & 1)][k >> 1] * f[c];
-            else v[k] = o[(8 * c + k) % VT][(8 * c + k) / VT] * f[0];
-        }
-    };
-
     if (waves == 1) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const uint32_t r = r0 + t * 16 + n16;
-            const float sum = column_sum(l[t]);
-            if (r >= live) continue;
-            const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
-            const float inv = a.splits > 1 ? 1.0f : one_over(sum);
-            float f[NGV];
-#pragma unroll
-            for (int g = 0; g < NGV; ++g) f[g] = __builtin_ldexpf(inv, e[t][g]);
-            const uint64_t row = part_row(a, at.split, at.b, s, h);
-            gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
-#pragma unroll
-            for (int c = 0; c < VT / 2; ++c) {
-                float v[8];
-                eight(acc[t], c, v, f);
-                const uint32_t j = eight_at(c);
-                if (j >= a.Dv) continue;
-                if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
-                else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
-            }
-            if (a.splits > 1 && kq == 0) part_stats(a)[row] = make_float2(m[t], sum);
-        }
+        rows.store(a, at, head, r0, live, n16, kq);
         return;
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const float sum = column_sum(l[t]);
+        const float sum = column_sum(rows.l[t]);
         __syncthreads();                           // the tiles (or the rows before) are done with this memory
         if (kq == 0) {
-            lds.join.m[wave][n16] = m[t];
+            lds.join.m[wave][n16] = rows.m[t];
             lds.join.l[wave][n16] = sum;
         }
         __syncthreads();
         float most = kAttnNone;
         for (uint32_t w = head_wave; w < 4; w += a.head_waves) most = fmaxf(most, lds.join.m[w][n16]);
-        const float keep = part_weight(m[t], most);
+        const float keep = part_weight(rows.m[t], most);
 #pragma unroll
         for (int i = 0; i < VT; ++i) {
-            const float f = __builtin_ldexpf(keep, e[t][VF ? i / 2 : 0]);
+            const float f = __builtin_ldexpf(keep, rows.e[t][VF ? i / 2 : 0]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) lds.join.o[wave][n16][lane_of(i, r)] = acc[t][i][r] * f;
+            for (int r = 0; r < 4; ++r) lds.join.o[wave][n16][R::lane_of(i, r, kq)] = rows.acc[t][i][r] * f;
         }
         __syncthreads();
         // 16 threads a row, 8 lanes at a time
@@ -662,7 +725,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             for (uint32_t w = hw; w < 4; w += a.head_waves) high = fmaxf(high, lds.join.m[w][row16]);
             for (uint32_t w = hw; w < 4; w += a.head_waves) {
                 const float mw = lds.join.m[w][row16];
-                whole += lds.join.l[w][row16] * (part_weight(mw, high));
+                whole += lds.join.l[w][row16] * part_weight(mw, high);
             }
             const uint32_t h = (at.head * a.head_waves + hw) * a.rep + (r - s * a.rep);
             const float inv = a.splits > 1 ? 1.0f : one_over(whole);
@@ -681,6 +744,195 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             if (a.splits > 1 && r < live && (threadIdx.x & 15) == 0) part_stats(a)[row] = make_float2(high, whole);
         }
     }
+}
+
+
+// ---------------------------------------------------------------------------
+// Many rows (a prompt's): the four waves of a block have 32 rows each of one
+// cached head and go through the same tiles, so each makes numbers of a quarter
+// of a tile, for all, in LDS: in the order in which the products take them, 16
+// bytes a lane, so that no read or write meets another's bank. Numbers cost a
+// wave 75 operations a tile then, not 300, of 700. Two buffers: while a tile is
+// used the next one's numbers are made, its words having been loaded the tile
+// before; one barrier a tile.
+// ---------------------------------------------------------------------------
+constexpr int kSharedTiles = 2;                    // of 16 rows a wave
+
+template <int DP, bool KF, bool VF, bool P16>
+struct alignas(16) AttnSharedLds {
+    static constexpr int NGK = KF ? DP / 32 : 1, NGV = VF ? DP / 32 : 1;
+    struct Buffer {
+        v4u k[4][DP / 32][64];
+        v4u v[2][DP / 16][64];
+        float ks[NGK][64], vs[NGV][64];
+    };
+    Buffer tile[2];
+    struct Where {
+        int64_t k_at[64], v_at[64];
+    };
+    Where where[P16 ? 1 : 4];
+};
+
+template <int DT, int DP, bool KF, bool VF, bool P16>
+__global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
+{
+    constexpr int NT = kSharedTiles;
+    using Lds = AttnSharedLds<DP, KF, VF, P16>;
+    using R = AttnRows<DT, DP, DP, KF, VF, NT>;
+    constexpr int KW = R::KW, VT = R::VT, NGK = Lds::NGK, NGV = Lds::NGV;
+    static_assert(DP == 64 || DP == 128, "a register a token's V");
+    __shared__ Lds lds;
+    const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    AttnAt at = attn_at(a, blockIdx.x);
+    at.tile = a.tiles - 1 - at.tile;               // those that see the most tokens first
+    const AttnSeq seq = attn_seq(a, at.b);
+    const uint32_t block_row = at.tile * (64 * NT), r0 = block_row + wave * (16 * NT);
+    const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
+    if (block_row >= live) return;                 // the same for the whole block
+    uint32_t from, to;
+    attn_part(attn_span(a, seq, block_row, min(block_row + 64 * NT, live)).some, at.split, a.splits, 64, &from, &to);
+    // (a wave without rows makes numbers only)
+    const AttnSpan span = r0 < live ? attn_span(a, seq, r0, min(r0 + 16 * NT, live)) : AttnSpan{0, 0};
+    const uint32_t all = min(span.all, to), some = min(span.some, to);
+    R rows;
+    rows.load(a, seq, at.b, at.head, min(r0, live - 1), live, n16, kq);
+
+    const gchar* const k_base = as_global(a.kc.data) + at.head * a.kc.st[2];
+    const gchar* const v_base = as_global(a.vc.data) + at.head * a.vc.st[2];
+    const gchar* const ks_base = as_global(a.kc.scales) + at.head * a.kc.sc[2] * 4;
+    const gchar* const vs_base = as_global(a.vc.scales) + at.head * a.vc.sc[2] * 4;
+    const int32_t* const table = a.table + at.b * a.table_stride;
+    const uint32_t k_bytes = a.D / 2, v_bytes = a.Dv / 2;
+    const uint32_t sel1 = (lane & 1) ? 0x03070105u : 0x06020400u;
+    const uint32_t sel2 = (lane & 2) ? 0x03020706u : 0x05040100u;
+    const uint32_t k_step = n16 * (uint32_t)a.kc.st[1], v_step = 4 * kq * (uint32_t)a.vc.st[1];
+    // this wave's quarter: K of tokens 16 wave on; V of half `half` of the
+    // tokens, products `part` * VT / 2 on; the scales of group `wave`, where there
+    // are so many
+    const uint32_t half = wave >> 1, part = wave & 1;
+    const uint32_t v_sel = part ? 0x07060302u : 0x05040100u;
+    const Numbers k_const = k_constants<DT>();
+    const VConstants v_const = v_constants();
+
+    uint32_t kw[KW], vw[8];
+    float ks = 0.0f, vs = 0.0f;
+    bool there = false;
+    const auto fetch = [&](AttnPlace& p) {
+        attn_settle(a, p);
+        there = p.there;
+        const int64_t page = p.page, in_page = p.in_page;
+        if (wave < NGK) {
+            const uint32_t g = KF ? min(wave * 32 / a.k_group, a.k_groups - 1) : 0;
+            ks = there ? gload<float>(ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1] + g) * 4) : 0.0f;
+        }
+        if (wave < NGV) {
+            const uint32_t g = VF ? min(wave * 32 / a.v_group, a.v_groups - 1) : 0;
+            vs = there ? gload<float>(vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1] + g) * 4) : 0.0f;
+        }
+        if constexpr (!P16) {
+            lds.where[wave].k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
+            lds.where[wave].v_at[lane] = page * a.vc.st[0] + in_page * a.vc.st[1];
+            wave_sync();
+        }
+        const gchar* row = P16 ? attn_group_at(p, wave, k_base, a.kc) : k_base + lds.where[wave].k_at[16 * wave + n16];
+        if constexpr (KF) {
+#pragma unroll
+            for (int st = 0; st < KW; ++st) {
+                const uint32_t off = 16 * st + 4 * kq;
+                kw[st] = gload<uint32_t>(row + attn_offset((P16 ? k_step : 0) + (off < k_bytes ? off : 0)));
+            }
+        } else if constexpr (KW == 2) {
+            const v2u w = gload<v2u>(row + attn_offset((P16 ? k_step : 0) + 8 * kq));
+            kw[0] = w[0];
+            kw[1] = w[1];
+        } else {
+            const v4u w = gload<v4u>(row + attn_offset((P16 ? k_step : 0) + 16 * kq));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kw[j] = w[j];
+        }
+        const uint32_t byte = attn_v_byte<DP, VF>(n16, 0, v_bytes);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const gchar* r = P16 ? attn_group_at(p, 2 * half + (i >> 2), v_base, a.vc)
+                                 : v_base + lds.where[wave].v_at[32 * half + 16 * (i >> 2) + 4 * kq + (i & 3)];
+            const uint32_t off = attn_offset((P16 ? v_step + (i & 3) * (uint32_t)a.vc.st[1] : 0) + byte);
+            if constexpr (DP == 64) vw[i] = gload<uint16_t>(r + off);
+            else vw[i] = gload<uint32_t>(r + off);
+        }
+    };
+    // the words' numbers, and the scales, to a buffer
+    const auto put = [&](typename Lds::Buffer& to_tile) {
+#pragma unroll
+        for (int st = 0; st < KW; ++st) to_tile.k[wave][st][lane] = k_numbers<DT>(kw[st], k_const);
+        uint32_t two[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w0 = vw[4 * (j >> 1) + 2 * (j & 1)], w1 = vw[4 * (j >> 1) + 2 * (j & 1) + 1];
+            if constexpr (DP == 64) {
+                uint32_t w = w0 | (w1 << 16);
+                if constexpr (VF) {
+                    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
+                    w = __builtin_amdgcn_perm(o, w, sel1);
+                }
+                two[j] = w >> (8 * part);
+            } else {
+                if constexpr (VF) {
+                    w0 = quad_bytes(w0, sel1, sel2);
+                    w1 = quad_bytes(w1, sel1, sel2);
+                }
+                two[j] = __builtin_amdgcn_perm(w1, w0, v_sel);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VT / 2; ++i) {
+            v4u v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = i == 0 ? v_numbers<0>(two[j], v_const) : i == 1 ? v_numbers<1>(two[j], v_const) :
+                       i == 2 ? v_numbers<2>(two[j], v_const) : v_numbers<3>(two[j], v_const);
+            to_tile.v[half][part * (VT / 2) + i][lane] = v;
+        }
+        if (wave < NGK) to_tile.ks[wave][lane] = ks * a.scale2;
+        if (wave < NGV) to_tile.vs[wave][lane] = vs;
+    };
+
+    AttnPlace next = attn_look_up(a, table, from + lane, to);
+    uint64_t valid = 0;
+    if (from < to) {
+        fetch(next);
+        valid = __ballot(there);
+        put(lds.tile[0]);
+        next = attn_look_up(a, table, from + 64 + lane, to);
+        fetch(next);
+        next = attn_look_up(a, table, (to - from > 128 ? from + 128 : to) + lane, to);
+    }
+    __syncthreads();
+    uint32_t buffer = 0;
+    for (uint32_t base = from; base < to; base += 64) {
+        const typename Lds::Buffer& tile = lds.tile[buffer];
+        const uint64_t next_valid = __ballot(there);
+        f32x4 x[NT][4];
+        float keep[NT];
+        bool moved[NT];
+        const bool used = base < some;
+        if (used) {
+            rows.scores(x, [&](int i, int st) { return tile.k[i][st][lane]; }, tile.ks, kq);
+            if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
+            rows.weigh(x, keep, moved);
+        }
+        // (behind the last tile nothing new is made or loaded, but it costs no
+        // branch)
+        put(lds.tile[buffer ^ 1]);
+        fetch(next);
+        next = attn_look_up(a, table, (to - base > 192 ? base + 192 : to) + lane, to);
+        __builtin_amdgcn_sched_barrier(0);
+        if (used) rows.add(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq);
+        valid = next_valid;
+        buffer ^= 1;
+        __syncthreads();
+    }
+    if (r0 < live) rows.store(a, at, at.head, r0, live, n16, kq);
 }
 
 }  // namespace

@@ -19,12 +19,32 @@ const void* attn_by_scales(int scales)
     }
 }
 
+template <int DT, int DP, bool P16>
+const void* attn_shared(int scales)
+{
+    switch (scales) {
+    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, false, false, P16>);
+    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, true, false, P16>);
+    default: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, true, true, P16>);
+    }
+}
+
+template <int DT, int DP, bool P16>
+const void* attn_by_rows(int scales, AttnRowsOf rows)
+{
+    switch (rows) {
+    case AttnRowsOf::kOneTile: return attn_by_scales<DT, DP, P16, 1>(scales);
+    case AttnRowsOf::kTwoTiles: return attn_by_scales<DT, DP, P16, 2>(scales);
+    default: return attn_shared<DT, DP, P16>(scales);
+    }
+}
+
 template <int DT, bool P16>
-const void* attn_kernel(int lanes, int scales, int tiles)
+const void* attn_kernel(int lanes, int scales, AttnRowsOf rows)
 {
     switch (lanes) {
-    case 64: return tiles == 1 ? attn_by_scales<DT, 64, P16, 1>(scales) : attn_by_scales<DT, 64, P16, 2>(scales);
-    case 128: return tiles == 1 ? attn_by_scales<DT, 128, P16, 1>(scales) : attn_by_scales<DT, 128, P16, 2>(scales);
+    case 64: return attn_by_rows<DT, 64, P16>(scales, rows);
+    case 128: return attn_by_rows<DT, 128, P16>(scales, rows);
     default: return attn_by_scales<DT, 256, P16, 1>(scales);
     }
 }
