@@ -241,7 +241,9 @@ struct AttnRows {
     // x^T = K Q^T, a token a row of the product, less the row's m. k_numbers_of(i,
     // st): step st of the tile's tokens 16 i to 16 i + 15; ks: K's scales by
     // token, of each step or one.
-    template <class F>
+    // HOLD: the numbers are made there and then, and the compiler is not to make
+    // those of all tokens before their products, for want of registers.
+    template <bool HOLD, class F>
     __device__ __forceinline__ void scores(f32x4 (&x)[NT][4], const F& k_numbers_of, const float (*ks)[64], uint32_t kq)
     {
         f32x4 scale[4];
@@ -267,7 +269,7 @@ struct AttnRows {
                     for (int t = 0; t < NT; ++t) x[t][i] = attn_mfma<DT>(k, q[t][st], st == 0 ? start[t][0] : x[t][i]);
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);     // (else the numbers of all tokens pile up in registers)
+            if (HOLD) __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!KF) {
 #pragma unroll
@@ -342,7 +344,7 @@ struct AttnRows {
     // By segments: the weights times V's scales, in fp16, and o^T += V^T P^T, 32
     // tokens a product. v_numbers_of(h, i): product i's V of half h of the tokens;
     // vs: V's scales by token, of each segment or one.
-    template <class F>
+    template <bool HOLD, class F>
     __device__ __forceinline__ void add(const f32x4 (&x)[NT][4], const float (&keep)[NT], const bool (&moved)[NT], const F& v_numbers_of,
                                         const float (*vs)[64], uint32_t kq)
     {
@@ -387,7 +389,7 @@ struct AttnRows {
                     const v4u v = v_numbers_of(h, i);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][h], acc[t][i]);
-                    if (i & 1) __builtin_amdgcn_sched_barrier(0);
+                    if (HOLD && (i & 1)) __builtin_amdgcn_sched_barrier(0);
                 }
         }
     }
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         wave_sync();
 
         f32x4 x[NT][4];
-        rows.scores(x, [&](int i, int st) { return k_numbers<DT>(kw[i][st], k_const); }, my.ks, kq);
+        rows.template scores<true>(x, [&](int i, int st) { return k_numbers<DT>(kw[i][st], k_const); }, my.ks, kq);
         if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
 
         // The next tile's scales and K; its V when this one's is used up. (Behind
@@ -680,7 +682,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                 }
             }
 
-        rows.add(x, keep, moved, [&](int h, int i) {
+        rows.template add<true>(x, keep, moved, [&](int h, int i) {
             v4u v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
         bool moved[NT];
         const bool used = base < some;
         if (used) {
-            rows.scores(x, [&](int i, int st) { return tile.k[i][st][lane]; }, tile.ks, kq);
+            rows.template scores<false>(x, [&](int i, int st) { return tile.k[i][st][lane]; }, tile.ks, kq);
             if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
             rows.weigh(x, keep, moved);
         }
@@ -927,7 +929,7 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
         fetch(next);
         next = attn_look_up(a, table, (to - base > 192 ? base + 192 : to) + lane, to);
         __builtin_amdgcn_sched_barrier(0);
-        if (used) rows.add(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq);
+        if (used) rows.template add<false>(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq);
         valid = next_valid;
         buffer ^= 1;
         __syncthreads();
