@@ -142,6 +142,30 @@ __device__ __forceinline__ uint32_t quad_bytes(uint32_t w, uint32_t sel1, uint32
     return __builtin_amdgcn_perm(p, w, sel2);
 }
 
+// The largest of three numbers that arithmetic has made (the compiler would first
+// quiet each; NaN loses here as there).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c)       // of a and two magnitudes
+{
+    float r;
+    asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// The least of 16 lanes' numbers.
+__device__ __forceinline__ int32_t least16(int32_t v)
+{
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));
+    return min(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));
+}
+
 __device__ __forceinline__ void wave_sync()
 {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -197,6 +221,7 @@ struct AttnRows {
     f32x4 acc[NT][VT];
     float m[NT], less[NT], l[NT], top[NT][NGV];    // less: m, or 0 where there is none yet
     int32_t e[NT][NGV];
+    float safe[NGV];                               // scales that no row's weights outgrow fp16 with
 
     // Rows r0 to live - 1 (or fewer) of a cached head: a column a row, 8 elements
     // a step in k_numbers' order.
@@ -226,6 +251,8 @@ struct AttnRows {
                     sum = 0.0f;
                 }
             }
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) safe[g] = 0.0f;
             m[t] = kAttnNone;
             less[t] = l[t] = 0.0f;
 #pragma unroll
@@ -307,12 +334,10 @@ struct AttnRows {
     {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float most = x[t][0][0];
+            float most = max3(x[t][0][0], x[t][0][1], x[t][0][2]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) most = fmaxf(most, x[t][i][r]);
-            most = column_max(most);
+            for (int k = 3; k < 15; k += 2) most = max3(most, x[t][k / 4][k % 4], x[t][(k + 1) / 4][(k + 1) % 4]);
+            most = column_max(fmaxf(most, x[t][3][3]));
             keep[t] = 1.0f;
             moved[t] = __any(most > (m[t] == kAttnNone ? kAttnNone : 6.0f));
             if (moved[t]) {
@@ -346,32 +371,44 @@ struct AttnRows {
     // vs: V's scales by token, of each segment or one.
     template <bool HOLD, class F>
     __device__ __forceinline__ void add(const f32x4 (&x)[NT][4], const float (&keep)[NT], const bool (&moved)[NT], const F& v_numbers_of,
-                                        const float (*vs)[64], uint32_t kq)
+                                        const float (*vs)[64], uint32_t kq, uint32_t lane)
     {
 #pragma unroll
         for (int g = 0; g < NGV; ++g) {
             constexpr int T = VT / NGV;            // products of a segment
             v4u p[NT][2];
+            // Weights are at most 2^6 (m follows beyond that): the tile's scales
+            // tell whether one could outgrow fp16. If so, or where a maximum has
+            // moved, the powers of two are set anew from the largest product.
+            bool set = __any(fabsf(vs[g][lane]) > safe[g]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4 w[4];
-                float high = 0.0f;
+            for (int t = 0; t < NT; ++t) set = set || moved[t];
+            if (set) {
+                int32_t least = 127;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[i] = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
+                for (int t = 0; t < NT; ++t) {
+                    float high = 0.0f;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) high = fmaxf(high, fabsf(w[i][r]));
-                }
-                if (moved[t]) top[t][g] *= keep[t];
-                top[t][g] = fmaxf(top[t][g], column_max(high));
-                if (moved[t] || __any(__builtin_ldexpf(top[t][g], -e[t][g]) > 256.0f)) {
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x4 w = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
+                        high = max3_abs(max3_abs(high, w[0], w[1]), w[2], w[3]);
+                    }
+                    top[t][g] = fmaxf(top[t][g] * keep[t], column_max(high));
                     int32_t now = __builtin_amdgcn_frexp_expf(top[t][g]);
                     now = top[t][g] > 0.0f ? min(max(now, -120), 120) : e[t][g];
                     const float f = __builtin_ldexpf(keep[t], e[t][g] - now);
                     e[t][g] = now;
+                    least = min(least, now);
 #pragma unroll
                     for (int i = 0; i < T; ++i) acc[t][g * T + i] *= f;
                 }
+                safe[g] = __builtin_ldexpf(0x1p9f, least16(least));        // 2^6 * 2^9 = 2^15
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f32x4 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
                 const float c = __builtin_ldexpf(1.0f, -e[t][g]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -499,7 +536,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnSeq& 
 // Waves that a SIMD is to hold: what their registers allow.
 constexpr int attn_waves(int lanes, bool kf, int tiles)
 {
-    return lanes == 256 ? 1 : (lanes == 64 || !kf ? 4 : 3) - tiles;
+    return lanes == 256 ? 1 : lanes == 64 ? 4 - tiles : kf && tiles == 2 ? 1 : 2;
 }
 
 template <int DT, int DP, int DVP, bool KF, bool VF, bool P16, int NT>
@@ -691,7 +728,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                        (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
             }
             return v;
-        }, my.vs, kq);
+        }, my.vs, kq, lane);
         fetch_v(next);
         next = after;
     }
@@ -929,7 +966,7 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
         fetch(next);
         next = attn_look_up(a, table, (to - base > 192 ? base + 192 : to) + lane, to);
         __builtin_amdgcn_sched_barrier(0);
-        if (used) rows.template add<false>(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq);
+        if (used) rows.template add<false>(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq, lane);
         valid = next_valid;
         buffer ^= 1;
         __syncthreads();
