@@ -1,0 +1,144 @@
+"""Attention over a paged cache in 4 bits: each kernel a call may take, at the
+sizes, masks and layouts where it could go wrong, against the definition in 64
+bits."""
+import pytest
+import torch
+
+import transformer_positional_encoding_amd as rp
+from test_cache_attention_gpu import call, check, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("heads, hq, S", [(4, 4, 1), (4, 16, 4), (8, 32, 1), (12, 24, 2), (8, 8, 16)])
+@pytest.mark.parametrize("D, page, dtype", [(128, 16, "bf16"), (128, 48, "f16"), (64, 16, "f16"), (64, 1024, "bf16")])
+def test_four_heads_beside_each_other(heads, hq, S, D, page, dtype):
+    lengths = [1, 16, 63, 64, 65, 0, 129, 700, S]
+    c = inputs(lengths, S, hq, heads, D, D, D, D, page, dtype, seed=31)
+    for causal in (True, False):
+        check(call(c, causal=causal), c, causal=causal)
+    counts = torch.tensor([S, 0, S + 2, 1, S, S, -1, max(1, S // 2), S], dtype=torch.int32)
+    got = call(c, counts=counts)
+    check(got, c, counts=counts)
+    for b, n in enumerate(counts.tolist()):
+        assert torch.equal(got[b, min(max(n, 0), S):].cpu(), c["out"][b, min(max(n, 0), S):])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_four_heads_pages_outside_the_cache_and_what_no_row_sees(D):
+    c = inputs([200, 170, 90, 333], 2, 8, 4, D, D, D, D, 16, "bf16", seed=32)
+    c["table"][0, 3], c["table"][0, 7], c["table"][1, :] = -1, 10 ** 6, -1
+    c["table"][2, 0] = c["k"][0].shape[0]
+    want = call(c)
+    check(want, c)
+    assert not bool(want[1].any())
+    for name in ("k", "v"):
+        data, scales = c[name]
+        live = torch.zeros(data.shape[:2], dtype=torch.bool)
+        for b, n in enumerate(c["lengths"].tolist()):
+            t = torch.arange(n)
+            at = c["table"][b, t // 16].long()
+            ok = (at >= 0) & (at < data.shape[0])
+            live[at[ok], (t % 16)[ok]] = True
+        data[~live], scales[~live] = 0x88, float("nan")
+    assert torch.equal(call(c), want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("span", [3.0, 12.0])
+def test_four_heads_scales_far_apart(D, span):
+    c = inputs([500, 333], 2, 8, 4, D, D, D, D, 16, "bf16", seed=33, span=span)
+    c["k"] = (c["k"][0], c["k"][1].clamp(max=4.0))
+    check(call(c), c)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("layout", ["halves", "gaps", "heads first", "scales shifted", "scales apart", "codes shifted"])
+def test_four_heads_layouts(D, layout):
+    """Caches whose heads' rows and scales lie side by side, and those where
+    they do not."""
+    c = inputs([130, 77, 1], 1, 8, 4, D, D, D, D, 16, "bf16", seed=34)
+    on = {n: c[n].cuda() for n in ("q", "table", "lengths")}
+
+    def laid(data, scales):
+        data, scales = data.cuda(), scales.cuda()
+        P = data.shape[0]
+        if layout == "halves":                     # K (or V) of a page beside other bytes
+            both = torch.full((P, 2, 16, 4, D // 2), 0x77, dtype=torch.uint8, device="cuda")
+            both[:, 1] = data
+            data = both[:, 1]
+        elif layout == "gaps":                     # more heads than are cached here
+            wide = torch.full((P, 16, 8, D // 2), 0x77, dtype=torch.uint8, device="cuda")
+            wide[:, :, 4:] = data
+            more = torch.full((P, 16, 8, 1), float("nan"), device="cuda")
+            more[:, :, 4:] = scales
+            data, scales = wide[:, :, 4:], more[:, :, 4:]
+        elif layout == "heads first":
+            data, scales = data.transpose(1, 2).contiguous().transpose(1, 2), scales.transpose(1, 2).contiguous().transpose(1, 2)
+        elif layout == "scales shifted":
+            more = torch.full((scales.numel() + 1,), float("nan"), device="cuda")
+            more[1:] = scales.reshape(-1)
+            scales = more[1:].view(scales.shape)
+        elif layout == "scales apart":
+            more = torch.full((P, 16, 5, 1), float("nan"), device="cuda")
+            more[:, :, :4] = scales
+            scales = more[:, :, :4]
+        else:
+            more = torch.full((data.numel() + 4,), 0x77, dtype=torch.uint8, device="cuda")
+            more[4:] = data.reshape(-1)
+            data = more[4:].view(data.shape)
+        return rp.RopeCache(data, scales)
+
+    got = rp.rope_cache_attention(on["q"], laid(*c["k"]), laid(*c["v"]), on["table"], on["lengths"], out=c["out"].cuda())
+    check(got, c)
+    if layout != "codes shifted":                  # (codes off 16 bytes: a score's 32-bit sums run in another order)
+        assert torch.equal(got, call(c))
+
+
+@pytest.mark.parametrize("S, hq, heads", [(17, 1, 1), (16, 8, 4), (64, 2, 2), (65, 1, 1), (32, 16, 4), (129, 3, 3)])
+@pytest.mark.parametrize("D, Dv, gk, gv, page", [(128, 128, 32, 32, 16), (128, 128, 128, 64, 24), (64, 64, 64, 64, 7), (64, 64, 32, 32, 48),
+                                                 (96, 128, 96, 32, 16), (128, 64, 64, 64, 5), (256, 192, 256, 64, 16)])
+def test_rows_of_a_prompt(S, hq, heads, D, Dv, gk, gv, page):
+    """One token more or less than a tile's, a page's and a block's rows; empty
+    sequences; tokens that were there before the prompt."""
+    for dtype, lengths in (("bf16", [S, 0, S + 1, 200]), ("f16", [63 + S, 1, 330, S - 1])):
+        c = inputs(lengths, S, hq, heads, D, Dv, gk, gv, page, dtype, seed=35)
+        counts = torch.tensor([S, S, S - 1, (S + 1) // 2], dtype=torch.int32)
+        check(call(c, counts=counts), c, counts=counts, what=f"{dtype} causal")
+        check(call(c, causal=False), c, causal=False, what=dtype)
+
+
+@pytest.mark.parametrize("S, hq, heads, D", [(1, 8, 4, 128), (1, 8, 4, 64), (6, 8, 2, 128), (70, 4, 2, 128)])
+def test_two_graphs_share_a_workspace(S, hq, heads, D):
+    """Two captured calls that split the same sequences and use one workspace,
+    replayed in turn, with the program's own work between them."""
+    c = [inputs([900, 333, 70], S, hq, heads, D, D, D, D, 16, "bf16", seed=s) for s in (36, 37)]
+    ws = torch.empty(rp.rope_cache_attention_workspace(3, S, hq, heads, D), dtype=torch.uint8, device="cuda")
+    args, outs, graphs = [], [], []
+    for one in c:
+        caches = [rp.RopeCache(one[n][0].cuda(), one[n][1].cuda()) for n in ("k", "v")]
+        args.append((one["q"].cuda(), *caches, one["table"].cuda(), one["lengths"].cuda()))
+        outs.append(one["out"].cuda())
+        rp.rope_cache_attention(*args[-1], out=outs[-1], workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            rp.rope_cache_attention(*args[-1], out=outs[-1], workspace=ws)
+    for i in range(4):
+        for a, o, g in zip(args, outs, graphs):
+            a[0].mul_(-0.9)
+            o.fill_(7.0)
+            g.replay()
+            assert torch.equal(o, rp.rope_cache_attention(*a)), i
+
+
+def test_the_same_sequence_twice_and_pages_shared():
+    """Rows of the table that name the same pages: sequences with a common
+    start, and one sequence asked about twice."""
+    c = inputs([400, 400, 380], 1, 8, 4, 128, 128, 128, 128, 16, "bf16", seed=38)
+    c["table"][1] = c["table"][0]
+    c["table"][2, :20] = c["table"][0, :20]
+    c["q"][1] = c["q"][0]
+    got = call(c)
+    check(got, c)
+    assert torch.equal(got[0], got[1])

@@ -80,9 +80,17 @@ bool codes_aligned(const CachePlan& c, uintptr_t bytes)
            c.st[1] % (int64_t)bytes == 0 && c.st[2] % (int64_t)bytes == 0;
 }
 
+// Whether the rows and scales of four heads lie beside each other, in 16-byte
+// pieces.
+bool heads_together(const CachePlan& c, int64_t heads, int64_t D)
+{
+    return heads % 4 == 0 && codes_aligned(c, 16) && c.st[2] == D / 2 && aligned16(c.scales) && c.sc[0] % 4 == 0 &&
+           c.sc[1] % 4 == 0 && c.sc[2] == 1;
+}
+
 // The matrix-core kernel of a call, and its lanes; NULL if it does not take the
 // shapes.
-const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes)
+const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes, int64_t heads)
 {
     const int64_t D = p.q.D, Dv = p.out.D;
     if (p.rope.dtype == ROPE_DTYPE_F32 || D > 256 || Dv > 256 || !rows_in_chunks(p.q, 2) || !rows_in_chunks(p.out, 2))
@@ -93,6 +101,9 @@ const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes)
     const int scales = !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
     if (!codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4)) return nullptr;
     const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
+    if (rows == AttnRowsOf::kOneTile && lanes < 256 && whole16 && scales == kAttnRowScales && Dv == D &&
+        heads_together(p.kc, heads, D) && heads_together(p.vc, heads, D))
+        rows = AttnRowsOf::kFourHeads;
     if (p.rope.dtype == ROPE_DTYPE_BF16)
         return whole16 ? attn_kernel_bf16(lanes, scales, rows) : attn_kernel_bf16_any(lanes, scales, rows);
     return whole16 ? attn_kernel_f16(lanes, scales, rows) : attn_kernel_f16_any(lanes, scales, rows);
@@ -104,7 +115,7 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     static_cast<AttnArgs&>(a) = attn_args(p);
     const int lanes = std::max(p.q.D, p.out.D) <= 64 ? 64 : std::max(p.q.D, p.out.D) <= 128 ? 128 : 256;
     const AttnRowsOf rows = lanes == 256 || a.rows <= 16 ? AttnRowsOf::kOneTile : a.rows <= 64 ? AttnRowsOf::kTwoTiles : AttnRowsOf::kShared;
-    const void* fn = mfma_kernel(p, rows, lanes);
+    const void* fn = mfma_kernel(p, rows, lanes, a.heads);
     const bool mfma = fn != nullptr;
     // Few rows: a wave a head, as far as heads go by fours, which then read
     // neighbouring bytes; else waves take turns at the tokens. Many: a wave its

@@ -42,6 +42,7 @@
 #pragma once
 
 #include "rope_attn_kernels.hpp"
+#include "rope_dma.hpp"
 
 namespace rope {
 namespace {
@@ -972,6 +973,175 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
         __syncthreads();
     }
     if (r0 < live) rows.store(a, at, at.head, r0, live, n16, kq);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows, four cached heads beside each other: a block's waves have a head
+// each, and load a tile's rows for all four, straight to LDS, while the tile
+// before is used: 256 (128) consecutive bytes a token and 16 of scales, where
+// each wave for itself would ask for 64 (32) and 4. The card brings the first
+// at the rate of a copy, not the second. 64 sequences of 1 to 8192 tokens, 32
+// heads on 8 of 128: 105 us (4.1 TB/s), 119 by waves on their own, whose loads
+// alone, without arithmetic, are 115; 64 heads on 16 of 64: 132 us, 203. A
+// token's 16-byte pieces stand in LDS in an order that its number turns, so
+// that neither K's reads (the same piece of 16 tokens) nor V's (four pieces of
+// four tokens) meet in a bank. Two buffers of 17 or 35 KB; one barrier a tile.
+// ---------------------------------------------------------------------------
+template <int DP>
+struct alignas(16) AttnHeadsLds {
+    static constexpr int kRow = 2 * DP;            // bytes of a token's four rows
+    struct Tile {
+        char k[64 * kRow], v[64 * kRow];
+        float ks[64][4], vs[64][4];
+    };
+    Tile tile[2];
+    struct Wave {
+        float ks[1][64], vs[1][64];
+    };
+    Wave wave[4];
+};
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
+{
+    using Lds = AttnHeadsLds<DP>;
+    using R = AttnRows<DT, DP, DP, false, false, 1>;
+    constexpr int KW = R::KW;
+    constexpr uint32_t kPieces = Lds::kRow / 16;   // of a token
+    constexpr uint32_t kTokens = 64 / kPieces;     // of a load
+    constexpr int kLoads = 16 / kTokens;           // of 16 tokens
+    static_assert(DP == 64 || DP == 128, "whole loads of 16 tokens");
+    __shared__ Lds lds;
+    const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const AttnAt at = attn_at(a, blockIdx.x);
+    const AttnSeq seq = attn_seq(a, at.b);
+    const uint32_t head0 = at.head * 4, r0 = at.tile * 16;
+    const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
+    if (r0 >= live) return;                        // the same for the whole block
+    const AttnSpan span = attn_span(a, seq, r0, min(r0 + 16, live));
+    uint32_t from, to;
+    attn_part(span.some, at.split, a.splits, 64, &from, &to);
+    const uint32_t all = min(span.all, to);
+    R rows;
+    rows.load(a, seq, at.b, head0 + wave, r0, live, n16, kq);
+
+    const gchar* const k_base = as_global(a.kc.data) + head0 * a.kc.st[2];
+    const gchar* const v_base = as_global(a.vc.data) + head0 * a.vc.st[2];
+    const int32_t* const table = a.table + at.b * a.table_stride;
+    const uint32_t lds_base = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) Lds*)&lds);
+    // a load's lanes: token lane / pieces of its kTokens, piece lane % pieces in
+    // its turned order
+    uint32_t k_off[kLoads], v_off[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const uint32_t tok = i * kTokens + lane / kPieces, piece = (lane % kPieces) ^ (tok % kPieces);
+        k_off[i] = tok * (uint32_t)a.kc.st[1] + 16 * piece;
+        v_off[i] = tok * (uint32_t)a.vc.st[1] + 16 * piece;
+    }
+    // this wave's quarter of a tile: 16 tokens of K and V; the first two waves
+    // also the scales
+    const auto issue = [&](const AttnPlace& p, uint32_t buffer) {
+        const gchar* k_row = attn_group_at(p, wave, k_base, a.kc);
+        const gchar* v_row = attn_group_at(p, wave, v_base, a.vc);
+        const uint32_t to_tile = lds_base + (uint32_t)offsetof(Lds, tile) + buffer * (uint32_t)sizeof(typename Lds::Tile);
+        const uint32_t mine = to_tile + wave * 16 * Lds::kRow;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            lds_dma16((const void*)k_row, k_off[i], mine + (uint32_t)offsetof(typename Lds::Tile, k) + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            lds_dma16((const void*)v_row, v_off[i], mine + (uint32_t)offsetof(typename Lds::Tile, v) + 1024 * i);
+        const int64_t page = p.page, in_page = p.in_page;
+        if (wave == 0)
+            lds_dma16_far(a.kc.scales + (page * a.kc.sc[0] + in_page * a.kc.sc[1] + head0),
+                          to_tile + (uint32_t)offsetof(typename Lds::Tile, ks));
+        if (wave == 1)
+            lds_dma16_far(a.vc.scales + (page * a.vc.sc[0] + in_page * a.vc.sc[1] + head0),
+                          to_tile + (uint32_t)offsetof(typename Lds::Tile, vs));
+    };
+
+    const Numbers k_const = k_constants<DT>();
+    const VConstants v_const = v_constants();
+    typename Lds::Wave& my = lds.wave[wave];
+    AttnPlace now = attn_look_up(a, table, from + lane, to);
+    attn_settle(a, now);
+    if (from < to) issue(now, 0);
+    AttnPlace next = attn_look_up(a, table, (to - from > 64 ? from + 64 : to) + lane, to);
+    uint32_t buffer = 0;
+    for (uint32_t base = from; base < to; base += 64) {
+        wait_vm<0>();                              // this wave's loads are there
+        // ... and everyone's, and everyone is done with the other buffer. (A bare
+        // barrier; the empty asm keeps this tile's reads behind it.)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const uint64_t valid = __ballot(now.there);
+        const typename Lds::Tile& tile = lds.tile[buffer];
+        my.ks[0][lane] = now.there ? tile.ks[lane][wave] * a.scale2 : 0.0f;
+        my.vs[0][lane] = now.there ? tile.vs[lane][wave] : 0.0f;
+        attn_settle(a, next);
+        if (to - base > 64) issue(next, buffer ^ 1);
+        const AttnPlace after = attn_look_up(a, table, (to - base > 128 ? base + 128 : to) + lane, to);
+        wave_sync();
+        uint32_t kw[4][KW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const char* row = tile.k + (16 * i + n16) * Lds::kRow;
+            if constexpr (KW == 4) {
+                const v4u w = *reinterpret_cast<const v4u*>(row + 16 * ((wave * 4 + kq) ^ n16));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kw[i][j] = w[j];
+            } else {
+                const v2u w = *reinterpret_cast<const v2u*>(row + 16 * ((wave * 2 + (kq >> 1)) ^ (n16 & 7)) + 8 * (kq & 1));
+                kw[i][0] = w[0];
+                kw[i][1] = w[1];
+            }
+        }
+        f32x4 x[1][4];
+        rows.template scores<true>(x, [&](int i, int st) { return k_numbers<DT>(kw[i][st], k_const); }, my.ks, kq);
+        if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
+        float keep[1];
+        bool moved[1];
+        rows.weigh(x, keep, moved);
+        // V's words, the codes of two tokens at equal nibbles of their halves
+        uint32_t two[2][DP / 64][4];
+        const auto word = [&](uint32_t i) -> uint32_t {
+            const uint32_t tok = 16 * (i >> 2) + 4 * kq + (i & 3);
+            if constexpr (DP == 128) {
+                const uint32_t piece = (wave * 4 + (n16 >> 2)) ^ (4 * kq + (i & 3));
+                return *reinterpret_cast<const uint32_t*>(tile.v + tok * Lds::kRow + 16 * piece + 4 * (n16 & 3));
+            } else {
+                const uint32_t piece = (wave * 2 + (n16 >> 3)) ^ ((4 * kq + (i & 3)) & 7);
+                return *reinterpret_cast<const uint16_t*>(tile.v + tok * Lds::kRow + 16 * piece + 2 * (n16 & 7));
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t i = 8 * h + 4 * (j >> 1) + 2 * (j & 1), w0 = word(i), w1 = word(i + 1);
+                if constexpr (DP == 64) {
+                    two[h][0][j] = w0 | (w1 << 16);
+                } else {
+                    two[h][0][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100);
+                    two[h][1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302);
+                }
+            }
+        rows.template add<true>(x, keep, moved, [&](int h, int i) {
+            v4u v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = two[h][i >> 2][j];
+                v[j] = (i & 3) == 0 ? v_numbers<0>(w, v_const) : (i & 3) == 1 ? v_numbers<1>(w, v_const) :
+                       (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
+            }
+            return v;
+        }, my.vs, kq, lane);
+        now = next;
+        next = after;
+        buffer ^= 1;
+    }
+    rows.store(a, at, head0 + wave, r0, live, n16, kq);
 }
 
 }  // namespace

@@ -35,6 +35,9 @@ const void* attn_by_rows(int scales, AttnRowsOf rows)
     switch (rows) {
     case AttnRowsOf::kOneTile: return attn_by_scales<DT, DP, P16, 1>(scales);
     case AttnRowsOf::kTwoTiles: return attn_by_scales<DT, DP, P16, 2>(scales);
+    case AttnRowsOf::kFourHeads:
+        if constexpr (P16) return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP>);
+        return nullptr;
     default: return attn_shared<DT, DP, P16>(scales);
     }
 }

@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "rope_device.hpp"
+#include "rope_dma.hpp"
 
 namespace rope {
 namespace {
@@ -101,23 +102,6 @@ struct ProjTile {
 // over 128 banks) then meet distinct 16-byte bank groups; the value depends
 // only on r mod 32, so every 32-row fragment uses the same slots.
 __device__ __forceinline__ int proj_swz(int r) { return ((r ^ (r >> 3)) & 3) | (r & 4); }
-
-// One direct global-to-LDS load of 16 bytes per lane from base + voff (base
-// the same for the whole wave, voff lane l's byte offset): lane l's bytes go
-// to LDS byte address lds_base + 16*l (lds_base the same for the whole wave).
-__device__ __forceinline__ void proj_dma16(const void* base, uint32_t voff, uint32_t lds_base)
-{
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(voff), "s"(base) : "memory");
-}
-
-// s_waitcnt vmcnt(N) with lgkmcnt and expcnt left free (gfx9 encoding:
-// vmcnt bits [3:0] and [15:14], expcnt [6:4], lgkmcnt [11:8]).
-template <int N>
-__device__ __forceinline__ void proj_wait_vm()
-{
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
 
 struct ProjArgs {
     const uint16_t* x;     // (M, K) 16-bit
@@ -280,7 +264,7 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
         const uint16_t* wk = a.w + k * kProjBK;
         const uint32_t sbase = wave_lds + (uint32_t)(slot * T_::STAGE);
 #pragma unroll
-        for (int i = 0; i < LW; ++i) proj_dma16(from_x[i] ? xk : wk, goff[i], sbase + i * 1024);
+        for (int i = 0; i < LW; ++i) lds_dma16(from_x[i] ? xk : wk, goff[i], sbase + i * 1024);
     };
 
     f32x16 acc[MT][NT];
@@ -320,7 +304,7 @@ __global__ void __launch_bounds__(ProjTile<BN>::THREADS)
     const int32_t KT = a.K / kProjBK;
     issue_stage(0, 0);
     for (int32_t kt = 0; kt < KT; ++kt) {
-        proj_wait_vm<0>();                             // this wave's loads of stage kt are in LDS
+        wait_vm<0>();                                  // this wave's loads of stage kt are in LDS
         // everyone's are, and everyone has consumed stage kt-1, whose slot is
         // refilled next. A bare barrier (no fence); the empty asm keeps the
         // compiler from moving this stage's LDS reads above it.
@@ -768,7 +752,7 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     const uint32_t smem_lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint16_t*)smem);
     const uint32_t wave_lds = __builtin_amdgcn_readfirstlane(smem_lds + wave * LW * 1024);
     auto load1 = [&](int32_t kt, int slot, int i) {
-        proj_dma16(src + kt * kProjBK, goff[i], wave_lds + (uint32_t)(slot * T_::STAGE) + i * 1024);
+        lds_dma16(src + kt * kProjBK, goff[i], wave_lds + (uint32_t)(slot * T_::STAGE) + i * 1024);
     };
 
     // ---------------------------------------------------------------- fragments
@@ -860,7 +844,7 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
 #pragma unroll
         for (int i = 0; i < LW; ++i) asm volatile("" : "+v"(toff[i]));   // kept here, not sunk to the uses
     };
-    auto tab_dma = [&](int i) { proj_dma16(tab_base, toff[i], tab_lds + (uint32_t)(i * 1024)); };
+    auto tab_dma = [&](int i) { lds_dma16(tab_base, toff[i], tab_lds + (uint32_t)(i * 1024)); };
     auto stage = [&](auto slot_c, auto more_c, auto first_c, int32_t kt) {
         constexpr int slot = decltype(slot_c)::value;
         constexpr bool more = decltype(more_c)::value;
@@ -871,7 +855,7 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 if (kk == 3 && j == 8 && more) {
-                    proj_wait_vm<0>();
+                    wait_vm<0>();
                     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0), vmcnt and expcnt free
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
@@ -898,7 +882,7 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
     for (int i = 0; i < LW; ++i) load1(0, 0, i);
     if constexpr (EPI >= 0)
         if (ntab) tab_offsets();
-    proj_wait_vm<0>();
+    wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -933,7 +917,7 @@ __global__ void __launch_bounds__(ProjSq::THREADS) __attribute__((amdgpu_waves_p
         }
     }
     stage(S1{}, Last{}, Later{}, kt);
-    proj_wait_vm<0>();                                 // this wave's table rows are in LDS
+    wait_vm<0>();                                      // this wave's table rows are in LDS
     __syncthreads();                                   // every wave is done with the ring
     if constexpr (ProjAdapters<ARGS>::kAny)
         ProjAdapters<ARGS>::template add_square<DT>(a, adapters, acc, n0 + wn * 128, lane);
