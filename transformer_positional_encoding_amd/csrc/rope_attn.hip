@@ -80,12 +80,12 @@ bool codes_aligned(const CachePlan& c, uintptr_t bytes)
            c.st[1] % (int64_t)bytes == 0 && c.st[2] % (int64_t)bytes == 0;
 }
 
-// Whether the rows and scales of four heads lie beside each other, in 16-byte
-// pieces.
-bool heads_together(const CachePlan& c, int64_t heads, int64_t D)
+// Whether the rows of four heads lie beside each other in 16-byte pieces, and
+// those of their scales that are one a row.
+bool heads_together(const CachePlan& c, int64_t heads, int64_t D, bool scales)
 {
-    return heads % 4 == 0 && codes_aligned(c, 16) && c.st[2] == D / 2 && aligned16(c.scales) && c.sc[0] % 4 == 0 &&
-           c.sc[1] % 4 == 0 && c.sc[2] == 1;
+    return heads % 4 == 0 && codes_aligned(c, 16) && c.st[2] == D / 2 &&
+           (!scales || (aligned16(c.scales) && c.sc[0] % 4 == 0 && c.sc[1] % 4 == 0 && c.sc[2] == 1));
 }
 
 // The matrix-core kernel of a call, and its lanes; NULL if it does not take the
@@ -101,9 +101,9 @@ const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes, int64_t h
     const int scales = !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
     if (!codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4)) return nullptr;
     const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
-    if (rows == AttnRowsOf::kOneTile && lanes < 256 && whole16 && scales == kAttnRowScales && Dv == D &&
-        heads_together(p.kc, heads, D) && heads_together(p.vc, heads, D))
-        rows = AttnRowsOf::kFourHeads;
+    if (rows != AttnRowsOf::kShared && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
+        heads_together(p.kc, heads, D, scales == kAttnRowScales) && heads_together(p.vc, heads, D, scales == kAttnRowScales))
+        rows = rows == AttnRowsOf::kOneTile ? AttnRowsOf::kFourHeads : AttnRowsOf::kFourHeadsTwoTiles;
     if (p.rope.dtype == ROPE_DTYPE_BF16)
         return whole16 ? attn_kernel_bf16(lanes, scales, rows) : attn_kernel_bf16_any(lanes, scales, rows);
     return whole16 ? attn_kernel_f16(lanes, scales, rows) : attn_kernel_f16_any(lanes, scales, rows);

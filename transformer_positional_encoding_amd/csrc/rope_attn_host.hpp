@@ -12,11 +12,11 @@ constexpr int kAttnSegments = 2;
 
 // Query rows of a cached head that a kernel takes: 16 or 32 a wave, by waves on
 // their own, or 32 a wave, 128 a block, whose waves share their tiles' numbers,
-// or 16 a wave of one of four heads that a block loads together.
-enum class AttnRowsOf { kOneTile, kTwoTiles, kShared, kFourHeads };
+// or 16 or 32 a wave of one of four heads that a block loads together.
+enum class AttnRowsOf { kOneTile, kTwoTiles, kShared, kFourHeads, kFourHeadsTwoTiles };
 
 // The kernel for rows of up to `lanes` lanes (64, 128; 256: kOneTile only;
-// kFourHeads: kAttnRowScales and pages of whole 16 tokens only).
+// kFourHeads: pages of whole 16 tokens only).
 // _any: for pages of any size, the others for pages of whole 16 tokens less
 // than 2^26 bytes apart.
 const void* attn_kernel_bf16(int lanes, int scales, AttnRowsOf rows);

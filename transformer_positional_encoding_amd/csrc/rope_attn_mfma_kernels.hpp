@@ -69,12 +69,19 @@ __device__ __forceinline__ f32x4 attn_mfma(const v4u& a, const v4u& b, const f32
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// A constant in a register, which takes part in three-operand logic as two
-// literals could not.
+// Constants in a register of each lane, or one of the wave: one of either takes
+// part in three-operand logic as two literals could not.
 __device__ __forceinline__ uint32_t vector_constant(uint32_t v)
 {
     uint32_t r;
     asm("v_mov_b32 %0, %1" : "=v"(r) : "i"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t scalar_constant(uint32_t v)
+{
+    uint32_t r;
+    asm("s_mov_b32 %0, %1" : "=s"(r) : "i"(v));
     return r;
 }
 
@@ -89,8 +96,8 @@ __device__ __forceinline__ uint32_t number(uint32_t w, const Numbers& c) { retur
 template <int DT>
 __device__ __forceinline__ Numbers k_constants()
 {
-    if constexpr (DT == ROPE_DTYPE_BF16) return Numbers{vector_constant(0x00780078u), vector_constant(0x41C041C0u)};
-    else return Numbers{vector_constant(0x03C003C0u), vector_constant(0x4E004E00u)};
+    if constexpr (DT == ROPE_DTYPE_BF16) return Numbers{scalar_constant(0x00780078u), vector_constant(0x41C041C0u)};
+    else return Numbers{scalar_constant(0x03C003C0u), vector_constant(0x4E004E00u)};
 }
 
 template <int DT>
@@ -107,8 +114,8 @@ struct VConstants {
 };
 __device__ __forceinline__ VConstants v_constants()
 {
-    return VConstants{{vector_constant(0x000F000Fu), vector_constant(0x64086408u)},
-                      {vector_constant(0x00F000F0u), vector_constant(0x64806480u)}};
+    return VConstants{{scalar_constant(0x000F000Fu), vector_constant(0x64086408u)},
+                      {scalar_constant(0x00F000F0u), vector_constant(0x64806480u)}};
 }
 
 // The codes at nibble i of both halves of w.
@@ -217,7 +224,7 @@ struct AttnRows {
     static constexpr int NGV = VF ? DVP / 32 : 1;
 
     v4u q[NT][KW];
-    f32x4 start[NT][KF ? KW : 1];
+    float start[NT][KF ? KW : 1];                  // -24 sum(q)
     int32_t last[NT];                              // the last token that a row sees
     f32x4 acc[NT][VT];
     float m[NT], less[NT], l[NT], top[NT][NGV];    // less: m, or 0 where there is none yet
@@ -247,8 +254,7 @@ struct AttnRows {
                 for (int k = 0; k < 8; ++k) sum += f.v[k];
                 q[t][st] = q_order(v);
                 if (KF || st == KW - 1) {
-                    const float c = -24.0f * column_sum(sum);
-                    start[t][KF ? st : 0] = f32x4{c, c, c, c};
+                    start[t][KF ? st : 0] = -24.0f * column_sum(sum);
                     sum = 0.0f;
                 }
             }
@@ -274,32 +280,52 @@ struct AttnRows {
     template <bool HOLD, class F>
     __device__ __forceinline__ void scores(f32x4 (&x)[NT][4], const F& k_numbers_of, const float (*ks)[64], uint32_t kq)
     {
-        f32x4 scale[4];
-        if constexpr (!KF) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) scale[i] = *reinterpret_cast<const f32x4*>(&ks[0][16 * i + 4 * kq]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        scores<HOLD>(x, k_numbers_of, ks, kq, [&](int t, int st) { return start[t][st]; });
+    }
+    // start_of: where the start's numbers are kept
+    template <bool HOLD, class F, class G>
+    __device__ __forceinline__ void scores(f32x4 (&x)[NT][4], const F& k_numbers_of, const float (*ks)[64], uint32_t kq,
+                                           const G& start_of)
+    {
+        if constexpr (KF) {
 #pragma unroll
             for (int st = 0; st < KW; ++st) {
-                const v4u k = k_numbers_of(i, st);
-                if constexpr (KF) {
+                f32x4 c[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float one = start_of(t, st);
+                    if (HOLD) asm volatile("" : "+v"(one));        // made here, not kept as four
+                    c[t] = f32x4{one, one, one, one};
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const v4u k = k_numbers_of(i, st);
                     const f32x4 s = *reinterpret_cast<const f32x4*>(&ks[st][16 * i + 4 * kq]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const f32x4 d = attn_mfma<DT>(k, q[t][st], start[t][st]);
+                        const f32x4 d = attn_mfma<DT>(k, q[t][st], c[t]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(d[r], s[r], st == 0 ? -less[t] : x[t][i][r]);
                     }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) x[t][i] = attn_mfma<DT>(k, q[t][st], st == 0 ? start[t][0] : x[t][i]);
+                    if (HOLD && (i & 1)) __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            if (HOLD) __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (!KF) {
+        } else {
+            f32x4 scale[4], c[NT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scale[i] = *reinterpret_cast<const f32x4*>(&ks[0][16 * i + 4 * kq]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) c[t] = f32x4{start_of(t, 0), start_of(t, 0), start_of(t, 0), start_of(t, 0)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int st = 0; st < KW; ++st) {
+                    const v4u k = k_numbers_of(i, st);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) x[t][i] = attn_mfma<DT>(k, q[t][st], st == 0 ? c[t] : x[t][i]);
+                }
+                if (HOLD) __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -374,6 +400,13 @@ struct AttnRows {
     __device__ __forceinline__ void add(const f32x4 (&x)[NT][4], const float (&keep)[NT], const bool (&moved)[NT], const F& v_numbers_of,
                                         const float (*vs)[64], uint32_t kq, uint32_t lane)
     {
+        add<HOLD>(x, keep, moved, v_numbers_of, vs, kq, lane, [&](int t, int g) -> float& { return top[t][g]; });
+    }
+    // top_of: where the largest weights are kept
+    template <bool HOLD, class F, class G>
+    __device__ __forceinline__ void add(const f32x4 (&x)[NT][4], const float (&keep)[NT], const bool (&moved)[NT], const F& v_numbers_of,
+                                        const float (*vs)[64], uint32_t kq, uint32_t lane, const G& top_of)
+    {
 #pragma unroll
         for (int g = 0; g < NGV; ++g) {
             constexpr int T = VT / NGV;            // products of a segment
@@ -394,9 +427,10 @@ struct AttnRows {
                         const f32x4 w = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
                         high = max3_abs(max3_abs(high, w[0], w[1]), w[2], w[3]);
                     }
-                    top[t][g] = fmaxf(top[t][g] * keep[t], column_max(high));
-                    int32_t now = __builtin_amdgcn_frexp_expf(top[t][g]);
-                    now = top[t][g] > 0.0f ? min(max(now, -120), 120) : e[t][g];
+                    high = fmaxf(top_of(t, g) * keep[t], column_max(high));
+                    top_of(t, g) = high;
+                    int32_t now = __builtin_amdgcn_frexp_expf(high);
+                    now = high > 0.0f ? min(max(now, -120), 120) : e[t][g];
                     const float f = __builtin_ldexpf(keep[t], e[t][g] - now);
                     e[t][g] = now;
                     least = min(least, now);
@@ -507,6 +541,14 @@ __device__ __forceinline__ const gchar* attn_group_at(const AttnPlace& p, int i,
 __device__ __forceinline__ uint32_t attn_offset(uint32_t v)
 {
     asm volatile("" : "+v"(v));
+    return v;
+}
+
+// This lane's number, made anew: a register less over a loop.
+__device__ __forceinline__ uint32_t attn_lane()
+{
+    uint32_t v;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(v));
     return v;
 }
 
@@ -987,26 +1029,29 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
 // that neither K's reads (the same piece of 16 tokens) nor V's (four pieces of
 // four tokens) meet in a bank. Two buffers of 17 or 35 KB; one barrier a tile.
 // ---------------------------------------------------------------------------
-template <int DP>
+template <int DP, bool KF, bool VF, int NT>
 struct alignas(16) AttnHeadsLds {
     static constexpr int kRow = 2 * DP;            // bytes of a token's four rows
+    static constexpr bool kScales = !KF && !VF;    // one a row: they come with the codes
+    static constexpr int NGK = KF ? DP / 32 : 1, NGV = VF ? DP / 32 : 1;
     struct Tile {
         char k[64 * kRow], v[64 * kRow];
-        float ks[64][4], vs[64][4];
+        float ks[kScales ? 64 : 1][4], vs[kScales ? 64 : 1][4];
     };
     Tile tile[2];
     struct Wave {
-        float ks[1][64], vs[1][64];
+        float ks[NGK][64], vs[NGV][64];
+        float start[NT][NGK][16], top[NT][NGV][16];        // the rows', where registers are short
     };
     Wave wave[4];
 };
 
-template <int DT, int DP>
+template <int DT, int DP, bool KF, bool VF, int NT>
 __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
 {
-    using Lds = AttnHeadsLds<DP>;
-    using R = AttnRows<DT, DP, DP, false, false, 1>;
-    constexpr int KW = R::KW;
+    using Lds = AttnHeadsLds<DP, KF, VF, NT>;
+    using R = AttnRows<DT, DP, DP, KF, VF, NT>;
+    constexpr int KW = R::KW, NGK = Lds::NGK, NGV = Lds::NGV;
     constexpr uint32_t kPieces = Lds::kRow / 16;   // of a token
     constexpr uint32_t kTokens = 64 / kPieces;     // of a load
     constexpr int kLoads = 16 / kTokens;           // of 16 tokens
@@ -1016,54 +1061,75 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AttnAt at = attn_at(a, blockIdx.x);
     const AttnSeq seq = attn_seq(a, at.b);
-    const uint32_t head0 = at.head * 4, r0 = at.tile * 16;
+    const uint32_t head0 = at.head * 4, head = head0 + wave, r0 = at.tile * 16 * NT;
     const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
     if (r0 >= live) return;                        // the same for the whole block
-    const AttnSpan span = attn_span(a, seq, r0, min(r0 + 16, live));
+    const AttnSpan span = attn_span(a, seq, r0, min(r0 + 16 * NT, live));
     uint32_t from, to;
     attn_part(span.some, at.split, a.splits, 64, &from, &to);
     const uint32_t all = min(span.all, to);
     R rows;
-    rows.load(a, seq, at.b, head0 + wave, r0, live, n16, kq);
+    rows.load(a, seq, at.b, head, r0, live, n16, kq);
 
     const gchar* const k_base = as_global(a.kc.data) + head0 * a.kc.st[2];
     const gchar* const v_base = as_global(a.vc.data) + head0 * a.vc.st[2];
+    const gchar* const ks_base = as_global(a.kc.scales) + (Lds::kScales ? head0 : head) * a.kc.sc[2] * 4;
+    const gchar* const vs_base = as_global(a.vc.scales) + (Lds::kScales ? head0 : head) * a.vc.sc[2] * 4;
     const int32_t* const table = a.table + at.b * a.table_stride;
+    const uint32_t sel1 = (lane & 1) ? 0x03070105u : 0x06020400u;
+    const uint32_t sel2 = (lane & 2) ? 0x03020706u : 0x05040100u;
     const uint32_t lds_base = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) Lds*)&lds);
     // a load's lanes: token lane / pieces of its kTokens, piece lane % pieces in
     // its turned order
-    uint32_t k_off[kLoads], v_off[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const uint32_t tok = i * kTokens + lane / kPieces, piece = (lane % kPieces) ^ (tok % kPieces);
-        k_off[i] = tok * (uint32_t)a.kc.st[1] + 16 * piece;
-        v_off[i] = tok * (uint32_t)a.vc.st[1] + 16 * piece;
-    }
-    // this wave's quarter of a tile: 16 tokens of K and V; the first two waves
-    // also the scales
+    const uint32_t tok0 = lane / kPieces, piece0 = 16 * ((lane % kPieces) ^ tok0);
+    const uint32_t k_tok = tok0 * (uint32_t)a.kc.st[1], v_tok = tok0 * (uint32_t)a.vc.st[1];
+    float ks[NGK], vs[NGV];
+    // this wave's quarter of a tile: 16 tokens of K and V. Scales: of all rows by
+    // the first two waves, or a lane's token's of this wave's head
     const auto issue = [&](const AttnPlace& p, uint32_t buffer) {
+        const int64_t page = p.page, in_page = p.in_page;
+        const gchar* sk = ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1]) * 4;
+        const gchar* sv = vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1]) * 4;
+        if constexpr (!Lds::kScales) {
+#pragma unroll
+            for (int g = 0; g < NGK; ++g) {
+                const uint32_t at_g = KF ? min((uint32_t)g * 32 / a.k_group, a.k_groups - 1) : 0;
+                ks[g] = p.there ? gload<float>(sk + at_g * 4) : 0.0f;
+            }
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) {
+                const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
+                vs[g] = p.there ? gload<float>(sv + at_g * 4) : 0.0f;
+            }
+        }
         const gchar* k_row = attn_group_at(p, wave, k_base, a.kc);
         const gchar* v_row = attn_group_at(p, wave, v_base, a.vc);
         const uint32_t to_tile = lds_base + (uint32_t)offsetof(Lds, tile) + buffer * (uint32_t)sizeof(typename Lds::Tile);
         const uint32_t mine = to_tile + wave * 16 * Lds::kRow;
+        const auto load = [&](const gchar* row, int64_t step, uint32_t tok, uint32_t to_codes) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            lds_dma16((const void*)k_row, k_off[i], mine + (uint32_t)offsetof(typename Lds::Tile, k) + 1024 * i);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            lds_dma16((const void*)v_row, v_off[i], mine + (uint32_t)offsetof(typename Lds::Tile, v) + 1024 * i);
-        const int64_t page = p.page, in_page = p.in_page;
-        if (wave == 0)
-            lds_dma16_far(a.kc.scales + (page * a.kc.sc[0] + in_page * a.kc.sc[1] + head0),
-                          to_tile + (uint32_t)offsetof(typename Lds::Tile, ks));
-        if (wave == 1)
-            lds_dma16_far(a.vc.scales + (page * a.vc.sc[0] + in_page * a.vc.sc[1] + head0),
-                          to_tile + (uint32_t)offsetof(typename Lds::Tile, vs));
+            for (int i = 0; i < kLoads; ++i)
+                lds_dma16((const void*)(row + (int64_t)(i * kTokens) * step),
+                          (attn_offset(piece0) ^ (16 * ((i * kTokens) % kPieces))) + tok, to_codes + 1024 * i);
+        };
+        load(k_row, a.kc.st[1], k_tok, mine + (uint32_t)offsetof(typename Lds::Tile, k));
+        load(v_row, a.vc.st[1], v_tok, mine + (uint32_t)offsetof(typename Lds::Tile, v));
+        if constexpr (Lds::kScales) {
+            if (wave == 0) lds_dma16_far((const void*)sk, to_tile + (uint32_t)offsetof(typename Lds::Tile, ks));
+            if (wave == 1) lds_dma16_far((const void*)sv, to_tile + (uint32_t)offsetof(typename Lds::Tile, vs));
+        }
     };
 
     const Numbers k_const = k_constants<DT>();
     const VConstants v_const = v_constants();
     typename Lds::Wave& my = lds.wave[wave];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) my.start[t][g][n16] = rows.start[t][g];
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) my.top[t][g][n16] = 0.0f;
+    }
     AttnPlace now = attn_look_up(a, table, from + lane, to);
     attn_settle(a, now);
     if (from < to) issue(now, 0);
@@ -1077,52 +1143,73 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
         asm volatile("" ::: "memory");
         const uint64_t valid = __ballot(now.there);
         const typename Lds::Tile& tile = lds.tile[buffer];
-        my.ks[0][lane] = now.there ? tile.ks[lane][wave] * a.scale2 : 0.0f;
-        my.vs[0][lane] = now.there ? tile.vs[lane][wave] : 0.0f;
+        if constexpr (Lds::kScales) {
+            my.ks[0][lane] = now.there ? tile.ks[lane][wave] * a.scale2 : 0.0f;
+            my.vs[0][lane] = now.there ? tile.vs[lane][wave] : 0.0f;
+        } else {
+#pragma unroll
+            for (int g = 0; g < NGK; ++g) my.ks[g][lane] = ks[g] * a.scale2;
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) my.vs[g][lane] = vs[g];
+        }
         attn_settle(a, next);
         if (to - base > 64) issue(next, buffer ^ 1);
-        const AttnPlace after = attn_look_up(a, table, (to - base > 128 ? base + 128 : to) + lane, to);
+        const AttnPlace after = attn_look_up(a, table, (to - base > 128 ? base + 128 : to) + attn_lane(), to);
         wave_sync();
-        uint32_t kw[4][KW];
+        // (KF: a word a step, where it is used)
+        const auto k_piece = [&](int i, uint32_t n) {
+            return tile.k + (16 * i + n16) * Lds::kRow + 16 * ((wave * (DP / 32) + n) ^ (n16 % kPieces));
+        };
+        uint32_t kw[4][KF ? 1 : KW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const char* row = tile.k + (16 * i + n16) * Lds::kRow;
-            if constexpr (KW == 4) {
-                const v4u w = *reinterpret_cast<const v4u*>(row + 16 * ((wave * 4 + kq) ^ n16));
+            if constexpr (KF) {
+            } else if constexpr (KW == 4) {
+                const v4u w = *reinterpret_cast<const v4u*>(k_piece(i, kq));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) kw[i][j] = w[j];
             } else {
-                const v2u w = *reinterpret_cast<const v2u*>(row + 16 * ((wave * 2 + (kq >> 1)) ^ (n16 & 7)) + 8 * (kq & 1));
+                const v2u w = *reinterpret_cast<const v2u*>(k_piece(i, kq >> 1) + 8 * (kq & 1));
                 kw[i][0] = w[0];
                 kw[i][1] = w[1];
             }
         }
-        f32x4 x[1][4];
-        rows.template scores<true>(x, [&](int i, int st) { return k_numbers<DT>(kw[i][st], k_const); }, my.ks, kq);
+        f32x4 x[NT][4];
+        rows.template scores<true>(x, [&](int i, int st) {
+            return k_numbers<DT>(KF ? *reinterpret_cast<const uint32_t*>(k_piece(i, st) + 4 * kq) : kw[i][KF ? 0 : st], k_const);
+        }, my.ks, kq, [&](int t, int st) { return my.start[t][st][n16]; });
         if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
-        float keep[1];
-        bool moved[1];
+        float keep[NT];
+        bool moved[NT];
         rows.weigh(x, keep, moved);
         // V's words, the codes of two tokens at equal nibbles of their halves
+        const uint32_t byte = attn_v_byte<DP, VF>(n16, 0, DP / 2);
         uint32_t two[2][DP / 64][4];
         const auto word = [&](uint32_t i) -> uint32_t {
-            const uint32_t tok = 16 * (i >> 2) + 4 * kq + (i & 3);
-            if constexpr (DP == 128) {
-                const uint32_t piece = (wave * 4 + (n16 >> 2)) ^ (4 * kq + (i & 3));
-                return *reinterpret_cast<const uint32_t*>(tile.v + tok * Lds::kRow + 16 * piece + 4 * (n16 & 3));
-            } else {
-                const uint32_t piece = (wave * 2 + (n16 >> 3)) ^ ((4 * kq + (i & 3)) & 7);
-                return *reinterpret_cast<const uint16_t*>(tile.v + tok * Lds::kRow + 16 * piece + 2 * (n16 & 7));
-            }
+            const uint32_t in16 = 4 * kq + (i & 3);
+            const char* at_v = tile.v + (16 * (i >> 2) + in16) * Lds::kRow +
+                               16 * ((wave * (DP / 32) + (byte >> 4)) ^ (in16 % kPieces)) + (byte & 15);
+            if constexpr (DP == 64) return *reinterpret_cast<const uint16_t*>(at_v);
+            else return *reinterpret_cast<const uint32_t*>(at_v);
         };
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t i = 8 * h + 4 * (j >> 1) + 2 * (j & 1), w0 = word(i), w1 = word(i + 1);
+                const uint32_t i = 8 * h + 4 * (j >> 1) + 2 * (j & 1);
+                uint32_t w0 = word(i), w1 = word(i + 1);
                 if constexpr (DP == 64) {
-                    two[h][0][j] = w0 | (w1 << 16);
+                    uint32_t w = w0 | (w1 << 16);
+                    if constexpr (VF) {
+                        const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0xB1, 0xF, 0xF, true);
+                        w = __builtin_amdgcn_perm(o, w, sel1);
+                    }
+                    two[h][0][j] = w;
                 } else {
+                    if constexpr (VF) {
+                        w0 = quad_bytes(w0, sel1, sel2);
+                        w1 = quad_bytes(w1, sel1, sel2);
+                    }
                     two[h][0][j] = __builtin_amdgcn_perm(w1, w0, 0x05040100);
                     two[h][1][j] = __builtin_amdgcn_perm(w1, w0, 0x07060302);
                 }
@@ -1136,12 +1223,12 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
                        (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
             }
             return v;
-        }, my.vs, kq, lane);
+        }, my.vs, kq, lane, [&](int t, int g) -> float& { return my.top[t][g][n16]; });
         now = next;
         next = after;
         buffer ^= 1;
     }
-    rows.store(a, at, head0 + wave, r0, live, n16, kq);
+    rows.store(a, at, head, r0, live, n16, kq);
 }
 
 }  // namespace

@@ -29,6 +29,16 @@ const void* attn_shared(int scales)
     }
 }
 
+template <int DT, int DP, int NT>
+const void* attn_heads(int scales)
+{
+    switch (scales) {
+    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, false, false, NT>);
+    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, true, false, NT>);
+    default: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, true, true, NT>);
+    }
+}
+
 template <int DT, int DP, bool P16>
 const void* attn_by_rows(int scales, AttnRowsOf rows)
 {
@@ -36,7 +46,10 @@ const void* attn_by_rows(int scales, AttnRowsOf rows)
     case AttnRowsOf::kOneTile: return attn_by_scales<DT, DP, P16, 1>(scales);
     case AttnRowsOf::kTwoTiles: return attn_by_scales<DT, DP, P16, 2>(scales);
     case AttnRowsOf::kFourHeads:
-        if constexpr (P16) return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP>);
+        if constexpr (P16) return attn_heads<DT, DP, 1>(scales);
+        return nullptr;
+    case AttnRowsOf::kFourHeadsTwoTiles:
+        if constexpr (P16) return attn_heads<DT, DP, 2>(scales);
         return nullptr;
     default: return attn_shared<DT, DP, P16>(scales);
     }
