@@ -142,3 +142,28 @@ def test_the_same_sequence_twice_and_pages_shared():
     got = call(c)
     check(got, c)
     assert torch.equal(got[0], got[1])
+
+
+@pytest.mark.parametrize("B, heads, S", [(2, 4, 1), (3, 1, 5), (65, 4, 1), (70, 2, 2), (130, 1, 1), (500, 1, 1), (900, 1, 1), (300, 4, 1)])
+@pytest.mark.parametrize("D, dtype", [(64, "bf16"), (80, "f32")])
+def test_sequences_of_all_lengths_are_split_alike(B, heads, S, D, dtype):
+    """One long sequence among short and empty ones, the long one at each end
+    and in the middle; a workspace of NaN of exactly the bytes asked for."""
+    for where in (0, B // 2, B - 1):
+        lengths = [(7 * b) % 41 for b in range(B)]
+        lengths[where] = 3000 if B < 100 else 700
+        c = inputs(lengths, S, 2 * heads, heads, D, D, D, D, 16, dtype, seed=39, cols=-(-lengths[where] // 16))
+        counts = torch.tensor([S if b == where or b % 3 else 0 for b in range(B)], dtype=torch.int32)
+        ws = torch.full((max(1, rp.rope_cache_attention_workspace(B, S, 2 * heads, heads, D)),), 255, dtype=torch.uint8, device="cuda")
+        got = call(c, counts=counts, workspace=ws)
+        check(got, c, counts=counts)
+        none = counts == 0
+        assert torch.equal(got.cpu()[none], c["out"][none])
+
+
+@pytest.mark.parametrize("lengths", [[0, 0, 0], [5000, 5000, 5000], [1, 8000, 1], [64, 128, 192], [8191, 63, 4097]])
+@pytest.mark.parametrize("S, heads, D", [(1, 4, 128), (3, 2, 64), (40, 1, 128)])
+def test_parts_of_equal_tokens(lengths, S, heads, D):
+    c = inputs(lengths, S, 2 * heads, heads, D, D, D, D, 16, "f16", seed=40, cols=512)
+    check(call(c), c)
+    check(call(c, causal=False), c, causal=False)

@@ -36,8 +36,14 @@ struct JoinMany {
     static const void* ptr() { return reinterpret_cast<const void*>(&rope_attn_join_many_kernel<DT>); }
 };
 
-// Parts up to which a wave joins a row.
-constexpr uint32_t kJoinFew = 8;
+// Whether waves join a row each, of up to kJoinFewParts parts: not where many
+// parts meet few rows. (16 parts of 3200 rows: 72 us a call of 16 sequences,
+// with a block a row and 32 lanes 135; 64 of 128, 4 sequences of up to 100000
+// tokens: 139 and 115.)
+bool join_few(const AttnArgs& a)
+{
+    return a.splits <= 32 || (a.splits <= 64 && (uint64_t)a.B * a.part_rows >= 512);
+}
 
 AttnArgs attn_args(const AttnPlan& p)
 {
@@ -66,10 +72,13 @@ AttnArgs attn_args(const AttnPlan& p)
     a.scale2 = (float)(p.scale * 1.4426950408889634);
     a.causal = p.causal ? 1 : 0;
     a.part = p.part;
-    a.part_rows = (uint64_t)p.B * (uint64_t)p.S * (uint64_t)p.q.N;
+    a.part_rows = (uint32_t)(p.S * p.q.N);
+    a.B = (uint32_t)p.B;
+    a.parts = a.splits == 1 ? 0 : a.B * a.splits;
+    a.most_parts = join_few(a) ? kJoinFewParts : kAttnMaxParts;
+    a.unit = kAttnGenThreads;
     a.rep_div = make_fastdiv(a.rep);
     a.heads_div = make_fastdiv(a.heads);
-    a.splits_div = make_fastdiv(a.splits);
     return a;
 }
 
@@ -125,7 +134,10 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     else if (a.heads % 4 == 0) a.head_waves = 4;
     else a.token_waves = a.heads % 2 == 0 ? 2 : 4;
     if (a.token_waves == 2) a.head_waves = 2;
-    if (mfma) a.heads_div = make_fastdiv(a.heads / a.head_waves);
+    if (mfma) {
+        a.heads_div = make_fastdiv(a.heads / a.head_waves);
+        a.unit = 64 * (a.row_waves > 1 ? 1 : a.token_waves);
+    }
     a.k_group = a.kc.group;
     a.v_group = a.vc.group;
     a.k_groups = a.D / a.k_group;
@@ -142,10 +154,11 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
                                      args, 0, s);
     if (err != hipSuccess || a.splits == 1) return launched(err);
     args[0] = &g;
-    if (a.splits > kJoinFew)       // (few rows, then)
-        return launched(hipLaunchKernel(by_type<JoinMany>(p.rope.dtype), dim3((uint32_t)a.part_rows, (a.Dv + kJoinLanes - 1) / kJoinLanes),
+    const uint64_t rows_of_all = (uint64_t)a.B * a.part_rows;
+    if (!join_few(a))
+        return launched(hipLaunchKernel(by_type<JoinMany>(p.rope.dtype), dim3((uint32_t)rows_of_all, (a.Dv + kJoinLanes - 1) / kJoinLanes),
                                         dim3(kJoinThreads), args, 0, s));
-    return launched(hipLaunchKernel(by_type<JoinFew>(p.rope.dtype), dim3((uint32_t)((a.part_rows + kJoinRows - 1) / kJoinRows)),
+    return launched(hipLaunchKernel(by_type<JoinFew>(p.rope.dtype), dim3((uint32_t)((rows_of_all + kJoinRows - 1) / kJoinRows)),
                                     dim3(kJoinThreads), args, 0, s));
 }
 

@@ -10,6 +10,8 @@
 // joined in order by a second kernel.
 #pragma once
 
+#include <type_traits>
+
 #include "rope_attn_plan.hpp"
 #include "rope_cache_kernels.hpp"
 
@@ -24,7 +26,10 @@ struct AttnArgs {
     uint32_t D, Dv, S, Hq, heads, rep;
     uint32_t rows;             // of a cached head: S * rep; row r is token r / rep, head r % rep of the group
     uint32_t tiles;            // of rows
-    uint32_t splits;
+    uint32_t splits;           // parts of a sequence's tokens, on average; 1: no parts
+    uint32_t B, parts;         // of all sequences: B * splits
+    uint32_t most_parts;       // of one sequence
+    uint32_t unit;             // tokens that a part is whole multiples of
     const int32_t* table;
     int64_t table_stride;
     const int32_t* lengths;
@@ -34,29 +39,18 @@ struct AttnArgs {
     int32_t most;              // tokens that a block table holds
     float scale2;              // scale * log2(e)
     int32_t causal;
-    float* part;               // per part, sequence, token and head: Dv sums; then m and l of all
-    uint64_t part_rows;        // B * S * Hq
-    FastDiv rep_div, heads_div, tiles_div, splits_div, page_div;
+    float* part;               // per part, token and head: Dv sums; then m and l of all
+    uint32_t part_rows;        // of a part: S * Hq
+    FastDiv rep_div, heads_div, tiles_div, page_div;
 };
 
-// A block's place: cached head (or group of heads), tile of rows, part, sequence,
-// the first changing fastest: heads lie beside each other in memory, and what
-// blocks read at the same time should too.
+// A block's place: cached head (or group of heads), tile of rows, part, the
+// first changing fastest: heads lie beside each other in memory, and what blocks
+// read at the same time should too.
 struct AttnAt {
-    uint32_t split, tile, head, b;
+    uint32_t part, tile, head, b;
+    uint32_t first, end;       // the part's tokens, as many as there are
 };
-
-__device__ __forceinline__ AttnAt attn_at(const AttnArgs& a, uint32_t block)
-{
-    AttnAt p;
-    const uint32_t i = fast_div(block, a.heads_div);
-    p.head = block - i * a.heads_div.d;
-    const uint32_t j = fast_div(i, a.tiles_div);
-    p.tile = i - j * a.tiles;
-    p.b = fast_div(j, a.splits_div);
-    p.split = j - p.b * a.splits;
-    return p;
-}
 
 // A sequence: its cached tokens, its new ones, and the place of the first.
 struct AttnSeq {
@@ -76,23 +70,132 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, uint32_t b)
     return s;
 }
 
-// The tokens [*t0, *t1) of part `split` of `splits` of n tokens, in whole units.
-__device__ __forceinline__ void attn_part(uint32_t n, uint32_t split, uint32_t splits, uint32_t unit, uint32_t* t0, uint32_t* t1)
+// Sums of the lanes up to each one, and the largest of all lanes.
+__device__ __forceinline__ uint32_t lanes_up_to(uint32_t v)
 {
-    const uint32_t units = (n + unit - 1) / unit, per = (units + splits - 1) / splits;
-    *t0 = (uint32_t)min((uint64_t)n, (uint64_t)split * per * unit);
-    *t1 = (uint32_t)min((uint64_t)n, ((uint64_t)split + 1) * per * unit);
+    const auto from = [&](auto ctrl, auto rows) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+    };
+    using All = std::integral_constant<int, 0xF>;
+    v += from(std::integral_constant<int, 0x111>{}, All{});        // lanes of 16: 1, 2, 4, 8 before
+    v += from(std::integral_constant<int, 0x112>{}, All{});
+    v += from(std::integral_constant<int, 0x114>{}, All{});
+    v += from(std::integral_constant<int, 0x118>{}, All{});
+    v += from(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+    v += from(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+    return v;
+}
+__device__ __forceinline__ uint32_t lanes_sum(uint32_t v) { return __builtin_amdgcn_readlane((int)lanes_up_to(v), 63); }
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+    return __builtin_amdgcn_readfirstlane((int)v);
 }
 
-// The partial result of (part, sequence, token, head).
-__device__ __forceinline__ uint64_t part_row(const AttnArgs& a, uint32_t split, uint32_t b, uint32_t s, uint32_t h)
+// Sequences are split into parts of the same number of tokens, whatever each
+// one's length, so that blocks end together: a.parts of them at most, which is
+// all the host can know. Every wave finds out for itself (and so do those that
+// join), from the lengths: the smallest part, within 1/16, that makes no more.
+// 16 sequences of 500 to 8000 tokens by 16 parts each: 91 us, so 55.
+struct AttnShare {
+    uint32_t b, first, n;      // a sequence, its first part and how many
+    uint32_t per;              // units of a part
+};
+constexpr int kAttnBatch = kAttnBlocks / 2 / 64;   // 64 sequences each: more are not split
+
+// Of the sequence that part `key` belongs to (b = a.B: of none), or of sequence
+// `key` itself.
+template <bool PART>
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, uint32_t key)
 {
-    return (uint64_t)split * a.part_rows + ((uint64_t)b * a.S + s) * a.Hq + h;
+    if (a.B == 1) {                                // (the same without the sums)
+        const AttnSeq seq = attn_seq(a, 0);
+        const uint32_t units = seq.count > 0 ? ((uint32_t)seq.tokens + a.unit - 1) / a.unit : 0, parts = min(a.parts, a.most_parts);
+        const uint32_t per = max(1u, (units + parts - 1) / parts), n = (units + per - 1) / per;
+        return AttnShare{PART && key >= n, 0, n, per};
+    }
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t u[kAttnBatch], high = 0, low = 0, most = 0;
+#pragma unroll
+    for (int c = 0; c < kAttnBatch; ++c) {
+        u[c] = 0;
+        if (c * 64 >= a.B) continue;
+        const uint32_t b = c * 64 + lane;
+        if (b < a.B) {
+            const AttnSeq seq = attn_seq(a, b);
+            u[c] = seq.count > 0 ? ((uint32_t)seq.tokens + a.unit - 1) / a.unit : 0;
+        }
+        high += u[c] >> 10;
+        low += u[c] & 1023;
+        most = max(most, u[c]);
+    }
+    high = lanes_sum(high);
+    low = lanes_sum(low);
+    most = lanes_max(most);
+    AttnShare s{a.B, 0, 0, 0};
+    s.per = max(max(1u, (most + a.most_parts - 1) / a.most_parts),
+                high / a.parts * 1024 + (high % a.parts * 1024 + low) / a.parts);
+    for (;; s.per += max(1u, s.per / 16)) {        // (ends: one part each is B, of no more than a.parts)
+        uint32_t n = 0;
+#pragma unroll
+        for (int c = 0; c < kAttnBatch; ++c)
+            if (c * 64 < a.B) n += (u[c] + s.per - 1) / s.per;
+        if (lanes_sum(n) <= a.parts) break;
+    }
+#pragma unroll
+    for (int c = 0; c < kAttnBatch; ++c) {
+        if (c * 64 >= a.B || s.b != a.B) continue;
+        const uint32_t n = (u[c] + s.per - 1) / s.per, up_to = lanes_up_to(n);
+        const uint64_t hit = PART ? __ballot(s.first + up_to > key) : key / 64 == (uint32_t)c ? 1ull << (key & 63) : 0;
+        if (hit != 0) {
+            const int at = __builtin_ctzll(hit);
+            s.b = c * 64 + at;
+            s.n = __builtin_amdgcn_readlane((int)n, at);
+            s.first += __builtin_amdgcn_readlane((int)up_to, at) - s.n;
+        } else {
+            s.first += __builtin_amdgcn_readlane((int)up_to, 63);
+        }
+    }
+    return s;
+}
+
+// False: nothing to do.
+__device__ __forceinline__ bool attn_at(const AttnArgs& a, uint32_t block, AttnAt* p)
+{
+    const uint32_t i = fast_div(block, a.heads_div);
+    p->head = block - i * a.heads_div.d;
+    p->part = fast_div(i, a.tiles_div);
+    p->tile = i - p->part * a.tiles;
+    p->b = p->part;
+    p->first = 0;
+    p->end = UINT32_MAX;
+    if (a.splits == 1) return true;
+    const AttnShare s = attn_share<true>(a, p->part);
+    if (s.b == a.B) return false;
+    p->b = s.b;
+    // (tokens are fewer than 2^31)
+    p->first = (uint32_t)min((uint64_t)INT32_MAX, (uint64_t)(p->part - s.first) * s.per * a.unit);
+    p->end = (uint32_t)min((uint64_t)INT32_MAX, (uint64_t)(p->part - s.first + 1) * s.per * a.unit);
+    return true;
+}
+
+// The tokens [*t0, *t1) of a part that are among the first n.
+__device__ __forceinline__ void attn_part(const AttnAt& at, uint32_t n, uint32_t* t0, uint32_t* t1)
+{
+    *t0 = min(at.first, n);
+    *t1 = min(at.end, n);
+}
+
+// The partial result of (part, token, head).
+__device__ __forceinline__ uint64_t part_row(const AttnArgs& a, uint32_t part, uint32_t s, uint32_t h)
+{
+    return (uint64_t)part * a.part_rows + (uint64_t)s * a.Hq + h;
 }
 
 __device__ __forceinline__ float2* part_stats(const AttnArgs& a)
 {
-    return reinterpret_cast<float2*>(a.part + (uint64_t)a.splits * a.part_rows * a.Dv);
+    return reinterpret_cast<float2*>(a.part + (uint64_t)a.parts * a.part_rows * a.Dv);
 }
 
 // How much a part counts whose maximum is m.
@@ -119,7 +222,8 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
     __shared__ int64_t v_at[kAttnGenThreads], vs_at[kAttnGenThreads];
     __shared__ float red[kAttnGenRows][kAttnGenThreads / 64];
     const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const AttnAt at = attn_at(a, blockIdx.x);
+    AttnAt at;
+    if (!attn_at(a, blockIdx.x, &at)) return;    // the same for the whole block
     const AttnSeq seq = attn_seq(a, at.b);
     const uint32_t r0 = at.tile * kAttnGenRows;
     const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
@@ -139,7 +243,7 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
         last[r] = a.causal ? seq.first + fast_div(min(r0 + r, a.rows - 1), a.rep_div) : INT64_MAX;
     }
     uint32_t from, to;
-    attn_part((uint32_t)seq.tokens, at.split, a.splits, kAttnGenThreads, &from, &to);
+    attn_part(at, (uint32_t)seq.tokens, &from, &to);
     __syncthreads();
     for (uint32_t base = from; base < to; base += kAttnGenThreads) {
         const uint32_t tok = base + t;
@@ -214,7 +318,7 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
         for (int w = 0; w < kAttnGenThreads / 64; ++w) sum += red[r][w];
         const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
         const float inv = one_over(sum);
-        const uint64_t row = part_row(a, at.split, at.b, s, h);
+        const uint64_t row = part_row(a, at.part, s, h);
         for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
             const uint32_t j = k * kAttnGenThreads + t;
             if (j >= a.Dv) continue;
@@ -233,41 +337,43 @@ constexpr int kJoinThreads = 512;
 constexpr int kJoinRows = kJoinThreads / 64;       // of a block, with few parts
 constexpr int kJoinLanes = 32;                     // of a block, with many
 constexpr int kJoinAhead = 4;                      // parts whose loads go out together
+constexpr int kJoinFewParts = 64;                  // of a sequence at most, where waves join rows
 
 template <int DT>
 __global__ void __launch_bounds__(kJoinThreads) rope_attn_join_few_kernel(AttnArgs a)
 {
     const uint32_t lane = threadIdx.x & 63;
-    const uint64_t row64 = (uint64_t)blockIdx.x * kJoinRows + (threadIdx.x >> 6);
-    if (row64 >= a.part_rows) return;
-    const uint32_t row = (uint32_t)row64;
-    const uint32_t tok = row / a.Hq, h = row - tok * a.Hq, b = tok / a.S, s = tok - b * a.S;
-    if ((int32_t)s >= attn_seq(a, b).count) return;
-    const float2* stats = part_stats(a) + row;
-    const int64_t out = b * a.out.sb + s * a.out.ss + h * a.out.sn;
-    const uint64_t step = a.part_rows * a.Dv;
-    float m = kAttnNone, l = 0.0f;
-    for (uint32_t i = 0; i < a.splits; ++i) m = fmaxf(m, stats[i * a.part_rows].x);
-    for (uint32_t i = 0; i < a.splits; ++i) {
-        const float2 st = stats[i * a.part_rows];
-        l = __builtin_fmaf(st.y, part_weight(st.x, m), l);
-    }
+    const uint32_t row = blockIdx.x * kJoinRows + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t b = row / a.part_rows, sh = row - b * a.part_rows;
+    const uint32_t s = sh / a.Hq, h = sh - s * a.Hq;
+    if (b >= a.B || (int32_t)s >= attn_seq(a, b).count) return;
+    const AttnShare share = attn_share<false>(a, b);
+    const uint64_t at = (uint64_t)share.first * a.part_rows + sh;
+    // a lane a part: the maximum and the sum
+    const float2 st = lane < share.n ? part_stats(a)[at + (uint64_t)lane * a.part_rows] : make_float2(kAttnNone, 0.0f);
+    float m = st.x;
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float weight = part_weight(st.x, m);
+    float l = lane < share.n ? st.y * weight : 0.0f;
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
     const float inv = one_over(l);
+    const int64_t out = b * a.out.sb + s * a.out.ss + h * a.out.sn;
+    const uint64_t step = (uint64_t)a.part_rows * a.Dv;
     for (uint32_t j = 2 * lane; j < a.Dv; j += 128) {          // (Dv is even)
-        const float* part = a.part + (uint64_t)row * a.Dv + j;
+        const float* part = a.part + at * a.Dv + j;
         float o[2] = {};
-        for (uint32_t i = 0; i < a.splits; i += kJoinAhead) {
+        for (uint32_t i = 0; i < share.n; i += kJoinAhead) {
             float2 v[kJoinAhead];
             float w[kJoinAhead];
 #pragma unroll
             for (int k = 0; k < kJoinAhead; ++k) {
-                const uint32_t at = min(i + k, a.splits - 1);
-                v[k] = *reinterpret_cast<const float2*>(part + at * step);
-                w[k] = part_weight(stats[at * a.part_rows].x, m);
+                const uint32_t one = min(i + k, share.n - 1);
+                v[k] = *reinterpret_cast<const float2*>(part + one * step);
+                w[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), (int)one));
             }
 #pragma unroll
             for (int k = 0; k < kJoinAhead; ++k)
-                if (i + k < a.splits && w[k] != 0.0f) {
+                if (i + k < share.n && w[k] != 0.0f) {
                     o[0] = __builtin_fmaf(v[k].x, w[k], o[0]);
                     o[1] = __builtin_fmaf(v[k].y, w[k], o[1]);
                 }
@@ -284,9 +390,11 @@ __global__ void __launch_bounds__(kJoinThreads) rope_attn_join_many_kernel(AttnA
     __shared__ float weight[kAttnMaxParts];
     __shared__ float sums[kStrandsOf][kJoinLanes];
     const uint32_t t = threadIdx.x, lane = t & 63;
-    const uint32_t row = blockIdx.x, j = blockIdx.y * kJoinLanes + (t & (kJoinLanes - 1)), strand = t / kJoinLanes;
-    const uint32_t tok = row / a.Hq, h = row - tok * a.Hq, b = tok / a.S, s = tok - b * a.S;
+    const uint32_t b = blockIdx.x / a.part_rows, sh = blockIdx.x - b * a.part_rows, j = blockIdx.y * kJoinLanes + (t & (kJoinLanes - 1)), strand = t / kJoinLanes;
+    const uint32_t s = sh / a.Hq, h = sh - s * a.Hq;
     if ((int32_t)s >= attn_seq(a, b).count) return;
+    const AttnShare share = attn_share<false>(a, b);
+    const uint64_t row = (uint64_t)share.first * a.part_rows + sh;
     const float2* stats = part_stats(a) + row;
     // every wave for itself: the parts' maximum and sum
     float m = kAttnNone, l = 0.0f;
@@ -294,14 +402,14 @@ __global__ void __launch_bounds__(kJoinThreads) rope_attn_join_many_kernel(AttnA
 #pragma unroll
     for (int k = 0; k < kAttnMaxParts / 64; ++k) {
         const uint32_t i = k * 64 + lane;
-        st[k] = i < a.splits ? stats[i * a.part_rows] : make_float2(kAttnNone, 0.0f);
+        st[k] = i < share.n ? stats[(uint64_t)i * a.part_rows] : make_float2(kAttnNone, 0.0f);
         m = fmaxf(m, st[k].x);
     }
     for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
 #pragma unroll
     for (int k = 0; k < kAttnMaxParts / 64; ++k) {
         const float w = part_weight(st[k].x, m);
-        if (k * 64 + lane < a.splits) {
+        if (k * 64 + lane < share.n) {
             l = __builtin_fmaf(st[k].y, w, l);
             if (t < 64) weight[k * 64 + lane] = w;
         }
@@ -309,16 +417,16 @@ __global__ void __launch_bounds__(kJoinThreads) rope_attn_join_many_kernel(AttnA
     for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
     __syncthreads();
     float o = 0.0f;
-    const uint64_t step = a.part_rows * a.Dv;
-    const float* part = a.part + (uint64_t)row * a.Dv + min(j, a.Dv - 1);
-    for (uint32_t i = strand; i < a.splits; i += kStrandsOf * kJoinAhead) {
+    const uint64_t step = (uint64_t)a.part_rows * a.Dv;
+    const float* part = a.part + row * a.Dv + min(j, a.Dv - 1);
+    for (uint32_t i = strand; i < share.n; i += kStrandsOf * kJoinAhead) {
         float v[kJoinAhead];
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) v[k] = part[min(i + k * kStrandsOf, a.splits - 1) * step];
+        for (int k = 0; k < kJoinAhead; ++k) v[k] = part[min(i + k * kStrandsOf, share.n - 1) * step];
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) {
             const uint32_t at = i + k * kStrandsOf;
-            if (at < a.splits && weight[at] != 0.0f) o = __builtin_fmaf(v[k], weight[at], o);
+            if (at < share.n && weight[at] != 0.0f) o = __builtin_fmaf(v[k], weight[at], o);
         }
     }
     sums[strand][t & (kJoinLanes - 1)] = o;

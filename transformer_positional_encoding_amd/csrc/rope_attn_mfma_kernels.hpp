@@ -483,7 +483,7 @@ struct AttnRows {
             if (r >= live) continue;
             const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
             const float inv = a.splits > 1 ? 1.0f : one_over(sum);
-            const uint64_t row = part_row(a, at.split, at.b, s, h);
+            const uint64_t row = part_row(a, at.part, s, h);
             gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
 #pragma unroll
             for (int c = 0; c < VT / 2; ++c) {     // 8 consecutive lanes
@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     typename Lds::Wave& my = lds.wave[wave];
 
-    const AttnAt at = attn_at(a, blockIdx.x);
+    AttnAt at;
+    if (!attn_at(a, blockIdx.x, &at)) return;      // the same for the whole block
     const AttnSeq seq = attn_seq(a, at.b);
     const uint32_t head_wave = wave & (a.head_waves - 1), token_wave = a.row_waves > 1 ? 0 : wave / a.head_waves;
     const uint32_t head = at.head * a.head_waves + head_wave, waves = a.token_waves;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
     if (r0 >= live) return;                        // where waves are joined the same for the whole block
     const AttnSpan span = attn_span(a, seq, r0, min(r0 + 16 * NT, live));
     uint32_t from, to;
-    attn_part(span.some, at.split, a.splits, 64 * waves, &from, &to);
+    attn_part(at, span.some, &from, &to);
     const uint32_t all = min(span.all, to);
     R rows;
     rows.load(a, seq, at.b, head, r0, live, n16, kq);
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
             }
             const uint32_t h = (at.head * a.head_waves + hw) * a.rep + (r - s * a.rep);
             const float inv = a.splits > 1 ? 1.0f : one_over(whole);
-            const uint64_t row = part_row(a, at.split, at.b, s, h);
+            const uint64_t row = part_row(a, at.part, s, h);
             gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
             for (uint32_t j = 8 * (threadIdx.x & 15); j < a.Dv && r < live; j += 128) {
                 float v[8] = {};
@@ -866,14 +867,15 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
     __shared__ Lds lds;
     const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    AttnAt at = attn_at(a, blockIdx.x);
+    AttnAt at;
+    if (!attn_at(a, blockIdx.x, &at)) return;      // the same for the whole block
     at.tile = a.tiles - 1 - at.tile;               // those that see the most tokens first
     const AttnSeq seq = attn_seq(a, at.b);
     const uint32_t block_row = at.tile * (64 * NT), r0 = block_row + wave * (16 * NT);
     const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
     if (block_row >= live) return;                 // the same for the whole block
     uint32_t from, to;
-    attn_part(attn_span(a, seq, block_row, min(block_row + 64 * NT, live)).some, at.split, a.splits, 64, &from, &to);
+    attn_part(at, attn_span(a, seq, block_row, min(block_row + 64 * NT, live)).some, &from, &to);
     // (a wave without rows makes numbers only)
     const AttnSpan span = r0 < live ? attn_span(a, seq, r0, min(r0 + 16 * NT, live)) : AttnSpan{0, 0};
     const uint32_t all = min(span.all, to), some = min(span.some, to);
@@ -1059,14 +1061,15 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
     __shared__ Lds lds;
     const uint32_t lane = threadIdx.x & 63, n16 = lane & 15, kq = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const AttnAt at = attn_at(a, blockIdx.x);
+    AttnAt at;
+    if (!attn_at(a, blockIdx.x, &at)) return;      // the same for the whole block
     const AttnSeq seq = attn_seq(a, at.b);
     const uint32_t head0 = at.head * 4, head = head0 + wave, r0 = at.tile * 16 * NT;
     const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
     if (r0 >= live) return;                        // the same for the whole block
     const AttnSpan span = attn_span(a, seq, r0, min(r0 + 16 * NT, live));
     uint32_t from, to;
-    attn_part(span.some, at.split, a.splits, 64, &from, &to);
+    attn_part(at, span.some, &from, &to);
     const uint32_t all = min(span.all, to);
     R rows;
     rows.load(a, seq, at.b, head, r0, live, n16, kq);

@@ -10,19 +10,14 @@ namespace rope {
 namespace {
 
 constexpr int64_t kI64Max = std::numeric_limits<int64_t>::max();
-// Blocks that fill the card several times over, and the fewest tokens that
-// are worth a block of their own.
-constexpr int64_t kAttnBlocks = 2048;
+// The fewest tokens that are worth a part of their own.
 constexpr int64_t kAttnSplitTokens = 64;
-// Rows of a tile: the partial results of a call are B * heads * tiles * 16 at
-// most for each part.
-constexpr int64_t kAttnTileRows = 16;
 
 }  // namespace
 
 int64_t attn_splits(int64_t B, int64_t heads, int64_t rows, int64_t tokens)
 {
-    const int64_t tiles = (rows + kAttnTileRows - 1) / kAttnTileRows;
+    const int64_t tiles = rows <= 16 ? 1 : (rows + 31) / 32;       // a wave's
     const int64_t base = std::max<int64_t>(1, B * heads * tiles);
     const int64_t want = std::min(kAttnMaxParts, kAttnBlocks / base);
     return std::max<int64_t>(1, std::min(want, tokens / kAttnSplitTokens));

@@ -6,7 +6,9 @@
 
 namespace rope {
 
-// Most parts that a sequence's tokens are divided into.
+// Parts of all sequences, by heads and tiles of rows, that fill the card; most
+// that one sequence's tokens are divided into.
+constexpr int64_t kAttnBlocks = 2048;
 constexpr int64_t kAttnMaxParts = 512;
 
 struct AttnPlan {
@@ -25,12 +27,12 @@ struct AttnPlan {
     double scale = 0;
     bool causal = false;
     float* part = nullptr;         // partial results of the splits
-    int64_t splits = 1;            // parts that a sequence's tokens are divided into
+    int64_t splits = 1;            // parts that a sequence's tokens are divided into, on average
     bool noop = false;
 };
 
-// Parts for B x heads sequences of `rows` rows each over up to `tokens` cached
-// tokens.
+// Parts, on average, for B x heads sequences of `rows` rows each over up to
+// `tokens` cached tokens.
 int64_t attn_splits(int64_t B, int64_t heads, int64_t rows, int64_t tokens);
 
 // Bytes of workspace for any number of tokens; 0 when nothing is computed or
