@@ -42,7 +42,7 @@ struct JoinMany {
 // tokens: 139 and 115.)
 bool join_few(const AttnArgs& a)
 {
-    return a.splits <= 32 || (a.splits <= 64 && (uint64_t)a.B * a.part_rows >= 512);
+    return a.parts <= 32 * a.B || (a.parts <= 64 * a.B && (uint64_t)a.B * a.part_rows >= 512);
 }
 
 AttnArgs attn_args(const AttnPlan& p)
@@ -59,7 +59,6 @@ AttnArgs attn_args(const AttnPlan& p)
     a.heads = (uint32_t)p.heads;
     a.rep = (uint32_t)p.rep;
     a.rows = (uint32_t)(p.S * p.rep);
-    a.splits = (uint32_t)p.splits;
     a.table = p.table;
     a.table_stride = p.table_stride;
     a.lengths = p.lengths;
@@ -74,7 +73,8 @@ AttnArgs attn_args(const AttnPlan& p)
     a.part = p.part;
     a.part_rows = (uint32_t)(p.S * p.q.N);
     a.B = (uint32_t)p.B;
-    a.parts = a.splits == 1 ? 0 : a.B * a.splits;
+    a.parts = (uint32_t)p.parts;
+    a.split = a.parts > a.B;
     a.most_parts = join_few(a) ? kJoinFewParts : kAttnMaxParts;
     a.unit = kAttnGenThreads;
     a.rep_div = make_fastdiv(a.rep);
@@ -145,14 +145,14 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     const uint32_t block_rows = !mfma ? kAttnGenRows : (rows == AttnRowsOf::kOneTile ? 16 : 32) * a.row_waves;
     a.tiles = (a.rows + block_rows - 1) / block_rows;
     a.tiles_div = make_fastdiv(a.tiles);
-    const uint64_t blocks = (uint64_t)p.B * a.heads_div.d * a.tiles * a.splits;
+    const uint64_t blocks = (uint64_t)a.parts * a.heads_div.d * a.tiles;
     if (blocks >= (1ull << 31) || blocks > kMaxGridItems / kAttnGenThreads)
         return set_error(ROPE_ERR_UNSUPPORTED, "a grid too large for one launch");
     AttnArgs g = a;
     void* args[] = {mfma ? (void*)&a : (void*)&g};
     hipError_t err = hipLaunchKernel(mfma ? fn : by_type<General>(p.rope.dtype), dim3((uint32_t)blocks), dim3(kAttnGenThreads),
                                      args, 0, s);
-    if (err != hipSuccess || a.splits == 1) return launched(err);
+    if (err != hipSuccess || !a.split) return launched(err);
     args[0] = &g;
     const uint64_t rows_of_all = (uint64_t)a.B * a.part_rows;
     if (!join_few(a))

@@ -26,8 +26,8 @@ struct AttnArgs {
     uint32_t D, Dv, S, Hq, heads, rep;
     uint32_t rows;             // of a cached head: S * rep; row r is token r / rep, head r % rep of the group
     uint32_t tiles;            // of rows
-    uint32_t splits;           // parts of a sequence's tokens, on average; 1: no parts
-    uint32_t B, parts;         // of all sequences: B * splits
+    uint32_t B, parts;         // of all sequences' tokens
+    bool split;                // parts > B: results are joined
     uint32_t most_parts;       // of one sequence
     uint32_t unit;             // tokens that a part is whole multiples of
     const int32_t* table;
@@ -95,14 +95,14 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 
 // Sequences are split into parts of the same number of tokens, whatever each
 // one's length, so that blocks end together: a.parts of them at most, which is
-// all the host can know. Every wave finds out for itself (and so do those that
+// all that the host can know. Every wave finds out for itself (and so do those that
 // join), from the lengths: the smallest part, within 1/16, that makes no more.
 // 16 sequences of 500 to 8000 tokens by 16 parts each: 91 us, so 55.
 struct AttnShare {
     uint32_t b, first, n;      // a sequence, its first part and how many
     uint32_t per;              // units of a part
 };
-constexpr int kAttnBatch = kAttnBlocks / 2 / 64;   // 64 sequences each: more are not split
+constexpr int kAttnBatch = kAttnMaxSplit / 64;
 
 // Of the sequence that part `key` belongs to (b = a.B: of none), or of sequence
 // `key` itself.
@@ -170,7 +170,7 @@ __device__ __forceinline__ bool attn_at(const AttnArgs& a, uint32_t block, AttnA
     p->b = p->part;
     p->first = 0;
     p->end = UINT32_MAX;
-    if (a.splits == 1) return true;
+    if (!a.split) return true;
     const AttnShare s = attn_share<true>(a, p->part);
     if (s.b == a.B) return false;
     p->b = s.b;
@@ -322,10 +322,10 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
         for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
             const uint32_t j = k * kAttnGenThreads + t;
             if (j >= a.Dv) continue;
-            if (a.splits == 1) Store<DT>::store1(a.out.data, at.b * a.out.sb + s * a.out.ss + h * a.out.sn + j, o[r][k] * inv);
+            if (!a.split) Store<DT>::store1(a.out.data, at.b * a.out.sb + s * a.out.ss + h * a.out.sn + j, o[r][k] * inv);
             else a.part[row * a.Dv + j] = o[r][k];
         }
-        if (a.splits > 1 && t == 0) part_stats(a)[row] = make_float2(m[r], sum);
+        if (a.split && t == 0) part_stats(a)[row] = make_float2(m[r], sum);
     }
 }
 

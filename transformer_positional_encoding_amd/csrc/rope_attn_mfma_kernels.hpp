@@ -472,7 +472,7 @@ struct AttnRows {
         return VF ? 32 * (i >> 1) + 8 * kq + 2 * r + (i & 1) : VT * (4 * kq + r) + i;
     }
 
-    // The rows' results, or (splits) their part of them.
+    // The rows' results, or (split) their part of them.
     __device__ __forceinline__ void store(const AttnArgs& a, const AttnAt& at, uint32_t head, uint32_t r0, uint32_t live, uint32_t n16,
                                           uint32_t kq)
     {
@@ -482,7 +482,7 @@ struct AttnRows {
             const float sum = column_sum(l[t]);
             if (r >= live) continue;
             const uint32_t s = fast_div(r, a.rep_div), h = head * a.rep + (r - s * a.rep);
-            const float inv = a.splits > 1 ? 1.0f : one_over(sum);
+            const float inv = a.split ? 1.0f : one_over(sum);
             const uint64_t row = part_row(a, at.part, s, h);
             gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
 #pragma unroll
@@ -494,10 +494,10 @@ struct AttnRows {
                     v[k] = f * (VF ? acc[t][2 * c + (k & 1)][k >> 1] : acc[t][(8 * c + k) % VT][(8 * c + k) / VT]);
                 const uint32_t j = VF ? 32 * c + 8 * kq : 4 * VT * kq + 8 * c;
                 if (j >= a.Dv) continue;
-                if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
+                if (!a.split) store_chunk<DT>(dst + j * 2, v);
                 else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
             }
-            if (a.splits > 1 && kq == 0) part_stats(a)[row] = make_float2(m[t], sum);
+            if (a.split && kq == 0) part_stats(a)[row] = make_float2(m[t], sum);
         }
     }
 };
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                 whole += lds.join.l[w][row16] * part_weight(mw, high);
             }
             const uint32_t h = (at.head * a.head_waves + hw) * a.rep + (r - s * a.rep);
-            const float inv = a.splits > 1 ? 1.0f : one_over(whole);
+            const float inv = a.split ? 1.0f : one_over(whole);
             const uint64_t row = part_row(a, at.part, s, h);
             gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
             for (uint32_t j = 8 * (threadIdx.x & 15); j < a.Dv && r < live; j += 128) {
@@ -821,10 +821,10 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
                     for (int k = 0; k < 8; ++k) v[k] += lds.join.o[w][row16][j + k];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] *= inv;
-                if (a.splits == 1) store_chunk<DT>(dst + j * 2, v);
+                if (!a.split) store_chunk<DT>(dst + j * 2, v);
                 else store_chunk<ROPE_DTYPE_F32>(as_global(a.part + row * a.Dv + j), v);
             }
-            if (a.splits > 1 && r < live && (threadIdx.x & 15) == 0) part_stats(a)[row] = make_float2(high, whole);
+            if (a.split && r < live && (threadIdx.x & 15) == 0) part_stats(a)[row] = make_float2(high, whole);
         }
     }
 }

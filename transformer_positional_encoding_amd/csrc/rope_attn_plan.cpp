@@ -15,12 +15,13 @@ constexpr int64_t kAttnSplitTokens = 64;
 
 }  // namespace
 
-int64_t attn_splits(int64_t B, int64_t heads, int64_t rows, int64_t tokens)
+int64_t attn_parts(int64_t B, int64_t heads, int64_t rows, int64_t tokens)
 {
-    const int64_t tiles = rows <= 16 ? 1 : (rows + 31) / 32;       // a wave's
-    const int64_t base = std::max<int64_t>(1, B * heads * tiles);
-    const int64_t want = std::min(kAttnMaxParts, kAttnBlocks / base);
-    return std::max<int64_t>(1, std::min(want, tokens / kAttnSplitTokens));
+    // up to 64 rows: as many as a wave takes; a block's 128 are worth 8 tiles
+    const int64_t tiles = rows <= 16 ? 1 : rows <= 64 ? (rows + 31) / 32 : (rows + 15) / 16;
+    const int64_t per_head = heads > kAttnBlocks / tiles ? 0 : kAttnBlocks / (heads * tiles);
+    const int64_t parts = std::min(per_head, B * std::min(kAttnMaxParts, tokens / kAttnSplitTokens));
+    return B <= kAttnMaxSplit && 4 * parts >= 5 * B ? parts : B;
 }
 
 int64_t attn_workspace_bytes(int64_t B, int64_t S, int64_t q_heads, int64_t heads, int64_t Dv)
@@ -28,8 +29,8 @@ int64_t attn_workspace_bytes(int64_t B, int64_t S, int64_t q_heads, int64_t head
     if (B <= 0 || S <= 0 || q_heads <= 0 || heads <= 0 || q_heads % heads != 0 || Dv <= 0 || Dv > ROPE_D_LIMIT) return 0;
     int64_t rows;
     if (__builtin_mul_overflow(B, S, &rows) || __builtin_mul_overflow(rows, q_heads, &rows) || rows >= (1ll << 31)) return 0;
-    const int64_t splits = attn_splits(B, heads, S * (q_heads / heads), kI64Max);
-    return splits == 1 ? 0 : splits * rows * (Dv + 2) * 4;
+    const int64_t parts = attn_parts(B, heads, S * (q_heads / heads), kI64Max);
+    return parts == B ? 0 : parts * S * q_heads * (Dv + 2) * 4;
 }
 
 rope_status_t make_attn_plan(int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* out, const rope_rows_t* q,
@@ -101,7 +102,7 @@ rope_status_t make_attn_plan(int64_t B, int64_t S, rope_dtype_t dtype, const rop
     p.counts = counts;
     // lengths are 32-bit numbers, so no sequence has 2^31 tokens or more
     p.most = p.table_pages > INT32_MAX / p.page_size ? INT32_MAX : p.table_pages * p.page_size;
-    p.splits = attn_splits(B, p.heads, S * p.rep, p.most);
+    p.parts = attn_parts(B, p.heads, S * p.rep, p.most);
     const int64_t need = attn_workspace_bytes(B, S, q->N, p.heads, out->D);
     if (need > 0) {
         if (workspace == nullptr) return fail(ROPE_ERR_NULLPTR, why, "workspace is NULL");

@@ -7,9 +7,10 @@
 namespace rope {
 
 // Parts of all sequences, by heads and tiles of rows, that fill the card; most
-// that one sequence's tokens are divided into.
+// that one sequence's tokens are divided into; most sequences that are.
 constexpr int64_t kAttnBlocks = 2048;
 constexpr int64_t kAttnMaxParts = 512;
+constexpr int64_t kAttnMaxSplit = 1024;
 
 struct AttnPlan {
     Plan rope;                     // dimensions and storage type
@@ -26,14 +27,15 @@ struct AttnPlan {
     const int32_t* counts = nullptr;
     double scale = 0;
     bool causal = false;
-    float* part = nullptr;         // partial results of the splits
-    int64_t splits = 1;            // parts that a sequence's tokens are divided into, on average
+    float* part = nullptr;         // partial results
+    int64_t parts = 0;             // that the sequences' tokens are divided into; B: not divided
     bool noop = false;
 };
 
-// Parts, on average, for B x heads sequences of `rows` rows each over up to
-// `tokens` cached tokens.
-int64_t attn_splits(int64_t B, int64_t heads, int64_t rows, int64_t tokens);
+// Parts for B sequences of `heads` cached heads and `rows` rows of each over up
+// to `tokens` cached tokens: as many as fill the card, if that is a quarter more
+// than sequences.
+int64_t attn_parts(int64_t B, int64_t heads, int64_t rows, int64_t tokens);
 
 // Bytes of workspace for any number of tokens; 0 when nothing is computed or
 // the arguments are out of range.
