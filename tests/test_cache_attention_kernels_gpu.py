@@ -167,3 +167,21 @@ def test_parts_of_equal_tokens(lengths, S, heads, D):
     c = inputs(lengths, S, 2 * heads, heads, D, D, D, D, 16, "f16", seed=40, cols=512)
     check(call(c), c)
     check(call(c, causal=False), c, causal=False)
+
+
+@pytest.mark.parametrize("S, hq, heads, D, gv, dtype", [(3, 8, 4, 128, 128, "bf16"), (3, 4, 2, 64, 64, "f16"), (9, 16, 4, 128, 32, "bf16"),
+                                                        (40, 4, 2, 128, 128, "f16"), (3, 4, 2, 256, 64, "bf16"), (3, 4, 2, 80, 80, "bf16"),
+                                                        (3, 4, 2, 64, 64, "f32")])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_scales_that_are_no_numbers_stay_with_those_who_see_them(S, hq, heads, D, gv, dtype, value, which):
+    """The newest token's scales: rows before it neither see it nor change."""
+    c = inputs([S, 200, 130], S, hq, heads, D, D, D, gv, 16, dtype, seed=41)
+    want = call(c)
+    for b, n in enumerate(c["lengths"].tolist()):
+        c[which][1][c["table"][b, (n - 1) // 16], (n - 1) % 16] = value
+    got = call(c)
+    assert torch.equal(got[:, :-1], want[:, :-1])
+    last = got[:, -1].float()
+    if which == "v" or value != value:
+        assert not bool(torch.isfinite(last).any())

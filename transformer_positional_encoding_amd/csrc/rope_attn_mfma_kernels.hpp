@@ -393,6 +393,22 @@ struct AttnRows {
         __builtin_amdgcn_sched_barrier(0);
     }
 
+    // Weights times scales, by the product whose 0 times anything is 0: a scale
+    // that is no number reaches only the rows that see its token. (Its operands
+    // come from LDS and from sums that have waited for the exponentials.)
+    __device__ __forceinline__ static f32x4 scaled(const f32x4& x, const float* vs)
+    {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(vs);
+        f32x4 w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float one;
+            asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(one) : "v"(x[r]), "v"(v[r]));
+            w[r] = one;
+        }
+        return w;
+    }
+
     // By segments: the weights times V's scales, in fp16, and o^T += V^T P^T, 32
     // tokens a product. v_numbers_of(h, i): product i's V of half h of the tokens;
     // vs: V's scales by token, of each segment or one.
@@ -424,7 +440,7 @@ struct AttnRows {
                     float high = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const f32x4 w = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
+                        const f32x4 w = scaled(x[t][i], &vs[g][16 * i + 4 * kq]);
                         high = max3_abs(max3_abs(high, w[0], w[1]), w[2], w[3]);
                     }
                     high = fmaxf(top_of(t, g) * keep[t], column_max(high));
@@ -443,7 +459,7 @@ struct AttnRows {
             for (int t = 0; t < NT; ++t) {
                 f32x4 w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = x[t][i] * *reinterpret_cast<const f32x4*>(&vs[g][16 * i + 4 * kq]);
+                for (int i = 0; i < 4; ++i) w[i] = scaled(x[t][i], &vs[g][16 * i + 4 * kq]);
                 const float c = __builtin_ldexpf(1.0f, -e[t][g]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
