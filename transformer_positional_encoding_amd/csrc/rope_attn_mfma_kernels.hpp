@@ -870,6 +870,10 @@ struct alignas(16) AttnSharedLds {
         int64_t k_at[64], v_at[64];
     };
     Where where[P16 ? 1 : 4];
+    struct Wave {
+        float start[kSharedTiles][NGK][16], top[kSharedTiles][NGV][16];    // the rows', where registers are short
+    };
+    Wave wave[4];
 };
 
 template <int DT, int DP, bool KF, bool VF, bool P16>
@@ -897,6 +901,14 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
     const uint32_t all = min(span.all, to), some = min(span.some, to);
     R rows;
     rows.load(a, seq, at.b, at.head, min(r0, live - 1), live, n16, kq);
+    typename Lds::Wave& my = lds.wave[wave];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) my.start[t][g][n16] = rows.start[t][g];
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) my.top[t][g][n16] = 0.0f;
+    }
 
     const gchar* const k_base = as_global(a.kc.data) + at.head * a.kc.st[2];
     const gchar* const v_base = as_global(a.vc.data) + at.head * a.vc.st[2];
@@ -1017,7 +1029,8 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
         bool moved[NT];
         const bool used = base < some;
         if (used) {
-            rows.template scores<false>(x, [&](int i, int st) { return tile.k[i][st][lane]; }, tile.ks, kq);
+            rows.template scores<false>(x, [&](int i, int st) { return tile.k[i][st][lane]; }, tile.ks, kq,
+                                        [&](int t, int st) { return my.start[t][st][n16]; });
             if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
             rows.weigh(x, keep, moved);
         }
@@ -1027,7 +1040,8 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
         fetch(next);
         next = attn_look_up(a, table, (to - base > 192 ? base + 192 : to) + lane, to);
         __builtin_amdgcn_sched_barrier(0);
-        if (used) rows.template add<false>(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq, lane);
+        if (used) rows.template add<false>(x, keep, moved, [&](int h, int i) { return tile.v[h][i][lane]; }, tile.vs, kq, lane,
+                                     [&](int t, int g) -> float& { return my.top[t][g][n16]; });
         valid = next_valid;
         buffer ^= 1;
         __syncthreads();
