@@ -1799,34 +1799,44 @@ def rope_qk_norm_bwd(q_grad, k_grad, q, k, q_weight=None, k_weight=None, positio
     ptrs = _norm_weights(q, k, q_weight, k_weight)
     if k is None and not (k_grad is None and dk is None):
         raise ValueError("k_grad and dk go with k")
-    given = tuple(t for t in (dq, dk) if t is not None)
-    want = weight_grads and not (q_weight is None and k_weight is None)
-    dev = q.device
-    with _allocating_on(stream, dev) if stream is not None and q.is_cuda else _nullcontext():
-        if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        if k is not None and dk is None:
-            dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        dw = [None if w is None or not weight_grads else torch.empty_like(w) for w in (q_weight, k_weight)]
-        if want and workspace is None:
-            workspace = torch.empty(library().rope_qk_norm_workspace(q.shape[3]), dtype=torch.uint8, device=dev)
-    if want and (not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev):
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    code = _dtype_code(q)
+    given = dq is not None or dk is not None
+    code, dev, none = _dtype_code(q), q.device, k is None
+    rows_q, rows_k = _rows("q", q), None if none else _rows("k", k)
+    rows_qg, rows_kg = _norm_rows("q_grad", q_grad, q), None if none else _norm_rows("k_grad", k_grad, k)
+    rows_dq = None if dq is None else _norm_rows("dq", dq, q)
+    rows_dk = None if dk is None else _norm_rows("dk", dk, k)
     turn = _turn_args(positions, inv_freq, pair_axes, rotary_mode, partial_slice, table_dtype, code, dev)
+    written = () if not given else tuple(t for t in (dq, dk) if t is not None)
+    dw_q = dw_k = None
+    at_dq = at_dk = at_space = None
+    space = 0
+    with _allocating_on(stream, dev) if stream is not None and q.is_cuda else _NOTHING:
+        if dq is None:
+            dq, rows_dq = _new_rows(q)
+        if dk is None and not none:
+            dk, rows_dk = _new_rows(k)
+        if weight_grads:
+            if q_weight is not None:
+                dw_q = q_weight.new_empty(q_weight.shape)
+                at_dq = dw_q.data_ptr() or None
+            if k_weight is not None:
+                dw_k = k_weight.new_empty(k_weight.shape)
+                at_dk = dw_k.data_ptr() or None
+            if dw_q is not None or dw_k is not None:
+                if workspace is None:
+                    workspace = q.new_empty(rope_qk_norm_workspace(q.shape[3]), dtype=torch.uint8)
+                elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev:
+                    raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+                at_space, space = workspace.data_ptr() or None, workspace.nbytes
     handle, current = _on_device(q, stream)
-    none = k is None
     with current:
-        st = _words_entry("rope_qk_norm_bwd")(
-            q.shape[0], q.shape[1], code, _norm_rows("dq", dq, q), None if none else _norm_rows("dk", dk, k),
-            *(None if w is None else w.data_ptr() or None for w in dw), _norm_rows("q_grad", q_grad, q),
-            None if none else _norm_rows("k_grad", k_grad, k), _rows("q", q), None if none else _rows("k", k), *ptrs, eps,
-            *turn, workspace.data_ptr() or None if want else None, workspace.nbytes if want else 0, handle)
+        st = _words_entry("rope_qk_norm_bwd")(q.shape[0], q.shape[1], code, rows_dq, rows_dk, at_dq, at_dk, rows_qg, rows_kg,
+                                              rows_q, rows_k, *ptrs, eps, *turn, at_space, space, handle)
     if st != ROPE_OK:
         raise RopeError(st, last_error())
     if given:
-        (_TORCH or _autograd())[2](given)
-    return dq, dk, dw[0], dw[1]
+        (_TORCH or _autograd())[2](written)
+    return dq, dk, dw_q, dw_k
 
 
 _QK_NORM_FN = None
