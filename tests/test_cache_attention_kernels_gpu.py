@@ -185,3 +185,20 @@ def test_scales_that_are_no_numbers_stay_with_those_who_see_them(S, hq, heads, D
     last = got[:, -1].float()
     if which == "v" or value != value:
         assert not bool(torch.isfinite(last).any())
+
+
+@pytest.mark.parametrize("D, Dv, gk, gv", [(64, 64, 16, 16), (128, 128, 16, 128), (128, 64, 128, 16), (128, 128, 64, 16), (96, 96, 48, 16),
+                                           (80, 80, 80, 16), (80, 128, 16, 32), (256, 256, 16, 16), (192, 80, 48, 80)])
+@pytest.mark.parametrize("S, hq, heads, page", [(1, 4, 1, 16), (1, 8, 4, 24), (5, 12, 2, 16), (20, 4, 1, 7), (70, 4, 4, 16)])
+def test_groups_of_16_lanes(D, Dv, gk, gv, S, hq, heads, page):
+    lengths = [S, 0, 200 + S, 77]
+    counts = torch.tensor([S, S, S, (S + 1) // 2], dtype=torch.int32)
+    for dtype, span in (("bf16", 0.5), ("f16", 3.0)):
+        c = inputs(lengths, S, hq, heads, D, Dv, gk, gv, page, dtype, seed=42, span=span)
+        if dtype == "f16":      # values that the type holds
+            c["v"] = (c["v"][0], c["v"][1].clamp(max=1000.0))
+        c["k"] = (c["k"][0], c["k"][1].clamp(max=4.0))
+        check(call(c, counts=counts), c, counts=counts, what=dtype)
+    c = inputs([500, 333], S, hq, heads, D, Dv, gk, gv, page, "bf16", seed=43, span=12.0)
+    c["k"] = (c["k"][0], c["k"][1].clamp(max=4.0))
+    check(call(c, causal=False), c, causal=False, what="far apart")

@@ -97,20 +97,27 @@ bool heads_together(const CachePlan& c, int64_t heads, int64_t D, bool scales)
            (!scales || (aligned16(c.scales) && c.sc[0] % 4 == 0 && c.sc[1] % 4 == 0 && c.sc[2] == 1));
 }
 
-// The matrix-core kernel of a call, and its lanes; NULL if it does not take the
-// shapes.
-const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes, int64_t heads)
+// How the matrix-core kernels for rows of up to `lanes` lanes see a call's
+// scales; -1 if they do not take it.
+int scales_of(const AttnPlan& p, int lanes)
 {
     const int64_t D = p.q.D, Dv = p.out.D;
-    if (p.rope.dtype == ROPE_DTYPE_F32 || D > 256 || Dv > 256 || !rows_in_chunks(p.q, 2) || !rows_in_chunks(p.out, 2))
-        return nullptr;
+    if (p.rope.dtype == ROPE_DTYPE_F32 || D > 256 || Dv > 256 || !rows_in_chunks(p.q, 2) || !rows_in_chunks(p.out, 2) ||
+        !codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4))
+        return -1;
     const bool k_row = p.kc.group == D, v_row = p.vc.group == Dv;
-    if ((!k_row && p.kc.group % 32 != 0) || (!v_row && p.vc.group % 32 != 0)) return nullptr;
+    if ((!k_row && p.kc.group % 16 != 0) || (!v_row && p.vc.group % 16 != 0)) return -1;
+    if ((!k_row && p.kc.group % 32 != 0) || (!v_row && p.vc.group % 32 != 0)) return kAttnHalves;
     const bool k_whole = k_row && D == lanes && codes_aligned(p.kc, lanes == 64 ? 8 : 16);
-    const int scales = !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
-    if (!codes_aligned(p.kc, 4) || !codes_aligned(p.vc, lanes == 64 ? 2 : 4)) return nullptr;
+    return !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
+}
+
+// The matrix-core kernel of a call.
+const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes, int scales, int64_t heads)
+{
+    const int64_t D = p.q.D, Dv = p.out.D;
     const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
-    if (rows != AttnRowsOf::kShared && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
+    if (rows != AttnRowsOf::kShared && scales != kAttnHalves && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
         heads_together(p.kc, heads, D, scales == kAttnRowScales) && heads_together(p.vc, heads, D, scales == kAttnRowScales))
         rows = rows == AttnRowsOf::kOneTile ? AttnRowsOf::kFourHeads : AttnRowsOf::kFourHeadsTwoTiles;
     if (p.rope.dtype == ROPE_DTYPE_BF16)
@@ -123,9 +130,10 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     AttnVecArgs a{};
     static_cast<AttnArgs&>(a) = attn_args(p);
     const int lanes = std::max(p.q.D, p.out.D) <= 64 ? 64 : std::max(p.q.D, p.out.D) <= 128 ? 128 : 256;
-    const AttnRowsOf rows = lanes == 256 || a.rows <= 16 ? AttnRowsOf::kOneTile : a.rows <= 64 ? AttnRowsOf::kTwoTiles : AttnRowsOf::kShared;
-    const void* fn = mfma_kernel(p, rows, lanes, a.heads);
-    const bool mfma = fn != nullptr;
+    const int scales = scales_of(p, lanes);
+    const AttnRowsOf rows = lanes == 256 || scales == kAttnHalves || a.rows <= 16 ? AttnRowsOf::kOneTile : a.rows <= 64 ? AttnRowsOf::kTwoTiles : AttnRowsOf::kShared;
+    const bool mfma = scales >= 0;
+    const void* fn = mfma ? mfma_kernel(p, rows, lanes, scales, a.heads) : by_type<General>(p.rope.dtype);
     // Few rows: a wave a head, as far as heads go by fours, which then read
     // neighbouring bytes; else waves take turns at the tokens. Many: a wave its
     // own rows.
@@ -150,7 +158,7 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
         return set_error(ROPE_ERR_UNSUPPORTED, "a grid too large for one launch");
     AttnArgs g = a;
     void* args[] = {mfma ? (void*)&a : (void*)&g};
-    hipError_t err = hipLaunchKernel(mfma ? fn : by_type<General>(p.rope.dtype), dim3((uint32_t)blocks), dim3(kAttnGenThreads),
+    hipError_t err = hipLaunchKernel(fn, dim3((uint32_t)blocks), dim3(kAttnGenThreads),
                                      args, 0, s);
     if (err != hipSuccess || !a.split) return launched(err);
     args[0] = &g;

@@ -9,6 +9,7 @@ namespace rope {
 constexpr int kAttnRowScales = 0;
 constexpr int kAttnKSegments = 1;
 constexpr int kAttnSegments = 2;
+constexpr int kAttnHalves = 3;
 
 // Query rows of a cached head that a kernel takes: 16 or 32 a wave, by waves on
 // their own, or 32 a wave, 128 a block, whose waves share their tiles' numbers,

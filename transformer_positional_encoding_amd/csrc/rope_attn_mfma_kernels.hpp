@@ -198,9 +198,15 @@ __device__ __forceinline__ float column_sum(float v)
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-template <int DP, int DVP, bool KF, bool VF, int NT>
+// Scales that a kernel takes of a row: one (0), one for 32 lanes (1) or for 16
+// (2, whose segments of 32 are two halves).
+constexpr int kHalves = 2;
+constexpr int attn_group(int f) { return f == kHalves ? 16 : 32; }
+constexpr int attn_groups(int f, int lanes) { return f == 0 ? 1 : lanes / attn_group(f); }
+
+template <int DP, int DVP, int KF, int VF, int NT>
 struct alignas(16) AttnLds {
-    static constexpr int NGK = KF ? DP / 32 : 1, NGV = VF ? DVP / 32 : 1;
+    static constexpr int NGK = attn_groups(KF, DP), NGV = attn_groups(VF, DVP);
     struct Wave {
         int64_t k_at[64], v_at[64];
         float ks[NGK][64], vs[NGV][64];
@@ -217,14 +223,15 @@ struct alignas(16) AttnLds {
 
 // A wave's query rows, 16 to a tile, and what it holds of their attention: all
 // that does not depend on where a tile's numbers come from.
-template <int DT, int DP, int DVP, bool KF, bool VF, int NT>
+template <int DT, int DP, int DVP, int KF, int VF, int NT>
 struct AttnRows {
     static constexpr int KW = DP / 32;             // steps of a product with K
     static constexpr int VT = DVP / 16;            // products of 16 lanes of V
-    static constexpr int NGV = VF ? DVP / 32 : 1;
+    static constexpr int NGK = attn_groups(KF, DP), NGV = attn_groups(VF, DVP);
+    static constexpr int HK = KF == kHalves ? 2 : 1, HV = VF == kHalves ? 2 : 1;   // scales of a segment
 
-    v4u q[NT][KW];
-    float start[NT][KF ? KW : 1];                  // -24 sum(q)
+    v4u q[NT][KW * HK];                            // (halves: a step's with the other half's lanes 0)
+    float start[NT][NGK];                          // -24 sum(q)
     int32_t last[NT];                              // the last token that a row sees
     f32x4 acc[NT][VT];
     float m[NT], less[NT], l[NT], top[NT][NGV];    // less: m, or 0 where there is none yet
@@ -248,14 +255,18 @@ struct AttnRows {
                 const uint32_t d = KF ? 32 * st + 8 * kq : kq * (DP / 4) + 8 * st;
                 v4u v{0, 0, 0, 0};
                 if (d < a.D) v = gload<v4u>(row + d * 2);
-                Lanes<DT> f;
-                f.unpack(v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sum += f.v[k];
-                q[t][st] = q_order(v);
-                if (KF || st == KW - 1) {
-                    start[t][KF ? st : 0] = -24.0f * column_sum(sum);
-                    sum = 0.0f;
+                for (int half = 0; half < HK; ++half) {
+                    const v4u part = HK == 1 || (half == 0) == (kq < 2) ? v : v4u{0, 0, 0, 0};
+                    Lanes<DT> f;
+                    f.unpack(part);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum += f.v[k];
+                    q[t][st * HK + half] = q_order(part);
+                    if (KF || st == KW - 1) {
+                        start[t][KF ? st * HK + half : 0] = -24.0f * column_sum(sum);
+                        sum = 0.0f;
+                    }
                 }
             }
 #pragma unroll
@@ -290,22 +301,28 @@ struct AttnRows {
         if constexpr (KF) {
 #pragma unroll
             for (int st = 0; st < KW; ++st) {
-                f32x4 c[NT];
+                f32x4 c[HK][NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float one = start_of(t, st);
-                    if (HOLD) asm volatile("" : "+v"(one));        // made here, not kept as four
-                    c[t] = f32x4{one, one, one, one};
-                }
+                for (int half = 0; half < HK; ++half)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float one = start_of(t, st * HK + half);
+                        if (HOLD) asm volatile("" : "+v"(one));    // made here, not kept as four
+                        c[half][t] = f32x4{one, one, one, one};
+                    }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const v4u k = k_numbers_of(i, st);
-                    const f32x4 s = *reinterpret_cast<const f32x4*>(&ks[st][16 * i + 4 * kq]);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const f32x4 d = attn_mfma<DT>(k, q[t][st], c[t]);
+                    for (int half = 0; half < HK; ++half) {
+                        const f32x4 s = *reinterpret_cast<const f32x4*>(&ks[st * HK + half][16 * i + 4 * kq]);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[t][i][r] = __builtin_fmaf(d[r], s[r], st == 0 ? -less[t] : x[t][i][r]);
+                        for (int t = 0; t < NT; ++t) {
+                            const f32x4 d = attn_mfma<DT>(k, q[t][st * HK + half], c[half][t]);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                x[t][i][r] = __builtin_fmaf(d[r], s[r], st == 0 && half == 0 ? -less[t] : x[t][i][r]);
+                        }
                     }
                     if (HOLD && (i & 1)) __builtin_amdgcn_sched_barrier(0);
                 }
@@ -423,63 +440,81 @@ struct AttnRows {
     __device__ __forceinline__ void add(const f32x4 (&x)[NT][4], const float (&keep)[NT], const bool (&moved)[NT], const F& v_numbers_of,
                                         const float (*vs)[64], uint32_t kq, uint32_t lane, const G& top_of)
     {
+        constexpr int T = VT / NGV * HV;           // products of a segment
+        const uint32_t low = (lane & 8) ? 0u : ~0u;        // rows of its first half
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) {
-            constexpr int T = VT / NGV;            // products of a segment
-            v4u p[NT][2];
-            // Weights are at most 2^6 (m follows beyond that): the tile's scales
-            // tell whether one could outgrow fp16. If so, or where a maximum has
-            // moved, the powers of two are set anew from the largest product.
-            bool set = __any(fabsf(vs[g][lane]) > safe[g]);
+        for (int seg = 0; seg < NGV / HV; ++seg) {
+            v4u p[HV][NT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) set = set || moved[t];
-            if (set) {
-                int32_t least = 127;
+            for (int half = 0; half < HV; ++half) {
+                const int g = seg * HV + half;
+                // Weights are at most 2^6 (m follows beyond that): the tile's scales
+                // tell whether one could outgrow fp16. If so, or where a maximum has
+                // moved, the powers of two are set anew from the largest product.
+                bool set = __any(fabsf(vs[g][lane]) > safe[g]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) set = set || moved[t];
+                if (set) {
+                    int32_t least = 127;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float high = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const f32x4 w = scaled(x[t][i], &vs[g][16 * i + 4 * kq]);
+                            high = max3_abs(max3_abs(high, w[0], w[1]), w[2], w[3]);
+                        }
+                        high = fmaxf(top_of(t, g) * keep[t], column_max(high));
+                        top_of(t, g) = high;
+                        int32_t now = __builtin_amdgcn_frexp_expf(high);
+                        now = high > 0.0f ? min(max(now, -120), 120) : e[t][g];
+                        float f = __builtin_ldexpf(keep[t], e[t][g] - now);
+                        e[t][g] = now;
+                        least = min(least, now);
+                        if (HV == 2) f = (half == 0) == (kq < 2) ? f : 1.0f;
+#pragma unroll
+                        for (int i = 0; i < T; ++i) acc[t][seg * T + i] *= f;
+                    }
+                    safe[g] = __builtin_ldexpf(0x1p9f, least16(least));    // 2^6 * 2^9 = 2^15
+                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float high = 0.0f;
+                    f32x4 w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4 w = scaled(x[t][i], &vs[g][16 * i + 4 * kq]);
-                        high = max3_abs(max3_abs(high, w[0], w[1]), w[2], w[3]);
-                    }
-                    high = fmaxf(top_of(t, g) * keep[t], column_max(high));
-                    top_of(t, g) = high;
-                    int32_t now = __builtin_amdgcn_frexp_expf(high);
-                    now = high > 0.0f ? min(max(now, -120), 120) : e[t][g];
-                    const float f = __builtin_ldexpf(keep[t], e[t][g] - now);
-                    e[t][g] = now;
-                    least = min(least, now);
+                    for (int i = 0; i < 4; ++i) w[i] = scaled(x[t][i], &vs[g][16 * i + 4 * kq]);
+                    const float c = __builtin_ldexpf(1.0f, -e[t][g]);
 #pragma unroll
-                    for (int i = 0; i < T; ++i) acc[t][g * T + i] *= f;
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const f32x4& v = w[2 * h + (j >> 1)];
+                            const f32x2 pair{v[2 * (j & 1)] * c, v[2 * (j & 1) + 1] * c};
+                            p[half][t][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
+                        }
                 }
-                safe[g] = __builtin_ldexpf(0x1p9f, least16(least));        // 2^6 * 2^9 = 2^15
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4 w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = scaled(x[t][i], &vs[g][16 * i + 4 * kq]);
-                const float c = __builtin_ldexpf(1.0f, -e[t][g]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f32x4& v = w[2 * h + (j >> 1)];
-                        const f32x2 pair{v[2 * (j & 1)] * c, v[2 * (j & 1) + 1] * c};
-                        p[t][h][j] = Store<ROPE_DTYPE_F16>::narrow(pair);
-                    }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = g * T; i < (g + 1) * T; ++i) {
+                for (int i = seg * T; i < (seg + 1) * T; ++i) {
                     const v4u v = v_numbers_of(h, i);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(v, p[t][h], acc[t][i]);
+                    for (int half = 0; half < HV; ++half) {
+                        const uint32_t rows = half == 0 ? low : ~low;
+                        const v4u of = HV == 1 ? v : v4u{v[0] & rows, v[1] & rows, v[2] & rows, v[3] & rows};
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) acc[t][i] = attn_mfma<ROPE_DTYPE_F16>(of, p[half][t][h], acc[t][i]);
+                    }
                     if (HOLD && (i & 1)) __builtin_amdgcn_sched_barrier(0);
                 }
         }
+    }
+
+    // The power of two of product i's sums.
+    __device__ __forceinline__ int32_t power(int t, int i, uint32_t kq) const
+    {
+        if constexpr (HV == 2) return kq < 2 ? e[t][i & ~1] : e[t][i | 1];
+        else return e[t][VF ? i / 2 : 0];
     }
 
     // Lane j of v that product i's row 4 kq + r holds.
@@ -503,7 +538,7 @@ struct AttnRows {
             gchar* dst = as_global(a.out.data) + (at.b * a.out.sb + s * a.out.ss + h * a.out.sn) * 2;
 #pragma unroll
             for (int c = 0; c < VT / 2; ++c) {     // 8 consecutive lanes
-                const float f = __builtin_ldexpf(inv, e[t][VF ? c : 0]);
+                const float f = __builtin_ldexpf(inv, power(t, 2 * c, kq));
                 float v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -570,7 +605,7 @@ __device__ __forceinline__ uint32_t attn_lane()
 
 // Where a register of a lane's V starts in its row: 4 bytes (2 of rows of up to
 // 64 lanes) that end with the row, or the first ones.
-template <int DVP, bool VF>
+template <int DVP, int VF>
 __device__ __forceinline__ uint32_t attn_v_byte(uint32_t n16, int c, uint32_t v_bytes)
 {
     const uint32_t off = VF ? (DVP == 64 ? 16 * (n16 & 1) + 2 * (n16 >> 1) : 64 * c + 16 * (n16 & 3) + 4 * (n16 >> 2))
@@ -593,12 +628,12 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnSeq& 
 }
 
 // Waves that a SIMD is to hold: what their registers allow.
-constexpr int attn_waves(int lanes, bool kf, int tiles)
+constexpr int attn_waves(int lanes, int kf, int tiles)
 {
-    return lanes == 256 ? 1 : lanes == 64 ? 4 - tiles : kf && tiles == 2 ? 1 : 2;
+    return lanes == 256 || kf == kHalves ? 1 : lanes == 64 ? 4 - tiles : kf && tiles == 2 ? 1 : 2;
 }
 
-template <int DT, int DP, int DVP, bool KF, bool VF, bool P16, int NT>
+template <int DT, int DP, int DVP, int KF, int VF, bool P16, int NT>
 __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_kernel(AttnVecArgs a)
 {
     using Lds = AttnLds<DP, DVP, KF, VF, NT>;
@@ -654,12 +689,12 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         const gchar* sv = vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1]) * 4;
 #pragma unroll
         for (int g = 0; g < NGK; ++g) {
-            const uint32_t at_g = KF ? min((uint32_t)g * 32 / a.k_group, a.k_groups - 1) : 0;
+            const uint32_t at_g = KF ? min((uint32_t)(g * attn_group(KF)) / a.k_group, a.k_groups - 1) : 0;
             ks[g] = there ? gload<float>(sk + at_g * 4) : 0.0f;
         }
 #pragma unroll
         for (int g = 0; g < NGV; ++g) {
-            const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
+            const uint32_t at_g = VF ? min((uint32_t)(g * attn_group(VF)) / a.v_group, a.v_groups - 1) : 0;
             vs[g] = there ? gload<float>(sv + at_g * 4) : 0.0f;
         }
         if constexpr (!P16) {
@@ -811,7 +846,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
         const float keep = part_weight(rows.m[t], most);
 #pragma unroll
         for (int i = 0; i < VT; ++i) {
-            const float f = __builtin_ldexpf(keep, rows.e[t][VF ? i / 2 : 0]);
+            const float f = __builtin_ldexpf(keep, rows.power(t, i, kq));
 #pragma unroll
             for (int r = 0; r < 4; ++r) lds.join.o[wave][n16][R::lane_of(i, r, kq)] = rows.acc[t][i][r] * f;
         }
@@ -857,9 +892,9 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 // ---------------------------------------------------------------------------
 constexpr int kSharedTiles = 2;                    // of 16 rows a wave
 
-template <int DP, bool KF, bool VF, bool P16>
+template <int DP, int KF, int VF, bool P16>
 struct alignas(16) AttnSharedLds {
-    static constexpr int NGK = KF ? DP / 32 : 1, NGV = VF ? DP / 32 : 1;
+    static constexpr int NGK = attn_groups(KF, DP), NGV = attn_groups(VF, DP);
     struct Buffer {
         v4u k[4][DP / 32][64];
         v4u v[2][DP / 16][64];
@@ -876,7 +911,7 @@ struct alignas(16) AttnSharedLds {
     Wave wave[4];
 };
 
-template <int DT, int DP, bool KF, bool VF, bool P16>
+template <int DT, int DP, int KF, int VF, bool P16>
 __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
 {
     constexpr int NT = kSharedTiles;
@@ -1061,11 +1096,11 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
 // that neither K's reads (the same piece of 16 tokens) nor V's (four pieces of
 // four tokens) meet in a bank. Two buffers of 17 or 35 KB; one barrier a tile.
 // ---------------------------------------------------------------------------
-template <int DP, bool KF, bool VF, int NT>
+template <int DP, int KF, int VF, int NT>
 struct alignas(16) AttnHeadsLds {
     static constexpr int kRow = 2 * DP;            // bytes of a token's four rows
     static constexpr bool kScales = !KF && !VF;    // one a row: they come with the codes
-    static constexpr int NGK = KF ? DP / 32 : 1, NGV = VF ? DP / 32 : 1;
+    static constexpr int NGK = attn_groups(KF, DP), NGV = attn_groups(VF, DP);
     struct Tile {
         char k[64 * kRow], v[64 * kRow];
         float ks[kScales ? 64 : 1][4], vs[kScales ? 64 : 1][4];
@@ -1078,7 +1113,7 @@ struct alignas(16) AttnHeadsLds {
     Wave wave[4];
 };
 
-template <int DT, int DP, bool KF, bool VF, int NT>
+template <int DT, int DP, int KF, int VF, int NT>
 __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
 {
     using Lds = AttnHeadsLds<DP, KF, VF, NT>;
@@ -1126,12 +1161,12 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
         if constexpr (!Lds::kScales) {
 #pragma unroll
             for (int g = 0; g < NGK; ++g) {
-                const uint32_t at_g = KF ? min((uint32_t)g * 32 / a.k_group, a.k_groups - 1) : 0;
+                const uint32_t at_g = KF ? min((uint32_t)(g * attn_group(KF)) / a.k_group, a.k_groups - 1) : 0;
                 ks[g] = p.there ? gload<float>(sk + at_g * 4) : 0.0f;
             }
 #pragma unroll
             for (int g = 0; g < NGV; ++g) {
-                const uint32_t at_g = VF ? min((uint32_t)g * 32 / a.v_group, a.v_groups - 1) : 0;
+                const uint32_t at_g = VF ? min((uint32_t)(g * attn_group(VF)) / a.v_group, a.v_groups - 1) : 0;
                 vs[g] = p.there ? gload<float>(sv + at_g * 4) : 0.0f;
             }
         }

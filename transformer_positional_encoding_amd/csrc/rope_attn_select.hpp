@@ -13,9 +13,10 @@ template <int DT, int DP, bool P16, int NT>
 const void* attn_by_scales(int scales)
 {
     switch (scales) {
-    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, false, false, P16, NT>);
-    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, true, false, P16, NT>);
-    default: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, true, true, P16, NT>);
+    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 0, 0, P16, NT>);
+    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 1, 0, P16, NT>);
+    case kAttnHalves: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, kHalves, kHalves, P16, 1>);
+    default: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 1, 1, P16, NT>);
     }
 }
 
@@ -23,9 +24,9 @@ template <int DT, int DP, bool P16>
 const void* attn_shared(int scales)
 {
     switch (scales) {
-    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, false, false, P16>);
-    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, true, false, P16>);
-    default: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, true, true, P16>);
+    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 0, 0, P16>);
+    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, 0, P16>);
+    default: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, 1, P16>);
     }
 }
 
@@ -33,9 +34,9 @@ template <int DT, int DP, int NT>
 const void* attn_heads(int scales)
 {
     switch (scales) {
-    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, false, false, NT>);
-    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, true, false, NT>);
-    default: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, true, true, NT>);
+    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 0, 0, NT>);
+    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, 0, NT>);
+    default: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, 1, NT>);
     }
 }
 
