@@ -12,6 +12,9 @@
 namespace rope {
 namespace {
 
+// Blocks of the general forward: what the card holds at a time.
+constexpr uint32_t kNormFwdBlocks = 2048;
+
 NormArgs norm_args(const NormPlan& p)
 {
     NormArgs a{};
@@ -46,14 +49,27 @@ const void* by_type(int dtype)
     }
 }
 
-template <int DT>
-struct FwdGeneral {
-    static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_fwd_general_kernel<DT>); }
+template <int NL>
+struct General {
+    template <int DT>
+    struct Fwd {
+        static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_fwd_general_kernel<DT, NL>); }
+    };
+    template <int DT>
+    struct Bwd {
+        static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_bwd_general_kernel<DT, NL>); }
+    };
 };
-template <int DT>
-struct BwdGeneral {
-    static const void* ptr() { return reinterpret_cast<const void*>(&rope_norm_bwd_general_kernel<DT>); }
-};
+template <int NL>
+const void* general_kernel(int dtype, bool backward)
+{
+    return backward ? by_type<General<NL>::template Bwd>(dtype) : by_type<General<NL>::template Fwd>(dtype);
+}
+const void* norm_general(const NormPlan& p, bool backward)
+{
+    return p.rope.D <= kNormFewLanes * 64 ? general_kernel<kNormFewLanes>(p.rope.dtype, backward)
+                                          : general_kernel<kNormLanes>(p.rope.dtype, backward);
+}
 template <int C, int PAR>
 struct Vec {
     template <int DT>
@@ -135,8 +151,8 @@ hipError_t launch_fwd(const NormPlan& p, hipStream_t s)
     }
     NormArgs g = a;
     void* args[] = {&g};
-    const uint32_t blocks = (uint32_t)std::min<uint64_t>(g.tokens, kMaxGridItems / kNormThreads);
-    return hipLaunchKernel(by_type<FwdGeneral>(p.rope.dtype), dim3(blocks), dim3(kNormThreads), args, 0, s);
+    const uint32_t blocks = std::min<uint32_t>(g.tokens, kNormFwdBlocks);
+    return hipLaunchKernel(norm_general(p, false), dim3(blocks), dim3(kNormThreads), args, 0, s);
 }
 
 hipError_t launch_bwd(const NormPlan& p, hipStream_t s)
@@ -150,7 +166,7 @@ hipError_t launch_bwd(const NormPlan& p, hipStream_t s)
         NormArgs g = a;
         void* args[] = {fn != nullptr ? (void*)&a : (void*)&g};
         blocks = (uint32_t)std::min<uint64_t>(fn != nullptr ? a.groups : a.tokens, kNormBwdBlocks);
-        hipError_t err = hipLaunchKernel(fn != nullptr ? fn : by_type<BwdGeneral>(p.rope.dtype), dim3(blocks), dim3(kNormThreads),
+        hipError_t err = hipLaunchKernel(fn != nullptr ? fn : norm_general(p, true), dim3(blocks), dim3(kNormThreads),
                                          args, fn != nullptr ? lds : 0, s);
         if (err != hipSuccess) return err;
     }

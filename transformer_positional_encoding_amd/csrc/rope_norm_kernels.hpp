@@ -78,117 +78,195 @@ __device__ __forceinline__ float lanes_sum(float v, uint32_t width)
 
 // ---------------------------------------------------------------------------
 // General kernels: any dimensions, alignment and slice. A block takes a token,
-// its waves the token's rows; cos and sin are evaluated once a token, a row
-// stands in LDS for its partners' sake.
+// each of its waves every fourth of the token's rows, with the next one's lanes
+// on the way; cos and sin are evaluated once a token, and a row stands in the
+// wave's part of LDS for its partners' sake. Single lanes, and a row a wave: the
+// instructions bound it. 2 x 2000 tokens of 36 heads: of 36 lanes 35 us (0.6
+// TB/s), of 128 with 20 of them rotated 53 (1.4); forward and backward of 4 x
+// 2000 tokens of 40 heads of 96, 24 rotated, 308 us (1 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 constexpr int kNormWaves = kNormThreads / 64;
-constexpr int kNormLanes = ROPE_D_LIMIT / 64;     // lanes of a row that a thread takes at most
+// NL: lanes of a row that a thread takes at most, for rows of up to 256 and of
+// any number.
+constexpr int kNormFewLanes = 4, kNormLanes = ROPE_D_LIMIT / 64;
 
-__device__ __forceinline__ void norm_turns(const NormArgs& a, uint32_t tok, float2* cs)
+// cos and sin of a token's pairs, once the rows of the token before are done.
+__device__ __forceinline__ void norm_turns(const NormArgs& a, uint32_t b, uint32_t s, float2* cs)
 {
-    const uint32_t b = fast_div(tok, a.s_div);
-    for (uint32_t i = threadIdx.x; i < a.turn.pairs; i += kNormThreads) cs[i] = turn_cos_sin(a.turn, b, tok - b * a.S, i);
+    if (!a.rotate) return;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < a.turn.pairs; i += kNormThreads) cs[i] = turn_cos_sin(a.turn, b, s, i);
+    __syncthreads();
 }
 
-template <int DT>
+// What a wave writes to its part of LDS is there for its other lanes.
+__device__ __forceinline__ void norm_wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// What a thread's lanes keep from row to row: where their pairs' partners and
+// angles are, and the weights of a kind.
+template <int NL>
+struct NormLanes {
+    int32_t partner[NL];                  // -1: not turned
+    uint32_t pair[NL];
+    bool first[NL];
+    float w[NL];
+    __device__ __forceinline__ NormLanes(const NormArgs& a, uint32_t lane)
+    {
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+            const uint32_t j = k * 64 + lane;
+            partner[k] = -1;
+            pair[k] = 0;
+            first[k] = false;
+            if (a.rotate && j >= a.turn.start && j < a.turn.start + a.turn.L && j < a.D) {
+                pair[k] = turn_pair(a.turn, j - a.turn.start, &first[k]);
+                partner[k] = (int32_t)(first[k] ? j + a.turn.half : j - a.turn.half);
+            }
+        }
+    }
+    __device__ __forceinline__ void weights(const NormArgs& a, int kind, uint32_t lane)
+    {
+#pragma unroll
+        for (int k = 0; k < NL; ++k) w[k] = k * 64 + lane < a.D ? norm_weight(a, kind, k * 64 + lane) : 0.0f;
+    }
+    // Number k of them of a row that stands in LDS, its pair turned.
+    __device__ __forceinline__ float turned(int k, uint32_t lane, const float* z, const float2* cs, bool back) const
+    {
+        float v = z[k * 64 + lane];
+        if (partner[k] >= 0) v = rotate_own_unfused(v, z[partner[k]], cs[pair[k]].x, cs[pair[k]].y, first[k] != back);
+        return v;
+    }
+};
+
+// A thread's lanes of a row.
+template <int DT, int NL>
+__device__ __forceinline__ void norm_row_lanes(const NormArgs& a, const Rows& x, uint32_t b, uint32_t s, uint32_t n, uint32_t lane,
+                                               float (&v)[NL])
+{
+    const int64_t row = b * x.sb + s * x.ss + n * x.sn;
+#pragma unroll
+    for (int k = 0; k < NL; ++k) {
+        if (k * 64 >= a.D) break;
+        const uint32_t j = k * 64 + lane;
+        v[k] = j < a.D ? Store<DT>::load1(x.data, row + j) : 0.0f;
+    }
+}
+
+template <int DT, int NL>
 __global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_general_kernel(NormArgs a)
 {
     __shared__ float2 cs[ROPE_D_LIMIT / 2];
     __shared__ float rows[kNormWaves][ROPE_D_LIMIT];
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float* z = rows[wave];
+    NormLanes<NL> own(a, lane);
     for (uint32_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x) {
-        if (a.rotate) norm_turns(a, tok, cs);      // (the rows of the token before are done)
         const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.S;
+        norm_turns(a, b, s, cs);
         for (int kind = 0; kind < 2; ++kind) {
-            const Rows& x = a.x[kind];
             const Rows& y = a.y[kind];
-            for (uint32_t n0 = 0; n0 < a.N[kind]; n0 += kNormWaves) {
-                const uint32_t n = n0 + wave;
-                const bool live = n < a.N[kind];
-                float ss = 0.0f;
-                if (live)
-                    for (uint32_t j = lane; j < a.D; j += 64) {
-                        const float v = Store<DT>::load1(x.data, b * x.sb + s * x.ss + n * x.sn + j);
-                        z[j] = v;
-                        ss = __builtin_fmaf(v, v, ss);
-                    }
+            float next[NL];
+            if (wave < a.N[kind]) norm_row_lanes<DT, NL>(a, a.x[kind], b, s, wave, lane, next);
+            own.weights(a, kind, lane);
+            for (uint32_t n = wave; n < a.N[kind]; n += kNormWaves) {
+                float v[NL], ss = 0.0f;
+#pragma unroll
+                for (int k = 0; k < NL; ++k) {
+                    if (k * 64 >= a.D) break;
+                    v[k] = next[k];
+                    ss = __builtin_fmaf(v[k], v[k], ss);
+                }
+                if (n + kNormWaves < a.N[kind]) norm_row_lanes<DT, NL>(a, a.x[kind], b, s, n + kNormWaves, lane, next);
                 const float r = rsqrtf(__builtin_fmaf(lanes_sum(ss, 64), a.inv_d, a.eps));
-                __syncthreads();
-                if (live)
-                    for (uint32_t j = lane; j < a.D; j += 64) {
-                        float v = z[j] * r * norm_weight(a, kind, j);
-                        if (a.rotate && j >= a.turn.start && j < a.turn.start + a.turn.L) {
-                            bool first;
-                            const uint32_t i = turn_pair(a.turn, j - a.turn.start, &first);
-                            const uint32_t p = first ? j + a.turn.half : j - a.turn.half;
-                            v = rotate_own_unfused(v, z[p] * r * norm_weight(a, kind, p), cs[i].x, cs[i].y, first);
-                        }
-                        Store<DT>::store1(y.data, b * y.sb + s * y.ss + n * y.sn + j, v);
-                    }
-                __syncthreads();
+                norm_wave_sync();                  // the row before is done
+#pragma unroll
+                for (int k = 0; k < NL; ++k) {
+                    if (k * 64 >= a.D) break;
+                    const uint32_t j = k * 64 + lane;
+                    if (j < a.D) z[j] = v[k] * r * own.w[k];
+                }
+                norm_wave_sync();
+                const int64_t row = b * y.sb + s * y.ss + n * y.sn;
+#pragma unroll
+                for (int k = 0; k < NL; ++k) {
+                    if (k * 64 >= a.D) break;
+                    const uint32_t j = k * 64 + lane;
+                    if (j < a.D) Store<DT>::store1(y.data, row + j, own.turned(k, lane, z, cs, false));
+                }
             }
         }
     }
 }
 
-template <int DT>
+template <int DT, int NL>
 __global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_general_kernel(NormArgs a)
 {
     __shared__ float2 cs[ROPE_D_LIMIT / 2];
     __shared__ float rows[kNormWaves][ROPE_D_LIMIT];
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float* z = rows[wave];
+    NormLanes<NL> own(a, lane);
     for (int kind = 0; kind < 2; ++kind) {
-        const Rows& x = a.x[kind];
         const Rows& y = a.y[kind];
-        const Rows& dy = a.dy[kind];
-        float dw[kNormLanes] = {};
+        float dw[NL] = {};
+        own.weights(a, kind, lane);
         for (uint32_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x) {
             if (a.N[kind] == 0) break;
-            if (a.rotate) norm_turns(a, tok, cs);
             const uint32_t b = fast_div(tok, a.s_div), s = tok - b * a.S;
-            for (uint32_t n0 = 0; n0 < a.N[kind]; n0 += kNormWaves) {
-                const uint32_t n = n0 + wave;
-                const bool live = n < a.N[kind];
-                if (live)
-                    for (uint32_t j = lane; j < a.D; j += 64)
-                        z[j] = Store<DT>::load1(dy.data, b * dy.sb + s * dy.ss + n * dy.sn + j);
-                __syncthreads();
-                float v[kNormLanes], g[kNormLanes], ss = 0.0f, dot = 0.0f;
+            norm_turns(a, b, s, cs);
+            float next[NL], up[NL];
+            if (wave < a.N[kind]) {
+                norm_row_lanes<DT, NL>(a, a.x[kind], b, s, wave, lane, next);
+                norm_row_lanes<DT, NL>(a, a.dy[kind], b, s, wave, lane, up);
+            }
+            for (uint32_t n = wave; n < a.N[kind]; n += kNormWaves) {
+                float v[NL], g[NL], ss = 0.0f, dot = 0.0f;
+                norm_wave_sync();                  // the row before is done
 #pragma unroll
-                for (int k = 0; k < kNormLanes; ++k) {
+                for (int k = 0; k < NL; ++k) {
+                    if (k * 64 >= a.D) break;
+                    v[k] = next[k];
+                    if (k * 64 + lane < a.D) z[k * 64 + lane] = up[k];
+                }
+                if (n + kNormWaves < a.N[kind]) {
+                    norm_row_lanes<DT, NL>(a, a.x[kind], b, s, n + kNormWaves, lane, next);
+                    norm_row_lanes<DT, NL>(a, a.dy[kind], b, s, n + kNormWaves, lane, up);
+                }
+                norm_wave_sync();
+#pragma unroll
+                for (int k = 0; k < NL; ++k) {
+                    if (k * 64 >= a.D) break;
                     const uint32_t j = k * 64 + lane;
-                    v[k] = g[k] = 0.0f;
-                    if (!live || j >= a.D) continue;
-                    v[k] = Store<DT>::load1(x.data, b * x.sb + s * x.ss + n * x.sn + j);
-                    g[k] = z[j];
-                    if (a.rotate && j >= a.turn.start && j < a.turn.start + a.turn.L) {
-                        bool first;
-                        const uint32_t i = turn_pair(a.turn, j - a.turn.start, &first);
-                        g[k] = rotate_own_unfused(g[k], z[first ? j + a.turn.half : j - a.turn.half], cs[i].x, cs[i].y, !first);
-                    }
+                    g[k] = 0.0f;
+                    if (j >= a.D) continue;
+                    g[k] = own.turned(k, lane, z, cs, true);
                     ss = __builtin_fmaf(v[k], v[k], ss);
-                    dot = __builtin_fmaf(g[k] * norm_weight(a, kind, j), v[k], dot);
+                    dot = __builtin_fmaf(g[k] * own.w[k], v[k], dot);
                 }
                 const float r = rsqrtf(__builtin_fmaf(lanes_sum(ss, 64), a.inv_d, a.eps));
                 const float m = lanes_sum(dot, 64) * r * a.inv_d;
+                const int64_t row = b * y.sb + s * y.ss + n * y.sn;
 #pragma unroll
-                for (int k = 0; k < kNormLanes; ++k) {
+                for (int k = 0; k < NL; ++k) {
+                    if (k * 64 >= a.D) break;
                     const uint32_t j = k * 64 + lane;
-                    if (!live || j >= a.D) continue;
+                    if (j >= a.D) continue;
                     const float nj = v[k] * r;
                     dw[k] = __builtin_fmaf(g[k], nj, dw[k]);
-                    Store<DT>::store1(y.data, b * y.sb + s * y.ss + n * y.sn + j,
-                                      r * (g[k] * norm_weight(a, kind, j) - nj * m));
+                    Store<DT>::store1(y.data, row + j, r * (g[k] * own.w[k] - nj * m));
                 }
-                __syncthreads();
             }
         }
         if (a.part == nullptr) continue;
+        norm_wave_sync();
 #pragma unroll
-        for (int k = 0; k < kNormLanes; ++k)
+        for (int k = 0; k < NL; ++k)
             if (k * 64 + lane < a.D) z[k * 64 + lane] = dw[k];
         __syncthreads();
         for (uint32_t j = threadIdx.x; j < a.D; j += kNormThreads) {
