@@ -97,6 +97,11 @@ bool heads_together(const CachePlan& c, int64_t heads, int64_t D, bool scales)
            (!scales || (aligned16(c.scales) && c.sc[0] % 4 == 0 && c.sc[1] % 4 == 0 && c.sc[2] == 1));
 }
 
+// (Four heads loaded together, and by waves on their own: 64 sequences of up to
+// 8192 tokens, 32 heads on 8 of 128 lanes 103 and 118 us; 64 heads on 16 of 64
+// 148 and 225; scales of 32 lanes 156 and 235; 16 sequences of 5 new tokens, 40
+// heads on 8, scales of 32 72 and 102.)
+
 // How the matrix-core kernels for rows of up to `lanes` lanes see a call's
 // scales; -1 if they do not take it.
 int scales_of(const AttnPlan& p, int lanes)
@@ -131,11 +136,18 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     static_cast<AttnArgs&>(a) = attn_args(p);
     const int lanes = std::max(p.q.D, p.out.D) <= 64 ? 64 : std::max(p.q.D, p.out.D) <= 128 ? 128 : 256;
     const int scales = scales_of(p, lanes);
-    const AttnRowsOf rows = lanes == 256 || scales == kAttnHalves || a.rows <= 16 ? AttnRowsOf::kOneTile : a.rows <= 64 ? AttnRowsOf::kTwoTiles : AttnRowsOf::kShared;
+    // Rows of a cached head: up to 16 a tile of them a wave; up to 64 two tiles
+    // (24 rows, 8 sequences of up to 8000 tokens, 32 heads on 8: 38 us, one tile
+    // 49, shared numbers 71; 64 rows 51, 65 and 66); more share their numbers (96
+    // rows 75, two tiles 69; 128 rows 79 and 86, 512 rows 247 and 284). Rows past
+    // 128 lanes, and scales of 16, leave registers for one tile only.
+    const AttnRowsOf rows = lanes == 256 || scales == kAttnHalves || a.rows <= 16 ? AttnRowsOf::kOneTile
+                            : a.rows <= 64                                        ? AttnRowsOf::kTwoTiles
+                                                                                  : AttnRowsOf::kShared;
     const bool mfma = scales >= 0;
     const void* fn = mfma ? mfma_kernel(p, rows, lanes, scales, a.heads) : by_type<General>(p.rope.dtype);
-    // Few rows: a wave a head, as far as heads go by fours, which then read
-    // neighbouring bytes; else waves take turns at the tokens. Many: a wave its
+    // Up to 64 rows: a wave a head, as far as heads go by fours, which then read
+    // neighbouring bytes; else waves take turns at the tokens. More: a wave its
     // own rows.
     a.head_waves = a.token_waves = a.row_waves = 1;
     if (a.rows > 64) a.row_waves = 4;

@@ -5,7 +5,7 @@ namespace rope {
 
 // Scales of a cached row: one of K and one of V; K's by 32-lane steps (also
 // where rows are short of the kernel's lanes, or not aligned for one load), V's
-// one; both by 32-lane segments.
+// one; both by 32-lane segments; both by halves of those (one tile of rows).
 constexpr int kAttnRowScales = 0;
 constexpr int kAttnKSegments = 1;
 constexpr int kAttnSegments = 2;

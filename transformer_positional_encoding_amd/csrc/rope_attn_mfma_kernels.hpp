@@ -1,7 +1,7 @@
 // rope_attn_mfma_kernels.hpp -- attention over a cache held in 4 bits on the
 // matrix cores: 16-bit queries, rows of whole 8-lane chunks up to 256 lanes,
-// one scale a row or groups of whole 32-lane segments.
-// Included by rope_attn.hip.
+// one scale a row or groups of whole 16 lanes.
+// Included by the rope_attn_*.hip files of a type each.
 //
 // A wave takes 16 query rows (NT such tiles) and 64 cached tokens at a time.
 // Both products have the cached rows as their first operand, so that a query
@@ -21,24 +21,32 @@
 // whose 16-bit halves, put side by side, hold the codes of two tokens at equal
 // nibbles. With a scale for each segment of 32 lanes (VF) a segment has to be
 // whole products, a byte a lane: lanes in fours exchange the bytes of words of
-// four segments.
+// four segments. With one for each half of a segment, each half has a product of
+// its own, the other half's lanes of q, or of V, being 0.
 //
 // Scales stay outside of the products: K's multiply the finished sums of their
 // lanes (one a row, or one for each 32-lane step, KF), V's the weights. exp(x -
-// m) times V's scale is rounded to fp16, times a power of two that keeps the
-// row's largest such weight of a segment within 2^-1 and 2^8 (2^-e below), so
-// that only weights below 2^-13 of the largest lose digits, and at most 2^-24
-// of it. m follows the maximum when it is passed by 2^6; a tile that moves
-// neither m nor e leaves the accumulators as they are.
+// m) times V's scale is rounded to fp16 (2^-11 of it, where bf16's store rounds
+// by 2^-8 afterwards), times a power of two, 2^-e. e is set from the row's
+// largest such weight of the scale's lanes when m moves or a tile's scales could
+// take a weight past 2^15; between that the weights are at most 2^6 * 2^9 of
+// what e was set from, and what is below 2^-14 loses digits, at most 2^-25. m
+// follows the maximum when it is passed by 2^6; a tile that moves neither m nor
+// e leaves the accumulators as they are.
 //
 // The bytes are 4 bits a code; at the rate of a large copy that is 10^13 codes a
 // second, against 4 * 10^13 operations of the vector units, so operations per
-// code decide: 1.1 for K, 1.6 for V (2.1 with VF), the softmax 0.4 for 4 rows
-// a head (its 16 columns) and 128 lanes.
+// code decide: of 64 tokens of 128 lanes, 16384 codes, a wave issues about 680
+// (128 for K's numbers, 190 for V's, 230 for 16 rows' softmax, the rest for
+// addresses), 1120 with a scale for 32 lanes, 760 and 1600 with 32 rows.
 //
-// Loads go straight to registers, a tile ahead; addresses by a lane a token,
-// through the wave's part of LDS. Four waves of a block share the rows and take
-// tiles in turn (join), or have rows of their own.
+// Three kernels differ in where a tile's numbers come from:
+//   rope_attn_mfma_kernel    any heads, strides and pages: loads go straight to
+//       registers, a tile ahead. Four waves of a block take heads beside each
+//       other, or share the rows and take tiles in turn (joined in LDS), or have
+//       rows of their own.
+//   rope_attn_heads_kernel   up to 64 rows, four heads that lie together.
+//   rope_attn_shared_kernel  more rows of one head.
 #pragma once
 
 #include "rope_attn_kernels.hpp"
@@ -888,7 +896,10 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 // bytes a lane, so that no read or write meets another's bank. Numbers cost a
 // wave 75 operations a tile then, not 300, of 700. Two buffers: while a tile is
 // used the next one's numbers are made, its words having been loaded the tile
-// before; one barrier a tile.
+// before; one barrier a tile. 3 sequences of 2039 new tokens behind up to 4096
+// others, 32 heads on 8 of 128 lanes: 480 us, 606 by waves on their own; with a
+// scale for 32 lanes 858, 1106. (32 rows a wave: 48 and 64 were slower, for want
+// of registers.)
 // ---------------------------------------------------------------------------
 constexpr int kSharedTiles = 2;                    // of 16 rows a wave
 

@@ -10,7 +10,9 @@ namespace rope {
 namespace {
 
 constexpr int64_t kI64Max = std::numeric_limits<int64_t>::max();
-// The fewest tokens that are worth a part of their own.
+// The fewest tokens that are worth a part of their own. (One sequence of 500
+// tokens, 4 heads of 64 lanes: 9.1 us by 64, 12.6 by 256; of 4000 10.8 and
+// 15.4.)
 constexpr int64_t kAttnSplitTokens = 64;
 
 }  // namespace
