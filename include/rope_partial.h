@@ -574,7 +574,9 @@ ROPE_API rope_status_t rope_cache_reserve(
  * keep their bytes.
  * Products with q are exact and summed in fp32, as are the softmax's sums
  * and its products with v; 16-bit outputs may round exp(x_t) times v's scale
- * to 11 bits before the product. out is rounded once.
+ * to 11 bits before the product. out is rounded once. Long sequences are
+ * summed in parts, whose size follows from the lengths of all. A scale that is
+ * infinite or NaN reaches the rows that see its token, and no other.
  *
  *   B, S          tokens of q and out; dtype: their storage type.
  *   out, q        (B, S, heads of q, lanes of v or k) rows; out's must not
@@ -594,7 +596,8 @@ ROPE_API rope_status_t rope_cache_reserve(
  * (ROPE_ERR_UNSUPPORTED unless ROPE_CACHE_INT4) and shapes; strides; scale; an
  * empty q is ROPE_OK; NULL or misaligned pointers; the workspace.
  * ROPE_ERR_UNSUPPORTED: 2^31 rows or more. Asynchronous on `stream`; nothing
- * is allocated; deterministic.
+ * is allocated; deterministic (the same call gives the same bits; a sequence in
+ * another batch may differ in its last ones).
  */
 ROPE_API rope_status_t rope_cache_attention(
     int64_t B, int64_t S, rope_dtype_t dtype, const rope_rows_t* out, const rope_rows_t* q, const rope_cache_t* k_cache,

@@ -1555,7 +1555,8 @@ def rope_cache_reserve(block_table, lengths, counts, free_pages, free_count, pag
     tokens) slots (-1 past a sequence's new tokens) and positions that
     :func:`rope_cache_write` takes, and int32 (B) what was added to each
     length: 0 for a refused sequence, the count for
-    :func:`rope_cache_attention`. At most RESERVE_MAX sequences."""
+    :func:`rope_cache_attention`. At most RESERVE_MAX sequences; no two of the
+    tensors may overlap."""
     import torch
     if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be an int32 tensor (B, columns)")
@@ -1621,7 +1622,8 @@ def rope_cache_attention(q, k_cache, v_cache, block_table, lengths, counts=None,
 
     Returns ``out``, (B, S, heads, v's dim) of q's type (allocated when None,
     then zero past each sequence's count; a given one keeps its bytes there). A
-    query that sees no token gives zeros. No gradient passes through the call:
+    query that sees no token gives zeros. Long sequences are summed in parts,
+    whose size follows from the lengths of the whole batch. No gradient passes through the call:
     tensors that need one are refused (while gradients are enabled)."""
     import torch
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
