@@ -45,6 +45,13 @@ bool join_few(const AttnArgs& a)
     return a.parts <= 32 * a.B || (a.parts <= 64 * a.B && (uint64_t)a.B * a.part_rows >= 512);
 }
 
+// Whether rows of codes start and step at multiples of `bytes`.
+bool codes_aligned(const CachePlan& c, uintptr_t bytes)
+{
+    return reinterpret_cast<uintptr_t>(c.data) % bytes == 0 && c.st[0] % (int64_t)bytes == 0 &&
+           c.st[1] % (int64_t)bytes == 0 && c.st[2] % (int64_t)bytes == 0;
+}
+
 AttnArgs attn_args(const AttnPlan& p)
 {
     AttnArgs a{};
@@ -77,16 +84,10 @@ AttnArgs attn_args(const AttnPlan& p)
     a.split = a.parts > a.B;
     a.most_parts = join_few(a) ? kJoinFewParts : kAttnMaxParts;
     a.unit = kAttnGenThreads;
+    a.words = codes_aligned(p.kc, 4) && p.kc.group % 8 == 0 ? 1 : 0;
     a.rep_div = make_fastdiv(a.rep);
     a.heads_div = make_fastdiv(a.heads);
     return a;
-}
-
-// Whether rows of codes start and step at multiples of `bytes`.
-bool codes_aligned(const CachePlan& c, uintptr_t bytes)
-{
-    return reinterpret_cast<uintptr_t>(c.data) % bytes == 0 && c.st[0] % (int64_t)bytes == 0 &&
-           c.st[1] % (int64_t)bytes == 0 && c.st[2] % (int64_t)bytes == 0;
 }
 
 // Whether the rows of four heads lie beside each other in 16-byte pieces, and

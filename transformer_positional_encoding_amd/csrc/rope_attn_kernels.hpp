@@ -39,6 +39,7 @@ struct AttnArgs {
     int32_t most;              // tokens that a block table holds
     float scale2;              // scale * log2(e)
     int32_t causal;
+    int32_t words;             // general kernel: K's codes by whole aligned words of 8
     float* part;               // per part, token and head: Dv sums; then m and l of all
     uint32_t part_rows;        // of a part: S * Hq
     FastDiv rep_div, heads_div, tiles_div, page_div;
@@ -207,22 +208,38 @@ __device__ __forceinline__ float part_weight(float m, float most)
 }
 __device__ __forceinline__ float one_over(float sum) { return sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum; }   // NaN stays
 
+// a * b, 0 where a is 0: a scale that is infinite or NaN reaches only the rows
+// that see its token. (Not right behind a transcendental or matrix instruction
+// that makes an operand: nothing waits for those here.)
+__device__ __forceinline__ float mul_or_0(float a, float b)
+{
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------------------
-// General kernel: any dimensions, groups, alignment and types. A block takes up
-// to 4 rows that share a cached head, 256 tokens at a time: a thread a token's
-// products with q, then a thread one to four lanes of v. Bound by its
-// instructions, a byte at a time: 16 sequences of up to 8192 tokens, 32 heads
-// on 8 of 128 lanes, float32: 690 us (0.16 TB/s).
+// General kernel: any dimensions, groups, alignment and types, all in fp32. A
+// block takes up to 4 rows that share a cached head, 256 tokens at a time: a
+// thread a token's products with q (a word of 8 codes at a time where words are
+// aligned and groups hold them whole), then a thread a byte of v's rows, two
+// lanes, of every so many tokens. q and the weights stand in LDS with the four
+// rows' values together. Bound by its instructions: 16 sequences of up to 8192
+// tokens, 32 heads on 8 of 128 lanes, float32: 156 us (0.7 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kAttnGenThreads = 256;
 constexpr int kAttnGenRows = 4;
+constexpr int kAttnGenBytes = ROPE_D_LIMIT / 2 / kAttnGenThreads;      // of v's row, a thread, at most
+constexpr int kAttnGenAhead = 4;                   // tokens whose loads go out together
 
+// The code in bits 4 i to 4 i + 3.
+__device__ __forceinline__ float code_of(uint32_t w, int i) { return (float)((int32_t)(w << (28 - 4 * i)) >> 28); }
 
 template <int DT>
 __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(AttnArgs a)
 {
-    __shared__ float q[kAttnGenRows][ROPE_D_LIMIT];
-    __shared__ float p[kAttnGenRows][kAttnGenThreads];
+    __shared__ float4 q[ROPE_D_LIMIT];
+    __shared__ float4 p[kAttnGenThreads];
     __shared__ int64_t v_at[kAttnGenThreads], vs_at[kAttnGenThreads];
     __shared__ float red[kAttnGenRows][kAttnGenThreads / 64];
     const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -233,50 +250,75 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
     const uint32_t live = min(a.rows, (uint32_t)seq.count * a.rep);
     if (r0 >= live) return;                      // the same for the whole block
     const uint32_t nr = min((uint32_t)kAttnGenRows, live - r0);
-    for (uint32_t r = 0; r < nr; ++r) {
-        const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
-        for (uint32_t j = t; j < a.D; j += kAttnGenThreads)
-            q[r][j] = Store<DT>::load1(a.q.data, at.b * a.q.sb + s * a.q.ss + h * a.q.sn + j);
+    for (uint32_t j = t; j < a.D; j += kAttnGenThreads) {
+        float v[kAttnGenRows] = {};
+#pragma unroll
+        for (int r = 0; r < kAttnGenRows; ++r) {
+            if (r >= (int)nr) continue;
+            const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
+            v[r] = Store<DT>::load1(a.q.data, at.b * a.q.sb + s * a.q.ss + h * a.q.sn + j);
+        }
+        q[j] = make_float4(v[0], v[1], v[2], v[3]);
     }
-    float m[kAttnGenRows], l[kAttnGenRows], o[kAttnGenRows][ROPE_D_LIMIT / kAttnGenThreads];
+    // this thread's bytes of v's rows, and its turn among the tokens
+    const uint32_t v_bytes = a.Dv / 2;
+    uint32_t cols = 1;
+    while (cols < v_bytes && cols < (uint32_t)kAttnGenThreads) cols *= 2;
+    const uint32_t strands = kAttnGenThreads / cols, strand = t / cols, col = t & (cols - 1);
+    float m[kAttnGenRows], l[kAttnGenRows], o[kAttnGenBytes][2][kAttnGenRows];
     int64_t last[kAttnGenRows];                  // the last token that the row sees
+#pragma unroll
     for (int r = 0; r < kAttnGenRows; ++r) {
         m[r] = kAttnNone;
         l[r] = 0.0f;
-        for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) o[r][k] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAttnGenBytes; ++k) o[k][0][r] = o[k][1][r] = 0.0f;
         last[r] = a.causal ? seq.first + fast_div(min(r0 + r, a.rows - 1), a.rep_div) : INT64_MAX;
     }
     uint32_t from, to;
     attn_part(at, (uint32_t)seq.tokens, &from, &to);
+    const bool words = a.words != 0;
     __syncthreads();
     for (uint32_t base = from; base < to; base += kAttnGenThreads) {
         const uint32_t tok = base + t;
         int64_t page = -1, in_page = 0;
         if (tok < to) {
-            const uint32_t col = fast_div(tok, a.page_div);
-            page = a.table[at.b * a.table_stride + col];
-            in_page = tok - col * a.page_div.d;
+            const uint32_t c = fast_div(tok, a.page_div);
+            page = a.table[at.b * a.table_stride + c];
+            in_page = tok - c * a.page_div.d;
         }
         const bool there = page >= 0 && page < a.pages;
-        float x[kAttnGenRows];
-        for (int r = 0; r < kAttnGenRows; ++r) x[r] = 0.0f;
+        float x[kAttnGenRows] = {};
         if (there) {
-            const char* k = a.kc.data + page * a.kc.st[0] + in_page * a.kc.st[1] + at.head * a.kc.st[2];
+            const gchar* k = as_global(a.kc.data) + page * a.kc.st[0] + in_page * a.kc.st[1] + at.head * a.kc.st[2];
             const float* ks = a.kc.scales + page * a.kc.sc[0] + in_page * a.kc.sc[1] + at.head * a.kc.sc[2];
-            for (uint32_t g = 0; g * a.kc.group < a.D; ++g) {
+            for (uint32_t g = 0, j = 0; j < a.D; ++g) {
                 float dot[kAttnGenRows] = {};
-                for (uint32_t j = g * a.kc.group; j < (g + 1) * a.kc.group; j += 2) {
-                    const uint32_t w = (uint8_t)k[j / 2];
-                    const float c0 = (float)((int32_t)(w << 28) >> 28), c1 = (float)((int32_t)(w << 24) >> 28);
-                    for (int r = 0; r < kAttnGenRows; ++r)
-                        dot[r] = __builtin_fmaf(q[r][j + 1], c1, __builtin_fmaf(q[r][j], c0, dot[r]));
+                const uint32_t end = j + a.kc.group;
+                while (j < end) {
+                    const int n = words ? 8 : 2;
+                    const uint32_t w = words ? gload<uint32_t>(k + j / 2) : (uint32_t)gload<uint8_t>(k + j / 2);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (i >= n) break;
+                        const float c = code_of(w, i);
+                        const float4 v = q[j + i];
+                        dot[0] = __builtin_fmaf(v.x, c, dot[0]);
+                        dot[1] = __builtin_fmaf(v.y, c, dot[1]);
+                        dot[2] = __builtin_fmaf(v.z, c, dot[2]);
+                        dot[3] = __builtin_fmaf(v.w, c, dot[3]);
+                    }
+                    j += n;
                 }
-                for (int r = 0; r < kAttnGenRows; ++r) x[r] = __builtin_fmaf(dot[r], ks[g], x[r]);
+                const float scale = ks[g];
+#pragma unroll
+                for (int r = 0; r < kAttnGenRows; ++r) x[r] = __builtin_fmaf(dot[r], scale, x[r]);
             }
         }
         v_at[t] = there ? page * a.vc.st[0] + in_page * a.vc.st[1] + at.head * a.vc.st[2] : -1;
         vs_at[t] = page * a.vc.sc[0] + in_page * a.vc.sc[1] + at.head * a.vc.sc[2];
         // the tile's maxima
+#pragma unroll
         for (int r = 0; r < kAttnGenRows; ++r) {
             x[r] = there && (int64_t)tok <= last[r] ? x[r] * a.scale2 : kAttnNone;
             float most = x[r];
@@ -284,52 +326,96 @@ __global__ void __launch_bounds__(kAttnGenThreads) rope_attn_general_kernel(Attn
             if (lane == 0) red[r][wave] = most;
         }
         __syncthreads();
+        float e[kAttnGenRows];
+#pragma unroll
         for (int r = 0; r < kAttnGenRows; ++r) {
             float most = m[r];
             for (int w = 0; w < kAttnGenThreads / 64; ++w) most = fmaxf(most, red[r][w]);
             const float keep = m[r] == most ? 1.0f : exp2f(m[r] - most);
             m[r] = most;
             const bool seen = there && (int64_t)tok <= last[r];
-            const float e = !seen ? 0.0f : exp2f(x[r] - most);
-            p[r][t] = e;
-            l[r] = l[r] * keep + e;              // this thread's share
-            for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) o[r][k] *= keep;
+            e[r] = !seen ? 0.0f : exp2f(x[r] - most);
+            l[r] = l[r] * keep + e[r];           // this thread's share
+#pragma unroll
+            for (int k = 0; k < kAttnGenBytes; ++k) {
+                o[k][0][r] *= keep;
+                o[k][1][r] *= keep;
+            }
         }
+        p[t] = make_float4(e[0], e[1], e[2], e[3]);
         __syncthreads();
         const uint32_t n = min((uint32_t)kAttnGenThreads, to - base);
-        for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
-            const uint32_t j = k * kAttnGenThreads + t;
-            if (j >= a.Dv) continue;
-            const uint32_t g = j / a.vc.group;
-            for (uint32_t i = 0; i < n; ++i) {
-                if (v_at[i] < 0) continue;
-                const uint32_t w = (uint8_t)a.vc.data[v_at[i] + j / 2];
-                const float v = (float)((int32_t)(w << ((j & 1u) ? 24 : 28)) >> 28) * a.vc.scales[vs_at[i] + g];
-                for (int r = 0; r < kAttnGenRows; ++r)
-                    if (p[r][i] != 0.0f) o[r][k] = __builtin_fmaf(p[r][i], v, o[r][k]);
+#pragma unroll
+        for (int k = 0; k < kAttnGenBytes; ++k) {
+            const uint32_t byte = k * kAttnGenThreads + col;
+            if (byte >= v_bytes) continue;
+            const uint32_t g = 2 * byte / a.vc.group;              // (groups are even)
+            for (uint32_t i = strand; i < n; i += strands * kAttnGenAhead) {
+                uint32_t w[kAttnGenAhead];
+                float scale[kAttnGenAhead];
+#pragma unroll
+                for (int u = 0; u < kAttnGenAhead; ++u) {
+                    const uint32_t one = i + u * strands;
+                    w[u] = 0;
+                    scale[u] = 0.0f;
+                    if (one >= n || v_at[one] < 0) continue;
+                    w[u] = gload<uint8_t>(as_global(a.vc.data) + v_at[one] + byte);
+                    scale[u] = a.vc.scales[vs_at[one] + g];
+                }
+#pragma unroll
+                for (int u = 0; u < kAttnGenAhead; ++u) {
+                    const float4 f = p[min(i + u * strands, (uint32_t)kAttnGenThreads - 1)];
+                    const float weight[kAttnGenRows] = {f.x, f.y, f.z, f.w};
+                    const float v0 = code_of(w[u], 0) * scale[u], v1 = code_of(w[u], 1) * scale[u];
+#pragma unroll
+                    for (int r = 0; r < kAttnGenRows; ++r) {
+                        o[k][0][r] += mul_or_0(weight[r], v0);
+                        o[k][1][r] += mul_or_0(weight[r], v1);
+                    }
+                }
             }
         }
         __syncthreads();                         // the next tile overwrites p, v_at and red
     }
+#pragma unroll
     for (int r = 0; r < kAttnGenRows; ++r) {
         float sum = l[r];
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
         if (lane == 0) red[r][wave] = sum;
     }
-    __syncthreads();
-    for (uint32_t r = 0; r < nr; ++r) {
-        float sum = 0.0f;
-        for (int w = 0; w < kAttnGenThreads / 64; ++w) sum += red[r][w];
-        const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
-        const float inv = one_over(sum);
-        const uint64_t row = part_row(a, at.part, s, h);
-        for (int k = 0; k < ROPE_D_LIMIT / kAttnGenThreads; ++k) {
-            const uint32_t j = k * kAttnGenThreads + t;
-            if (j >= a.Dv) continue;
-            if (!a.split) Store<DT>::store1(a.out.data, at.b * a.out.sb + s * a.out.ss + h * a.out.sn + j, o[r][k] * inv);
-            else a.part[row * a.Dv + j] = o[r][k];
+    // the strands' sums, added in order by the first (q's place is free)
+    float* const parts = reinterpret_cast<float*>(q);
+    static_assert(sizeof(q) >= kAttnGenThreads * 2 * kAttnGenRows * sizeof(float), "one byte's sums of all threads");
+#pragma unroll
+    for (int k = 0; k < kAttnGenBytes; ++k) {
+        __syncthreads();
+        if (strands > 1) {                       // (k is 0 then)
+#pragma unroll
+            for (int i = 0; i < 2 * kAttnGenRows; ++i) parts[i * kAttnGenThreads + t] = o[k][i & 1][i >> 1];
+            __syncthreads();
+            if (strand == 0)
+#pragma unroll
+                for (int i = 0; i < 2 * kAttnGenRows; ++i)
+                    for (uint32_t of = 1; of < strands; ++of) o[k][i & 1][i >> 1] += parts[i * kAttnGenThreads + of * cols + t];
         }
-        if (a.split && t == 0) part_stats(a)[row] = make_float2(m[r], sum);
+        const uint32_t byte = k * kAttnGenThreads + col;
+        if (strand != 0 || byte >= v_bytes) continue;
+#pragma unroll
+        for (int r = 0; r < kAttnGenRows; ++r) {
+            if (r >= (int)nr) continue;
+            float sum = 0.0f;
+            for (int w = 0; w < kAttnGenThreads / 64; ++w) sum += red[r][w];
+            const uint32_t s = fast_div(r0 + r, a.rep_div), h = at.head * a.rep + (r0 + r - s * a.rep);
+            const uint64_t row = part_row(a, at.part, s, h);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!a.split)
+                    Store<DT>::store1(a.out.data, at.b * a.out.sb + s * a.out.ss + h * a.out.sn + 2 * byte + i, o[k][i][r] * one_over(sum));
+                else
+                    a.part[row * a.Dv + 2 * byte + i] = o[k][i][r];
+            }
+            if (a.split && byte == 0) part_stats(a)[row] = make_float2(m[r], sum);
+        }
     }
 }
 

@@ -424,14 +424,7 @@ struct AttnRows {
     __device__ __forceinline__ static f32x4 scaled(const f32x4& x, const float* vs)
     {
         const f32x4 v = *reinterpret_cast<const f32x4*>(vs);
-        f32x4 w;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            float one;
-            asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(one) : "v"(x[r]), "v"(v[r]));
-            w[r] = one;
-        }
-        return w;
+        return f32x4{mul_or_0(x[0], v[0]), mul_or_0(x[1], v[1]), mul_or_0(x[2], v[2]), mul_or_0(x[3], v[3])};
     }
 
     // By segments: the weights times V's scales, in fp16, and o^T += V^T P^T, 32
