@@ -113,17 +113,19 @@ int scales_of(const AttnPlan& p, int lanes)
         return -1;
     const bool k_row = p.kc.group == D, v_row = p.vc.group == Dv;
     if ((!k_row && p.kc.group % 16 != 0) || (!v_row && p.vc.group % 16 != 0)) return -1;
-    if ((!k_row && p.kc.group % 32 != 0) || (!v_row && p.vc.group % 32 != 0)) return kAttnHalves;
+    const bool k_halves = !k_row && p.kc.group % 32 != 0, v_halves = !v_row && p.vc.group % 32 != 0;
+    if (v_halves) return k_halves ? kAttnHalves : kAttnVHalves;
+    if (k_halves) return v_row ? kAttnKHalves : kAttnHalves;
     const bool k_whole = k_row && D == lanes && codes_aligned(p.kc, lanes == 64 ? 8 : 16);
     return !v_row ? kAttnSegments : k_whole ? kAttnRowScales : kAttnKSegments;
 }
 
 // The matrix-core kernel of a call.
-const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, int lanes, int scales, int64_t heads)
+const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, bool few, int lanes, int scales, int64_t heads)
 {
     const int64_t D = p.q.D, Dv = p.out.D;
     const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
-    if (rows != AttnRowsOf::kShared && scales != kAttnHalves && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
+    if (few && scales != kAttnHalves && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
         heads_together(p.kc, heads, D, scales == kAttnRowScales) && heads_together(p.vc, heads, D, scales == kAttnRowScales))
         rows = rows == AttnRowsOf::kOneTile ? AttnRowsOf::kFourHeads : AttnRowsOf::kFourHeadsTwoTiles;
     if (p.rope.dtype == ROPE_DTYPE_BF16)
@@ -142,11 +144,11 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     // 49, shared numbers 71; 64 rows 51, 65 and 66); more share their numbers (96
     // rows 75, two tiles 69; 128 rows 79 and 86, 512 rows 247 and 284). Rows past
     // 128 lanes, and scales of 16, leave registers for one tile only.
-    const AttnRowsOf rows = lanes == 256 || scales == kAttnHalves || a.rows <= 16 ? AttnRowsOf::kOneTile
+    const AttnRowsOf rows = lanes == 256 || scales >= kAttnKHalves || a.rows <= 16 ? AttnRowsOf::kOneTile
                             : a.rows <= 64                                        ? AttnRowsOf::kTwoTiles
                                                                                   : AttnRowsOf::kShared;
     const bool mfma = scales >= 0;
-    const void* fn = mfma ? mfma_kernel(p, rows, lanes, scales, a.heads) : by_type<General>(p.rope.dtype);
+    const void* fn = mfma ? mfma_kernel(p, rows, a.rows <= 64, lanes, scales, a.heads) : by_type<General>(p.rope.dtype);
     // Up to 64 rows: a wave a head, as far as heads go by fours, which then read
     // neighbouring bytes; else waves take turns at the tokens. More: a wave its
     // own rows.

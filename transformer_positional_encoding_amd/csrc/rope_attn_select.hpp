@@ -15,6 +15,8 @@ const void* attn_by_scales(int scales)
     switch (scales) {
     case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 0, 0, P16, NT>);
     case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 1, 0, P16, NT>);
+    case kAttnKHalves: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, kHalves, 0, P16, 1>);
+    case kAttnVHalves: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 1, kHalves, P16, 1>);
     case kAttnHalves: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, kHalves, kHalves, P16, 1>);
     default: return reinterpret_cast<const void*>(&rope_attn_mfma_kernel<DT, DP, DP, 1, 1, P16, NT>);
     }
@@ -36,6 +38,8 @@ const void* attn_heads(int scales)
     switch (scales) {
     case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 0, 0, NT>);
     case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, 0, NT>);
+    case kAttnKHalves: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, kHalves, 0, 1>);
+    case kAttnVHalves: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, kHalves, 1>);
     default: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, 1, NT>);
     }
 }
