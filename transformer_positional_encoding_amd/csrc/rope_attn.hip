@@ -125,7 +125,7 @@ const void* mfma_kernel(const AttnPlan& p, AttnRowsOf rows, bool few, int lanes,
 {
     const int64_t D = p.q.D, Dv = p.out.D;
     const bool whole16 = p.page_size % 16 == 0 && p.kc.st[1] < (1 << 26) && p.vc.st[1] < (1 << 26);
-    if (few && scales != kAttnHalves && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
+    if (few && lanes < 256 && whole16 && D == lanes && Dv == lanes &&
         heads_together(p.kc, heads, D, scales == kAttnRowScales) && heads_together(p.vc, heads, D, scales == kAttnRowScales))
         rows = rows == AttnRowsOf::kOneTile ? AttnRowsOf::kFourHeads : AttnRowsOf::kFourHeadsTwoTiles;
     if (p.rope.dtype == ROPE_DTYPE_BF16)

@@ -20,7 +20,7 @@ constexpr int kAttnHalves = 5;
 enum class AttnRowsOf { kOneTile, kTwoTiles, kShared, kFourHeads, kFourHeadsTwoTiles };
 
 // The kernel for rows of up to `lanes` lanes (64, 128; 256: kOneTile only;
-// kFourHeads: pages of whole 16 tokens and not kAttnHalves).
+// kFourHeads: pages of whole 16 tokens only).
 // _any: for pages of any size, the others for pages of whole 16 tokens less
 // than 2^26 bytes apart.
 const void* attn_kernel_bf16(int lanes, int scales, AttnRowsOf rows);

@@ -1104,15 +1104,17 @@ template <int DP, int KF, int VF, int NT>
 struct alignas(16) AttnHeadsLds {
     static constexpr int kRow = 2 * DP;            // bytes of a token's four rows
     static constexpr bool kScales = !KF && !VF;    // one a row: they come with the codes
+    static constexpr bool kRows = KF != kHalves || VF != kHalves;
     static constexpr int NGK = attn_groups(KF, DP), NGV = attn_groups(VF, DP);
     struct Tile {
         char k[64 * kRow], v[64 * kRow];
-        float ks[kScales ? 64 : 1][4], vs[kScales ? 64 : 1][4];
+        float ks[kScales ? 64 : 0][4], vs[kScales ? 64 : 0][4];
     };
     Tile tile[2];
     struct Wave {
         float ks[NGK][64], vs[NGV][64];
-        float start[NT][NGK][16], top[NT][NGV][16];        // the rows', where registers are short
+        // the rows', where registers are short (where scales leave room for them)
+        float start[kRows ? NT : 0][NGK][16], top[kRows ? NT : 0][NGV][16];
     };
     Wave wave[4];
 };
@@ -1195,12 +1197,14 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
     const Numbers k_const = k_constants<DT>();
     const VConstants v_const = v_constants();
     typename Lds::Wave& my = lds.wave[wave];
+    if constexpr (Lds::kRows) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int g = 0; g < NGK; ++g) my.start[t][g][n16] = rows.start[t][g];
+            for (int g = 0; g < NGK; ++g) my.start[t][g][n16] = rows.start[t][g];
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) my.top[t][g][n16] = 0.0f;
+            for (int g = 0; g < NGV; ++g) my.top[t][g][n16] = 0.0f;
+        }
     }
     AttnPlace now = attn_look_up(a, table, from + lane, to);
     attn_settle(a, now);
@@ -1249,7 +1253,10 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
         f32x4 x[NT][4];
         rows.template scores<true>(x, [&](int i, int st) {
             return k_numbers<DT>(KF ? *reinterpret_cast<const uint32_t*>(k_piece(i, st) + 4 * kq) : kw[i][KF ? 0 : st], k_const);
-        }, my.ks, kq, [&](int t, int st) { return my.start[t][st][n16]; });
+        }, my.ks, kq, [&](int t, int st) {
+            if constexpr (Lds::kRows) return my.start[t][st][n16];
+            else return rows.start[t][st];
+        });
         if (base + 64 > all || valid != ~0ull) rows.hide(x, base, valid, kq);
         float keep[NT];
         bool moved[NT];
@@ -1295,7 +1302,10 @@ __global__ void __launch_bounds__(256, 2) rope_attn_heads_kernel(AttnVecArgs a)
                        (i & 3) == 2 ? v_numbers<2>(w, v_const) : v_numbers<3>(w, v_const);
             }
             return v;
-        }, my.vs, kq, lane, [&](int t, int g) -> float& { return my.top[t][g][n16]; });
+        }, my.vs, kq, lane, [&](int t, int g) -> float& {
+            if constexpr (Lds::kRows) return my.top[t][g][n16];
+            else return rows.top[t][g];
+        });
         now = next;
         next = after;
         buffer ^= 1;

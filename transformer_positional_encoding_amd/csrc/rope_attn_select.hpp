@@ -40,6 +40,7 @@ const void* attn_heads(int scales)
     case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, 0, NT>);
     case kAttnKHalves: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, kHalves, 0, 1>);
     case kAttnVHalves: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, kHalves, 1>);
+    case kAttnHalves: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, kHalves, kHalves, 1>);
     default: return reinterpret_cast<const void*>(&rope_attn_heads_kernel<DT, DP, 1, 1, NT>);
     }
 }
