@@ -143,10 +143,13 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     // (24 rows, 8 sequences of up to 8000 tokens, 32 heads on 8: 38 us, one tile
     // 49, shared numbers 71; 64 rows 51, 65 and 66); more share their numbers (96
     // rows 75, two tiles 69; 128 rows 79 and 86, 512 rows 247 and 284). Rows past
-    // 128 lanes, and scales of 16, leave registers for one tile only.
-    const AttnRowsOf rows = lanes == 256 || scales >= kAttnKHalves || a.rows <= 16 ? AttnRowsOf::kOneTile
-                            : a.rows <= 64                                        ? AttnRowsOf::kTwoTiles
-                                                                                  : AttnRowsOf::kShared;
+    // 128 lanes and scales of 16 leave registers for one tile a wave; the latter
+    // share their numbers all the same (3 prompts of 2039 tokens behind up to
+    // 4096: 2090 us, 3820 by waves on their own), the former do not.
+    const bool halves = scales >= kAttnKHalves;
+    const AttnRowsOf rows = lanes < 256 && a.rows > 64              ? AttnRowsOf::kShared
+                            : lanes < 256 && a.rows > 16 && !halves ? AttnRowsOf::kTwoTiles
+                                                                    : AttnRowsOf::kOneTile;
     const bool mfma = scales >= 0;
     const void* fn = mfma ? mfma_kernel(p, rows, a.rows <= 64, lanes, scales, a.heads) : by_type<General>(p.rope.dtype);
     // Up to 64 rows: a wave a head, as far as heads go by fours, which then read
@@ -165,7 +168,7 @@ rope_status_t launch_attn(const AttnPlan& p, hipStream_t s)
     a.v_group = a.vc.group;
     a.k_groups = a.D / a.k_group;
     a.v_groups = a.Dv / a.v_group;
-    const uint32_t block_rows = !mfma ? kAttnGenRows : (rows == AttnRowsOf::kOneTile ? 16 : 32) * a.row_waves;
+    const uint32_t block_rows = !mfma ? kAttnGenRows : (rows == AttnRowsOf::kOneTile || halves ? 16 : 32) * a.row_waves;
     a.tiles = (a.rows + block_rows - 1) / block_rows;
     a.tiles_div = make_fastdiv(a.tiles);
     const uint64_t blocks = (uint64_t)a.parts * a.heads_div.d * a.tiles;

@@ -15,8 +15,9 @@ constexpr int kAttnVHalves = 4;
 constexpr int kAttnHalves = 5;
 
 // Query rows of a cached head that a kernel takes: 16 or 32 a wave, by waves on
-// their own, or 32 a wave, 128 a block, whose waves share their tiles' numbers,
-// or 16 or 32 a wave of one of four heads that a block loads together.
+// their own, or 32 a wave, 128 a block, whose waves share their tiles' numbers
+// (16 and 64 with scales of halves), or 16 or 32 a wave of one of four heads that
+// a block loads together.
 enum class AttnRowsOf { kOneTile, kTwoTiles, kShared, kFourHeads, kFourHeadsTwoTiles };
 
 // The kernel for rows of up to `lanes` lanes (64, 128; 256: kOneTile only;

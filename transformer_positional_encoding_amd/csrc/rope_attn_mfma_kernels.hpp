@@ -883,8 +883,8 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 
 
 // ---------------------------------------------------------------------------
-// Many rows (a prompt's): the four waves of a block have 32 rows each of one
-// cached head and go through the same tiles, so each makes numbers of a quarter
+// Many rows (a prompt's): the four waves of a block have 32 rows each (NT 2; 16
+// where scales of 16 lanes leave no registers for more) of one cached head and go through the same tiles, so each makes numbers of a quarter
 // of a tile, for all, in LDS: in the order in which the products take them, 16
 // bytes a lane, so that no read or write meets another's bank. Numbers cost a
 // wave 75 operations a tile then, not 300, of 700. Two buffers: while a tile is
@@ -894,9 +894,7 @@ __global__ void __launch_bounds__(256, attn_waves(DVP, KF, NT)) rope_attn_mfma_k
 // scale for 32 lanes 858, 1106. (32 rows a wave: 48 and 64 were slower, for want
 // of registers.)
 // ---------------------------------------------------------------------------
-constexpr int kSharedTiles = 2;                    // of 16 rows a wave
-
-template <int DP, int KF, int VF, bool P16>
+template <int DP, int KF, int VF, bool P16, int NT>
 struct alignas(16) AttnSharedLds {
     static constexpr int NGK = attn_groups(KF, DP), NGV = attn_groups(VF, DP);
     struct Buffer {
@@ -910,16 +908,15 @@ struct alignas(16) AttnSharedLds {
     };
     Where where[P16 ? 1 : 4];
     struct Wave {
-        float start[kSharedTiles][NGK][16], top[kSharedTiles][NGV][16];    // the rows', where registers are short
+        float start[NT][NGK][16], top[NT][NGV][16];    // the rows', where registers are short
     };
     Wave wave[4];
 };
 
-template <int DT, int DP, int KF, int VF, bool P16>
+template <int DT, int DP, int KF, int VF, bool P16, int NT>
 __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
 {
-    constexpr int NT = kSharedTiles;
-    using Lds = AttnSharedLds<DP, KF, VF, P16>;
+    using Lds = AttnSharedLds<DP, KF, VF, P16, NT>;
     using R = AttnRows<DT, DP, DP, KF, VF, NT>;
     constexpr int KW = R::KW, VT = R::VT, NGK = Lds::NGK, NGV = Lds::NGV;
     static_assert(DP == 64 || DP == 128, "a register a token's V");
@@ -967,19 +964,24 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
     const VConstants v_const = v_constants();
 
     uint32_t kw[KW], vw[8];
-    float ks = 0.0f, vs = 0.0f;
+    constexpr int SK = (NGK + 3) / 4, SV = (NGV + 3) / 4;  // scales' groups of a wave: wave, wave + 4
+    float ks[SK] = {}, vs[SV] = {};
     bool there = false;
     const auto fetch = [&](AttnPlace& p) {
         attn_settle(a, p);
         there = p.there;
         const int64_t page = p.page, in_page = p.in_page;
-        if (wave < NGK) {
-            const uint32_t g = KF ? min(wave * 32 / a.k_group, a.k_groups - 1) : 0;
-            ks = there ? gload<float>(ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1] + g) * 4) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < SK; ++n) {
+            if (wave + 4 * n >= NGK) continue;
+            const uint32_t g = KF ? min((wave + 4 * n) * attn_group(KF) / a.k_group, a.k_groups - 1) : 0;
+            ks[n] = there ? gload<float>(ks_base + (page * a.kc.sc[0] + in_page * a.kc.sc[1] + g) * 4) : 0.0f;
         }
-        if (wave < NGV) {
-            const uint32_t g = VF ? min(wave * 32 / a.v_group, a.v_groups - 1) : 0;
-            vs = there ? gload<float>(vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1] + g) * 4) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < SV; ++n) {
+            if (wave + 4 * n >= NGV) continue;
+            const uint32_t g = VF ? min((wave + 4 * n) * attn_group(VF) / a.v_group, a.v_groups - 1) : 0;
+            vs[n] = there ? gload<float>(vs_base + (page * a.vc.sc[0] + in_page * a.vc.sc[1] + g) * 4) : 0.0f;
         }
         if constexpr (!P16) {
             lds.where[wave].k_at[lane] = page * a.kc.st[0] + in_page * a.kc.st[1];
@@ -1044,8 +1046,12 @@ __global__ void __launch_bounds__(256, 2) rope_attn_shared_kernel(AttnVecArgs a)
                        i == 2 ? v_numbers<2>(two[j], v_const) : v_numbers<3>(two[j], v_const);
             to_tile.v[half][part * (VT / 2) + i][lane] = v;
         }
-        if (wave < NGK) to_tile.ks[wave][lane] = ks * a.scale2;
-        if (wave < NGV) to_tile.vs[wave][lane] = vs;
+#pragma unroll
+        for (int n = 0; n < SK; ++n)
+            if (wave + 4 * n < NGK) to_tile.ks[wave + 4 * n][lane] = ks[n] * a.scale2;
+#pragma unroll
+        for (int n = 0; n < SV; ++n)
+            if (wave + 4 * n < NGV) to_tile.vs[wave + 4 * n][lane] = vs[n];
     };
 
     AttnPlace next = attn_look_up(a, table, from + lane, to);

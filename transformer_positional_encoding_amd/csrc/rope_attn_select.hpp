@@ -26,9 +26,12 @@ template <int DT, int DP, bool P16>
 const void* attn_shared(int scales)
 {
     switch (scales) {
-    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 0, 0, P16>);
-    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, 0, P16>);
-    default: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, 1, P16>);
+    case kAttnRowScales: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 0, 0, P16, 2>);
+    case kAttnKSegments: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, 0, P16, 2>);
+    case kAttnSegments: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, 1, P16, 2>);
+    case kAttnKHalves: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, kHalves, 0, P16, 1>);
+    case kAttnVHalves: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, 1, kHalves, P16, 1>);
+    default: return reinterpret_cast<const void*>(&rope_attn_shared_kernel<DT, DP, kHalves, kHalves, P16, 1>);
     }
 }
 
