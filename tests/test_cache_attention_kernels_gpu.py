@@ -202,3 +202,22 @@ def test_groups_of_16_lanes(D, Dv, gk, gv, S, hq, heads, page):
     c = inputs([500, 333], S, hq, heads, D, Dv, gk, gv, page, "bf16", seed=43, span=12.0)
     c["k"] = (c["k"][0], c["k"][1].clamp(max=4.0))
     check(call(c, causal=False), c, causal=False, what="far apart")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gk, gv", [(16, None), (None, 16), (16, 16), (32, None), (32, 16), (16, 32), (64, 16), (32, 32)])
+@pytest.mark.parametrize("S, hq, heads, page", [(1, 4, 4, 16), (3, 16, 8, 48), (9, 8, 4, 64), (40, 4, 4, 16), (100, 8, 4, 32)])
+def test_four_heads_groups_of_lanes(D, gk, gv, S, hq, heads, page):
+    gk, gv = gk or D, gv or D
+    lengths = [S, 0, 300 + S, 65]
+    counts = torch.tensor([S, S, S, (S + 1) // 2], dtype=torch.int32)
+    for dtype, span in (("bf16", 3.0), ("f16", 0.5)):
+        c = inputs(lengths, S, hq, heads, D, D, gk, gv, page, dtype, seed=44, span=span)
+        c["k"] = (c["k"][0], c["k"][1].clamp(max=4.0))
+        got = call(c, counts=counts)
+        check(got, c, counts=counts, what=dtype)
+        for b, n in enumerate(counts.tolist()):
+            assert torch.equal(got[b, n:].cpu(), c["out"][b, n:])
+    c = inputs([500, 333], S, hq, heads, D, D, gk, gv, page, "bf16", seed=45, span=12.0)
+    c["k"] = (c["k"][0], c["k"][1].clamp(max=4.0))
+    check(call(c, causal=False), c, causal=False, what="far apart")
